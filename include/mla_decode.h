@@ -55,7 +55,7 @@ typedef enum {
   MLA_ERR_CUDA = -5                /* a CUDA runtime call failed (launch, attribute) */
 } mla_status;
 
-typedef enum { MLA_KV_BF16 = 0, MLA_KV_FP8_E4M3 = 1 } mla_kv_dtype;
+typedef enum { MLA_KV_BF16 = 0, MLA_KV_FP8_E4M3 = 1, MLA_KV_FP4_E2M1 = 2 } mla_kv_dtype;
 typedef enum { MLA_MASK_CAUSAL = 0, MLA_MASK_DENSE = 1 } mla_mask;
 typedef enum { MLA_Q_BF16 = 0, MLA_Q_FP8_E4M3 = 1 } mla_q_dtype;
 
@@ -368,6 +368,123 @@ int mla_decode_run_sparse(const mla_plan_t *plan, const void *query, const void 
 int mla_merge_states(const void *o_parts, const float *lse_parts, int32_t n_parts, int64_t rows,
                      float scale, void *out, float *lse_out, void *stream);
 
+/*
+ * The 4-bit cache (MLA_KV_FP4_E2M1).  A row is 576 e2m1 codes (magnitudes 0,
+ * 0.5, 1, 1.5, 2, 3, 4, 6 and a sign) and 36 e4m3 scales, one per group of 16
+ * dims: value = code * scale, exact in bf16.  A page of ps rows is a block of
+ * ps * MLA_FP4_ROW_BYTES bytes: first the codes of its rows, 288 bytes each
+ * (dim 2 i in the low nibble of byte i), then their scales, 36 bytes each.  So
+ * the cache is uint8 [num_pages, page_size, 324] by size.  There is no code for
+ * a NaN or an infinity: mla_cache_append saturates (a NaN stores as +-6 times
+ * its group's scale and does not count in the group's largest magnitude).
+ */
+#define MLA_FP4_ROW_BYTES 324
+
+typedef enum { MLA_ROPE_INTERLEAVED = 0, MLA_ROPE_HALF = 1 } mla_rope_style;
+typedef enum { MLA_ROPE_NONE = 0, MLA_ROPE_LINEAR = 1, MLA_ROPE_YARN = 2 } mla_rope_scaling;
+
+/* Rotation table of mla_rope_table.  Zero-initialise, then set what applies. */
+typedef struct mla_rope_params {
+  int32_t max_position;  /* rows of the table: positions 0 .. max_position - 1 */
+  int32_t scaling;       /* mla_rope_scaling */
+  double base;           /* > 1; pair i of 32 turns by base^(-i/32) per position */
+  double amplitude;      /* multiplies cosines and sines (1: a pure rotation) */
+  double factor;         /* LINEAR, YARN: frequencies are divided by this */
+  double original_max_position; /* YARN: the context the frequencies were trained on */
+  double beta_fast, beta_slow;  /* YARN: pairs that turn more than beta_fast times over
+                                   it are kept, less than beta_slow divided, between
+                                   blended linearly in the pair index */
+} mla_rope_params;
+
+/*
+ * Enqueue the rotation table: table[p][0..31] = amplitude * cos(p f_i) and
+ * table[p][32..63] = amplitude * sin(p f_i), fp32, computed in 64 bits.  Made
+ * once per model; 256 bytes a position, 16-byte aligned, device memory.
+ * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_ALIGNMENT, MLA_ERR_CUDA.
+ */
+int mla_rope_table(const mla_rope_params *params, float *table, void *stream);
+
+/* Static parameters of mla_cache_append and mla_cache_gather. */
+typedef struct mla_cache_params {
+  int32_t batch;             /* B >= 0 requests */
+  int32_t packed;            /* 0: q_len tokens per request; 1: qo_indptr */
+  int32_t q_len;             /* fixed: >= 1 */
+  int32_t page_size;         /* 32 or 64 */
+  int32_t max_pages_per_req; /* row stride of block_tables */
+  int32_t kv_dtype;          /* mla_kv_dtype */
+  int64_t num_pages;         /* physical pages in kv_cache */
+  int32_t num_heads;         /* append with a query: H in {16, 32, 64, 128} */
+  int32_t q_dtype;           /* append with a query: mla_q_dtype of `query` */
+} mla_cache_params;
+
+/*
+ * Write the cache rows of each request's newest tokens and, in the same
+ * launch, form their query rows for mla_decode_run.  Token i of request b
+ * (token t = b * q_len + i, or qo_indptr[b] + i) takes cache position
+ * p = seq_lens[b] - q + i, q being the request's number of tokens here:
+ * seq_lens already counts them, as mla_decode_run wants it.
+ *
+ *   y     = [rmsnorm(latent[t]) * norm_weight, R_p k_pe[t]]
+ *   row p = y (bf16), e4m3(y / kv_scale), or 4 bits of y / kv_scale
+ *   query[t][h] = [q_nope[t][h], R_p q_pe[t][h]], for e4m3 divided by q_scale
+ *
+ * with rmsnorm(x) = x / sqrt(mean(x^2) + eps) over the 512 latent dims (left
+ * out when norm_weight is NULL) and R_p the rotation of the 64 RoPE dims by
+ * row p of rope_table: neighbouring dims (INTERLEAVED) or dims i and i + 32
+ * (HALF) form a pair.  Everything is fp32 until the one final rounding (nearest
+ * even, saturating for e4m3 and e2m1).  Inside a group of 16 dims of a 4-bit
+ * row the scale is e4m3(amax / 6) and the codes are e2m1(value / scale); a
+ * group whose scale rounds to 0 stores zeros.
+ *
+ * latent       bf16, row t at latent + t * latent_stride, 512 wide
+ * k_pe         bf16, row t at k_pe + t * k_pe_stride, 64 wide
+ * norm_weight  bf16 [512] or NULL; with it 1e-30 <= eps <= 3e38
+ * rope_table   fp32 [max_position][64] (mla_rope_table)
+ * positions    int32 [total_q] rotation positions, or NULL: the cache position
+ * total_q      tokens (fixed: batch * q_len).  Packed: rows at or past
+ *              qo_indptr[B] are padding: nothing is written for them.  qo_indptr
+ *              must not decrease; a request may have no token.
+ * kv_scale     > 0; 1 for a bf16 cache
+ * kv_cache     the pages, by kv_dtype; only the tokens' rows are written
+ * q_pe, query  both or neither: [total_q][H] rows of 64 by the strides, and
+ *              bf16 or e4m3 [total_q, H, 576] contiguous
+ * q_nope       [total_q][H] rows of 512 by the strides; NULL (bf16 query only)
+ *              leaves dims [0, 512) of `query` as they are
+ * q_scale      > 0; 1 for a bf16 query
+ * status       int32 device word or NULL: bits of mla_decode_status_offset are
+ *              ORed in (2: a bad qo_indptr, 1: a bad length, 16: a page id out
+ *              of [0, num_pages), 128: a rotation position out of the table).
+ *              Such a token's rows are not written.
+ * Strides are in elements and multiples of 8, may be 0; row pointers 16-byte
+ * aligned.  Inputs must not overlap kv_cache or query.  A cache row that two
+ * tokens map to (a page that two requests share at that row) holds either's
+ * bytes.  Capture-safe; no workspace.  Call with the tensors' device current.
+ * Errors (nothing enqueued): MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED,
+ * MLA_ERR_ALIGNMENT; MLA_ERR_CUDA if the launch fails.
+ */
+int mla_cache_append(const mla_cache_params *params, const void *latent, int64_t latent_stride,
+                     const void *k_pe, int64_t k_pe_stride, const void *norm_weight, float eps,
+                     const float *rope_table, int32_t max_position, int32_t rope_style,
+                     const int32_t *positions, const int32_t *block_tables,
+                     const int32_t *seq_lens, const int32_t *qo_indptr, int64_t total_q,
+                     float kv_scale, void *kv_cache, const void *q_nope,
+                     int64_t q_nope_token_stride, int64_t q_nope_head_stride, const void *q_pe,
+                     int64_t q_pe_token_stride, int64_t q_pe_head_stride, float q_scale,
+                     void *query, int32_t *status, void *stream);
+
+/*
+ * Read cache rows back: out[t] = bf16(kv_scale * row p of request b), 576 wide,
+ * for the tokens and positions of mla_cache_append (qo_indptr = the running sum
+ * of seq_lens reads whole sequences).  out: bf16 [total_q, 576], 16-byte
+ * aligned, not overlapping the cache; rows whose position or page is bad
+ * (flagged in `status`) and padding rows are left as they were.
+ * Errors and capture rules as mla_cache_append.
+ */
+int mla_cache_gather(const mla_cache_params *params, const void *kv_cache,
+                     const int32_t *block_tables, const int32_t *seq_lens,
+                     const int32_t *qo_indptr, int64_t total_q, float kv_scale, void *out,
+                     int32_t *status, void *stream);
+
 /* Workspace bytes of a plan (the value mla_decode_plan returned). */
 size_t mla_decode_workspace_size(const mla_plan_t *plan);
 
@@ -409,6 +526,7 @@ int32_t mla_decode_kernels_per_run(const mla_plan_t *plan);
  *  16  a block_tables entry of a visible page out of [0, num_pages)
  *  32  an internal wait timed out (the run unwound; results are invalid)
  *  64  a device bmm1 scale negative or not finite (read as 0)
+ * 128  a rotation position outside the table (mla_cache_append's status only)
  * Reading it is the caller's choice (a device-to-host copy after the stream
  * syncs).
  */

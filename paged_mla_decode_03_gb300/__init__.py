@@ -25,14 +25,18 @@ __all__ = [
     "mla_decode_plan", "mla_decode_run", "mla_decode_run_profiled", "mla_decode_run_dcp",
     "mla_decode_run_sparse", "mla_decode_destroy", "mla_decode_workspace_size",
     "mla_decode_status_offset", "mla_decode_status_string", "Plan", "decode",
-    "HEAD_DIM_QK", "HEAD_DIM_V",
+    "HEAD_DIM_QK", "HEAD_DIM_V", "FP4_ROW_BYTES", "MlaCacheParams", "MlaRopeParams",
+    "cache_append", "cache_gather", "rope_table",
 ]
 
 HEAD_DIM_QK = 576
 HEAD_DIM_V = 512
 MLA_OK = 0
 MLA_STATIC_WORKSPACE_BYTES = 48 * 1024 * 1024  # scratch of mla_decode_run_static_workspace
-KV_BF16, KV_FP8_E4M3 = 0, 1
+KV_BF16, KV_FP8_E4M3, KV_FP4_E2M1 = 0, 1, 2
+FP4_ROW_BYTES = 324  # a 4-bit cache row: 288 bytes of e2m1 codes, 36 e4m3 scales
+ROPE_STYLES = {"interleaved": 0, "half": 1}
+ROPE_SCALINGS = {None: 0, "linear": 1, "yarn": 2}
 Q_BF16, Q_FP8_E4M3 = 0, 1
 MASK_CAUSAL, MASK_DENSE = 0, 1
 
@@ -68,6 +72,35 @@ class MlaDecodeParams(ctypes.Structure):
         ("cp_rank", ctypes.c_int32),
         ("sparse_top_k", ctypes.c_int32),
         ("e4m3_widen", ctypes.c_int32),
+    ]
+
+
+class MlaCacheParams(ctypes.Structure):
+    """Mirror of ``mla_cache_params`` (natural C alignment)."""
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("packed", ctypes.c_int32),
+        ("q_len", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("max_pages_per_req", ctypes.c_int32),
+        ("kv_dtype", ctypes.c_int32),
+        ("num_pages", ctypes.c_int64),
+        ("num_heads", ctypes.c_int32),
+        ("q_dtype", ctypes.c_int32),
+    ]
+
+
+class MlaRopeParams(ctypes.Structure):
+    """Mirror of ``mla_rope_params`` (natural C alignment)."""
+    _fields_ = [
+        ("max_position", ctypes.c_int32),
+        ("scaling", ctypes.c_int32),
+        ("base", ctypes.c_double),
+        ("amplitude", ctypes.c_double),
+        ("factor", ctypes.c_double),
+        ("original_max_position", ctypes.c_double),
+        ("beta_fast", ctypes.c_double),
+        ("beta_slow", ctypes.c_double),
     ]
 
 
@@ -110,6 +143,16 @@ def load_library():
     lib.mla_decode_run_sparse.restype = ctypes.c_int
     lib.mla_merge_states.argtypes = [vp, vp, i32, i64, ctypes.c_float, vp, vp, vp]
     lib.mla_merge_states.restype = ctypes.c_int
+    f32 = ctypes.c_float
+    lib.mla_rope_table.argtypes = [ctypes.POINTER(MlaRopeParams), vp, vp]
+    lib.mla_rope_table.restype = ctypes.c_int
+    lib.mla_cache_append.argtypes = [ctypes.POINTER(MlaCacheParams), vp, i64, vp, i64, vp, f32, vp,
+                                     i32, i32, vp, vp, vp, vp, i64, f32, vp, vp, i64, i64, vp,
+                                     i64, i64, f32, vp, vp, vp]
+    lib.mla_cache_append.restype = ctypes.c_int
+    lib.mla_cache_gather.argtypes = [ctypes.POINTER(MlaCacheParams), vp, vp, vp, vp, i64, f32, vp,
+                                     vp, vp]
+    lib.mla_cache_gather.restype = ctypes.c_int
     lib.mla_decode_destroy.argtypes = [vp]
     lib.mla_decode_destroy.restype = None
     lib.mla_decode_workspace_size.argtypes = [vp]
@@ -541,6 +584,227 @@ def merge_states(o_parts: torch.Tensor, lse_parts: torch.Tensor, *, scale: float
     if rc != 0:
         raise MlaDecodeError(rc, "mla_merge_states")
     return out, lse
+
+
+def _cache_kind(kv_cache: torch.Tensor) -> Tuple[torch.Tensor, int]:
+    """The cache as [pages, page_size, row], and its KV_* type."""
+    if kv_cache.dim() == 4:
+        if kv_cache.shape[1] != 1:
+            raise ValueError("rank-4 kv_cache must be [pages, 1, page_size, row]")
+        kv_cache = kv_cache.squeeze(1)
+    if kv_cache.dim() != 3:
+        raise ValueError("kv_cache must be [pages, page_size, row]")
+    row = kv_cache.shape[2]
+    if kv_cache.dtype == torch.uint8 and row == FP4_ROW_BYTES:
+        kind = KV_FP4_E2M1
+    elif row != HEAD_DIM_QK:
+        raise ValueError("kv_cache must be [pages, page_size, 576], or uint8 "
+                         "[pages, page_size, 324] for 4 bits")
+    elif kv_cache.dtype == torch.bfloat16:
+        kind = KV_BF16
+    elif kv_cache.dtype in (torch.float8_e4m3fn, torch.uint8):
+        kind = KV_FP8_E4M3
+    else:
+        raise ValueError(f"unsupported kv_cache dtype {kv_cache.dtype}")
+    return kv_cache, kind
+
+
+def _int32(name: str, t: Optional[torch.Tensor], shape, device) -> None:
+    if t is None:
+        return
+    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor on {device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _bf16_rows(name: str, t: torch.Tensor, shape, device) -> None:
+    if t.dtype != torch.bfloat16 or t.device != device:
+        raise ValueError(f"{name} must be a bf16 tensor on {device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.numel() and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dim must be contiguous")
+
+
+def _outer(t: torch.Tensor, dim: int) -> int:
+    """Stride of an outer dim, 0 where it has one element (it is never applied)."""
+    return t.stride(dim) if t.shape[dim] > 1 else 0
+
+
+def _stream_of(stream, device: torch.device) -> int:
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
+
+
+def _cache_call(kv_cache, block_tables, seq_lens, qo_indptr, q_len, total_q, status):
+    """Checks that ``cache_append`` and ``cache_gather`` share -> parameters."""
+    if not kv_cache.is_cuda or not kv_cache.is_contiguous():
+        raise ValueError("kv_cache must be a contiguous CUDA tensor")
+    kv_cache, kind = _cache_kind(kv_cache)
+    dev = kv_cache.device
+    batch = int(seq_lens.shape[0])
+    _int32("seq_lens", seq_lens, (batch,), dev)
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [batch, pages]")
+    _int32("block_tables", block_tables, (batch, block_tables.shape[1]), dev)
+    _int32("qo_indptr", qo_indptr, (batch + 1,), dev)
+    _int32("status", status, (1,), dev)
+    if (qo_indptr is None) == (q_len is None):
+        raise ValueError("give qo_indptr (packed) or q_len (the same for every request)")
+    if q_len is not None and (q_len < 1 or total_q != batch * q_len):
+        raise ValueError(f"{total_q} tokens are not {batch} requests of {q_len}")
+    p = MlaCacheParams(batch=batch, packed=int(qo_indptr is not None), q_len=q_len or 0,
+                       page_size=int(kv_cache.shape[1]), kv_dtype=kind,
+                       max_pages_per_req=int(block_tables.shape[1]),
+                       num_pages=int(kv_cache.shape[0]))
+    return p, dev
+
+
+def _on_device(dev: torch.device, call):
+    """``call()`` with ``dev`` current (the kernels launch on the current device)."""
+    if torch.cuda.current_device() == dev.index:
+        return call()
+    with torch.cuda.device(dev):
+        return call()
+
+
+def rope_table(max_position: int, *, base: float = 10000.0, scaling: Optional[str] = None,
+               factor: float = 1.0, original_max_position: int = 4096, beta_fast: float = 32.0,
+               beta_slow: float = 1.0, amplitude: float = 1.0, device=None,
+               stream=None) -> torch.Tensor:
+    """The rotation table of ``cache_append`` (``mla_rope_table``): fp32
+    ``[max_position, 64]``, 32 cosines then 32 sines per position, from angles in
+    64 bits.  ``scaling``: None, ``"linear"`` (every frequency divided by
+    ``factor``) or ``"yarn"`` (frequencies that turn fewer than ``beta_slow``
+    times over ``original_max_position`` divided by ``factor``, those that turn
+    more than ``beta_fast`` times kept, a linear blend between).  ``amplitude``
+    multiplies cosines and sines."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {list(ROPE_SCALINGS)}, got {scaling!r}")
+    dev = torch.device("cuda" if device is None else device)
+    if dev.type != "cuda":
+        raise ValueError("rope_table runs on the GPU")
+    if dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
+    p = MlaRopeParams(max_position=max_position, scaling=ROPE_SCALINGS[scaling], base=base,
+                      amplitude=amplitude, factor=factor,
+                      original_max_position=original_max_position, beta_fast=beta_fast,
+                      beta_slow=beta_slow)
+    table = torch.empty((max(max_position, 0), 64), dtype=torch.float32, device=dev)
+    rc = _on_device(dev, lambda: load_library().mla_rope_table(
+        ctypes.byref(p), _ptr(table) if max_position > 0 else 16, _stream_of(stream, dev)))
+    if rc != MLA_OK:
+        raise MlaDecodeError(rc, "mla_rope_table")
+    return table
+
+
+def cache_append(latent: torch.Tensor, k_pe: torch.Tensor, kv_cache: torch.Tensor,
+                 block_tables: torch.Tensor, seq_lens: torch.Tensor, *,
+                 rope_table: torch.Tensor, norm_weight: Optional[torch.Tensor] = None,
+                 eps: float = 1e-6, rope_style: str = "interleaved",
+                 qo_indptr: Optional[torch.Tensor] = None, q_len: Optional[int] = None,
+                 positions: Optional[torch.Tensor] = None, kv_scale: float = 1.0,
+                 q_nope: Optional[torch.Tensor] = None, q_pe: Optional[torch.Tensor] = None,
+                 query: Optional[torch.Tensor] = None, q_scale: float = 1.0,
+                 status: Optional[torch.Tensor] = None, stream=None):
+    """Norm, rotate, quantise and store the newest tokens' cache rows, and form
+    their query rows in the same launch (``mla_cache_append``).
+
+    ``latent`` bf16 ``[T, 512]`` and ``k_pe`` bf16 ``[T, 64]`` (row strides
+    free): the tokens of all requests, ``q_len`` each or packed by
+    ``qo_indptr``.  ``seq_lens`` already counts them: token i of a request of q
+    tokens goes to position ``seq_lens[b] - q + i``.  ``kv_cache``: bf16, e4m3
+    (``[pages, page_size, 576]``) or 4-bit (uint8 ``[pages, page_size, 324]``);
+    its values are divided by ``kv_scale``.  ``norm_weight`` bf16 ``[512]``:
+    RMS norm of the latent first (None: no norm).  ``q_pe`` bf16 ``[T, H, 64]``
+    and ``q_nope`` bf16 ``[T, H, 512]`` (strides free) give ``query``
+    ``[T, H, 576]`` (or ``[B, q_len, H, 576]``), made as bf16 when not given;
+    an e4m3 one is divided by ``q_scale``; without ``q_nope`` only the RoPE dims
+    of a given bf16 ``query`` are written.  ``status``: int32 ``[1]``, contract
+    violations are ORed in (see ``include/mla_decode.h``).  Returns ``query``."""
+    if latent.dim() != 2 or not latent.is_cuda:
+        raise ValueError("latent must be a CUDA tensor [tokens, 512]")
+    T = int(latent.shape[0])
+    p, dev = _cache_call(kv_cache, block_tables, seq_lens, qo_indptr, q_len, T, status)
+    _bf16_rows("latent", latent, (T, HEAD_DIM_V), dev)
+    _bf16_rows("k_pe", k_pe, (T, 64), dev)
+    if norm_weight is not None:
+        _bf16_rows("norm_weight", norm_weight, (HEAD_DIM_V,), dev)
+    if rope_table.dtype != torch.float32 or rope_table.device != dev or rope_table.dim() != 2 \
+            or rope_table.shape[1] != 64 or not rope_table.is_contiguous():
+        raise ValueError(f"rope_table must be a contiguous fp32 tensor [positions, 64] on {dev}")
+    if rope_style not in ROPE_STYLES:
+        raise ValueError(f"rope_style must be one of {list(ROPE_STYLES)}, got {rope_style!r}")
+    _int32("positions", positions, (T,), dev)
+    qn = qp = (0, 0)
+    if q_pe is not None:
+        if q_pe.dim() != 3:
+            raise ValueError("q_pe must be [tokens, heads, 64]")
+        H = int(q_pe.shape[1])
+        _bf16_rows("q_pe", q_pe, (T, H, 64), dev)
+        qp = (_outer(q_pe, 0), _outer(q_pe, 1))
+        if query is None:
+            if q_nope is None:
+                raise ValueError("without q_nope, query must be given (its latent part stays)")
+            query = torch.empty((T, H, HEAD_DIM_QK), dtype=torch.bfloat16, device=dev)
+        if query.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or query.device != dev \
+                or not query.is_contiguous():
+            raise ValueError(f"query must be a contiguous bf16 or float8_e4m3fn tensor on {dev}")
+        if tuple(query.shape) != (T, H, HEAD_DIM_QK) and (
+                q_len is None or tuple(query.shape) != (T // q_len, q_len, H, HEAD_DIM_QK)):
+            raise ValueError(f"query must be [{T}, {H}, 576], got {tuple(query.shape)}")
+        p.num_heads = H
+        p.q_dtype = Q_BF16 if query.dtype == torch.bfloat16 else Q_FP8_E4M3
+        if q_nope is not None:
+            _bf16_rows("q_nope", q_nope, (T, H, HEAD_DIM_V), dev)
+            qn = (_outer(q_nope, 0), _outer(q_nope, 1))
+    elif query is not None or q_nope is not None:
+        raise ValueError("query and q_nope go with q_pe")
+    lib = load_library()
+    rc = _on_device(dev, lambda: lib.mla_cache_append(
+        ctypes.byref(p), _ptr(latent), _outer(latent, 0), _ptr(k_pe), _outer(k_pe, 0),
+        _ptr(norm_weight), eps, _ptr(rope_table), int(rope_table.shape[0]),
+        ROPE_STYLES[rope_style], _ptr(positions), _ptr(block_tables), _ptr(seq_lens),
+        _ptr(qo_indptr), T, kv_scale, _ptr(kv_cache), _ptr(q_nope), qn[0], qn[1], _ptr(q_pe),
+        qp[0], qp[1], q_scale, _ptr(query), _ptr(status), _stream_of(stream, dev)))
+    if rc != MLA_OK:
+        raise MlaDecodeError(rc, "mla_cache_append")
+    return query
+
+
+def cache_gather(kv_cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, *,
+                 total_q: Optional[int] = None, qo_indptr: Optional[torch.Tensor] = None,
+                 q_len: Optional[int] = None, kv_scale: float = 1.0,
+                 out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                 stream=None) -> torch.Tensor:
+    """Cache rows as bf16 ``[total_q, 576]``, times ``kv_scale``
+    (``mla_cache_gather``): the rows of each request's last ``q_len`` positions,
+    or, packed by ``qo_indptr`` (then ``total_q`` or ``out`` is needed), of its
+    last ``qo_indptr[b + 1] - qo_indptr[b]``; the running sum of ``seq_lens``
+    reads whole sequences.  Rows of ``out`` that no position belongs to, or whose
+    page id is bad (flagged in ``status``), stay as they were."""
+    if total_q is None:
+        if out is not None:
+            total_q = int(out.shape[0])
+        elif q_len is not None:
+            total_q = int(seq_lens.shape[0]) * q_len
+        else:
+            raise ValueError("total_q is needed for packed rows")
+    p, dev = _cache_call(kv_cache, block_tables, seq_lens, qo_indptr, q_len, total_q, status)
+    if out is None:
+        out = torch.empty((total_q, HEAD_DIM_QK), dtype=torch.bfloat16, device=dev)
+    _bf16_rows("out", out, (total_q, HEAD_DIM_QK), dev)
+    if not out.is_contiguous():
+        raise ValueError("out must be contiguous")
+    lib = load_library()
+    rc = _on_device(dev, lambda: lib.mla_cache_gather(
+        ctypes.byref(p), _ptr(kv_cache), _ptr(block_tables), _ptr(seq_lens), _ptr(qo_indptr),
+        total_q, kv_scale, _ptr(out), _ptr(status), _stream_of(stream, dev)))
+    if rc != MLA_OK:
+        raise MlaDecodeError(rc, "mla_cache_gather")
+    return out
 
 
 def dcp_gather(out: torch.Tensor, lse: torch.Tensor, group=None):

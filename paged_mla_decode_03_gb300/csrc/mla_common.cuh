@@ -19,7 +19,7 @@ constexpr size_t kPartitionSmemMax = 160 * 1024;
 
 // Status word bits (workspace header word kHdrStatus).
 constexpr int kStatusSeqLen = 1, kStatusQLen = 2, kStatusCausal = 4, kStatusCapacity = 8,
-              kStatusPage = 16, kStatusTimeout = 32, kStatusScale = 64;
+              kStatusPage = 16, kStatusTimeout = 32, kStatusScale = 64, kStatusPosition = 128;
 
 struct Problem {
   int batch, num_heads, max_q, max_seq_len, page_size, max_pages;
