@@ -98,6 +98,12 @@ typedef struct mla_decode_params {
                                 (about 2^-8 relative).  Nonzero: every e4m3 value is
                                 widened exactly to bf16 before bf16 MMAs (P in bf16).
                                 Sparse top-k always widens. */
+  int32_t window;            /* sliding window W (0: off): of the rows that the mask lets a
+                                query row see, up to row `last`, it sees rows
+                                last - W + 1 .. last and the first `sinks` rows.  (W = 1:
+                                its last row alone.)  Not with cp_world > 1 or sparse_top_k. */
+  int32_t sinks;             /* with a window: rows 0 .. sinks - 1 stay visible (>= 0; 0
+                                without one) */
 } mla_decode_params;
 
 typedef struct mla_plan_s mla_plan_t; /* opaque; host memory only */
@@ -121,7 +127,9 @@ int mla_decode_plan(const mla_decode_params *params, mla_plan_t **plan,
  * kv_cache     bf16 or fp8-e4m3 (per params.kv_dtype), [num_pages, page_size, 576]
  *              (a rank-4 [num_pages, 1, page_size, 576] cache is the same memory).
  * block_tables int32 [B, max_pages_per_req]; entries at or past a request's
- *              ceil(seq_lens[b] / page_size) pages are never read.
+ *              ceil(seq_lens[b] / page_size) pages are never read, nor, under a
+ *              sliding window, those of pages that none of its query rows sees
+ *              any row of.
  * seq_lens     int32 [B]; 1 <= seq_lens[b] <= max_seq_len; for causal masking
  *              q_len(b) <= seq_lens[b].
  * qo_indptr    packed: int32 [B + 1], qo_indptr[0] = 0, strictly increasing,

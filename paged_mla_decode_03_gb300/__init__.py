@@ -72,6 +72,8 @@ class MlaDecodeParams(ctypes.Structure):
         ("cp_rank", ctypes.c_int32),
         ("sparse_top_k", ctypes.c_int32),
         ("e4m3_widen", ctypes.c_int32),
+        ("window", ctypes.c_int32),
+        ("sinks", ctypes.c_int32),
     ]
 
 
@@ -389,17 +391,18 @@ class Plan:
                  max_total_q: int = 0, kv_dtype: str = "bf16", causal: bool = True,
                  return_lse: bool = False, device: int = 0, q_dtype: str = "bf16",
                  cp_world: int = 1, cp_rank: int = 0, sparse_top_k: int = 0,
-                 e4m3_widen: bool = False):
+                 e4m3_widen: bool = False, window: int = 0, sinks: int = 0):
         self.params = MlaDecodeParams(
             batch=batch, num_heads=num_heads, max_seq_len_q=max_seq_len_q,
             max_seq_len=max_seq_len, page_size=page_size, max_pages_per_req=max_pages_per_req,
             num_pages=num_pages, packed=int(bool(packed)), max_total_q=max_total_q,
-            kv_dtype=KV_FP8_E4M3 if kv_dtype in ("e4m3", "fp8", torch.float8_e4m3fn) else KV_BF16,
+            kv_dtype=(KV_FP8_E4M3 if kv_dtype in ("e4m3", "fp8", torch.float8_e4m3fn)
+                      else KV_FP4_E2M1 if kv_dtype in ("fp4", "e2m1") else KV_BF16),
             mask=MASK_CAUSAL if causal else MASK_DENSE, return_lse=int(bool(return_lse)),
             device=device,
             q_dtype=Q_FP8_E4M3 if q_dtype in ("e4m3", "fp8", torch.float8_e4m3fn) else Q_BF16,
             cp_world=cp_world, cp_rank=cp_rank, sparse_top_k=sparse_top_k,
-            e4m3_widen=int(bool(e4m3_widen)))
+            e4m3_widen=int(bool(e4m3_widen)), window=window, sinks=sinks)
         self.cp_world = cp_world
         self.sparse_top_k = sparse_top_k
         self.handle, self.workspace_bytes = mla_decode_plan(self.params)
@@ -470,13 +473,15 @@ def decode(query: torch.Tensor, kv_cache: torch.Tensor, workspace_buffer: torch.
            bmm1_scale=1.0, bmm2_scale=1.0, mask_type: str = "causal",
            return_lse: bool = False, cp_world: int = 1, cp_rank: int = 0,
            causal_seqlens_kv_global: Optional[torch.Tensor] = None,
-           sparse_indices: Optional[torch.Tensor] = None, e4m3_widen: bool = False):
+           sparse_indices: Optional[torch.Tensor] = None, e4m3_widen: bool = False,
+           window: int = 0, sinks: int = 0):
     """Paged MLA decode.  Returns ``out`` (and ``lse`` when ``return_lse``).
 
     ``query``: bf16 or float8_e4m3fn (quantised with a q_scale the caller folds
     into ``bmm1_scale``), ``[B, SQ, H, 576]`` (qo_indptr None) or ``[total_q, H, 576]``.
     ``kv_cache``: bf16 or float8_e4m3fn, ``[pages, page_size, 576]`` or
-    ``[pages, 1, page_size, 576]``.  ``workspace_buffer`` must hold at least
+    ``[pages, 1, page_size, 576]``, or 4-bit, uint8 ``[pages, page_size, 324]``
+    (``MLA_KV_FP4_E2M1`` in the header).  ``workspace_buffer`` must hold at least
     the plan's workspace bytes (see ``Plan``).  Plans are cached per static key.
     ``bmm1_scale`` / ``bmm2_scale``: floats, or one-element fp32 CUDA tensors the
     kernels read at run time (for scales that change between graph replays).
@@ -489,22 +494,14 @@ def decode(query: torch.Tensor, kv_cache: torch.Tensor, workspace_buffer: torch.
     ``e4m3_widen``: with an e4m3 cache, widen every e4m3 value exactly to bf16
     and multiply on bf16 tensor cores instead of the FP8 ones (see
     ``mla_decode_params.e4m3_widen`` in ``include/mla_decode.h``).
+    ``window`` > 0: a query row sees the last ``window`` rows up to its bound, and
+    the first ``sinks`` rows.
     """
     if query.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or not query.is_cuda:
         raise ValueError("query must be a bf16 or float8_e4m3fn CUDA tensor")
     q_dtype = "bf16" if query.dtype == torch.bfloat16 else "e4m3"
-    if kv_cache.dim() == 4:
-        if kv_cache.shape[1] != 1:
-            raise ValueError("rank-4 kv_cache must be [pages, 1, page_size, 576]")
-        kv_cache = kv_cache.squeeze(1)
-    if kv_cache.dim() != 3 or kv_cache.shape[-1] != HEAD_DIM_QK:
-        raise ValueError("kv_cache must be [pages, page_size, 576]")
-    if kv_cache.dtype == torch.bfloat16:
-        kv_dtype = "bf16"
-    elif kv_cache.dtype in (torch.float8_e4m3fn, torch.uint8):
-        kv_dtype = "e4m3"
-    else:
-        raise ValueError(f"unsupported kv_cache dtype {kv_cache.dtype}")
+    kv_cache, kind = _cache_kind(kv_cache)
+    kv_dtype = ("bf16", "e4m3", "fp4")[kind]
     packed = qo_indptr is not None
     H = int(query.shape[-2])
     B = int(seq_lens.shape[0])
@@ -527,7 +524,7 @@ def decode(query: torch.Tensor, kv_cache: torch.Tensor, workspace_buffer: torch.
     key = (B, H, sq, int(max_seq_len), int(kv_cache.shape[1]), int(block_tables.shape[1]),
            int(kv_cache.shape[0]), packed, total_q if packed else 0, kv_dtype, causal,
            bool(return_lse), query.device.index or 0, q_dtype, int(cp_world), int(cp_rank),
-           top_k, bool(e4m3_widen))
+           top_k, bool(e4m3_widen), int(window), int(sinks))
     plan = _plans.get(key)
     if plan is None:
         plan = Plan(batch=B, num_heads=H, max_seq_len_q=sq, max_seq_len=int(max_seq_len),
@@ -535,7 +532,8 @@ def decode(query: torch.Tensor, kv_cache: torch.Tensor, workspace_buffer: torch.
                     num_pages=int(kv_cache.shape[0]), packed=packed, max_total_q=total_q,
                     kv_dtype=kv_dtype, causal=causal, return_lse=return_lse,
                     device=query.device.index or 0, q_dtype=q_dtype, cp_world=int(cp_world),
-                    cp_rank=int(cp_rank), sparse_top_k=top_k, e4m3_widen=e4m3_widen)
+                    cp_rank=int(cp_rank), sparse_top_k=top_k, e4m3_widen=e4m3_widen,
+                    window=int(window), sinks=int(sinks))
         _plans[key] = plan
     if workspace_buffer.numel() * workspace_buffer.element_size() < plan.workspace_bytes:
         raise ValueError(f"workspace_buffer needs {plan.workspace_bytes} bytes")

@@ -27,6 +27,8 @@ cudaError_t launch_qsplit(const Problem& p, const Layout& lay, void* ws, int sm_
                           cudaStream_t stream);
 cudaError_t launch_decode_sm103(const Problem& p, const Layout& lay, void* ws,
                                 cudaStream_t stream);
+cudaError_t decode_fp4_setup(int sm_count, int* n_pairs);
+cudaError_t launch_decode_fp4(const Problem& p, const Layout& lay, void* ws, cudaStream_t stream);
 }  // namespace mla
 
 struct mla_plan_s {
@@ -135,7 +137,8 @@ int mla_decode_plan(const mla_decode_params* params, mla_plan_t** plan, size_t* 
     return MLA_ERR_INVALID_ARG;
   if (p.packed != 0 && p.packed != 1) return MLA_ERR_INVALID_ARG;
   if (p.packed && p.max_total_q < 0) return MLA_ERR_INVALID_ARG;
-  if (p.kv_dtype != MLA_KV_BF16 && p.kv_dtype != MLA_KV_FP8_E4M3) return MLA_ERR_INVALID_ARG;
+  if (p.kv_dtype != MLA_KV_BF16 && p.kv_dtype != MLA_KV_FP8_E4M3 && p.kv_dtype != MLA_KV_FP4_E2M1)
+    return MLA_ERR_INVALID_ARG;
   if (p.q_dtype != MLA_Q_BF16 && p.q_dtype != MLA_Q_FP8_E4M3) return MLA_ERR_INVALID_ARG;
   if (p.mask != MLA_MASK_CAUSAL && p.mask != MLA_MASK_DENSE) return MLA_ERR_INVALID_ARG;
   if (p.cp_world < 0 || (p.cp_world <= 1 && p.cp_rank != 0) ||
@@ -143,6 +146,11 @@ int mla_decode_plan(const mla_decode_params* params, mla_plan_t** plan, size_t* 
     return MLA_ERR_INVALID_ARG;
   if (p.sparse_top_k < 0 || p.sparse_top_k > (1 << 24) || (p.sparse_top_k > 0 && p.cp_world > 1))
     return MLA_ERR_INVALID_ARG;
+  if (p.window < 0 || p.sinks < 0 || p.sinks > (1 << 30) || (p.window == 0 && p.sinks > 0))
+    return MLA_ERR_INVALID_ARG;
+  if (p.window > 0 && (p.cp_world > 1 || p.sparse_top_k > 0)) return MLA_ERR_UNSUPPORTED;
+  if (p.window > 0 && p.kv_dtype != MLA_KV_FP4_E2M1) return MLA_ERR_UNSUPPORTED;
+  if (p.kv_dtype == MLA_KV_FP4_E2M1 && p.sparse_top_k > 0) return MLA_ERR_UNSUPPORTED;
   if (!supported_heads(p.num_heads)) return MLA_ERR_UNSUPPORTED;
   if (p.page_size != 32 && p.page_size != 64) return MLA_ERR_UNSUPPORTED;
   // cache rows are addressed with 32-bit row coordinates
@@ -159,7 +167,9 @@ int mla_decode_plan(const mla_decode_params* params, mla_plan_t** plan, size_t* 
   int sms = 0, n_pairs = 0;
   cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, p.device);
   if (e == cudaSuccess)
-    e = mla::decode_sm103_setup(p.kv_dtype, p.sparse_top_k > 0, uses_f8_mma(p), sms, &n_pairs);
+    e = p.kv_dtype == MLA_KV_FP4_E2M1
+            ? mla::decode_fp4_setup(sms, &n_pairs)
+            : mla::decode_sm103_setup(p.kv_dtype, p.sparse_top_k > 0, uses_f8_mma(p), sms, &n_pairs);
   if (e == cudaSuccess) e = mla::partition_setup();
   cudaStream_t side = nullptr;
   if (e == cudaSuccess) e = cudaStreamCreateWithFlags(&side, cudaStreamNonBlocking);
@@ -319,6 +329,8 @@ int run_impl(const mla_plan_t* plan, const void* query, const void* kv_cache,
   p.qo_indptr = prm.packed ? qo_indptr : nullptr;
   p.out = out;
   p.lse = prm.return_lse ? lse : nullptr;
+  p.window = prm.window;
+  p.sinks = prm.sinks;
 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // while the stream is being captured into a graph, the events become
@@ -340,7 +352,10 @@ int run_impl(const mla_plan_t* plan, const void* query, const void* kv_cache,
       cudaEventRecordWithFlags(static_cast<cudaEvent_t>(event_before_decode), s, ev_flags) !=
           cudaSuccess)
     return MLA_ERR_CUDA;
-  if (mla::launch_decode_sm103(p, plan->lay, workspace, s) != cudaSuccess) return MLA_ERR_CUDA;
+  if ((prm.kv_dtype == MLA_KV_FP4_E2M1 ? mla::launch_decode_fp4(p, plan->lay, workspace, s)
+                                       : mla::launch_decode_sm103(p, plan->lay, workspace, s)) !=
+      cudaSuccess)
+    return MLA_ERR_CUDA;
   if (event_after_decode &&
       cudaEventRecordWithFlags(static_cast<cudaEvent_t>(event_after_decode), s, ev_flags) !=
           cudaSuccess)

@@ -41,7 +41,24 @@ struct Problem {
   const int* sparse_idx;         // [tokens, sparse_k] logical KV positions, or nullptr
   void* out;                     // bf16 [tokens, H, 512]
   float* lse;                    // fp32 [tokens, H] or nullptr
+  int window, sinks;             // window > 0: query row i sees the last `window` rows up to
+                                 // its bound and the first `sinks` rows
 };
+
+// Sliding window: rows of a request that its work leaves out.  Query row 0 (the
+// earliest) sees rows from lo = last - window + 1 on, the others later ones, and
+// every row the first `sinks`.  Work items walk virtual rows: [0, s) are the
+// rows themselves, s = sinks rounded up to whole tiles, and virtual row v >= s is
+// row v + skip; skip is a multiple of a tile, so a tile never straddles the gap.
+__host__ __device__ inline int window_sink_rows(int sinks) {
+  return (sinks + kKvTile - 1) / kKvTile * kKvTile;
+}
+__host__ __device__ inline int window_skip(int window, int sinks, int causal, int L, int q) {
+  if (window <= 0) return 0;
+  const int lo = (causal ? L - q : L - 1) - window + 1;
+  const int first = lo > 0 ? lo / kKvTile * kKvTile : 0, s = window_sink_rows(sinks);
+  return first > s ? first - s : 0;
+}
 
 // bmm1 of this run: the host value, or the device value when one was given.
 // A negative or non-finite device value sets kStatusScale and reads as 0.

@@ -17,7 +17,8 @@
 // becomes a separate item writing a partial; every other group is one item
 // writing the output directly.  So workers are balanced to within one tile
 // plus one overhead, and there are at most n + #groups items and n - 1 cut
-// points.  Under sparse top-k selection a group is one token's H rows and its
+// points.  Under a sliding window L counts the rows that the window and the sinks
+// reach (virtual rows, see window_skip).  Under sparse top-k selection a group is one token's H rows and its
 // KV range is the token's list of k positions (T = ceil(k / 64)).  One CTA
 // of 128-1024 threads; the range boundaries are tabulated in shared memory
 // once, so cut points and owners are table lookups.
@@ -169,8 +170,11 @@ partition_kernel(Problem p, Layout lay, char* __restrict__ ws) {
   const int R = lay.rows_per_group;
   const int H = p.num_heads;
   const bool sparse = p.sparse_k > 0;
-  // KV rows a group of request b walks: its cache rows, or the token's list
-  auto kv_rows = [&](int L) { return sparse ? p.sparse_k : L; };
+  // KV rows a group of a request (length L, q tokens) walks: its cache rows, those
+  // its sliding window reaches, or the token's list
+  auto kv_rows = [&](int L, int q) {
+    return sparse ? p.sparse_k : L - window_skip(p.window, p.sinks, p.causal, L, q);
+  };
   // per-request and per-group scratch: in shared memory when it fits (no
   // memory round trip between the phases below), else in the workspace
   extern __shared__ __align__(16) unsigned char scratch_smem[];
@@ -271,7 +275,7 @@ partition_kernel(Problem p, Layout lay, char* __restrict__ ws) {
   for (int b = threadIdx.x; b < B && n_groups > 0; b += blockDim.x) {
     const int gb = r_gbase[b];  // scanned: first group of request b
     const int ge = (b + 1 < B) ? r_gbase[b + 1] : n_groups;
-    W_total += (long long)(ge - gb) * (kOverheadTiles + (kv_rows(r_len[b]) + kKvTile - 1) / kKvTile);
+    W_total += (long long)(ge - gb) * (kOverheadTiles + (kv_rows(r_len[b], r_qlen[b]) + kKvTile - 1) / kKvTile);
   }
   __syncthreads();
   if (threadIdx.x == 0) sh.carry_ll = 0;
@@ -289,7 +293,7 @@ partition_kernel(Problem p, Layout lay, char* __restrict__ ws) {
   for (int b = threadIdx.x; b < B; b += blockDim.x) {
     const int gb = r_gbase[b];
     const int ge = (b + 1 < B) ? r_gbase[b + 1] : n_groups;
-    const int T = (kv_rows(r_len[b]) + kKvTile - 1) / kKvTile;
+    const int T = (kv_rows(r_len[b], r_qlen[b]) + kKvTile - 1) / kKvTile;
     for (int g = gb; g < ge && g < n_groups; ++g) {
       const int k = g - gb;
       const int slot = lanes > 1 ? k * n_req_groups + gb / G : g;
@@ -316,7 +320,7 @@ partition_kernel(Problem p, Layout lay, char* __restrict__ ws) {
   // 3. Cut points inside each group -> chunk counts.
   for (int g = threadIdx.x; g < n_groups; g += blockDim.x) {
     const int b = g_req[g];
-    const int T = (kv_rows(r_len[b]) + kKvTile - 1) / kKvTile;
+    const int T = (kv_rows(r_len[b], r_qlen[b]) + kKvTile - 1) / kKvTile;
     const long long S = g_start[g], c = kOverheadTiles + T;
     int nch = 1;
     if (W > 0) {
@@ -350,7 +354,7 @@ partition_kernel(Problem p, Layout lay, char* __restrict__ ws) {
     for (int g = threadIdx.x; g < n_groups; g += blockDim.x) {
       const int b = g_req[g];
       const int L = r_len[b];
-      const int KV = kv_rows(L);
+      const int KV = kv_rows(L, r_qlen[b]);
       const int T = (KV + kKvTile - 1) / kKvTile;
       const long long S = g_start[g], c = kOverheadTiles + T;
       const int nch = g_nch[g];
@@ -551,7 +555,10 @@ partition_warp_kernel(Problem p, Layout lay, char* __restrict__ ws) {
   const int R = lay.rows_per_group;
   const int H = p.num_heads;
   const bool sparse = p.sparse_k > 0;
-  auto tiles_of = [&](int L) { return ((sparse ? p.sparse_k : L) + kKvTile - 1) / kKvTile; };
+  auto kv_rows = [&](int L, int q) {
+    return sparse ? p.sparse_k : L - window_skip(p.window, p.sinks, p.causal, L, q);
+  };
+  auto tiles_of = [&](int L, int q) { return (kv_rows(L, q) + kKvTile - 1) / kKvTile; };
 
   // 1. Per-request lengths (clamped and flagged as in the block kernel) and
   //    the request's number of row groups, over the lane's run of requests.
@@ -587,7 +594,7 @@ partition_warp_kernel(Problem p, Layout lay, char* __restrict__ ws) {
       g_max = max(g_max, gc);
     }
     my_groups += gc;
-    my_cost += (long long)gc * (kOverheadTiles + tiles_of(L));
+    my_cost += (long long)gc * (kOverheadTiles + tiles_of(L, q));
   }
   status = warp_or(status);
   g_min = warp_min(g_min);
@@ -618,7 +625,7 @@ partition_warp_kernel(Problem p, Layout lay, char* __restrict__ ws) {
   for (int b = rb.lo; b < rb.hi; ++b) {
     const int gb = sh.gbase[b];
     const int ge = (b + 1 < B) ? sh.gbase[b + 1] : n_groups;
-    const int T = tiles_of(sh.len[b]);
+    const int T = tiles_of(sh.len[b], sh.q[b]);
     for (int g = gb; g < ge && g < n_groups; ++g) {
       const int k = g - gb;
       const int slot = lanes > 1 ? k * n_req_groups + gb / G : g;
@@ -656,7 +663,7 @@ partition_warp_kernel(Problem p, Layout lay, char* __restrict__ ws) {
   //    slot and combine entry bases of every group.
   int s_items = 0, s_slot = 0, s_comb = 0;
   for (int g = rg.lo; g < rg.hi; ++g) {
-    const int T = tiles_of(sh.len[sh.g_req[g]]);
+    const int T = tiles_of(sh.len[sh.g_req[g]], sh.q[sh.g_req[g]]);
     const long long S = sh.g_start[g], c = kOverheadTiles + T;
     int nch = 1;
     if (W > 0) {
@@ -702,8 +709,8 @@ partition_warp_kernel(Problem p, Layout lay, char* __restrict__ ws) {
     for (int g = rg.lo; g < rg.hi; ++g) {
       const int b = sh.g_req[g];
       const int L = sh.len[b];
-      const int KV = sparse ? p.sparse_k : L;
-      const int T = tiles_of(L);
+      const int KV = kv_rows(L, sh.q[b]);
+      const int T = tiles_of(L, sh.q[b]);
       const long long S = sh.g_start[g], c = kOverheadTiles + T;
       const int nch = sh.g_nch[g];
       int k = 0, prev = 0;
