@@ -57,6 +57,7 @@ constexpr int kCtaRows = 64;         // query rows of a CTA
 constexpr int kRows = 2 * kCtaRows;  // query rows of a work item
 constexpr int kChunks = 9;           // 64-dim chunks of a row: 8 latent, 1 RoPE
 constexpr int kKSlots = 12;
+constexpr int kGroup = 3;            // chunks that share a full and an empty barrier
 constexpr int kConvWarps = 8;
 constexpr int kSoftWarps = 4;
 constexpr int kFirstSoft = 2, kFirstConv = kFirstSoft + kSoftWarps;
@@ -102,9 +103,9 @@ constexpr uint32_t TM_S = 256;  // two 32-column buffers; lane: query row and KV
 
 enum Bar {
   STG_FULL0, STG_EMPTY0 = STG_FULL0 + 2,
-  K_FULL0 = STG_EMPTY0 + 2,            // even CTA: both CTAs' chunk is in its slot
-  K_EMPTY0 = K_FULL0 + kKSlots,
-  V_FULL0 = K_EMPTY0 + kKSlots,        // even CTA
+  K_FULL0 = STG_EMPTY0 + 2,            // even CTA: both CTAs' chunks are in a group's slots
+  K_EMPTY0 = K_FULL0 + kKSlots / kGroup,
+  V_FULL0 = K_EMPTY0 + kKSlots / kGroup,  // even CTA
   PV_DONE0 = V_FULL0 + 2,              // by tile parity: V stage and P free, O stable
   S_FULL0 = PV_DONE0 + 2, S_EMPTY0 = S_FULL0 + 2,  // S_EMPTY: even CTA
   P_FULL = S_EMPTY0 + 2,               // even CTA
@@ -140,22 +141,12 @@ __device__ __forceinline__ bool wait_bar(const Ctx& c, int bar, uint32_t parity)
   give_up(c);
   return false;
 }
-// The same for barriers that the other CTA's threads arrive on.
-__device__ __forceinline__ bool wait_bar_cluster(const Ctx& c, int bar, uint32_t parity) {
-  uint64_t* b = &c.bars[bar];
-  for (uint32_t i = 0; i < kWaitLimit; ++i) {
-    if (mbar_try_wait_acq_cluster(b, parity)) return true;
-    if ((i & 1023) == 1023 && *c.abort) return false;
-  }
-  give_up(c);
-  return false;
-}
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
   for (uint32_t i = 0; i < kWaitLimit; ++i)
     if (mbar_try_wait(bar, parity)) return;
 }
 __device__ __forceinline__ void arrive_leader(const Ctx& c, int bar, uint32_t count) {
-  mbar_arrive_cluster(c.leader_bars + 8u * bar, count);
+  mbar_arrive_pair(c.leader_bars + 8u * bar, count);
 }
 
 __device__ __forceinline__ int n_tiles_of(const WorkItem& it) {
@@ -255,9 +246,11 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
 
   if (tid == 0) {
     for (int i = 0; i < NUM_BARS; ++i) {
-      uint32_t n = 1;  // copies' expect, or one commit
+      uint32_t n = 1;  // one commit
+      if (i >= STG_FULL0 && i < STG_FULL0 + 2) n = 1 + 32;  // bulk copies, each lane's own
       if (i >= STG_EMPTY0 && i < STG_EMPTY0 + 2) n = kConvWarps;
-      if (i >= K_FULL0 && i < K_FULL0 + kKSlots) n = 8;  // a latent chunk's warp counts four times
+      // a latent chunk's warp counts four times, as the RoPE chunk has four warps
+      if (i >= K_FULL0 && i < K_FULL0 + kKSlots / kGroup) n = 2 * 4 * kGroup;
       if (i >= V_FULL0 && i < V_FULL0 + 2) n = 2 * kConvWarps;
       if (i >= S_EMPTY0 && i < S_EMPTY0 + 2) n = 2 * kSoftWarps;
       if (i == P_FULL) n = 2 * kSoftWarps;
@@ -289,8 +282,9 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
   if (warp == 0) {
     // ------------------------------------------------------------ copies
     // Page ids a batch of 32 ahead (one per lane), as virtual page slots of the
-    // item.  Lane 0 copies codes and scales of the own rows and the other rows'
-    // scales, every lane one of the other rows' V codes (128 bytes).
+    // item.  Lane 0 issues the bulk copies (codes of the own rows, scales); the
+    // other rows' V codes, 128 bytes of each 288, go by 16-byte copies of all
+    // lanes (one bulk copy a row took 4000 cycles to issue).
     const int ps = p.page_size, npg = kTile / ps;
     const size_t page_bytes = (size_t)ps * kFp4RowBytes;
     const unsigned char* cache = static_cast<const unsigned char*>(p.kv_cache);
@@ -334,8 +328,7 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
           }
           page[h] = cache + (size_t)(on[h] ? pages[h] : 0) * page_bytes;
           row[h] = ps == kTile ? h * kHalf : 0;
-          if (on[h])
-            bytes += (h == rank ? kHalf * kFp4CodeBytes : kHalf * 128) + kHalf * kFp4ScaleBytes;
+          if (on[h]) bytes += (h == rank ? kHalf * kFp4CodeBytes : 0) + kHalf * kFp4ScaleBytes;
         }
         unsigned char* stg = sm + OFF_STG + s * kStage;
         uint64_t* full = &c.bars[STG_FULL0 + s];
@@ -354,10 +347,17 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
           }
         }
         __syncwarp();
+        // the other rows' V codes, eight 16-byte units of a row: eight lanes a row
         const int o = rank ^ 1;
-        if (on[o])
-          bulk_load(stg + STG_OTHER + lane * 128,
-                    page[o] + (row[o] + lane) * kFp4CodeBytes + 128 * rank, 128, full);
+        if (on[o]) {
+          const unsigned char* src = page[o] + row[o] * kFp4CodeBytes + 128 * rank + 16 * (lane & 7);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int r = 4 * k + (lane >> 3);
+            cp_async_16(stg + STG_OTHER + r * 128 + 16 * (lane & 7), src + r * kFp4CodeBytes);
+          }
+        }
+        cp_async_arrive(full);
       }
     }
   done_copy:
@@ -369,62 +369,78 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
       }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issue
-    if (rank == 0 && lane == 0) {
+    // The whole warp walks the loops and one lane issues (see elect_one).
+    if (rank == 0) {
       constexpr uint32_t idesc_qk = idesc_half(kRows, kTile, false, false);
       constexpr uint32_t idesc_pv = idesc_half(kRows, 256, false, true);
-      const uint32_t q_base = smem_u32(sm + OFF_Q), k_base = smem_u32(sm + OFF_K);
-      const uint32_t v_base = smem_u32(sm + OFF_V), p_base = smem_u32(sm + OFF_P);
-      uint32_t g = 0;      // tile whose QK comes next
-      uint32_t slot = 0, round = 0;  // ring place of its next chunk
+      // operand descriptors; a step along an operand adds its bytes / 16
+      const uint64_t q_desc = smem_desc(smem_u32(sm + OFF_Q), 16, 1024, kSwizzle128B);
+      const uint64_t k_desc = smem_desc(smem_u32(sm + OFF_K), 16, 1024, kSwizzle128B);
+      const uint64_t p_desc = smem_desc(smem_u32(sm + OFF_P), 16, 1024, kSwizzle128B);
+      const uint64_t v_desc = smem_desc(smem_u32(sm + OFF_V), kVChunk, 1024, kSwizzle128B);
+      uint32_t g = 0;                 // tile whose QK comes next
+      uint32_t group = 0, round = 0;  // ring place of its next three chunks
       int n_item = 0;
       auto pv = [&](uint32_t gp, bool first) -> bool {
-        const int s = gp & 1;
-        if (!wait_bar_cluster(c, V_FULL0 + s, (gp >> 1) & 1)) return false;
-        if (!wait_bar_cluster(c, P_FULL, gp & 1)) return false;
+        const uint32_t s = gp & 1;
+        if (!wait_bar(c, V_FULL0 + s, (gp >> 1) & 1)) return false;
+        if (!wait_bar(c, P_FULL, gp & 1)) return false;
         tc_fence_after();
-        for (int ks = 0; ks < kTile / 16; ++ks) {
-          const uint64_t a = smem_desc(p_base + ks * 32, 16, 1024, kSwizzle128B);
-          for (int j = 0; j < 2; ++j) {
-            const uint64_t b = smem_desc(v_base + s * kVStage + j * 2 * kVChunk + ks * 16 * 128,
-                                         kVChunk, 1024, kSwizzle128B);
-            mma_f16_pair_ss(tmem + TM_O + 128 * j, a, b, idesc_pv, (first && ks == 0) ? 0u : 1u);
-          }
+        if (elect_one()) {
+          const uint64_t v = v_desc + s * (kVStage >> 4);
+#pragma unroll
+          for (int ks = 0; ks < kTile / 16; ++ks)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              mma_f16_pair_ss(tmem + TM_O + 128 * j, p_desc + 2 * ks,
+                              v + ((j * 2 * kVChunk + ks * 16 * 128) >> 4), idesc_pv,
+                              (first && ks == 0) ? 0u : 1u);
+          mma_commit_pair(&c.bars[PV_DONE0 + s]);
         }
-        mma_commit_pair(&c.bars[PV_DONE0 + s]);
+        __syncwarp();
         return true;
       };
       for (int idx = item_begin; idx < item_end; ++idx) {
-        const WorkItem it = items[idx];
-        const int nt = n_tiles_of(it);
+        const int nt = __shfl_sync(0xffffffffu, n_tiles_of(items[idx]), 0);
         if (nt <= 0) continue;
-        if (!wait_bar_cluster(c, Q_FULL, n_item & 1)) goto done_mma;
+        if (!wait_bar(c, Q_FULL, n_item & 1)) goto done_mma;
         ++n_item;
         for (int t = 0; t < nt; ++t, ++g) {
-          const int sb = g & 1;
-          if (!wait_bar_cluster(c, S_EMPTY0 + sb, ((g >> 1) & 1) ^ 1)) goto done_mma;
-          for (int k = 0; k < kChunks; ++k) {
-            if (!wait_bar_cluster(c, K_FULL0 + slot, round & 1)) goto done_mma;
-            tc_fence_after();
+          const uint32_t sb = g & 1;
+          if (!wait_bar(c, S_EMPTY0 + sb, ((g >> 1) & 1) ^ 1)) goto done_mma;
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              mma_f16_pair_ss(tmem + TM_S + 32 * sb,
-                              smem_desc(q_base + k * kQChunk + ks * 32, 16, 1024, kSwizzle128B),
-                              smem_desc(k_base + slot * kKChunk + ks * 32, 16, 1024, kSwizzle128B),
-                              idesc_qk, (k | ks) != 0 ? 1u : 0u);
-            mma_commit_pair(&c.bars[K_EMPTY0 + slot]);
-            if (++slot == kKSlots) {
-              slot = 0;
+          for (int k3 = 0; k3 < kChunks / kGroup; ++k3) {
+            if (!wait_bar(c, K_FULL0 + group, round & 1)) goto done_mma;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t kd = k_desc + group * (kGroup * kKChunk >> 4);
+#pragma unroll
+              for (int k = 0; k < kGroup; ++k)
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                  mma_f16_pair_ss(tmem + TM_S + 32 * sb,
+                                  q_desc + ((kGroup * k3 + k) * kQChunk >> 4) + 2 * ks,
+                                  kd + (k * kKChunk >> 4) + 2 * ks, idesc_qk,
+                                  (k3 | k | ks) != 0 ? 1u : 0u);
+              mma_commit_pair(&c.bars[K_EMPTY0 + group]);
+              if (k3 == kChunks / kGroup - 1) {
+                mma_commit_pair(&c.bars[S_FULL0 + sb]);
+                if (t + 1 == nt) mma_commit_pair(&c.bars[Q_EMPTY]);
+              }
+            }
+            __syncwarp();
+            if (++group == kKSlots / kGroup) {
+              group = 0;
               ++round;
             }
           }
-          mma_commit_pair(&c.bars[S_FULL0 + sb]);
-          if (t + 1 == nt) mma_commit_pair(&c.bars[Q_EMPTY]);
           if (t > 0 && !pv(g - 1, t == 1)) goto done_mma;
         }
         if (!pv(g - 1, nt == 1)) goto done_mma;
       }
     done_mma:
-      mma_commit_pair(&c.bars[DRAIN]);
+      __syncwarp();
+      if (elect_one()) mma_commit_pair(&c.bars[DRAIN]);
       drain_wait(&c.bars[DRAIN], 0);
     }
   } else if (warp < kFirstConv) {
@@ -628,37 +644,32 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
       const uint32_t sc = on_own ? *reinterpret_cast<const uint32_t*>(sc_own + 4 * w) : 0u;
       const uint4* src = reinterpret_cast<const uint4*>(stg + STG_OWN + lane * kFp4CodeBytes + 32 * w);
       uint4 c0 = src[0], c1 = src[1];
-      if (!wait_bar(c, K_EMPTY0 + kslot, (kround & 1) ^ 1)) return false;
-      if (in_half && !wait_bar(c, PV_DONE0 + s, ((g >> 1) & 1) ^ 1)) return false;
+      uint4 x[8];
       {
-        unsigned char* kd = sm + OFF_K + kslot * kKChunk + lane * 128;
-        unsigned char* vd = sm + OFF_V + s * kVStage + vc * kVChunk + (kHalf * rank + lane) * 128;
         const uint32_t cw[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint4 lo, hi;
-          convert16(cw[2 * e], cw[2 * e + 1], scale_pair((sc >> (8 * e)) & 0xFFu), lo, hi);
-          put(kd, 2 * e, lane, lo);
-          put(kd, 2 * e + 1, lane, hi);
-          if (in_half) {
-            put(vd, 2 * e, lane, lo);
-            put(vd, 2 * e + 1, lane, hi);
-          }
-        }
+        for (int e = 0; e < 4; ++e)
+          convert16(cw[2 * e], cw[2 * e + 1], scale_pair((sc >> (8 * e)) & 0xFFu), x[2 * e], x[2 * e + 1]);
       }
+      if (!wait_bar(c, K_EMPTY0 + kslot / kGroup, (kround & 1) ^ 1)) return false;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) put(sm + OFF_K + kslot * kKChunk + lane * 128, e, lane, x[e]);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) arrive_leader(c, K_FULL0 + kslot, 4);
+      if (lane == 0) arrive_leader(c, K_FULL0 + kslot / kGroup, 4);
       if (in_half) {
         // a quarter of the RoPE chunk
         const uint32_t rs = on_own ? (uint32_t)sc_own[32 + vc] : 0u;
         const uint2 rc = *reinterpret_cast<const uint2*>(stg + STG_OWN + lane * kFp4CodeBytes + 256 + 8 * vc);
-        if (!wait_bar(c, K_EMPTY0 + rslot, (rround & 1) ^ 1)) return false;
+        if (!wait_bar(c, K_EMPTY0 + rslot / kGroup, (rround & 1) ^ 1)) return false;
         unsigned char* rd = sm + OFF_K + rslot * kKChunk + lane * 128;
         uint4 lo, hi;
         convert16(rc.x, rc.y, scale_pair(rs), lo, hi);
         put(rd, 2 * vc, lane, lo);
         put(rd, 2 * vc + 1, lane, hi);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) arrive_leader(c, K_FULL0 + rslot / kGroup, 1);
       } else {
         const uint32_t so = on_oth ? *reinterpret_cast<const uint32_t*>(
                                          stg + STG_SCALES + (kHalf * (rank ^ 1) + lane) * kFp4ScaleBytes +
@@ -667,24 +678,23 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
         const uint4* os = reinterpret_cast<const uint4*>(stg + STG_OTHER + lane * 128 + 32 * vc);
         c0 = os[0];
         c1 = os[1];
-        if (!wait_bar(c, PV_DONE0 + s, ((g >> 1) & 1) ^ 1)) return false;
-        unsigned char* vd = sm + OFF_V + s * kVStage + vc * kVChunk + (kHalf * (rank ^ 1) + lane) * 128;
         const uint32_t cw[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint4 lo, hi;
-          convert16(cw[2 * e], cw[2 * e + 1], scale_pair((so >> (8 * e)) & 0xFFu), lo, hi);
-          put(vd, 2 * e, lane, lo);
-          put(vd, 2 * e + 1, lane, hi);
-        }
+        for (int e = 0; e < 4; ++e)
+          convert16(cw[2 * e], cw[2 * e + 1], scale_pair((so >> (8 * e)) & 0xFFu), x[2 * e], x[2 * e + 1]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c.bars[STG_EMPTY0 + s]);  // every code is in registers
+      // V: the own rows' chunk once more (V dims of this CTA), or the other rows'
+      if (!wait_bar(c, PV_DONE0 + s, ((g >> 1) & 1) ^ 1)) return false;
+      {
+        unsigned char* vd = sm + OFF_V + s * kVStage + vc * kVChunk + (in_half ? own : oth) * 128;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) put(vd, e, lane, x[e]);
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&c.bars[STG_EMPTY0 + s]);
-        if (in_half) arrive_leader(c, K_FULL0 + rslot, 1);
-        arrive_leader(c, V_FULL0 + s, 1);
-      }
+      if (lane == 0) arrive_leader(c, V_FULL0 + s, 1);
       // nine chunks a tile through twelve slots
       kslot += kChunks;
       if (kslot >= kKSlots) {

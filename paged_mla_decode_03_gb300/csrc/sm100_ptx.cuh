@@ -445,6 +445,14 @@ __host__ __device__ constexpr uint32_t idesc_half(int M, int N, bool a_mn_major,
   return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
+// One lane of a converged warp.  MMAs are issued inside `if (elect_one())`, with
+// everything else done by the whole warp: the descriptors then stay in uniform
+// registers (19 cycles an MMA; under `if (lane == 0)` it was 60).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ void mma_f16_pair_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                                 uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -463,11 +471,20 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
       : "memory");
 }
 // Arrive `count` times on a barrier of any CTA of the cluster (shared::cluster
-// address), releasing this thread's earlier writes to the cluster.
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar, uint32_t count) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_bar),
-               "r"(count)
+// address).  The release is at CTA scope: for what only this CTA's own shared
+// memory and TMEM hold and its own tensor core reads (a cluster-scope release is
+// a memory barrier of about a thousand cycles).
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_bar, uint32_t count) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_bar), "r"(count)
                : "memory");
+}
+// 16 bytes, asynchronously and past L1; the arrival counts on `bar` (as one of
+// its expected arrivals) once this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 // Untiled copy of `bytes` (a multiple of 16) between 16-byte aligned addresses.
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
