@@ -26,15 +26,14 @@
 //  * O = P V (M = 128, N = 256 twice): CTA r provides V dims [256 r, 256 r +
 //    256) of all 64 rows, two stages of 32 KB.
 // The codes come by bulk copies into a two-stage staging area (the CTA's own
-// rows whole, of the other rows only its V dims), and eight warps turn them
-// into f16 in the swizzled operand layouts: warp w the w-th latent chunk of the
-// own rows, then a share of the rest, one row a lane.
+// rows whole, of the other rows only its V dims), and sixteen warps turn them
+// into f16 in the swizzled operand layouts, one row a lane.
 //
-// Warp roles (448 threads): 0 copies, 1 MMA issue (even CTA) and TMEM, 2-5
-// softmax, correction and epilogue (thread = TMEM lane = row and column half),
-// 6-13 conversion and query load.  QK of tile t + 1 is issued before PV of tile
-// t, so the tensor cores work while the softmax of tile t runs.  Every wait is
-// bounded; a timeout sets the status word and both CTAs unwind.
+// Warp roles (896 threads): 0 copies, 1 issues QK (even CTA) and owns TMEM, 2
+// issues PV, 4-11 softmax, correction and epilogue, 12-27 conversion and query
+// load.  QK runs up to two tiles ahead of PV, so the tensor cores work while a
+// softmax runs.  Every wait is bounded; a timeout sets the status word and both
+// CTAs unwind.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -58,9 +57,9 @@ constexpr int kRows = 2 * kCtaRows;  // query rows of a work item
 constexpr int kChunks = 9;           // 64-dim chunks of a row: 8 latent, 1 RoPE
 constexpr int kKSlots = 12;
 constexpr int kGroup = 3;            // chunks that share a full and an empty barrier
-constexpr int kConvWarps = 8;
-constexpr int kSoftWarps = 4;
-constexpr int kFirstSoft = 2, kFirstConv = kFirstSoft + kSoftWarps;
+constexpr int kConvWarps = 16;
+constexpr int kSoftWarps = 8;
+constexpr int kFirstSoft = 4, kFirstConv = kFirstSoft + kSoftWarps;
 constexpr int kThreads = 32 * (kFirstConv + kConvWarps);
 constexpr uint32_t kWaitLimit = 1u << 22;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -84,13 +83,13 @@ constexpr uint32_t STG_OTHER = STG_OWN + kHalf * kFp4CodeBytes;
 constexpr uint32_t STG_SCALES = STG_OTHER + kHalf * 128;
 constexpr uint32_t kStage = STG_SCALES + kTile * kFp4ScaleBytes;
 constexpr uint32_t OFF_BARS = OFF_STG + 2 * kStage;
-constexpr uint32_t OFF_XMAX = OFF_BARS + 512;       // float [2][128]: tile maxima by tile parity
-constexpr uint32_t OFF_XSUM = OFF_XMAX + 2 * 128 * 4;  // float [128]: row sums, end of an item
-constexpr uint32_t OFF_QSCALE = OFF_XSUM + 128 * 4;    // float [4][64]: 2^-k by item
+constexpr uint32_t OFF_XMAX = OFF_BARS + 320;       // float [2][256]: tile maxima by tile parity
+constexpr uint32_t OFF_XSUM = OFF_XMAX + 2 * 256 * 4;  // float [256]: row sums, end of an item
+constexpr uint32_t OFF_QSCALE = OFF_XSUM + 256 * 4;    // float [4][64]: 2^-k by item
 constexpr uint32_t OFF_TMEM = OFF_QSCALE + 4 * kCtaRows * 4;
 constexpr uint32_t OFF_ABORT = OFF_TMEM + 16;
 constexpr uint32_t OFF_LOADED = OFF_ABORT + 16;        // int [2][2]: staged halves, by stage
-constexpr uint32_t kSmemBytes = OFF_LOADED + 16 + 1024;
+constexpr uint32_t kSmemBytes = OFF_LOADED + 16;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 static_assert(OFF_K % 1024 == 0 && OFF_V % 1024 == 0 && OFF_P % 1024 == 0 && kStage % 16 == 0 &&
                   OFF_STG % 16 == 0 && STG_SCALES % 16 == 0 && OFF_BARS % 8 == 0,
@@ -113,11 +112,11 @@ enum Bar {
   QS_FULL0,                            // 4: by item, the query rows' scales are written
   XM0 = QS_FULL0 + 4,                  // 4: [tile parity][pair of warps] maxima exchanged
   XS0 = XM0 + 4,                       // 2: [pair of warps] row sums exchanged
-  EPI = XS0 + 2,                       // the four warps' partial is written
-  DRAIN,
-  NUM_BARS
+  EPI = XS0 + 2,                       // the partial is written
+  DRAIN0,                              // 2: every MMA of an issuing warp has completed
+  NUM_BARS = DRAIN0 + 2
 };
-static_assert(NUM_BARS * 8 <= 512, "barrier area");
+static_assert(NUM_BARS * 8 <= 320, "barrier area");
 
 struct Ctx {
   uint64_t* bars;
@@ -177,13 +176,19 @@ __device__ __forceinline__ uint32_t scale_pair(uint32_t code) {
   asm("{\n .reg .b16 lo;\n mov.b32 {lo, _}, %1;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n}" : "=r"(h) : "r"(code));
   return __byte_perm(h, h, 0x1010);
 }
-// One group: 16 codes (two words) times its scale, as two 16-byte units of f16.
-__device__ __forceinline__ void convert16(uint32_t c0, uint32_t c1, uint32_t scale, uint4& lo, uint4& hi) {
+// Eight codes times their scale, as a 16-byte unit of f16.
+__device__ __forceinline__ uint4 convert8(uint32_t codes, uint32_t scale) {
   uint32_t h[4];
-  e2m1x8_to_f16x2(c0, h);
-  lo = make_uint4(hmul2(h[0], scale), hmul2(h[1], scale), hmul2(h[2], scale), hmul2(h[3], scale));
-  e2m1x8_to_f16x2(c1, h);
-  hi = make_uint4(hmul2(h[0], scale), hmul2(h[1], scale), hmul2(h[2], scale), hmul2(h[3], scale));
+  e2m1x8_to_f16x2(codes, h);
+  return make_uint4(hmul2(h[0], scale), hmul2(h[1], scale), hmul2(h[2], scale), hmul2(h[3], scale));
+}
+// Two groups: 32 codes and their two scales.
+__device__ __forceinline__ void convert32(const uint4 codes, uint32_t scales, uint4 (&x)[4]) {
+  const uint32_t s0 = scale_pair(scales & 0xFFu), s1 = scale_pair(scales >> 8);
+  x[0] = convert8(codes.x, s0);
+  x[1] = convert8(codes.y, s0);
+  x[2] = convert8(codes.z, s1);
+  x[3] = convert8(codes.w, s1);
 }
 __device__ __forceinline__ void put(unsigned char* row, int unit, int r, uint4 v) {
   *reinterpret_cast<uint4*>(row + ((unit ^ (r & 7)) << 4)) = v;
@@ -226,9 +231,14 @@ __device__ __forceinline__ uint4 e4m3x8_to_f16(const uint2 x) {
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* sm = reinterpret_cast<unsigned char*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  // The swizzled tiles need 1024-byte alignment, and there is no room to round
+  // up: the block has no other shared memory, so its dynamic part starts at
+  // offset 0 of its window.  A block placed otherwise reports and leaves.
+  extern __shared__ __align__(1024) unsigned char sm[];
+  if ((smem_u32(sm) & 1023) != 0) {
+    if (threadIdx.x == 0) atomicOr(reinterpret_cast<int*>(ws) + kHdrStatus, kStatusTimeout);
+    return;
+  }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = (int)cluster_ctarank();
   const int worker = (int)cluster_id_x();
@@ -249,14 +259,14 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
       uint32_t n = 1;  // one commit
       if (i >= STG_FULL0 && i < STG_FULL0 + 2) n = 1 + 32;  // bulk copies, each lane's own
       if (i >= STG_EMPTY0 && i < STG_EMPTY0 + 2) n = kConvWarps;
-      // a latent chunk's warp counts four times, as the RoPE chunk has four warps
-      if (i >= K_FULL0 && i < K_FULL0 + kKSlots / kGroup) n = 2 * 4 * kGroup;
+      // a latent chunk's two warps count four times each, as the RoPE chunk has eight
+      if (i >= K_FULL0 && i < K_FULL0 + kKSlots / kGroup) n = 2 * 8 * kGroup;
       if (i >= V_FULL0 && i < V_FULL0 + 2) n = 2 * kConvWarps;
       if (i >= S_EMPTY0 && i < S_EMPTY0 + 2) n = 2 * kSoftWarps;
       if (i == P_FULL) n = 2 * kSoftWarps;
       if (i == Q_FULL) n = 2 * kConvWarps;
       if (i >= QS_FULL0 && i < QS_FULL0 + 4) n = kConvWarps;
-      if (i >= XM0 && i < XS0 + 2) n = 2;
+      if (i >= XM0 && i < XS0 + 2) n = kSoftWarps / 2;
       if (i == EPI) n = kSoftWarps;
       mbar_init(&c.bars[i], n);
     }
@@ -368,49 +378,27 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
         drain_wait(&c.bars[STG_FULL0 + (gi & 1)], (gi >> 1) & 1);
       }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issue
+    // ------------------------------------------------------------ QK issue
     // The whole warp walks the loops and one lane issues (see elect_one).
     if (rank == 0) {
-      constexpr uint32_t idesc_qk = idesc_half(kRows, kTile, false, false);
-      constexpr uint32_t idesc_pv = idesc_half(kRows, 256, false, true);
+      constexpr uint32_t idesc = idesc_half(kRows, kTile, false, false);
       // operand descriptors; a step along an operand adds its bytes / 16
       const uint64_t q_desc = smem_desc(smem_u32(sm + OFF_Q), 16, 1024, kSwizzle128B);
       const uint64_t k_desc = smem_desc(smem_u32(sm + OFF_K), 16, 1024, kSwizzle128B);
-      const uint64_t p_desc = smem_desc(smem_u32(sm + OFF_P), 16, 1024, kSwizzle128B);
-      const uint64_t v_desc = smem_desc(smem_u32(sm + OFF_V), kVChunk, 1024, kSwizzle128B);
-      uint32_t g = 0;                 // tile whose QK comes next
-      uint32_t group = 0, round = 0;  // ring place of its next three chunks
+      uint32_t g = 0;
+      uint32_t group = 0, round = 0;  // ring place of the next three chunks
       int n_item = 0;
-      auto pv = [&](uint32_t gp, bool first) -> bool {
-        const uint32_t s = gp & 1;
-        if (!wait_bar(c, V_FULL0 + s, (gp >> 1) & 1)) return false;
-        if (!wait_bar(c, P_FULL, gp & 1)) return false;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t v = v_desc + s * (kVStage >> 4);
-#pragma unroll
-          for (int ks = 0; ks < kTile / 16; ++ks)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-              mma_f16_pair_ss(tmem + TM_O + 128 * j, p_desc + 2 * ks,
-                              v + ((j * 2 * kVChunk + ks * 16 * 128) >> 4), idesc_pv,
-                              (first && ks == 0) ? 0u : 1u);
-          mma_commit_pair(&c.bars[PV_DONE0 + s]);
-        }
-        __syncwarp();
-        return true;
-      };
       for (int idx = item_begin; idx < item_end; ++idx) {
         const int nt = __shfl_sync(0xffffffffu, n_tiles_of(items[idx]), 0);
         if (nt <= 0) continue;
-        if (!wait_bar(c, Q_FULL, n_item & 1)) goto done_mma;
+        if (!wait_bar(c, Q_FULL, n_item & 1)) goto done_qk;
         ++n_item;
         for (int t = 0; t < nt; ++t, ++g) {
           const uint32_t sb = g & 1;
-          if (!wait_bar(c, S_EMPTY0 + sb, ((g >> 1) & 1) ^ 1)) goto done_mma;
+          if (!wait_bar(c, S_EMPTY0 + sb, ((g >> 1) & 1) ^ 1)) goto done_qk;
 #pragma unroll
           for (int k3 = 0; k3 < kChunks / kGroup; ++k3) {
-            if (!wait_bar(c, K_FULL0 + group, round & 1)) goto done_mma;
+            if (!wait_bar(c, K_FULL0 + group, round & 1)) goto done_qk;
             tc_fence_after();
             if (elect_one()) {
               const uint64_t kd = k_desc + group * (kGroup * kKChunk >> 4);
@@ -420,7 +408,7 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
                 for (int ks = 0; ks < 4; ++ks)
                   mma_f16_pair_ss(tmem + TM_S + 32 * sb,
                                   q_desc + ((kGroup * k3 + k) * kQChunk >> 4) + 2 * ks,
-                                  kd + (k * kKChunk >> 4) + 2 * ks, idesc_qk,
+                                  kd + (k * kKChunk >> 4) + 2 * ks, idesc,
                                   (k3 | k | ks) != 0 ? 1u : 0u);
               mma_commit_pair(&c.bars[K_EMPTY0 + group]);
               if (k3 == kChunks / kGroup - 1) {
@@ -434,21 +422,56 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
               ++round;
             }
           }
-          if (t > 0 && !pv(g - 1, t == 1)) goto done_mma;
         }
-        if (!pv(g - 1, nt == 1)) goto done_mma;
       }
-    done_mma:
+    done_qk:
       __syncwarp();
-      if (elect_one()) mma_commit_pair(&c.bars[DRAIN]);
-      drain_wait(&c.bars[DRAIN], 0);
+      if (elect_one()) mma_commit_pair(&c.bars[DRAIN0]);
+      drain_wait(&c.bars[DRAIN0], 0);
     }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ PV issue
+    // A warp of its own: its waits for P would hold up the next tile's QK.
+    if (rank == 0) {
+      constexpr uint32_t idesc = idesc_half(kRows, 256, false, true);
+      const uint64_t p_desc = smem_desc(smem_u32(sm + OFF_P), 16, 1024, kSwizzle128B);
+      const uint64_t v_desc = smem_desc(smem_u32(sm + OFF_V), kVChunk, 1024, kSwizzle128B);
+      uint32_t g = 0;
+      for (int idx = item_begin; idx < item_end; ++idx) {
+        const int nt = __shfl_sync(0xffffffffu, n_tiles_of(items[idx]), 0);
+        for (int t = 0; t < nt; ++t, ++g) {
+          const uint32_t s = g & 1;
+          if (!wait_bar(c, V_FULL0 + s, (g >> 1) & 1)) goto done_pv;
+          if (!wait_bar(c, P_FULL, g & 1)) goto done_pv;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t v = v_desc + s * (kVStage >> 4);
+#pragma unroll
+            for (int ks = 0; ks < kTile / 16; ++ks)
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                mma_f16_pair_ss(tmem + TM_O + 128 * j, p_desc + 2 * ks,
+                                v + ((j * 2 * kVChunk + ks * 16 * 128) >> 4), idesc,
+                                (t == 0 && ks == 0) ? 0u : 1u);
+            mma_commit_pair(&c.bars[PV_DONE0 + s]);
+          }
+          __syncwarp();
+        }
+      }
+    done_pv:
+      __syncwarp();
+      if (elect_one()) mma_commit_pair(&c.bars[DRAIN0 + 1]);
+      drain_wait(&c.bars[DRAIN0 + 1], 0);
+    }
+  } else if (warp < kFirstSoft) {
+    // (warps 4-11 need TMEM lane quarters 0-3 twice)
   } else if (warp < kFirstConv) {
     // ------------------------------------------------------------ softmax, correction, epilogue
-    // Thread = TMEM lane l = 32 (warp mod 4) + lane: query row l mod 64 of the
-    // CTA, KV columns (of S) or V dims (of O) half l / 64.  The row's other
-    // thread is in warp ^ 2.
-    const int quad = warp & 3;
+    // Thread = TMEM lane l = 32 (warp mod 4) + lane and column part cc: query row
+    // l mod 64 of the CTA, KV rows (columns of S) 32 (l / 64) + 16 cc + [0, 16),
+    // V dims (columns of O) 256 (l / 64) + 128 cc + [0, 128).  A row's four
+    // threads are in four warps that exchange maxima through shared memory.
+    const int quad = warp & 3, cc = (warp - kFirstSoft) >> 2;
     const int l = 32 * quad + lane, hh = quad >> 1, row = l & 63;
     const int q = kCtaRows * rank + row;  // row of the work item
     const int pair = quad & 1;
@@ -488,13 +511,13 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
         const int sb = g & 1;
         if (!wait_bar(c, S_FULL0 + sb, (g >> 1) & 1)) goto done_soft;
         tc_fence_after();
-        float sv[32];
+        float sv[16];
         {
-          uint32_t v[32];
-          tmem_ld_32x32b_x32(tm + TM_S + 32 * sb, v);
+          uint32_t v[16];
+          tmem_ld_32x32b_x16(tm + TM_S + 32 * sb + 16 * cc, v);
           tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 32; ++j) sv[j] = __uint_as_float(v[j]) * scale;
+          for (int j = 0; j < 16; ++j) sv[j] = __uint_as_float(v[j]) * scale;
         }
         tc_fence_before();
         __syncwarp();
@@ -506,31 +529,34 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
                            (r0 >= clean_lo || r0 + kTile <= p.sinks);
         if (!clean) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const int at = r0 + 32 * hh + j;
-            if (!(at <= last && 32 * hh + j < valid && (at >= low || at < p.sinks))) sv[j] = -INFINITY;
+          for (int j = 0; j < 16; ++j) {
+            const int k = 32 * hh + 16 * cc + j, at = r0 + k;
+            if (!(at <= last && k < valid && (at >= low || at < p.sinks))) sv[j] = -INFINITY;
           }
         }
-        float mt[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float mt[4] = {sv[0], sv[1], sv[2], sv[3]};
 #pragma unroll
-        for (int j = 0; j < 32; ++j) mt[j & 3] = fmaxf(mt[j & 3], sv[j]);
-        float m_tile = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
-        xmax[sb * 128 + l] = m_tile;
+        for (int j = 4; j < 16; ++j) mt[j & 3] = fmaxf(mt[j & 3], sv[j]);
+        const float m_own = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
+        float* xm = xmax + sb * 256;
+        xm[128 * cc + l] = m_own;
         __syncwarp();
         if (lane == 0) mbar_arrive(&c.bars[XM0 + 2 * sb + pair]);
         if (!wait_bar(c, XM0 + 2 * sb + pair, (g >> 1) & 1)) goto done_soft;
-        m_tile = fmaxf(m_tile, xmax[sb * 128 + (l ^ 64)]);
+        // (all four from shared memory: the same result in the row's four threads)
+        const float m_tile = fmaxf(fmaxf(xm[row], xm[row + 64]), fmaxf(xm[row + 128], xm[row + 192]));
         const float m_new = (m_tile > m + kRescaleThreshold || t == 0) ? m_tile : m;
         const bool need = t > 0 && m_new != m;
         const float f = need ? ex2(m - m_new) : 1.f;  // m = -inf: 0
         m = m_new;
         l_part *= f;
         const float ref = (m == -INFINITY ? 0.f : m) - kPShift;
-        uint32_t pw[16];
+        // (rows past the request's own compute something that nothing reads)
+        uint32_t pw[8];
         float rs[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float a = row_ok ? ex2(sv[2 * j] - ref) : 0.f, b = row_ok ? ex2(sv[2 * j + 1] - ref) : 0.f;
+        for (int j = 0; j < 8; ++j) {
+          const float a = ex2(sv[2 * j] - ref), b = ex2(sv[2 * j + 1] - ref);
           rs[j & 3] += a + b;
           const __half2 h = __floats2half2_rn(a, b);
           pw[j] = *reinterpret_cast<const uint32_t*>(&h);
@@ -538,38 +564,38 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
         l_part += (rs[0] + rs[1]) + (rs[2] + rs[3]);
         // PV of the previous tile is done: its P may be replaced, and O is stable
         if (g > 0 && !wait_bar(c, PV_DONE0 + ((g - 1) & 1), ((g - 1) >> 1) & 1)) goto done_soft;
-        tc_fence_after();
         if (__any_sync(0xffffffffu, need)) {
+          tc_fence_after();
 #pragma unroll 1
           for (int k = 0; k < 8; ++k) {
-            uint32_t x[32];
-            tmem_ld_32x32b_x32(tm + TM_O + 32 * k, x);
+            uint32_t x[16];
+            tmem_ld_32x32b_x16(tm + TM_O + 128 * cc + 16 * k, x);
             tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * f);
-            tmem_st_32x32b_x16(tm + TM_O + 32 * k, *reinterpret_cast<const uint32_t(*)[16]>(x));
-            tmem_st_32x32b_x16(tm + TM_O + 32 * k + 16, *reinterpret_cast<const uint32_t(*)[16]>(x + 16));
+            for (int j = 0; j < 16; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * f);
+            tmem_st_32x32b_x16(tm + TM_O + 128 * cc + 16 * k, x);
           }
           tmem_wait_st();
           tc_fence_before();
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          put(prow, 4 * hh + u, row, make_uint4(pw[4 * u], pw[4 * u + 1], pw[4 * u + 2], pw[4 * u + 3]));
+        for (int u = 0; u < 2; ++u)
+          put(prow, 4 * hh + 2 * cc + u, row,
+              make_uint4(pw[4 * u], pw[4 * u + 1], pw[4 * u + 2], pw[4 * u + 3]));
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) arrive_leader(c, P_FULL, 1);
       }
-      // the row's sum: both threads' shares
-      xsum[l] = l_part;
+      // the row's sum: its four threads' shares
+      xsum[128 * cc + l] = l_part;
       __syncwarp();
       if (lane == 0) mbar_arrive(&c.bars[XS0 + pair]);
       if (!wait_bar(c, XS0 + pair, n_item & 1)) goto done_soft;
-      const float l_row = l_part + xsum[l ^ 64];
+      const float l_row = (xsum[row] + xsum[row + 64]) + (xsum[row + 128] + xsum[row + 192]);
       const float lse = l_row > 0.f ? (m - kPShift + log2f(l_row)) * kLn2 : -INFINITY;
       const float inv = l_row > 0.f ? 1.f / l_row : 0.f;
       const size_t grow = (size_t)it.q_start * H + row0 + q;
-      if (row_ok && hh == 0) {
+      if (row_ok && hh == 0 && cc == 0) {
         if (it.slot >= 0)
           part_lse[(size_t)it.slot * kRows + q] = lse;
         else if (p.return_lse)
@@ -579,9 +605,9 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
       tc_fence_after();
       const float s2 = it.slot < 0 ? inv * bmm2 : inv;
 #pragma unroll 1
-      for (int k = 0; k < 16; ++k) {
+      for (int k = 0; k < 8; ++k) {
         uint32_t x[16];
-        tmem_ld_32x32b_x16(tm + TM_O + 16 * k, x);
+        tmem_ld_32x32b_x16(tm + TM_O + 128 * cc + 16 * k, x);
         tmem_wait_ld();
         if (!row_ok) continue;
         uint32_t o[8];
@@ -591,24 +617,25 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
                                                          __uint_as_float(x[2 * e + 1]) * s2);
           o[e] = *reinterpret_cast<const uint32_t*>(&h);
         }
+        const int chunk = 16 * hh + 8 * cc + k;  // of 16 dims
         uint4 *d0, *d1;
         if (it.slot < 0) {
-          d0 = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.out) + grow * kVDim + 256 * hh + 16 * k);
+          d0 = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.out) + grow * kVDim + 16 * chunk);
           d1 = d0 + 1;
         } else {
-          d0 = part_o + part_unit(it.slot, kRows, 16 * hh + k, 0, q);
-          d1 = part_o + part_unit(it.slot, kRows, 16 * hh + k, 1, q);
+          d0 = part_o + part_unit(it.slot, kRows, chunk, 0, q);
+          d1 = part_o + part_unit(it.slot, kRows, chunk, 1, q);
         }
         *d0 = make_uint4(o[0], o[1], o[2], o[3]);
         *d1 = make_uint4(o[4], o[5], o[6], o[7]);
       }
       tc_fence_before();
       if (it.slot >= 0) {
-        // the four warps' partial is visible GPU-wide, then this CTA counts its chunk
+        // the warps' partial is visible GPU-wide, then this CTA counts its chunk
         __threadfence();
         __syncwarp();
         if (lane == 0) mbar_arrive(&c.bars[EPI]);
-        if (quad == 0) {
+        if (warp == kFirstSoft) {
           if (!wait_bar(c, EPI, n_split & 1)) goto done_soft;
           if (lane == 0 && it.comb >= 0) {
             __threadfence();
@@ -622,13 +649,16 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
   done_soft:;
   } else {
     // ------------------------------------------------------------ conversion and query load
-    const int w = warp - kFirstConv;       // own latent chunk
-    const bool in_half = (w >> 2) == rank;  // its dims are V dims of this CTA
-    const int vc = w & 3;                   // V chunk: the own rows' (in_half) or the other rows'
+    // Warp w: latent dims [32 w, 32 w + 32) of the own rows, one row a lane, into
+    // K; then, if those are V dims of this CTA, the same values into V and eight
+    // RoPE dims into K, else 32 V dims of the other rows.
+    const int w = warp - kFirstConv;
+    const bool in_half = (w >> 3) == rank;
+    const int vw = w & 7;  // V part of 32 dims; RoPE part of 8
     float* qscale = reinterpret_cast<float*>(sm + OFF_QSCALE);
     uint32_t g = 0;
     // ring places of this warp's chunk and of the RoPE chunk
-    uint32_t kslot = w, kround = 0, rslot = 8, rround = 0;
+    uint32_t kslot = w >> 1, kround = 0, rslot = 8, rround = 0;
     int n_item = 0;
     auto convert_tile = [&](const WorkItem& it, const Walk& walk, int t) -> bool {
       const int s = g & 1;
@@ -639,58 +669,42 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
       const int v0 = it.kv_begin + t * kTile, r0 = walk.row(v0);
       const int own = kHalf * rank + lane, oth = kHalf * (rank ^ 1) + lane;
       const bool on_own = v0 + own < it.kv_end && loaded[2 * s + rank] && walk.seen(r0 + own, r0 + own);
-      const bool on_oth = v0 + oth < it.kv_end && loaded[2 * s + (rank ^ 1)] && walk.seen(r0 + oth, r0 + oth);
-      const unsigned char* sc_own = stg + STG_SCALES + (kHalf * rank + lane) * kFp4ScaleBytes;
-      const uint32_t sc = on_own ? *reinterpret_cast<const uint32_t*>(sc_own + 4 * w) : 0u;
-      const uint4* src = reinterpret_cast<const uint4*>(stg + STG_OWN + lane * kFp4CodeBytes + 32 * w);
-      uint4 c0 = src[0], c1 = src[1];
-      uint4 x[8];
-      {
-        const uint32_t cw[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          convert16(cw[2 * e], cw[2 * e + 1], scale_pair((sc >> (8 * e)) & 0xFFu), x[2 * e], x[2 * e + 1]);
-      }
+      const unsigned char* sc_own = stg + STG_SCALES + own * kFp4ScaleBytes;
+      const unsigned char* codes = stg + STG_OWN + lane * kFp4CodeBytes;
+      const uint32_t sc = on_own ? *reinterpret_cast<const uint16_t*>(sc_own + 2 * w) : 0u;
+      uint4 x[4];
+      convert32(*reinterpret_cast<const uint4*>(codes + 16 * w), sc, x);
       if (!wait_bar(c, K_EMPTY0 + kslot / kGroup, (kround & 1) ^ 1)) return false;
+      {
+        unsigned char* kd = sm + OFF_K + kslot * kKChunk + lane * 128;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) put(sm + OFF_K + kslot * kKChunk + lane * 128, e, lane, x[e]);
+        for (int e = 0; e < 4; ++e) put(kd, 4 * (w & 1) + e, lane, x[e]);
+      }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) arrive_leader(c, K_FULL0 + kslot / kGroup, 4);
       if (in_half) {
-        // a quarter of the RoPE chunk
-        const uint32_t rs = on_own ? (uint32_t)sc_own[32 + vc] : 0u;
-        const uint2 rc = *reinterpret_cast<const uint2*>(stg + STG_OWN + lane * kFp4CodeBytes + 256 + 8 * vc);
+        const uint32_t rs = on_own ? (uint32_t)sc_own[32 + (vw >> 1)] : 0u;
+        const uint4 y = convert8(*reinterpret_cast<const uint32_t*>(codes + 256 + 4 * vw), scale_pair(rs));
         if (!wait_bar(c, K_EMPTY0 + rslot / kGroup, (rround & 1) ^ 1)) return false;
-        unsigned char* rd = sm + OFF_K + rslot * kKChunk + lane * 128;
-        uint4 lo, hi;
-        convert16(rc.x, rc.y, scale_pair(rs), lo, hi);
-        put(rd, 2 * vc, lane, lo);
-        put(rd, 2 * vc + 1, lane, hi);
+        put(sm + OFF_K + rslot * kKChunk + lane * 128, vw, lane, y);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) arrive_leader(c, K_FULL0 + rslot / kGroup, 1);
       } else {
-        const uint32_t so = on_oth ? *reinterpret_cast<const uint32_t*>(
-                                         stg + STG_SCALES + (kHalf * (rank ^ 1) + lane) * kFp4ScaleBytes +
-                                         16 * rank + 4 * vc)
+        const bool on_oth = v0 + oth < it.kv_end && loaded[2 * s + (rank ^ 1)] && walk.seen(r0 + oth, r0 + oth);
+        const uint32_t so = on_oth ? *reinterpret_cast<const uint16_t*>(stg + STG_SCALES + oth * kFp4ScaleBytes +
+                                                                        16 * rank + 2 * vw)
                                    : 0u;
-        const uint4* os = reinterpret_cast<const uint4*>(stg + STG_OTHER + lane * 128 + 32 * vc);
-        c0 = os[0];
-        c1 = os[1];
-        const uint32_t cw[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          convert16(cw[2 * e], cw[2 * e + 1], scale_pair((so >> (8 * e)) & 0xFFu), x[2 * e], x[2 * e + 1]);
+        convert32(*reinterpret_cast<const uint4*>(stg + STG_OTHER + lane * 128 + 16 * vw), so, x);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&c.bars[STG_EMPTY0 + s]);  // every code is in registers
-      // V: the own rows' chunk once more (V dims of this CTA), or the other rows'
       if (!wait_bar(c, PV_DONE0 + s, ((g >> 1) & 1) ^ 1)) return false;
       {
-        unsigned char* vd = sm + OFF_V + s * kVStage + vc * kVChunk + (in_half ? own : oth) * 128;
+        unsigned char* vd = sm + OFF_V + s * kVStage + (vw >> 1) * kVChunk + (in_half ? own : oth) * 128;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) put(vd, e, lane, x[e]);
+        for (int e = 0; e < 4; ++e) put(vd, 4 * (vw & 1) + e, lane, x[e]);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -709,19 +723,19 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
       ++g;
       return true;
     };
-    // Rows [8 w, 8 w + 8) of the item's query in this CTA: f16 in nine swizzled
+    // Rows [4 w, 4 w + 4) of the item's query in this CTA: f16 in nine swizzled
     // chunks, and each row's factor 2^-k.  Rows past the query's end are zero.
     auto load_query = [&](const WorkItem& it, int n) -> bool {
       const long long q_rows = p.total_q * H;
-      const long long first = (long long)it.q_start * H + (long long)it.g * kRows + kCtaRows * rank + 8 * w;
+      const long long first = (long long)it.q_start * H + (long long)it.g * kRows + kCtaRows * rank + 4 * w;
       const int u2 = 64 + (lane & 7);
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
-        uint4 x[4][3];
+        uint4 x[2][3];
         if (p.q_fp8) {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const long long qr = first + 4 * half + r;
+          for (int r = 0; r < 2; ++r) {
+            const long long qr = first + 2 * half + r;
             const uint2* src = reinterpret_cast<const uint2*>(p.query) + (qr < q_rows ? qr : 0) * 72;
             const bool in = qr < q_rows;
             uint2 y[3] = {in ? __ldg(src + lane) : make_uint2(0, 0), in ? __ldg(src + 32 + lane) : make_uint2(0, 0),
@@ -731,8 +745,8 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
           }
         } else {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const long long qr = first + 4 * half + r;
+          for (int r = 0; r < 2; ++r) {
+            const long long qr = first + 2 * half + r;
             const uint4* src = reinterpret_cast<const uint4*>(p.query) + (qr < q_rows ? qr : 0) * 72;
             const bool in = qr < q_rows;
             x[r][0] = in ? __ldg(src + lane) : make_uint4(0, 0, 0, 0);
@@ -743,8 +757,8 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
         // every QK of the previous item has read its query
         if (half == 0 && !wait_bar(c, Q_EMPTY, (n & 1) ^ 1)) return false;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = 8 * w + 4 * half + r;
+        for (int r = 0; r < 2; ++r) {
+          const int row = 4 * w + 2 * half + r;
           int k = 0;
           if (!p.q_fp8) {
             uint32_t mb = __vmaxu2(__vmaxu2(max_bits(x[r][0]), max_bits(x[r][1])), max_bits(x[r][2]));
