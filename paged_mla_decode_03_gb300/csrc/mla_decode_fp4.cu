@@ -29,7 +29,7 @@
 // rows whole, of the other rows only its V dims), and sixteen warps turn them
 // into f16 in the swizzled operand layouts, one row a lane.
 //
-// Warp roles (896 threads): 0 copies, 1 issues QK (even CTA) and owns TMEM, 2
+// Warp roles (896 threads): 0 and 3 copy, 1 issues QK (even CTA) and owns TMEM, 2
 // issues PV, 4-11 softmax, correction and epilogue, 12-27 conversion and query
 // load.  QK runs up to two tiles ahead of PV, so the tensor cores work while a
 // softmax runs.  Every wait is bounded; a timeout sets the status word and both
@@ -61,6 +61,7 @@ constexpr int kConvWarps = 16;
 constexpr int kSoftWarps = 8;
 constexpr int kFirstSoft = 4, kFirstConv = kFirstSoft + kSoftWarps;
 constexpr int kThreads = 32 * (kFirstConv + kConvWarps);
+constexpr int kAhead = 6;            // tiles prefetched to L2 (under 16: at most one batch of page ids on)
 constexpr uint32_t kWaitLimit = 1u << 22;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -88,8 +89,8 @@ constexpr uint32_t OFF_XSUM = OFF_XMAX + 2 * 256 * 4;  // float [256]: row sums,
 constexpr uint32_t OFF_QSCALE = OFF_XSUM + 256 * 4;    // float [4][64]: 2^-k by item
 constexpr uint32_t OFF_TMEM = OFF_QSCALE + 4 * kCtaRows * 4;
 constexpr uint32_t OFF_ABORT = OFF_TMEM + 16;
-constexpr uint32_t OFF_LOADED = OFF_ABORT + 16;        // int [2][2]: staged halves, by stage
-constexpr uint32_t kSmemBytes = OFF_LOADED + 16;
+constexpr uint32_t OFF_MASK = OFF_ABORT + 16;  // uint32 [2][2]: rows in use, by stage and half
+constexpr uint32_t kSmemBytes = OFF_MASK + 16;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 static_assert(OFF_K % 1024 == 0 && OFF_V % 1024 == 0 && OFF_P % 1024 == 0 && kStage % 16 == 0 &&
                   OFF_STG % 16 == 0 && STG_SCALES % 16 == 0 && OFF_BARS % 8 == 0,
@@ -126,19 +127,21 @@ struct Ctx {
   int* status;
 };
 
-__device__ __forceinline__ void give_up(const Ctx& c) {
+// A wait ran out, here or in the other CTA: flag the status word and make both
+// CTAs unwind.
+__device__ __noinline__ void give_up(const Ctx& c) {
   *c.abort = 1;
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(c.peer_abort), "r"(1) : "memory");
   atomicOr(c.status, kStatusTimeout);
 }
+// False after too many polls, or once either CTA has given up; the caller then
+// leaves its role through give_up (kept out of the loops: their code competes
+// for the instruction cache).
 __device__ __forceinline__ bool wait_bar(const Ctx& c, int bar, uint32_t parity) {
   uint64_t* b = &c.bars[bar];
-  for (uint32_t i = 0; i < kWaitLimit; ++i) {
-    if (mbar_try_wait(b, parity)) return true;
-    if ((i & 1023) == 1023 && *c.abort) return false;
-  }
-  give_up(c);
-  return false;
+  for (uint32_t i = kWaitLimit; !mbar_try_wait(b, parity); --i)
+    if (i == 0 || ((i & 1023) == 0 && *c.abort)) return false;
+  return true;
 }
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
   for (uint32_t i = 0; i < kWaitLimit; ++i)
@@ -170,11 +173,12 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
-// The f16 value of an e4m3 code, in both halves of a word.
-__device__ __forceinline__ uint32_t scale_pair(uint32_t code) {
+// The f16 values of two e4m3 codes, each in both halves of a word.
+__device__ __forceinline__ void scale_pairs(uint32_t codes, uint32_t& s0, uint32_t& s1) {
   uint32_t h;
-  asm("{\n .reg .b16 lo;\n mov.b32 {lo, _}, %1;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n}" : "=r"(h) : "r"(code));
-  return __byte_perm(h, h, 0x1010);
+  asm("{\n .reg .b16 lo;\n mov.b32 {lo, _}, %1;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n}" : "=r"(h) : "r"(codes));
+  s0 = __byte_perm(h, h, 0x1010);
+  s1 = __byte_perm(h, h, 0x3232);
 }
 // Eight codes times their scale, as a 16-byte unit of f16.
 __device__ __forceinline__ uint4 convert8(uint32_t codes, uint32_t scale) {
@@ -182,13 +186,18 @@ __device__ __forceinline__ uint4 convert8(uint32_t codes, uint32_t scale) {
   e2m1x8_to_f16x2(codes, h);
   return make_uint4(hmul2(h[0], scale), hmul2(h[1], scale), hmul2(h[2], scale), hmul2(h[3], scale));
 }
-// Two groups: 32 codes and their two scales.
-__device__ __forceinline__ void convert32(const uint4 codes, uint32_t scales, uint4 (&x)[4]) {
-  const uint32_t s0 = scale_pair(scales & 0xFFu), s1 = scale_pair(scales >> 8);
-  x[0] = convert8(codes.x, s0);
-  x[1] = convert8(codes.y, s0);
-  x[2] = convert8(codes.z, s1);
-  x[3] = convert8(codes.w, s1);
+// 64 codes and their four scales.
+__device__ __forceinline__ void convert64(const uint4 a, const uint4 b, uint32_t scales, uint4 (&x)[8]) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    uint32_t s0, s1;
+    scale_pairs(scales >> (16 * e), s0, s1);
+    x[4 * e] = convert8(w[4 * e], s0);
+    x[4 * e + 1] = convert8(w[4 * e + 1], s0);
+    x[4 * e + 2] = convert8(w[4 * e + 2], s1);
+    x[4 * e + 3] = convert8(w[4 * e + 3], s1);
+  }
 }
 __device__ __forceinline__ void put(unsigned char* row, int unit, int r, uint4 v) {
   *reinterpret_cast<uint4*>(row + ((unit ^ (r & 7)) << 4)) = v;
@@ -252,16 +261,16 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
   c.leader_bars = map_to_rank(smem_u32(sm + OFF_BARS), 0);
   c.status = reinterpret_cast<int*>(ws) + kHdrStatus;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + OFF_TMEM);
-  volatile int* loaded = reinterpret_cast<volatile int*>(sm + OFF_LOADED);
+  volatile uint32_t* row_mask = reinterpret_cast<volatile uint32_t*>(sm + OFF_MASK);
 
   if (tid == 0) {
     for (int i = 0; i < NUM_BARS; ++i) {
       uint32_t n = 1;  // one commit
       if (i >= STG_FULL0 && i < STG_FULL0 + 2) n = 1 + 32;  // bulk copies, each lane's own
-      if (i >= STG_EMPTY0 && i < STG_EMPTY0 + 2) n = kConvWarps;
-      // a latent chunk's two warps count four times each, as the RoPE chunk has eight
-      if (i >= K_FULL0 && i < K_FULL0 + kKSlots / kGroup) n = 2 * 8 * kGroup;
-      if (i >= V_FULL0 && i < V_FULL0 + 2) n = 2 * kConvWarps;
+      if (i >= STG_EMPTY0 && i < STG_EMPTY0 + 2) n = kConvWarps / 2;
+      // a latent chunk's warp counts four times, as the RoPE chunk has four warps
+      if (i >= K_FULL0 && i < K_FULL0 + kKSlots / kGroup) n = 2 * 4 * kGroup;
+      if (i >= V_FULL0 && i < V_FULL0 + 2) n = kConvWarps;  // half the warps of both CTAs
       if (i >= S_EMPTY0 && i < S_EMPTY0 + 2) n = 2 * kSoftWarps;
       if (i == P_FULL) n = 2 * kSoftWarps;
       if (i == Q_FULL) n = 2 * kConvWarps;
@@ -288,14 +297,17 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
   const uint32_t tmem = *tmem_slot;
   const int item_begin = worker_begin[worker], item_end = worker_begin[worker + 1];
   const int H = p.num_heads;
+  const int h_shift = __ffs(H) - 1;  // a power of two
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 3) {
     // ------------------------------------------------------------ copies
     // Page ids a batch of 32 ahead (one per lane), as virtual page slots of the
-    // item.  Lane 0 issues the bulk copies (codes of the own rows, scales); the
-    // other rows' V codes, 128 bytes of each 288, go by 16-byte copies of all
-    // lanes (one bulk copy a row took 4000 cycles to issue).
-    const int ps = p.page_size, npg = kTile / ps;
+    // item.  Warp 0's lane 0 issues the bulk copies: codes of the own rows, scales.
+    // Warp 3 fetches the other rows' V codes, 128 bytes of each 288, by 16-byte
+    // copies (one bulk copy a row took 4000 cycles to issue), and brings later
+    // tiles to L2.
+    const bool bulk = warp == 0;
+    const int ps = p.page_size, ps_shift = ps == kTile ? 6 : 5, npg = kTile >> ps_shift;
     const size_t page_bytes = (size_t)ps * kFp4RowBytes;
     const unsigned char* cache = static_cast<const unsigned char*>(p.kv_cache);
     uint32_t g = 0;
@@ -305,10 +317,15 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
       if (nt <= 0) continue;
       const Walk walk(p, it);
       const int* bt = p.block_tables + (size_t)it.b * p.max_pages;
-      const int n_pages = (it.kv_end - it.kv_begin + ps - 1) / ps;
-      auto page_at = [&](int i) {
+      const int n_pages = (it.kv_end - it.kv_begin + ps - 1) >> ps_shift;
+      // a page's id, -1 for one that is not read
+      auto page_at = [&](int i) -> int {
         const int r = walk.row(it.kv_begin + i * ps);
-        return i < n_pages && walk.seen(r, r + ps - 1) ? bt[r / ps] : -1;
+        if (i >= n_pages || !walk.seen(r, r + ps - 1)) return -1;
+        const int id = bt[r >> ps_shift];
+        if (id >= 0 && (long long)id < p.num_pages) return id;
+        if (bulk) atomicOr(c.status, kStatusPage);
+        return -1;
       };
       int cur = page_at(lane), nxt = page_at(32 + lane);
       for (int t = 0; t < nt; ++t, ++g) {
@@ -317,66 +334,81 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
           cur = nxt;
           nxt = page_at(slot0 + 32 + lane);
         }
-        int pages[2];
-        pages[0] = __shfl_sync(0xffffffffu, cur, slot0 & 31);
-        pages[1] = __shfl_sync(0xffffffffu, cur, (slot0 + npg - 1) & 31);
+        const int id0 = __shfl_sync(0xffffffffu, cur, slot0 & 31);
+        const int id1 = __shfl_sync(0xffffffffu, cur, (slot0 + npg - 1) & 31);
+        // a half is read if some query row sees a row of it
+        const int j0 = it.kv_begin + t * kTile, r0 = walk.row(j0);
+        const bool on0 = id0 >= 0 && walk.seen(r0, r0 + kHalf - 1);
+        const bool on1 = id1 >= 0 && j0 + kHalf < it.kv_end && walk.seen(r0 + kHalf, r0 + kTile - 1);
         const int s = g & 1;
-        const bool ok = lane == 0 ? wait_bar(c, STG_EMPTY0 + s, ((g >> 1) & 1) ^ 1) : false;
-        if (!__shfl_sync(0xffffffffu, ok, 0)) goto done_copy;
-        const int j0 = it.kv_begin + t * kTile;
-        bool on[2];
-        const unsigned char* page[2];
-        int row[2];
-        uint32_t bytes = 0;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = walk.row(j0) + h * kHalf;
-          on[h] = j0 + h * kHalf < it.kv_end && walk.seen(r, r + kHalf - 1);
-          if (on[h] && (pages[h] < 0 || (long long)pages[h] >= p.num_pages)) {
-            if (lane == 0) atomicOr(c.status, kStatusPage);
-            on[h] = false;
-          }
-          page[h] = cache + (size_t)(on[h] ? pages[h] : 0) * page_bytes;
-          row[h] = ps == kTile ? h * kHalf : 0;
-          if (on[h]) bytes += (h == rank ? kHalf * kFp4CodeBytes : 0) + kHalf * kFp4ScaleBytes;
-        }
         unsigned char* stg = sm + OFF_STG + s * kStage;
         uint64_t* full = &c.bars[STG_FULL0 + s];
-        if (lane == 0) {
-          loaded[2 * s] = on[0];
-          loaded[2 * s + 1] = on[1];
-          mbar_arrive_expect_tx(full, bytes);
+        if (bulk) {
+          // rows past the item's end, that no query row sees, or on a page that is
+          // not read, enter as zeros
+          const uint32_t mask0 = __ballot_sync(0xffffffffu, on0 && j0 + lane < it.kv_end &&
+                                                                walk.seen(r0 + lane, r0 + lane));
+          const uint32_t mask1 =
+              __ballot_sync(0xffffffffu, on1 && j0 + kHalf + lane < it.kv_end &&
+                                             walk.seen(r0 + kHalf + lane, r0 + kHalf + lane));
+          if (!wait_bar(c, STG_EMPTY0 + s, ((g >> 1) & 1) ^ 1)) goto fail_copy;
+          if (lane == 0) {
+            const int row1 = npg == 1 ? kHalf : 0;  // first row of half 1 in its page
+            const unsigned char* pg0 = cache + (size_t)(on0 ? id0 : 0) * page_bytes;
+            const unsigned char* pg1 = cache + (size_t)(on1 ? id1 : 0) * page_bytes;
+            const unsigned char* sc0 = pg0 + (size_t)ps * kFp4CodeBytes;
+            const unsigned char* sc1 = pg1 + (size_t)ps * kFp4CodeBytes + row1 * kFp4ScaleBytes;
+            constexpr uint32_t kScales = kHalf * kFp4ScaleBytes, kCodes = kHalf * kFp4CodeBytes;
+            const bool own = rank == 0 ? on0 : on1;
+            row_mask[2 * s] = mask0;
+            row_mask[2 * s + 1] = mask1;
+            mbar_arrive_expect_tx(full, (on0 ? kScales : 0) + (on1 ? kScales : 0) + (own ? kCodes : 0));
+            if (own) bulk_load(stg + STG_OWN, rank == 0 ? pg0 : pg1 + row1 * kFp4CodeBytes, kCodes, full);
+            if (on0 && on1 && npg == 1) {
+              bulk_load(stg + STG_SCALES, sc0, 2 * kScales, full);
+            } else {
+              if (on0) bulk_load(stg + STG_SCALES, sc0, kScales, full);
+              if (on1) bulk_load(stg + STG_SCALES + kScales, sc1, kScales, full);
+            }
+          }
+          __syncwarp();
+        } else {
+          if (!wait_bar(c, STG_EMPTY0 + s, ((g >> 1) & 1) ^ 1)) goto fail_copy;
+          // eight 16-byte units of a row: eight lanes a row
+          if (rank == 0 ? on1 : on0) {
+            const unsigned char* src = cache + (size_t)(rank == 0 ? id1 : id0) * page_bytes +
+                                       (rank == 0 && npg == 1 ? kHalf * kFp4CodeBytes : 0) +
+                                       (lane >> 3) * kFp4CodeBytes + 128 * rank + 16 * (lane & 7);
+            unsigned char* dst = stg + STG_OTHER + 16 * lane;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (!on[h]) continue;
-            bulk_load(stg + STG_SCALES + h * kHalf * kFp4ScaleBytes,
-                      page[h] + (size_t)ps * kFp4CodeBytes + row[h] * kFp4ScaleBytes,
-                      kHalf * kFp4ScaleBytes, full);
-            if (h == rank)
-              bulk_load(stg + STG_OWN, page[h] + row[h] * kFp4CodeBytes, kHalf * kFp4CodeBytes, full);
+            for (int i = 0; i < 8; ++i) cp_async_16(dst + i * 512, src + i * 4 * kFp4CodeBytes);
+          }
+          cp_async_arrive(full);
+          // this CTA's half of the tiles up to kAhead on, to L2: two staged tiles
+          // cover an L2 round trip but not one to HBM
+          for (int a = t == 0 ? 2 : kAhead; a <= kAhead; ++a) {
+            const int i = (t + a) * npg + (npg == 2 ? rank : 0);
+            const int from = __shfl_sync(0xffffffffu, (i >> 5) == (slot0 >> 5) ? cur : nxt, i & 31);
+            if (t + a < nt && lane < 2 && from >= 0) {
+              const unsigned char* pg = cache + (size_t)from * page_bytes;
+              const int r = npg == 2 ? 0 : kHalf * rank;
+              bulk_prefetch_l2(lane == 0 ? pg + r * kFp4CodeBytes
+                                         : pg + (size_t)ps * kFp4CodeBytes + r * kFp4ScaleBytes,
+                               kHalf * (lane == 0 ? kFp4CodeBytes : kFp4ScaleBytes));
+            }
           }
         }
-        __syncwarp();
-        // the other rows' V codes, eight 16-byte units of a row: eight lanes a row
-        const int o = rank ^ 1;
-        if (on[o]) {
-          const unsigned char* src = page[o] + row[o] * kFp4CodeBytes + 128 * rank + 16 * (lane & 7);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int r = 4 * k + (lane >> 3);
-            cp_async_16(stg + STG_OTHER + r * 128 + 16 * (lane & 7), src + r * kFp4CodeBytes);
-          }
-        }
-        cp_async_arrive(full);
       }
     }
+    goto done_copy;
+  fail_copy:
+    give_up(c);
   done_copy:
     // no copy issued here may still be landing when the CTA leaves
-    if (lane == 0)
-      for (uint32_t k = 0; k < 2 && k < g; ++k) {
-        const uint32_t gi = g - 1 - k;
-        drain_wait(&c.bars[STG_FULL0 + (gi & 1)], (gi >> 1) & 1);
-      }
+    for (uint32_t k = 0; k < 2 && k < g; ++k) {
+      const uint32_t gi = g - 1 - k;
+      drain_wait(&c.bars[STG_FULL0 + (gi & 1)], (gi >> 1) & 1);
+    }
   } else if (warp == 1) {
     // ------------------------------------------------------------ QK issue
     // The whole warp walks the loops and one lane issues (see elect_one).
@@ -391,14 +423,14 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
       for (int idx = item_begin; idx < item_end; ++idx) {
         const int nt = __shfl_sync(0xffffffffu, n_tiles_of(items[idx]), 0);
         if (nt <= 0) continue;
-        if (!wait_bar(c, Q_FULL, n_item & 1)) goto done_qk;
+        if (!wait_bar(c, Q_FULL, n_item & 1)) goto fail_qk;
         ++n_item;
         for (int t = 0; t < nt; ++t, ++g) {
           const uint32_t sb = g & 1;
-          if (!wait_bar(c, S_EMPTY0 + sb, ((g >> 1) & 1) ^ 1)) goto done_qk;
+          if (!wait_bar(c, S_EMPTY0 + sb, ((g >> 1) & 1) ^ 1)) goto fail_qk;
 #pragma unroll
           for (int k3 = 0; k3 < kChunks / kGroup; ++k3) {
-            if (!wait_bar(c, K_FULL0 + group, round & 1)) goto done_qk;
+            if (!wait_bar(c, K_FULL0 + group, round & 1)) goto fail_qk;
             tc_fence_after();
             if (elect_one()) {
               const uint64_t kd = k_desc + group * (kGroup * kKChunk >> 4);
@@ -424,6 +456,9 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
           }
         }
       }
+      goto done_qk;
+    fail_qk:
+      give_up(c);
     done_qk:
       __syncwarp();
       if (elect_one()) mma_commit_pair(&c.bars[DRAIN0]);
@@ -441,8 +476,8 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
         const int nt = __shfl_sync(0xffffffffu, n_tiles_of(items[idx]), 0);
         for (int t = 0; t < nt; ++t, ++g) {
           const uint32_t s = g & 1;
-          if (!wait_bar(c, V_FULL0 + s, (g >> 1) & 1)) goto done_pv;
-          if (!wait_bar(c, P_FULL, g & 1)) goto done_pv;
+          if (!wait_bar(c, V_FULL0 + s, (g >> 1) & 1)) goto fail_pv;
+          if (!wait_bar(c, P_FULL, g & 1)) goto fail_pv;
           tc_fence_after();
           if (elect_one()) {
             const uint64_t v = v_desc + s * (kVStage >> 4);
@@ -458,13 +493,14 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
           __syncwarp();
         }
       }
+      goto done_pv;
+    fail_pv:
+      give_up(c);
     done_pv:
       __syncwarp();
       if (elect_one()) mma_commit_pair(&c.bars[DRAIN0 + 1]);
       drain_wait(&c.bars[DRAIN0 + 1], 0);
     }
-  } else if (warp < kFirstSoft) {
-    // (warps 4-11 need TMEM lane quarters 0-3 twice)
   } else if (warp < kFirstConv) {
     // ------------------------------------------------------------ softmax, correction, epilogue
     // Thread = TMEM lane l = 32 (warp mod 4) + lane and column part cc: query row
@@ -497,28 +533,23 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
       const int n_rows = min(kRows, rows_total - row0);
       const bool row_ok = q < n_rows;
       auto last_of = [&](int r) {
-        return p.causal ? causal_last(it.mask_base, (row0 + r) / H, W) : it.seq_len - 1;
+        return p.causal ? causal_last(it.mask_base, (row0 + r) >> h_shift, W) : it.seq_len - 1;
       };
       const int last = last_of(min(q, n_rows - 1));
       const int low = p.window > 0 ? last - p.window + 1 : INT_MIN;  // first row of the window
       // tiles inside [clean_lo, clean_hi) need no mask for any row of the item
       const int clean_hi = last_of(0) + 1;
       const int clean_lo = p.window > 0 ? last_of(n_rows - 1) - p.window + 1 : INT_MIN;
-      if (!wait_bar(c, QS_FULL0 + (n_item & 3), (n_item >> 2) & 1)) goto done_soft;
+      if (!wait_bar(c, QS_FULL0 + (n_item & 3), (n_item >> 2) & 1)) goto fail_soft;
       const float scale = bmm1 * qscale[(n_item & 3) * kCtaRows + row];
       float m = -INFINITY, l_part = 0.f;
       for (int t = 0; t < nt; ++t, ++g) {
         const int sb = g & 1;
-        if (!wait_bar(c, S_FULL0 + sb, (g >> 1) & 1)) goto done_soft;
+        if (!wait_bar(c, S_FULL0 + sb, (g >> 1) & 1)) goto fail_soft;
         tc_fence_after();
-        float sv[16];
-        {
-          uint32_t v[16];
-          tmem_ld_32x32b_x16(tm + TM_S + 32 * sb + 16 * cc, v);
-          tmem_wait_ld();
-#pragma unroll
-          for (int j = 0; j < 16; ++j) sv[j] = __uint_as_float(v[j]) * scale;
-        }
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(tm + TM_S + 32 * sb + 16 * cc, v);
+        tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_leader(c, S_EMPTY0 + sb, 1);
@@ -527,43 +558,61 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
         const int valid = it.kv_end - v0;               // rows of the tile inside the item
         const bool clean = valid >= kTile && r0 + kTile <= clean_hi &&
                            (r0 >= clean_lo || r0 + kTile <= p.sinks);
+        uint32_t hidden = 0;  // columns that the mask takes out
         if (!clean) {
-#pragma unroll
+#pragma unroll 1
           for (int j = 0; j < 16; ++j) {
             const int k = 32 * hh + 16 * cc + j, at = r0 + k;
-            if (!(at <= last && k < valid && (at >= low || at < p.sinks))) sv[j] = -INFINITY;
+            if (!(at <= last && k < valid && (at >= low || at < p.sinks))) hidden |= 1u << j;
           }
-        }
-        float mt[4] = {sv[0], sv[1], sv[2], sv[3]};
 #pragma unroll
-        for (int j = 4; j < 16; ++j) mt[j & 3] = fmaxf(mt[j & 3], sv[j]);
-        const float m_own = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
+          for (int j = 0; j < 16; ++j)
+            if ((hidden >> j) & 1u) v[j] = 0xFF800000u;  // -inf
+        }
+        float mt[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          mt[j] = fmaxf(fmaxf(__uint_as_float(v[j]), __uint_as_float(v[j + 4])),
+                        fmaxf(__uint_as_float(v[j + 8]), __uint_as_float(v[j + 12])));
         float* xm = xmax + sb * 256;
-        xm[128 * cc + l] = m_own;
+        xm[128 * cc + l] = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
         __syncwarp();
         if (lane == 0) mbar_arrive(&c.bars[XM0 + 2 * sb + pair]);
-        if (!wait_bar(c, XM0 + 2 * sb + pair, (g >> 1) & 1)) goto done_soft;
-        // (all four from shared memory: the same result in the row's four threads)
-        const float m_tile = fmaxf(fmaxf(xm[row], xm[row + 64]), fmaxf(xm[row + 128], xm[row + 192]));
+        if (!wait_bar(c, XM0 + 2 * sb + pair, (g >> 1) & 1)) goto fail_soft;
+        // (all four from shared memory: the same result in the row's four threads;
+        // the scale is not negative, so it may come after the maximum)
+        const float m_raw = fmaxf(fmaxf(xm[row], xm[row + 64]), fmaxf(xm[row + 128], xm[row + 192]));
+        const float m_tile = m_raw == -INFINITY ? m_raw : m_raw * scale;
         const float m_new = (m_tile > m + kRescaleThreshold || t == 0) ? m_tile : m;
         const bool need = t > 0 && m_new != m;
         const float f = need ? ex2(m - m_new) : 1.f;  // m = -inf: 0
         m = m_new;
-        l_part *= f;
-        const float ref = (m == -INFINITY ? 0.f : m) - kPShift;
+        const float ref = kPShift - (m == -INFINITY ? 0.f : m);
         // (rows past the request's own compute something that nothing reads)
+        const uint64_t scale2 = pack_f32x2(scale, scale), ref2 = pack_f32x2(ref, ref);
         uint32_t pw[8];
-        float rs[4] = {0.f, 0.f, 0.f, 0.f};
+        uint64_t rs[2] = {0, 0};
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float a = ex2(sv[2 * j] - ref), b = ex2(sv[2 * j + 1] - ref);
-          rs[j & 3] += a + b;
+          float a, b;
+          unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), scale2, ref2), a, b);
+          a = ex2(a);
+          b = ex2(b);
+          if (!clean) {  // (-inf times a scale of zero is no zero)
+            if ((hidden >> (2 * j)) & 1u) a = 0.f;
+            if ((hidden >> (2 * j + 1)) & 1u) b = 0.f;
+          }
+          rs[j & 1] = add_f32x2(rs[j & 1], pack_f32x2(a, b));
           const __half2 h = __floats2half2_rn(a, b);
           pw[j] = *reinterpret_cast<const uint32_t*>(&h);
         }
-        l_part += (rs[0] + rs[1]) + (rs[2] + rs[3]);
+        {
+          float a, b;
+          unpack_f32x2(add_f32x2(rs[0], rs[1]), a, b);
+          l_part = fmaf(l_part, f, a + b);
+        }
         // PV of the previous tile is done: its P may be replaced, and O is stable
-        if (g > 0 && !wait_bar(c, PV_DONE0 + ((g - 1) & 1), ((g - 1) >> 1) & 1)) goto done_soft;
+        if (g > 0 && !wait_bar(c, PV_DONE0 + ((g - 1) & 1), ((g - 1) >> 1) & 1)) goto fail_soft;
         if (__any_sync(0xffffffffu, need)) {
           tc_fence_after();
 #pragma unroll 1
@@ -590,7 +639,7 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
       xsum[128 * cc + l] = l_part;
       __syncwarp();
       if (lane == 0) mbar_arrive(&c.bars[XS0 + pair]);
-      if (!wait_bar(c, XS0 + pair, n_item & 1)) goto done_soft;
+      if (!wait_bar(c, XS0 + pair, n_item & 1)) goto fail_soft;
       const float l_row = (xsum[row] + xsum[row + 64]) + (xsum[row + 128] + xsum[row + 192]);
       const float lse = l_row > 0.f ? (m - kPShift + log2f(l_row)) * kLn2 : -INFINITY;
       const float inv = l_row > 0.f ? 1.f / l_row : 0.f;
@@ -601,7 +650,7 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
         else if (p.return_lse)
           p.lse[grow] = lse;
       }
-      if (!wait_bar(c, PV_DONE0 + ((g - 1) & 1), ((g - 1) >> 1) & 1)) goto done_soft;
+      if (!wait_bar(c, PV_DONE0 + ((g - 1) & 1), ((g - 1) >> 1) & 1)) goto fail_soft;
       tc_fence_after();
       const float s2 = it.slot < 0 ? inv * bmm2 : inv;
 #pragma unroll 1
@@ -636,7 +685,7 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&c.bars[EPI]);
         if (warp == kFirstSoft) {
-          if (!wait_bar(c, EPI, n_split & 1)) goto done_soft;
+          if (!wait_bar(c, EPI, n_split & 1)) goto fail_soft;
           if (lane == 0 && it.comb >= 0) {
             __threadfence();
             atomicAdd(comb_done + it.comb, 1);
@@ -646,81 +695,95 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
       }
       ++n_item;
     }
+    goto done_soft;
+  fail_soft:
+    give_up(c);
   done_soft:;
   } else {
     // ------------------------------------------------------------ conversion and query load
-    // Warp w: latent dims [32 w, 32 w + 32) of the own rows, one row a lane, into
-    // K; then, if those are V dims of this CTA, the same values into V and eight
-    // RoPE dims into K, else 32 V dims of the other rows.
+    // Two groups of eight warps take alternate tiles (and staging stages): a
+    // tile's conversion is a chain of waits and shared-memory round trips longer
+    // than a tile's MMAs.  Warp k of a group: latent dims [64 k, 64 k + 64) of the
+    // own rows, one row a lane, into K; then, if those are V dims of this CTA, the
+    // same values into V and 16 RoPE dims into K, else 64 V dims of the other rows.
     const int w = warp - kFirstConv;
-    const bool in_half = (w >> 3) == rank;
-    const int vw = w & 7;  // V part of 32 dims; RoPE part of 8
+    const uint32_t grp = (uint32_t)w >> 3;
+    const int k = w & 7, vc = k & 3;
+    const bool in_half = (k >> 2) == rank;
     float* qscale = reinterpret_cast<float*>(sm + OFF_QSCALE);
     uint32_t g = 0;
-    // ring places of this warp's chunk and of the RoPE chunk
-    uint32_t kslot = w >> 1, kround = 0, rslot = 8, rround = 0;
+    // ring places (chunk 9 g + k of twelve) of this warp's chunk and the RoPE chunk
+    uint32_t kslot = (kChunks * grp + k) % kKSlots, kround = (kChunks * grp + k) / kKSlots;
+    uint32_t rslot = (kChunks * grp + 8) % kKSlots, rround = (kChunks * grp + 8) / kKSlots;
     int n_item = 0;
-    auto convert_tile = [&](const WorkItem& it, const Walk& walk, int t) -> bool {
-      const int s = g & 1;
+    auto convert_tile = [&]() -> bool {
+      const int s = (int)grp;
       if (!wait_bar(c, STG_FULL0 + s, (g >> 1) & 1)) return false;
       const unsigned char* stg = sm + OFF_STG + s * kStage;
-      // rows past the item's end, that no query row sees, or on a page that was
-      // not loaded, are zeros
-      const int v0 = it.kv_begin + t * kTile, r0 = walk.row(v0);
       const int own = kHalf * rank + lane, oth = kHalf * (rank ^ 1) + lane;
-      const bool on_own = v0 + own < it.kv_end && loaded[2 * s + rank] && walk.seen(r0 + own, r0 + own);
-      const unsigned char* sc_own = stg + STG_SCALES + own * kFp4ScaleBytes;
       const unsigned char* codes = stg + STG_OWN + lane * kFp4CodeBytes;
-      const uint32_t sc = on_own ? *reinterpret_cast<const uint16_t*>(sc_own + 2 * w) : 0u;
-      uint4 x[4];
-      convert32(*reinterpret_cast<const uint4*>(codes + 16 * w), sc, x);
+      const unsigned char* sc_own = stg + STG_SCALES + own * kFp4ScaleBytes;
+      const unsigned char* sc_oth = stg + STG_SCALES + oth * kFp4ScaleBytes;
+      const uint4 c0 = *reinterpret_cast<const uint4*>(codes + 32 * k);
+      const uint4 c1 = *reinterpret_cast<const uint4*>(codes + 32 * k + 16);
+      const unsigned char* second = in_half ? codes + 256 + 8 * vc : stg + STG_OTHER + lane * 128 + 32 * vc;
+      uint32_t sc = *reinterpret_cast<const uint32_t*>(sc_own + 4 * k);
+      uint32_t s2 = in_half ? (uint32_t)sc_own[32 + vc]
+                            : *reinterpret_cast<const uint32_t*>(sc_oth + 16 * rank + 4 * vc);
+      const uint32_t m1 = row_mask[2 * s + rank], m2 = in_half ? m1 : row_mask[2 * s + (rank ^ 1)];
+      if (!((m1 >> lane) & 1u)) sc = 0u;
+      if (!((m2 >> lane) & 1u)) s2 = 0u;
+      uint4 x[8];
+      convert64(c0, c1, sc, x);
+      // The group's previous tile is through QK.  (Its chunks' slots come round
+      // before the other group's tile fills the ones between: without this wait a
+      // slot's empty barrier could be two uses behind, where its parity reads as
+      // the phase that is waited for.)
+      if (!wait_bar(c, S_FULL0 + s, ((g >> 1) & 1) ^ 1)) return false;
       if (!wait_bar(c, K_EMPTY0 + kslot / kGroup, (kround & 1) ^ 1)) return false;
-      {
-        unsigned char* kd = sm + OFF_K + kslot * kKChunk + lane * 128;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) put(kd, 4 * (w & 1) + e, lane, x[e]);
-      }
+      for (int e = 0; e < 8; ++e) put(sm + OFF_K + kslot * kKChunk + lane * 128, e, lane, x[e]);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) arrive_leader(c, K_FULL0 + kslot / kGroup, 4);
+      uint4 y0, y1;
       if (in_half) {
-        const uint32_t rs = on_own ? (uint32_t)sc_own[32 + (vw >> 1)] : 0u;
-        const uint4 y = convert8(*reinterpret_cast<const uint32_t*>(codes + 256 + 4 * vw), scale_pair(rs));
-        if (!wait_bar(c, K_EMPTY0 + rslot / kGroup, (rround & 1) ^ 1)) return false;
-        put(sm + OFF_K + rslot * kKChunk + lane * 128, vw, lane, y);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) arrive_leader(c, K_FULL0 + rslot / kGroup, 1);
+        const uint2 rc = *reinterpret_cast<const uint2*>(second);
+        uint32_t s0, s1;
+        scale_pairs(s2, s0, s1);
+        y0 = convert8(rc.x, s0);
+        y1 = convert8(rc.y, s0);
       } else {
-        const bool on_oth = v0 + oth < it.kv_end && loaded[2 * s + (rank ^ 1)] && walk.seen(r0 + oth, r0 + oth);
-        const uint32_t so = on_oth ? *reinterpret_cast<const uint16_t*>(stg + STG_SCALES + oth * kFp4ScaleBytes +
-                                                                        16 * rank + 2 * vw)
-                                   : 0u;
-        convert32(*reinterpret_cast<const uint4*>(stg + STG_OTHER + lane * 128 + 16 * vw), so, x);
+        convert64(*reinterpret_cast<const uint4*>(second), *reinterpret_cast<const uint4*>(second + 16), s2, x);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&c.bars[STG_EMPTY0 + s]);  // every code is in registers
       if (!wait_bar(c, PV_DONE0 + s, ((g >> 1) & 1) ^ 1)) return false;
       {
-        unsigned char* vd = sm + OFF_V + s * kVStage + (vw >> 1) * kVChunk + (in_half ? own : oth) * 128;
+        unsigned char* vd = sm + OFF_V + s * kVStage + vc * kVChunk + (in_half ? own : oth) * 128;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) put(vd, 4 * (vw & 1) + e, lane, x[e]);
+        for (int e = 0; e < 8; ++e) put(vd, e, lane, x[e]);
+      }
+      if (in_half) {
+        if (!wait_bar(c, K_EMPTY0 + rslot / kGroup, (rround & 1) ^ 1)) return false;
+        unsigned char* rd = sm + OFF_K + rslot * kKChunk + lane * 128;
+        put(rd, 2 * vc, lane, y0);
+        put(rd, 2 * vc + 1, lane, y1);
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) arrive_leader(c, V_FULL0 + s, 1);
-      // nine chunks a tile through twelve slots
-      kslot += kChunks;
-      if (kslot >= kKSlots) {
-        kslot -= kKSlots;
-        ++kround;
+      if (lane == 0) {
+        if (in_half) arrive_leader(c, K_FULL0 + rslot / kGroup, 1);
+        arrive_leader(c, V_FULL0 + s, 1);
       }
-      rslot += kChunks;
-      if (rslot >= kKSlots) {
-        rslot -= kKSlots;
-        ++rround;
-      }
-      ++g;
+      // the group's next tile: eighteen chunks on
+      constexpr uint32_t kStep = 2 * kChunks - kKSlots;
+      kslot += kStep;
+      kround += 1 + kslot / kKSlots;
+      kslot %= kKSlots;
+      rslot += kStep;
+      rround += 1 + rslot / kKSlots;
+      rslot %= kKSlots;
       return true;
     };
     // Rows [4 w, 4 w + 4) of the item's query in this CTA: f16 in nine swizzled
@@ -791,13 +854,15 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
       if (nt <= 0) continue;
       // the first tile before the query: its conversion needs nothing of the
       // previous item but ring places
-      const Walk walk(p, it);
-      if (n_item > 0 && !convert_tile(it, walk, 0)) goto done_conv;
-      if (!load_query(it, n_item)) goto done_conv;
-      for (int t = n_item > 0 ? 1 : 0; t < nt; ++t)
-        if (!convert_tile(it, walk, t)) goto done_conv;
+      for (int t = 0; t < nt; ++t, ++g) {
+        if ((g & 1) == grp && !convert_tile()) goto fail_conv;
+        if (t == 0 && !load_query(it, n_item)) goto fail_conv;
+      }
       ++n_item;
     }
+    goto done_conv;
+  fail_conv:
+    give_up(c);
   done_conv:;
   }
 
