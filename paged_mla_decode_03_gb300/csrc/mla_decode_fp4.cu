@@ -379,9 +379,13 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
             const unsigned char* src = cache + (size_t)(rank == 0 ? id1 : id0) * page_bytes +
                                        (rank == 0 && npg == 1 ? kHalf * kFp4CodeBytes : 0) +
                                        (lane >> 3) * kFp4CodeBytes + 128 * rank + 16 * (lane & 7);
-            unsigned char* dst = stg + STG_OTHER + 16 * lane;
+            // unit u of row r goes to u ^ (r mod 8), so that eight rows' reads of one
+            // unit meet eight bank groups
+            unsigned char* dst = stg + STG_OTHER + (lane >> 3) * 128;
+            const int u = lane & 7, r7 = lane >> 3;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) cp_async_16(dst + i * 512, src + i * 4 * kFp4CodeBytes);
+            for (int i = 0; i < 8; ++i)
+              cp_async_16(dst + i * 512 + ((u ^ (r7 + 4 * (i & 1))) << 4), src + i * 4 * kFp4CodeBytes);
           }
           cp_async_arrive(full);
           // this CTA's half of the tiles up to kAhead on, to L2: two staged tiles
@@ -724,15 +728,22 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
       const unsigned char* codes = stg + STG_OWN + lane * kFp4CodeBytes;
       const unsigned char* sc_own = stg + STG_SCALES + own * kFp4ScaleBytes;
       const unsigned char* sc_oth = stg + STG_SCALES + oth * kFp4ScaleBytes;
-      const uint4 c0 = *reinterpret_cast<const uint4*>(codes + 32 * k);
-      const uint4 c1 = *reinterpret_cast<const uint4*>(codes + 32 * k + 16);
-      const unsigned char* second = in_half ? codes + 256 + 8 * vc : stg + STG_OTHER + lane * 128 + 32 * vc;
+      // (rows are 18 units of 16 bytes apart: rows 4 to 7 of eight take their two
+      // units in the other order, and no two rows of a phase share a bank group)
+      const int swap = (lane >> 2) & 1;
+      uint4 c0 = *reinterpret_cast<const uint4*>(codes + 32 * k + 16 * swap);
+      uint4 c1 = *reinterpret_cast<const uint4*>(codes + 32 * k + 16 * (swap ^ 1));
       uint32_t sc = *reinterpret_cast<const uint32_t*>(sc_own + 4 * k);
       uint32_t s2 = in_half ? (uint32_t)sc_own[32 + vc]
                             : *reinterpret_cast<const uint32_t*>(sc_oth + 16 * rank + 4 * vc);
       const uint32_t m1 = row_mask[2 * s + rank], m2 = in_half ? m1 : row_mask[2 * s + (rank ^ 1)];
       if (!((m1 >> lane) & 1u)) sc = 0u;
       if (!((m2 >> lane) & 1u)) s2 = 0u;
+      if (swap) {
+        const uint4 c2 = c0;
+        c0 = c1;
+        c1 = c2;
+      }
       uint4 x[8];
       convert64(c0, c1, sc, x);
       // The group's previous tile is through QK.  (Its chunks' slots come round
@@ -746,17 +757,25 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) arrive_leader(c, K_FULL0 + kslot / kGroup, 4);
-      uint4 y0, y1;
       if (in_half) {
-        const uint2 rc = *reinterpret_cast<const uint2*>(second);
+        const uint2 rc = *reinterpret_cast<const uint2*>(codes + 256 + 8 * vc);
         uint32_t s0, s1;
         scale_pairs(s2, s0, s1);
-        y0 = convert8(rc.x, s0);
-        y1 = convert8(rc.y, s0);
+        const uint4 y0 = convert8(rc.x, s0), y1 = convert8(rc.y, s0);
+        if (!wait_bar(c, K_EMPTY0 + rslot / kGroup, (rround & 1) ^ 1)) return false;
+        unsigned char* rd = sm + OFF_K + rslot * kKChunk + lane * 128;
+        put(rd, 2 * vc, lane, y0);
+        put(rd, 2 * vc + 1, lane, y1);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) arrive_leader(c, K_FULL0 + rslot / kGroup, 1);
       } else {
-        convert64(*reinterpret_cast<const uint4*>(second), *reinterpret_cast<const uint4*>(second + 16), s2, x);
+        const unsigned char* other = stg + STG_OTHER + lane * 128;
+        c0 = *reinterpret_cast<const uint4*>(other + (((2 * vc) ^ (lane & 7)) << 4));
+        c1 = *reinterpret_cast<const uint4*>(other + (((2 * vc + 1) ^ (lane & 7)) << 4));
+        convert64(c0, c1, s2, x);
+        __syncwarp();
       }
-      __syncwarp();
       if (lane == 0) mbar_arrive(&c.bars[STG_EMPTY0 + s]);  // every code is in registers
       if (!wait_bar(c, PV_DONE0 + s, ((g >> 1) & 1) ^ 1)) return false;
       {
@@ -764,18 +783,9 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) put(vd, e, lane, x[e]);
       }
-      if (in_half) {
-        if (!wait_bar(c, K_EMPTY0 + rslot / kGroup, (rround & 1) ^ 1)) return false;
-        unsigned char* rd = sm + OFF_K + rslot * kKChunk + lane * 128;
-        put(rd, 2 * vc, lane, y0);
-        put(rd, 2 * vc + 1, lane, y1);
-      }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        if (in_half) arrive_leader(c, K_FULL0 + rslot / kGroup, 1);
-        arrive_leader(c, V_FULL0 + s, 1);
-      }
+      if (lane == 0) arrive_leader(c, V_FULL0 + s, 1);
       // the group's next tile: eighteen chunks on
       constexpr uint32_t kStep = 2 * kChunks - kKSlots;
       kslot += kStep;
