@@ -19,21 +19,25 @@
 // bytes: the tensor cores and the shared memory that feeds them, not HBM.  A
 // pair splits a tile so that nothing but barriers passes between its CTAs:
 //  * CTA r holds the item's query rows [64 r, 64 r + 64) whole (Q, S, P, O): a
-//    row's softmax needs no other CTA.  O takes 256 columns of TMEM, S two
-//    buffers of 32;
+//    row's softmax needs no other CTA.  TMEM: O 256 columns, S two buffers of 32,
+//    six of the query's nine 64-dim chunks 192;
 //  * S = Q K^T (M = 128, N = 64): CTA r provides tile rows [32 r, 32 r + 32) of
-//    K in nine 64-dim chunks, through a ring of twelve 4 KB slots;
+//    K in nine 64-dim chunks, two stages of 36 KB;
 //  * O = P V (M = 128, N = 256 twice): CTA r provides V dims [256 r, 256 r +
 //    256) of all 64 rows, two stages of 32 KB.
 // The codes come by bulk copies into a two-stage staging area (the CTA's own
 // rows whole, of the other rows only its V dims), and sixteen warps turn them
-// into f16 in the swizzled operand layouts, one row a lane.
+// into f16 in the swizzled operand layouts, one row a lane.  Shared-memory
+// bandwidth is the scarce resource: a tile's MMAs read 24 KB of Q, 68 KB of K and
+// V and 16 KB of P, its conversion writes 68 KB and reads 15.  (With all of Q in
+// shared memory the MMAs read 48 KB more; with the staged codes read across bank
+// conflicts a long call took 476 us instead of 417.)
 //
 // Warp roles (896 threads): 0 and 3 copy, 1 issues QK (even CTA) and owns TMEM, 2
 // issues PV, 4-11 softmax, correction and epilogue, 12-27 conversion and query
-// load.  QK runs up to two tiles ahead of PV, so the tensor cores work while a
-// softmax runs.  Every wait is bounded; a timeout sets the status word and both
-// CTAs unwind.
+// load.  Softmax and conversion each run in two groups that take alternate
+// tiles: their chains of waits and round trips are longer than a tile's MMAs.
+// Every wait is bounded; a timeout sets the status word and both CTAs unwind.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -55,8 +59,8 @@ constexpr int kHalf = kTile / 2;     // KV rows of a tile that one CTA brings fo
 constexpr int kCtaRows = 64;         // query rows of a CTA
 constexpr int kRows = 2 * kCtaRows;  // query rows of a work item
 constexpr int kChunks = 9;           // 64-dim chunks of a row: 8 latent, 1 RoPE
-constexpr int kKSlots = 12;
-constexpr int kGroup = 3;            // chunks that share a full and an empty barrier
+constexpr int kGroup = 3;            // chunks that share a full barrier
+constexpr int kTmemChunks = 6;       // the query's chunks that live in TMEM
 constexpr int kConvWarps = 16;
 constexpr int kSoftWarps = 8;
 constexpr int kFirstSoft = 4, kFirstConv = kFirstSoft + kSoftWarps;
@@ -73,23 +77,26 @@ constexpr uint32_t kQChunk = kCtaRows * 128;  // 64 rows x 64 dims f16, 128B swi
 constexpr uint32_t kKChunk = kHalf * 128;     // 32 rows x 64 dims
 constexpr uint32_t kVChunk = kTile * 128;     // 64 rows x 64 dims
 constexpr uint32_t kVStage = 4 * kVChunk;
-constexpr uint32_t OFF_Q = 0;
-constexpr uint32_t OFF_K = OFF_Q + kChunks * kQChunk;
-constexpr uint32_t OFF_V = OFF_K + kKSlots * kKChunk;
+constexpr uint32_t kKStage = kChunks * kKChunk;
+constexpr uint32_t kPTile = kCtaRows * 128;
+constexpr uint32_t OFF_Q = 0;  // chunks kTmemChunks..8
+constexpr uint32_t OFF_K = OFF_Q + (kChunks - kTmemChunks) * kQChunk;
+constexpr uint32_t OFF_V = OFF_K + 2 * kKStage;
 constexpr uint32_t OFF_P = OFF_V + 2 * kVStage;
-constexpr uint32_t OFF_STG = OFF_P + kCtaRows * 128;
+constexpr uint32_t OFF_STG = OFF_P + 2 * kPTile;
 // a staging stage: own rows' codes, other rows' V codes, scales of the tile's two halves
 constexpr uint32_t STG_OWN = 0;
 constexpr uint32_t STG_OTHER = STG_OWN + kHalf * kFp4CodeBytes;
 constexpr uint32_t STG_SCALES = STG_OTHER + kHalf * 128;
 constexpr uint32_t kStage = STG_SCALES + kTile * kFp4ScaleBytes;
 constexpr uint32_t OFF_BARS = OFF_STG + 2 * kStage;
-constexpr uint32_t OFF_XMAX = OFF_BARS + 320;       // float [2][256]: tile maxima by tile parity
-constexpr uint32_t OFF_XSUM = OFF_XMAX + 2 * 256 * 4;  // float [256]: row sums, end of an item
-constexpr uint32_t OFF_QSCALE = OFF_XSUM + 256 * 4;    // float [4][64]: 2^-k by item
+constexpr uint32_t OFF_XMAX = OFF_BARS + 352;              // float [4][128]: tile maxima by tile mod 4
+constexpr uint32_t OFF_MREF = OFF_XMAX + 4 * 128 * 4;      // float [2][64]: references by tile parity
+constexpr uint32_t OFF_XSUM = OFF_MREF + 2 * kCtaRows * 4;  // float [2][2][128]: (sum, reference) by group
+constexpr uint32_t OFF_QSCALE = OFF_XSUM + 4 * 128 * 4;    // float [4][64]: 2^-k by item
 constexpr uint32_t OFF_TMEM = OFF_QSCALE + 4 * kCtaRows * 4;
-constexpr uint32_t OFF_ABORT = OFF_TMEM + 16;
-constexpr uint32_t OFF_MASK = OFF_ABORT + 16;  // uint32 [2][2]: rows in use, by stage and half
+constexpr uint32_t OFF_ABORT = OFF_TMEM + 8;
+constexpr uint32_t OFF_MASK = OFF_ABORT + 8;  // uint32 [2][2]: rows in use, by stage and half
 constexpr uint32_t kSmemBytes = OFF_MASK + 16;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 static_assert(OFF_K % 1024 == 0 && OFF_V % 1024 == 0 && OFF_P % 1024 == 0 && kStage % 16 == 0 &&
@@ -100,24 +107,27 @@ static_assert(OFF_K % 1024 == 0 && OFF_V % 1024 == 0 && OFF_P % 1024 == 0 && kSt
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t TM_O = 0;    // lane: query row (mod 64) and V half; 256 V dims
 constexpr uint32_t TM_S = 256;  // two 32-column buffers; lane: query row and KV half
+constexpr uint32_t TM_Q = 320;  // chunks 0..5 of the query row (mod 64), pairs of f16
 
 enum Bar {
   STG_FULL0, STG_EMPTY0 = STG_FULL0 + 2,
-  K_FULL0 = STG_EMPTY0 + 2,            // even CTA: both CTAs' chunks are in a group's slots
-  K_EMPTY0 = K_FULL0 + kKSlots / kGroup,
-  V_FULL0 = K_EMPTY0 + kKSlots / kGroup,  // even CTA
+  K_FULL0 = STG_EMPTY0 + 2,   // even CTA: [tile parity][3], both CTAs' chunks are there
+  V_FULL0 = K_FULL0 + 2 * (kChunks / kGroup),  // even CTA
   PV_DONE0 = V_FULL0 + 2,              // by tile parity: V stage and P free, O stable
-  S_FULL0 = PV_DONE0 + 2, S_EMPTY0 = S_FULL0 + 2,  // S_EMPTY: even CTA
-  P_FULL = S_EMPTY0 + 2,               // even CTA
-  Q_FULL, Q_EMPTY,                     // Q_FULL: even CTA
-  QS_FULL0,                            // 4: by item, the query rows' scales are written
+  S_FULL0 = PV_DONE0 + 2,              // S computed, K stage free
+  S_EMPTY0 = S_FULL0 + 2,              // even CTA
+  P_FULL0 = S_EMPTY0 + 2,              // even CTA
+  Q_FULL = P_FULL0 + 2, Q_EMPTY,       // Q_FULL: even CTA
+  QX,                                  // a query's scales (and shared-memory chunks) are written
+  QS_FULL0,                            // 4: by item, the same for the softmax
   XM0 = QS_FULL0 + 4,                  // 4: [tile parity][pair of warps] maxima exchanged
-  XS0 = XM0 + 4,                       // 2: [pair of warps] row sums exchanged
+  MR0 = XM0 + 4,                       // 4: the same, reference published
+  XS0 = MR0 + 4,                       // 2: [pair] row sums exchanged
   EPI = XS0 + 2,                       // the partial is written
   DRAIN0,                              // 2: every MMA of an issuing warp has completed
   NUM_BARS = DRAIN0 + 2
 };
-static_assert(NUM_BARS * 8 <= 320, "barrier area");
+static_assert(NUM_BARS * 8 <= 352, "barrier area");
 
 struct Ctx {
   uint64_t* bars;
@@ -265,17 +275,17 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
 
   if (tid == 0) {
     for (int i = 0; i < NUM_BARS; ++i) {
-      uint32_t n = 1;  // one commit
-      if (i >= STG_FULL0 && i < STG_FULL0 + 2) n = 1 + 32;  // bulk copies, each lane's own
-      if (i >= STG_EMPTY0 && i < STG_EMPTY0 + 2) n = kConvWarps / 2;
+      uint32_t n = 1;  // one commit, or one warp
+      if (i >= STG_FULL0 && i < STG_EMPTY0) n = 1 + 32;  // bulk copies, each lane's own
+      if (i >= STG_EMPTY0 && i < K_FULL0) n = kConvWarps / 2;
       // a latent chunk's warp counts four times, as the RoPE chunk has four warps
-      if (i >= K_FULL0 && i < K_FULL0 + kKSlots / kGroup) n = 2 * 4 * kGroup;
+      if (i >= K_FULL0 && i < V_FULL0) n = 2 * 4 * kGroup;
       if (i >= V_FULL0 && i < V_FULL0 + 2) n = kConvWarps;  // half the warps of both CTAs
-      if (i >= S_EMPTY0 && i < S_EMPTY0 + 2) n = 2 * kSoftWarps;
-      if (i == P_FULL) n = 2 * kSoftWarps;
+      if (i >= S_EMPTY0 && i < P_FULL0 + 2) n = kSoftWarps;  // half the warps of both CTAs
       if (i == Q_FULL) n = 2 * kConvWarps;
-      if (i >= QS_FULL0 && i < QS_FULL0 + 4) n = kConvWarps;
-      if (i >= XM0 && i < XS0 + 2) n = kSoftWarps / 2;
+      if (i == QX || (i >= QS_FULL0 && i < QS_FULL0 + 4)) n = kConvWarps;
+      if (i >= XM0 && i < XM0 + 4) n = 2;
+      if (i >= XS0 && i < XS0 + 2) n = 4;
       if (i == EPI) n = kSoftWarps;
       mbar_init(&c.bars[i], n);
     }
@@ -340,7 +350,7 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
         const int j0 = it.kv_begin + t * kTile, r0 = walk.row(j0);
         const bool on0 = id0 >= 0 && walk.seen(r0, r0 + kHalf - 1);
         const bool on1 = id1 >= 0 && j0 + kHalf < it.kv_end && walk.seen(r0 + kHalf, r0 + kTile - 1);
-        const int s = g & 1;
+        const uint32_t s = g & 1, use = g >> 1;
         unsigned char* stg = sm + OFF_STG + s * kStage;
         uint64_t* full = &c.bars[STG_FULL0 + s];
         if (bulk) {
@@ -351,7 +361,7 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
           const uint32_t mask1 =
               __ballot_sync(0xffffffffu, on1 && j0 + kHalf + lane < it.kv_end &&
                                              walk.seen(r0 + kHalf + lane, r0 + kHalf + lane));
-          if (!wait_bar(c, STG_EMPTY0 + s, ((g >> 1) & 1) ^ 1)) goto fail_copy;
+          if (!wait_bar(c, STG_EMPTY0 + s, (use & 1) ^ 1)) goto fail_copy;
           if (lane == 0) {
             const int row1 = npg == 1 ? kHalf : 0;  // first row of half 1 in its page
             const unsigned char* pg0 = cache + (size_t)(on0 ? id0 : 0) * page_bytes;
@@ -373,7 +383,7 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
           }
           __syncwarp();
         } else {
-          if (!wait_bar(c, STG_EMPTY0 + s, ((g >> 1) & 1) ^ 1)) goto fail_copy;
+          if (!wait_bar(c, STG_EMPTY0 + s, (use & 1) ^ 1)) goto fail_copy;
           // eight 16-byte units of a row: eight lanes a row
           if (rank == 0 ? on1 : on0) {
             const unsigned char* src = cache + (size_t)(rank == 0 ? id1 : id0) * page_bytes +
@@ -388,7 +398,7 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
               cp_async_16(dst + i * 512 + ((u ^ (r7 + 4 * (i & 1))) << 4), src + i * 4 * kFp4CodeBytes);
           }
           cp_async_arrive(full);
-          // this CTA's half of the tiles up to kAhead on, to L2: two staged tiles
+          // this CTA's half of the tiles up to kAhead on, to L2: the staged tiles
           // cover an L2 round trip but not one to HBM
           for (int a = t == 0 ? 2 : kAhead; a <= kAhead; ++a) {
             const int i = (t + a) * npg + (npg == 2 ? rank : 0);
@@ -422,7 +432,6 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
       const uint64_t q_desc = smem_desc(smem_u32(sm + OFF_Q), 16, 1024, kSwizzle128B);
       const uint64_t k_desc = smem_desc(smem_u32(sm + OFF_K), 16, 1024, kSwizzle128B);
       uint32_t g = 0;
-      uint32_t group = 0, round = 0;  // ring place of the next three chunks
       int n_item = 0;
       for (int idx = item_begin; idx < item_end; ++idx) {
         const int nt = __shfl_sync(0xffffffffu, n_tiles_of(items[idx]), 0);
@@ -432,31 +441,30 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
         for (int t = 0; t < nt; ++t, ++g) {
           const uint32_t sb = g & 1;
           if (!wait_bar(c, S_EMPTY0 + sb, ((g >> 1) & 1) ^ 1)) goto fail_qk;
+          const uint64_t kd = k_desc + sb * (kKStage >> 4);
 #pragma unroll
           for (int k3 = 0; k3 < kChunks / kGroup; ++k3) {
-            if (!wait_bar(c, K_FULL0 + group, round & 1)) goto fail_qk;
+            if (!wait_bar(c, K_FULL0 + sb * (kChunks / kGroup) + k3, (g >> 1) & 1)) goto fail_qk;
             tc_fence_after();
             if (elect_one()) {
-              const uint64_t kd = k_desc + group * (kGroup * kKChunk >> 4);
 #pragma unroll
-              for (int k = 0; k < kGroup; ++k)
+              for (int k = kGroup * k3; k < kGroup * (k3 + 1); ++k)
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                  mma_f16_pair_ss(tmem + TM_S + 32 * sb,
-                                  q_desc + ((kGroup * k3 + k) * kQChunk >> 4) + 2 * ks,
-                                  kd + (k * kKChunk >> 4) + 2 * ks, idesc,
-                                  (k3 | k | ks) != 0 ? 1u : 0u);
-              mma_commit_pair(&c.bars[K_EMPTY0 + group]);
+                for (int ks = 0; ks < 4; ++ks) {
+                  const uint64_t b_desc = kd + (k * kKChunk >> 4) + 2 * ks;
+                  if (k < kTmemChunks)
+                    mma_f16_pair_ts(tmem + TM_S + 32 * sb, tmem + TM_Q + 32 * k + 8 * ks, b_desc, idesc,
+                                    (k | ks) != 0 ? 1u : 0u);
+                  else
+                    mma_f16_pair_ss(tmem + TM_S + 32 * sb,
+                                    q_desc + ((k - kTmemChunks) * kQChunk >> 4) + 2 * ks, b_desc, idesc, 1u);
+                }
               if (k3 == kChunks / kGroup - 1) {
                 mma_commit_pair(&c.bars[S_FULL0 + sb]);
                 if (t + 1 == nt) mma_commit_pair(&c.bars[Q_EMPTY]);
               }
             }
             __syncwarp();
-            if (++group == kKSlots / kGroup) {
-              group = 0;
-              ++round;
-            }
           }
         }
       }
@@ -481,7 +489,7 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
         for (int t = 0; t < nt; ++t, ++g) {
           const uint32_t s = g & 1;
           if (!wait_bar(c, V_FULL0 + s, (g >> 1) & 1)) goto fail_pv;
-          if (!wait_bar(c, P_FULL, g & 1)) goto fail_pv;
+          if (!wait_bar(c, P_FULL0 + s, (g >> 1) & 1)) goto fail_pv;
           tc_fence_after();
           if (elect_one()) {
             const uint64_t v = v_desc + s * (kVStage >> 4);
@@ -489,7 +497,7 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
             for (int ks = 0; ks < kTile / 16; ++ks)
 #pragma unroll
               for (int j = 0; j < 2; ++j)
-                mma_f16_pair_ss(tmem + TM_O + 128 * j, p_desc + 2 * ks,
+                mma_f16_pair_ss(tmem + TM_O + 128 * j, p_desc + s * (kPTile >> 4) + 2 * ks,
                                 v + ((j * 2 * kVChunk + ks * 16 * 128) >> 4), idesc,
                                 (t == 0 && ks == 0) ? 0u : 1u);
             mma_commit_pair(&c.bars[PV_DONE0 + s]);
@@ -507,11 +515,12 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
     }
   } else if (warp < kFirstConv) {
     // ------------------------------------------------------------ softmax, correction, epilogue
-    // Thread = TMEM lane l = 32 (warp mod 4) + lane and column part cc: query row
-    // l mod 64 of the CTA, KV rows (columns of S) 32 (l / 64) + 16 cc + [0, 16),
-    // V dims (columns of O) 256 (l / 64) + 128 cc + [0, 128).  A row's four
-    // threads are in four warps that exchange maxima through shared memory.
-    const int quad = warp & 3, cc = (warp - kFirstSoft) >> 2;
+    // Two groups of four warps take alternate tiles.  Thread = TMEM lane l = 32
+    // (warp mod 4) + lane: query row l mod 64 of the CTA and KV rows (columns of S)
+    // 32 (l / 64) + [0, 32).  The row's other thread is in warp ^ 2 of the group;
+    // the running reference passes from tile to tile, and so between the groups,
+    // through shared memory.
+    const int quad = warp & 3, grp = (warp - kFirstSoft) >> 2;
     const int l = 32 * quad + lane, hh = quad >> 1, row = l & 63;
     const int q = kCtaRows * rank + row;  // row of the work item
     const int pair = quad & 1;
@@ -519,15 +528,15 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
     const float bmm1 = run_bmm1(p, c.status) * kLog2e;
     const float bmm2 = run_bmm2(p);
     const int W = max(p.cp_world, 1);
-    float* xmax = reinterpret_cast<float*>(sm + OFF_XMAX);
+    float* mref = reinterpret_cast<float*>(sm + OFF_MREF);
     float* xsum = reinterpret_cast<float*>(sm + OFF_XSUM);
     const float* qscale = reinterpret_cast<const float*>(sm + OFF_QSCALE);
-    unsigned char* prow = sm + OFF_P + row * 128;
+    unsigned char* prow = sm + OFF_P + kPTile * grp + row * 128;
     uint4* part_o = reinterpret_cast<uint4*>(ws + lay.part_o);
     float* part_lse = reinterpret_cast<float*>(ws + lay.part_lse);
     int* comb_done = reinterpret_cast<int*>(ws + lay.comb_done);
     uint32_t g = 0;
-    int n_item = 0, n_split = 0;
+    int n_item = 0;
     for (int idx = item_begin; idx < item_end; ++idx) {
       const WorkItem it = items[idx];
       const int nt = n_tiles_of(it);
@@ -546,17 +555,18 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
       const int clean_lo = p.window > 0 ? last_of(n_rows - 1) - p.window + 1 : INT_MIN;
       if (!wait_bar(c, QS_FULL0 + (n_item & 3), (n_item >> 2) & 1)) goto fail_soft;
       const float scale = bmm1 * qscale[(n_item & 3) * kCtaRows + row];
+      // this group's share of the row sum, relative to its latest reference m
       float m = -INFINITY, l_part = 0.f;
       for (int t = 0; t < nt; ++t, ++g) {
-        const int sb = g & 1;
-        if (!wait_bar(c, S_FULL0 + sb, (g >> 1) & 1)) goto fail_soft;
+        if ((int)(g & 1) != grp) continue;
+        if (!wait_bar(c, S_FULL0 + grp, (g >> 1) & 1)) goto fail_soft;
         tc_fence_after();
-        uint32_t v[16];
-        tmem_ld_32x32b_x16(tm + TM_S + 32 * sb + 16 * cc, v);
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(tm + TM_S + 32 * grp, v);
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_leader(c, S_EMPTY0 + sb, 1);
+        if (lane == 0) arrive_leader(c, S_EMPTY0 + grp, 1);
         const int v0 = it.kv_begin + t * kTile;        // virtual row of the tile
         const int r0 = walk.row(v0);                    // its row
         const int valid = it.kv_end - v0;               // rows of the tile inside the item
@@ -565,39 +575,55 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
         uint32_t hidden = 0;  // columns that the mask takes out
         if (!clean) {
 #pragma unroll 1
-          for (int j = 0; j < 16; ++j) {
-            const int k = 32 * hh + 16 * cc + j, at = r0 + k;
+          for (int j = 0; j < 32; ++j) {
+            const int k = 32 * hh + j, at = r0 + k;
             if (!(at <= last && k < valid && (at >= low || at < p.sinks))) hidden |= 1u << j;
           }
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
+          for (int j = 0; j < 32; ++j)
             if ((hidden >> j) & 1u) v[j] = 0xFF800000u;  // -inf
         }
         float mt[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          mt[j] = fmaxf(fmaxf(__uint_as_float(v[j]), __uint_as_float(v[j + 4])),
-                        fmaxf(__uint_as_float(v[j + 8]), __uint_as_float(v[j + 12])));
-        float* xm = xmax + sb * 256;
-        xm[128 * cc + l] = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
+        for (int j = 0; j < 4; ++j) mt[j] = __uint_as_float(v[j]);
+#pragma unroll
+        for (int j = 4; j < 32; ++j) mt[j & 3] = fmaxf(mt[j & 3], __uint_as_float(v[j]));
+        // (four buffers: a partner that still reads the maxima of tile g has let QK
+        // of tile g + 2 into S, but not of g + 4)
+        float* xmax = reinterpret_cast<float*>(sm + OFF_XMAX) + 128 * (g & 3);
+        xmax[l] = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
+        // The reference after the previous tile, which the other group had.  Every
+        // tile but the very first waits for it, and before its own maximum goes
+        // out, so that the barriers' phases stay in step.
+        float m_prev = -INFINITY;
+        if (g > 0) {
+          if (!wait_bar(c, MR0 + 2 * (grp ^ 1) + pair, ((g - 1) >> 1) & 1)) goto fail_soft;
+          if (t > 0) m_prev = mref[kCtaRows * (grp ^ 1) + row];
+        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&c.bars[XM0 + 2 * sb + pair]);
-        if (!wait_bar(c, XM0 + 2 * sb + pair, (g >> 1) & 1)) goto fail_soft;
-        // (all four from shared memory: the same result in the row's four threads;
-        // the scale is not negative, so it may come after the maximum)
-        const float m_raw = fmaxf(fmaxf(xm[row], xm[row + 64]), fmaxf(xm[row + 128], xm[row + 192]));
+        if (lane == 0) mbar_arrive(&c.bars[XM0 + 2 * grp + pair]);
+        if (!wait_bar(c, XM0 + 2 * grp + pair, (g >> 1) & 1)) goto fail_soft;
+        // (both from shared memory: the same result in the row's two threads; the
+        // scale is not negative, so it may come after the maximum)
+        const float m_raw = fmaxf(xmax[row], xmax[row + 64]);
         const float m_tile = m_raw == -INFINITY ? m_raw : m_raw * scale;
-        const float m_new = (m_tile > m + kRescaleThreshold || t == 0) ? m_tile : m;
-        const bool need = t > 0 && m_new != m;
-        const float f = need ? ex2(m - m_new) : 1.f;  // m = -inf: 0
-        m = m_new;
+        const float m_new = (m_tile > m_prev + kRescaleThreshold || t == 0) ? m_tile : m_prev;
+        if (hh == 0) {
+          mref[kCtaRows * grp + row] = m_new;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&c.bars[MR0 + 2 * grp + pair]);
+        }
+        const bool need = t > 0 && m_new != m_prev;
+        if (m_new > m) {  // rebase this group's share (0 while m = -inf)
+          l_part *= ex2(m - m_new);
+          m = m_new;
+        }
         const float ref = kPShift - (m == -INFINITY ? 0.f : m);
         // (rows past the request's own compute something that nothing reads)
         const uint64_t scale2 = pack_f32x2(scale, scale), ref2 = pack_f32x2(ref, ref);
-        uint32_t pw[8];
         uint64_t rs[2] = {0, 0};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 16; ++j) {
           float a, b;
           unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), scale2, ref2), a, b);
           a = ex2(a);
@@ -608,47 +634,57 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
           }
           rs[j & 1] = add_f32x2(rs[j & 1], pack_f32x2(a, b));
           const __half2 h = __floats2half2_rn(a, b);
-          pw[j] = *reinterpret_cast<const uint32_t*>(&h);
+          v[j] = *reinterpret_cast<const uint32_t*>(&h);
         }
         {
           float a, b;
           unpack_f32x2(add_f32x2(rs[0], rs[1]), a, b);
-          l_part = fmaf(l_part, f, a + b);
+          l_part += a + b;
         }
-        // PV of the previous tile is done: its P may be replaced, and O is stable
-        if (g > 0 && !wait_bar(c, PV_DONE0 + ((g - 1) & 1), ((g - 1) >> 1) & 1)) goto fail_soft;
+        // this P tile has been read
+        if (!wait_bar(c, PV_DONE0 + grp, ((g >> 1) & 1) ^ 1)) goto fail_soft;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          put(prow, 4 * hh + u, row, make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]));
         if (__any_sync(0xffffffffu, need)) {
+          // O, stable once PV of the previous tile is done, to the new reference
+          if (!wait_bar(c, PV_DONE0 + (grp ^ 1), ((g - 1) >> 1) & 1)) goto fail_soft;
           tc_fence_after();
+          const float f = need ? ex2(m_prev - m_new) : 1.f;  // m_prev = -inf: 0
 #pragma unroll 1
-          for (int k = 0; k < 8; ++k) {
+          for (int k = 0; k < 16; ++k) {
             uint32_t x[16];
-            tmem_ld_32x32b_x16(tm + TM_O + 128 * cc + 16 * k, x);
+            tmem_ld_32x32b_x16(tm + TM_O + 16 * k, x);
             tmem_wait_ld();
 #pragma unroll
             for (int j = 0; j < 16; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * f);
-            tmem_st_32x32b_x16(tm + TM_O + 128 * cc + 16 * k, x);
+            tmem_st_32x32b_x16(tm + TM_O + 16 * k, x);
           }
           tmem_wait_st();
           tc_fence_before();
         }
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-          put(prow, 4 * hh + 2 * cc + u, row,
-              make_uint4(pw[4 * u], pw[4 * u + 1], pw[4 * u + 2], pw[4 * u + 3]));
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) arrive_leader(c, P_FULL, 1);
+        if (lane == 0) arrive_leader(c, P_FULL0 + grp, 1);
       }
-      // the row's sum: its four threads' shares
-      xsum[128 * cc + l] = l_part;
+      // the row's sum: two threads of each group, each relative to its reference
+      xsum[256 * grp + l] = l_part;
+      xsum[256 * grp + 128 + l] = m;
       __syncwarp();
       if (lane == 0) mbar_arrive(&c.bars[XS0 + pair]);
       if (!wait_bar(c, XS0 + pair, n_item & 1)) goto fail_soft;
-      const float l_row = (xsum[row] + xsum[row + 64]) + (xsum[row + 128] + xsum[row + 192]);
-      const float lse = l_row > 0.f ? (m - kPShift + log2f(l_row)) * kLn2 : -INFINITY;
+      float m_fin, l_row = 0.f;
+      {
+        const float m0 = xsum[128 + row], m1 = xsum[256 + 128 + row];
+        m_fin = fmaxf(m0, m1);  // a reference never falls within an item
+        const float l0 = xsum[row] + xsum[row + 64], l1 = xsum[256 + row] + xsum[256 + row + 64];
+        if (m0 != -INFINITY) l_row += l0 * ex2(m0 - m_fin);
+        if (m1 != -INFINITY) l_row += l1 * ex2(m1 - m_fin);
+      }
+      const float lse = l_row > 0.f ? (m_fin - kPShift + log2f(l_row)) * kLn2 : -INFINITY;
       const float inv = l_row > 0.f ? 1.f / l_row : 0.f;
       const size_t grow = (size_t)it.q_start * H + row0 + q;
-      if (row_ok && hh == 0 && cc == 0) {
+      if (row_ok && hh == 0 && grp == 0) {
         if (it.slot >= 0)
           part_lse[(size_t)it.slot * kRows + q] = lse;
         else if (p.return_lse)
@@ -657,10 +693,11 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
       if (!wait_bar(c, PV_DONE0 + ((g - 1) & 1), ((g - 1) >> 1) & 1)) goto fail_soft;
       tc_fence_after();
       const float s2 = it.slot < 0 ? inv * bmm2 : inv;
+      // columns of O, V dims 256 hh + 128 grp + [0, 128), 16 at a time
 #pragma unroll 1
       for (int k = 0; k < 8; ++k) {
         uint32_t x[16];
-        tmem_ld_32x32b_x16(tm + TM_O + 128 * cc + 16 * k, x);
+        tmem_ld_32x32b_x16(tm + TM_O + 128 * grp + 16 * k, x);
         tmem_wait_ld();
         if (!row_ok) continue;
         uint32_t o[8];
@@ -670,7 +707,7 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
                                                          __uint_as_float(x[2 * e + 1]) * s2);
           o[e] = *reinterpret_cast<const uint32_t*>(&h);
         }
-        const int chunk = 16 * hh + 8 * cc + k;  // of 16 dims
+        const int chunk = 16 * hh + 8 * grp + k;  // of 16 dims
         uint4 *d0, *d1;
         if (it.slot < 0) {
           d0 = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.out) + grow * kVDim + 16 * chunk);
@@ -683,19 +720,14 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
         *d1 = make_uint4(o[4], o[5], o[6], o[7]);
       }
       tc_fence_before();
-      if (it.slot >= 0) {
-        // the warps' partial is visible GPU-wide, then this CTA counts its chunk
+      // both groups have read O before the next item's first PV overwrites it
+      if (it.slot >= 0) __threadfence();  // ... and the partial is visible GPU-wide
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c.bars[EPI]);
+      if (!wait_bar(c, EPI, n_item & 1)) goto fail_soft;
+      if (it.slot >= 0 && warp == kFirstSoft && lane == 0 && it.comb >= 0) {
         __threadfence();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c.bars[EPI]);
-        if (warp == kFirstSoft) {
-          if (!wait_bar(c, EPI, n_split & 1)) goto fail_soft;
-          if (lane == 0 && it.comb >= 0) {
-            __threadfence();
-            atomicAdd(comb_done + it.comb, 1);
-          }
-        }
-        ++n_split;
+        atomicAdd(comb_done + it.comb, 1);
       }
       ++n_item;
     }
@@ -716,12 +748,9 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
     const bool in_half = (k >> 2) == rank;
     float* qscale = reinterpret_cast<float*>(sm + OFF_QSCALE);
     uint32_t g = 0;
-    // ring places (chunk 9 g + k of twelve) of this warp's chunk and the RoPE chunk
-    uint32_t kslot = (kChunks * grp + k) % kKSlots, kround = (kChunks * grp + k) / kKSlots;
-    uint32_t rslot = (kChunks * grp + 8) % kKSlots, rround = (kChunks * grp + 8) / kKSlots;
     int n_item = 0;
     auto convert_tile = [&]() -> bool {
-      const int s = (int)grp;
+      const uint32_t s = grp;
       if (!wait_bar(c, STG_FULL0 + s, (g >> 1) & 1)) return false;
       const unsigned char* stg = sm + OFF_STG + s * kStage;
       const int own = kHalf * rank + lane, oth = kHalf * (rank ^ 1) + lane;
@@ -746,29 +775,24 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
       }
       uint4 x[8];
       convert64(c0, c1, sc, x);
-      // The group's previous tile is through QK.  (Its chunks' slots come round
-      // before the other group's tile fills the ones between: without this wait a
-      // slot's empty barrier could be two uses behind, where its parity reads as
-      // the phase that is waited for.)
-      if (!wait_bar(c, S_FULL0 + s, ((g >> 1) & 1) ^ 1)) return false;
-      if (!wait_bar(c, K_EMPTY0 + kslot / kGroup, (kround & 1) ^ 1)) return false;
+      // QK of the group's previous tile has read this K stage
+      if (!wait_bar(c, S_FULL0 + grp, ((g >> 1) & 1) ^ 1)) return false;
+      unsigned char* ks = sm + OFF_K + grp * kKStage + lane * 128;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) put(sm + OFF_K + kslot * kKChunk + lane * 128, e, lane, x[e]);
+      for (int e = 0; e < 8; ++e) put(ks + k * kKChunk, e, lane, x[e]);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) arrive_leader(c, K_FULL0 + kslot / kGroup, 4);
+      if (lane == 0) arrive_leader(c, K_FULL0 + 3 * grp + k / kGroup, 4);
       if (in_half) {
         const uint2 rc = *reinterpret_cast<const uint2*>(codes + 256 + 8 * vc);
         uint32_t s0, s1;
         scale_pairs(s2, s0, s1);
         const uint4 y0 = convert8(rc.x, s0), y1 = convert8(rc.y, s0);
-        if (!wait_bar(c, K_EMPTY0 + rslot / kGroup, (rround & 1) ^ 1)) return false;
-        unsigned char* rd = sm + OFF_K + rslot * kKChunk + lane * 128;
-        put(rd, 2 * vc, lane, y0);
-        put(rd, 2 * vc + 1, lane, y1);
+        put(ks + 8 * kKChunk, 2 * vc, lane, y0);
+        put(ks + 8 * kKChunk, 2 * vc + 1, lane, y1);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) arrive_leader(c, K_FULL0 + rslot / kGroup, 1);
+        if (lane == 0) arrive_leader(c, K_FULL0 + 3 * grp + 2, 1);
       } else {
         const unsigned char* other = stg + STG_OTHER + lane * 128;
         c0 = *reinterpret_cast<const uint4*>(other + (((2 * vc) ^ (lane & 7)) << 4));
@@ -777,85 +801,89 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
         __syncwarp();
       }
       if (lane == 0) mbar_arrive(&c.bars[STG_EMPTY0 + s]);  // every code is in registers
-      if (!wait_bar(c, PV_DONE0 + s, ((g >> 1) & 1) ^ 1)) return false;
+      if (!wait_bar(c, PV_DONE0 + grp, ((g >> 1) & 1) ^ 1)) return false;
       {
-        unsigned char* vd = sm + OFF_V + s * kVStage + vc * kVChunk + (in_half ? own : oth) * 128;
+        unsigned char* vd = sm + OFF_V + grp * kVStage + vc * kVChunk + (in_half ? own : oth) * 128;
 #pragma unroll
         for (int e = 0; e < 8; ++e) put(vd, e, lane, x[e]);
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) arrive_leader(c, V_FULL0 + s, 1);
-      // the group's next tile: eighteen chunks on
-      constexpr uint32_t kStep = 2 * kChunks - kKSlots;
-      kslot += kStep;
-      kround += 1 + kslot / kKSlots;
-      kslot %= kKSlots;
-      rslot += kStep;
-      rround += 1 + rslot / kKSlots;
-      rslot %= kKSlots;
+      if (lane == 0) arrive_leader(c, V_FULL0 + grp, 1);
       return true;
     };
-    // Rows [4 w, 4 w + 4) of the item's query in this CTA: f16 in nine swizzled
-    // chunks, and each row's factor 2^-k.  Rows past the query's end are zero.
+    // The item's query, rows [64 rank, 64 rank + 64) (those past the query's end
+    // are zero).  First the rows' factors and shared-memory chunks, four rows a
+    // warp, a row's 72 16-byte units over its lanes; then, with the factors, the
+    // TMEM chunks, a thread per row and 96 dims (both copies of a row, see
+    // mma_f16_pair_ts).
+    const long long q_rows = p.total_q * H;
+    auto unit_of = [&](long long qr, int u) -> uint4 {  // unit u of a row, as f16 times 1 or raw bf16
+      if (qr >= q_rows) return make_uint4(0, 0, 0, 0);
+      if (p.q_fp8) return e4m3x8_to_f16(__ldg(reinterpret_cast<const uint2*>(p.query) + qr * 72 + u));
+      return __ldg(reinterpret_cast<const uint4*>(p.query) + qr * 72 + u);
+    };
     auto load_query = [&](const WorkItem& it, int n) -> bool {
-      const long long q_rows = p.total_q * H;
-      const long long first = (long long)it.q_start * H + (long long)it.g * kRows + kCtaRows * rank + 4 * w;
-      const int u2 = 64 + (lane & 7);
+      const long long q0 = (long long)it.q_start * H + (long long)it.g * kRows + kCtaRows * rank;
+      float* scales = qscale + (n & 3) * kCtaRows;
+      constexpr int kFirstUnit = 8 * kTmemChunks;  // of the shared-memory chunks
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
         uint4 x[2][3];
-        if (p.q_fp8) {
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const long long qr = first + 2 * half + r;
-            const uint2* src = reinterpret_cast<const uint2*>(p.query) + (qr < q_rows ? qr : 0) * 72;
-            const bool in = qr < q_rows;
-            uint2 y[3] = {in ? __ldg(src + lane) : make_uint2(0, 0), in ? __ldg(src + 32 + lane) : make_uint2(0, 0),
-                          in ? __ldg(src + u2) : make_uint2(0, 0)};
-#pragma unroll
-            for (int k = 0; k < 3; ++k) x[r][k] = make_uint4(y[k].x, y[k].y, 0, 0);
-          }
-        } else {
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const long long qr = first + 2 * half + r;
-            const uint4* src = reinterpret_cast<const uint4*>(p.query) + (qr < q_rows ? qr : 0) * 72;
-            const bool in = qr < q_rows;
-            x[r][0] = in ? __ldg(src + lane) : make_uint4(0, 0, 0, 0);
-            x[r][1] = in ? __ldg(src + 32 + lane) : make_uint4(0, 0, 0, 0);
-            x[r][2] = in ? __ldg(src + u2) : make_uint4(0, 0, 0, 0);
-          }
+        for (int r = 0; r < 2; ++r) {
+          const long long qr = q0 + 4 * w + 2 * half + r;
+          x[r][0] = unit_of(qr, lane);
+          x[r][1] = unit_of(qr, 32 + lane);
+          x[r][2] = unit_of(qr, 64 + (lane & 7));
         }
         // every QK of the previous item has read its query
         if (half == 0 && !wait_bar(c, Q_EMPTY, (n & 1) ^ 1)) return false;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const int row = 4 * w + 2 * half + r;
-          int k = 0;
+          int e = 0;
           if (!p.q_fp8) {
             uint32_t mb = __vmaxu2(__vmaxu2(max_bits(x[r][0]), max_bits(x[r][1])), max_bits(x[r][2]));
             mb = __reduce_max_sync(0xffffffffu, max(mb & 0xFFFFu, mb >> 16));
-            k = query_exponent(mb);
+            e = query_exponent(mb);
           }
-          const float up = __uint_as_float((uint32_t)(127 + k) << 23);
+          const float up = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
-          for (int e = 0; e < 3; ++e) {
-            const int unit = e < 2 ? 32 * e + lane : u2;
-            const uint4 v = p.q_fp8 ? e4m3x8_to_f16(make_uint2(x[r][e].x, x[r][e].y))
-                                    : bf16x8_to_f16(x[r][e], up);
-            if (e < 2 || lane < 8)
-              put(sm + OFF_Q + (unit >> 3) * kQChunk + row * 128, unit & 7, row, v);
+          for (int i = 1; i < 3; ++i) {
+            const int unit = i == 1 ? 32 + lane : 64 + lane;
+            const uint4 f = p.q_fp8 ? x[r][i] : bf16x8_to_f16(x[r][i], up);
+            if (unit >= kFirstUnit && unit < 72)
+              put(sm + OFF_Q + ((unit - kFirstUnit) >> 3) * kQChunk + row * 128, unit & 7, row, f);
           }
-          if (lane == 0) qscale[(n & 3) * kCtaRows + row] = __uint_as_float((uint32_t)(127 - k) << 23);
+          if (lane == 0) scales[row] = __uint_as_float((uint32_t)(127 - e) << 23);
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
+        mbar_arrive(&c.bars[QX]);
         mbar_arrive(&c.bars[QS_FULL0 + (n & 3)]);
-        arrive_leader(c, Q_FULL, 1);
       }
+      if (!wait_bar(c, QX, n & 1)) return false;
+      const int quad = warp & 3, row = (32 * quad + lane) & 63, part = w >> 2;
+      const float up = 1.f / scales[row];  // a power of two: exact
+      const uint32_t tq = tmem + ((uint32_t)(32 * quad) << 16) + TM_Q + 48 * part;
+#pragma unroll 1
+      for (int j = 0; j < 3; ++j) {  // 32 dims: four units, sixteen columns
+        uint4 x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[u] = unit_of(q0 + row, 12 * part + 4 * j + u);
+        if (!p.q_fp8) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) x[u] = bf16x8_to_f16(x[u], up);
+        }
+        tmem_st_32x32b_x16(tq + 16 * j, *reinterpret_cast<const uint32_t(*)[16]>(x));
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_leader(c, Q_FULL, 1);
       return true;
     };
     for (int idx = item_begin; idx < item_end; ++idx) {
