@@ -137,16 +137,14 @@ struct Ctx {
   int* status;
 };
 
-// A wait ran out, here or in the other CTA: flag the status word and make both
-// CTAs unwind.
-__device__ __noinline__ void give_up(const Ctx& c) {
+// A wait ran out, here or in the other CTA: make both CTAs unwind.
+__device__ __forceinline__ void tell_abort(const Ctx& c) {
   *c.abort = 1;
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(c.peer_abort), "r"(1) : "memory");
-  atomicOr(c.status, kStatusTimeout);
 }
 // False after too many polls, or once either CTA has given up; the caller then
-// leaves its role through give_up (kept out of the loops: their code competes
-// for the instruction cache).
+// leaves its role, and the block gives up at its end (kept out of the loops: their
+// code competes for the instruction cache).
 __device__ __forceinline__ bool wait_bar(const Ctx& c, int bar, uint32_t parity) {
   uint64_t* b = &c.bars[bar];
   for (uint32_t i = kWaitLimit; !mbar_try_wait(b, parity); --i)
@@ -416,7 +414,7 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
     }
     goto done_copy;
   fail_copy:
-    give_up(c);
+    tell_abort(c);
   done_copy:
     // no copy issued here may still be landing when the CTA leaves
     for (uint32_t k = 0; k < 2 && k < g; ++k) {
@@ -470,7 +468,7 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
       }
       goto done_qk;
     fail_qk:
-      give_up(c);
+      tell_abort(c);
     done_qk:
       __syncwarp();
       if (elect_one()) mma_commit_pair(&c.bars[DRAIN0]);
@@ -507,7 +505,7 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
       }
       goto done_pv;
     fail_pv:
-      give_up(c);
+      tell_abort(c);
     done_pv:
       __syncwarp();
       if (elect_one()) mma_commit_pair(&c.bars[DRAIN0 + 1]);
@@ -733,7 +731,7 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
     }
     goto done_soft;
   fail_soft:
-    give_up(c);
+    tell_abort(c);
   done_soft:;
   } else {
     // ------------------------------------------------------------ conversion and query load
@@ -813,73 +811,75 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
       return true;
     };
     // The item's query, rows [64 rank, 64 rank + 64) (those past the query's end
-    // are zero).  First the rows' factors and shared-memory chunks, four rows a
-    // warp, a row's 72 16-byte units over its lanes; then, with the factors, the
-    // TMEM chunks, a thread per row and 96 dims (both copies of a row, see
-    // mma_f16_pair_ts).
+    // are zero).
     const long long q_rows = p.total_q * H;
-    auto unit_of = [&](long long qr, int u) -> uint4 {  // unit u of a row, as f16 times 1 or raw bf16
+    auto unit_of = [&](long long qr, int u) -> uint4 {  // unit u (eight dims) of a row, raw
       if (qr >= q_rows) return make_uint4(0, 0, 0, 0);
-      if (p.q_fp8) return e4m3x8_to_f16(__ldg(reinterpret_cast<const uint2*>(p.query) + qr * 72 + u));
+      if (p.q_fp8) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p.query) + qr * 72 + u);
+        return make_uint4(v.x, v.y, 0, 0);
+      }
       return __ldg(reinterpret_cast<const uint4*>(p.query) + qr * 72 + u);
     };
-    auto load_query = [&](const WorkItem& it, int n) -> bool {
-      const long long q0 = (long long)it.q_start * H + (long long)it.g * kRows + kCtaRows * rank;
-      float* scales = qscale + (n & 3) * kCtaRows;
-      constexpr int kFirstUnit = 8 * kTmemChunks;  // of the shared-memory chunks
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        uint4 x[2][3];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const long long qr = q0 + 4 * w + 2 * half + r;
-          x[r][0] = unit_of(qr, lane);
-          x[r][1] = unit_of(qr, 32 + lane);
-          x[r][2] = unit_of(qr, 64 + (lane & 7));
+    auto first_row = [&](const WorkItem& it) {
+      return (long long)it.q_start * H + (long long)it.g * kRows + kCtaRows * rank;
+    };
+    // The rows' factors 2^-k, while the item before is still running: four rows a
+    // warp, a row's 72 units over its lanes.
+    auto query_scales = [&](const WorkItem& it, int n) {
+      const long long q0 = first_row(it) + 4 * w;
+#pragma unroll 2
+      for (int r = 0; r < 4; ++r) {
+        int e = 0;
+        if (!p.q_fp8) {
+          const uint4 a = unit_of(q0 + r, lane), b = unit_of(q0 + r, 32 + lane),
+                      d = unit_of(q0 + r, 64 + (lane & 7));
+          uint32_t mb = __vmaxu2(__vmaxu2(max_bits(a), max_bits(b)), max_bits(d));
+          mb = __reduce_max_sync(0xffffffffu, max(mb & 0xFFFFu, mb >> 16));
+          e = query_exponent(mb);
         }
-        // every QK of the previous item has read its query
-        if (half == 0 && !wait_bar(c, Q_EMPTY, (n & 1) ^ 1)) return false;
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int row = 4 * w + 2 * half + r;
-          int e = 0;
-          if (!p.q_fp8) {
-            uint32_t mb = __vmaxu2(__vmaxu2(max_bits(x[r][0]), max_bits(x[r][1])), max_bits(x[r][2]));
-            mb = __reduce_max_sync(0xffffffffu, max(mb & 0xFFFFu, mb >> 16));
-            e = query_exponent(mb);
-          }
-          const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-          for (int i = 1; i < 3; ++i) {
-            const int unit = i == 1 ? 32 + lane : 64 + lane;
-            const uint4 f = p.q_fp8 ? x[r][i] : bf16x8_to_f16(x[r][i], up);
-            if (unit >= kFirstUnit && unit < 72)
-              put(sm + OFF_Q + ((unit - kFirstUnit) >> 3) * kQChunk + row * 128, unit & 7, row, f);
-          }
-          if (lane == 0) scales[row] = __uint_as_float((uint32_t)(127 - e) << 23);
-        }
+        if (lane == 0)
+          qscale[(n & 3) * kCtaRows + 4 * w + r] = __uint_as_float((uint32_t)(127 - e) << 23);
       }
-      fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&c.bars[QX]);
         mbar_arrive(&c.bars[QS_FULL0 + (n & 3)]);
       }
-      if (!wait_bar(c, QX, n & 1)) return false;
+    };
+    // The values: the TMEM chunks by a thread per row and 96 dims (both copies of a
+    // row, see mma_f16_pair_ts), loaded before every QK of the previous item has
+    // read its query; the shared-memory chunks three units a thread.
+    auto load_query = [&](const WorkItem& it, int n) -> bool {
+      const long long q0 = first_row(it);
+      const float* scales = qscale + (n & 3) * kCtaRows;
+      auto as_f16 = [&](const uint4 x, float up) {
+        return p.q_fp8 ? e4m3x8_to_f16(make_uint2(x.x, x.y)) : bf16x8_to_f16(x, up);
+      };
       const int quad = warp & 3, row = (32 * quad + lane) & 63, part = w >> 2;
+      uint4 x[4], f[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) x[u] = unit_of(q0 + row, 12 * part + u);
+      if (!wait_bar(c, QX, n & 1)) return false;
       const float up = 1.f / scales[row];  // a power of two: exact
+      if (!wait_bar(c, Q_EMPTY, (n & 1) ^ 1)) return false;
       const uint32_t tq = tmem + ((uint32_t)(32 * quad) << 16) + TM_Q + 48 * part;
+      constexpr int kPerRow = 8 * (kChunks - kTmemChunks);  // shared-memory units of a row
+      static_assert(kCtaRows * kPerRow == 3 * 32 * kConvWarps, "three units a thread");
 #pragma unroll 1
       for (int j = 0; j < 3; ++j) {  // 32 dims: four units, sixteen columns
-        uint4 x[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) x[u] = unit_of(q0 + row, 12 * part + 4 * j + u);
-        if (!p.q_fp8) {
+        for (int u = 0; u < 4; ++u) f[u] = as_f16(x[u], up);
+        tmem_st_32x32b_x16(tq + 16 * j, *reinterpret_cast<const uint32_t(*)[16]>(f));
+        const int at = 32 * (kConvWarps * j + w) + lane, r = at / kPerRow, u2 = at - r * kPerRow;
+        const uint4 y = unit_of(q0 + r, 8 * kTmemChunks + u2);
+        if (j < 2) {
 #pragma unroll
-          for (int u = 0; u < 4; ++u) x[u] = bf16x8_to_f16(x[u], up);
+          for (int u = 0; u < 4; ++u) x[u] = unit_of(q0 + row, 12 * part + 4 * (j + 1) + u);
         }
-        tmem_st_32x32b_x16(tq + 16 * j, *reinterpret_cast<const uint32_t(*)[16]>(x));
+        put(sm + OFF_Q + (u2 >> 3) * kQChunk + r * 128, u2 & 7, r, as_f16(y, 1.f / scales[r]));
       }
+      fence_proxy_async_smem();
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -890,22 +890,31 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
       const WorkItem it = items[idx];
       const int nt = n_tiles_of(it);
       if (nt <= 0) continue;
+      if (n_item == 0) query_scales(it, 0);
       // the first tile before the query: its conversion needs nothing of the
-      // previous item but ring places
+      // previous item but free stages
       for (int t = 0; t < nt; ++t, ++g) {
         if ((g & 1) == grp && !convert_tile()) goto fail_conv;
-        if (t == 0 && !load_query(it, n_item)) goto fail_conv;
+        if (t > 0) continue;
+        if (!load_query(it, n_item)) goto fail_conv;
+        for (int nx = idx + 1; nx < item_end; ++nx) {
+          const WorkItem itn = items[nx];
+          if (n_tiles_of(itn) <= 0) continue;
+          query_scales(itn, n_item + 1);
+          break;
+        }
       }
       ++n_item;
     }
     goto done_conv;
   fail_conv:
-    give_up(c);
+    tell_abort(c);
   done_conv:;
   }
 
   tc_fence_before();
   __syncthreads();
+  if (tid == 0 && *c.abort) atomicOr(c.status, kStatusTimeout);
   cluster_sync();  // neither CTA touches the other's memory or TMEM any more
   if (warp == 1) {
     tc_fence_after();
