@@ -778,20 +778,20 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
       unsigned char* ks = sm + OFF_K + grp * kKStage + lane * 128;
 #pragma unroll
       for (int e = 0; e < 8; ++e) put(ks + k * kKChunk, e, lane, x[e]);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) arrive_leader(c, K_FULL0 + 3 * grp + k / kGroup, 4);
       if (in_half) {
         const uint2 rc = *reinterpret_cast<const uint2*>(codes + 256 + 8 * vc);
         uint32_t s0, s1;
         scale_pairs(s2, s0, s1);
-        const uint4 y0 = convert8(rc.x, s0), y1 = convert8(rc.y, s0);
-        put(ks + 8 * kKChunk, 2 * vc, lane, y0);
-        put(ks + 8 * kKChunk, 2 * vc + 1, lane, y1);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) arrive_leader(c, K_FULL0 + 3 * grp + 2, 1);
-      } else {
+        put(ks + 8 * kKChunk, 2 * vc, lane, convert8(rc.x, s0));
+        put(ks + 8 * kKChunk, 2 * vc + 1, lane, convert8(rc.y, s0));
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        arrive_leader(c, K_FULL0 + 3 * grp + k / kGroup, 4);
+        if (in_half) arrive_leader(c, K_FULL0 + 3 * grp + 2, 1);
+      }
+      if (!in_half) {
         const unsigned char* other = stg + STG_OTHER + lane * 128;
         c0 = *reinterpret_cast<const uint4*>(other + (((2 * vc) ^ (lane & 7)) << 4));
         c1 = *reinterpret_cast<const uint4*>(other + (((2 * vc + 1) ^ (lane & 7)) << 4));
