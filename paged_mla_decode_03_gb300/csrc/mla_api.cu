@@ -20,7 +20,8 @@ cudaError_t launch_partition(const Problem& p, const Layout& lay, void* ws, cuda
 cudaError_t partition_setup();
 cudaError_t launch_combine(const Problem& p, const Layout& lay, void* ws, int grid,
                            cudaStream_t stream);
-cudaError_t decode_sm103_setup(int kv_dtype, int sparse, int f8_mma, int sm_count, int* n_pairs);
+cudaError_t decode_sm103_setup(int kv_dtype, int sparse, int f8_mma, int window, int sm_count,
+                               int* n_pairs);
 cudaError_t launch_merge_states(const void* o_parts, const float* lse_parts, int n, long long rows,
                                 float scale, void* out, float* lse_out, cudaStream_t stream);
 cudaError_t launch_qsplit(const Problem& p, const Layout& lay, void* ws, int sm_count,
@@ -59,6 +60,12 @@ bool uses_f8_mma(const mla_decode_params& p) {
 // the FP8 MMA path with a bf16 query: the query is split before the decode
 bool uses_q_split(const mla_decode_params& p) {
   return uses_f8_mma(p) && p.q_dtype == MLA_Q_BF16;
+}
+
+// The sliding window the kernels run with: one that reaches back over every
+// length the plan admits hides nothing.
+int effective_window(const mla_decode_params& p) {
+  return p.window > 0 && p.window < p.max_seq_len ? p.window : 0;
 }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -149,7 +156,6 @@ int mla_decode_plan(const mla_decode_params* params, mla_plan_t** plan, size_t* 
   if (p.window < 0 || p.sinks < 0 || p.sinks > (1 << 30) || (p.window == 0 && p.sinks > 0))
     return MLA_ERR_INVALID_ARG;
   if (p.window > 0 && (p.cp_world > 1 || p.sparse_top_k > 0)) return MLA_ERR_UNSUPPORTED;
-  if (p.window > 0 && p.kv_dtype != MLA_KV_FP4_E2M1) return MLA_ERR_UNSUPPORTED;
   if (p.kv_dtype == MLA_KV_FP4_E2M1 && p.sparse_top_k > 0) return MLA_ERR_UNSUPPORTED;
   if (!supported_heads(p.num_heads)) return MLA_ERR_UNSUPPORTED;
   if (p.page_size != 32 && p.page_size != 64) return MLA_ERR_UNSUPPORTED;
@@ -169,7 +175,8 @@ int mla_decode_plan(const mla_decode_params* params, mla_plan_t** plan, size_t* 
   if (e == cudaSuccess)
     e = p.kv_dtype == MLA_KV_FP4_E2M1
             ? mla::decode_fp4_setup(sms, &n_pairs)
-            : mla::decode_sm103_setup(p.kv_dtype, p.sparse_top_k > 0, uses_f8_mma(p), sms, &n_pairs);
+            : mla::decode_sm103_setup(p.kv_dtype, p.sparse_top_k > 0, uses_f8_mma(p), effective_window(p) > 0, sms,
+                                      &n_pairs);
   if (e == cudaSuccess) e = mla::partition_setup();
   cudaStream_t side = nullptr;
   if (e == cudaSuccess) e = cudaStreamCreateWithFlags(&side, cudaStreamNonBlocking);
@@ -200,7 +207,10 @@ int mla_decode_plan(const mla_decode_params* params, mla_plan_t** plan, size_t* 
     if (p.packed)
       groups = std::min(groups, (long long)p.batch +
                                     ceil_div(p.max_total_q * p.num_heads, rows_per_group));
-    const long long kv_rows = p.sparse_top_k > 0 ? p.sparse_top_k : p.max_seq_len;
+    long long kv_rows = p.sparse_top_k > 0 ? p.sparse_top_k : p.max_seq_len;
+    if (effective_window(p) > 0)  // whole tiles of the sinks, and of the q_len windows
+      kv_rows = std::min(kv_rows, (long long)mla::window_sink_rows(p.sinks) + p.window +
+                                      p.max_seq_len_q + mla::kKvTile);
     const long long units = std::max(groups, 1LL) * (mla::kOverheadTiles + ceil_div(kv_rows, mla::kKvTile));
     n_pairs = (int)std::max(1LL, std::min<long long>(n_pairs, units / mla::kMinUnits));
   }
@@ -329,8 +339,8 @@ int run_impl(const mla_plan_t* plan, const void* query, const void* kv_cache,
   p.qo_indptr = prm.packed ? qo_indptr : nullptr;
   p.out = out;
   p.lse = prm.return_lse ? lse : nullptr;
-  p.window = prm.window;
-  p.sinks = prm.sinks;
+  p.window = effective_window(prm);
+  p.sinks = p.window > 0 ? prm.sinks : 0;
 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // while the stream is being captured into a graph, the events become
