@@ -607,22 +607,27 @@ def _cache_kind(kv_cache: torch.Tensor) -> Tuple[torch.Tensor, int]:
     return kv_cache, kind
 
 
-def _int32(name: str, t: Optional[torch.Tensor], shape, device) -> None:
-    if t is None:
-        return
-    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor on {device}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+# cache_append and cache_gather run every layer of every step, so a call's checks
+# are plain comparisons, and the message is worked out once one has failed.
+
+def _is_int32(t: torch.Tensor, dev: int, shape) -> bool:
+    return (t.dtype is torch.int32 and t.get_device() == dev and t.shape == shape
+            and t.is_contiguous())
 
 
-def _bf16_rows(name: str, t: torch.Tensor, shape, device) -> None:
-    if t.dtype != torch.bfloat16 or t.device != device:
-        raise ValueError(f"{name} must be a bf16 tensor on {device}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.numel() and t.stride(-1) != 1:
-        raise ValueError(f"{name}: the last dim must be contiguous")
+def _is_bf16_rows(t: torch.Tensor, dev: int, shape) -> bool:
+    return (t.dtype is torch.bfloat16 and t.get_device() == dev and t.shape == shape
+            and (t.stride(-1) == 1 or t.numel() == 0))
+
+
+def _refuse(name: str, t, what: str, dev: int, shape) -> None:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    raise ValueError(f"{name} must be {what} of shape {tuple(shape)} on cuda:{dev}, got "
+                     f"{t.dtype} {tuple(t.shape)} (strides {t.stride()}) on {t.device}")
+
+
+_INT32, _BF16_ROWS = "a contiguous int32 tensor", "a bf16 tensor with a contiguous last dim"
 
 
 def _outer(t: torch.Tensor, dim: int) -> int:
@@ -630,42 +635,66 @@ def _outer(t: torch.Tensor, dim: int) -> int:
     return t.stride(dim) if t.shape[dim] > 1 else 0
 
 
-def _stream_of(stream, device: torch.device) -> int:
+def _stream_of(stream, dev: int) -> int:
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return torch.cuda.current_stream(dev).cuda_stream
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
 
 
+try:  # the same handle without the Stream object around it (a microsecond and a half less)
+    from torch._C import _cuda_getCurrentRawStream as _raw_stream
+except ImportError:  # pragma: no cover - a torch without CUDA
+    def _raw_stream(dev: int) -> int:
+        return torch.cuda.current_stream(dev).cuda_stream
+
+
+_cache_params: Dict[tuple, MlaCacheParams] = {}
+
+
+def _params_of(*key) -> MlaCacheParams:
+    """The parameter record of a static key (fields in order), made once."""
+    p = _cache_params.get(key)
+    if p is None:
+        if len(_cache_params) >= 1024:
+            _cache_params.clear()
+        p = _cache_params[key] = MlaCacheParams(*key)
+    return p
+
+
 def _cache_call(kv_cache, block_tables, seq_lens, qo_indptr, q_len, total_q, status):
-    """Checks that ``cache_append`` and ``cache_gather`` share -> parameters."""
-    if not kv_cache.is_cuda or not kv_cache.is_contiguous():
+    """Checks that ``cache_append`` and ``cache_gather`` share -> (device, the
+    parameters' first seven fields)."""
+    dev = kv_cache.get_device()
+    if dev < 0 or not kv_cache.is_contiguous():
         raise ValueError("kv_cache must be a contiguous CUDA tensor")
     kv_cache, kind = _cache_kind(kv_cache)
-    dev = kv_cache.device
-    batch = int(seq_lens.shape[0])
-    _int32("seq_lens", seq_lens, (batch,), dev)
+    pages, page_size, _ = kv_cache.shape
+    batch = seq_lens.shape[0]
+    if not _is_int32(seq_lens, dev, (batch,)):
+        _refuse("seq_lens", seq_lens, _INT32, dev, (batch,))
     if block_tables.dim() != 2:
         raise ValueError("block_tables must be [batch, pages]")
-    _int32("block_tables", block_tables, (batch, block_tables.shape[1]), dev)
-    _int32("qo_indptr", qo_indptr, (batch + 1,), dev)
-    _int32("status", status, (1,), dev)
+    width = block_tables.shape[1]
+    if not _is_int32(block_tables, dev, (batch, width)):
+        _refuse("block_tables", block_tables, _INT32, dev, (batch, width))
     if (qo_indptr is None) == (q_len is None):
         raise ValueError("give qo_indptr (packed) or q_len (the same for every request)")
-    if q_len is not None and (q_len < 1 or total_q != batch * q_len):
+    if q_len is None:
+        if not _is_int32(qo_indptr, dev, (batch + 1,)):
+            _refuse("qo_indptr", qo_indptr, _INT32, dev, (batch + 1,))
+    elif q_len < 1 or total_q != batch * q_len:
         raise ValueError(f"{total_q} tokens are not {batch} requests of {q_len}")
-    p = MlaCacheParams(batch=batch, packed=int(qo_indptr is not None), q_len=q_len or 0,
-                       page_size=int(kv_cache.shape[1]), kv_dtype=kind,
-                       max_pages_per_req=int(block_tables.shape[1]),
-                       num_pages=int(kv_cache.shape[0]))
-    return p, dev
+    if status is not None and not _is_int32(status, dev, (1,)):
+        _refuse("status", status, _INT32, dev, (1,))
+    return dev, (batch, int(q_len is None), q_len or 0, page_size, width, kind, pages)
 
 
-def _on_device(dev: torch.device, call):
-    """``call()`` with ``dev`` current (the kernels launch on the current device)."""
-    if torch.cuda.current_device() == dev.index:
-        return call()
+def _call_on(dev: int, fn, *args) -> int:
+    """``fn(*args)`` with ``dev`` current (the kernels launch on the current device)."""
+    if torch.cuda.current_device() == dev:
+        return fn(*args)
     with torch.cuda.device(dev):
-        return call()
+        return fn(*args)
 
 
 def rope_table(max_position: int, *, base: float = 10000.0, scaling: Optional[str] = None,
@@ -691,8 +720,8 @@ def rope_table(max_position: int, *, base: float = 10000.0, scaling: Optional[st
                       original_max_position=original_max_position, beta_fast=beta_fast,
                       beta_slow=beta_slow)
     table = torch.empty((max(max_position, 0), 64), dtype=torch.float32, device=dev)
-    rc = _on_device(dev, lambda: load_library().mla_rope_table(
-        ctypes.byref(p), _ptr(table) if max_position > 0 else 16, _stream_of(stream, dev)))
+    rc = _call_on(dev.index, load_library().mla_rope_table, ctypes.byref(p),
+                  table.data_ptr() if max_position > 0 else 16, _stream_of(stream, dev.index))
     if rc != MLA_OK:
         raise MlaDecodeError(rc, "mla_rope_table")
     return table
@@ -724,49 +753,58 @@ def cache_append(latent: torch.Tensor, k_pe: torch.Tensor, kv_cache: torch.Tenso
     violations are ORed in (see ``include/mla_decode.h``).  Returns ``query``."""
     if latent.dim() != 2 or not latent.is_cuda:
         raise ValueError("latent must be a CUDA tensor [tokens, 512]")
-    T = int(latent.shape[0])
-    p, dev = _cache_call(kv_cache, block_tables, seq_lens, qo_indptr, q_len, T, status)
-    _bf16_rows("latent", latent, (T, HEAD_DIM_V), dev)
-    _bf16_rows("k_pe", k_pe, (T, 64), dev)
-    if norm_weight is not None:
-        _bf16_rows("norm_weight", norm_weight, (HEAD_DIM_V,), dev)
-    if rope_table.dtype != torch.float32 or rope_table.device != dev or rope_table.dim() != 2 \
-            or rope_table.shape[1] != 64 or not rope_table.is_contiguous():
-        raise ValueError(f"rope_table must be a contiguous fp32 tensor [positions, 64] on {dev}")
-    if rope_style not in ROPE_STYLES:
+    T = latent.shape[0]
+    dev, key = _cache_call(kv_cache, block_tables, seq_lens, qo_indptr, q_len, T, status)
+    if not _is_bf16_rows(latent, dev, (T, 512)):
+        _refuse("latent", latent, _BF16_ROWS, dev, (T, 512))
+    if not _is_bf16_rows(k_pe, dev, (T, 64)):
+        _refuse("k_pe", k_pe, _BF16_ROWS, dev, (T, 64))
+    if norm_weight is not None and not _is_bf16_rows(norm_weight, dev, (512,)):
+        _refuse("norm_weight", norm_weight, _BF16_ROWS, dev, (512,))
+    if not (rope_table.dtype is torch.float32 and rope_table.get_device() == dev
+            and rope_table.dim() == 2 and rope_table.shape[1] == 64 and rope_table.is_contiguous()):
+        _refuse("rope_table", rope_table, "a contiguous fp32 tensor", dev, ("positions", 64))
+    style = ROPE_STYLES.get(rope_style)
+    if style is None:
         raise ValueError(f"rope_style must be one of {list(ROPE_STYLES)}, got {rope_style!r}")
-    _int32("positions", positions, (T,), dev)
-    qn = qp = (0, 0)
+    if positions is not None and not _is_int32(positions, dev, (T,)):
+        _refuse("positions", positions, _INT32, dev, (T,))
+    H = q_dtype = 0
+    n_ptr = p_ptr = q_ptr = None
+    n_token = n_head = p_token = p_head = 0
     if q_pe is not None:
         if q_pe.dim() != 3:
             raise ValueError("q_pe must be [tokens, heads, 64]")
-        H = int(q_pe.shape[1])
-        _bf16_rows("q_pe", q_pe, (T, H, 64), dev)
-        qp = (_outer(q_pe, 0), _outer(q_pe, 1))
+        H = q_pe.shape[1]
+        if not _is_bf16_rows(q_pe, dev, (T, H, 64)):
+            _refuse("q_pe", q_pe, _BF16_ROWS, dev, (T, H, 64))
         if query is None:
             if q_nope is None:
                 raise ValueError("without q_nope, query must be given (its latent part stays)")
-            query = torch.empty((T, H, HEAD_DIM_QK), dtype=torch.bfloat16, device=dev)
-        if query.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or query.device != dev \
-                or not query.is_contiguous():
-            raise ValueError(f"query must be a contiguous bf16 or float8_e4m3fn tensor on {dev}")
-        if tuple(query.shape) != (T, H, HEAD_DIM_QK) and (
-                q_len is None or tuple(query.shape) != (T // q_len, q_len, H, HEAD_DIM_QK)):
-            raise ValueError(f"query must be [{T}, {H}, 576], got {tuple(query.shape)}")
-        p.num_heads = H
-        p.q_dtype = Q_BF16 if query.dtype == torch.bfloat16 else Q_FP8_E4M3
+            query = torch.empty((T, H, HEAD_DIM_QK), dtype=torch.bfloat16, device=latent.device)
+        if query.dtype is torch.float8_e4m3fn:
+            q_dtype = Q_FP8_E4M3
+        elif query.dtype is not torch.bfloat16:
+            _refuse("query", query, "a contiguous bf16 or float8_e4m3fn tensor", dev, (T, H, 576))
+        if query.get_device() != dev or not query.is_contiguous() or not (
+                query.shape == (T, H, 576)
+                or (q_len is not None and query.shape == (key[0], q_len, H, 576))):
+            _refuse("query", query, "a contiguous bf16 or float8_e4m3fn tensor", dev, (T, H, 576))
+        p_ptr, p_token, p_head = q_pe.data_ptr(), _outer(q_pe, 0), _outer(q_pe, 1)
+        q_ptr = query.data_ptr()
         if q_nope is not None:
-            _bf16_rows("q_nope", q_nope, (T, H, HEAD_DIM_V), dev)
-            qn = (_outer(q_nope, 0), _outer(q_nope, 1))
+            if not _is_bf16_rows(q_nope, dev, (T, H, 512)):
+                _refuse("q_nope", q_nope, _BF16_ROWS, dev, (T, H, 512))
+            n_ptr, n_token, n_head = q_nope.data_ptr(), _outer(q_nope, 0), _outer(q_nope, 1)
     elif query is not None or q_nope is not None:
         raise ValueError("query and q_nope go with q_pe")
-    lib = load_library()
-    rc = _on_device(dev, lambda: lib.mla_cache_append(
-        ctypes.byref(p), _ptr(latent), _outer(latent, 0), _ptr(k_pe), _outer(k_pe, 0),
-        _ptr(norm_weight), eps, _ptr(rope_table), int(rope_table.shape[0]),
-        ROPE_STYLES[rope_style], _ptr(positions), _ptr(block_tables), _ptr(seq_lens),
-        _ptr(qo_indptr), T, kv_scale, _ptr(kv_cache), _ptr(q_nope), qn[0], qn[1], _ptr(q_pe),
-        qp[0], qp[1], q_scale, _ptr(query), _ptr(status), _stream_of(stream, dev)))
+    rc = _call_on(
+        dev, load_library().mla_cache_append, _params_of(*key, H, q_dtype), latent.data_ptr(),
+        _outer(latent, 0), k_pe.data_ptr(), _outer(k_pe, 0), _ptr(norm_weight), eps,
+        rope_table.data_ptr(), rope_table.shape[0], style, _ptr(positions),
+        block_tables.data_ptr(), seq_lens.data_ptr(), _ptr(qo_indptr), T, kv_scale,
+        kv_cache.data_ptr(), n_ptr, n_token, n_head, p_ptr, p_token, p_head, q_scale, q_ptr,
+        _ptr(status), _raw_stream(dev) if stream is None else _stream_of(stream, dev))
     if rc != MLA_OK:
         raise MlaDecodeError(rc, "mla_cache_append")
     return query
@@ -790,16 +828,15 @@ def cache_gather(kv_cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: t
             total_q = int(seq_lens.shape[0]) * q_len
         else:
             raise ValueError("total_q is needed for packed rows")
-    p, dev = _cache_call(kv_cache, block_tables, seq_lens, qo_indptr, q_len, total_q, status)
+    dev, key = _cache_call(kv_cache, block_tables, seq_lens, qo_indptr, q_len, total_q, status)
     if out is None:
-        out = torch.empty((total_q, HEAD_DIM_QK), dtype=torch.bfloat16, device=dev)
-    _bf16_rows("out", out, (total_q, HEAD_DIM_QK), dev)
-    if not out.is_contiguous():
-        raise ValueError("out must be contiguous")
-    lib = load_library()
-    rc = _on_device(dev, lambda: lib.mla_cache_gather(
-        ctypes.byref(p), _ptr(kv_cache), _ptr(block_tables), _ptr(seq_lens), _ptr(qo_indptr),
-        total_q, kv_scale, _ptr(out), _ptr(status), _stream_of(stream, dev)))
+        out = torch.empty((total_q, HEAD_DIM_QK), dtype=torch.bfloat16, device=kv_cache.device)
+    elif not _is_bf16_rows(out, dev, (total_q, HEAD_DIM_QK)) or not out.is_contiguous():
+        _refuse("out", out, "a contiguous bf16 tensor", dev, (total_q, HEAD_DIM_QK))
+    rc = _call_on(dev, load_library().mla_cache_gather, _params_of(*key, 0, 0),
+                  kv_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
+                  _ptr(qo_indptr), total_q, kv_scale, out.data_ptr(), _ptr(status),
+                  _raw_stream(dev) if stream is None else _stream_of(stream, dev))
     if rc != MLA_OK:
         raise MlaDecodeError(rc, "mla_cache_gather")
     return out

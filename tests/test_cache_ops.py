@@ -443,3 +443,34 @@ def test_append_in_a_graph_and_on_a_side_stream():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, first) and torch.equal(query, q_first)
+
+
+@pytest.mark.gpu
+def test_binding_refuses_what_the_kernel_cannot_take():
+    s = Setup("bf16", 64, [50, 9], [2, 2], 16, packed=False, seed=11)
+    cache = new_cache("bf16", s.pages, 64)
+    ok = dict(latent=s.latent, k_pe=s.k_pe, kv_cache=cache, block_tables=s.tables, seq_lens=s.lens, rope_table=s.table,
+              norm_weight=s.weight, q_len=2, q_nope=s.q_nope, q_pe=s.q_pe)
+    query = mla.cache_append(**ok)
+    assert query.shape == (4, 16, 576)
+    bad = [dict(latent=s.latent.float()), dict(latent=s.latent[:3]), dict(k_pe=s.k_pe[:, ::2]), dict(k_pe=s.k_pe.cpu()),
+           dict(norm_weight=s.weight[:256]), dict(rope_table=s.table.double()), dict(rope_table=s.table[:, :32]),
+           dict(seq_lens=s.lens.long()), dict(block_tables=s.tables[:, ::2]), dict(block_tables=s.tables[0]),
+           dict(q_len=None), dict(q_len=3), dict(qo_indptr=s.indptr), dict(rope_style="both"), dict(q_pe=s.q_pe[:, :8]),
+           dict(q_nope=s.q_nope[..., :256]), dict(query=query[:2]), dict(query=query.half()), dict(q_pe=None),
+           dict(positions=torch.zeros(3, dtype=torch.int32, device="cuda")), dict(kv_cache=cache[:, :, :512]),
+           dict(kv_cache=cache.half()), dict(status=torch.zeros(2, dtype=torch.int32, device="cuda")),
+           dict(q_nope=None)]
+    for kw in bad:
+        with pytest.raises((ValueError, mla.MlaDecodeError)):
+            mla.cache_append(**{**ok, **kw})
+    for kw in (dict(kv_scale=0.0), dict(kv_scale=2.0), dict(q_scale=3.0), dict(eps=0.0)):
+        with pytest.raises(mla.MlaDecodeError):
+            mla.cache_append(**{**ok, **kw})
+    for kw in (dict(out=torch.zeros(4, 576, device="cuda")), dict(q_len=None), dict(total_q=5)):
+        with pytest.raises(ValueError):
+            mla.cache_gather(**{**dict(kv_cache=cache, block_tables=s.tables, seq_lens=s.lens, q_len=2), **kw})
+    none = torch.zeros(0, dtype=torch.int32, device="cuda")
+    assert mla.cache_gather(cache, s.tables[:0], none, q_len=1).shape == (0, 576)
+    e = torch.zeros(0, 576, dtype=torch.bfloat16, device="cuda")
+    assert mla.cache_append(e[:, :512], e[:, 512:], cache, s.tables[:0], none, rope_table=s.table, q_len=1) is None
