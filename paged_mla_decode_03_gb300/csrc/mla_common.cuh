@@ -143,6 +143,23 @@ __host__ __device__ inline size_t align_up(size_t x, size_t a) { return (x + a -
 // measured ~3.2), and every busy worker gets at least kMinUnits units.
 constexpr long long kOverheadTiles = 3;
 constexpr long long kMinUnits = 4;
+// The 4-bit kernel's tiles are shorter and its item overhead the same time:
+// measured 1.3 us a tile and about 6 us an item.
+constexpr long long kOverheadTilesFp4 = 5;
+
+// Whether every row group goes to a worker of its own, uncut: the largest group
+// costs little more than an even share of the work, and cutting would add an
+// item's overhead to every worker, the partials' round trip and the combine's
+// tail (some 6 us), together about kCutTiles tiles.  For 64 groups of 18 tiles on
+// 76 workers: 18 + 3 units uncut against 17.7 + 3 + 6.  Asked for sliding windows
+// (whose groups are nearly equal) and the 4-bit cache; the other plans keep the
+// partition they have always had.
+constexpr long long kCutTiles = 6;
+__host__ __device__ inline bool partition_uncut(bool asked, long long n_groups, long long n_workers,
+                                                long long max_cost, long long total_cost) {
+  return asked && n_groups > 0 && n_groups <= n_workers &&
+         max_cost <= total_cost / n_workers + kCutTiles;
+}
 
 // The query split of the FP8 MMA path with a bf16 query (mla_qsplit.cu), one
 // record of kQSplitUnits 16-byte units per (query row, CTA half): latent hi

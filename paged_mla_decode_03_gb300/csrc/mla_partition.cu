@@ -120,6 +120,7 @@ __device__ T block_exclusive_scan(T* data, int n, Shared& sh) {
 struct Bounds {
   long long W, n, lanes, nl, WL;
   const long long* table;  // boundary(p) for p in [0, n], or nullptr
+  long long overhead;      // units of a group besides its tiles
   // start unit of worker p's range (the arithmetic behind the table)
   __device__ long long boundary_of(long long p) const {
     if (p >= lanes * nl) return W;
@@ -150,7 +151,7 @@ struct Bounds {
 
 // Tile cut position of range boundary p inside a group starting at unit S.
 __device__ __forceinline__ int cut_tile(const Bounds& bd, long long p, long long S, int T) {
-  const long long t = bd.boundary(p) - S - kOverheadTiles;
+  const long long t = bd.boundary(p) - S - bd.overhead;
   return (int)min(max(t, 0LL), (long long)T);
 }
 
@@ -170,6 +171,8 @@ partition_kernel(Problem p, Layout lay, char* __restrict__ ws) {
   const int R = lay.rows_per_group;
   const int H = p.num_heads;
   const bool sparse = p.sparse_k > 0;
+  const bool fp4 = p.kv_dtype == 2;
+  const long long c0 = fp4 ? kOverheadTilesFp4 : kOverheadTiles;
   // KV rows a group of a request (length L, q tokens) walks: its cache rows, those
   // its sliding window reaches, or the token's list
   auto kv_rows = [&](int L, int q) {
@@ -275,7 +278,7 @@ partition_kernel(Problem p, Layout lay, char* __restrict__ ws) {
   for (int b = threadIdx.x; b < B && n_groups > 0; b += blockDim.x) {
     const int gb = r_gbase[b];  // scanned: first group of request b
     const int ge = (b + 1 < B) ? r_gbase[b + 1] : n_groups;
-    W_total += (long long)(ge - gb) * (kOverheadTiles + (kv_rows(r_len[b], r_qlen[b]) + kKvTile - 1) / kKvTile);
+    W_total += (long long)(ge - gb) * (c0 + (kv_rows(r_len[b], r_qlen[b]) + kKvTile - 1) / kKvTile);
   }
   __syncthreads();
   if (threadIdx.x == 0) sh.carry_ll = 0;
@@ -299,7 +302,7 @@ partition_kernel(Problem p, Layout lay, char* __restrict__ ws) {
       const int slot = lanes > 1 ? k * n_req_groups + gb / G : g;
       g_req[slot] = b;
       g_k[slot] = k;
-      g_start[slot] = kOverheadTiles + T;  // cost; scanned into the start unit below
+      g_start[slot] = c0 + T;  // cost; scanned into the start unit below
     }
   }
   __syncthreads();
@@ -311,8 +314,20 @@ partition_kernel(Problem p, Layout lay, char* __restrict__ ws) {
   bd.nl = n_eff / lanes;  // busy workers per lane; the rest get empty ranges
   bd.WL = W / lanes;      // every lane has the same cost
   bd.table = nullptr;
+  bd.overhead = c0;
+  const bool ask = p.window > 0 || fp4;
+  long long max_cost = 0;
+  if (ask) {  // (uniform over the block)
+    int t_max = 0;
+    for (int b = threadIdx.x; b < B; b += blockDim.x)
+      if (r_len[b] > 0) t_max = max(t_max, (kv_rows(r_len[b], r_qlen[b]) + kKvTile - 1) / kKvTile);
+    max_cost = c0 + block_max(t_max, sh);
+  }
   if (n <= kBoundTable) {
-    for (long long q = threadIdx.x; q <= n; q += blockDim.x) sh.bound[q] = bd.boundary_of(q);
+    // uncut: worker q's range starts where group q does
+    const bool uncut = partition_uncut(ask, n_groups, n, max_cost, W);
+    for (long long q = threadIdx.x; q <= n; q += blockDim.x)
+      sh.bound[q] = !uncut ? bd.boundary_of(q) : q < n_groups ? g_start[q] : W;
     __syncthreads();
     bd.table = sh.bound;
   }
@@ -321,7 +336,7 @@ partition_kernel(Problem p, Layout lay, char* __restrict__ ws) {
   for (int g = threadIdx.x; g < n_groups; g += blockDim.x) {
     const int b = g_req[g];
     const int T = (kv_rows(r_len[b], r_qlen[b]) + kKvTile - 1) / kKvTile;
-    const long long S = g_start[g], c = kOverheadTiles + T;
+    const long long S = g_start[g], c = c0 + T;
     int nch = 1;
     if (W > 0) {
       const long long p_lo = bd.first_above(S);           // boundaries after the group start
@@ -356,12 +371,12 @@ partition_kernel(Problem p, Layout lay, char* __restrict__ ws) {
       const int L = r_len[b];
       const int KV = kv_rows(L, r_qlen[b]);
       const int T = (KV + kKvTile - 1) / kKvTile;
-      const long long S = g_start[g], c = kOverheadTiles + T;
+      const long long S = g_start[g], c = c0 + T;
       const int nch = g_nch[g];
       const int g_local = g_k[g];
       int k = 0, prev = 0;
       // an item belongs to the worker whose range holds its first KV tile
-      long long start_unit = S + kOverheadTiles;
+      long long start_unit = S + c0;
       auto emit = [&](int t0, int t1, long long unit) {
         WorkItem it;
         it.b = b;
@@ -385,7 +400,7 @@ partition_kernel(Problem p, Layout lay, char* __restrict__ ws) {
           const int t = cut_tile(bd, q, S, T);
           if (t > prev && t < T) {
             emit(prev, t, start_unit);
-            start_unit = S + kOverheadTiles + t;
+            start_unit = S + c0 + t;
             prev = t;
           }
         }
@@ -555,6 +570,8 @@ partition_warp_kernel(Problem p, Layout lay, char* __restrict__ ws) {
   const int R = lay.rows_per_group;
   const int H = p.num_heads;
   const bool sparse = p.sparse_k > 0;
+  const bool fp4 = p.kv_dtype == 2;
+  const long long c0 = fp4 ? kOverheadTilesFp4 : kOverheadTiles;
   auto kv_rows = [&](int L, int q) {
     return sparse ? p.sparse_k : L - window_skip(p.window, p.sinks, p.causal, L, q);
   };
@@ -562,7 +579,7 @@ partition_warp_kernel(Problem p, Layout lay, char* __restrict__ ws) {
 
   // 1. Per-request lengths (clamped and flagged as in the block kernel) and
   //    the request's number of row groups, over the lane's run of requests.
-  int status = 0, g_min = 1 << 30, g_max = 0, my_groups = 0;
+  int status = 0, g_min = 1 << 30, g_max = 0, my_groups = 0, t_max = 0;
   long long my_cost = 0;
   const Run rb(B, lane);
   for (int b = rb.lo; b < rb.hi; ++b) {
@@ -592,9 +609,10 @@ partition_warp_kernel(Problem p, Layout lay, char* __restrict__ ws) {
     if (gc > 0) {
       g_min = min(g_min, gc);
       g_max = max(g_max, gc);
+      t_max = max(t_max, tiles_of(L, q));
     }
     my_groups += gc;
-    my_cost += (long long)gc * (kOverheadTiles + tiles_of(L, q));
+    my_cost += (long long)gc * (c0 + tiles_of(L, q));
   }
   status = warp_or(status);
   g_min = warp_min(g_min);
@@ -632,7 +650,7 @@ partition_warp_kernel(Problem p, Layout lay, char* __restrict__ ws) {
       if (slot < 0 || slot >= n_groups) continue;  // unreachable: slots are a permutation
       sh.g_req[slot] = b;
       sh.g_k[slot] = k;
-      sh.g_start[slot] = kOverheadTiles + T;
+      sh.g_start[slot] = c0 + T;
     }
   }
   __syncwarp();
@@ -655,7 +673,13 @@ partition_warp_kernel(Problem p, Layout lay, char* __restrict__ ws) {
   bd.nl = n_eff / lanes;
   bd.WL = W / lanes;
   bd.table = nullptr;
-  for (long long q = lane; q <= n; q += 32) sh.bound[q] = bd.boundary_of(q);
+  bd.overhead = c0;
+  {
+    // uncut: worker q's range starts where group q does
+    const bool uncut = partition_uncut(p.window > 0 || fp4, n_groups, n, c0 + warp_max(t_max), W);
+    for (long long q = lane; q <= n; q += 32)
+      sh.bound[q] = !uncut ? bd.boundary_of(q) : q < n_groups ? sh.g_start[q] : W;
+  }
   __syncwarp();
   bd.table = sh.bound;
 
@@ -664,7 +688,7 @@ partition_warp_kernel(Problem p, Layout lay, char* __restrict__ ws) {
   int s_items = 0, s_slot = 0, s_comb = 0;
   for (int g = rg.lo; g < rg.hi; ++g) {
     const int T = tiles_of(sh.len[sh.g_req[g]], sh.q[sh.g_req[g]]);
-    const long long S = sh.g_start[g], c = kOverheadTiles + T;
+    const long long S = sh.g_start[g], c = c0 + T;
     int nch = 1;
     if (W > 0) {
       const long long p_lo = bd.first_above(S);
@@ -711,10 +735,10 @@ partition_warp_kernel(Problem p, Layout lay, char* __restrict__ ws) {
       const int L = sh.len[b];
       const int KV = kv_rows(L, sh.q[b]);
       const int T = tiles_of(L, sh.q[b]);
-      const long long S = sh.g_start[g], c = kOverheadTiles + T;
+      const long long S = sh.g_start[g], c = c0 + T;
       const int nch = sh.g_nch[g];
       int k = 0, prev = 0;
-      long long start_unit = S + kOverheadTiles;
+      long long start_unit = S + c0;
       auto emit = [&](int t0, int t1, long long unit) {
         const int idx = sh.g_item[g] + k;
         ++k;
@@ -740,7 +764,7 @@ partition_warp_kernel(Problem p, Layout lay, char* __restrict__ ws) {
           const int t = cut_tile(bd, q, S, T);
           if (t > prev && t < T) {
             emit(prev, t, start_unit);
-            start_unit = S + kOverheadTiles + t;
+            start_unit = S + c0 + t;
             prev = t;
           }
         }
