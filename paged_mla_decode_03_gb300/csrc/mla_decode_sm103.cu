@@ -926,12 +926,16 @@ decode_sm103_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
           sparse ? it.kv_begin
                  : min(kWindow ? INT_MAX : it.kv_end,
                        p.causal ? causal_last(it.mask_base, first_qi, W) + 1 : it.seq_len);
-      // sliding window: the row's own first row, and that of the item's last row
-      const WindowWalk walk(p, it);
-      const int low = last - p.window + 1;
-      const int clean_low =
-          (p.causal ? causal_last(it.mask_base, (row0 + min(R, rows_total - row0) - 1) / H, W)
-                    : it.seq_len - 1) - p.window + 1;
+      // sliding window: virtual rows past the sinks' tiles are `skip` rows further
+      // on; from clean_low on a row is inside every query row's window (the rest
+      // is worked out where a tile needs it: registers are short here)
+      const int skip =
+          kWindow ? window_skip(p.window, p.sinks, p.causal, it.seq_len, it.q_len) : 0;
+      int clean_low = INT_MIN;
+      if constexpr (kWindow)
+        clean_low =
+            (p.causal ? it.mask_base + (row0 + min(R, rows_total - row0) - 1) / H : it.seq_len - 1) -
+            p.window + 1;
       const uint32_t g_last = g + (uint32_t)nt - 1;
       // (l, m) hand-off slot of this item and the phase of its barrier: only
       // items of two or more tiles (both groups take part) count
@@ -991,7 +995,8 @@ decode_sm103_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
         if (lane == 0) mbar_arrive_cluster_relaxed(xfree_peer0 + 8u * sb);
         // mask, then the row maximum of the tile (log2 units)
         const int j0 = it.kv_begin + t * kTile;
-        const int jr = kWindow ? walk.row(j0) : j0;  // with a window j0 is a virtual row
+        // with a window j0 is a virtual row
+        const int jr = kWindow && j0 >= window_sink_rows(p.sinks) ? j0 + skip : j0;
         const int c0 = jr + 32 * hh;  // KV index of sv[0]
         // tiles with masked columns are scaled before the -inf mask goes in,
         // so that bmm1 = 0 never multiplies -inf (the same for the whole tile)
@@ -1018,7 +1023,8 @@ decode_sm103_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
               const int col = c0 + j;
-              const bool in_range = kWindow ? (col - jr + j0 < it.kv_end && (col >= low || col < p.sinks))
+              const bool in_range = kWindow ? (col - jr + j0 < it.kv_end &&
+                                               (col > last - p.window || col < p.sinks))
                                             : col < it.kv_end;
               sv[j] = (col <= last && in_range && ((usable >> j) & 1u)) ? sv[j] * scale : -INFINITY;
               tm[j & 3] = fmaxf(tm[j & 3], sv[j]);
@@ -1066,14 +1072,16 @@ decode_sm103_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
         // zero V rows past the end of the KV range (last tile of the item); with a
         // window also those that no query row sees
         const int valid = it.kv_end - j0;
-        if (kWindow && !(walk.seen(jr, jr) && walk.seen(jr + kTile - 1, jr + kTile - 1) &&
-                         (jr >= walk.low || jr + kTile <= p.sinks))) {
+        if (kWindow && pre_scaled) {
+          const int low = (p.causal ? it.mask_base : it.seq_len - 1) - p.window + 1;
           unsigned char* stage = sm + OFF_KV + (g % kStages) * C::kStage;
           constexpr int kChunks = kF8 ? 2 : kLatChunks;
           constexpr uint32_t kChunkBytes = kF8 ? kChunk8 : kChunkKV;
-          for (int e = g_tid; e < kTile * kChunks * 8; e += kGroupWarps * 32) {
+          // rows [sinks, low) of the tile
+          const int z0 = max(p.sinks - jr, 0), z1 = min(low - jr, kTile);
+#pragma unroll 1
+          for (int e = z0 * kChunks * 8 + g_tid; e < z1 * kChunks * 8; e += kGroupWarps * 32) {
             const int row = e / (8 * kChunks), ch = (e / 8) % kChunks, u = e % 8;
-            if (walk.seen(jr + row, jr + row)) continue;
             *reinterpret_cast<uint4*>(stage + ch * kChunkBytes + row * 128 + u * 16) =
                 make_uint4(0, 0, 0, 0);
           }
