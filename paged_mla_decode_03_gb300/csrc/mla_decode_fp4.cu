@@ -207,8 +207,13 @@ __device__ __forceinline__ void convert64(const uint4 a, const uint4 b, uint32_t
     x[4 * e + 3] = convert8(w[4 * e + 3], s1);
   }
 }
-__device__ __forceinline__ void put(unsigned char* row, int unit, int r, uint4 v) {
-  *reinterpret_cast<uint4*>(row + ((unit ^ (r & 7)) << 4)) = v;
+// Unit `unit` (16 bytes) of a 128-byte row r in the 128B-swizzled layout: at
+// unit ^ (r mod 8).  `row` is swizzled_row's address, so a store takes one XOR.
+__device__ __forceinline__ uint32_t swizzled_row(uint32_t tile, int r) {
+  return tile + 128 * r + ((r & 7) << 4);
+}
+__device__ __forceinline__ void put(uint32_t row, int unit, uint4 v) {
+  st_shared_v4(row ^ (unit << 4), v);
 }
 
 // The power of two that brings a query row's largest magnitude (bf16 bits, sign
@@ -529,7 +534,7 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
     float* mref = reinterpret_cast<float*>(sm + OFF_MREF);
     float* xsum = reinterpret_cast<float*>(sm + OFF_XSUM);
     const float* qscale = reinterpret_cast<const float*>(sm + OFF_QSCALE);
-    unsigned char* prow = sm + OFF_P + kPTile * grp + row * 128;
+    const uint32_t prow = swizzled_row(smem_u32(sm) + OFF_P + kPTile * grp, row);
     uint4* part_o = reinterpret_cast<uint4*>(ws + lay.part_o);
     float* part_lse = reinterpret_cast<float*>(ws + lay.part_lse);
     int* comb_done = reinterpret_cast<int*>(ws + lay.comb_done);
@@ -643,7 +648,7 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
         if (!wait_bar(c, PV_DONE0 + grp, ((g >> 1) & 1) ^ 1)) goto fail_soft;
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-          put(prow, 4 * hh + u, row, make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]));
+          put(prow, 4 * hh + u, make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]));
         if (__any_sync(0xffffffffu, need)) {
           // O, stable once PV of the previous tile is done, to the new reference
           if (!wait_bar(c, PV_DONE0 + (grp ^ 1), ((g - 1) >> 1) & 1)) goto fail_soft;
@@ -747,6 +752,11 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
     float* qscale = reinterpret_cast<float*>(sm + OFF_QSCALE);
     uint32_t g = 0;
     int n_item = 0;
+    // this lane's rows in the group's stages
+    const uint32_t k_row = swizzled_row(smem_u32(sm) + OFF_K + grp * kKStage + k * kKChunk, lane);
+    const uint32_t r_row = swizzled_row(smem_u32(sm) + OFF_K + grp * kKStage + 8 * kKChunk, lane);
+    const uint32_t v_row = swizzled_row(smem_u32(sm) + OFF_V + grp * kVStage + vc * kVChunk,
+                                        kHalf * (in_half ? rank : rank ^ 1) + lane);
     auto convert_tile = [&]() -> bool {
       const uint32_t s = grp;
       if (!wait_bar(c, STG_FULL0 + s, (g >> 1) & 1)) return false;
@@ -775,15 +785,14 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
       convert64(c0, c1, sc, x);
       // QK of the group's previous tile has read this K stage
       if (!wait_bar(c, S_FULL0 + grp, ((g >> 1) & 1) ^ 1)) return false;
-      unsigned char* ks = sm + OFF_K + grp * kKStage + lane * 128;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) put(ks + k * kKChunk, e, lane, x[e]);
+      for (int e = 0; e < 8; ++e) put(k_row, e, x[e]);
       if (in_half) {
         const uint2 rc = *reinterpret_cast<const uint2*>(codes + 256 + 8 * vc);
         uint32_t s0, s1;
         scale_pairs(s2, s0, s1);
-        put(ks + 8 * kKChunk, 2 * vc, lane, convert8(rc.x, s0));
-        put(ks + 8 * kKChunk, 2 * vc + 1, lane, convert8(rc.y, s0));
+        put(r_row, 2 * vc, convert8(rc.x, s0));
+        put(r_row, 2 * vc + 1, convert8(rc.y, s0));
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -800,11 +809,8 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
       }
       if (lane == 0) mbar_arrive(&c.bars[STG_EMPTY0 + s]);  // every code is in registers
       if (!wait_bar(c, PV_DONE0 + grp, ((g >> 1) & 1) ^ 1)) return false;
-      {
-        unsigned char* vd = sm + OFF_V + grp * kVStage + vc * kVChunk + (in_half ? own : oth) * 128;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) put(vd, e, lane, x[e]);
-      }
+      for (int e = 0; e < 8; ++e) put(v_row, e, x[e]);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) arrive_leader(c, V_FULL0 + grp, 1);
@@ -877,7 +883,7 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
 #pragma unroll
           for (int u = 0; u < 4; ++u) x[u] = unit_of(q0 + row, 12 * part + 4 * (j + 1) + u);
         }
-        put(sm + OFF_Q + (u2 >> 3) * kQChunk + r * 128, u2 & 7, r, as_f16(y, 1.f / scales[r]));
+        put(swizzled_row(smem_u32(sm) + OFF_Q + (u2 >> 3) * kQChunk, r), u2 & 7, as_f16(y, 1.f / scales[r]));
       }
       fence_proxy_async_smem();
       tmem_wait_st();
