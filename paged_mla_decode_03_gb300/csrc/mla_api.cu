@@ -28,8 +28,8 @@ cudaError_t launch_qsplit(const Problem& p, const Layout& lay, void* ws, int sm_
                           cudaStream_t stream);
 cudaError_t launch_decode_sm103(const Problem& p, const Layout& lay, void* ws,
                                 cudaStream_t stream);
-cudaError_t decode_fp4_setup(int sm_count, int* n_pairs);
-cudaError_t launch_decode_fp4(const Problem& p, const Layout& lay, void* ws, cudaStream_t stream);
+cudaError_t decode_pair_setup(int kv_dtype, int sm_count, int* n_pairs);
+cudaError_t launch_decode_pair(const Problem& p, const Layout& lay, void* ws, cudaStream_t stream);
 }  // namespace mla
 
 struct mla_plan_s {
@@ -51,21 +51,30 @@ constexpr size_t kHeaderBytes = sizeof(int) * mla::kHdrWords;
 
 bool supported_heads(int h) { return h == 16 || h == 32 || h == 64 || h == 128; }
 
-// An e4m3 cache runs on the FP8 MMAs unless widening was asked for (sparse
-// top-k always widens).
+// The sliding window the kernels run with: one that reaches back over every
+// length the plan admits hides nothing.
+int effective_window(const mla_decode_params& p) {
+  return p.window > 0 && p.window < p.max_seq_len ? p.window : 0;
+}
+
+// The f16 MMAs across CTA pairs (mla_decode_pair.cu): a 4-bit cache, and an e4m3
+// one with a window (32 x 4 x 128 heads, window 4096: 303 us a call on the FP8
+// MMAs, whose tiles exchange scores between the CTAs).
+bool uses_pair_mma(const mla_decode_params& p) {
+  return p.kv_dtype == MLA_KV_FP4_E2M1 ||
+         (p.kv_dtype == MLA_KV_FP8_E4M3 && effective_window(p) > 0);
+}
+
+// Otherwise an e4m3 cache runs on the FP8 MMAs unless widening was asked for
+// (sparse top-k always widens).
 bool uses_f8_mma(const mla_decode_params& p) {
-  return p.kv_dtype == MLA_KV_FP8_E4M3 && p.sparse_top_k == 0 && p.e4m3_widen == 0;
+  return p.kv_dtype == MLA_KV_FP8_E4M3 && p.sparse_top_k == 0 && p.e4m3_widen == 0 &&
+         !uses_pair_mma(p);
 }
 
 // the FP8 MMA path with a bf16 query: the query is split before the decode
 bool uses_q_split(const mla_decode_params& p) {
   return uses_f8_mma(p) && p.q_dtype == MLA_Q_BF16;
-}
-
-// The sliding window the kernels run with: one that reaches back over every
-// length the plan admits hides nothing.
-int effective_window(const mla_decode_params& p) {
-  return p.window > 0 && p.window < p.max_seq_len ? p.window : 0;
 }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -121,8 +130,9 @@ int make_layout(const mla_decode_params& prm, int n_workers, int n_ctas, int row
   off = align_up(off + sizeof(int) * (size_t)std::max(lay->max_combine, 1), 256);
   // the FP8 MMA path (e4m3 cache, dense, not widened) with a bf16 query: the
   // query's e4m3 parts, split once per call before the decode (q_split_offset)
+  // (the condition of uses_q_split, spelled out)
   if (prm.kv_dtype == MLA_KV_FP8_E4M3 && prm.sparse_top_k == 0 && prm.e4m3_widen == 0 &&
-      prm.q_dtype == MLA_Q_BF16) {
+      (prm.window <= 0 || prm.window >= prm.max_seq_len) && prm.q_dtype == MLA_Q_BF16) {
     const long long tokens = prm.packed ? prm.max_total_q : B * prm.max_seq_len_q;
     const size_t halves = 2 * (size_t)std::max(tokens, 1LL) * (size_t)prm.num_heads;
     off = align_up(off + halves * kQSplitUnits * 16, 256);
@@ -173,8 +183,8 @@ int mla_decode_plan(const mla_decode_params* params, mla_plan_t** plan, size_t* 
   int sms = 0, n_pairs = 0;
   cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, p.device);
   if (e == cudaSuccess)
-    e = p.kv_dtype == MLA_KV_FP4_E2M1
-            ? mla::decode_fp4_setup(sms, &n_pairs)
+    e = uses_pair_mma(p)
+            ? mla::decode_pair_setup(p.kv_dtype, sms, &n_pairs)
             : mla::decode_sm103_setup(p.kv_dtype, p.sparse_top_k > 0, uses_f8_mma(p), effective_window(p) > 0, sms,
                                       &n_pairs);
   if (e == cudaSuccess) e = mla::partition_setup();
@@ -362,9 +372,8 @@ int run_impl(const mla_plan_t* plan, const void* query, const void* kv_cache,
       cudaEventRecordWithFlags(static_cast<cudaEvent_t>(event_before_decode), s, ev_flags) !=
           cudaSuccess)
     return MLA_ERR_CUDA;
-  if ((prm.kv_dtype == MLA_KV_FP4_E2M1 ? mla::launch_decode_fp4(p, plan->lay, workspace, s)
-                                       : mla::launch_decode_sm103(p, plan->lay, workspace, s)) !=
-      cudaSuccess)
+  if ((uses_pair_mma(prm) ? mla::launch_decode_pair(p, plan->lay, workspace, s)
+                          : mla::launch_decode_sm103(p, plan->lay, workspace, s)) != cudaSuccess)
     return MLA_ERR_CUDA;
   if (event_after_decode &&
       cudaEventRecordWithFlags(static_cast<cudaEvent_t>(event_after_decode), s, ev_flags) !=

@@ -143,9 +143,13 @@ __host__ __device__ inline size_t align_up(size_t x, size_t a) { return (x + a -
 // measured ~3.2), and every busy worker gets at least kMinUnits units.
 constexpr long long kOverheadTiles = 3;
 constexpr long long kMinUnits = 4;
-// The 4-bit kernel's tiles are shorter and its item overhead the same time:
-// measured 1.3 us a tile and about 6 us an item.
-constexpr long long kOverheadTilesFp4 = 5;
+// Whether a run is on the MMAs across CTA pairs (mla_decode_pair.cu).  Their tiles
+// are shorter and the item overhead is the same time: measured 1.2 us a tile and
+// about 6 us an item.
+__host__ __device__ inline bool pair_mma(const Problem& p) {
+  return p.kv_dtype == 2 || (p.kv_dtype == 1 && p.window > 0);
+}
+constexpr long long kOverheadTilesPair = 5;
 
 // Whether every row group goes to a worker of its own, uncut: the largest group
 // costs little more than an even share of the work, and cutting would add an

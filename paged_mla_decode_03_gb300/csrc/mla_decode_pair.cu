@@ -1,5 +1,6 @@
-// Paged MLA decode over a 4-bit cache (mla_fp4.cuh) on sm_103a: a persistent
-// kernel of CTA pairs whose tcgen05 MMAs span both CTAs (cta_group::2).
+// Paged MLA decode over a 4-bit cache (mla_fp4.cuh), and over an e4m3 cache with
+// a sliding window, on sm_103a: a persistent kernel of CTA pairs whose tcgen05
+// MMAs span both CTAs (cta_group::2).
 //
 // What it computes, for the 128 query rows of a work item and the KV rows
 // [kv_begin, kv_end) of its request, in 64-row tiles with an online softmax:
@@ -7,7 +8,7 @@
 // with K row j = 576 values code * scale and V its first 512.
 //
 // Numbers.  A cache value has at most six significant bits and lies in
-// [2^-10, 2688], so it is exact in f16, and both products run on f16 MMAs with
+// [2^-10, 2688] (e4m3: four bits, [2^-9, 448]), so it is exact in f16, and both products run on f16 MMAs with
 // fp32 accumulation.  A query row enters times a power of two that brings its
 // largest element to [2^14, 2^15): every element down to 2^-31 of it is exact
 // in f16, and its scores are multiplied back by 2^-k.  P enters as f16 (2^-11
@@ -83,25 +84,37 @@ constexpr uint32_t OFF_Q = 0;  // chunks kTmemChunks..8
 constexpr uint32_t OFF_K = OFF_Q + (kChunks - kTmemChunks) * kQChunk;
 constexpr uint32_t OFF_V = OFF_K + 2 * kKStage;
 constexpr uint32_t OFF_P = OFF_V + 2 * kVStage;
-constexpr uint32_t OFF_STG = OFF_P + 2 * kPTile;
-// a staging stage: own rows' codes, other rows' V codes, scales of the tile's two halves
-constexpr uint32_t STG_OWN = 0;
-constexpr uint32_t STG_OTHER = STG_OWN + kHalf * kFp4CodeBytes;
-constexpr uint32_t STG_SCALES = STG_OTHER + kHalf * 128;
-constexpr uint32_t kStage = STG_SCALES + kTile * kFp4ScaleBytes;
-constexpr uint32_t OFF_BARS = OFF_STG + 2 * kStage;
-constexpr uint32_t OFF_XMAX = OFF_BARS + 352;              // float [4][128]: tile maxima by tile mod 4
-constexpr uint32_t OFF_MREF = OFF_XMAX + 4 * 128 * 4;      // float [2][64]: references by tile parity
-constexpr uint32_t OFF_XSUM = OFF_MREF + 2 * kCtaRows * 4;  // float [2][2][128]: (sum, reference) by group
-constexpr uint32_t OFF_QSCALE = OFF_XSUM + 4 * 128 * 4;    // float [4][64]: 2^-k by item
-constexpr uint32_t OFF_TMEM = OFF_QSCALE + 4 * kCtaRows * 4;
-constexpr uint32_t OFF_ABORT = OFF_TMEM + 8;
-constexpr uint32_t OFF_MASK = OFF_ABORT + 8;  // uint32 [2][2]: rows in use, by stage and half
-constexpr uint32_t kSmemBytes = OFF_MASK + 16;
-static_assert(kSmemBytes <= 232448, "shared memory budget");
-static_assert(OFF_K % 1024 == 0 && OFF_V % 1024 == 0 && OFF_P % 1024 == 0 && kStage % 16 == 0 &&
-                  OFF_STG % 16 == 0 && STG_SCALES % 16 == 0 && OFF_BARS % 8 == 0,
-              "alignment");
+
+// The cache's format: 4 bits, or e4m3 (576 bytes a row, values exact in f16).
+enum Cache { kFp4, kE4m3 };
+template <int kCache> struct Cfg {
+  static constexpr uint32_t kCodeBytes = kCache == kFp4 ? kFp4CodeBytes : kQkDim;  // of a row
+  static constexpr uint32_t kScaleBytes = kCache == kFp4 ? kFp4ScaleBytes : 0;
+  static constexpr uint32_t kVBytes = kCache == kFp4 ? 128 : 256;  // codes of 256 dims
+  static constexpr uint32_t kRowBytes = kCodeBytes + kScaleBytes;
+  // P tiles: the staged e4m3 rows leave room for one
+  static constexpr uint32_t kPTiles = kCache == kFp4 ? 2 : 1;
+  static constexpr uint32_t OFF_STG = OFF_P + kPTiles * kPTile;
+  // a staging stage: own rows' codes, other rows' V codes, scales of the tile's two halves
+  static constexpr uint32_t STG_OWN = 0;
+  static constexpr uint32_t STG_OTHER = STG_OWN + kHalf * kCodeBytes;
+  static constexpr uint32_t STG_SCALES = STG_OTHER + kHalf * kVBytes;
+  static constexpr uint32_t kStage = STG_SCALES + kTile * kScaleBytes;
+  static constexpr uint32_t OFF_BARS = OFF_STG + 2 * kStage;
+  static constexpr uint32_t OFF_XMAX = OFF_BARS + 352;              // float [4][128]: tile maxima by tile mod 4
+  static constexpr uint32_t OFF_MREF = OFF_XMAX + 4 * 128 * 4;      // float [2][64]: references by tile parity
+  static constexpr uint32_t OFF_XSUM = OFF_MREF + 2 * kCtaRows * 4;  // float [2][2][128]: (sum, reference) by group
+  static constexpr uint32_t OFF_QSCALE = OFF_XSUM + 4 * 128 * 4;    // float [4][64]: 2^-k by item
+  static constexpr uint32_t OFF_TMEM = OFF_QSCALE + 4 * kCtaRows * 4;
+  static constexpr uint32_t OFF_ABORT = OFF_TMEM + 8;
+  static constexpr uint32_t OFF_MASK = OFF_ABORT + 8;  // uint32 [2][2]: rows in use, by stage and half
+  static constexpr uint32_t kSmemBytes = OFF_MASK + 16;
+  static_assert(kSmemBytes <= 232448, "shared memory budget");
+  static_assert(OFF_STG % 16 == 0 && kStage % 16 == 0 && STG_OTHER % 16 == 0 && STG_SCALES % 16 == 0 &&
+                    OFF_BARS % 8 == 0,
+                "alignment");
+};
+static_assert(OFF_K % 1024 == 0 && OFF_V % 1024 == 0 && OFF_P % 1024 == 0, "alignment");
 
 // TMEM columns
 constexpr uint32_t kTmemCols = 512;
@@ -238,6 +251,11 @@ __device__ __forceinline__ uint4 bf16x8_to_f16(const uint4 x, float up) {
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
+__device__ __forceinline__ void exchange(uint4& a, uint4& b, bool on) {
+  const uint4 t = a;
+  a = on ? b : a;
+  b = on ? t : b;
+}
 __device__ __forceinline__ uint4 e4m3x8_to_f16(const uint2 x) {
   const uint32_t w[2] = {x.x, x.y};
   uint32_t o[4];
@@ -249,10 +267,18 @@ __device__ __forceinline__ uint4 e4m3x8_to_f16(const uint2 x) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// 16 e4m3 codes as two 16-byte units of f16.
+__device__ __forceinline__ void widen16(const uint4 c, uint4& a, uint4& b) {
+  a = e4m3x8_to_f16(make_uint2(c.x, c.y));
+  b = e4m3x8_to_f16(make_uint2(c.z, c.w));
+}
+
 }  // namespace
 
+template <int kCache>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
+decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
+  using C = Cfg<kCache>;
   // The swizzled tiles need 1024-byte alignment, and there is no room to round
   // up: the block has no other shared memory, so its dynamic part starts at
   // offset 0 of its window.  A block placed otherwise reports and leaves.
@@ -268,13 +294,13 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
   const int* worker_begin = reinterpret_cast<const int*>(ws + lay.worker_ranges);
 
   Ctx c;
-  c.bars = reinterpret_cast<uint64_t*>(sm + OFF_BARS);
-  c.abort = reinterpret_cast<volatile int*>(sm + OFF_ABORT);
-  c.peer_abort = map_to_rank(smem_u32(sm + OFF_ABORT), rank ^ 1);
-  c.leader_bars = map_to_rank(smem_u32(sm + OFF_BARS), 0);
+  c.bars = reinterpret_cast<uint64_t*>(sm + C::OFF_BARS);
+  c.abort = reinterpret_cast<volatile int*>(sm + C::OFF_ABORT);
+  c.peer_abort = map_to_rank(smem_u32(sm + C::OFF_ABORT), rank ^ 1);
+  c.leader_bars = map_to_rank(smem_u32(sm + C::OFF_BARS), 0);
   c.status = reinterpret_cast<int*>(ws) + kHdrStatus;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + OFF_TMEM);
-  volatile uint32_t* row_mask = reinterpret_cast<volatile uint32_t*>(sm + OFF_MASK);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::OFF_TMEM);
+  volatile uint32_t* row_mask = reinterpret_cast<volatile uint32_t*>(sm + C::OFF_MASK);
 
   if (tid == 0) {
     for (int i = 0; i < NUM_BARS; ++i) {
@@ -321,7 +347,7 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
     // tiles to L2.
     const bool bulk = warp == 0;
     const int ps = p.page_size, ps_shift = ps == kTile ? 6 : 5, npg = kTile >> ps_shift;
-    const size_t page_bytes = (size_t)ps * kFp4RowBytes;
+    const size_t page_bytes = (size_t)ps * C::kRowBytes;
     const unsigned char* cache = static_cast<const unsigned char*>(p.kv_cache);
     uint32_t g = 0;
     for (int idx = item_begin; idx < item_end; ++idx) {
@@ -354,7 +380,7 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
         const bool on0 = id0 >= 0 && walk.seen(r0, r0 + kHalf - 1);
         const bool on1 = id1 >= 0 && j0 + kHalf < it.kv_end && walk.seen(r0 + kHalf, r0 + kTile - 1);
         const uint32_t s = g & 1, use = g >> 1;
-        unsigned char* stg = sm + OFF_STG + s * kStage;
+        unsigned char* stg = sm + C::OFF_STG + s * C::kStage;
         uint64_t* full = &c.bars[STG_FULL0 + s];
         if (bulk) {
           // rows past the item's end, that no query row sees, or on a page that is
@@ -369,36 +395,40 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
             const int row1 = npg == 1 ? kHalf : 0;  // first row of half 1 in its page
             const unsigned char* pg0 = cache + (size_t)(on0 ? id0 : 0) * page_bytes;
             const unsigned char* pg1 = cache + (size_t)(on1 ? id1 : 0) * page_bytes;
-            const unsigned char* sc0 = pg0 + (size_t)ps * kFp4CodeBytes;
-            const unsigned char* sc1 = pg1 + (size_t)ps * kFp4CodeBytes + row1 * kFp4ScaleBytes;
-            constexpr uint32_t kScales = kHalf * kFp4ScaleBytes, kCodes = kHalf * kFp4CodeBytes;
+            const unsigned char* sc0 = pg0 + (size_t)ps * C::kCodeBytes;
+            const unsigned char* sc1 = pg1 + (size_t)ps * C::kCodeBytes + row1 * C::kScaleBytes;
+            constexpr uint32_t kScales = kHalf * C::kScaleBytes, kCodes = kHalf * C::kCodeBytes;
             const bool own = rank == 0 ? on0 : on1;
             row_mask[2 * s] = mask0;
             row_mask[2 * s + 1] = mask1;
             mbar_arrive_expect_tx(full, (on0 ? kScales : 0) + (on1 ? kScales : 0) + (own ? kCodes : 0));
-            if (own) bulk_load(stg + STG_OWN, rank == 0 ? pg0 : pg1 + row1 * kFp4CodeBytes, kCodes, full);
-            if (on0 && on1 && npg == 1) {
-              bulk_load(stg + STG_SCALES, sc0, 2 * kScales, full);
+            if (own) bulk_load(stg + C::STG_OWN, rank == 0 ? pg0 : pg1 + row1 * C::kCodeBytes, kCodes, full);
+            if constexpr (kCache == kE4m3) {
+              // (no scales)
+            } else if (on0 && on1 && npg == 1) {
+              bulk_load(stg + C::STG_SCALES, sc0, 2 * kScales, full);
             } else {
-              if (on0) bulk_load(stg + STG_SCALES, sc0, kScales, full);
-              if (on1) bulk_load(stg + STG_SCALES + kScales, sc1, kScales, full);
+              if (on0) bulk_load(stg + C::STG_SCALES, sc0, kScales, full);
+              if (on1) bulk_load(stg + C::STG_SCALES + kScales, sc1, kScales, full);
             }
           }
           __syncwarp();
         } else {
           if (!wait_bar(c, STG_EMPTY0 + s, (use & 1) ^ 1)) goto fail_copy;
-          // eight 16-byte units of a row: eight lanes a row
+          // kUnits 16-byte units of a row: kUnits lanes a row.  Unit u of row r goes to
+          // u ^ (r mod 8), so that eight rows' reads of one unit meet eight bank groups
           if (rank == 0 ? on1 : on0) {
+            constexpr int kUnits = C::kVBytes / 16, kRowsAStep = 32 / kUnits;
+            const int u = lane % kUnits, r0u = lane / kUnits;
             const unsigned char* src = cache + (size_t)(rank == 0 ? id1 : id0) * page_bytes +
-                                       (rank == 0 && npg == 1 ? kHalf * kFp4CodeBytes : 0) +
-                                       (lane >> 3) * kFp4CodeBytes + 128 * rank + 16 * (lane & 7);
-            // unit u of row r goes to u ^ (r mod 8), so that eight rows' reads of one
-            // unit meet eight bank groups
-            unsigned char* dst = stg + STG_OTHER + (lane >> 3) * 128;
-            const int u = lane & 7, r7 = lane >> 3;
+                                       (rank == 0 && npg == 1 ? kHalf * C::kCodeBytes : 0) +
+                                       C::kVBytes * rank + 16 * u;
+            unsigned char* dst = stg + C::STG_OTHER;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              cp_async_16(dst + i * 512 + ((u ^ (r7 + 4 * (i & 1))) << 4), src + i * 4 * kFp4CodeBytes);
+            for (int i = 0; i < kHalf / kRowsAStep; ++i) {
+              const int r = i * kRowsAStep + r0u;
+              cp_async_16(dst + r * C::kVBytes + ((u ^ (r & 7)) << 4), src + r * C::kCodeBytes);
+            }
           }
           cp_async_arrive(full);
           // this CTA's half of the tiles up to kAhead on, to L2: the staged tiles
@@ -406,12 +436,12 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
           for (int a = t == 0 ? 2 : kAhead; a <= kAhead; ++a) {
             const int i = (t + a) * npg + (npg == 2 ? rank : 0);
             const int from = __shfl_sync(0xffffffffu, (i >> 5) == (slot0 >> 5) ? cur : nxt, i & 31);
-            if (t + a < nt && lane < 2 && from >= 0) {
+            if (t + a < nt && lane < (kCache == kFp4 ? 2 : 1) && from >= 0) {
               const unsigned char* pg = cache + (size_t)from * page_bytes;
               const int r = npg == 2 ? 0 : kHalf * rank;
-              bulk_prefetch_l2(lane == 0 ? pg + r * kFp4CodeBytes
-                                         : pg + (size_t)ps * kFp4CodeBytes + r * kFp4ScaleBytes,
-                               kHalf * (lane == 0 ? kFp4CodeBytes : kFp4ScaleBytes));
+              bulk_prefetch_l2(lane == 0 ? pg + r * C::kCodeBytes
+                                         : pg + (size_t)ps * C::kCodeBytes + r * C::kScaleBytes,
+                               kHalf * (lane == 0 ? C::kCodeBytes : C::kScaleBytes));
             }
           }
         }
@@ -500,7 +530,7 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
             for (int ks = 0; ks < kTile / 16; ++ks)
 #pragma unroll
               for (int j = 0; j < 2; ++j)
-                mma_f16_pair_ss(tmem + TM_O + 128 * j, p_desc + s * (kPTile >> 4) + 2 * ks,
+                mma_f16_pair_ss(tmem + TM_O + 128 * j, p_desc + (C::kPTiles == 2 ? s * (kPTile >> 4) : 0) + 2 * ks,
                                 v + ((j * 2 * kVChunk + ks * 16 * 128) >> 4), idesc,
                                 (t == 0 && ks == 0) ? 0u : 1u);
             mma_commit_pair(&c.bars[PV_DONE0 + s]);
@@ -531,10 +561,10 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
     const float bmm1 = run_bmm1(p, c.status) * kLog2e;
     const float bmm2 = run_bmm2(p);
     const int W = max(p.cp_world, 1);
-    float* mref = reinterpret_cast<float*>(sm + OFF_MREF);
-    float* xsum = reinterpret_cast<float*>(sm + OFF_XSUM);
-    const float* qscale = reinterpret_cast<const float*>(sm + OFF_QSCALE);
-    const uint32_t prow = swizzled_row(smem_u32(sm) + OFF_P + kPTile * grp, row);
+    float* mref = reinterpret_cast<float*>(sm + C::OFF_MREF);
+    float* xsum = reinterpret_cast<float*>(sm + C::OFF_XSUM);
+    const float* qscale = reinterpret_cast<const float*>(sm + C::OFF_QSCALE);
+    const uint32_t prow = swizzled_row(smem_u32(sm) + OFF_P + (C::kPTiles == 2 ? kPTile * grp : 0), row);
     uint4* part_o = reinterpret_cast<uint4*>(ws + lay.part_o);
     float* part_lse = reinterpret_cast<float*>(ws + lay.part_lse);
     int* comb_done = reinterpret_cast<int*>(ws + lay.comb_done);
@@ -593,7 +623,7 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
         for (int j = 4; j < 32; ++j) mt[j & 3] = fmaxf(mt[j & 3], __uint_as_float(v[j]));
         // (four buffers: a partner that still reads the maxima of tile g has let QK
         // of tile g + 2 into S, but not of g + 4)
-        float* xmax = reinterpret_cast<float*>(sm + OFF_XMAX) + 128 * (g & 3);
+        float* xmax = reinterpret_cast<float*>(sm + C::OFF_XMAX) + 128 * (g & 3);
         xmax[l] = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
         // The reference after the previous tile, which the other group had.  Every
         // tile but the very first waits for it, and before its own maximum goes
@@ -645,7 +675,11 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
           l_part += a + b;
         }
         // this P tile has been read
-        if (!wait_bar(c, PV_DONE0 + grp, ((g >> 1) & 1) ^ 1)) goto fail_soft;
+        if constexpr (C::kPTiles == 2) {
+          if (!wait_bar(c, PV_DONE0 + grp, ((g >> 1) & 1) ^ 1)) goto fail_soft;
+        } else {
+          if (g > 0 && !wait_bar(c, PV_DONE0 + (grp ^ 1), ((g - 1) >> 1) & 1)) goto fail_soft;
+        }
 #pragma unroll
         for (int u = 0; u < 4; ++u)
           put(prow, 4 * hh + u, make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]));
@@ -749,7 +783,7 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
     const uint32_t grp = (uint32_t)w >> 3;
     const int k = w & 7, vc = k & 3;
     const bool in_half = (k >> 2) == rank;
-    float* qscale = reinterpret_cast<float*>(sm + OFF_QSCALE);
+    float* qscale = reinterpret_cast<float*>(sm + C::OFF_QSCALE);
     uint32_t g = 0;
     int n_item = 0;
     // this lane's rows in the group's stages
@@ -760,39 +794,61 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
     auto convert_tile = [&]() -> bool {
       const uint32_t s = grp;
       if (!wait_bar(c, STG_FULL0 + s, (g >> 1) & 1)) return false;
-      const unsigned char* stg = sm + OFF_STG + s * kStage;
-      const int own = kHalf * rank + lane, oth = kHalf * (rank ^ 1) + lane;
-      const unsigned char* codes = stg + STG_OWN + lane * kFp4CodeBytes;
-      const unsigned char* sc_own = stg + STG_SCALES + own * kFp4ScaleBytes;
-      const unsigned char* sc_oth = stg + STG_SCALES + oth * kFp4ScaleBytes;
-      // (rows are 18 units of 16 bytes apart: rows 4 to 7 of eight take their two
-      // units in the other order, and no two rows of a phase share a bank group)
-      const int swap = (lane >> 2) & 1;
-      uint4 c0 = *reinterpret_cast<const uint4*>(codes + 32 * k + 16 * swap);
-      uint4 c1 = *reinterpret_cast<const uint4*>(codes + 32 * k + 16 * (swap ^ 1));
-      uint32_t sc = *reinterpret_cast<const uint32_t*>(sc_own + 4 * k);
-      uint32_t s2 = in_half ? (uint32_t)sc_own[32 + vc]
-                            : *reinterpret_cast<const uint32_t*>(sc_oth + 16 * rank + 4 * vc);
+      const unsigned char* stg = sm + C::OFF_STG + s * C::kStage;
+      const unsigned char* codes = stg + C::STG_OWN + lane * C::kCodeBytes;
+      const unsigned char* other = stg + C::STG_OTHER + lane * C::kVBytes;
+      // whether this lane's rows are in use (the others are zeros)
       const uint32_t m1 = row_mask[2 * s + rank], m2 = in_half ? m1 : row_mask[2 * s + (rank ^ 1)];
-      if (!((m1 >> lane) & 1u)) sc = 0u;
-      if (!((m2 >> lane) & 1u)) s2 = 0u;
-      if (swap) {
-        const uint4 c2 = c0;
-        c0 = c1;
-        c1 = c2;
-      }
+      const bool on1 = (m1 >> lane) & 1u, on2 = (m2 >> lane) & 1u;
       uint4 x[8];
-      convert64(c0, c1, sc, x);
+      uint32_t s2 = 0;  // 4 bits: the second part's scales
+      if constexpr (kCache == kFp4) {
+        const unsigned char* scales = stg + C::STG_SCALES;
+        const unsigned char* sc_own = scales + (kHalf * rank + lane) * C::kScaleBytes;
+        const unsigned char* sc_oth = scales + (kHalf * (rank ^ 1) + lane) * C::kScaleBytes;
+        // (rows are 18 units of 16 bytes apart: rows 4 to 7 of eight take their two
+        // units in the other order, and no two rows of a phase share a bank group)
+        const int swap = (lane >> 2) & 1;
+        const uint4 a = *reinterpret_cast<const uint4*>(codes + 32 * k + 16 * swap);
+        const uint4 b = *reinterpret_cast<const uint4*>(codes + 32 * k + 16 * (swap ^ 1));
+        uint32_t sc = *reinterpret_cast<const uint32_t*>(sc_own + 4 * k);
+        s2 = in_half ? (uint32_t)sc_own[32 + vc]
+                     : *reinterpret_cast<const uint32_t*>(sc_oth + 16 * rank + 4 * vc);
+        if (!on1) sc = 0u;
+        if (!on2) s2 = 0u;
+        convert64(swap ? b : a, swap ? a : b, sc, x);
+      } else {
+        // (rows are 36 units apart: pairs of rows start at four places of the order,
+        // and the units are put back by two rounds of exchanges)
+        const int r2 = (lane >> 1) & 3;
+        uint4 u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          u[i] = on1 ? *reinterpret_cast<const uint4*>(codes + 64 * k + 16 * (i ^ r2)) : make_uint4(0, 0, 0, 0);
+        exchange(u[0], u[1], r2 & 1);
+        exchange(u[2], u[3], r2 & 1);
+        exchange(u[0], u[2], r2 & 2);
+        exchange(u[1], u[3], r2 & 2);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) widen16(u[i], x[2 * i], x[2 * i + 1]);
+      }
       // QK of the group's previous tile has read this K stage
       if (!wait_bar(c, S_FULL0 + grp, ((g >> 1) & 1) ^ 1)) return false;
 #pragma unroll
       for (int e = 0; e < 8; ++e) put(k_row, e, x[e]);
-      if (in_half) {
-        const uint2 rc = *reinterpret_cast<const uint2*>(codes + 256 + 8 * vc);
-        uint32_t s0, s1;
-        scale_pairs(s2, s0, s1);
-        put(r_row, 2 * vc, convert8(rc.x, s0));
-        put(r_row, 2 * vc + 1, convert8(rc.y, s0));
+      if (in_half) {  // 16 RoPE dims
+        uint4 y0, y1;
+        if constexpr (kCache == kFp4) {
+          const uint2 rc = *reinterpret_cast<const uint2*>(codes + 256 + 8 * vc);
+          uint32_t s0, s1;
+          scale_pairs(s2, s0, s1);
+          y0 = convert8(rc.x, s0);
+          y1 = convert8(rc.y, s0);
+        } else {
+          widen16(on1 ? *reinterpret_cast<const uint4*>(codes + 512 + 16 * vc) : make_uint4(0, 0, 0, 0), y0, y1);
+        }
+        put(r_row, 2 * vc, y0);
+        put(r_row, 2 * vc + 1, y1);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -800,11 +856,17 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
         arrive_leader(c, K_FULL0 + 3 * grp + k / kGroup, 4);
         if (in_half) arrive_leader(c, K_FULL0 + 3 * grp + 2, 1);
       }
-      if (!in_half) {
-        const unsigned char* other = stg + STG_OTHER + lane * 128;
-        c0 = *reinterpret_cast<const uint4*>(other + (((2 * vc) ^ (lane & 7)) << 4));
-        c1 = *reinterpret_cast<const uint4*>(other + (((2 * vc + 1) ^ (lane & 7)) << 4));
-        convert64(c0, c1, s2, x);
+      if (!in_half) {  // V of the other rows
+        if constexpr (kCache == kFp4) {
+          convert64(*reinterpret_cast<const uint4*>(other + (((2 * vc) ^ (lane & 7)) << 4)),
+                    *reinterpret_cast<const uint4*>(other + (((2 * vc + 1) ^ (lane & 7)) << 4)), s2, x);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            widen16(on2 ? *reinterpret_cast<const uint4*>(other + (((4 * vc + i) ^ (lane & 7)) << 4))
+                        : make_uint4(0, 0, 0, 0),
+                    x[2 * i], x[2 * i + 1]);
+        }
         __syncwarp();
       }
       if (lane == 0) mbar_arrive(&c.bars[STG_EMPTY0 + s]);  // every code is in registers
@@ -930,43 +992,54 @@ decode_fp4_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
 
 namespace {
 
-cudaLaunchConfig_t pair_launch(int grid, cudaStream_t stream, cudaLaunchAttribute* attr) {
+cudaLaunchConfig_t pair_launch(int grid, size_t smem, cudaStream_t stream, cudaLaunchAttribute* attr) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cfg;
 }
 
-}  // namespace
-
-cudaError_t decode_fp4_setup(int sm_count, int* n_pairs) {
-  cudaError_t e = cudaFuncSetAttribute(decode_fp4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kSmemBytes);
+template <int kCache>
+cudaError_t setup_one(int sm_count, int* n_pairs) {
+  auto kernel = decode_pair_kernel<kCache>;
+  constexpr size_t kSmem = Cfg<kCache>::kSmemBytes;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = 2;
   attr.val.clusterDim.y = 1;
   attr.val.clusterDim.z = 1;
-  const cudaLaunchConfig_t cfg = pair_launch(2 * (sm_count / 2), nullptr, &attr);
+  const cudaLaunchConfig_t cfg = pair_launch(2 * (sm_count / 2), kSmem, nullptr, &attr);
   int clusters = 0;
-  e = cudaOccupancyMaxActiveClusters(&clusters, decode_fp4_kernel, &cfg);
+  e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
   if (e != cudaSuccess) return e;
   if (clusters <= 0) return cudaErrorInvalidConfiguration;
   *n_pairs = std::min(clusters, sm_count / 2);
   return cudaSuccess;
 }
 
-cudaError_t launch_decode_fp4(const Problem& p, const Layout& lay, void* ws, cudaStream_t stream) {
+template <int kCache>
+cudaError_t launch_one(const Problem& p, const Layout& lay, void* ws, cudaStream_t stream) {
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
-  const cudaLaunchConfig_t cfg = pair_launch(lay.n_ctas, stream, &attr);
-  return cudaLaunchKernelEx(&cfg, decode_fp4_kernel, p, lay, static_cast<char*>(ws));
+  const cudaLaunchConfig_t cfg = pair_launch(lay.n_ctas, Cfg<kCache>::kSmemBytes, stream, &attr);
+  return cudaLaunchKernelEx(&cfg, decode_pair_kernel<kCache>, p, lay, static_cast<char*>(ws));
+}
+
+}  // namespace
+
+cudaError_t decode_pair_setup(int kv_dtype, int sm_count, int* n_pairs) {
+  return kv_dtype == 2 ? setup_one<kFp4>(sm_count, n_pairs) : setup_one<kE4m3>(sm_count, n_pairs);
+}
+
+cudaError_t launch_decode_pair(const Problem& p, const Layout& lay, void* ws, cudaStream_t stream) {
+  return p.kv_dtype == 2 ? launch_one<kFp4>(p, lay, ws, stream) : launch_one<kE4m3>(p, lay, ws, stream);
 }
 
 }  // namespace mla

@@ -50,8 +50,8 @@
 // (14-21) widen each staged e4m3 tile to bf16 in shared memory (exact; the
 // k_scale lives in bmm1/bmm2), and the bf16 ring is 3 deep beside a 2-deep
 // e4m3 staging ring.
-// Under a sliding window (separate instantiations, so that the others keep their
-// code) an item's KV rows are virtual ones: the sinks' tiles, then the tiles from
+// Under a sliding window (bf16 cache; a separate instantiation, so that the others
+// keep their code) an item's KV rows are virtual ones: the sinks' tiles, then the tiles from
 // the earliest window on; rows outside a query row's own window are masked.
 // Under sparse top-k selection (a separate instantiation, two warps more) a
 // work item is one token's H query rows and its KV tiles are 64 entries of
@@ -1567,7 +1567,7 @@ cudaError_t launch_one(int grid, cudaStream_t stream, const Problem& p, const La
 template <bool kFp8, bool kSparse, bool kF8 = false>
 cudaError_t launch_pdl(int grid, cudaStream_t stream, const Problem& p, const Layout& lay, char* ws,
                        const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c) {
-  if constexpr (!kSparse)
+  if constexpr (!kSparse && !kFp8 && !kF8)
     if (p.window > 0)
       return launch_one<kFp8, false, kF8, true>(grid, stream, p, lay, ws, a, b, c);
   return launch_one<kFp8, kSparse, kF8, false>(grid, stream, p, lay, ws, a, b, c);
@@ -1577,12 +1577,9 @@ cudaError_t launch_pdl(int grid, cudaStream_t stream, const Problem& p, const La
 
 cudaError_t decode_sm103_setup(int kv_dtype, int sparse, int f8_mma, int window, int sm_count,
                                int* n_pairs) {
-  if (window) {
-    if (sparse) return cudaErrorInvalidValue;
-    if (kv_dtype != 1) return setup_one<false, false, false, true>(sm_count, n_pairs);
-    return f8_mma ? setup_one<false, false, true, true>(sm_count, n_pairs)
-                  : setup_one<true, false, false, true>(sm_count, n_pairs);
-  }
+  if (window)  // an e4m3 cache with a window runs on the pair MMAs
+    return sparse || kv_dtype == 1 ? cudaErrorInvalidValue
+                                   : setup_one<false, false, false, true>(sm_count, n_pairs);
   if (kv_dtype == 1 && f8_mma && !sparse) return setup_one<false, false, true>(sm_count, n_pairs);
   if (kv_dtype == 1)
     return sparse ? setup_one<true, true>(sm_count, n_pairs)

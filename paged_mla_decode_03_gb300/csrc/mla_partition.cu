@@ -171,8 +171,8 @@ partition_kernel(Problem p, Layout lay, char* __restrict__ ws) {
   const int R = lay.rows_per_group;
   const int H = p.num_heads;
   const bool sparse = p.sparse_k > 0;
-  const bool fp4 = p.kv_dtype == 2;
-  const long long c0 = fp4 ? kOverheadTilesFp4 : kOverheadTiles;
+  const bool pair = pair_mma(p);
+  const long long c0 = pair ? kOverheadTilesPair : kOverheadTiles;
   // KV rows a group of a request (length L, q tokens) walks: its cache rows, those
   // its sliding window reaches, or the token's list
   auto kv_rows = [&](int L, int q) {
@@ -315,7 +315,7 @@ partition_kernel(Problem p, Layout lay, char* __restrict__ ws) {
   bd.WL = W / lanes;      // every lane has the same cost
   bd.table = nullptr;
   bd.overhead = c0;
-  const bool ask = p.window > 0 || fp4;
+  const bool ask = p.window > 0 || pair;
   long long max_cost = 0;
   if (ask) {  // (uniform over the block)
     int t_max = 0;
@@ -570,8 +570,8 @@ partition_warp_kernel(Problem p, Layout lay, char* __restrict__ ws) {
   const int R = lay.rows_per_group;
   const int H = p.num_heads;
   const bool sparse = p.sparse_k > 0;
-  const bool fp4 = p.kv_dtype == 2;
-  const long long c0 = fp4 ? kOverheadTilesFp4 : kOverheadTiles;
+  const bool pair = pair_mma(p);
+  const long long c0 = pair ? kOverheadTilesPair : kOverheadTiles;
   auto kv_rows = [&](int L, int q) {
     return sparse ? p.sparse_k : L - window_skip(p.window, p.sinks, p.causal, L, q);
   };
@@ -676,7 +676,7 @@ partition_warp_kernel(Problem p, Layout lay, char* __restrict__ ws) {
   bd.overhead = c0;
   {
     // uncut: worker q's range starts where group q does
-    const bool uncut = partition_uncut(p.window > 0 || fp4, n_groups, n, c0 + warp_max(t_max), W);
+    const bool uncut = partition_uncut(p.window > 0 || pair, n_groups, n, c0 + warp_max(t_max), W);
     for (long long q = lane; q <= n; q += 32)
       sh.bound[q] = !uncut ? bd.boundary_of(q) : q < n_groups ? sh.g_start[q] : W;
   }

@@ -92,7 +92,7 @@ class Case:
         g = torch.Generator().manual_seed(seed + 1)
         x = (torch.randn(self.T + pad, heads, 576, generator=g) * q_gain).to(torch.bfloat16)
         self.query = (x.float() / q_gain).to(torch.float8_e4m3fn).cuda() if q_fp8 else x.cuda()
-        self.split_q = kind == "e4m3" and not widen and not q_fp8
+        self.split_q = kind == "e4m3" and not widen and not q_fp8 and not 0 < window < (max_len or max(ls))
         self.max_len = max_len or max(ls)
         self.out = torch.full((self.T + pad, heads, 512), 3.0, dtype=torch.bfloat16, device="cuda")
         self.lse = torch.full((self.T + pad, heads), 3.0, dtype=torch.float32, device="cuda")

@@ -9,9 +9,8 @@ import torch
 import paged_mla_decode_03_gb300 as mla
 from attention_ref import Case
 
-# P as the kernels store it: bf16; two e4m3 parts, whose residue ends at half the
-# smallest e4m3 subnormal; f16 (the default of Case.check)
-P = {"bf16": dict(p_bits=8, p_floor=0.0), "e4m3": dict(p_bits=8, p_floor=2.0 ** -10), "fp4": {}}
+# P as the kernels store it: bf16, or f16 (the default of Case.check)
+P = {"bf16": dict(p_bits=8, p_floor=0.0), "e4m3": {}, "fp4": {}}
 
 CASES = [  # page, lengths, query lengths, heads, window, sinks, options
     (64, [1], [1], 16, 1, 0, {}),
@@ -37,7 +36,7 @@ CASES = [  # page, lengths, query lengths, heads, window, sinks, options
 @pytest.mark.parametrize("ps,ls,qs,heads,window,sinks,kw", CASES)
 def test_window(kind, widen, ps, ls, qs, heads, window, sinks, kw):
     c = Case(kind, ps, ls, qs, heads, window=window, sinks=sinks, seed=heads + window, widen=widen, **kw).run()
-    c.check(**(P["bf16"] if widen else P[kind]))
+    c.check(**P[kind])
 
 
 @pytest.mark.gpu
@@ -65,6 +64,7 @@ def test_a_window_over_everything_is_no_window(kind):
     b.run()
     torch.cuda.synchronize()
     assert torch.equal(a.out, b.out) and torch.equal(a.lse, b.lse)
+    # (the same rows through one plan's partition: the window is not even looked at)
     # one row short of it, the first row of the longer request is out
     Case(kind, 64, [300, 77], [1, 1], 64, window=299, seed=1).run().check(**P[kind])
 
