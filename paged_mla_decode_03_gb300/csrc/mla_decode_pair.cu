@@ -267,6 +267,10 @@ __device__ __forceinline__ uint4 e4m3x8_to_f16(const uint2 x) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// A word whose first n bits are set (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t first_bits(int n) {
+  return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
+}
 // 16 e4m3 codes as two 16-byte units of f16.
 __device__ __forceinline__ void widen16(const uint4 c, uint4& a, uint4& b) {
   a = e4m3x8_to_f16(make_uint2(c.x, c.y));
@@ -582,7 +586,7 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
         return p.causal ? causal_last(it.mask_base, (row0 + r) >> h_shift, W) : it.seq_len - 1;
       };
       const int last = last_of(min(q, n_rows - 1));
-      const int low = p.window > 0 ? last - p.window + 1 : INT_MIN;  // first row of the window
+      const int low = p.window > 0 ? last - p.window + 1 : -1;  // first row of the window
       // tiles inside [clean_lo, clean_hi) need no mask for any row of the item
       const int clean_hi = last_of(0) + 1;
       const int clean_lo = p.window > 0 ? last_of(n_rows - 1) - p.window + 1 : INT_MIN;
@@ -607,11 +611,11 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
                            (r0 >= clean_lo || r0 + kTile <= p.sinks);
         uint32_t hidden = 0;  // columns that the mask takes out
         if (!clean) {
-#pragma unroll 1
-          for (int j = 0; j < 32; ++j) {
-            const int k = 32 * hh + j, at = r0 + k;
-            if (!(at <= last && k < valid && (at >= low || at < p.sinks))) hidden |= 1u << j;
-          }
+          // of this thread's columns, rows r0 + 32 hh + [0, 32): those up to `last` and
+          // inside the item, from the window's first row on or among the sinks
+          const int at = r0 + 32 * hh;
+          hidden = ~(first_bits(min(last + 1 - at, valid - 32 * hh)) &
+                     (~first_bits(low - at) | first_bits(p.sinks - at)));
 #pragma unroll
           for (int j = 0; j < 32; ++j)
             if ((hidden >> j) & 1u) v[j] = 0xFF800000u;  // -inf

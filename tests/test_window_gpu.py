@@ -64,7 +64,6 @@ def test_a_window_over_everything_is_no_window(kind):
     b.run()
     torch.cuda.synchronize()
     assert torch.equal(a.out, b.out) and torch.equal(a.lse, b.lse)
-    # (the same rows through one plan's partition: the window is not even looked at)
     # one row short of it, the first row of the longer request is out
     Case(kind, 64, [300, 77], [1, 1], 64, window=299, seed=1).run().check(**P[kind])
 
