@@ -20,8 +20,7 @@ cudaError_t launch_partition(const Problem& p, const Layout& lay, void* ws, cuda
 cudaError_t partition_setup();
 cudaError_t launch_combine(const Problem& p, const Layout& lay, void* ws, int grid,
                            cudaStream_t stream);
-cudaError_t decode_sm103_setup(int kv_dtype, int sparse, int f8_mma, int window, int sm_count,
-                               int* n_pairs);
+cudaError_t decode_sm103_setup(int kv_dtype, int sparse, int f8_mma, int sm_count, int* n_pairs);
 cudaError_t launch_merge_states(const void* o_parts, const float* lse_parts, int n, long long rows,
                                 float scale, void* out, float* lse_out, cudaStream_t stream);
 cudaError_t launch_qsplit(const Problem& p, const Layout& lay, void* ws, int sm_count,
@@ -61,8 +60,7 @@ int effective_window(const mla_decode_params& p) {
 // one with a window (32 x 4 x 128 heads, window 4096: 303 us a call on the FP8
 // MMAs, whose tiles exchange scores between the CTAs).
 bool uses_pair_mma(const mla_decode_params& p) {
-  return p.kv_dtype == MLA_KV_FP4_E2M1 ||
-         (p.kv_dtype == MLA_KV_FP8_E4M3 && effective_window(p) > 0);
+  return p.kv_dtype == MLA_KV_FP4_E2M1 || effective_window(p) > 0;
 }
 
 // Otherwise an e4m3 cache runs on the FP8 MMAs unless widening was asked for
@@ -185,8 +183,7 @@ int mla_decode_plan(const mla_decode_params* params, mla_plan_t** plan, size_t* 
   if (e == cudaSuccess)
     e = uses_pair_mma(p)
             ? mla::decode_pair_setup(p.kv_dtype, sms, &n_pairs)
-            : mla::decode_sm103_setup(p.kv_dtype, p.sparse_top_k > 0, uses_f8_mma(p), effective_window(p) > 0, sms,
-                                      &n_pairs);
+            : mla::decode_sm103_setup(p.kv_dtype, p.sparse_top_k > 0, uses_f8_mma(p), sms, &n_pairs);
   if (e == cudaSuccess) e = mla::partition_setup();
   cudaStream_t side = nullptr;
   if (e == cudaSuccess) e = cudaStreamCreateWithFlags(&side, cudaStreamNonBlocking);

@@ -147,7 +147,7 @@ constexpr long long kMinUnits = 4;
 // are shorter and the item overhead is the same time: measured 1.2 us a tile and
 // about 6 us an item.
 __host__ __device__ inline bool pair_mma(const Problem& p) {
-  return p.kv_dtype == 2 || (p.kv_dtype == 1 && p.window > 0);
+  return p.kv_dtype == 2 || p.window > 0;
 }
 constexpr long long kOverheadTilesPair = 5;
 

@@ -41,6 +41,7 @@
 // Every wait is bounded; a timeout sets the status word and both CTAs unwind.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <climits>
@@ -71,7 +72,6 @@ constexpr uint32_t kWaitLimit = 1u << 22;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
-constexpr float kPShift = 7.0f;            // P is stored times 2^7
 
 // shared memory, from a 1024-aligned base
 constexpr uint32_t kQChunk = kCtaRows * 128;  // 64 rows x 64 dims f16, 128B swizzle
@@ -85,22 +85,26 @@ constexpr uint32_t OFF_K = OFF_Q + (kChunks - kTmemChunks) * kQChunk;
 constexpr uint32_t OFF_V = OFF_K + 2 * kKStage;
 constexpr uint32_t OFF_P = OFF_V + 2 * kVStage;
 
-// The cache's format: 4 bits, or e4m3 (576 bytes a row, values exact in f16).
-enum Cache { kFp4, kE4m3 };
+// The cache's format: 4 bits; e4m3 (576 bytes a row, values exact in f16); bf16
+// (bf16 MMAs, and TMA brings K and V where the MMAs read them: no staging, and
+// the conversion warps only load queries and clear unused rows).
+enum Cache { kFp4, kE4m3, kBf16 };
 template <int kCache> struct Cfg {
-  static constexpr uint32_t kCodeBytes = kCache == kFp4 ? kFp4CodeBytes : kQkDim;  // of a row
+  static constexpr bool kTma = kCache == kBf16;
+  static constexpr float kPShift = kTma ? 0.f : 7.f;  // P is stored times 2^kPShift (bf16 has the range)
+  static constexpr uint32_t kCodeBytes = kCache == kFp4 ? kFp4CodeBytes : kTma ? 2 * kQkDim : kQkDim;  // of a row
   static constexpr uint32_t kScaleBytes = kCache == kFp4 ? kFp4ScaleBytes : 0;
   static constexpr uint32_t kVBytes = kCache == kFp4 ? 128 : 256;  // codes of 256 dims
   static constexpr uint32_t kRowBytes = kCodeBytes + kScaleBytes;
   // P tiles: the staged e4m3 rows leave room for one
-  static constexpr uint32_t kPTiles = kCache == kFp4 ? 2 : 1;
+  static constexpr uint32_t kPTiles = kCache == kE4m3 ? 1 : 2;
   static constexpr uint32_t OFF_STG = OFF_P + kPTiles * kPTile;
   // a staging stage: own rows' codes, other rows' V codes, scales of the tile's two halves
   static constexpr uint32_t STG_OWN = 0;
   static constexpr uint32_t STG_OTHER = STG_OWN + kHalf * kCodeBytes;
   static constexpr uint32_t STG_SCALES = STG_OTHER + kHalf * kVBytes;
   static constexpr uint32_t kStage = STG_SCALES + kTile * kScaleBytes;
-  static constexpr uint32_t OFF_BARS = OFF_STG + 2 * kStage;
+  static constexpr uint32_t OFF_BARS = OFF_STG + (kTma ? 0 : 2 * kStage);
   static constexpr uint32_t OFF_XMAX = OFF_BARS + 352;              // float [4][128]: tile maxima by tile mod 4
   static constexpr uint32_t OFF_MREF = OFF_XMAX + 4 * 128 * 4;      // float [2][64]: references by tile parity
   static constexpr uint32_t OFF_XSUM = OFF_MREF + 2 * kCtaRows * 4;  // float [2][2][128]: (sum, reference) by group
@@ -123,7 +127,7 @@ constexpr uint32_t TM_S = 256;  // two 32-column buffers; lane: query row and KV
 constexpr uint32_t TM_Q = 320;  // chunks 0..5 of the query row (mod 64), pairs of f16
 
 enum Bar {
-  STG_FULL0, STG_EMPTY0 = STG_FULL0 + 2,
+  STG_FULL0, STG_EMPTY0 = STG_FULL0 + 2,  // by tile parity (TMA: K landed, V landed)
   K_FULL0 = STG_EMPTY0 + 2,   // even CTA: [tile parity][3], both CTAs' chunks are there
   V_FULL0 = K_FULL0 + 2 * (kChunks / kGroup),  // even CTA
   PV_DONE0 = V_FULL0 + 2,              // by tile parity: V stage and P free, O stable
@@ -267,6 +271,10 @@ __device__ __forceinline__ uint4 e4m3x8_to_f16(const uint2 x) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+__device__ __forceinline__ uint4 e4m3x8_to_bf16(const uint2 x) {
+  return make_uint4(e4m3x2_to_bf16x2(x.x & 0xFFFFu), e4m3x2_to_bf16x2(x.x >> 16),
+                    e4m3x2_to_bf16x2(x.y & 0xFFFFu), e4m3x2_to_bf16x2(x.y >> 16));
+}
 // A word whose first n bits are set (none for n <= 0, all for n >= 32).
 __device__ __forceinline__ uint32_t first_bits(int n) {
   return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
@@ -281,7 +289,8 @@ __device__ __forceinline__ void widen16(const uint4 c, uint4& a, uint4& b) {
 
 template <int kCache>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
+decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
+                   const __grid_constant__ CUtensorMap tm_kv) {  // (bf16 cache only)
   using C = Cfg<kCache>;
   // The swizzled tiles need 1024-byte alignment, and there is no room to round
   // up: the block has no other shared memory, so its dynamic part starts at
@@ -309,11 +318,11 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
   if (tid == 0) {
     for (int i = 0; i < NUM_BARS; ++i) {
       uint32_t n = 1;  // one commit, or one warp
-      if (i >= STG_FULL0 && i < STG_EMPTY0) n = 1 + 32;  // bulk copies, each lane's own
-      if (i >= STG_EMPTY0 && i < K_FULL0) n = kConvWarps / 2;
+      if (i >= STG_FULL0 && i < STG_EMPTY0) n = C::kTma ? 1 : 1 + 32;  // bulk copies, each lane's own
+      if (i >= STG_EMPTY0 && i < K_FULL0) n = C::kTma ? 1 : kConvWarps / 2;
       // a latent chunk's warp counts four times, as the RoPE chunk has four warps
-      if (i >= K_FULL0 && i < V_FULL0) n = 2 * 4 * kGroup;
-      if (i >= V_FULL0 && i < V_FULL0 + 2) n = kConvWarps;  // half the warps of both CTAs
+      if (i >= K_FULL0 && i < V_FULL0) n = C::kTma ? 2 : 2 * 4 * kGroup;
+      if (i >= V_FULL0 && i < V_FULL0 + 2) n = C::kTma ? 2 : kConvWarps;  // half the warps of both CTAs
       if (i >= S_EMPTY0 && i < P_FULL0 + 2) n = kSoftWarps;  // half the warps of both CTAs
       if (i == Q_FULL) n = 2 * kConvWarps;
       if (i == QX || (i >= QS_FULL0 && i < QS_FULL0 + 4)) n = kConvWarps;
@@ -386,7 +395,48 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
         const uint32_t s = g & 1, use = g >> 1;
         unsigned char* stg = sm + C::OFF_STG + s * C::kStage;
         uint64_t* full = &c.bars[STG_FULL0 + s];
-        if (bulk) {
+        if constexpr (C::kTma) {
+          const int row1 = npg == 1 ? kHalf : 0;  // first row of half 1 in its page
+          const int y0 = id0 * ps, y1 = id1 * ps + row1;
+          if (bulk) {
+            // K: the own rows' nine chunks, once QK of two tiles ago has read the stage
+            const uint32_t mask0 = __ballot_sync(0xffffffffu, on0 && j0 + lane < it.kv_end &&
+                                                                  walk.seen(r0 + lane, r0 + lane));
+            const uint32_t mask1 =
+                __ballot_sync(0xffffffffu, on1 && j0 + kHalf + lane < it.kv_end &&
+                                               walk.seen(r0 + kHalf + lane, r0 + kHalf + lane));
+            if (!wait_bar(c, S_FULL0 + s, (use & 1) ^ 1)) goto fail_copy;
+            if (lane == 0) {
+              row_mask[2 * s] = mask0;
+              row_mask[2 * s + 1] = mask1;
+              const bool own = rank == 0 ? on0 : on1;
+              mbar_arrive_expect_tx(full, own ? kKStage : 0);
+              if (own)
+                for (int ch = 0; ch < kChunks; ++ch)
+                  tma_load_2d(sm + OFF_K + s * kKStage + ch * kKChunk, &tm_kv, 64 * ch, rank == 0 ? y0 : y1, full);
+            }
+          } else {
+            // V: this CTA's dims of all rows, once PV of two tiles ago has
+            if (!wait_bar(c, PV_DONE0 + s, (use & 1) ^ 1)) goto fail_copy;
+            if (lane == 0) {
+              uint64_t* v_full = &c.bars[STG_EMPTY0 + s];
+              mbar_arrive_expect_tx(v_full, ((on0 ? 1 : 0) + (on1 ? 1 : 0)) * (kVStage / 2));
+              for (int ch = 0; ch < 4; ++ch) {
+                unsigned char* dst = sm + OFF_V + s * kVStage + ch * kVChunk;
+                if (on0) tma_load_2d(dst, &tm_kv, 256 * rank + 64 * ch, y0, v_full);
+                if (on1) tma_load_2d(dst + kHalf * 128, &tm_kv, 256 * rank + 64 * ch, y1, v_full);
+              }
+            }
+            for (int a = t == 0 ? 2 : kAhead; a <= kAhead; ++a) {
+              const int i = (t + a) * npg + (npg == 2 ? rank : 0);
+              const int from = __shfl_sync(0xffffffffu, (i >> 5) == (slot0 >> 5) ? cur : nxt, i & 31);
+              if (t + a < nt && lane == 0 && from >= 0)
+                bulk_prefetch_l2(cache + (size_t)from * page_bytes + (npg == 2 ? 0 : kHalf * rank) * C::kCodeBytes,
+                                 kHalf * C::kCodeBytes);
+            }
+          }
+          __syncwarp();
+        } else if (bulk) {
           // rows past the item's end, that no query row sees, or on a page that is
           // not read, enter as zeros
           const uint32_t mask0 = __ballot_sync(0xffffffffu, on0 && j0 + lane < it.kv_end &&
@@ -458,13 +508,13 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
     // no copy issued here may still be landing when the CTA leaves
     for (uint32_t k = 0; k < 2 && k < g; ++k) {
       const uint32_t gi = g - 1 - k;
-      drain_wait(&c.bars[STG_FULL0 + (gi & 1)], (gi >> 1) & 1);
+      drain_wait(&c.bars[(C::kTma && !bulk ? STG_EMPTY0 : STG_FULL0) + (gi & 1)], (gi >> 1) & 1);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ QK issue
     // The whole warp walks the loops and one lane issues (see elect_one).
     if (rank == 0) {
-      constexpr uint32_t idesc = idesc_half(kRows, kTile, false, false);
+      constexpr uint32_t idesc = C::kTma ? idesc_f16(kRows, kTile, false, false) : idesc_half(kRows, kTile, false, false);
       // operand descriptors; a step along an operand adds its bytes / 16
       const uint64_t q_desc = smem_desc(smem_u32(sm + OFF_Q), 16, 1024, kSwizzle128B);
       const uint64_t k_desc = smem_desc(smem_u32(sm + OFF_K), 16, 1024, kSwizzle128B);
@@ -517,7 +567,7 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
     // ------------------------------------------------------------ PV issue
     // A warp of its own: its waits for P would hold up the next tile's QK.
     if (rank == 0) {
-      constexpr uint32_t idesc = idesc_half(kRows, 256, false, true);
+      constexpr uint32_t idesc = C::kTma ? idesc_f16(kRows, 256, false, true) : idesc_half(kRows, 256, false, true);
       const uint64_t p_desc = smem_desc(smem_u32(sm + OFF_P), 16, 1024, kSwizzle128B);
       const uint64_t v_desc = smem_desc(smem_u32(sm + OFF_V), kVChunk, 1024, kSwizzle128B);
       uint32_t g = 0;
@@ -655,7 +705,7 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
           l_part *= ex2(m - m_new);
           m = m_new;
         }
-        const float ref = kPShift - (m == -INFINITY ? 0.f : m);
+        const float ref = C::kPShift - (m == -INFINITY ? 0.f : m);
         // (rows past the request's own compute something that nothing reads)
         const uint64_t scale2 = pack_f32x2(scale, scale), ref2 = pack_f32x2(ref, ref);
         uint64_t rs[2] = {0, 0};
@@ -670,8 +720,13 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
             if ((hidden >> (2 * j + 1)) & 1u) b = 0.f;
           }
           rs[j & 1] = add_f32x2(rs[j & 1], pack_f32x2(a, b));
-          const __half2 h = __floats2half2_rn(a, b);
-          v[j] = *reinterpret_cast<const uint32_t*>(&h);
+          if constexpr (C::kTma) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+            v[j] = *reinterpret_cast<const uint32_t*>(&h);
+          } else {
+            const __half2 h = __floats2half2_rn(a, b);
+            v[j] = *reinterpret_cast<const uint32_t*>(&h);
+          }
         }
         {
           float a, b;
@@ -722,7 +777,7 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
         if (m0 != -INFINITY) l_row += l0 * ex2(m0 - m_fin);
         if (m1 != -INFINITY) l_row += l1 * ex2(m1 - m_fin);
       }
-      const float lse = l_row > 0.f ? (m_fin - kPShift + log2f(l_row)) * kLn2 : -INFINITY;
+      const float lse = l_row > 0.f ? (m_fin - C::kPShift + log2f(l_row)) * kLn2 : -INFINITY;
       const float inv = l_row > 0.f ? 1.f / l_row : 0.f;
       const size_t grow = (size_t)it.q_start * H + row0 + q;
       if (row_ok && hh == 0 && grp == 0) {
@@ -795,7 +850,32 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
     const uint32_t r_row = swizzled_row(smem_u32(sm) + OFF_K + grp * kKStage + 8 * kKChunk, lane);
     const uint32_t v_row = swizzled_row(smem_u32(sm) + OFF_V + grp * kVStage + vc * kVChunk,
                                         kHalf * (in_half ? rank : rank ^ 1) + lane);
+    // bf16: the first warp of a group passes a tile's K and V on and clears the V
+    // rows that are not in use (their K only makes scores that the mask replaces).
+    auto pass_tile = [&]() -> bool {
+      if (k != 0) return true;
+      const uint32_t use = g >> 1;
+      if (!wait_bar(c, STG_FULL0 + grp, use & 1)) return false;
+      const uint32_t m0 = row_mask[2 * grp], m1 = row_mask[2 * grp + 1];  // (before K goes on: see the copies)
+      __syncwarp();
+      if (lane < 3) arrive_leader(c, K_FULL0 + 3 * grp + lane, 1);
+      if (!wait_bar(c, STG_EMPTY0 + grp, use & 1)) return false;
+      if ((m0 & m1) != 0xffffffffu) {
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          if (((h ? m1 : m0) >> lane) & 1u) continue;
+          const uint32_t v = smem_u32(sm) + OFF_V + grp * kVStage + (kHalf * h + lane) * 128;
+#pragma unroll 1
+          for (int e = 0; e < 32; ++e) st_shared_v4(v + (e >> 3) * kVChunk + (e & 7) * 16, make_uint4(0, 0, 0, 0));
+        }
+        fence_proxy_async_smem();
+      }
+      __syncwarp();
+      if (lane == 0) arrive_leader(c, V_FULL0 + grp, 1);
+      return true;
+    };
     auto convert_tile = [&]() -> bool {
+      if constexpr (C::kTma) return pass_tile();
       const uint32_t s = grp;
       if (!wait_bar(c, STG_FULL0 + s, (g >> 1) & 1)) return false;
       const unsigned char* stg = sm + C::OFF_STG + s * C::kStage;
@@ -903,7 +983,7 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
 #pragma unroll 2
       for (int r = 0; r < 4; ++r) {
         int e = 0;
-        if (!p.q_fp8) {
+        if (!p.q_fp8 && !C::kTma) {
           const uint4 a = unit_of(q0 + r, lane), b = unit_of(q0 + r, 32 + lane),
                       d = unit_of(q0 + r, 64 + (lane & 7));
           uint32_t mb = __vmaxu2(__vmaxu2(max_bits(a), max_bits(b)), max_bits(d));
@@ -925,7 +1005,8 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws) {
     auto load_query = [&](const WorkItem& it, int n) -> bool {
       const long long q0 = first_row(it);
       const float* scales = qscale + (n & 3) * kCtaRows;
-      auto as_f16 = [&](const uint4 x, float up) {
+      auto as_f16 = [&](const uint4 x, float up) {  // (as bf16 for bf16 MMAs)
+        if constexpr (C::kTma) return p.q_fp8 ? e4m3x8_to_bf16(make_uint2(x.x, x.y)) : x;
         return p.q_fp8 ? e4m3x8_to_f16(make_uint2(x.x, x.y)) : bf16x8_to_f16(x, up);
       };
       const int quad = warp & 3, row = (32 * quad + lane) & 63, part = w >> 2;
@@ -1027,23 +1108,48 @@ cudaError_t setup_one(int sm_count, int* n_pairs) {
   return cudaSuccess;
 }
 
+// The bf16 cache's rows, boxes of 64 dims x 32 rows in the 128B-swizzled layout.
+bool encode_rows(CUtensorMap* map, const Problem& p) {
+  static PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+    cudaDriverEntryPointQueryResult q;
+    void* ptr = nullptr;
+    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
+                                                     &q) == cudaSuccess &&
+                    q == cudaDriverEntryPointSuccess;
+    return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr) : nullptr;
+  }();
+  if (!encode) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)kQkDim, (cuuint64_t)p.num_pages * p.page_size};
+  cuuint64_t strides[1] = {2 * kQkDim};
+  cuuint32_t box[2] = {64, kHalf}, step[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p.kv_cache), dims, strides, box,
+                step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int kCache>
 cudaError_t launch_one(const Problem& p, const Layout& lay, void* ws, cudaStream_t stream) {
+  CUtensorMap map = {};
+  if (Cfg<kCache>::kTma && !encode_rows(&map, p)) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   const cudaLaunchConfig_t cfg = pair_launch(lay.n_ctas, Cfg<kCache>::kSmemBytes, stream, &attr);
-  return cudaLaunchKernelEx(&cfg, decode_pair_kernel<kCache>, p, lay, static_cast<char*>(ws));
+  return cudaLaunchKernelEx(&cfg, decode_pair_kernel<kCache>, p, lay, static_cast<char*>(ws), map);
 }
 
 }  // namespace
 
 cudaError_t decode_pair_setup(int kv_dtype, int sm_count, int* n_pairs) {
-  return kv_dtype == 2 ? setup_one<kFp4>(sm_count, n_pairs) : setup_one<kE4m3>(sm_count, n_pairs);
+  return kv_dtype == 2   ? setup_one<kFp4>(sm_count, n_pairs)
+         : kv_dtype == 1 ? setup_one<kE4m3>(sm_count, n_pairs)
+                         : setup_one<kBf16>(sm_count, n_pairs);
 }
 
 cudaError_t launch_decode_pair(const Problem& p, const Layout& lay, void* ws, cudaStream_t stream) {
-  return p.kv_dtype == 2 ? launch_one<kFp4>(p, lay, ws, stream) : launch_one<kE4m3>(p, lay, ws, stream);
+  return p.kv_dtype == 2   ? launch_one<kFp4>(p, lay, ws, stream)
+         : p.kv_dtype == 1 ? launch_one<kE4m3>(p, lay, ws, stream)
+                           : launch_one<kBf16>(p, lay, ws, stream);
 }
 
 }  // namespace mla

@@ -50,9 +50,6 @@
 // (14-21) widen each staged e4m3 tile to bf16 in shared memory (exact; the
 // k_scale lives in bmm1/bmm2), and the bf16 ring is 3 deep beside a 2-deep
 // e4m3 staging ring.
-// Under a sliding window (bf16 cache; a separate instantiation, so that the others
-// keep their code) an item's KV rows are virtual ones: the sinks' tiles, then the tiles from
-// the earliest window on; rows outside a query row's own window are masked.
 // Under sparse top-k selection (a separate instantiation, two warps more) a
 // work item is one token's H query rows and its KV tiles are 64 entries of
 // the token's position list: warp 0 and the two extra warps gather the listed
@@ -223,20 +220,6 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
 __device__ __forceinline__ int n_tiles_of(const WorkItem& it) {
   return (it.kv_end - it.kv_begin + kTile - 1) / kTile;
 }
-
-// Sliding window: the rows that an item's virtual rows stand for (see
-// window_skip), and which of them some query row of the request sees.  A page
-// without one is not read (the caller may have given it away).
-struct WindowWalk {
-  int sink_end, skip, sinks, low;  // low: first row of the earliest window
-  __device__ WindowWalk(const Problem& p, const WorkItem& it)
-      : sink_end(window_sink_rows(p.sinks)),
-        skip(window_skip(p.window, p.sinks, p.causal, it.seq_len, it.q_len)),
-        sinks(p.sinks),
-        low((p.causal ? it.seq_len - it.q_len : it.seq_len - 1) - p.window + 1) {}
-  __device__ int row(int v) const { return v < sink_end ? v : v + skip; }
-  __device__ bool seen(int first, int last) const { return last >= low || first < sinks; }
-};
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -527,13 +510,12 @@ out:
   }
 }
 
-template <bool kFp8, bool kSparse, bool kF8, bool kWindow>
+template <bool kFp8, bool kSparse, bool kF8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8, kSparse, kF8>::kThreads, 1)
 decode_sm103_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
                     const __grid_constant__ CUtensorMap tm_q_rope,
                     const __grid_constant__ CUtensorMap tm_kv,
                     const __grid_constant__ CUtensorMap tm_kv_rope) {
-  static_assert(!(kWindow && kSparse), "a position list has no window");
   using C = Cfg<kFp8, kSparse, kF8>;
   constexpr int kStages = C::kStages;
   extern __shared__ unsigned char smem_raw[];
@@ -634,21 +616,8 @@ decode_sm103_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
       // a page boundary); only the pages the item's rows touch are read
       const int* bt = p.block_tables + (size_t)it.b * p.max_pages + it.kv_begin / ps;
       const int n_pages = (it.kv_end - it.kv_begin + ps - 1) / ps;
-      // the page of virtual slot i of the item; -1 past its end.  With a window,
-      // kUnseen for a page that no query row sees a row of
-      constexpr int kUnseen = INT_MIN;
-      auto page_at = [&](int i) -> int {
-        if constexpr (kWindow) {
-          if (i >= n_pages) return -1;
-          const WindowWalk walk(p, it);
-          const int r = walk.row(it.kv_begin + i * ps);
-          return walk.seen(r, r + ps - 1) ? bt[r / ps - it.kv_begin / ps] : kUnseen;
-        } else {
-          return i < n_pages ? bt[i] : -1;
-        }
-      };
-      int cur = page_at(lane);
-      int nxt = page_at(32 + lane);
+      int cur = lane < n_pages ? bt[lane] : -1;
+      int nxt = 32 + lane < n_pages ? bt[32 + lane] : -1;
       const bool q_ok = lane == 0 ? wait_bar(c, Q_FREE, (n_item & 1) ^ 1) : false;
       if (!__shfl_sync(0xffffffffu, q_ok, 0)) goto done_producer;
       ++n_item;
@@ -667,7 +636,8 @@ decode_sm103_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
         const int slot0 = t * npg;  // never straddles a batch: npg divides 32
         if (slot0 > 0 && (slot0 & 31) == 0) {
           cur = nxt;
-          nxt = page_at(slot0 + 32 + lane);
+          const int i = slot0 + 32 + lane;
+          nxt = i < n_pages ? bt[i] : -1;
         }
         int pages[2];
         pages[0] = __shfl_sync(0xffffffffu, cur, slot0 & 31);
@@ -682,7 +652,7 @@ decode_sm103_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
           const int j0 = it.kv_begin + t * kTile;
           uint32_t bytes = 0;
           for (int pg = 0; pg < npg; ++pg) {
-            if (j0 + pg * ps >= it.kv_end || (kWindow && pages[pg] == kUnseen)) {
+            if (j0 + pg * ps >= it.kv_end) {
               pages[pg] = -1;
               continue;
             }
@@ -924,18 +894,8 @@ decode_sm103_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
       const int first_qi = row0 / H;
       const int clean_end =
           sparse ? it.kv_begin
-                 : min(kWindow ? INT_MAX : it.kv_end,
+                 : min(it.kv_end,
                        p.causal ? causal_last(it.mask_base, first_qi, W) + 1 : it.seq_len);
-      // sliding window: virtual rows past the sinks' tiles are `skip` rows further
-      // on; from clean_low on a row is inside every query row's window (the rest
-      // is worked out where a tile needs it: registers are short here)
-      const int skip =
-          kWindow ? window_skip(p.window, p.sinks, p.causal, it.seq_len, it.q_len) : 0;
-      int clean_low = INT_MIN;
-      if constexpr (kWindow)
-        clean_low =
-            (p.causal ? it.mask_base + (row0 + min(R, rows_total - row0) - 1) / H : it.seq_len - 1) -
-            p.window + 1;
       const uint32_t g_last = g + (uint32_t)nt - 1;
       // (l, m) hand-off slot of this item and the phase of its barrier: only
       // items of two or more tiles (both groups take part) count
@@ -995,14 +955,10 @@ decode_sm103_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
         if (lane == 0) mbar_arrive_cluster_relaxed(xfree_peer0 + 8u * sb);
         // mask, then the row maximum of the tile (log2 units)
         const int j0 = it.kv_begin + t * kTile;
-        // with a window j0 is a virtual row
-        const int jr = kWindow && j0 >= window_sink_rows(p.sinks) ? j0 + skip : j0;
-        const int c0 = jr + 32 * hh;  // KV index of sv[0]
+        const int c0 = j0 + 32 * hh;  // KV index of sv[0]
         // tiles with masked columns are scaled before the -inf mask goes in,
         // so that bmm1 = 0 never multiplies -inf (the same for the whole tile)
-        const bool pre_scaled =
-            jr + kTile > clean_end ||
-            (kWindow && (j0 + kTile > it.kv_end || (jr < clean_low && jr + kTile > p.sinks)));
+        const bool pre_scaled = j0 + kTile > clean_end;
         const float sc = pre_scaled ? 1.f : scale;  // what the scores still need
         uint32_t usable = 0xffffffffu;              // of this thread's 32 columns
         if (sparse) {
@@ -1023,10 +979,8 @@ decode_sm103_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
               const int col = c0 + j;
-              const bool in_range = kWindow ? (col - jr + j0 < it.kv_end &&
-                                               (col > last - p.window || col < p.sinks))
-                                            : col < it.kv_end;
-              sv[j] = (col <= last && in_range && ((usable >> j) & 1u)) ? sv[j] * scale : -INFINITY;
+              sv[j] = (col <= last && col < it.kv_end && ((usable >> j) & 1u)) ? sv[j] * scale
+                                                                                : -INFINITY;
               tm[j & 3] = fmaxf(tm[j & 3], sv[j]);
             }
           }
@@ -1069,23 +1023,8 @@ decode_sm103_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
 #pragma unroll
           for (int j = 0; j < 32; ++j) sv[j] = 0.f;
         }
-        // zero V rows past the end of the KV range (last tile of the item); with a
-        // window also those that no query row sees
+        // zero V rows past the end of the KV range (last tile of the item)
         const int valid = it.kv_end - j0;
-        if (kWindow && pre_scaled) {
-          const int low = (p.causal ? it.mask_base : it.seq_len - 1) - p.window + 1;
-          unsigned char* stage = sm + OFF_KV + (g % kStages) * C::kStage;
-          constexpr int kChunks = kF8 ? 2 : kLatChunks;
-          constexpr uint32_t kChunkBytes = kF8 ? kChunk8 : kChunkKV;
-          // rows [sinks, low) of the tile
-          const int z0 = max(p.sinks - jr, 0), z1 = min(low - jr, kTile);
-#pragma unroll 1
-          for (int e = z0 * kChunks * 8 + g_tid; e < z1 * kChunks * 8; e += kGroupWarps * 32) {
-            const int row = e / (8 * kChunks), ch = (e / 8) % kChunks, u = e % 8;
-            *reinterpret_cast<uint4*>(stage + ch * kChunkBytes + row * 128 + u * 16) =
-                make_uint4(0, 0, 0, 0);
-          }
-        }
         if (valid < kTile) {
           unsigned char* stage = sm + OFF_KV + (g % kStages) * C::kStage;
           constexpr int kChunks = kF8 ? 2 : kLatChunks;  // 128-byte rows per KV row
@@ -1521,10 +1460,10 @@ bool encode_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int e
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool kFp8, bool kSparse, bool kF8 = false, bool kWindow = false>
+template <bool kFp8, bool kSparse, bool kF8 = false>
 cudaError_t setup_one(int sm_count, int* n_pairs) {
   using C = Cfg<kFp8, kSparse, kF8>;
-  auto kernel = decode_sm103_kernel<kFp8, kSparse, kF8, kWindow>;
+  auto kernel = decode_sm103_kernel<kFp8, kSparse, kF8>;
   cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
@@ -1548,8 +1487,8 @@ cudaError_t setup_one(int sm_count, int* n_pairs) {
 }
 
 // Launch as a programmatic dependent of the previous kernel in the stream.
-template <bool kFp8, bool kSparse, bool kF8, bool kWindow>
-cudaError_t launch_one(int grid, cudaStream_t stream, const Problem& p, const Layout& lay, char* ws,
+template <bool kFp8, bool kSparse, bool kF8 = false>
+cudaError_t launch_pdl(int grid, cudaStream_t stream, const Problem& p, const Layout& lay, char* ws,
                        const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c) {
   using C = Cfg<kFp8, kSparse, kF8>;
   cudaLaunchConfig_t cfg = {};
@@ -1562,24 +1501,12 @@ cudaError_t launch_one(int grid, cudaStream_t stream, const Problem& p, const La
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_sm103_kernel<kFp8, kSparse, kF8, kWindow>, p, lay, ws, a, b, c);
-}
-template <bool kFp8, bool kSparse, bool kF8 = false>
-cudaError_t launch_pdl(int grid, cudaStream_t stream, const Problem& p, const Layout& lay, char* ws,
-                       const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c) {
-  if constexpr (!kSparse && !kFp8 && !kF8)
-    if (p.window > 0)
-      return launch_one<kFp8, false, kF8, true>(grid, stream, p, lay, ws, a, b, c);
-  return launch_one<kFp8, kSparse, kF8, false>(grid, stream, p, lay, ws, a, b, c);
+  return cudaLaunchKernelEx(&cfg, decode_sm103_kernel<kFp8, kSparse, kF8>, p, lay, ws, a, b, c);
 }
 
 }  // namespace
 
-cudaError_t decode_sm103_setup(int kv_dtype, int sparse, int f8_mma, int window, int sm_count,
-                               int* n_pairs) {
-  if (window)  // an e4m3 cache with a window runs on the pair MMAs
-    return sparse || kv_dtype == 1 ? cudaErrorInvalidValue
-                                   : setup_one<false, false, false, true>(sm_count, n_pairs);
+cudaError_t decode_sm103_setup(int kv_dtype, int sparse, int f8_mma, int sm_count, int* n_pairs) {
   if (kv_dtype == 1 && f8_mma && !sparse) return setup_one<false, false, true>(sm_count, n_pairs);
   if (kv_dtype == 1)
     return sparse ? setup_one<true, true>(sm_count, n_pairs)
