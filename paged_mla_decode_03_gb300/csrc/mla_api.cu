@@ -56,9 +56,10 @@ int effective_window(const mla_decode_params& p) {
   return p.window > 0 && p.window < p.max_seq_len ? p.window : 0;
 }
 
-// The f16 MMAs across CTA pairs (mla_decode_pair.cu): a 4-bit cache, and an e4m3
-// one with a window (32 x 4 x 128 heads, window 4096: 303 us a call on the FP8
-// MMAs, whose tiles exchange scores between the CTAs).
+// The MMAs across CTA pairs (mla_decode_pair.cu): a 4-bit cache, and every cache
+// with a window.  An e4m3 one (32 x 4 x 128 heads, window 4096) takes 189 us a call
+// there and took 303 on the FP8 MMAs, whose tiles exchange scores between the CTAs; a
+// bf16 one (64 x 128 heads, window 1024) 49 and 79.
 bool uses_pair_mma(const mla_decode_params& p) {
   return p.kv_dtype == MLA_KV_FP4_E2M1 || effective_window(p) > 0;
 }
@@ -206,7 +207,7 @@ int mla_decode_plan(const mla_decode_params* params, mla_plan_t** plan, size_t* 
   const int rows_per_group = p.sparse_top_k > 0 ? p.num_heads : 128;
   // No run of this plan keeps more workers busy than its largest possible
   // work allows (the partitioner gives a busy worker at least kMinUnits units
-  // of kOverheadTiles + tiles per row group), so a small plan launches a
+  // of overhead + tiles per row group), so a small plan launches a
   // smaller grid; the work list is the same as with every pair.
   {
     const long long g_max = ceil_div((long long)p.max_seq_len_q * p.num_heads, rows_per_group);
@@ -218,7 +219,8 @@ int mla_decode_plan(const mla_decode_params* params, mla_plan_t** plan, size_t* 
     if (effective_window(p) > 0)  // whole tiles of the sinks, and of the q_len windows
       kv_rows = std::min(kv_rows, (long long)mla::window_sink_rows(p.sinks) + p.window +
                                       p.max_seq_len_q + mla::kKvTile);
-    const long long units = std::max(groups, 1LL) * (mla::kOverheadTiles + ceil_div(kv_rows, mla::kKvTile));
+    const long long overhead = uses_pair_mma(p) ? mla::kOverheadTilesPair : mla::kOverheadTiles;
+    const long long units = std::max(groups, 1LL) * (overhead + ceil_div(kv_rows, mla::kKvTile));
     n_pairs = (int)std::max(1LL, std::min<long long>(n_pairs, units / mla::kMinUnits));
   }
   const int rc = make_layout(p, n_pairs, 2 * n_pairs, rows_per_group, &pl->lay);

@@ -370,14 +370,15 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
       const Walk walk(p, it);
       const int* bt = p.block_tables + (size_t)it.b * p.max_pages;
       const int n_pages = (it.kv_end - it.kv_begin + ps - 1) >> ps_shift;
-      // a page's id, -1 for one that is not read
+      // a page's id, -1 for one that is not read; a bad id's rows are zeros (TMA:
+      // the rows past the cache's end, which the copy fills with zeros)
       auto page_at = [&](int i) -> int {
         const int r = walk.row(it.kv_begin + i * ps);
         if (i >= n_pages || !walk.seen(r, r + ps - 1)) return -1;
         const int id = bt[r >> ps_shift];
         if (id >= 0 && (long long)id < p.num_pages) return id;
         if (bulk) atomicOr(c.status, kStatusPage);
-        return -1;
+        return C::kTma ? (int)p.num_pages : -1;
       };
       int cur = page_at(lane), nxt = page_at(32 + lane);
       for (int t = 0; t < nt; ++t, ++g) {
@@ -430,7 +431,7 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
             for (int a = t == 0 ? 2 : kAhead; a <= kAhead; ++a) {
               const int i = (t + a) * npg + (npg == 2 ? rank : 0);
               const int from = __shfl_sync(0xffffffffu, (i >> 5) == (slot0 >> 5) ? cur : nxt, i & 31);
-              if (t + a < nt && lane == 0 && from >= 0)
+              if (t + a < nt && lane == 0 && from >= 0 && from < p.num_pages)
                 bulk_prefetch_l2(cache + (size_t)from * page_bytes + (npg == 2 ? 0 : kHalf * rank) * C::kCodeBytes,
                                  kHalf * C::kCodeBytes);
             }

@@ -144,7 +144,7 @@ class Case:
             self._ksum = float(cache_values(self.cache).abs().sum(-1).nan_to_num(0).max())
         return self.query[t].double().abs().amax(-1) * self._ksum * self.bmm1
 
-    def check(self, p_bits=11, p_floor=2.0 ** -32, what=""):
+    def check(self, p_bits=11, p_floor=2.0 ** -32, what="", status=0):
         """Every row against the reference.  The output's rounding to bf16 is off by
         2^-8 of it; a split request's partials, rounded to bf16 before they are
         joined, by 2^-8 of A = sum p |v|; P, rounded to ``p_bits`` + 1 bits, by
@@ -156,7 +156,7 @@ class Case:
         times sum |k|, 2^-17 bmm1 max |q| sum |k| <= 2^-17 bmm1 qk.  All outputs together
         are within 1e-2 in 2-norm (roundings of 2^-8 average out far below)."""
         got, want = [], []
-        assert self.status() == 0, f"{what}: status {self.status()}"
+        assert self.status() == status, f"{what}: status {self.status()}"
         out, lse = self.out.double(), self.lse.double()
         for t, o, e, (a, d, v) in self.reference():
             d = d * 2.0 ** -18 + 2e-6 + (self.qk(t) * 2.0 ** -17 if self.split_q else 0.0)

@@ -99,3 +99,16 @@ def test_host_entry_takes_a_window():
                     staging=staging, workspace=c.workspace, h_lse=h_lse, bmm1_scale=c.bmm1, bmm2_scale=c.bmm2)
     torch.cuda.synchronize()
     assert torch.equal(h_out, c.out.cpu()) and torch.equal(h_lse, c.lse.cpu())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "fp4"])
+@pytest.mark.parametrize("ps,bad", [(64, -1), (32, 2 ** 31 - 1), (32, None)])
+def test_a_bad_page_in_a_window_is_flagged_and_reads_as_zeros(kind, ps, bad):
+    c = Case(kind, ps, [900, 130], [1, 1], 128, window=600, sinks=2, seed=6)
+    at = 800 // ps
+    page = int(c.bt_host[0, at])
+    c.tables[0, at] = c.cache.shape[0] if bad is None else bad  # None: one past the last
+    c.run()
+    c.cache[page].zero_()
+    c.check(status=16, **P[kind])
