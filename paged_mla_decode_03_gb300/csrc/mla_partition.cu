@@ -570,16 +570,11 @@ partition_warp_kernel(Problem p, Layout lay, char* __restrict__ ws) {
   const int R = lay.rows_per_group;
   const int H = p.num_heads;
   const bool sparse = p.sparse_k > 0;
-  const bool pair = pair_mma(p);
-  const long long c0 = pair ? kOverheadTilesPair : kOverheadTiles;
-  auto kv_rows = [&](int L, int q) {
-    return sparse ? p.sparse_k : L - window_skip(p.window, p.sinks, p.causal, L, q);
-  };
-  auto tiles_of = [&](int L, int q) { return (kv_rows(L, q) + kKvTile - 1) / kKvTile; };
+  auto tiles_of = [&](int L) { return ((sparse ? p.sparse_k : L) + kKvTile - 1) / kKvTile; };
 
   // 1. Per-request lengths (clamped and flagged as in the block kernel) and
   //    the request's number of row groups, over the lane's run of requests.
-  int status = 0, g_min = 1 << 30, g_max = 0, my_groups = 0, t_max = 0;
+  int status = 0, g_min = 1 << 30, g_max = 0, my_groups = 0;
   long long my_cost = 0;
   const Run rb(B, lane);
   for (int b = rb.lo; b < rb.hi; ++b) {
@@ -609,10 +604,9 @@ partition_warp_kernel(Problem p, Layout lay, char* __restrict__ ws) {
     if (gc > 0) {
       g_min = min(g_min, gc);
       g_max = max(g_max, gc);
-      t_max = max(t_max, tiles_of(L, q));
     }
     my_groups += gc;
-    my_cost += (long long)gc * (c0 + tiles_of(L, q));
+    my_cost += (long long)gc * (kOverheadTiles + tiles_of(L));
   }
   status = warp_or(status);
   g_min = warp_min(g_min);
@@ -643,14 +637,14 @@ partition_warp_kernel(Problem p, Layout lay, char* __restrict__ ws) {
   for (int b = rb.lo; b < rb.hi; ++b) {
     const int gb = sh.gbase[b];
     const int ge = (b + 1 < B) ? sh.gbase[b + 1] : n_groups;
-    const int T = tiles_of(sh.len[b], sh.q[b]);
+    const int T = tiles_of(sh.len[b]);
     for (int g = gb; g < ge && g < n_groups; ++g) {
       const int k = g - gb;
       const int slot = lanes > 1 ? k * n_req_groups + gb / G : g;
       if (slot < 0 || slot >= n_groups) continue;  // unreachable: slots are a permutation
       sh.g_req[slot] = b;
       sh.g_k[slot] = k;
-      sh.g_start[slot] = c0 + T;
+      sh.g_start[slot] = kOverheadTiles + T;
     }
   }
   __syncwarp();
@@ -673,13 +667,7 @@ partition_warp_kernel(Problem p, Layout lay, char* __restrict__ ws) {
   bd.nl = n_eff / lanes;
   bd.WL = W / lanes;
   bd.table = nullptr;
-  bd.overhead = c0;
-  {
-    // uncut: worker q's range starts where group q does
-    const bool uncut = partition_uncut(p.window > 0 || pair, n_groups, n, c0 + warp_max(t_max), W);
-    for (long long q = lane; q <= n; q += 32)
-      sh.bound[q] = !uncut ? bd.boundary_of(q) : q < n_groups ? sh.g_start[q] : W;
-  }
+  for (long long q = lane; q <= n; q += 32) sh.bound[q] = bd.boundary_of(q);
   __syncwarp();
   bd.table = sh.bound;
 
@@ -687,8 +675,8 @@ partition_warp_kernel(Problem p, Layout lay, char* __restrict__ ws) {
   //    slot and combine entry bases of every group.
   int s_items = 0, s_slot = 0, s_comb = 0;
   for (int g = rg.lo; g < rg.hi; ++g) {
-    const int T = tiles_of(sh.len[sh.g_req[g]], sh.q[sh.g_req[g]]);
-    const long long S = sh.g_start[g], c = c0 + T;
+    const int T = tiles_of(sh.len[sh.g_req[g]]);
+    const long long S = sh.g_start[g], c = kOverheadTiles + T;
     int nch = 1;
     if (W > 0) {
       const long long p_lo = bd.first_above(S);
@@ -733,12 +721,12 @@ partition_warp_kernel(Problem p, Layout lay, char* __restrict__ ws) {
     for (int g = rg.lo; g < rg.hi; ++g) {
       const int b = sh.g_req[g];
       const int L = sh.len[b];
-      const int KV = kv_rows(L, sh.q[b]);
-      const int T = tiles_of(L, sh.q[b]);
-      const long long S = sh.g_start[g], c = c0 + T;
+      const int KV = sparse ? p.sparse_k : L;
+      const int T = tiles_of(L);
+      const long long S = sh.g_start[g], c = kOverheadTiles + T;
       const int nch = sh.g_nch[g];
       int k = 0, prev = 0;
-      long long start_unit = S + c0;
+      long long start_unit = S + kOverheadTiles;
       auto emit = [&](int t0, int t1, long long unit) {
         const int idx = sh.g_item[g] + k;
         ++k;
@@ -764,7 +752,7 @@ partition_warp_kernel(Problem p, Layout lay, char* __restrict__ ws) {
           const int t = cut_tile(bd, q, S, T);
           if (t > prev && t < T) {
             emit(prev, t, start_unit);
-            start_unit = S + c0 + t;
+            start_unit = S + kOverheadTiles + t;
             prev = t;
           }
         }
@@ -806,13 +794,18 @@ partition_warp_kernel(Problem p, Layout lay, char* __restrict__ ws) {
   }
 }
 
+// mla_partition_pair.cu
+bool partition_pair_picked(const Problem& p, const Layout& lay);
+cudaError_t launch_partition_pair(const Problem& p, const Layout& lay, void* ws, cudaStream_t stream);
+
 cudaError_t launch_partition(const Problem& p, const Layout& lay, void* ws, cudaStream_t stream) {
   const size_t smem = lay.scratch_in_smem ? lay.scratch_bytes : 0;
   long long need = std::max<long long>(std::max<long long>(p.batch, lay.max_groups),
                                        (long long)lay.n_workers + 1);
   const int threads = (int)std::min<long long>(kMaxThreads,
                                                 std::max<long long>(128, (need + 31) / 32 * 32));
-  if (partition_warp_picked(p, lay))
+  if (partition_pair_picked(p, lay)) return launch_partition_pair(p, lay, ws, stream);
+  if (!pair_mma(p) && partition_warp_picked(p, lay))
     partition_warp_kernel<<<1, 32, 0, stream>>>(p, lay, static_cast<char*>(ws));
   else
     partition_kernel<<<1, threads, smem, stream>>>(p, lay, static_cast<char*>(ws));

@@ -1,12 +1,29 @@
-// Runs a partition kernel's source (the block or the single-warp form) on host
-// threads for plans with a sliding window or a 4-bit cache, one problem per text
-// file, and writes the work list.  Built by tests/test_window_partition.py from
+// Runs a partition kernel's source (the block form, or the one with a thread for
+// each request, group and boundary) on host threads for plans with a sliding window
+// or a 4-bit cache, one problem per text file, and writes the work list.  Built by tests/test_window_partition.py from
 // generated copies of the kernel source and of the plan's layout arithmetic.
 #include <cstdio>
 #include <deque>
 #include <string>
 
 #include "partition_host.inc"
+
+// more host stand-ins, of what the second form uses
+template <typename T, typename F>
+T host_reduce(T v, F f) {
+  T r = host_exchange(v, 0);
+  for (int l = 1; l < 32; ++l) r = f(r, host_exchange(v, l));
+  return r;
+}
+inline int __reduce_min_sync(unsigned, int v) { return host_reduce(v, [](int a, int b) { return min(a, b); }); }
+inline int __reduce_max_sync(unsigned, int v) { return host_reduce(v, [](int a, int b) { return max(a, b); }); }
+inline unsigned __reduce_add_sync(unsigned, unsigned v) { return host_reduce(v, [](unsigned a, unsigned b) { return a + b; }); }
+inline unsigned __reduce_or_sync(unsigned, unsigned v) { return host_reduce(v, [](unsigned a, unsigned b) { return a | b; }); }
+inline unsigned __ballot_sync(unsigned, bool on) {
+  return __reduce_or_sync(0xffffffffu, on ? 1u << (threadIdx.x & 31) : 0u);
+}
+inline int __popc(unsigned v) { return __builtin_popcount(v); }
+#include "partition_pair_host.inc"
 #include "mla_decode.h"
 
 namespace {
@@ -18,7 +35,7 @@ enum { MLA_OK = 0, MLA_ERR_UNSUPPORTED = -2 };
 
 int main(int argc, char** argv) {
   if (argc != 4) return 2;
-  const bool warp_kernel = std::string(argv[3]) == "warp";
+  const bool pair_kernel = std::string(argv[3]) == "pair";
   FILE* f = std::fopen(argv[1], "r");
   if (!f) return 2;
   int B, H, packed, max_q, max_seq_len, n_workers, causal, window, sinks, kv_dtype;
@@ -62,9 +79,9 @@ int main(int argc, char** argv) {
   p.qo_indptr = packed ? qo.data() : nullptr;
   p.window = window;
   p.sinks = sinks;
-  if (warp_kernel && !mla::partition_warp_fits(p, lay)) return 4;
+  if (pair_kernel && !mla::partition_pair_fits(p, lay)) return 4;
   const long long need = std::max<long long>(std::max<long long>(B, lay.max_groups), (long long)lay.n_workers + 1);
-  const int threads = warp_kernel ? 32 : (int)std::min<long long>(1024, std::max<long long>(128, (need + 31) / 32 * 32));
+  const int threads = pair_kernel ? mla::partition_pair_threads(p, lay) : (int)std::min<long long>(1024, std::max<long long>(128, (need + 31) / 32 * 32));
   blockDim.x = threads;
   std::barrier<> block_bar(threads);
   g_block_barrier = &block_bar;
@@ -79,8 +96,8 @@ int main(int argc, char** argv) {
   for (int t = 0; t < threads; ++t)
     th.emplace_back([&, t] {
       threadIdx.x = t;
-      if (warp_kernel)
-        mla::partition_warp_kernel(p, lay, reinterpret_cast<char*>(ws.data()));
+      if (pair_kernel)
+        mla::partition_pair_kernel(p, lay, reinterpret_cast<char*>(ws.data()));
       else
         mla::partition_kernel(p, lay, reinterpret_cast<char*>(ws.data()));
     });

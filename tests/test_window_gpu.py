@@ -110,5 +110,6 @@ def test_a_bad_page_in_a_window_is_flagged_and_reads_as_zeros(kind, ps, bad):
     page = int(c.bt_host[0, at])
     c.tables[0, at] = c.cache.shape[0] if bad is None else bad  # None: one past the last
     c.run()
+    c.tables[0, at] = page  # the reference reads a page of zeros there
     c.cache[page].zero_()
     c.check(status=16, **P[kind])

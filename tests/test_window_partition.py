@@ -29,6 +29,10 @@ def runner(tmp_path_factory):
     src = src.replace("extern __shared__ __align__(16) unsigned char scratch_smem[];",
                       "unsigned char* scratch_smem = g_scratch;")
     (out / "partition_host.inc").write_text(src[:src.index("cudaError_t launch_partition(")] + "}  // namespace mla\n")
+    src = open(os.path.join(CSRC, "mla_partition_pair.cu")).read()
+    src = src.replace('#include "mla_common.cuh"\n#include "sm100_ptx.cuh"\n', "")
+    src = src.replace("ptx::pdl_launch_dependents();", "")
+    (out / "partition_pair_host.inc").write_text(src[:src.index("bool partition_pair_picked(")] + "}  // namespace mla\n")
     api = open(os.path.join(CSRC, "mla_api.cu")).read()
     (out / "make_layout.inc").write_text(_function_text(api, "int make_layout(") + "\n")
     exe = out / "window_partition"
@@ -49,20 +53,30 @@ def _rows_of(begin, end, skip, sinks):
     return np.where(v < s, v, v + skip)
 
 
-def _check(runner, ls, qs, H, packed, causal, window, sinks, kv_dtype, n_workers, kernel):
+def _run(runner, ls, qo, max_q, max_len, H, packed, causal, window, sinks, kv_dtype, n_workers, kernel):
+    """The work list (head, items, worker ranges, combine entries), or None where the
+    kernel does not take the plan."""
     exe, out = runner
-    max_q = max(qs)
-    total = sum(qs)
-    qo = np.concatenate([[0], np.cumsum(qs)])
     with open(out / "in.txt", "w") as f:
-        f.write(f"{len(ls)} {H} {int(packed)} {max_q} {max(ls)} {n_workers} {int(causal)} {window} {sinks} "
-                f"{kv_dtype} {total}\n{' '.join(map(str, ls))}\n{' '.join(map(str, qo))}\n")
+        f.write(f"{len(ls)} {H} {int(packed)} {max_q} {max_len} {n_workers} {int(causal)} {window} {sinks} "
+                f"{kv_dtype} {qo[-1]}\n{' '.join(map(str, ls))}\n{' '.join(map(str, qo))}\n")
     r = subprocess.run([str(exe), str(out / "in.txt"), str(out / "out.txt"), kernel], capture_output=True, text=True,
                        env=dict(os.environ, ASAN_OPTIONS="detect_leaks=0:abort_on_error=1"), timeout=300)
-    if kernel == "warp" and r.returncode == 4:
-        return False
+    if kernel == "pair" and r.returncode == 4:
+        return None
     assert r.returncode == 0, (r.returncode, r.stderr[-3000:])
-    head, items, ranges, combine = [[int(x) for x in line.split()] for line in open(out / "out.txt").read().split("\n")[:4]]
+    return [[int(x) for x in line.split()] for line in open(out / "out.txt").read().split("\n")[:4]]
+
+
+def _check(runner, ls, qs, H, packed, causal, window, sinks, kv_dtype, n_workers, kernel):
+    qo = np.concatenate([[0], np.cumsum(qs)])
+    args = (runner, ls, qo, max(qs), max(ls), H, packed, causal, window, sinks, kv_dtype, n_workers)
+    got = _run(*args, kernel)
+    if got is None:
+        return False
+    if kernel == "pair":
+        assert got == _run(*args, "block")
+    head, items, ranges, combine = got
     status, n_items, n_combine, max_partials, max_combine = head
     assert status == 0 and n_combine <= max_combine
     items = [items[10 * i:10 * i + 10] for i in range(n_items)]
@@ -100,6 +114,7 @@ def _check(runner, ls, qs, H, packed, causal, window, sinks, kv_dtype, n_workers
                 slots += [it[4] for it in parts]
             costs.append((OVERHEAD + -(-end // TILE), len(parts)))
     assert not by_group
+    assert n_items == sum(n for _, n in costs) and n_combine == sum(n > 1 for _, n in costs)
     assert len(set(slots)) == len(slots) and all(0 <= s < max_partials for s in slots)
     # uncut where that costs the largest worker no more than kCutTiles tiles
     if len(costs) <= n_workers and max(c for c, _ in costs) <= sum(c for c, _ in costs) // n_workers + CUT:
@@ -114,7 +129,7 @@ def _check(runner, ls, qs, H, packed, causal, window, sinks, kv_dtype, n_workers
     return True
 
 
-@pytest.mark.parametrize("kernel", ["block", "warp"])
+@pytest.mark.parametrize("kernel", ["block", "pair"])
 @pytest.mark.parametrize("kv_dtype,window,sinks", [(0, 64, 0), (0, 1000, 4), (1, 130, 70), (2, 0, 0), (2, 33, 1)])
 def test_a_batch_of_equal_requests(runner, kernel, kv_dtype, window, sinks):
     assert _check(runner, [2000] * 64, [1] * 64, 128, False, True, window, sinks, kv_dtype, 76, kernel)
@@ -122,7 +137,7 @@ def test_a_batch_of_equal_requests(runner, kernel, kv_dtype, window, sinks):
     assert _check(runner, [1], [1], 16, False, True, window, sinks, kv_dtype, 5, kernel)
 
 
-@pytest.mark.parametrize("kernel", ["block", "warp"])
+@pytest.mark.parametrize("kernel", ["block", "pair"])
 @pytest.mark.parametrize("seed", range(16))
 def test_random_shapes(runner, kernel, seed):
     rng = np.random.default_rng(900 + seed)
@@ -136,3 +151,21 @@ def test_random_shapes(runner, kernel, seed):
     _check(runner, ls, qs, int(rng.choice([16, 32, 64, 128])), packed, bool(rng.integers(2)), window,
            int(rng.choice([0, 1, 64, 65, 500])) if window else 0, 2 if not window else int(rng.integers(3)),
            int(rng.integers(1, 77)), kernel)
+
+
+@pytest.mark.parametrize("seed", range(8))
+def test_bad_lengths_are_flagged_alike(runner, seed):
+    """Lengths out of the contract: both forms stay in bounds (the sanitizers look),
+    flag the same and leave the same list."""
+    rng = np.random.default_rng(70 + seed)
+    B = int(rng.integers(1, 40))
+    qs = rng.integers(1, 5, B)
+    ls = rng.integers(1, 500, B)
+    qo = np.concatenate([[0], np.cumsum(qs)])
+    qo[int(rng.integers(B + 1))] = int(rng.choice([-7, 0, qo[-1], 2 ** 30]))
+    qo[-1] = max(1, qo[-1])
+    ls[int(rng.integers(B))] = int(rng.choice([-5, 0, 10 ** 9]))
+    args = (runner, ls, qo, 4, 500, 128, True, True, 100, 3, 0, 20)
+    got = _run(*args, "pair")
+    assert got[0][0] & 3
+    assert got == _run(*args, "block")
