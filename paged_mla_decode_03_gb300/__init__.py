@@ -502,6 +502,10 @@ def decode(query: torch.Tensor, kv_cache: torch.Tensor, workspace_buffer: torch.
     q_dtype = "bf16" if query.dtype == torch.bfloat16 else "e4m3"
     kv_cache, kind = _cache_kind(kv_cache)
     kv_dtype = ("bf16", "e4m3", "fp4")[kind]
+    if (kind == KV_FP4_E2M1 or window) and not (
+            query.is_contiguous() and kv_cache.is_contiguous() and block_tables.is_contiguous()
+            and seq_lens.is_contiguous()):
+        raise ValueError("query, kv_cache, block_tables and seq_lens must be contiguous")
     packed = qo_indptr is not None
     H = int(query.shape[-2])
     B = int(seq_lens.shape[0])
@@ -615,9 +619,13 @@ def _is_int32(t: torch.Tensor, dev: int, shape) -> bool:
             and t.is_contiguous())
 
 
-def _is_bf16_rows(t: torch.Tensor, dev: int, shape) -> bool:
-    return (t.dtype is torch.bfloat16 and t.get_device() == dev and t.shape == shape
-            and (t.stride(-1) == 1 or t.numel() == 0))
+def _rows(name: str, t: torch.Tensor, dev: int, shape) -> Tuple[int, ...]:
+    """The strides of a bf16 tensor of that shape with a contiguous last dim."""
+    strides = t.stride()
+    if not (t.dtype is torch.bfloat16 and t.get_device() == dev and t.shape == shape
+            and (strides[-1] == 1 or t.numel() == 0)):
+        _refuse(name, t, "a bf16 tensor with a contiguous last dim", dev, shape)
+    return strides
 
 
 def _refuse(name: str, t, what: str, dev: int, shape) -> None:
@@ -627,12 +635,7 @@ def _refuse(name: str, t, what: str, dev: int, shape) -> None:
                      f"{t.dtype} {tuple(t.shape)} (strides {t.stride()}) on {t.device}")
 
 
-_INT32, _BF16_ROWS = "a contiguous int32 tensor", "a bf16 tensor with a contiguous last dim"
-
-
-def _outer(t: torch.Tensor, dim: int) -> int:
-    """Stride of an outer dim, 0 where it has one element (it is never applied)."""
-    return t.stride(dim) if t.shape[dim] > 1 else 0
+_INT32 = "a contiguous int32 tensor"
 
 
 def _stream_of(stream, dev: int) -> int:
@@ -755,12 +758,12 @@ def cache_append(latent: torch.Tensor, k_pe: torch.Tensor, kv_cache: torch.Tenso
         raise ValueError("latent must be a CUDA tensor [tokens, 512]")
     T = latent.shape[0]
     dev, key = _cache_call(kv_cache, block_tables, seq_lens, qo_indptr, q_len, T, status)
-    if not _is_bf16_rows(latent, dev, (T, 512)):
-        _refuse("latent", latent, _BF16_ROWS, dev, (T, 512))
-    if not _is_bf16_rows(k_pe, dev, (T, 64)):
-        _refuse("k_pe", k_pe, _BF16_ROWS, dev, (T, 64))
-    if norm_weight is not None and not _is_bf16_rows(norm_weight, dev, (512,)):
-        _refuse("norm_weight", norm_weight, _BF16_ROWS, dev, (512,))
+    lat_row = _rows("latent", latent, dev, (T, 512))[0]
+    pe_row = _rows("k_pe", k_pe, dev, (T, 64))[0]
+    w_ptr = None
+    if norm_weight is not None:
+        _rows("norm_weight", norm_weight, dev, (512,))
+        w_ptr = norm_weight.data_ptr()
     if not (rope_table.dtype is torch.float32 and rope_table.get_device() == dev
             and rope_table.dim() == 2 and rope_table.shape[1] == 64 and rope_table.is_contiguous()):
         _refuse("rope_table", rope_table, "a contiguous fp32 tensor", dev, ("positions", 64))
@@ -776,8 +779,7 @@ def cache_append(latent: torch.Tensor, k_pe: torch.Tensor, kv_cache: torch.Tenso
         if q_pe.dim() != 3:
             raise ValueError("q_pe must be [tokens, heads, 64]")
         H = q_pe.shape[1]
-        if not _is_bf16_rows(q_pe, dev, (T, H, 64)):
-            _refuse("q_pe", q_pe, _BF16_ROWS, dev, (T, H, 64))
+        p_token, p_head, _ = _rows("q_pe", q_pe, dev, (T, H, 64))
         if query is None:
             if q_nope is None:
                 raise ValueError("without q_nope, query must be given (its latent part stays)")
@@ -790,17 +792,17 @@ def cache_append(latent: torch.Tensor, k_pe: torch.Tensor, kv_cache: torch.Tenso
                 query.shape == (T, H, 576)
                 or (q_len is not None and query.shape == (key[0], q_len, H, 576))):
             _refuse("query", query, "a contiguous bf16 or float8_e4m3fn tensor", dev, (T, H, 576))
-        p_ptr, p_token, p_head = q_pe.data_ptr(), _outer(q_pe, 0), _outer(q_pe, 1)
-        q_ptr = query.data_ptr()
+        p_ptr, q_ptr = q_pe.data_ptr(), query.data_ptr()
         if q_nope is not None:
-            if not _is_bf16_rows(q_nope, dev, (T, H, 512)):
-                _refuse("q_nope", q_nope, _BF16_ROWS, dev, (T, H, 512))
-            n_ptr, n_token, n_head = q_nope.data_ptr(), _outer(q_nope, 0), _outer(q_nope, 1)
+            n_token, n_head, _ = _rows("q_nope", q_nope, dev, (T, H, 512))
+            n_ptr = q_nope.data_ptr()
     elif query is not None or q_nope is not None:
         raise ValueError("query and q_nope go with q_pe")
+    if T == 1:  # the stride of a dim of one element is any number, and never applied
+        lat_row = pe_row = n_token = p_token = 0
     rc = _call_on(
         dev, load_library().mla_cache_append, _params_of(*key, H, q_dtype), latent.data_ptr(),
-        _outer(latent, 0), k_pe.data_ptr(), _outer(k_pe, 0), _ptr(norm_weight), eps,
+        lat_row, k_pe.data_ptr(), pe_row, w_ptr, eps,
         rope_table.data_ptr(), rope_table.shape[0], style, _ptr(positions),
         block_tables.data_ptr(), seq_lens.data_ptr(), _ptr(qo_indptr), T, kv_scale,
         kv_cache.data_ptr(), n_ptr, n_token, n_head, p_ptr, p_token, p_head, q_scale, q_ptr,
@@ -831,7 +833,8 @@ def cache_gather(kv_cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: t
     dev, key = _cache_call(kv_cache, block_tables, seq_lens, qo_indptr, q_len, total_q, status)
     if out is None:
         out = torch.empty((total_q, HEAD_DIM_QK), dtype=torch.bfloat16, device=kv_cache.device)
-    elif not _is_bf16_rows(out, dev, (total_q, HEAD_DIM_QK)) or not out.is_contiguous():
+    elif not (out.dtype is torch.bfloat16 and out.get_device() == dev
+              and out.shape == (total_q, HEAD_DIM_QK) and out.is_contiguous()):
         _refuse("out", out, "a contiguous bf16 tensor", dev, (total_q, HEAD_DIM_QK))
     rc = _call_on(dev, load_library().mla_cache_gather, _params_of(*key, 0, 0),
                   kv_cache.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),

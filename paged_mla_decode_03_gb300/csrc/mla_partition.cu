@@ -120,7 +120,7 @@ __device__ T block_exclusive_scan(T* data, int n, Shared& sh) {
 struct Bounds {
   long long W, n, lanes, nl, WL;
   const long long* table;  // boundary(p) for p in [0, n], or nullptr
-  long long overhead;      // units of a group besides its tiles
+  long long overhead = kOverheadTiles;  // units of a group besides its tiles
   // start unit of worker p's range (the arithmetic behind the table)
   __device__ long long boundary_of(long long p) const {
     if (p >= lanes * nl) return W;
