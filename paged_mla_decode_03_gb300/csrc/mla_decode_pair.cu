@@ -142,7 +142,8 @@ enum Bar {
   XS0 = MR0 + 4,                       // 2: [pair] row sums exchanged
   EPI = XS0 + 2,                       // the partial is written
   DRAIN0,                              // 2: every MMA of an issuing warp has completed
-  NUM_BARS = DRAIN0 + 2
+  QSTG = DRAIN0 + 2, Q_READ,           // the block's first query is staged; has been read
+  NUM_BARS
 };
 static_assert(NUM_BARS * 8 <= 352, "barrier area");
 
@@ -285,6 +286,78 @@ __device__ __forceinline__ void widen16(const uint4 c, uint4& a, uint4& b) {
   b = e4m3x8_to_f16(make_uint2(c.z, c.w));
 }
 
+// A work item's query, rows [64 rank, 64 rank + 64), where it is read from.
+struct Query {
+  const unsigned char* base;  // row 0, in global or in shared memory
+  int pitch, n;               // bytes from row to row; rows (the others are zeros)
+  int fp8;
+  __device__ uint4 unit(int r, int u) const {  // eight dims, raw
+    if (r >= n) return make_uint4(0, 0, 0, 0);
+    const unsigned char* at = base + r * pitch;
+    if (fp8) {
+      const uint2 v = reinterpret_cast<const uint2*>(at)[u];
+      return make_uint4(v.x, v.y, 0, 0);
+    }
+    return reinterpret_cast<const uint4*>(at)[u];
+  }
+};
+
+// The block's first query, from rows staged in shared memory (see below).  A
+// function of its own leaves the conversion loops their registers: inlined, those
+// spilled and a long call took 6% more.
+template <int kCache>
+__device__ __noinline__ bool first_query(Ctx c, unsigned char* sm, uint32_t tmem, Query q, int w) {
+  const int lane = threadIdx.x & 31, quad = (kFirstConv + w) & 3;
+  float* scales = reinterpret_cast<float*>(sm + Cfg<kCache>::OFF_QSCALE);
+  if (!wait_bar(c, QSTG, 0)) return false;
+  // the rows' factors 2^-k: four rows a warp, a row's 72 units over its lanes
+#pragma unroll 1
+  for (int r = 4 * w; r < 4 * w + 4; ++r) {
+    int e = 0;
+    if (!q.fp8 && kCache != kBf16) {
+      const uint4 a = q.unit(r, lane), b = q.unit(r, 32 + lane), d = q.unit(r, 64 + (lane & 7));
+      uint32_t mb = __vmaxu2(__vmaxu2(max_bits(a), max_bits(b)), max_bits(d));
+      mb = __reduce_max_sync(0xffffffffu, max(mb & 0xFFFFu, mb >> 16));
+      e = query_exponent(mb);
+    }
+    if (lane == 0) scales[r] = __uint_as_float((uint32_t)(127 - e) << 23);
+  }
+  __syncwarp();
+  if (lane == 0) {
+    mbar_arrive(&c.bars[QX]);
+    mbar_arrive(&c.bars[QS_FULL0]);
+  }
+  if (!wait_bar(c, QX, 0)) return false;
+  auto as_operand = [&](const uint4 x, float up) {  // f16, or bf16 for bf16 MMAs
+    if constexpr (Cfg<kCache>::kTma) return q.fp8 ? e4m3x8_to_bf16(make_uint2(x.x, x.y)) : x;
+    return q.fp8 ? e4m3x8_to_f16(make_uint2(x.x, x.y)) : bf16x8_to_f16(x, up);
+  };
+  // as in load_query
+  const int row = (32 * quad + lane) & 63, part = w >> 2;
+  const float up = 1.f / scales[row];
+  const uint32_t tq = tmem + ((uint32_t)(32 * quad) << 16) + TM_Q + 48 * part;
+  constexpr int kPerRow = 8 * (kChunks - kTmemChunks);
+#pragma unroll 1
+  for (int j = 0; j < 3; ++j) {
+    uint4 f[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) f[u] = as_operand(q.unit(row, 12 * part + 4 * j + u), up);
+    tmem_st_32x32b_x16(tq + 16 * j, *reinterpret_cast<const uint32_t(*)[16]>(f));
+    const int at = 32 * (kConvWarps * j + w) + lane, r = at / kPerRow, u2 = at - r * kPerRow;
+    put(swizzled_row(smem_u32(sm) + OFF_Q + (u2 >> 3) * kQChunk, r), u2 & 7,
+        as_operand(q.unit(r, 8 * kTmemChunks + u2), 1.f / scales[r]));
+  }
+  fence_proxy_async_smem();
+  tmem_wait_st();
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) {
+    arrive_leader(c, Q_FULL, 1);
+    mbar_arrive(&c.bars[Q_READ]);
+  }
+  return wait_bar(c, Q_READ, 0);  // K and V may go where it was staged
+}
+
 }  // namespace
 
 template <int kCache>
@@ -329,6 +402,8 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
       if (i >= XM0 && i < XM0 + 4) n = 2;
       if (i >= XS0 && i < XS0 + 2) n = 4;
       if (i == EPI) n = kSoftWarps;
+      if (i == QSTG) n = kCtaRows;
+      if (i == Q_READ) n = kConvWarps;
       mbar_init(&c.bars[i], n);
     }
     *c.abort = 0;
@@ -417,7 +492,9 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
                   tma_load_2d(sm + OFF_K + s * kKStage + ch * kKChunk, &tm_kv, 64 * ch, rank == 0 ? y0 : y1, full);
             }
           } else {
-            // V: this CTA's dims of all rows, once PV of two tiles ago has
+            // V: this CTA's dims of all rows, once PV of two tiles ago has, and the
+            // first query, which is staged there
+            if (g == 0 && !wait_bar(c, Q_READ, 0)) goto fail_copy;
             if (!wait_bar(c, PV_DONE0 + s, (use & 1) ^ 1)) goto fail_copy;
             if (lane == 0) {
               uint64_t* v_full = &c.bars[STG_EMPTY0 + s];
@@ -428,7 +505,10 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
                 if (on1) tma_load_2d(dst + kHalf * 128, &tm_kv, 256 * rank + 64 * ch, y1, v_full);
               }
             }
-            for (int a = t == 0 ? 2 : kAhead; a <= kAhead; ++a) {
+            // (not before the block's first tile is there: the prefetches of all blocks
+            // would queue in front of it)
+            if (g == 1 && !wait_bar(c, STG_EMPTY0, 0)) goto fail_copy;
+            for (int a = g == 0 ? kAhead + 1 : g == 1 ? 1 : t == 0 ? 2 : kAhead; a <= kAhead; ++a) {
               const int i = (t + a) * npg + (npg == 2 ? rank : 0);
               const int from = __shfl_sync(0xffffffffu, (i >> 5) == (slot0 >> 5) ? cur : nxt, i & 31);
               if (t + a < nt && lane == 0 && from >= 0 && from < p.num_pages)
@@ -1040,17 +1120,41 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
       if (lane == 0) arrive_leader(c, Q_FULL, 1);
       return true;
     };
+    // The block's first query is staged where K or V will be, by copies of whole rows:
+    // one round trip.  (By the passes above, in five, it was there 21,000 cycles after
+    // the launch, and 15,000 this way.)
+    constexpr uint32_t kQPitch = 2 * kQkDim + 16;  // an odd number of units: no bank conflicts
+    constexpr uint32_t OFF_QSTG = C::kTma ? OFF_V : OFF_K;  // (TMA writes K as soon as it can)
+    static_assert(kCtaRows * kQPitch <= (C::kTma ? 2 * kVStage + 2 * kPTile : 2 * (kKStage + kVStage)), "room");
+    for (int idx = item_begin; idx < item_end; ++idx) {
+      const WorkItem it = items[idx];
+      if (n_tiles_of(it) <= 0) continue;
+      const long long q0 = first_row(it);
+      const int n = (int)min((long long)kCtaRows, q_rows - q0), bytes = p.q_fp8 ? kQkDim : 2 * kQkDim;
+      if (lane < 4) {
+        const int r = 4 * w + lane;
+        mbar_arrive_expect_tx(&c.bars[QSTG], r < n ? bytes : 0);
+        if (r < n)
+          bulk_load(sm + OFF_QSTG + r * kQPitch, static_cast<const unsigned char*>(p.query) + (q0 + r) * bytes, bytes,
+                    &c.bars[QSTG]);
+      }
+      __syncwarp();
+      if (!first_query<kCache>(c, sm, tmem, Query{sm + OFF_QSTG, (int)kQPitch, n, p.q_fp8}, w)) {
+        drain_wait(&c.bars[QSTG], 0);  // (rows may still be landing)
+        goto fail_conv;
+      }
+      break;
+    }
     for (int idx = item_begin; idx < item_end; ++idx) {
       const WorkItem it = items[idx];
       const int nt = n_tiles_of(it);
       if (nt <= 0) continue;
-      if (n_item == 0) query_scales(it, 0);
-      // the first tile before the query: its conversion needs nothing of the
-      // previous item but free stages
+      // a later item's first tile before its query: its conversion needs nothing of
+      // the previous item but free stages
       for (int t = 0; t < nt; ++t, ++g) {
         if ((g & 1) == grp && !convert_tile()) goto fail_conv;
         if (t > 0) continue;
-        if (!load_query(it, n_item)) goto fail_conv;
+        if (n_item > 0 && !load_query(it, n_item)) goto fail_conv;
         for (int nx = idx + 1; nx < item_end; ++nx) {
           const WorkItem itn = items[nx];
           if (n_tiles_of(itn) <= 0) continue;
