@@ -96,6 +96,10 @@ template <int kCache> struct Cfg {
   static constexpr uint32_t kScaleBytes = kCache == kFp4 ? kFp4ScaleBytes : 0;
   static constexpr uint32_t kVBytes = kCache == kFp4 ? 128 : 256;  // codes of 256 dims
   static constexpr uint32_t kRowBytes = kCodeBytes + kScaleBytes;
+  // V: 64-dim chunks of the tile's 64 rows; TMA brings a half's four chunks together,
+  // so there they are of 32 rows, a half after the other
+  static constexpr uint32_t kVChunkStep = kTma ? kVChunk / 2 : kVChunk;
+  static constexpr uint32_t kVHalfGap = kTma ? kVStage / 2 - kVChunk / 2 : 0;
   // P tiles: the staged e4m3 rows leave room for one
   static constexpr uint32_t kPTiles = kCache == kE4m3 ? 1 : 2;
   static constexpr uint32_t OFF_STG = OFF_P + kPTiles * kPTile;
@@ -104,8 +108,12 @@ template <int kCache> struct Cfg {
   static constexpr uint32_t STG_OTHER = STG_OWN + kHalf * kCodeBytes;
   static constexpr uint32_t STG_SCALES = STG_OTHER + kHalf * kVBytes;
   static constexpr uint32_t kStage = STG_SCALES + kTile * kScaleBytes;
-  static constexpr uint32_t OFF_BARS = OFF_STG + (kTma ? 0 : 2 * kStage);
-  static constexpr uint32_t OFF_XMAX = OFF_BARS + 352;              // float [4][128]: tile maxima by tile mod 4
+  // bf16: three stages of K, the third where the others have their staging.  (K of
+  // tile g + 2 can go out when QK of g is done, and QK of g + 2 wants it some 500
+  // cycles later; a third stage gives its copy a whole tile.)
+  static constexpr uint32_t OFF_K2 = OFF_STG;
+  static constexpr uint32_t OFF_BARS = OFF_STG + (kTma ? kKStage : 2 * kStage);
+  static constexpr uint32_t OFF_XMAX = OFF_BARS + 384;              // float [4][128]: tile maxima by tile mod 4
   static constexpr uint32_t OFF_MREF = OFF_XMAX + 4 * 128 * 4;      // float [2][64]: references by tile parity
   static constexpr uint32_t OFF_XSUM = OFF_MREF + 2 * kCtaRows * 4;  // float [2][2][128]: (sum, reference) by group
   static constexpr uint32_t OFF_QSCALE = OFF_XSUM + 4 * 128 * 4;    // float [4][64]: 2^-k by item
@@ -114,7 +122,7 @@ template <int kCache> struct Cfg {
   static constexpr uint32_t OFF_MASK = OFF_ABORT + 8;  // uint32 [2][2]: rows in use, by stage and half
   static constexpr uint32_t kSmemBytes = OFF_MASK + 16;
   static_assert(kSmemBytes <= 232448, "shared memory budget");
-  static_assert(OFF_STG % 16 == 0 && kStage % 16 == 0 && STG_OTHER % 16 == 0 && STG_SCALES % 16 == 0 &&
+  static_assert((kTma ? OFF_K2 % 1024 == 0 : OFF_STG % 16 == 0) && kStage % 16 == 0 && STG_OTHER % 16 == 0 && STG_SCALES % 16 == 0 &&
                     OFF_BARS % 8 == 0,
                 "alignment");
 };
@@ -127,7 +135,7 @@ constexpr uint32_t TM_S = 256;  // two 32-column buffers; lane: query row and KV
 constexpr uint32_t TM_Q = 320;  // chunks 0..5 of the query row (mod 64), pairs of f16
 
 enum Bar {
-  STG_FULL0, STG_EMPTY0 = STG_FULL0 + 2,  // by tile parity (TMA: K landed, V landed)
+  STG_FULL0, STG_EMPTY0 = STG_FULL0 + 2,  // by tile parity (TMA: unused, V landed)
   K_FULL0 = STG_EMPTY0 + 2,   // even CTA: [tile parity][3], both CTAs' chunks are there
   V_FULL0 = K_FULL0 + 2 * (kChunks / kGroup),  // even CTA
   PV_DONE0 = V_FULL0 + 2,              // by tile parity: V stage and P free, O stable
@@ -143,9 +151,11 @@ enum Bar {
   EPI = XS0 + 2,                       // the partial is written
   DRAIN0,                              // 2: every MMA of an issuing warp has completed
   QSTG = DRAIN0 + 2, Q_READ,           // the block's first query is staged; has been read
-  NUM_BARS
+  KE0,                                 // TMA, 3: by tile mod 3, QK has read the K stage
+  NUM_BARS = KE0 + 3,
+  K_TMA0 = K_FULL0 + 3                 // TMA, 3: by tile mod 3, K landed (K_FULL0: by tile mod 3, too)
 };
-static_assert(NUM_BARS * 8 <= 352, "barrier area");
+static_assert(kChunks / kGroup == 3 && NUM_BARS * 8 <= 384, "barrier area");
 
 struct Ctx {
   uint64_t* bars;
@@ -363,7 +373,8 @@ __device__ __noinline__ bool first_query(Ctx c, unsigned char* sm, uint32_t tmem
 template <int kCache>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
-                   const __grid_constant__ CUtensorMap tm_kv) {  // (bf16 cache only)
+                   const __grid_constant__ CUtensorMap tm_k,   // (bf16 cache only)
+                   const __grid_constant__ CUtensorMap tm_v) {
   using C = Cfg<kCache>;
   // The swizzled tiles need 1024-byte alignment, and there is no room to round
   // up: the block has no other shared memory, so its dynamic part starts at
@@ -394,7 +405,7 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
       if (i >= STG_FULL0 && i < STG_EMPTY0) n = C::kTma ? 1 : 1 + 32;  // bulk copies, each lane's own
       if (i >= STG_EMPTY0 && i < K_FULL0) n = C::kTma ? 1 : kConvWarps / 2;
       // a latent chunk's warp counts four times, as the RoPE chunk has four warps
-      if (i >= K_FULL0 && i < V_FULL0) n = C::kTma ? 2 : 2 * 4 * kGroup;
+      if (i >= K_FULL0 && i < V_FULL0) n = !C::kTma ? 2 * 4 * kGroup : i < K_TMA0 ? 2 : 1;
       if (i >= V_FULL0 && i < V_FULL0 + 2) n = C::kTma ? 2 : kConvWarps;  // half the warps of both CTAs
       if (i >= S_EMPTY0 && i < P_FULL0 + 2) n = kSoftWarps;  // half the warps of both CTAs
       if (i == Q_FULL) n = 2 * kConvWarps;
@@ -475,35 +486,33 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
           const int row1 = npg == 1 ? kHalf : 0;  // first row of half 1 in its page
           const int y0 = id0 * ps, y1 = id1 * ps + row1;
           if (bulk) {
-            // K: the own rows' nine chunks, once QK of two tiles ago has read the stage
+            // K: the own rows' nine chunks, once QK of three tiles ago has read the stage
+            const uint32_t use3 = g / 3, s3 = g - 3 * use3;
+            if (!wait_bar(c, KE0 + s3, (use3 & 1) ^ 1)) goto fail_copy;
+            if (lane == 0) {
+              const bool own = rank == 0 ? on0 : on1;
+              unsigned char* dst = sm + (s3 == 2 ? C::OFF_K2 : OFF_K + s3 * kKStage);
+              mbar_arrive_expect_tx(&c.bars[K_TMA0 + s3], own ? kKStage : 0);
+              if (own) tma_load_3d(dst, &tm_k, 0, rank == 0 ? y0 : y1, 0, &c.bars[K_TMA0 + s3]);
+            }
+          } else {
+            // V: this CTA's dims of all rows, once PV of two tiles ago has, and the
+            // first query, which is staged there
             const uint32_t mask0 = __ballot_sync(0xffffffffu, on0 && j0 + lane < it.kv_end &&
                                                                   walk.seen(r0 + lane, r0 + lane));
             const uint32_t mask1 =
                 __ballot_sync(0xffffffffu, on1 && j0 + kHalf + lane < it.kv_end &&
                                                walk.seen(r0 + kHalf + lane, r0 + kHalf + lane));
-            if (!wait_bar(c, S_FULL0 + s, (use & 1) ^ 1)) goto fail_copy;
-            if (lane == 0) {
-              row_mask[2 * s] = mask0;
-              row_mask[2 * s + 1] = mask1;
-              const bool own = rank == 0 ? on0 : on1;
-              mbar_arrive_expect_tx(full, own ? kKStage : 0);
-              if (own)
-                for (int ch = 0; ch < kChunks; ++ch)
-                  tma_load_2d(sm + OFF_K + s * kKStage + ch * kKChunk, &tm_kv, 64 * ch, rank == 0 ? y0 : y1, full);
-            }
-          } else {
-            // V: this CTA's dims of all rows, once PV of two tiles ago has, and the
-            // first query, which is staged there
             if (g == 0 && !wait_bar(c, Q_READ, 0)) goto fail_copy;
             if (!wait_bar(c, PV_DONE0 + s, (use & 1) ^ 1)) goto fail_copy;
             if (lane == 0) {
               uint64_t* v_full = &c.bars[STG_EMPTY0 + s];
+              row_mask[2 * s] = mask0;
+              row_mask[2 * s + 1] = mask1;
               mbar_arrive_expect_tx(v_full, ((on0 ? 1 : 0) + (on1 ? 1 : 0)) * (kVStage / 2));
-              for (int ch = 0; ch < 4; ++ch) {
-                unsigned char* dst = sm + OFF_V + s * kVStage + ch * kVChunk;
-                if (on0) tma_load_2d(dst, &tm_kv, 256 * rank + 64 * ch, y0, v_full);
-                if (on1) tma_load_2d(dst + kHalf * 128, &tm_kv, 256 * rank + 64 * ch, y1, v_full);
-              }
+              unsigned char* dst = sm + OFF_V + s * kVStage;
+              if (on0) tma_load_3d(dst, &tm_v, 0, y0, 4 * rank, v_full);
+              if (on1) tma_load_3d(dst + kVStage / 2, &tm_v, 0, y1, 4 * rank, v_full);
             }
             // (not before the block's first tile is there: the prefetches of all blocks
             // would queue in front of it)
@@ -587,9 +596,12 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
     tell_abort(c);
   done_copy:
     // no copy issued here may still be landing when the CTA leaves
-    for (uint32_t k = 0; k < 2 && k < g; ++k) {
+    for (uint32_t k = 0; k < (C::kTma && bulk ? 3 : 2) && k < g; ++k) {
       const uint32_t gi = g - 1 - k;
-      drain_wait(&c.bars[(C::kTma && !bulk ? STG_EMPTY0 : STG_FULL0) + (gi & 1)], (gi >> 1) & 1);
+      if (C::kTma && bulk)
+        drain_wait(&c.bars[K_TMA0 + gi % 3], (gi / 3) & 1);
+      else
+        drain_wait(&c.bars[(C::kTma ? STG_EMPTY0 : STG_FULL0) + (gi & 1)], (gi >> 1) & 1);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ QK issue
@@ -609,10 +621,17 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
         for (int t = 0; t < nt; ++t, ++g) {
           const uint32_t sb = g & 1;
           if (!wait_bar(c, S_EMPTY0 + sb, ((g >> 1) & 1) ^ 1)) goto fail_qk;
-          const uint64_t kd = k_desc + sb * (kKStage >> 4);
+          const uint32_t use3 = g / 3, s3 = g - 3 * use3;  // (TMA)
+          const uint64_t kd = k_desc + (!C::kTma     ? sb * (kKStage >> 4)
+                                        : s3 == 2 ? (C::OFF_K2 - OFF_K) >> 4
+                                                  : s3 * (kKStage >> 4));
 #pragma unroll
           for (int k3 = 0; k3 < kChunks / kGroup; ++k3) {
-            if (!wait_bar(c, K_FULL0 + sb * (kChunks / kGroup) + k3, (g >> 1) & 1)) goto fail_qk;
+            if constexpr (C::kTma) {
+              if (k3 == 0 && !wait_bar(c, K_FULL0 + s3, use3 & 1)) goto fail_qk;
+            } else {
+              if (!wait_bar(c, K_FULL0 + sb * (kChunks / kGroup) + k3, (g >> 1) & 1)) goto fail_qk;
+            }
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
@@ -629,6 +648,7 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
                 }
               if (k3 == kChunks / kGroup - 1) {
                 mma_commit_pair(&c.bars[S_FULL0 + sb]);
+                if (C::kTma) mma_commit_pair(&c.bars[KE0 + s3]);
                 if (t + 1 == nt) mma_commit_pair(&c.bars[Q_EMPTY]);
               }
             }
@@ -650,7 +670,7 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
     if (rank == 0) {
       constexpr uint32_t idesc = C::kTma ? idesc_f16(kRows, 256, false, true) : idesc_half(kRows, 256, false, true);
       const uint64_t p_desc = smem_desc(smem_u32(sm + OFF_P), 16, 1024, kSwizzle128B);
-      const uint64_t v_desc = smem_desc(smem_u32(sm + OFF_V), kVChunk, 1024, kSwizzle128B);
+      const uint64_t v_desc = smem_desc(smem_u32(sm + OFF_V), C::kVChunkStep, 1024, kSwizzle128B);
       uint32_t g = 0;
       for (int idx = item_begin; idx < item_end; ++idx) {
         const int nt = __shfl_sync(0xffffffffu, n_tiles_of(items[idx]), 0);
@@ -666,7 +686,7 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
 #pragma unroll
               for (int j = 0; j < 2; ++j)
                 mma_f16_pair_ss(tmem + TM_O + 128 * j, p_desc + (C::kPTiles == 2 ? s * (kPTile >> 4) : 0) + 2 * ks,
-                                v + ((j * 2 * kVChunk + ks * 16 * 128) >> 4), idesc,
+                                v + ((j * 2 * C::kVChunkStep + ks * 16 * 128 + (ks >> 1) * C::kVHalfGap) >> 4), idesc,
                                 (t == 0 && ks == 0) ? 0u : 1u);
             mma_commit_pair(&c.bars[PV_DONE0 + s]);
           }
@@ -931,28 +951,32 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
     const uint32_t r_row = swizzled_row(smem_u32(sm) + OFF_K + grp * kKStage + 8 * kKChunk, lane);
     const uint32_t v_row = swizzled_row(smem_u32(sm) + OFF_V + grp * kVStage + vc * kVChunk,
                                         kHalf * (in_half ? rank : rank ^ 1) + lane);
-    // bf16: the first warp of a group passes a tile's K and V on and clears the V
-    // rows that are not in use (their K only makes scores that the mask replaces).
+    // bf16: warp 0 passes every tile's K on, one warp a group its V (a warp for both
+    // held up K of tile g + 2 for V of tile g), after clearing the V rows that are not in
+    // use (their K only makes scores that the mask replaces).  (K's stages are by tile
+    // mod 3, so a warp of one group would skip phases of their barriers, and a wait for
+    // a phase passes while the one before it is still open.)
     auto pass_tile = [&]() -> bool {
-      if (k != 0) return true;
-      const uint32_t use = g >> 1;
-      if (!wait_bar(c, STG_FULL0 + grp, use & 1)) return false;
-      const uint32_t m0 = row_mask[2 * grp], m1 = row_mask[2 * grp + 1];  // (before K goes on: see the copies)
-      __syncwarp();
-      if (lane < 3) arrive_leader(c, K_FULL0 + 3 * grp + lane, 1);
-      if (!wait_bar(c, STG_EMPTY0 + grp, use & 1)) return false;
-      if ((m0 & m1) != 0xffffffffu) {
+      if (w == 0) {
+        const uint32_t use3 = g / 3, s3 = g - 3 * use3;
+        if (!wait_bar(c, K_TMA0 + s3, use3 & 1)) return false;
+        if (lane == 0) arrive_leader(c, K_FULL0 + s3, 1);
+      } else if (k == 1 && (g & 1) == grp) {
+        if (!wait_bar(c, STG_EMPTY0 + grp, (g >> 1) & 1)) return false;
+        const uint32_t m0 = row_mask[2 * grp], m1 = row_mask[2 * grp + 1];
+        if ((m0 & m1) != 0xffffffffu) {
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          if (((h ? m1 : m0) >> lane) & 1u) continue;
-          const uint32_t v = smem_u32(sm) + OFF_V + grp * kVStage + (kHalf * h + lane) * 128;
+          for (int h = 0; h < 2; ++h) {
+            if (((h ? m1 : m0) >> lane) & 1u) continue;
+            const uint32_t v = smem_u32(sm) + OFF_V + grp * kVStage + h * (kVStage / 2) + lane * 128;
 #pragma unroll 1
-          for (int e = 0; e < 32; ++e) st_shared_v4(v + (e >> 3) * kVChunk + (e & 7) * 16, make_uint4(0, 0, 0, 0));
+            for (int e = 0; e < 32; ++e) st_shared_v4(v + (e >> 3) * C::kVChunkStep + (e & 7) * 16, make_uint4(0, 0, 0, 0));
+          }
+          fence_proxy_async_smem();
         }
-        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) arrive_leader(c, V_FULL0 + grp, 1);
       }
-      __syncwarp();
-      if (lane == 0) arrive_leader(c, V_FULL0 + grp, 1);
       return true;
     };
     auto convert_tile = [&]() -> bool {
@@ -1152,7 +1176,7 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
       // a later item's first tile before its query: its conversion needs nothing of
       // the previous item but free stages
       for (int t = 0; t < nt; ++t, ++g) {
-        if ((g & 1) == grp && !convert_tile()) goto fail_conv;
+        if ((C::kTma || (g & 1) == grp) && !convert_tile()) goto fail_conv;
         if (t > 0) continue;
         if (n_item > 0 && !load_query(it, n_item)) goto fail_conv;
         for (int nx = idx + 1; nx < item_end; ++nx) {
@@ -1213,8 +1237,10 @@ cudaError_t setup_one(int sm_count, int* n_pairs) {
   return cudaSuccess;
 }
 
-// The bf16 cache's rows, boxes of 64 dims x 32 rows in the 128B-swizzled layout.
-bool encode_rows(CUtensorMap* map, const Problem& p) {
+// The bf16 cache as (64 dims, rows, chunks of 64 dims), boxes of 32 rows and `chunks`
+// chunks in the 128B-swizzled layout: an operand's half tile is one copy.  (By boxes of
+// one chunk the issue of V's eight took longer than a tile's MMAs.)
+bool encode_rows(CUtensorMap* map, const Problem& p, int chunks) {
   static PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
     cudaDriverEntryPointQueryResult q;
     void* ptr = nullptr;
@@ -1224,23 +1250,23 @@ bool encode_rows(CUtensorMap* map, const Problem& p) {
     return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr) : nullptr;
   }();
   if (!encode) return false;
-  cuuint64_t dims[2] = {(cuuint64_t)kQkDim, (cuuint64_t)p.num_pages * p.page_size};
-  cuuint64_t strides[1] = {2 * kQkDim};
-  cuuint32_t box[2] = {64, kHalf}, step[2] = {1, 1};
-  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p.kv_cache), dims, strides, box,
+  cuuint64_t dims[3] = {64, (cuuint64_t)p.num_pages * p.page_size, kChunks};
+  cuuint64_t strides[2] = {2 * kQkDim, 128};
+  cuuint32_t box[3] = {64, kHalf, (cuuint32_t)chunks}, step[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p.kv_cache), dims, strides, box,
                 step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int kCache>
 cudaError_t launch_one(const Problem& p, const Layout& lay, void* ws, cudaStream_t stream) {
-  CUtensorMap map = {};
-  if (Cfg<kCache>::kTma && !encode_rows(&map, p)) return cudaErrorInvalidValue;
+  CUtensorMap tm_k = {}, tm_v = {};
+  if (Cfg<kCache>::kTma && !(encode_rows(&tm_k, p, kChunks) && encode_rows(&tm_v, p, 4))) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   const cudaLaunchConfig_t cfg = pair_launch(lay.n_ctas, Cfg<kCache>::kSmemBytes, stream, &attr);
-  return cudaLaunchKernelEx(&cfg, decode_pair_kernel<kCache>, p, lay, static_cast<char*>(ws), map);
+  return cudaLaunchKernelEx(&cfg, decode_pair_kernel<kCache>, p, lay, static_cast<char*>(ws), tm_k, tm_v);
 }
 
 }  // namespace
