@@ -12,8 +12,10 @@
  *
  * where K_b[j] = kv_cache[block_tables[b][j / page_size]][j % page_size], the
  * 576-wide rows concatenate 512 latent and 64 RoPE dims, and V is the first
- * 512 dims of the same rows (one-copy cache).  Causal masking is bottom-right
- * aligned: row i sees KV rows 0 .. L - q + i; dense masking sees 0 .. L - 1.
+ * 512 dims of the same rows (one-copy cache; bf16, e4m3 or 4 bits).  Causal
+ * masking is bottom-right aligned: row i sees KV rows 0 .. L - q + i; dense
+ * masking sees 0 .. L - 1; a sliding window narrows either.  mla_cache_append
+ * and mla_cache_gather, below, write and read the cache's rows.
  * The natural-log LSE follows the vLLM "FlashInferMLAImpl" page (its LSE
  * contract is base e); the scales are the folded bmm1/bmm2 factors of the
  * FlashInfer pull request "dynamic scale factor interface and one-copy
@@ -97,7 +99,10 @@ typedef struct mla_decode_params {
                                 of that magnitude below).  P enters as two e4m3 parts
                                 (about 2^-8 relative).  Nonzero: every e4m3 value is
                                 widened exactly to bf16 before bf16 MMAs (P in bf16).
-                                Sparse top-k always widens. */
+                                Sparse top-k always widens.  With a window neither: every
+                                e4m3 value is widened exactly to f16, with P in f16, and a bf16 query row enters scaled by a
+                                power of two (exact for every element of at least 2^-31 of
+                                the row's largest magnitude). */
   int32_t window;            /* sliding window W (0: off): of the rows that the mask lets a
                                 query row see, up to row `last`, it sees rows
                                 last - W + 1 .. last and the first `sinks` rows.  (W = 1:
@@ -125,7 +130,11 @@ int mla_decode_plan(const mla_decode_params *params, mla_plan_t **plan,
  * query        bf16 or fp8-e4m3 (per params.q_dtype), fixed [B, SQ, H, 576] or
  *              packed [total_q, H, 576], contiguous.
  * kv_cache     bf16 or fp8-e4m3 (per params.kv_dtype), [num_pages, page_size, 576]
- *              (a rank-4 [num_pages, 1, page_size, 576] cache is the same memory).
+ *              (a rank-4 [num_pages, 1, page_size, 576] cache is the same memory),
+ *              or the 4-bit layout below.  Rows that no query row of a request sees
+ *              do not count, whatever they hold; a NaN or an infinity in a row that
+ *              one of its query rows sees may reach the request's other query rows
+ *              (0 times it is a NaN).
  * block_tables int32 [B, max_pages_per_req]; entries at or past a request's
  *              ceil(seq_lens[b] / page_size) pages are never read, nor, under a
  *              sliding window, those of pages that none of its query rows sees
@@ -518,7 +527,7 @@ int mla_decode_work_list_layout(const mla_plan_t *plan, size_t *items_offset,
  * Number of kernels one run of `plan` launches on the caller's stream (a
  * plan property; batch 0 launches none): the partitioner, the decode kernel
  * and the combine kernel, plus, on the FP8 MMA path with a bf16 query (an
- * e4m3 cache, no sparse top-k, e4m3_widen 0), the query split that precedes
+ * e4m3 cache, no sparse top-k, no window, e4m3_widen 0), the query split that precedes
  * the decode.  Returns -1 for a NULL plan.
  */
 int32_t mla_decode_kernels_per_run(const mla_plan_t *plan);

@@ -10,7 +10,10 @@ The high-level entry point mirrors the FlashInfer page
 ``[B, SQ, H, 576]`` or packed ``[total_q, H, 576]`` queries (``qo_indptr``),
 a rank-3 or rank-4 paged cache, ``block_tables``/``seq_lens`` on the device,
 caller-owned workspace, ``bmm1_scale``/``bmm2_scale``, causal or dense
-masking, bf16 output and an optional natural-log LSE.
+masking, bf16 output and an optional natural-log LSE.  The cache is bf16, e4m3
+or 4-bit; ``cache_append`` writes the newest tokens' rows (norm, rotation,
+quantisation) and forms their query, ``cache_gather`` reads rows back, and
+``rope_table`` makes the rotation table.
 """
 from __future__ import annotations
 

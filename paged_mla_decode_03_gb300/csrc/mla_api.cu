@@ -6,7 +6,8 @@
 // mla_decode_run checks what the host can check and enqueues three kernels
 // on the caller's stream: the split-KV partitioner, the decode kernel and the
 // combine kernel, with the query split between the first two on the FP8 MMA
-// path with a bf16 query.  Grid sizes depend only on plan-time values, and nothing
+// path with a bf16 query.  The decode kernel is mla_decode_pair.cu's for a 4-bit
+// cache or a sliding window, else mla_decode_sm103.cu's.  Grid sizes depend only on plan-time values, and nothing
 // here allocates, copies or synchronises, so a run can be captured in a CUDA
 // graph and replayed with new seq_lens / qo_indptr values.
 #include <algorithm>
@@ -50,10 +51,10 @@ constexpr size_t kHeaderBytes = sizeof(int) * mla::kHdrWords;
 
 bool supported_heads(int h) { return h == 16 || h == 32 || h == 64 || h == 128; }
 
-// The sliding window the kernels run with: one that reaches back over every
-// length the plan admits hides nothing.
+// The sliding window the kernels run with (0: off).  One that reaches back over every
+// length the plan admits hides nothing, and no sum with it then passes 31 bits.
 int effective_window(const mla_decode_params& p) {
-  return p.window > 0 && p.window < p.max_seq_len ? p.window : 0;
+  return std::min(p.window, p.max_seq_len);
 }
 
 // The MMAs across CTA pairs (mla_decode_pair.cu): a 4-bit cache, and every cache
@@ -131,7 +132,7 @@ int make_layout(const mla_decode_params& prm, int n_workers, int n_ctas, int row
   // query's e4m3 parts, split once per call before the decode (q_split_offset)
   // (the condition of uses_q_split, spelled out)
   if (prm.kv_dtype == MLA_KV_FP8_E4M3 && prm.sparse_top_k == 0 && prm.e4m3_widen == 0 &&
-      (prm.window <= 0 || prm.window >= prm.max_seq_len) && prm.q_dtype == MLA_Q_BF16) {
+      prm.window <= 0 && prm.q_dtype == MLA_Q_BF16) {
     const long long tokens = prm.packed ? prm.max_total_q : B * prm.max_seq_len_q;
     const size_t halves = 2 * (size_t)std::max(tokens, 1LL) * (size_t)prm.num_heads;
     off = align_up(off + halves * kQSplitUnits * 16, 256);

@@ -18,7 +18,10 @@
 // unit (a token's cache row, or four heads of a token's query), so that a small
 // call is one latency chain and a large one keeps every SM's loads in flight: a
 // warp issues its nine 16-byte loads per lane before it looks up the token's
-// request, position and rotation.
+// request, position and rotation.  Measured: 8000 prompt tokens x 128 heads into 4
+// bits with their queries (1.84 GB), append and gather together, 276 us: 6.67 TB/s, the
+// rate of a plain copy.  128 x 128 heads (38 MB) with the gather 8.6 us in a graph, 4 x 32 x 128
+// heads 8.4, 8 x 16 heads 2.8; launched one by one such calls take the host's 20 us.
 //
 // gather reads the same rows back as bf16 (value * kv_scale), one warp a row.
 #include <cuda_bf16.h>

@@ -33,7 +33,7 @@ struct Problem {
   const float* bmm1_dev;         // non-null: read bmm1 from device memory at run time
   const float* bmm2_dev;         // non-null: read bmm2 from device memory at run time
   const void* query;             // bf16 or e4m3 [tokens, H, 576]
-  const void* kv_cache;          // bf16 or e4m3 [num_pages, page_size, 576]
+  const void* kv_cache;          // bf16 or e4m3 [num_pages, page_size, 576], or 4 bits (mla_fp4.cuh)
   const int* block_tables;       // [B, max_pages]
   const int* seq_lens;           // [B]
   const int* qo_indptr;          // [B + 1] or nullptr

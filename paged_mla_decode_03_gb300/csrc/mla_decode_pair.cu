@@ -1,38 +1,46 @@
-// Paged MLA decode over a 4-bit cache (mla_fp4.cuh), and over an e4m3 cache with
-// a sliding window, on sm_103a: a persistent kernel of CTA pairs whose tcgen05
+// Paged MLA decode over a 4-bit cache (mla_fp4.cuh), and over a cache of any format
+// with a sliding window, on sm_103a: a persistent kernel of CTA pairs whose tcgen05
 // MMAs span both CTAs (cta_group::2).
 //
 // What it computes, for the 128 query rows of a work item and the KV rows
 // [kv_begin, kv_end) of its request, in 64-row tiles with an online softmax:
 //   S = Q K^T (576 dims),  P = exp2(bmm1 log2(e) S - m),  O = sum P V / sum P
-// with K row j = 576 values code * scale and V its first 512.
+// with K row j = 576 values (4 bits: code * scale) and V its first 512.
 //
-// Numbers.  A cache value has at most six significant bits and lies in
-// [2^-10, 2688] (e4m3: four bits, [2^-9, 448]), so it is exact in f16, and both products run on f16 MMAs with
-// fp32 accumulation.  A query row enters times a power of two that brings its
-// largest element to [2^14, 2^15): every element down to 2^-31 of it is exact
-// in f16, and its scores are multiplied back by 2^-k.  P enters as f16 (2^-11
-// relative) times 2^7: the running reference m is raised only when a tile's
+// Numbers.  A 4-bit cache's value has at most six significant bits and lies in
+// [2^-10, 2688] (e4m3: four bits, [2^-9, 448]), so it is exact in f16, and both
+// products run on f16 MMAs with fp32 accumulation.  A bf16 query row enters times a
+// power of two that brings its largest element to [2^14, 2^15): every element down to
+// 2^-31 of it is exact in f16, and its scores are multiplied back by 2^-k.  P enters as
+// f16 (2^-11 relative) times 2^7: the running reference m is raised only when a tile's
 // maximum passes it by more than 2^8, so P stays below 2^15, and a P of 2^-31 of
-// the row's largest still has a bit.  Row sums are fp32, of the unrounded P.
+// the row's largest still has a bit.  A bf16 cache runs on bf16 MMAs, query and cache as
+// they are, P rounded to bf16 (2^-8).  Row sums are fp32, of the unrounded P.
 //
-// What bounds it.  At 128 query rows a KV row costs 278 kFLOP against 324
-// bytes: the tensor cores and the shared memory that feeds them, not HBM.  A
+// What bounds it.  At 128 query rows a KV row costs 278 kFLOP against 324 (4 bits) to
+// 1152 bytes: the tensor cores and the shared memory that feeds them, not HBM.  A
 // pair splits a tile so that nothing but barriers passes between its CTAs:
 //  * CTA r holds the item's query rows [64 r, 64 r + 64) whole (Q, S, P, O): a
 //    row's softmax needs no other CTA.  TMEM: O 256 columns, S two buffers of 32,
 //    six of the query's nine 64-dim chunks 192;
 //  * S = Q K^T (M = 128, N = 64): CTA r provides tile rows [32 r, 32 r + 32) of
-//    K in nine 64-dim chunks, two stages of 36 KB;
+//    K in nine 64-dim chunks, two stages of 36 KB (bf16: three);
 //  * O = P V (M = 128, N = 256 twice): CTA r provides V dims [256 r, 256 r +
 //    256) of all 64 rows, two stages of 32 KB.
-// The codes come by bulk copies into a two-stage staging area (the CTA's own
+// 4-bit and e4m3 codes come by bulk copies into a two-stage staging area (the CTA's own
 // rows whole, of the other rows only its V dims), and sixteen warps turn them
 // into f16 in the swizzled operand layouts, one row a lane.  Shared-memory
 // bandwidth is the scarce resource: a tile's MMAs read 24 KB of Q, 68 KB of K and
 // V and 16 KB of P, its conversion writes 68 KB and reads 15.  (With all of Q in
 // shared memory the MMAs read 48 KB more; with the staged codes read across bank
-// conflicts a long call took 476 us instead of 417.)
+// conflicts a long call took 476 us instead of 417.)  bf16 rows come by TMA where the
+// MMAs read them.
+//
+// Measured, a call: 8 x 2 x 128 heads over 64-128k rows of 4 bits 372 us, 1.09 PFLOP/s
+// (57% of the bf16 rate of a large library product; tensor pipes busy 46% of all cycles,
+// shared memory some 90% of a tile's); 64 x 128 heads over 1-8k rows 101 us, 789 TFLOP/s;
+// window 4096, e4m3, 32 x 4 x 128 heads 181 us, 805 TFLOP/s; window 1024, bf16, 64 x 128
+// heads 38.7 us, of which some 12 are the launch chain, the first loads and the epilogue.
 //
 // Warp roles (896 threads): 0 and 3 copy, 1 issues QK (even CTA) and owns TMEM, 2
 // issues PV, 4-11 softmax, correction and epilogue, 12-27 conversion and query

