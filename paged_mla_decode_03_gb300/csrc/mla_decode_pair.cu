@@ -15,7 +15,8 @@
 // f16 (2^-11 relative) times 2^7: the running reference m is raised only when a tile's
 // maximum passes it by more than 2^8, so P stays below 2^15, and a P of 2^-31 of
 // the row's largest still has a bit.  A bf16 cache runs on bf16 MMAs, query and cache as
-// they are, P rounded to bf16 (2^-8).  Row sums are fp32, of the unrounded P.
+// they are, P rounded to bf16 (by 2^-8 of it at most) and O divided by the sum of
+// the rounded P.  Row sums are fp32, of the unrounded P for the LSE and elsewhere for O too.
 //
 // What bounds it.  At 128 query rows a KV row costs 278 kFLOP against 324 (4 bits) to
 // 1152 bytes: the tensor cores and the shared memory that feeds them, not HBM.  A
@@ -123,8 +124,8 @@ template <int kCache> struct Cfg {
   static constexpr uint32_t OFF_BARS = OFF_STG + (kTma ? kKStage : 2 * kStage);
   static constexpr uint32_t OFF_XMAX = OFF_BARS + 384;              // float [4][128]: tile maxima by tile mod 4
   static constexpr uint32_t OFF_MREF = OFF_XMAX + 4 * 128 * 4;      // float [2][64]: references by tile parity
-  static constexpr uint32_t OFF_XSUM = OFF_MREF + 2 * kCtaRows * 4;  // float [2][2][128]: (sum, reference) by group
-  static constexpr uint32_t OFF_QSCALE = OFF_XSUM + 4 * 128 * 4;    // float [4][64]: 2^-k by item
+  static constexpr uint32_t OFF_XSUM = OFF_MREF + 2 * kCtaRows * 4;  // float [2][3][128]: (sum, reference, sum of the rounded P) by group
+  static constexpr uint32_t OFF_QSCALE = OFF_XSUM + 6 * 128 * 4;    // float [4][64]: 2^-k by item
   static constexpr uint32_t OFF_TMEM = OFF_QSCALE + 4 * kCtaRows * 4;
   static constexpr uint32_t OFF_ABORT = OFF_TMEM + 8;
   static constexpr uint32_t OFF_MASK = OFF_ABORT + 8;  // uint32 [2][2]: rows in use, by stage and half
@@ -752,7 +753,9 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
       if (!wait_bar(c, QS_FULL0 + (n_item & 3), (n_item >> 2) & 1)) goto fail_soft;
       const float scale = bmm1 * qscale[(n_item & 3) * kCtaRows + row];
       // this group's share of the row sum, relative to its latest reference m
-      float m = -INFINITY, l_part = 0.f;
+      // (bf16: and the sum of P as it is rounded, by which O is divided: the rounding of a
+      // row's large P, 2^-8 of each, then cancels, where the exact sum keeps it whole)
+      float m = -INFINITY, l_part = 0.f, r_part = 0.f;
       for (int t = 0; t < nt; ++t, ++g) {
         if ((int)(g & 1) != grp) continue;
         if (!wait_bar(c, S_FULL0 + grp, (g >> 1) & 1)) goto fail_soft;
@@ -811,13 +814,15 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
         }
         const bool need = t > 0 && m_new != m_prev;
         if (m_new > m) {  // rebase this group's share (0 while m = -inf)
-          l_part *= ex2(m - m_new);
+          const float f = ex2(m - m_new);
+          l_part *= f;
+          r_part *= f;
           m = m_new;
         }
         const float ref = C::kPShift - (m == -INFINITY ? 0.f : m);
         // (rows past the request's own compute something that nothing reads)
         const uint64_t scale2 = pack_f32x2(scale, scale), ref2 = pack_f32x2(ref, ref);
-        uint64_t rs[2] = {0, 0};
+        uint64_t rs[2] = {0, 0}, rr = 0;
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           float a, b;
@@ -832,6 +837,7 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
           if constexpr (C::kTma) {
             const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
             v[j] = *reinterpret_cast<const uint32_t*>(&h);
+            rr = add_f32x2(rr, pack_f32x2(__uint_as_float(v[j] << 16), __uint_as_float(v[j] & 0xFFFF0000u)));
           } else {
             const __half2 h = __floats2half2_rn(a, b);
             v[j] = *reinterpret_cast<const uint32_t*>(&h);
@@ -841,6 +847,10 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
           float a, b;
           unpack_f32x2(add_f32x2(rs[0], rs[1]), a, b);
           l_part += a + b;
+          if constexpr (C::kTma) {
+            unpack_f32x2(rr, a, b);
+            r_part += a + b;
+          }
         }
         // this P tile has been read
         if constexpr (C::kPTiles == 2) {
@@ -873,21 +883,25 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
         if (lane == 0) arrive_leader(c, P_FULL0 + grp, 1);
       }
       // the row's sum: two threads of each group, each relative to its reference
-      xsum[256 * grp + l] = l_part;
-      xsum[256 * grp + 128 + l] = m;
+      xsum[384 * grp + l] = l_part;
+      xsum[384 * grp + 128 + l] = m;
+      if constexpr (C::kTma) xsum[384 * grp + 256 + l] = r_part;
       __syncwarp();
       if (lane == 0) mbar_arrive(&c.bars[XS0 + pair]);
       if (!wait_bar(c, XS0 + pair, n_item & 1)) goto fail_soft;
-      float m_fin, l_row = 0.f;
+      float m_fin, l_row = 0.f, r_row = 0.f;
       {
-        const float m0 = xsum[128 + row], m1 = xsum[256 + 128 + row];
+        const float m0 = xsum[128 + row], m1 = xsum[384 + 128 + row];
         m_fin = fmaxf(m0, m1);  // a reference never falls within an item
-        const float l0 = xsum[row] + xsum[row + 64], l1 = xsum[256 + row] + xsum[256 + row + 64];
-        if (m0 != -INFINITY) l_row += l0 * ex2(m0 - m_fin);
-        if (m1 != -INFINITY) l_row += l1 * ex2(m1 - m_fin);
+        const float f0 = m0 != -INFINITY ? ex2(m0 - m_fin) : 0.f, f1 = m1 != -INFINITY ? ex2(m1 - m_fin) : 0.f;
+        auto joined = [&](int at) {
+          return (xsum[at + row] + xsum[at + row + 64]) * f0 + (xsum[384 + at + row] + xsum[384 + at + row + 64]) * f1;
+        };
+        l_row = joined(0);
+        r_row = C::kTma ? joined(256) : l_row;
       }
       const float lse = l_row > 0.f ? (m_fin - C::kPShift + log2f(l_row)) * kLn2 : -INFINITY;
-      const float inv = l_row > 0.f ? 1.f / l_row : 0.f;
+      const float inv = r_row > 0.f ? 1.f / r_row : 0.f;
       const size_t grow = (size_t)it.q_start * H + row0 + q;
       if (row_ok && hh == 0 && grp == 0) {
         if (it.slot >= 0)
