@@ -123,7 +123,10 @@ int make_layout(const mla_decode_params& prm, int n_workers, int n_ctas, int row
   lay->scratch_bytes = req_bytes + grp_bytes;
   lay->scratch_in_smem = lay->scratch_bytes <= kPartitionSmemMax ? 1 : 0;
   lay->part_o = off;
-  off = align_up(off + kPartBytesPerRow * R * (size_t)lay->max_partials, 256);
+  // (fp32 with a window over a bf16 cache: the condition of partial_f32)
+  const size_t part_bytes =
+      prm.window > 0 && prm.kv_dtype == MLA_KV_BF16 ? 32 * kPartUnitsF32 * 16 : kPartBytesPerRow;
+  off = align_up(off + part_bytes * R * (size_t)lay->max_partials, 256);
   lay->part_lse = off;
   off = align_up(off + sizeof(float) * R * (size_t)lay->max_partials, 256);
   lay->comb_done = off;

@@ -59,8 +59,12 @@ __device__ bool wait_count(const int* counter, int target, int* status) {
 // kernel, whose CTAs release it right after their prologue, the combine's
 // CTAs run on SMs the decode kernel has finished with and merge a group as
 // soon as both CTAs of every chunk of it have counted their partial.
+template <bool kF32>  // fp32 partials (partial_f32)
 __global__ void __launch_bounds__(kThreads, 4)
 combine_kernel(Problem p, Layout lay, char* __restrict__ ws) {
+  constexpr bool kB16 = kPartialBf16 && !kF32;
+  constexpr int kUnits = kF32 ? kPartUnitsF32 : kPartUnits;
+  constexpr int kChunks = kF32 ? 1 : kBatch;  // a round trip: the registers of two of bf16
   int* status = reinterpret_cast<int*>(ws) + kHdrStatus;
   const int* done = reinterpret_cast<const int*>(ws + lay.comb_done);
   const int* hdr = reinterpret_cast<const int*>(ws);
@@ -89,22 +93,22 @@ combine_kernel(Problem p, Layout lay, char* __restrict__ ws) {
       float acc[16];
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[e] = 0.f;
-      for (int k0 = 0; k0 < c.n_chunks; k0 += kBatch) {
+      for (int k0 = 0; k0 < c.n_chunks; k0 += kChunks) {
         // this row's 16 dims of each chunk as stored (8 words of bf16 pairs,
         // or 16 fp32 words), widened where they are used: half the registers
         // of widening them here, so more blocks fit on an SM
-        uint32_t xw[kBatch][4 * kPartUnits];
-        float l[kBatch];
+        uint32_t xw[kChunks][4 * kUnits];
+        float l[kChunks];
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
+        for (int u = 0; u < kChunks; ++u) {
           l[u] = -INFINITY;
 #pragma unroll
-          for (int v = 0; v < 4 * kPartUnits; ++v) xw[u][v] = 0u;
+          for (int v = 0; v < 4 * kUnits; ++v) xw[u][v] = 0u;
           if (k0 + u < c.n_chunks) {
             const size_t slot = (size_t)(c.first_slot + (k0 + u) * c.stride);
 #pragma unroll
-            for (int v = 0; v < kPartUnits; ++v) {
-              const uint4 a = part_o[part_unit(slot, R, t, v, r)];
+            for (int v = 0; v < kUnits; ++v) {
+              const uint4 a = part_o[kF32 ? part_unit_f32(slot, R, t, v, r) : part_unit(slot, R, t, v, r)];
               xw[u][4 * v] = a.x;
               xw[u][4 * v + 1] = a.y;
               xw[u][4 * v + 2] = a.z;
@@ -115,22 +119,22 @@ combine_kernel(Problem p, Layout lay, char* __restrict__ ws) {
         }
         float m_new = m;
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) m_new = fmaxf(m_new, l[u]);
+        for (int u = 0; u < kChunks; ++u) m_new = fmaxf(m_new, l[u]);
         const float m_use = (m_new == -INFINITY) ? 0.f : m_new;
         const float f = expf(m - m_use);  // m = -inf: 0
         sum *= f;
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[e] *= f;
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
+        for (int u = 0; u < kChunks; ++u) {
           const float w = expf(l[u] - m_use);  // absent chunks: l = -inf, w = 0
           sum += w;
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             // bf16: dim e is the low half of word e / 2 for even e, the high half for odd e
-            const float xe = kPartialBf16 ? __uint_as_float((e & 1) ? (xw[u][e >> 1] & 0xFFFF0000u)
-                                                                   : (xw[u][e >> 1] << 16))
-                                          : __uint_as_float(xw[u][e]);
+            const float xe = kB16 ? __uint_as_float((e & 1) ? (xw[u][e >> 1] & 0xFFFF0000u)
+                                                            : (xw[u][e >> 1] << 16))
+                                  : __uint_as_float(xw[u][e]);
             acc[e] += w * xe;
           }
         }
@@ -163,7 +167,8 @@ cudaError_t launch_combine(const Problem& p, const Layout& lay, void* ws, int gr
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, combine_kernel, p, lay, static_cast<char*>(ws));
+  return partial_f32(p) ? cudaLaunchKernelEx(&cfg, combine_kernel<true>, p, lay, static_cast<char*>(ws))
+                        : cudaLaunchKernelEx(&cfg, combine_kernel<false>, p, lay, static_cast<char*>(ws));
 }
 
 }  // namespace mla

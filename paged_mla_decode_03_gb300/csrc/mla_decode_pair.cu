@@ -919,6 +919,14 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
         tmem_ld_32x32b_x16(tm + TM_O + 128 * grp + 16 * k, x);
         tmem_wait_ld();
         if (!row_ok) continue;
+        if (C::kTma && it.slot >= 0) {  // (partial_f32: the bf16 kernel has windows alone)
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            part_o[part_unit_f32(it.slot, kRows, 16 * hh + 8 * grp + k, u, q)] =
+                make_uint4(__float_as_uint(__uint_as_float(x[4 * u]) * s2), __float_as_uint(__uint_as_float(x[4 * u + 1]) * s2),
+                           __float_as_uint(__uint_as_float(x[4 * u + 2]) * s2), __float_as_uint(__uint_as_float(x[4 * u + 3]) * s2));
+          continue;
+        }
         uint32_t o[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
