@@ -58,9 +58,9 @@ int effective_window(const mla_decode_params& p) {
 }
 
 // The MMAs across CTA pairs (mla_decode_pair.cu): a 4-bit cache, and every cache
-// with a window.  An e4m3 one (32 x 4 x 128 heads, window 4096) takes 189 us a call
+// with a window.  An e4m3 one (32 x 4 x 128 heads, window 4096) takes 181 us a call
 // there and took 303 on the FP8 MMAs, whose tiles exchange scores between the CTAs; a
-// bf16 one (64 x 128 heads, window 1024) 49 and 79.
+// bf16 one (64 x 128 heads, window 1024) 39 and 79.
 bool uses_pair_mma(const mla_decode_params& p) {
   return p.kv_dtype == MLA_KV_FP4_E2M1 || effective_window(p) > 0;
 }

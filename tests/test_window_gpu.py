@@ -115,3 +115,29 @@ def test_a_bad_page_in_a_window_is_flagged_and_reads_as_zeros(kind, ps, bad):
     c.tables[0, at] = page  # the reference reads a page of zeros there
     c.cache[page].zero_()
     c.check(status=16, **P[kind])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind,window", [("fp4", 0), ("bf16", 20)])
+def test_more_row_groups_than_the_small_work_list_takes(kind, window):
+    # 1100 row groups: the work list comes from the block form of the partitioner
+    rng = np.random.default_rng(8)
+    ls = [int(x) for x in rng.integers(1, 65, 1100)]
+    Case(kind, 64, ls, [1] * 1100, 128, window=window, seed=8).run().check(**P[kind])
+
+
+@pytest.mark.gpu
+def test_two_plans_on_two_streams():
+    """Two windowed decodes in flight at once, each with its own workspace."""
+    a = Case("bf16", 64, [900, 700], [1, 1], 128, window=300, seed=21)
+    b = Case("fp4", 64, [800, 1500], [2, 2], 64, window=500, sinks=9, seed=22)
+    torch.cuda.synchronize()
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(5):
+        with torch.cuda.stream(s):
+            a.run()
+        with torch.cuda.stream(t):
+            b.run()
+    torch.cuda.synchronize()
+    a.check(**P["bf16"])
+    b.check(**P["fp4"])
