@@ -177,7 +177,7 @@ struct Ctx {
 // A wait ran out, here or in the other CTA: make both CTAs unwind.
 __device__ __forceinline__ void tell_abort(const Ctx& c) {
   *c.abort = 1;
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(c.peer_abort), "r"(1) : "memory");
+  asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], %1;" ::"r"(c.peer_abort), "r"(1) : "memory");
 }
 // False after too many polls, or once either CTA has given up; the caller then
 // leaves its role, and the block gives up at its end (kept out of the loops: their
@@ -188,10 +188,19 @@ __device__ __forceinline__ bool wait_bar(const Ctx& c, int bar, uint32_t parity)
     if (i == 0 || ((i & 1023) == 0 && *c.abort)) return false;
   return true;
 }
+// The same on a barrier that both CTAs' threads arrive at (arrive_leader).
+__device__ __forceinline__ bool wait_pair(const Ctx& c, int bar, uint32_t parity) {
+  uint64_t* b = &c.bars[bar];
+  for (uint32_t i = kWaitLimit; !mbar_try_wait_pair(b, parity); --i)
+    if (i == 0 || ((i & 1023) == 0 && *c.abort)) return false;
+  fence_acquire_pair();
+  return true;
+}
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
   for (uint32_t i = 0; i < kWaitLimit; ++i)
     if (mbar_try_wait(bar, parity)) return;
 }
+// One lane's arrival for its warp, after __syncwarp (see mbar_arrive_pair).
 __device__ __forceinline__ void arrive_leader(const Ctx& c, int bar, uint32_t count) {
   mbar_arrive_pair(c.leader_bars + 8u * bar, count);
 }
@@ -625,11 +634,11 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
       for (int idx = item_begin; idx < item_end; ++idx) {
         const int nt = __shfl_sync(0xffffffffu, n_tiles_of(items[idx]), 0);
         if (nt <= 0) continue;
-        if (!wait_bar(c, Q_FULL, n_item & 1)) goto fail_qk;
+        if (!wait_pair(c, Q_FULL, n_item & 1)) goto fail_qk;
         ++n_item;
         for (int t = 0; t < nt; ++t, ++g) {
           const uint32_t sb = g & 1;
-          if (!wait_bar(c, S_EMPTY0 + sb, ((g >> 1) & 1) ^ 1)) goto fail_qk;
+          if (!wait_pair(c, S_EMPTY0 + sb, ((g >> 1) & 1) ^ 1)) goto fail_qk;
           const uint32_t use3 = g / 3, s3 = g - 3 * use3;  // (TMA)
           const uint64_t kd = k_desc + (!C::kTma     ? sb * (kKStage >> 4)
                                         : s3 == 2 ? (C::OFF_K2 - OFF_K) >> 4
@@ -637,9 +646,9 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
 #pragma unroll
           for (int k3 = 0; k3 < kChunks / kGroup; ++k3) {
             if constexpr (C::kTma) {
-              if (k3 == 0 && !wait_bar(c, K_FULL0 + s3, use3 & 1)) goto fail_qk;
+              if (k3 == 0 && !wait_pair(c, K_FULL0 + s3, use3 & 1)) goto fail_qk;
             } else {
-              if (!wait_bar(c, K_FULL0 + sb * (kChunks / kGroup) + k3, (g >> 1) & 1)) goto fail_qk;
+              if (!wait_pair(c, K_FULL0 + sb * (kChunks / kGroup) + k3, (g >> 1) & 1)) goto fail_qk;
             }
             tc_fence_after();
             if (elect_one()) {
@@ -685,8 +694,8 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
         const int nt = __shfl_sync(0xffffffffu, n_tiles_of(items[idx]), 0);
         for (int t = 0; t < nt; ++t, ++g) {
           const uint32_t s = g & 1;
-          if (!wait_bar(c, V_FULL0 + s, (g >> 1) & 1)) goto fail_pv;
-          if (!wait_bar(c, P_FULL0 + s, (g >> 1) & 1)) goto fail_pv;
+          if (!wait_pair(c, V_FULL0 + s, (g >> 1) & 1)) goto fail_pv;
+          if (!wait_pair(c, P_FULL0 + s, (g >> 1) & 1)) goto fail_pv;
           tc_fence_after();
           if (elect_one()) {
             const uint64_t v = v_desc + s * (kVStage >> 4);
@@ -765,7 +774,8 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_leader(c, S_EMPTY0 + grp, 1);
+        // (relaxed: what was read is in registers)
+        if (lane == 0) mbar_arrive_cluster_relaxed(c.leader_bars + 8u * (S_EMPTY0 + grp));
         const int v0 = it.kv_begin + t * kTile;        // virtual row of the tile
         const int r0 = walk.row(v0);                    // its row
         const int valid = it.kv_end - v0;               // rows of the tile inside the item
@@ -878,7 +888,6 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
           tmem_wait_st();
           tc_fence_before();
         }
-        fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) arrive_leader(c, P_FULL0 + grp, 1);
       }
@@ -1002,7 +1011,6 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
 #pragma unroll 1
             for (int e = 0; e < 32; ++e) st_shared_v4(v + (e >> 3) * C::kVChunkStep + (e & 7) * 16, make_uint4(0, 0, 0, 0));
           }
-          fence_proxy_async_smem();
         }
         __syncwarp();
         if (lane == 0) arrive_leader(c, V_FULL0 + grp, 1);
@@ -1069,7 +1077,6 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
         put(r_row, 2 * vc, y0);
         put(r_row, 2 * vc + 1, y1);
       }
-      fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
         arrive_leader(c, K_FULL0 + 3 * grp + k / kGroup, 4);
@@ -1092,7 +1099,6 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
       if (!wait_bar(c, PV_DONE0 + grp, ((g >> 1) & 1) ^ 1)) return false;
 #pragma unroll
       for (int e = 0; e < 8; ++e) put(v_row, e, x[e]);
-      fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) arrive_leader(c, V_FULL0 + grp, 1);
       return true;
@@ -1167,7 +1173,6 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
         }
         put(swizzled_row(smem_u32(sm) + OFF_Q + (u2 >> 3) * kQChunk, r), u2 & 7, as_f16(y, 1.f / scales[r]));
       }
-      fence_proxy_async_smem();
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();

@@ -497,12 +497,32 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
                : "memory");
 }
 // Arrive `count` times on a barrier of any CTA of the cluster (shared::cluster
-// address).  The release is at CTA scope: for what only this CTA's own shared
-// memory and TMEM hold and its own tensor core reads (a cluster-scope release is
-// a memory barrier of about a thousand cycles).
+// address), and the wait for it, for shared memory that ordinary stores wrote (this
+// thread's, and those it has synchronised with) and that the tensor cores read when
+// the other CTA's thread issues their MMA: a release and an acquire at cluster scope
+// that carry the writes to the async proxy, restricted to shared memory.  (A long call
+// over 4 bits: 376 us; by a proxy fence in every lane and a restricted release 404, and by an
+// arrival with a full release at cluster scope, a memory barrier of about a thousand
+// cycles, 558.)  Tensor memory is ordered by its own fences.
 __device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_bar, uint32_t count) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_bar), "r"(count)
-               : "memory");
+  asm volatile(
+      "fence.proxy.async::generic.release.sync_restrict::shared::cta.cluster;\n\t"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_bar), "r"(count)
+      : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait_pair(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n"
+      " mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void fence_acquire_pair() {
+  asm volatile("fence.proxy.async::generic.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
 }
 // Brings `bytes` (a multiple of 16, from a 16-byte aligned address) to L2.
 __device__ __forceinline__ void bulk_prefetch_l2(const void* src, uint32_t bytes) {
