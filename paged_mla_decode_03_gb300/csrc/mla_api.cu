@@ -57,24 +57,15 @@ int effective_window(const mla_decode_params& p) {
   return std::min(p.window, p.max_seq_len);
 }
 
-// The MMAs across CTA pairs (mla_decode_pair.cu): a 4-bit cache, and every cache
-// with a window.  An e4m3 one (32 x 4 x 128 heads, window 4096) takes 181 us a call
-// there and took 303 on the FP8 MMAs, whose tiles exchange scores between the CTAs; a
-// bf16 one (64 x 128 heads, window 1024) 39 and 79.
-bool uses_pair_mma(const mla_decode_params& p) {
-  return p.kv_dtype == MLA_KV_FP4_E2M1 || effective_window(p) > 0;
-}
-
-// Otherwise an e4m3 cache runs on the FP8 MMAs unless widening was asked for
-// (sparse top-k always widens).
-bool uses_f8_mma(const mla_decode_params& p) {
-  return p.kv_dtype == MLA_KV_FP8_E4M3 && p.sparse_top_k == 0 && p.e4m3_widen == 0 &&
-         !uses_pair_mma(p);
+static_assert(mla::kKvFp8 == MLA_KV_FP8_E4M3 && mla::kKvFp4 == MLA_KV_FP4_E2M1, "cache types");
+bool uses_pair_mma(const mla_decode_params& p) { return mla::pair_mma(p.kv_dtype, p.window); }
+bool uses_fp8_mma(const mla_decode_params& p) {
+  return mla::fp8_mma(p.kv_dtype, p.window, p.sparse_top_k, p.e4m3_widen);
 }
 
 // the FP8 MMA path with a bf16 query: the query is split before the decode
 bool uses_q_split(const mla_decode_params& p) {
-  return uses_f8_mma(p) && p.q_dtype == MLA_Q_BF16;
+  return uses_fp8_mma(p) && p.q_dtype == MLA_Q_BF16;
 }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -123,19 +114,14 @@ int make_layout(const mla_decode_params& prm, int n_workers, int n_ctas, int row
   lay->scratch_bytes = req_bytes + grp_bytes;
   lay->scratch_in_smem = lay->scratch_bytes <= kPartitionSmemMax ? 1 : 0;
   lay->part_o = off;
-  // (fp32 with a window over a bf16 cache: the condition of partial_f32)
-  const size_t part_bytes =
-      prm.window > 0 && prm.kv_dtype == MLA_KV_BF16 ? 32 * kPartUnitsF32 * 16 : kPartBytesPerRow;
-  off = align_up(off + part_bytes * R * (size_t)lay->max_partials, 256);
+  off = align_up(off + part_row_bytes(prm.kv_dtype, prm.window) * R * (size_t)lay->max_partials, 256);
   lay->part_lse = off;
   off = align_up(off + sizeof(float) * R * (size_t)lay->max_partials, 256);
   lay->comb_done = off;
   off = align_up(off + sizeof(int) * (size_t)std::max(lay->max_combine, 1), 256);
-  // the FP8 MMA path (e4m3 cache, dense, not widened) with a bf16 query: the
-  // query's e4m3 parts, split once per call before the decode (q_split_offset)
-  // (the condition of uses_q_split, spelled out)
-  if (prm.kv_dtype == MLA_KV_FP8_E4M3 && prm.sparse_top_k == 0 && prm.e4m3_widen == 0 &&
-      prm.window <= 0 && prm.q_dtype == MLA_Q_BF16) {
+  // the FP8 MMA path with a bf16 query (uses_q_split): the query's e4m3 parts, split
+  // once per call before the decode (q_split_offset)
+  if (fp8_mma(prm.kv_dtype, prm.window, prm.sparse_top_k, prm.e4m3_widen) && prm.q_dtype == MLA_Q_BF16) {
     const long long tokens = prm.packed ? prm.max_total_q : B * prm.max_seq_len_q;
     const size_t halves = 2 * (size_t)std::max(tokens, 1LL) * (size_t)prm.num_heads;
     off = align_up(off + halves * kQSplitUnits * 16, 256);
@@ -188,7 +174,7 @@ int mla_decode_plan(const mla_decode_params* params, mla_plan_t** plan, size_t* 
   if (e == cudaSuccess)
     e = uses_pair_mma(p)
             ? mla::decode_pair_setup(p.kv_dtype, sms, &n_pairs)
-            : mla::decode_sm103_setup(p.kv_dtype, p.sparse_top_k > 0, uses_f8_mma(p), sms, &n_pairs);
+            : mla::decode_sm103_setup(p.kv_dtype, p.sparse_top_k > 0, uses_fp8_mma(p), sms, &n_pairs);
   if (e == cudaSuccess) e = mla::partition_setup();
   cudaStream_t side = nullptr;
   if (e == cudaSuccess) e = cudaStreamCreateWithFlags(&side, cudaStreamNonBlocking);
@@ -331,7 +317,7 @@ int run_impl(const mla_plan_t* plan, const void* query, const void* kv_cache,
   p.packed = prm.packed;
   p.kv_dtype = prm.kv_dtype;
   p.q_fp8 = prm.q_dtype == MLA_Q_FP8_E4M3;
-  p.f8_mma = uses_f8_mma(prm);
+  p.f8_mma = uses_fp8_mma(prm);
   p.cp_world = dcp ? prm.cp_world : 1;
   p.cp_rank = dcp ? prm.cp_rank : 0;
   p.seq_lens_global = seq_lens_global;

@@ -167,7 +167,7 @@ cudaError_t launch_combine(const Problem& p, const Layout& lay, void* ws, int gr
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return partial_f32(p) ? cudaLaunchKernelEx(&cfg, combine_kernel<true>, p, lay, static_cast<char*>(ws))
+  return partial_f32(p.kv_dtype, p.window) ? cudaLaunchKernelEx(&cfg, combine_kernel<true>, p, lay, static_cast<char*>(ws))
                         : cudaLaunchKernelEx(&cfg, combine_kernel<false>, p, lay, static_cast<char*>(ws));
 }
 

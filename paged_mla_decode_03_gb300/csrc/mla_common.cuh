@@ -143,12 +143,22 @@ __host__ __device__ inline size_t align_up(size_t x, size_t a) { return (x + a -
 // measured ~3.2), and every busy worker gets at least kMinUnits units.
 constexpr long long kOverheadTiles = 3;
 constexpr long long kMinUnits = 4;
-// Whether a run is on the MMAs across CTA pairs (mla_decode_pair.cu).  Their tiles
-// are shorter and the item overhead is the same time: measured 1.2 us a tile and
-// about 6 us an item.
-__host__ __device__ inline bool pair_mma(const Problem& p) {
-  return p.kv_dtype == 2 || p.window > 0;
+// Which kernels a run takes.  The plan sizes the workspace by these and the kernels
+// write it by them, so each is asked in one place (window: any positive value alike).
+constexpr int kKvFp8 = 1, kKvFp4 = 2;  // of mla_kv_dtype
+// The MMAs across CTA pairs (mla_decode_pair.cu): a 4-bit cache, and every cache with a
+// window.  An e4m3 one (32 x 4 x 128 heads, window 4096) takes 182 us a call there and took
+// 303 on the FP8 MMAs, whose tiles exchange scores between the CTAs; a bf16 one (64 x 128
+// heads, window 1024) 39 and 79.
+__host__ __device__ inline bool pair_mma(int kv_dtype, int window) { return kv_dtype == kKvFp4 || window > 0; }
+__host__ __device__ inline bool pair_mma(const Problem& p) { return pair_mma(p.kv_dtype, p.window); }
+// Otherwise an e4m3 cache runs on the FP8 MMAs unless widening was asked for (sparse
+// top-k always widens).
+__host__ __device__ inline bool fp8_mma(int kv_dtype, int window, int sparse_k, int widen) {
+  return kv_dtype == kKvFp8 && sparse_k <= 0 && widen == 0 && !pair_mma(kv_dtype, window);
 }
+// Tiles across pairs are shorter and the item overhead is the same time: measured 1.2 us
+// a tile and about 6 us an item.
 constexpr long long kOverheadTilesPair = 5;
 
 // Whether every row group goes to a worker of its own, uncut: the largest group
@@ -193,8 +203,11 @@ __host__ __device__ inline size_t part_unit(size_t slot, int R, int c, int u, in
 // Windowed runs over a bf16 cache, whose P is rounded to bf16 too, keep fp32 partials,
 // four units a chunk (with bf16 ones a split row's error was 0.0027 of its norm, 1.6
 // times that of the output's own rounding).
-__host__ __device__ inline bool partial_f32(const Problem& p) { return p.window > 0 && p.kv_dtype == 0; }
+__host__ __device__ inline bool partial_f32(int kv_dtype, int window) { return window > 0 && kv_dtype == 0; }
 constexpr int kPartUnitsF32 = 4;
+__host__ __device__ inline size_t part_row_bytes(int kv_dtype, int window) {
+  return partial_f32(kv_dtype, window) ? 32 * kPartUnitsF32 * 16 : kPartBytesPerRow;
+}
 __host__ __device__ inline size_t part_unit_f32(size_t slot, int R, int c, int u, int q) {
   return ((slot * 32 + (size_t)c) * kPartUnitsF32 + (size_t)u) * (size_t)R + (size_t)q;
 }
