@@ -134,7 +134,8 @@ int mla_decode_plan(const mla_decode_params *params, mla_plan_t **plan,
  *              or the 4-bit layout below.  Rows that no query row of a request sees
  *              do not count, whatever they hold; a NaN or an infinity in a row that
  *              one of its query rows sees may reach the request's other query rows
- *              (0 times it is a NaN).
+ *              (0 times it is a NaN).  Sums of V over a request's rows are fp32 and
+ *              divided at their end: bf16 values near fp32's range overflow in them.
  * block_tables int32 [B, max_pages_per_req]; entries at or past a request's
  *              ceil(seq_lens[b] / page_size) pages are never read, nor, under a
  *              sliding window, those of pages that none of its query rows sees

@@ -1,6 +1,6 @@
 // Split-KV combine: merges the normalised partials of every split
-// (request, row group), stored in bf16 (part_unit in mla_common.cuh), by
-// their natural-log LSEs (fp32), accumulating in fp32.
+// (request, row group), stored in bf16, f16 or fp32 (part_format in
+// mla_common.cuh), by their natural-log LSEs (fp32), accumulating in fp32.
 //
 // For chunks k with partial output O_k (already divided by its own softmax
 // denominator) and lse_k = ln sum_{j in chunk k} exp(s_j):
@@ -22,6 +22,7 @@
 // one memory round trip per kBatch chunks.  Blocks past the live number of
 // entries exit at once, so the grid depends only on plan-time bounds.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include <algorithm>
 
@@ -59,10 +60,10 @@ __device__ bool wait_count(const int* counter, int target, int* status) {
 // kernel, whose CTAs release it right after their prologue, the combine's
 // CTAs run on SMs the decode kernel has finished with and merge a group as
 // soon as both CTAs of every chunk of it have counted their partial.
-template <bool kF32>  // fp32 partials (partial_f32)
+template <int kFormat>  // of the partials (part_format)
 __global__ void __launch_bounds__(kThreads, 4)
 combine_kernel(Problem p, Layout lay, char* __restrict__ ws) {
-  constexpr bool kB16 = kPartialBf16 && !kF32;
+  constexpr bool kF32 = kFormat == kPartF32 || (kFormat == kPartBf16 && !kPartialBf16);
   constexpr int kUnits = kF32 ? kPartUnitsF32 : kPartUnits;
   constexpr int kChunks = kF32 ? 1 : kBatch;  // a round trip: the registers of two of bf16
   int* status = reinterpret_cast<int*>(ws) + kHdrStatus;
@@ -131,16 +132,21 @@ combine_kernel(Problem p, Layout lay, char* __restrict__ ws) {
           sum += w;
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            // bf16: dim e is the low half of word e / 2 for even e, the high half for odd e
-            const float xe = kB16 ? __uint_as_float((e & 1) ? (xw[u][e >> 1] & 0xFFFF0000u)
-                                                            : (xw[u][e >> 1] << 16))
-                                  : __uint_as_float(xw[u][e]);
+            // 16 bits: dim e is the low half of word e / 2 for even e, the high half for odd e
+            float xe;
+            if constexpr (kF32)
+              xe = __uint_as_float(xw[u][e]);
+            else if constexpr (kFormat == kPartF16)
+              xe = __half2float(__ushort_as_half((unsigned short)((e & 1) ? xw[u][e >> 1] >> 16 : xw[u][e >> 1])));
+            else
+              xe = __uint_as_float((e & 1) ? (xw[u][e >> 1] & 0xFFFF0000u) : (xw[u][e >> 1] << 16));
             acc[e] += w * xe;
           }
         }
         m = m_new;
       }
-      const float s2 = sum > 0.f ? run_bmm2(p) / sum : 0.f;
+      float s2 = sum > 0.f ? run_bmm2(p) / sum : 0.f;
+      if constexpr (kFormat == kPartF16) s2 *= 1.f / (1 << part_shift(p.kv_dtype));
       const size_t grow = (size_t)c.q_start * H + (size_t)c.g * R + r;
       __nv_bfloat162 o[8];
 #pragma unroll
@@ -167,8 +173,11 @@ cudaError_t launch_combine(const Problem& p, const Layout& lay, void* ws, int gr
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return partial_f32(p.kv_dtype, p.window) ? cudaLaunchKernelEx(&cfg, combine_kernel<true>, p, lay, static_cast<char*>(ws))
-                        : cudaLaunchKernelEx(&cfg, combine_kernel<false>, p, lay, static_cast<char*>(ws));
+  const PartFormat f = part_format(p.kv_dtype, p.window);
+  auto kernel = f == kPartF32   ? combine_kernel<kPartF32>
+                : f == kPartF16 ? combine_kernel<kPartF16>
+                                : combine_kernel<kPartBf16>;
+  return cudaLaunchKernelEx(&cfg, kernel, p, lay, static_cast<char*>(ws));
 }
 
 }  // namespace mla

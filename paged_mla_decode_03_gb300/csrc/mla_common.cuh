@@ -78,7 +78,7 @@ __device__ __forceinline__ float run_bmm2(const Problem& p) {
 // [kv_begin, kv_end).  Under sparse top-k selection R = H (one token, q_start
 // + g) and [kv_begin, kv_end) indexes the token's position list.
 // slot < 0: the item covers the whole KV range and writes `out` directly;
-// otherwise it writes a normalised partial (bf16 O, fp32 natural-log LSE) into
+// otherwise it writes a normalised partial (O by part_format, fp32 natural-log LSE) into
 // partial slot `slot` for the combine kernel.
 struct WorkItem {
   int b, g, kv_begin, kv_end;
@@ -200,13 +200,21 @@ constexpr size_t kPartBytesPerRow = 32 * kPartUnits * 16;
 __host__ __device__ inline size_t part_unit(size_t slot, int R, int c, int u, int q) {
   return ((slot * 32 + (size_t)c) * kPartUnits + (size_t)u) * (size_t)R + (size_t)q;
 }
-// Windowed runs over a bf16 cache, whose P is rounded to bf16 too, keep fp32 partials,
-// four units a chunk (with bf16 ones a split row's error was 0.0027 of its norm, 1.6
-// times that of the output's own rounding).
-__host__ __device__ inline bool partial_f32(int kv_dtype, int window) { return window > 0 && kv_dtype == 0; }
+// Runs on the MMAs across CTA pairs, whose bf16 partials were an error of 0.0021 (4 bits) and
+// 0.0027 (bf16) of a split row's norm beside the 0.0017 of the output's own rounding, keep
+//  * over 4 bits and e4m3 f16 ones times 2^part_shift, laid out as the bf16 ones.  V, and so
+//    O, is at most 2688 and 448 there, so they are in range, off by 2^-11 of the value at most from
+//    2^-18 (e4m3: 2^-21) up and by 2^-29 (2^-32) below: 0.0017.  (fp32 ones, as near: 64 x 128
+//    heads over 4 bits 111 us a call instead of 102, 8 x 2 x 128 heads 391 instead of 376.)
+//  * over bf16, whose values have no such bound, fp32 ones, four units a chunk: 0.0022.
+enum PartFormat { kPartBf16, kPartF16, kPartF32 };
+__host__ __device__ inline PartFormat part_format(int kv_dtype, int window) {
+  return !pair_mma(kv_dtype, window) ? kPartBf16 : kv_dtype == kKvFp8 || kv_dtype == kKvFp4 ? kPartF16 : kPartF32;
+}
+__host__ __device__ constexpr int part_shift(int kv_dtype) { return kv_dtype == kKvFp4 ? 4 : 7; }
 constexpr int kPartUnitsF32 = 4;
 __host__ __device__ inline size_t part_row_bytes(int kv_dtype, int window) {
-  return partial_f32(kv_dtype, window) ? 32 * kPartUnitsF32 * 16 : kPartBytesPerRow;
+  return part_format(kv_dtype, window) == kPartF32 ? 32 * kPartUnitsF32 * 16 : kPartBytesPerRow;
 }
 __host__ __device__ inline size_t part_unit_f32(size_t slot, int R, int c, int u, int q) {
   return ((slot * 32 + (size_t)c) * kPartUnitsF32 + (size_t)u) * (size_t)R + (size_t)q;

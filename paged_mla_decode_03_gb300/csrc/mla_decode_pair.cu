@@ -105,6 +105,7 @@ template <int kCache> struct Cfg {
   static constexpr uint32_t kScaleBytes = kCache == kFp4 ? kFp4ScaleBytes : 0;
   static constexpr uint32_t kVBytes = kCache == kFp4 ? 128 : 256;  // codes of 256 dims
   static constexpr uint32_t kRowBytes = kCodeBytes + kScaleBytes;
+  static constexpr int kPartShift = part_shift(kCache == kFp4 ? kKvFp4 : kKvFp8);
   // V: 64-dim chunks of the tile's 64 rows; TMA brings a half's four chunks together,
   // so there they are of 32 rows, a half after the other
   static constexpr uint32_t kVChunkStep = kTma ? kVChunk / 2 : kVChunk;
@@ -920,7 +921,7 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
       }
       if (!wait_bar(c, PV_DONE0 + ((g - 1) & 1), ((g - 1) >> 1) & 1)) goto fail_soft;
       tc_fence_after();
-      const float s2 = it.slot < 0 ? inv * bmm2 : inv;
+      const float s2 = it.slot < 0 ? inv * bmm2 : C::kTma ? inv : inv * (1 << C::kPartShift);
       // columns of O, V dims 256 hh + 128 grp + [0, 128), 16 at a time
 #pragma unroll 1
       for (int k = 0; k < 8; ++k) {
@@ -928,27 +929,32 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
         tmem_ld_32x32b_x16(tm + TM_O + 128 * grp + 16 * k, x);
         tmem_wait_ld();
         if (!row_ok) continue;
-        if (C::kTma && it.slot >= 0) {  // (partial_f32: the bf16 kernel has windows alone)
+        const int chunk = 16 * hh + 8 * grp + k;  // of 16 dims
+        if (C::kTma && it.slot >= 0) {  // fp32 (part_format)
 #pragma unroll
           for (int u = 0; u < 4; ++u)
-            part_o[part_unit_f32(it.slot, kRows, 16 * hh + 8 * grp + k, u, q)] =
+            part_o[part_unit_f32(it.slot, kRows, chunk, u, q)] =
                 make_uint4(__float_as_uint(__uint_as_float(x[4 * u]) * s2), __float_as_uint(__uint_as_float(x[4 * u + 1]) * s2),
                            __float_as_uint(__uint_as_float(x[4 * u + 2]) * s2), __float_as_uint(__uint_as_float(x[4 * u + 3]) * s2));
           continue;
         }
         uint32_t o[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(x[2 * e]) * s2,
-                                                         __uint_as_float(x[2 * e + 1]) * s2);
-          o[e] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        const int chunk = 16 * hh + 8 * grp + k;  // of 16 dims
         uint4 *d0, *d1;
         if (it.slot < 0) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(x[2 * e]) * s2,
+                                                           __uint_as_float(x[2 * e + 1]) * s2);
+            o[e] = *reinterpret_cast<const uint32_t*>(&h);
+          }
           d0 = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.out) + grow * kVDim + 16 * chunk);
           d1 = d0 + 1;
-        } else {
+        } else {  // f16, times 2^kPartShift
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const __half2 h = __floats2half2_rn(__uint_as_float(x[2 * e]) * s2, __uint_as_float(x[2 * e + 1]) * s2);
+            o[e] = *reinterpret_cast<const uint32_t*>(&h);
+          }
           d0 = part_o + part_unit(it.slot, kRows, chunk, 0, q);
           d1 = part_o + part_unit(it.slot, kRows, chunk, 1, q);
         }

@@ -68,7 +68,7 @@ def test_partials_and_query_split_have_their_room(tmp_path):
 
 def test_the_plan_follows_the_kernels_conditions(tmp_path):
     def change(text):
-        text, n = re.subn(r"(bool partial_f32\([^)]*\) \{ return )[^;]*;", r"\1kv_dtype == 1;", text)
+        text, n = re.subn(r"(PartFormat part_format\([^)]*\) \{\s*return )[^;]*;", r"\1kv_dtype == 1 ? kPartF32 : kPartBf16;", text)
         text, m = re.subn(r"(bool fp8_mma\([^)]*\) \{\s*return )[^;]*;", r"\1window == 1;", text)
         assert n == 1 and m == 1
         return text
