@@ -400,6 +400,7 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
   // offset 0 of its window.  A block placed otherwise reports and leaves.
   extern __shared__ __align__(1024) unsigned char sm[];
   if ((smem_u32(sm) & 1023) != 0) {
+    pdl_wait();  // the partitioner writes the whole status word
     if (threadIdx.x == 0) atomicOr(reinterpret_cast<int*>(ws) + kHdrStatus, kStatusTimeout);
     return;
   }

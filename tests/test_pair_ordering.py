@@ -21,6 +21,14 @@ def _function(text, name):
     return text[at:end]
 
 
+def test_no_status_is_reported_before_the_partitioner_has_written_the_word():
+    """The partitioner releases the decode kernel at its start and stores the whole word later."""
+    src = _read("mla_decode_pair.cu")
+    body = src[src.index("decode_pair_kernel(const Problem p"):src.index("cudaLaunchConfig_t pair_launch(")]
+    first = re.search(r"kHdrStatus[^;]*kStatus\w+", body).start()
+    assert "pdl_wait()" in body[:first]
+
+
 def test_arrivals_at_the_other_cta_release_at_cluster_scope():
     body = _function(_read("sm100_ptx.cuh"), "mbar_arrive_pair")
     arrive = body.index("mbarrier.arrive.")
