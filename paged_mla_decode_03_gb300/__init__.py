@@ -498,17 +498,17 @@ def decode(query: torch.Tensor, kv_cache: torch.Tensor, workspace_buffer: torch.
     and multiply on bf16 tensor cores instead of the FP8 ones (see
     ``mla_decode_params.e4m3_widen`` in ``include/mla_decode.h``).
     ``window`` > 0: a query row sees the last ``window`` rows up to its bound, and
-    the first ``sinks`` rows.
+    the first ``sinks`` rows.  Over a 4-bit cache and with a window every tensor has to be
+    contiguous, of its type and count and on the query's device (ValueError).
     """
     if query.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or not query.is_cuda:
         raise ValueError("query must be a bf16 or float8_e4m3fn CUDA tensor")
     q_dtype = "bf16" if query.dtype == torch.bfloat16 else "e4m3"
     kv_cache, kind = _cache_kind(kv_cache)
     kv_dtype = ("bf16", "e4m3", "fp4")[kind]
-    if (kind == KV_FP4_E2M1 or window) and not (
-            query.is_contiguous() and kv_cache.is_contiguous() and block_tables.is_contiguous()
-            and seq_lens.is_contiguous()):
-        raise ValueError("query, kv_cache, block_tables and seq_lens must be contiguous")
+    if kind == KV_FP4_E2M1 or window:
+        _check_decode(query, kv_cache, workspace_buffer, block_tables, seq_lens, qo_indptr, out,
+                      lse if return_lse else None, causal_seqlens_kv_global)
     packed = qo_indptr is not None
     H = int(query.shape[-2])
     B = int(seq_lens.shape[0])
@@ -614,8 +614,8 @@ def _cache_kind(kv_cache: torch.Tensor) -> Tuple[torch.Tensor, int]:
     return kv_cache, kind
 
 
-# cache_append and cache_gather run every layer of every step, so a call's checks
-# are plain comparisons, and the message is worked out once one has failed.
+# cache_append, cache_gather and decode run every layer of every step, so a call's
+# checks are plain comparisons, and the message is worked out once one has failed.
 
 def _is_int32(t: torch.Tensor, dev: int, shape) -> bool:
     return (t.dtype is torch.int32 and t.get_device() == dev and t.shape == shape
@@ -665,6 +665,40 @@ def _params_of(*key) -> MlaCacheParams:
             _cache_params.clear()
         p = _cache_params[key] = MlaCacheParams(*key)
     return p
+
+
+def _check_decode(query, kv_cache, workspace, block_tables, seq_lens, qo_indptr, out, lse,
+                  global_lens) -> None:
+    """What ``decode`` asks of its tensors over a 4-bit cache or with a window: the kernels
+    take their types, counts and strides for granted."""
+    dev = query.get_device()
+    packed = qo_indptr is not None
+    if not (query.dim() == (3 if packed else 4) and query.shape[-1] == HEAD_DIM_QK
+            and query.is_contiguous()):
+        _refuse("query", query, "a contiguous tensor", dev,
+                ("tokens", "heads", 576) if packed else ("batch", "tokens", "heads", 576))
+    if kv_cache.get_device() != dev or not kv_cache.is_contiguous():
+        _refuse("kv_cache", kv_cache, "a contiguous tensor", dev, kv_cache.shape)
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        _refuse("workspace_buffer", workspace, "a contiguous tensor", dev, workspace.shape)
+    batch = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
+    if batch < 0 or not _is_int32(seq_lens, dev, (batch,)):
+        _refuse("seq_lens", seq_lens, _INT32, dev, ("batch",))
+    if not packed and query.shape[0] != batch:
+        raise ValueError(f"query holds {query.shape[0]} requests, seq_lens {batch}")
+    if block_tables.dim() != 2 or not _is_int32(block_tables, dev, (batch, block_tables.shape[1])):
+        _refuse("block_tables", block_tables, _INT32, dev, (batch, "pages"))
+    if packed and not _is_int32(qo_indptr, dev, (batch + 1,)):
+        _refuse("qo_indptr", qo_indptr, _INT32, dev, (batch + 1,))
+    if global_lens is not None and not _is_int32(global_lens, dev, (batch,)):
+        _refuse("causal_seqlens_kv_global", global_lens, _INT32, dev, (batch,))
+    rows = query.numel() // HEAD_DIM_QK
+    if out is not None and not (out.dtype is torch.bfloat16 and out.get_device() == dev
+                                and out.numel() == rows * HEAD_DIM_V and out.is_contiguous()):
+        _refuse("out", out, "a contiguous bf16 tensor", dev, (*query.shape[:-1], HEAD_DIM_V))
+    if lse is not None and not (lse.dtype is torch.float32 and lse.get_device() == dev
+                                and lse.numel() == rows and lse.is_contiguous()):
+        _refuse("lse", lse, "a contiguous fp32 tensor", dev, query.shape[:-1])
 
 
 def _cache_call(kv_cache, block_tables, seq_lens, qo_indptr, q_len, total_q, status):
