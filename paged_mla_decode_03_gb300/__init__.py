@@ -17,6 +17,7 @@ quantisation) and forms their query, ``cache_gather`` reads rows back, and
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Dict, Optional, Tuple
@@ -647,6 +648,18 @@ def _stream_of(stream, dev: int) -> int:
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
 
 
+def _made_on(stream, dev: int):
+    """A context whose allocations and copies belong to ``stream``, where a call that was
+    given one runs: memory of the current stream may still be in use there, and would be
+    given away while the kernel writes it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = (torch.cuda.ExternalStream(stream, device=torch.device("cuda", dev)) if stream > 1
+                  else torch.cuda.default_stream(dev))  # (0 and 1: the legacy default stream)
+    return torch.cuda.stream(stream)
+
+
 try:  # the same handle without the Stream object around it (a microsecond and a half less)
     from torch._C import _cuda_getCurrentRawStream as _raw_stream
 except ImportError:  # pragma: no cover - a torch without CUDA
@@ -747,7 +760,8 @@ def rope_table(max_position: int, *, base: float = 10000.0, scaling: Optional[st
     ``factor``) or ``"yarn"`` (frequencies that turn fewer than ``beta_slow``
     times over ``original_max_position`` divided by ``factor``, those that turn
     more than ``beta_fast`` times kept, a linear blend between).  ``amplitude``
-    multiplies cosines and sines."""
+    multiplies cosines and sines.  The table is made on ``stream`` (the current one) and
+    belongs to it."""
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"scaling must be one of {list(ROPE_SCALINGS)}, got {scaling!r}")
     dev = torch.device("cuda" if device is None else device)
@@ -759,7 +773,8 @@ def rope_table(max_position: int, *, base: float = 10000.0, scaling: Optional[st
                       amplitude=amplitude, factor=factor,
                       original_max_position=original_max_position, beta_fast=beta_fast,
                       beta_slow=beta_slow)
-    table = torch.empty((max(max_position, 0), 64), dtype=torch.float32, device=dev)
+    with _made_on(stream, dev.index):
+        table = torch.empty((max(max_position, 0), 64), dtype=torch.float32, device=dev)
     rc = _call_on(dev.index, load_library().mla_rope_table, ctypes.byref(p),
                   table.data_ptr() if max_position > 0 else 16, _stream_of(stream, dev.index))
     if rc != MLA_OK:
@@ -790,7 +805,8 @@ def cache_append(latent: torch.Tensor, k_pe: torch.Tensor, kv_cache: torch.Tenso
     ``[T, H, 576]`` (or ``[B, q_len, H, 576]``), made as bf16 when not given;
     an e4m3 one is divided by ``q_scale``; without ``q_nope`` only the RoPE dims
     of a given bf16 ``query`` are written.  ``status``: int32 ``[1]``, contract
-    violations are ORed in (see ``include/mla_decode.h``).  Returns ``query``."""
+    violations are ORed in (see ``include/mla_decode.h``).  Returns ``query``; one that the
+    call makes belongs to ``stream`` (the current one), where the kernel runs."""
     if latent.dim() != 2 or not latent.is_cuda:
         raise ValueError("latent must be a CUDA tensor [tokens, 512]")
     T = latent.shape[0]
@@ -820,7 +836,9 @@ def cache_append(latent: torch.Tensor, k_pe: torch.Tensor, kv_cache: torch.Tenso
         if query is None:
             if q_nope is None:
                 raise ValueError("without q_nope, query must be given (its latent part stays)")
-            query = torch.empty((T, H, HEAD_DIM_QK), dtype=torch.bfloat16, device=latent.device)
+            with _made_on(stream, dev):
+                query = torch.empty((T, H, HEAD_DIM_QK), dtype=torch.bfloat16,
+                                    device=latent.device)
         if query.dtype is torch.float8_e4m3fn:
             q_dtype = Q_FP8_E4M3
         elif query.dtype is not torch.bfloat16:
@@ -859,7 +877,8 @@ def cache_gather(kv_cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: t
     or, packed by ``qo_indptr`` (then ``total_q`` or ``out`` is needed), of its
     last ``qo_indptr[b + 1] - qo_indptr[b]``; the running sum of ``seq_lens``
     reads whole sequences.  Rows of ``out`` that no position belongs to, or whose
-    page id is bad (flagged in ``status``), stay as they were."""
+    page id is bad (flagged in ``status``), stay as they were.  An ``out`` that the call
+    makes belongs to ``stream`` (the current one), where the kernel runs."""
     if total_q is None:
         if out is not None:
             total_q = int(out.shape[0])
@@ -869,7 +888,8 @@ def cache_gather(kv_cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: t
             raise ValueError("total_q is needed for packed rows")
     dev, key = _cache_call(kv_cache, block_tables, seq_lens, qo_indptr, q_len, total_q, status)
     if out is None:
-        out = torch.empty((total_q, HEAD_DIM_QK), dtype=torch.bfloat16, device=kv_cache.device)
+        with _made_on(stream, dev):
+            out = torch.empty((total_q, HEAD_DIM_QK), dtype=torch.bfloat16, device=kv_cache.device)
     elif not (out.dtype is torch.bfloat16 and out.get_device() == dev
               and out.shape == (total_q, HEAD_DIM_QK) and out.is_contiguous()):
         _refuse("out", out, "a contiguous bf16 tensor", dev, (total_q, HEAD_DIM_QK))
