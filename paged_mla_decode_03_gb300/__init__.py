@@ -563,7 +563,8 @@ def merge_states(o_parts: torch.Tensor, lse_parts: torch.Tensor, *, scale: float
     """Merge partial attention states of the same rows by their natural-log
     LSEs (``mla_merge_states``): ``o_parts`` bf16 ``[n, ..., 512]``,
     ``lse_parts`` fp32 ``[n, ...]`` (the leading dims after ``n`` flattened to
-    rows).  Returns ``(out, lse)`` with the parts' row shape."""
+    rows).  Returns ``(out, lse)`` with the parts' row shape; what the call makes belongs to
+    ``stream`` (the current one), where the kernel runs."""
     if o_parts.dtype != torch.bfloat16 or lse_parts.dtype != torch.float32:
         raise TypeError("o_parts must be bf16 and lse_parts fp32")
     if not (o_parts.is_cuda and lse_parts.is_cuda):
@@ -572,15 +573,17 @@ def merge_states(o_parts: torch.Tensor, lse_parts: torch.Tensor, *, scale: float
     row_shape = tuple(o_parts.shape[1:-1])
     if o_parts.shape[-1] != HEAD_DIM_V or tuple(lse_parts.shape) != (n,) + row_shape:
         raise ValueError("o_parts [n, ..., 512] and lse_parts [n, ...] disagree")
-    o_parts = o_parts.contiguous()
-    lse_parts = lse_parts.contiguous()
     rows = 1
     for d in row_shape:
         rows *= int(d)
-    if out is None:
-        out = torch.empty(row_shape + (HEAD_DIM_V,), dtype=torch.bfloat16, device=o_parts.device)
-    if lse is None:
-        lse = torch.empty(row_shape, dtype=torch.float32, device=o_parts.device)
+    with _made_on(stream, o_parts.get_device()):
+        o_parts = o_parts.contiguous()
+        lse_parts = lse_parts.contiguous()
+        if out is None:
+            out = torch.empty(row_shape + (HEAD_DIM_V,), dtype=torch.bfloat16,
+                              device=o_parts.device)
+        if lse is None:
+            lse = torch.empty(row_shape, dtype=torch.float32, device=o_parts.device)
     if stream is None:
         stream = torch.cuda.current_stream().cuda_stream
     elif isinstance(stream, torch.cuda.Stream):

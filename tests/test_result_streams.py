@@ -20,7 +20,10 @@ def _makers():
     tables = torch.arange(T, dtype=torch.int32, device="cuda")[:, None]
     lens = torch.full((T,), 7, dtype=torch.int32, device="cuda")
     table = mla.rope_table(32)
+    parts = torch.randn(2, 512, 300, generator=g).to(torch.bfloat16).cuda().transpose(1, 2)  # (copied by the call)
+    lses = torch.randn(300, 2, generator=g).cuda().t()
     return {
+        "merge": lambda s: mla.merge_states(parts, lses, stream=s)[0],
         "append": lambda s: mla.cache_append(x[:, :512], x[:, 512:], cache, tables, lens, rope_table=table, q_len=1,
                                              q_nope=qn, q_pe=qp, stream=s),
         "gather": lambda s: mla.cache_gather(cache, tables, lens, q_len=1, stream=s),
@@ -42,7 +45,7 @@ def _as(kind, stream):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", ["object", "handle"])
-@pytest.mark.parametrize("name", ["append", "gather", "table"])
+@pytest.mark.parametrize("name", ["append", "gather", "table", "merge"])
 def test_memory_that_the_current_stream_still_uses_is_left_alone(makers, name, kind):
     side = torch.cuda.Stream()
     want = makers[name](None).clone()
@@ -59,7 +62,7 @@ def test_memory_that_the_current_stream_still_uses_is_left_alone(makers, name, k
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", ["object", "handle"])
-@pytest.mark.parametrize("name", ["append", "gather", "table"])
+@pytest.mark.parametrize("name", ["append", "gather", "table", "merge"])
 def test_memory_that_the_kernel_still_writes_is_not_given_away(makers, name, kind):
     side = torch.cuda.Stream()
     shape = makers[name](None)
@@ -74,7 +77,7 @@ def test_memory_that_the_kernel_still_writes_is_not_given_away(makers, name, kin
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("name", ["append", "gather", "table"])
+@pytest.mark.parametrize("name", ["append", "gather", "table", "merge"])
 def test_the_default_stream_by_its_handle(makers, name):
     want = makers[name](None).clone()
     torch.cuda.synchronize()
