@@ -805,8 +805,9 @@ def cache_append(latent: torch.Tensor, k_pe: torch.Tensor, kv_cache: torch.Tenso
     its values are divided by ``kv_scale``.  ``norm_weight`` bf16 ``[512]``:
     RMS norm of the latent first (None: no norm).  ``q_pe`` bf16 ``[T, H, 64]``
     and ``q_nope`` bf16 ``[T, H, 512]`` (strides free) give ``query``
-    ``[T, H, 576]`` (or ``[B, q_len, H, 576]``), made as bf16 when not given;
-    an e4m3 one is divided by ``q_scale``; without ``q_nope`` only the RoPE dims
+    ``[T, H, 576]`` (or ``[B, q_len, H, 576]``), made as bf16 when not given (rows
+    of tokens without a place in the cache are zeros then, and stay as they were in a
+    given one); an e4m3 one is divided by ``q_scale``; without ``q_nope`` only the RoPE dims
     of a given bf16 ``query`` are written.  ``status``: int32 ``[1]``, contract
     violations are ORed in (see ``include/mla_decode.h``).  Returns ``query``; one that the
     call makes belongs to ``stream`` (the current one), where the kernel runs."""
@@ -840,7 +841,7 @@ def cache_append(latent: torch.Tensor, k_pe: torch.Tensor, kv_cache: torch.Tenso
             if q_nope is None:
                 raise ValueError("without q_nope, query must be given (its latent part stays)")
             with _made_on(stream, dev):
-                query = torch.empty((T, H, HEAD_DIM_QK), dtype=torch.bfloat16,
+                query = torch.zeros((T, H, HEAD_DIM_QK), dtype=torch.bfloat16,
                                     device=latent.device)
         if query.dtype is torch.float8_e4m3fn:
             q_dtype = Q_FP8_E4M3
@@ -881,7 +882,7 @@ def cache_gather(kv_cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: t
     last ``qo_indptr[b + 1] - qo_indptr[b]``; the running sum of ``seq_lens``
     reads whole sequences.  Rows of ``out`` that no position belongs to, or whose
     page id is bad (flagged in ``status``), stay as they were.  An ``out`` that the call
-    makes belongs to ``stream`` (the current one), where the kernel runs."""
+    makes has zeros there and belongs to ``stream`` (the current one), where the kernel runs."""
     if total_q is None:
         if out is not None:
             total_q = int(out.shape[0])
@@ -892,7 +893,7 @@ def cache_gather(kv_cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: t
     dev, key = _cache_call(kv_cache, block_tables, seq_lens, qo_indptr, q_len, total_q, status)
     if out is None:
         with _made_on(stream, dev):
-            out = torch.empty((total_q, HEAD_DIM_QK), dtype=torch.bfloat16, device=kv_cache.device)
+            out = torch.zeros((total_q, HEAD_DIM_QK), dtype=torch.bfloat16, device=kv_cache.device)
     elif not (out.dtype is torch.bfloat16 and out.get_device() == dev
               and out.shape == (total_q, HEAD_DIM_QK) and out.is_contiguous()):
         _refuse("out", out, "a contiguous bf16 tensor", dev, (total_q, HEAD_DIM_QK))

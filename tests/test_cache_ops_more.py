@@ -1,0 +1,28 @@
+"""More of cache_append and cache_gather: calls that the first tests leave out."""
+import pytest
+import torch
+
+import paged_mla_decode_03_gb300 as mla
+from test_cache_ops import Setup, close_bf16, new_cache
+
+
+def _dirty(*shapes):
+    """Leaves memory of these shapes full of NaN in the allocator's hands."""
+    for s in [torch.full(shape, float("nan"), dtype=torch.bfloat16, device="cuda") for shape in shapes]:
+        del s
+
+
+@pytest.mark.gpu
+def test_rows_without_a_place_are_zeros_in_tensors_that_the_call_makes():
+    s = Setup("bf16", 32, [40, 5], [3, 2], 16, packed=True, seed=21, pad=4)
+    s.tables[0, 1] = -1  # the page of request 0's tokens
+    cache = new_cache("bf16", s.pages, 32)
+    _dirty((s.T, 16, 576), (s.T, 576))
+    query = mla.cache_append(s.latent, s.k_pe, cache, s.tables, s.lens, rope_table=s.table, norm_weight=s.weight,
+                             q_nope=s.q_nope, q_pe=s.q_pe, **s.which)
+    _, _, q, tq = s.reference()
+    close_bf16(query[3:5], q[3:5], (q.abs() + tq)[3:5], "query")
+    assert (query[:3] == 0).all() and (query[5:] == 0).all()
+    _dirty((s.T, 16, 576), (s.T, 576))
+    rows = mla.cache_gather(cache, s.tables, s.lens, total_q=s.T, **s.which)
+    assert (rows[:3] == 0).all() and (rows[5:] == 0).all() and (rows[3:5] != 0).any(-1).all()
