@@ -267,7 +267,8 @@ __device__ __forceinline__ void append_row(const AppendArgs& a, long long t, int
 #pragma unroll
       for (int e = 0; e < 16; ++e) y[e] = __fmul_rn(y[e], 0x1p-96f);
       ss = sum_of_squares(y);
-      eps = 0.f;  // eps 2^-192 is below every rounding of the sum
+      // (exact, or below every rounding of the mean, which is at least 2^-73 here)
+      eps = __fmul_rn(__fmul_rn(eps, 0x1p-96f), 0x1p-96f);
     }
     const float rstd = __frsqrt_rn(__fadd_rn(__fmul_rn(ss, 1.f / 512.f), eps));
     float w[16];

@@ -26,3 +26,19 @@ def test_rows_without_a_place_are_zeros_in_tensors_that_the_call_makes():
     _dirty((s.T, 16, 576), (s.T, 576))
     rows = mla.cache_gather(cache, s.tables, s.lens, total_q=s.T, **s.which)
     assert (rows[:3] == 0).all() and (rows[5:] == 0).all() and (rows[3:5] != 0).any(-1).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("power,eps", [(60, 1e-6), (60, 2.0 ** 100), (60, 2.0 ** 127), (62, 3e38), (70, 3e38), (100, 3e38), (0, 3e38)])
+def test_an_eps_beside_a_sum_past_the_range(power, eps):
+    """Latents whose squares' sum passes fp32's range, with an eps that counts beside their mean."""
+    s = Setup("bf16", 32, [40], [3], 16, packed=False, seed=22)
+    g = torch.Generator().manual_seed(23)
+    x = torch.randn(3, 576, generator=g)
+    x[:, :512] *= 2.0 ** power
+    x = x.to(torch.bfloat16).cuda()
+    s.latent, s.k_pe = x[:, :512], x[:, 512:]
+    cache = new_cache("bf16", s.pages, 32)
+    mla.cache_append(s.latent, s.k_pe, cache, s.tables, s.lens, rope_table=s.table, norm_weight=s.weight, eps=eps, q_len=3)
+    y, ty, _, _ = s.reference(eps=float(torch.tensor(eps, dtype=torch.float32)))
+    s.check(cache, y, ty, 1.0, "bf16")
