@@ -260,13 +260,16 @@ __device__ __forceinline__ void append_row(const AppendArgs& a, long long t, int
   widen8(x1, y + 8);
   widen8(xr, r);
   if (a.norm_weight) {
-    float ss = sum_of_squares(y), eps = a.eps;
-    // latents near the top of bf16's range: the same on a scale of 2^-96 (no
-    // lane diverges: the sum is the warp's)
+    float ss = sum_of_squares(y), eps = a.eps, back = 1.f;
+    // latents near the top of bf16's range: the mean on a scale of 2^-192, and so rstd
+    // on one of 2^96 (no lane diverges: the sum is the warp's; the latents themselves
+    // stay as they are, small ones beside them would lose bits)
     if (ss > 3.4028235e38f) {
+      float z[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) y[e] = __fmul_rn(y[e], 0x1p-96f);
-      ss = sum_of_squares(y);
+      for (int e = 0; e < 16; ++e) z[e] = __fmul_rn(y[e], 0x1p-96f);
+      ss = sum_of_squares(z);
+      back = 0x1p-96f;
       // (exact, or below every rounding of the mean, which is at least 2^-73 here)
       eps = __fmul_rn(__fmul_rn(eps, 0x1p-96f), 0x1p-96f);
     }
@@ -275,7 +278,7 @@ __device__ __forceinline__ void append_row(const AppendArgs& a, long long t, int
     widen8(w0, w);
     widen8(w1, w + 8);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) y[e] = __fmul_rn(__fmul_rn(y[e], rstd), w[e]);
+    for (int e = 0; e < 16; ++e) y[e] = __fmul_rn(__fmul_rn(__fmul_rn(y[e], rstd), back), w[e]);
   }
   turn8(r, turn, u, a.half_style);
   if (kKv == MLA_KV_BF16) {

@@ -42,3 +42,19 @@ def test_an_eps_beside_a_sum_past_the_range(power, eps):
     mla.cache_append(s.latent, s.k_pe, cache, s.tables, s.lens, rope_table=s.table, norm_weight=s.weight, eps=eps, q_len=3)
     y, ty, _, _ = s.reference(eps=float(torch.tensor(eps, dtype=torch.float32)))
     s.check(cache, y, ty, 1.0, "bf16")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("power", [65, 70, 120])
+def test_small_latents_beside_huge_ones(power):
+    s = Setup("bf16", 32, [40], [2], 16, packed=False, seed=24)
+    g = torch.Generator().manual_seed(25)
+    x = torch.randn(2, 576, generator=g)
+    x[:, :512:2] *= 2.0 ** power
+    x[:, 1:512:2] *= 2.0 ** (power - 118)  # normed: about 2^-118
+    x = x.to(torch.bfloat16).cuda()
+    s.latent, s.k_pe = x[:, :512], x[:, 512:]
+    cache = new_cache("bf16", s.pages, 32)
+    mla.cache_append(s.latent, s.k_pe, cache, s.tables, s.lens, rope_table=s.table, norm_weight=s.weight, q_len=2)
+    y, ty, _, _ = s.reference()
+    s.check(cache, y, ty, 1.0, "bf16")
