@@ -145,7 +145,9 @@ combine_kernel(Problem p, Layout lay, char* __restrict__ ws) {
         }
         m = m_new;
       }
-      float s2 = sum > 0.f ? run_bmm2(p) / sum : 0.f;
+      // 0: the empty sum.  (A NaN is none; in bf16 partials it has always been taken for one.)
+      const bool any = kFormat == kPartBf16 ? sum > 0.f : sum != 0.f;
+      float s2 = any ? run_bmm2(p) / sum : 0.f;
       if constexpr (kFormat == kPartF16) s2 *= 1.f / (1 << part_shift(p.kv_dtype));
       const size_t grow = (size_t)c.q_start * H + (size_t)c.g * R + r;
       __nv_bfloat162 o[8];
@@ -156,7 +158,7 @@ combine_kernel(Problem p, Layout lay, char* __restrict__ ws) {
       dst[0] = *reinterpret_cast<uint4*>(o);
       dst[1] = *reinterpret_cast<uint4*>(o + 4);
       const float m_use = (m == -INFINITY) ? 0.f : m;
-      if (p.return_lse && t == 0) p.lse[grow] = (sum > 0.f) ? m_use + logf(sum) : -INFINITY;
+      if (p.return_lse && t == 0) p.lse[grow] = any ? m_use + logf(sum) : -INFINITY;
     }
   }
 }

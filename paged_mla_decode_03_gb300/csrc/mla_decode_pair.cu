@@ -911,8 +911,9 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
         l_row = joined(0);
         r_row = C::kTma ? joined(256) : l_row;
       }
-      const float lse = l_row > 0.f ? (m_fin - C::kPShift + log2f(l_row)) * kLn2 : -INFINITY;
-      const float inv = r_row > 0.f ? 1.f / r_row : 0.f;
+      // (0: the row sees nothing; a NaN among its scores stays one)
+      const float lse = l_row != 0.f ? (m_fin - C::kPShift + log2f(l_row)) * kLn2 : -INFINITY;
+      const float inv = r_row != 0.f ? 1.f / r_row : 0.f;
       const size_t grow = (size_t)it.q_start * H + row0 + q;
       if (row_ok && hh == 0 && grp == 0) {
         if (it.slot >= 0)
