@@ -462,13 +462,14 @@ typedef struct mla_cache_params {
  * total_q      tokens (fixed: batch * q_len).  Packed: rows at or past
  *              qo_indptr[B] are padding: nothing is written for them.  qo_indptr
  *              must not decrease; a request may have no token.
- * kv_scale     > 0; 1 for a bf16 cache
+ * kv_scale     a normal fp32 number > 0, which divides as the product with its fp32
+ *              reciprocal; 1 for a bf16 cache
  * kv_cache     the pages, by kv_dtype; only the tokens' rows are written
  * q_pe, query  both or neither: [total_q][H] rows of 64 by the strides, and
  *              bf16 or e4m3 [total_q, H, 576] contiguous
  * q_nope       [total_q][H] rows of 512 by the strides; NULL (bf16 query only)
  *              leaves dims [0, 512) of `query` as they are
- * q_scale      > 0; 1 for a bf16 query
+ * q_scale      as kv_scale; 1 for a bf16 query
  * status       int32 device word or NULL: bits of mla_decode_status_offset are
  *              ORed in (2: a bad qo_indptr, 1: a bad length, 16: a page id out
  *              of [0, num_pages), 128: a rotation position out of the table).

@@ -498,7 +498,8 @@ int row_map(const mla_cache_params* p, const void* cache, const int32_t* block_t
   return MLA_OK;
 }
 
-bool scale_ok(float v) { return v > 0.f && v <= 3.0e38f; }
+// Quantising multiplies by the reciprocal, which a subnormal scale would not have.
+bool scale_ok(float v) { return v >= 1.17549435e-38f && v <= 3.0e38f; }
 
 template <int kKv>
 void launch_append(const AppendArgs& a, bool q_fp8, unsigned blocks, cudaStream_t s) {
