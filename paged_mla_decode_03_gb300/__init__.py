@@ -396,6 +396,9 @@ class Plan:
                  return_lse: bool = False, device: int = 0, q_dtype: str = "bf16",
                  cp_world: int = 1, cp_rank: int = 0, sparse_top_k: int = 0,
                  e4m3_widen: bool = False, window: int = 0, sinks: int = 0):
+        for name, v in (("window", window), ("sinks", sinks)):
+            if not -2 ** 31 <= v < 2 ** 31:  # (ctypes would cut it to its low 32 bits)
+                raise ValueError(f"{name} = {v} does not fit 32 bits")
         self.params = MlaDecodeParams(
             batch=batch, num_heads=num_heads, max_seq_len_q=max_seq_len_q,
             max_seq_len=max_seq_len, page_size=page_size, max_pages_per_req=max_pages_per_req,
