@@ -3,7 +3,7 @@ import pytest
 import torch
 
 import paged_mla_decode_03_gb300 as mla
-from test_cache_ops import Setup, close_bf16, new_cache
+from test_cache_ops import Setup, close_bf16, close_e4m3, new_cache
 
 
 def _dirty(*shapes):
@@ -58,3 +58,23 @@ def test_small_latents_beside_huge_ones(power):
     mla.cache_append(s.latent, s.k_pe, cache, s.tables, s.lens, rope_table=s.table, norm_weight=s.weight, q_len=2)
     y, ty, _, _ = s.reference()
     s.check(cache, y, ty, 1.0, "bf16")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "fp4"])
+@pytest.mark.parametrize("q_fp8", [False, True])
+@pytest.mark.parametrize("heads,packed", [(16, False), (128, True)])
+def test_every_cache_with_every_query(kind, q_fp8, heads, packed):
+    s = Setup(kind, 64, [70, 64, 3], [3, 3, 3], heads, packed=packed, seed=26, style="half", pad=2 if packed else 0)
+    cache = new_cache(kind, s.pages, 64)
+    query = torch.full((s.T, heads, 576), 3.0, dtype=torch.bfloat16, device="cuda")
+    if q_fp8:
+        query = query.to(torch.float8_e4m3fn)
+    kvs, qsc = (0.0125 if kind == "e4m3" else 1.0), (0.0110 if q_fp8 else 1.0)
+    mla.cache_append(s.latent, s.k_pe, cache, s.tables, s.lens, rope_table=s.table, norm_weight=s.weight,
+                     rope_style="half", kv_scale=kvs, q_nope=s.q_nope, q_pe=s.q_pe, query=query, q_scale=qsc, **s.which)
+    y, ty, q, tq = s.reference()
+    s.check(cache, y, ty, kvs, kind)
+    inv = float(torch.tensor(1.0 / qsc, dtype=torch.float32))
+    (close_e4m3 if q_fp8 else close_bf16)(query[:s.n], q * inv, (q.abs() + tq) * inv, "query")
+    assert (query[s.n:].float() == 3.0).all()
