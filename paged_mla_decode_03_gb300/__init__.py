@@ -38,6 +38,9 @@ HEAD_DIM_V = 512
 MLA_OK = 0
 MLA_STATIC_WORKSPACE_BYTES = 48 * 1024 * 1024  # scratch of mla_decode_run_static_workspace
 KV_BF16, KV_FP8_E4M3, KV_FP4_E2M1 = 0, 1, 2
+KV_DTYPES = {"bf16": KV_BF16, "bfloat16": KV_BF16, torch.bfloat16: KV_BF16,
+             "e4m3": KV_FP8_E4M3, "fp8": KV_FP8_E4M3, torch.float8_e4m3fn: KV_FP8_E4M3,
+             "fp4": KV_FP4_E2M1, "e2m1": KV_FP4_E2M1}
 FP4_ROW_BYTES = 324  # a 4-bit cache row: 288 bytes of e2m1 codes, 36 e4m3 scales
 ROPE_STYLES = {"interleaved": 0, "half": 1}
 ROPE_SCALINGS = {None: 0, "linear": 1, "yarn": 2}
@@ -396,6 +399,8 @@ class Plan:
                  return_lse: bool = False, device: int = 0, q_dtype: str = "bf16",
                  cp_world: int = 1, cp_rank: int = 0, sparse_top_k: int = 0,
                  e4m3_widen: bool = False, window: int = 0, sinks: int = 0):
+        if kv_dtype not in KV_DTYPES:
+            raise ValueError(f"kv_dtype must be one of {list(KV_DTYPES)}, got {kv_dtype!r}")
         for name, v in (("window", window), ("sinks", sinks)):
             if not -2 ** 31 <= v < 2 ** 31:  # (ctypes would cut it to its low 32 bits)
                 raise ValueError(f"{name} = {v} does not fit 32 bits")
@@ -403,8 +408,7 @@ class Plan:
             batch=batch, num_heads=num_heads, max_seq_len_q=max_seq_len_q,
             max_seq_len=max_seq_len, page_size=page_size, max_pages_per_req=max_pages_per_req,
             num_pages=num_pages, packed=int(bool(packed)), max_total_q=max_total_q,
-            kv_dtype=(KV_FP8_E4M3 if kv_dtype in ("e4m3", "fp8", torch.float8_e4m3fn)
-                      else KV_FP4_E2M1 if kv_dtype in ("fp4", "e2m1") else KV_BF16),
+            kv_dtype=KV_DTYPES[kv_dtype],
             mask=MASK_CAUSAL if causal else MASK_DENSE, return_lse=int(bool(return_lse)),
             device=device,
             q_dtype=Q_FP8_E4M3 if q_dtype in ("e4m3", "fp8", torch.float8_e4m3fn) else Q_BF16,
