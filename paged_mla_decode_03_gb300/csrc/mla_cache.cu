@@ -8,9 +8,9 @@
 //   query row h = quantise([q_nope_h, R_p q_pe_h] / q_scale)
 // R_p turns each pair (a, b) into (a c - b s, b c + a s), with c and s from
 // row p of a table.  Every step is a separately rounded fp32 operation and the
-// sum of squares carries its rounding error along (two fp32 words), so rstd is
-// the correctly rounded one and a row does not depend on how the sum is split
-// over lanes; only the quantisation rounds further.
+// sum of squares carries its rounding error along (two fp32 words), so the mean is
+// the rounded exact one and a row does not depend on how the sum is split over
+// lanes.  (rstd has two roundings more, of mean + eps and of the root.)
 //
 // What bounds it: bytes.  A token moves 1152 B in and 324-1152 B out for the
 // cache row and, per head, 1152 B in and 576 or 1152 B out for the query, with

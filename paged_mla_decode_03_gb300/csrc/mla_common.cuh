@@ -165,7 +165,7 @@ constexpr long long kOverheadTilesPair = 5;
 // costs little more than an even share of the work, and cutting would add an
 // item's overhead to every worker, the partials' round trip and the combine's
 // tail (some 6 us), together about kCutTiles tiles.  For 64 groups of 18 tiles on
-// 76 workers: 18 + 3 units uncut against 17.7 + 3 + 6.  Asked for sliding windows
+// 76 workers: 18 + 5 units uncut against an even share of 64 x 23 / 76 = 19.4 and 6.  Asked for sliding windows
 // (whose groups are nearly equal) and the 4-bit cache; the other plans keep the
 // partition they have always had.
 constexpr long long kCutTiles = 6;

@@ -37,11 +37,12 @@
 // conflicts a long call took 476 us instead of 417.)  bf16 rows come by TMA where the
 // MMAs read them.
 //
-// Measured, a call: 8 x 2 x 128 heads over 64-128k rows of 4 bits 372 us, 1.09 PFLOP/s
-// (57% of the bf16 rate of a large library product; tensor pipes busy 46% of all cycles,
-// shared memory some 90% of a tile's); 64 x 128 heads over 1-8k rows 101 us, 789 TFLOP/s;
-// window 4096, e4m3, 32 x 4 x 128 heads 181 us, 805 TFLOP/s; window 1024, bf16, 64 x 128
-// heads 38.7 us, of which some 12 are the launch chain, the first loads and the epilogue.
+// Measured, a call: 8 x 2 x 128 heads over 64-128k rows of 4 bits 377 us, 1.08 PFLOP/s
+// (56% of the bf16 rate of a large library product; tensor pipes busy 45% of all cycles,
+// shared memory some 90% of a tile's, bank conflicts among them); 64 x 128 heads over 1-8k
+// rows 103 us, 779 TFLOP/s; window 4096, e4m3, 32 x 4 x 128 heads 182 us, 801 TFLOP/s;
+// window 1024, bf16, 64 x 128 heads 38.8 us, of which some 12 are the launch chain, the
+// first loads and the epilogue.
 //
 // Warp roles (896 threads): 0 and 3 copy, 1 issues QK (even CTA) and owns TMEM, 2
 // issues PV, 4-11 softmax, correction and epilogue, 12-27 conversion and query
