@@ -518,35 +518,37 @@ def decode(query: torch.Tensor, kv_cache: torch.Tensor, workspace_buffer: torch.
         _check_decode(query, kv_cache, workspace_buffer, block_tables, seq_lens, qo_indptr, out,
                       lse if return_lse else None, causal_seqlens_kv_global)
     packed = qo_indptr is not None
-    H = int(query.shape[-2])
-    B = int(seq_lens.shape[0])
+    q_shape = query.shape
+    H = q_shape[-2]
+    B = seq_lens.shape[0]
+    pages, page_size, _ = kv_cache.shape
+    width = block_tables.shape[1]
+    dev = query.get_device()
     if packed:
         if max_seq_len_q is None:
             raise ValueError("max_seq_len_q is required for packed launches")
-        total_q = int(query.shape[0])
+        total_q = q_shape[0]
         sq = int(max_seq_len_q)
         out_shape = (total_q, H, HEAD_DIM_V)
         lse_shape = (total_q, H)
     else:
         total_q = 0
-        sq = int(query.shape[1])
+        sq = q_shape[1]
         out_shape = (B, sq, H, HEAD_DIM_V)
         lse_shape = (B * sq, H)
     causal = mask_type == "causal"
     if mask_type not in ("causal", "dense"):
         raise ValueError(mask_type)
     top_k = int(sparse_indices.shape[-1]) if sparse_indices is not None else 0
-    key = (B, H, sq, int(max_seq_len), int(kv_cache.shape[1]), int(block_tables.shape[1]),
-           int(kv_cache.shape[0]), packed, total_q if packed else 0, kv_dtype, causal,
-           bool(return_lse), query.device.index or 0, q_dtype, int(cp_world), int(cp_rank),
-           top_k, bool(e4m3_widen), int(window), int(sinks))
+    key = (B, H, sq, int(max_seq_len), page_size, width, pages, packed, total_q, kv_dtype, causal,
+           bool(return_lse), dev, q_dtype, int(cp_world), int(cp_rank), top_k, bool(e4m3_widen),
+           int(window), int(sinks))
     plan = _plans.get(key)
     if plan is None:
         plan = Plan(batch=B, num_heads=H, max_seq_len_q=sq, max_seq_len=int(max_seq_len),
-                    page_size=int(kv_cache.shape[1]), max_pages_per_req=int(block_tables.shape[1]),
-                    num_pages=int(kv_cache.shape[0]), packed=packed, max_total_q=total_q,
-                    kv_dtype=kv_dtype, causal=causal, return_lse=return_lse,
-                    device=query.device.index or 0, q_dtype=q_dtype, cp_world=int(cp_world),
+                    page_size=page_size, max_pages_per_req=width, num_pages=pages, packed=packed,
+                    max_total_q=total_q, kv_dtype=kv_dtype, causal=causal, return_lse=return_lse,
+                    device=dev, q_dtype=q_dtype, cp_world=int(cp_world),
                     cp_rank=int(cp_rank), sparse_top_k=top_k, e4m3_widen=e4m3_widen,
                     window=int(window), sinks=int(sinks))
         _plans[key] = plan
@@ -558,7 +560,7 @@ def decode(query: torch.Tensor, kv_cache: torch.Tensor, workspace_buffer: torch.
         lse = torch.empty(lse_shape, dtype=torch.float32, device=query.device)
     plan.run(query, kv_cache, block_tables, seq_lens, out, qo_indptr=qo_indptr, total_q=total_q,
              lse=lse if return_lse else None, workspace=workspace_buffer,
-             bmm1_scale=bmm1_scale, bmm2_scale=bmm2_scale,
+             bmm1_scale=bmm1_scale, bmm2_scale=bmm2_scale, stream=_raw_stream(dev),
              seq_lens_global=causal_seqlens_kv_global if causal else None,
              sparse_indices=sparse_indices)
     return (out, lse) if return_lse else out
@@ -696,7 +698,8 @@ def _check_decode(query, kv_cache, workspace, block_tables, seq_lens, qo_indptr,
     take their types, counts and strides for granted."""
     dev = query.get_device()
     packed = qo_indptr is not None
-    if not (query.dim() == (3 if packed else 4) and query.shape[-1] == HEAD_DIM_QK
+    shape = query.shape
+    if not (len(shape) == (3 if packed else 4) and shape[-1] == HEAD_DIM_QK
             and query.is_contiguous()):
         _refuse("query", query, "a contiguous tensor", dev,
                 ("tokens", "heads", 576) if packed else ("batch", "tokens", "heads", 576))
@@ -707,8 +710,8 @@ def _check_decode(query, kv_cache, workspace, block_tables, seq_lens, qo_indptr,
     batch = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
     if batch < 0 or not _is_int32(seq_lens, dev, (batch,)):
         _refuse("seq_lens", seq_lens, _INT32, dev, ("batch",))
-    if not packed and query.shape[0] != batch:
-        raise ValueError(f"query holds {query.shape[0]} requests, seq_lens {batch}")
+    if not packed and shape[0] != batch:
+        raise ValueError(f"query holds {shape[0]} requests, seq_lens {batch}")
     if block_tables.dim() != 2 or not _is_int32(block_tables, dev, (batch, block_tables.shape[1])):
         _refuse("block_tables", block_tables, _INT32, dev, (batch, "pages"))
     if packed and not _is_int32(qo_indptr, dev, (batch + 1,)):
@@ -718,10 +721,10 @@ def _check_decode(query, kv_cache, workspace, block_tables, seq_lens, qo_indptr,
     rows = query.numel() // HEAD_DIM_QK
     if out is not None and not (out.dtype is torch.bfloat16 and out.get_device() == dev
                                 and out.numel() == rows * HEAD_DIM_V and out.is_contiguous()):
-        _refuse("out", out, "a contiguous bf16 tensor", dev, (*query.shape[:-1], HEAD_DIM_V))
+        _refuse("out", out, "a contiguous bf16 tensor", dev, (*shape[:-1], HEAD_DIM_V))
     if lse is not None and not (lse.dtype is torch.float32 and lse.get_device() == dev
                                 and lse.numel() == rows and lse.is_contiguous()):
-        _refuse("lse", lse, "a contiguous fp32 tensor", dev, query.shape[:-1])
+        _refuse("lse", lse, "a contiguous fp32 tensor", dev, shape[:-1])
 
 
 def _cache_call(kv_cache, block_tables, seq_lens, qo_indptr, q_len, total_q, status):
