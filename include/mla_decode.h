@@ -99,7 +99,7 @@ typedef struct mla_decode_params {
                                 of that magnitude below).  P enters as two e4m3 parts
                                 (about 2^-8 relative).  Nonzero: every e4m3 value is
                                 widened exactly to bf16 before bf16 MMAs (P in bf16).
-                                Sparse top-k always widens.  With a window neither: every
+                                Sparse top-k always widens.  With a window or shared prefixes neither: every
                                 e4m3 value is widened exactly to f16, with P in f16, and a bf16 query row enters scaled by a
                                 power of two (exact for every element of at least 2^-31 of
                                 the row's largest magnitude). */
@@ -109,6 +109,9 @@ typedef struct mla_decode_params {
                                 its last row alone.)  Not with cp_world > 1 or sparse_top_k. */
   int32_t sinks;             /* with a window: rows 0 .. sinks - 1 stay visible (>= 0; 0
                                 without one) */
+  int32_t prefix_groups;     /* groups of requests that share their first rows (0: none;
+                                > 0: run with mla_decode_run_prefix; at most batch).  Not with
+                                a window, cp_world > 1 or sparse_top_k */
 } mla_decode_params;
 
 typedef struct mla_plan_s mla_plan_t; /* opaque; host memory only */
@@ -364,6 +367,41 @@ int mla_decode_run_sparse(const mla_plan_t *plan, const void *query, const void 
                           void *stream);
 
 /*
+ * Decode over a batch whose requests share their first rows: a system prompt,
+ * a document, the prompt of a beam search.  The result is mla_decode_run's, to
+ * rounding; the shared rows are read once for 128 query rows of a group, whichever requests
+ * they belong to, where each request reads them for itself otherwise.
+ *
+ * prefix_lens    device int32 [G], G = params.prefix_groups: the first
+ *                prefix_lens[g] rows of group g's requests hold the same values.
+ *                They are read through the table of the group's first request that has rows;
+ *                the requests' tables may name the same pages there, or others
+ *                with the same contents.  A length past what a query row of
+ *                the group sees counts as far as all of them see; a group is
+ *                shared by whole tiles of 64 rows, and where that saves time.
+ * prefix_indptr  device int32 [G + 1]: group g is the requests
+ *                prefix_indptr[g] .. prefix_indptr[g + 1] - 1.  Not decreasing,
+ *                within [0, B]; requests before the first and from the last on
+ *                share nothing, nor does a group of fewer than two.  NULL: B / G
+ *                requests each (G divides B).
+ * bmm1_dev, bmm2_dev  both NULL, or both one fp32 in device memory that
+ *                stands in for bmm1_scale and bmm2_scale (mla_decode_run_device_scales).
+ *
+ * A NaN or an infinity in a shared row may reach the query rows of all requests of its
+ * group.  plan: made with params.prefix_groups > 0.  All other arguments, errors and
+ * capture rules as mla_decode_run; the other run entry points refuse such a
+ * plan and this one refuses any other (MLA_ERR_INVALID_ARG).  Status bit 256
+ * (mla_decode_status_offset): a bad prefix_indptr (then nothing is shared) or a
+ * negative length (read as 0).
+ */
+int mla_decode_run_prefix(const mla_plan_t *plan, const void *query, const void *kv_cache,
+                          const int32_t *block_tables, const int32_t *seq_lens,
+                          const int32_t *qo_indptr, int64_t total_q, const int32_t *prefix_lens,
+                          const int32_t *prefix_indptr, float bmm1_scale, float bmm2_scale,
+                          const float *bmm1_dev, const float *bmm2_dev, void *out, float *lse,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Merge n partial attention states of the same query rows into one: the
  * exchange step of decode-context parallelism (DCP), where each rank runs
  * mla_decode_run over its own shard of every request's KV rows with
@@ -546,6 +584,7 @@ int32_t mla_decode_kernels_per_run(const mla_plan_t *plan);
  *  32  an internal wait timed out (the run unwound; results are invalid)
  *  64  a device bmm1 scale negative or not finite (read as 0)
  * 128  a rotation position outside the table (mla_cache_append's status only)
+ * 256  a prefix_indptr that decreases or leaves [0, B], or a negative prefix length
  * Reading it is the caller's choice (a device-to-host copy after the stream
  * syncs).
  */

@@ -27,7 +27,7 @@ import torch
 __all__ = [
     "MLA_OK", "MlaDecodeError", "MlaDecodeParams", "load_library", "library_path",
     "mla_decode_plan", "mla_decode_run", "mla_decode_run_profiled", "mla_decode_run_dcp",
-    "mla_decode_run_sparse", "mla_decode_destroy", "mla_decode_workspace_size",
+    "mla_decode_run_sparse", "mla_decode_run_prefix", "mla_decode_destroy", "mla_decode_workspace_size",
     "mla_decode_status_offset", "mla_decode_status_string", "Plan", "decode",
     "HEAD_DIM_QK", "HEAD_DIM_V", "FP4_ROW_BYTES", "MlaCacheParams", "MlaRopeParams",
     "cache_append", "cache_gather", "rope_table",
@@ -81,6 +81,7 @@ class MlaDecodeParams(ctypes.Structure):
         ("e4m3_widen", ctypes.c_int32),
         ("window", ctypes.c_int32),
         ("sinks", ctypes.c_int32),
+        ("prefix_groups", ctypes.c_int32),
     ]
 
 
@@ -150,6 +151,9 @@ def load_library():
     lib.mla_decode_run_sparse.argtypes = [vp, vp, vp, vp, vp, vp, i64, vp, ctypes.c_float,
                                           ctypes.c_float, vp, vp, vp, sz, vp]
     lib.mla_decode_run_sparse.restype = ctypes.c_int
+    lib.mla_decode_run_prefix.argtypes = [vp, vp, vp, vp, vp, vp, i64, vp, vp, ctypes.c_float,
+                                          ctypes.c_float, vp, vp, vp, vp, vp, sz, vp]
+    lib.mla_decode_run_prefix.restype = ctypes.c_int
     lib.mla_merge_states.argtypes = [vp, vp, i32, i64, ctypes.c_float, vp, vp, vp]
     lib.mla_merge_states.restype = ctypes.c_int
     f32 = ctypes.c_float
@@ -306,6 +310,37 @@ def mla_decode_run_sparse(plan: int, query, kv_cache, block_tables, seq_lens, qo
         raise MlaDecodeError(rc, "mla_decode_run_sparse")
 
 
+def mla_decode_run_prefix(plan: int, query, kv_cache, block_tables, seq_lens, qo_indptr,
+                          total_q: int, prefix_lens, prefix_indptr, bmm1_scale, bmm2_scale,
+                          out, lse, workspace, workspace_bytes: Optional[int] = None,
+                          stream=None) -> None:
+    """Decode over shared prefixes (``mla_decode_run_prefix``): ``prefix_lens`` int32 ``[G]``,
+    ``prefix_indptr`` int32 ``[G + 1]`` or None.  The scales are floats, or both
+    one-element fp32 CUDA tensors that the kernels read when they run."""
+    lib = load_library()
+    if workspace_bytes is None:
+        workspace_bytes = _nbytes(workspace)
+    if stream is None:
+        stream = torch.cuda.current_stream().cuda_stream
+    elif isinstance(stream, torch.cuda.Stream):
+        stream = stream.cuda_stream
+    dev1 = dev2 = None
+    if isinstance(bmm1_scale, torch.Tensor) or isinstance(bmm2_scale, torch.Tensor):
+        for t in (bmm1_scale, bmm2_scale):
+            if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or not t.is_cuda \
+                    or t.numel() != 1:
+                raise TypeError("device scales must be one-element fp32 CUDA tensors, both of them")
+        dev1, dev2 = bmm1_scale.data_ptr(), bmm2_scale.data_ptr()
+        bmm1_scale = bmm2_scale = 0.0
+    rc = lib.mla_decode_run_prefix(ctypes.c_void_p(plan), _ptr(query), _ptr(kv_cache),
+                                   _ptr(block_tables), _ptr(seq_lens), _ptr(qo_indptr),
+                                   int(total_q), _ptr(prefix_lens), _ptr(prefix_indptr),
+                                   bmm1_scale, bmm2_scale, dev1, dev2, _ptr(out), _ptr(lse),
+                                   _ptr(workspace), int(workspace_bytes), stream)
+    if rc != MLA_OK:
+        raise MlaDecodeError(rc, "mla_decode_run_prefix")
+
+
 def mla_decode_host_staging_bytes(plan: int, total_q: int = 0) -> int:
     """Device staging bytes of ``mla_decode_run_host`` for one step."""
     return int(load_library().mla_decode_host_staging_bytes(ctypes.c_void_p(plan), int(total_q)))
@@ -398,10 +433,11 @@ class Plan:
                  max_total_q: int = 0, kv_dtype: str = "bf16", causal: bool = True,
                  return_lse: bool = False, device: int = 0, q_dtype: str = "bf16",
                  cp_world: int = 1, cp_rank: int = 0, sparse_top_k: int = 0,
-                 e4m3_widen: bool = False, window: int = 0, sinks: int = 0):
+                 e4m3_widen: bool = False, window: int = 0, sinks: int = 0,
+                 prefix_groups: int = 0):
         if kv_dtype not in KV_DTYPES:
             raise ValueError(f"kv_dtype must be one of {list(KV_DTYPES)}, got {kv_dtype!r}")
-        for name, v in (("window", window), ("sinks", sinks)):
+        for name, v in (("window", window), ("sinks", sinks), ("prefix_groups", prefix_groups)):
             if not -2 ** 31 <= v < 2 ** 31:  # (ctypes would cut it to its low 32 bits)
                 raise ValueError(f"{name} = {v} does not fit 32 bits")
         self.params = MlaDecodeParams(
@@ -413,19 +449,28 @@ class Plan:
             device=device,
             q_dtype=Q_FP8_E4M3 if q_dtype in ("e4m3", "fp8", torch.float8_e4m3fn) else Q_BF16,
             cp_world=cp_world, cp_rank=cp_rank, sparse_top_k=sparse_top_k,
-            e4m3_widen=int(bool(e4m3_widen)), window=window, sinks=sinks)
+            e4m3_widen=int(bool(e4m3_widen)), window=window, sinks=sinks,
+            prefix_groups=prefix_groups)
         self.cp_world = cp_world
+        self.prefix_groups = prefix_groups
         self.sparse_top_k = sparse_top_k
         self.handle, self.workspace_bytes = mla_decode_plan(self.params)
 
     def run(self, query, kv_cache, block_tables, seq_lens, out, *, qo_indptr=None, total_q=0,
             lse=None, workspace=None, bmm1_scale=1.0, bmm2_scale=1.0, stream=None,
-            seq_lens_global=None, sparse_indices=None):
+            seq_lens_global=None, sparse_indices=None, prefix_lens=None, prefix_indptr=None):
         """Scales are Python floats, or one-element fp32 CUDA tensors (then both
         must be, and the kernels read them when they run).  A plan with
         ``cp_world`` > 1 runs one DCP rank's decode (``seq_lens_global``: the
         global KV lengths, required under causal masking); a plan with
-        ``sparse_top_k`` > 0 a sparse top-k decode over ``sparse_indices``."""
+        ``sparse_top_k`` > 0 a sparse top-k decode over ``sparse_indices``, one with
+        ``prefix_groups`` > 0 a decode over the shared prefixes that ``prefix_lens`` and
+        ``prefix_indptr`` give."""
+        if self.prefix_groups > 0:
+            mla_decode_run_prefix(self.handle, query, kv_cache, block_tables, seq_lens, qo_indptr,
+                                  total_q, prefix_lens, prefix_indptr, bmm1_scale, bmm2_scale, out,
+                                  lse, workspace, None, stream)
+            return
         if self.sparse_top_k > 0:
             mla_decode_run_sparse(self.handle, query, kv_cache, block_tables, seq_lens,
                                   qo_indptr, total_q, sparse_indices, bmm1_scale, bmm2_scale,
@@ -485,7 +530,8 @@ def decode(query: torch.Tensor, kv_cache: torch.Tensor, workspace_buffer: torch.
            return_lse: bool = False, cp_world: int = 1, cp_rank: int = 0,
            causal_seqlens_kv_global: Optional[torch.Tensor] = None,
            sparse_indices: Optional[torch.Tensor] = None, e4m3_widen: bool = False,
-           window: int = 0, sinks: int = 0):
+           window: int = 0, sinks: int = 0, prefix_lens: Optional[torch.Tensor] = None,
+           prefix_indptr: Optional[torch.Tensor] = None):
     """Paged MLA decode.  Returns ``out`` (and ``lse`` when ``return_lse``).
 
     ``query``: bf16 or float8_e4m3fn (quantised with a q_scale the caller folds
@@ -506,7 +552,14 @@ def decode(query: torch.Tensor, kv_cache: torch.Tensor, workspace_buffer: torch.
     and multiply on bf16 tensor cores instead of the FP8 ones (see
     ``mla_decode_params.e4m3_widen`` in ``include/mla_decode.h``).
     ``window`` > 0: a query row sees the last ``window`` rows up to its bound, and
-    the first ``sinks`` rows.  Over a 4-bit cache and with a window every tensor has to be
+    the first ``sinks`` rows.
+    ``prefix_lens``: int32 ``[G]``; the requests of group g hold the same first
+    ``prefix_lens[g]`` rows (a system prompt, the prompt of a beam search), which are then
+    read and multiplied for the group together; the result is the same, to rounding.
+    Group g is the requests ``prefix_indptr[g]`` to ``prefix_indptr[g + 1]`` (int32
+    ``[G + 1]``), or, without it, a G-th of the batch (see ``mla_decode_run_prefix`` in
+    ``include/mla_decode.h``).
+    Over a 4-bit cache, with a window and with shared prefixes every tensor has to be
     contiguous, of its type and count and on the query's device (ValueError).
     """
     if query.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or not query.is_cuda:
@@ -514,7 +567,12 @@ def decode(query: torch.Tensor, kv_cache: torch.Tensor, workspace_buffer: torch.
     q_dtype = "bf16" if query.dtype == torch.bfloat16 else "e4m3"
     kv_cache, kind = _cache_kind(kv_cache)
     kv_dtype = ("bf16", "e4m3", "fp4")[kind]
-    if kind == KV_FP4_E2M1 or window:
+    groups = 0
+    if prefix_lens is not None:
+        groups = _prefix_groups(prefix_lens, prefix_indptr, query.get_device(), seq_lens.shape[0])
+    elif prefix_indptr is not None:
+        raise ValueError("prefix_indptr goes with prefix_lens")
+    if kind == KV_FP4_E2M1 or window or groups:
         _check_decode(query, kv_cache, workspace_buffer, block_tables, seq_lens, qo_indptr, out,
                       lse if return_lse else None, causal_seqlens_kv_global)
     packed = qo_indptr is not None
@@ -542,7 +600,7 @@ def decode(query: torch.Tensor, kv_cache: torch.Tensor, workspace_buffer: torch.
     top_k = int(sparse_indices.shape[-1]) if sparse_indices is not None else 0
     key = (B, H, sq, int(max_seq_len), page_size, width, pages, packed, total_q, kv_dtype, causal,
            bool(return_lse), dev, q_dtype, int(cp_world), int(cp_rank), top_k, bool(e4m3_widen),
-           int(window), int(sinks))
+           int(window), int(sinks), groups)
     plan = _plans.get(key)
     if plan is None:
         plan = Plan(batch=B, num_heads=H, max_seq_len_q=sq, max_seq_len=int(max_seq_len),
@@ -550,7 +608,7 @@ def decode(query: torch.Tensor, kv_cache: torch.Tensor, workspace_buffer: torch.
                     max_total_q=total_q, kv_dtype=kv_dtype, causal=causal, return_lse=return_lse,
                     device=dev, q_dtype=q_dtype, cp_world=int(cp_world),
                     cp_rank=int(cp_rank), sparse_top_k=top_k, e4m3_widen=e4m3_widen,
-                    window=int(window), sinks=int(sinks))
+                    window=int(window), sinks=int(sinks), prefix_groups=groups)
         _plans[key] = plan
     if workspace_buffer.numel() * workspace_buffer.element_size() < plan.workspace_bytes:
         raise ValueError(f"workspace_buffer needs {plan.workspace_bytes} bytes")
@@ -562,8 +620,22 @@ def decode(query: torch.Tensor, kv_cache: torch.Tensor, workspace_buffer: torch.
              lse=lse if return_lse else None, workspace=workspace_buffer,
              bmm1_scale=bmm1_scale, bmm2_scale=bmm2_scale, stream=_raw_stream(dev),
              seq_lens_global=causal_seqlens_kv_global if causal else None,
-             sparse_indices=sparse_indices)
+             sparse_indices=sparse_indices, prefix_lens=prefix_lens,
+             prefix_indptr=prefix_indptr)
     return (out, lse) if return_lse else out
+
+
+def _prefix_groups(lens: torch.Tensor, indptr: Optional[torch.Tensor], dev: int, batch: int) -> int:
+    """The number of prefix groups that a call's tensors describe."""
+    groups = lens.shape[0] if lens.dim() == 1 else 0
+    if groups < 1 or not _is_int32(lens, dev, (groups,)):
+        _refuse("prefix_lens", lens, _INT32, dev, ("groups",))
+    if indptr is None:
+        if batch % groups:
+            raise ValueError(f"{groups} groups do not divide {batch} requests: give prefix_indptr")
+    elif not _is_int32(indptr, dev, (groups + 1,)):
+        _refuse("prefix_indptr", indptr, _INT32, dev, (groups + 1,))
+    return groups
 
 
 def merge_states(o_parts: torch.Tensor, lse_parts: torch.Tensor, *, scale: float = 1.0,

@@ -7,7 +7,8 @@
 // on the caller's stream: the split-KV partitioner, the decode kernel and the
 // combine kernel, with the query split between the first two on the FP8 MMA
 // path with a bf16 query.  The decode kernel is mla_decode_pair.cu's for a 4-bit
-// cache or a sliding window, else mla_decode_sm103.cu's.  Grid sizes depend only on plan-time values, and nothing
+// cache, a sliding window or shared prefixes (which have a partitioner and a join of their
+// own, mla_prefix.cu), else mla_decode_sm103.cu's.  Grid sizes depend only on plan-time values, and nothing
 // here allocates, copies or synchronises, so a run can be captured in a CUDA
 // graph and replayed with new seq_lens / qo_indptr values.
 #include <algorithm>
@@ -15,6 +16,7 @@
 
 #include "../../include/mla_decode.h"
 #include "mla_common.cuh"
+#include "mla_prefix.cuh"
 
 namespace mla {
 cudaError_t launch_partition(const Problem& p, const Layout& lay, void* ws, cudaStream_t stream);
@@ -30,11 +32,17 @@ cudaError_t launch_decode_sm103(const Problem& p, const Layout& lay, void* ws,
                                 cudaStream_t stream);
 cudaError_t decode_pair_setup(int kv_dtype, int sm_count, int* n_pairs);
 cudaError_t launch_decode_pair(const Problem& p, const Layout& lay, void* ws, cudaStream_t stream);
+cudaError_t prefix_setup();
+cudaError_t launch_partition_prefix(const Problem& p, const PrefixArgs& pa, const Layout& lay, const PrefixLayout& pl,
+                                    void* ws, cudaStream_t stream);
+cudaError_t launch_join_prefix(const Problem& p, const Layout& lay, const PrefixLayout& pl, void* ws, int sm_count,
+                               cudaStream_t stream);
 }  // namespace mla
 
 struct mla_plan_s {
   mla_decode_params prm;
   mla::Layout lay;
+  mla::PrefixLayout pre;  // plans with prefix groups
   int sm_count;
   int combine_grid;
   // mla_decode_run_host copies the query on this stream while the
@@ -58,9 +66,11 @@ int effective_window(const mla_decode_params& p) {
 }
 
 static_assert(mla::kKvFp8 == MLA_KV_FP8_E4M3 && mla::kKvFp4 == MLA_KV_FP4_E2M1, "cache types");
-bool uses_pair_mma(const mla_decode_params& p) { return mla::pair_mma(p.kv_dtype, p.window); }
+bool uses_pair_mma(const mla_decode_params& p) {
+  return mla::pair_mma(p.kv_dtype, p.window) || p.prefix_groups > 0;
+}
 bool uses_fp8_mma(const mla_decode_params& p) {
-  return mla::fp8_mma(p.kv_dtype, p.window, p.sparse_top_k, p.e4m3_widen);
+  return mla::fp8_mma(p.kv_dtype, p.window, p.sparse_top_k, p.e4m3_widen) && p.prefix_groups == 0;
 }
 
 // the FP8 MMA path with a bf16 query: the query is split before the decode
@@ -156,6 +166,9 @@ int mla_decode_plan(const mla_decode_params* params, mla_plan_t** plan, size_t* 
     return MLA_ERR_INVALID_ARG;
   if (p.window > 0 && (p.cp_world > 1 || p.sparse_top_k > 0)) return MLA_ERR_UNSUPPORTED;
   if (p.kv_dtype == MLA_KV_FP4_E2M1 && p.sparse_top_k > 0) return MLA_ERR_UNSUPPORTED;
+  if (p.prefix_groups < 0 || (p.batch > 0 && p.prefix_groups > p.batch)) return MLA_ERR_INVALID_ARG;
+  if (p.prefix_groups > 0 && (p.window > 0 || p.cp_world > 1 || p.sparse_top_k > 0))
+    return MLA_ERR_UNSUPPORTED;
   if (!supported_heads(p.num_heads)) return MLA_ERR_UNSUPPORTED;
   if (p.page_size != 32 && p.page_size != 64) return MLA_ERR_UNSUPPORTED;
   // cache rows are addressed with 32-bit row coordinates
@@ -176,6 +189,7 @@ int mla_decode_plan(const mla_decode_params* params, mla_plan_t** plan, size_t* 
             ? mla::decode_pair_setup(p.kv_dtype, sms, &n_pairs)
             : mla::decode_sm103_setup(p.kv_dtype, p.sparse_top_k > 0, uses_fp8_mma(p), sms, &n_pairs);
   if (e == cudaSuccess) e = mla::partition_setup();
+  if (e == cudaSuccess && p.prefix_groups > 0) e = mla::prefix_setup();
   cudaStream_t side = nullptr;
   if (e == cudaSuccess) e = cudaStreamCreateWithFlags(&side, cudaStreamNonBlocking);
   cudaSetDevice(prev);
@@ -211,9 +225,16 @@ int mla_decode_plan(const mla_decode_params* params, mla_plan_t** plan, size_t* 
                                       p.max_seq_len_q + mla::kKvTile);
     const long long overhead = uses_pair_mma(p) ? mla::kOverheadTilesPair : mla::kOverheadTiles;
     const long long units = std::max(groups, 1LL) * (overhead + ceil_div(kv_rows, mla::kKvTile));
-    n_pairs = (int)std::max(1LL, std::min<long long>(n_pairs, units / mla::kMinUnits));
+    if (p.prefix_groups == 0)
+      n_pairs = (int)std::max(1LL, std::min<long long>(n_pairs, units / mla::kMinUnits));
   }
-  const int rc = make_layout(p, n_pairs, 2 * n_pairs, rows_per_group, &pl->lay);
+  int rc = MLA_OK;
+  if (p.prefix_groups == 0)
+    rc = make_layout(p, n_pairs, 2 * n_pairs, rows_per_group, &pl->lay);
+  else if (!mla::make_prefix_layout(p.batch, p.num_heads, p.max_seq_len_q, p.packed != 0, p.max_total_q, p.kv_dtype,
+                                    p.prefix_groups, std::min(n_pairs, mla::kPrefixWorkers), kHeaderBytes, &pl->lay,
+                                    &pl->pre))
+    rc = MLA_ERR_UNSUPPORTED;
   if (rc != MLA_OK) {
     delete pl;
     return rc;
@@ -271,11 +292,14 @@ int run_impl(const mla_plan_t* plan, const void* query, const void* kv_cache,
              const float* bmm2_dev, void* out, float* lse, void* workspace,
              size_t workspace_bytes, void* stream, void* event_before_decode,
              void* event_after_decode, const int32_t* seq_lens_global = nullptr,
-             const int32_t* sparse_idx = nullptr, cudaEvent_t join_before_decode = nullptr) {
+             const int32_t* sparse_idx = nullptr, cudaEvent_t join_before_decode = nullptr,
+             const mla::PrefixArgs* prefix = nullptr) {
   if (!plan) return MLA_ERR_INVALID_ARG;
   const mla_decode_params& prm = plan->prm;
   // a sparse plan needs its position lists; no other plan takes them
   if ((prm.sparse_top_k > 0) != (sparse_idx != nullptr)) return MLA_ERR_INVALID_ARG;
+  // a plan with prefix groups needs their lengths
+  if ((prm.prefix_groups > 0) != (prefix != nullptr)) return MLA_ERR_INVALID_ARG;
   if (prm.batch == 0) return MLA_OK;
   if (sparse_idx && !aligned(sparse_idx, 4)) return MLA_ERR_ALIGNMENT;
   // a causal decode-context-parallel plan needs the global lengths; no other
@@ -350,7 +374,9 @@ int run_impl(const mla_plan_t* plan, const void* query, const void* kv_cache,
     if (cudaStreamIsCapturing(s, &cs) != cudaSuccess) return MLA_ERR_CUDA;
     if (cs == cudaStreamCaptureStatusActive) ev_flags = cudaEventRecordExternal;
   }
-  if (mla::launch_partition(p, plan->lay, workspace, s) != cudaSuccess) return MLA_ERR_CUDA;
+  if ((prefix ? mla::launch_partition_prefix(p, *prefix, plan->lay, plan->pre, workspace, s)
+              : mla::launch_partition(p, plan->lay, workspace, s)) != cudaSuccess)
+    return MLA_ERR_CUDA;
   // work enqueued elsewhere that the decode needs (the host entry's query copy)
   if (join_before_decode && cudaStreamWaitEvent(s, join_before_decode, 0) != cudaSuccess)
     return MLA_ERR_CUDA;
@@ -368,7 +394,8 @@ int run_impl(const mla_plan_t* plan, const void* query, const void* kv_cache,
       cudaEventRecordWithFlags(static_cast<cudaEvent_t>(event_after_decode), s, ev_flags) !=
           cudaSuccess)
     return MLA_ERR_CUDA;
-  if (mla::launch_combine(p, plan->lay, workspace, plan->combine_grid, s) != cudaSuccess)
+  if ((prefix ? mla::launch_join_prefix(p, plan->lay, plan->pre, workspace, plan->sm_count, s)
+              : mla::launch_combine(p, plan->lay, workspace, plan->combine_grid, s)) != cudaSuccess)
     return MLA_ERR_CUDA;
   return MLA_OK;
 }
@@ -433,6 +460,22 @@ int mla_decode_run_sparse(const mla_plan_t* plan, const void* query, const void*
                   nullptr, nullptr, nullptr, sparse_indices);
 }
 
+int mla_decode_run_prefix(const mla_plan_t* plan, const void* query, const void* kv_cache,
+                          const int32_t* block_tables, const int32_t* seq_lens,
+                          const int32_t* qo_indptr, int64_t total_q, const int32_t* prefix_lens,
+                          const int32_t* prefix_indptr, float bmm1_scale, float bmm2_scale,
+                          const float* bmm1_dev, const float* bmm2_dev, void* out, float* lse,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  if (!plan || plan->prm.prefix_groups <= 0 || !prefix_lens) return MLA_ERR_INVALID_ARG;
+  if ((bmm1_dev == nullptr) != (bmm2_dev == nullptr)) return MLA_ERR_INVALID_ARG;
+  if (!prefix_indptr && plan->prm.batch % plan->prm.prefix_groups != 0) return MLA_ERR_INVALID_ARG;
+  if (!aligned(prefix_lens, 4) || (prefix_indptr && !aligned(prefix_indptr, 4))) return MLA_ERR_ALIGNMENT;
+  const mla::PrefixArgs args{plan->prm.prefix_groups, prefix_lens, prefix_indptr};
+  return run_impl(plan, query, kv_cache, block_tables, seq_lens, qo_indptr, total_q, bmm1_scale,
+                  bmm2_scale, bmm1_dev, bmm2_dev, out, lse, workspace, workspace_bytes, stream,
+                  nullptr, nullptr, nullptr, nullptr, nullptr, &args);
+}
+
 int mla_merge_states(const void* o_parts, const float* lse_parts, int32_t n_parts, int64_t rows,
                      float scale, void* out, float* lse_out, void* stream) {
   if (n_parts < 1 || rows < 0 || rows > (1LL << 40) || (double)n_parts * (double)rows > 9.0e15)
@@ -471,7 +514,7 @@ int mla_decode_run_host(const mla_plan_t* plan, const void* h_query, const void*
   int cur = -1;
   if (cudaGetDevice(&cur) != cudaSuccess) return MLA_ERR_CUDA;
   if (cur != prm.device || (prm.cp_world > 1 && prm.mask == MLA_MASK_CAUSAL) ||
-      prm.sparse_top_k > 0)
+      prm.sparse_top_k > 0 || prm.prefix_groups > 0)
     return MLA_ERR_INVALID_ARG;
   if (prm.return_lse && !h_lse) return MLA_ERR_INVALID_ARG;
   if (prm.packed) {

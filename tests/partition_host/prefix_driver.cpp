@@ -1,0 +1,110 @@
+// Runs the partitioner of plans with shared prefixes (its source, with host stand-ins) on
+// host threads, one problem per text file, and writes the work list and the join's entries.
+// Built by tests/test_prefix_partition.py.
+#include <cstdio>
+#include <deque>
+#include <string>
+
+#include "shim.h"
+
+template <typename T, typename F>
+T host_reduce(T v, F f) {
+  T r = host_exchange(v, 0);
+  for (int l = 1; l < 32; ++l) r = f(r, host_exchange(v, l));
+  return r;
+}
+inline int __reduce_min_sync(unsigned, int v) { return host_reduce(v, [](int a, int b) { return min(a, b); }); }
+inline int __reduce_max_sync(unsigned, int v) { return host_reduce(v, [](int a, int b) { return max(a, b); }); }
+inline unsigned __reduce_add_sync(unsigned, unsigned v) { return host_reduce(v, [](unsigned a, unsigned b) { return a + b; }); }
+inline unsigned __reduce_or_sync(unsigned, unsigned v) { return host_reduce(v, [](unsigned a, unsigned b) { return a | b; }); }
+inline int __popc(unsigned v) { return __builtin_popcount(v); }
+inline int atomicMax(int* p, int v) {
+  std::atomic_ref<int> a(*p);
+  int old = a.load();
+  while (old < v && !a.compare_exchange_weak(old, v)) {
+  }
+  return old;
+}
+#include "mla_common_host.h"
+#include "mla_prefix_host.h"
+#include "partition_prefix_host.inc"
+
+int main(int argc, char** argv) {
+  if (argc != 3) return 2;
+  FILE* f = std::fopen(argv[1], "r");
+  if (!f) return 2;
+  int B, H, packed, max_q, max_seq_len, n_workers, causal, kv_dtype, G, uniform, global_scratch;
+  long long total_q;
+  if (std::fscanf(f, "%d %d %d %d %d %d %d %d %d %d %d %lld", &B, &H, &packed, &max_q, &max_seq_len, &n_workers,
+                  &causal, &kv_dtype, &G, &uniform, &global_scratch, &total_q) != 12)
+    return 2;
+  std::vector<int> seq_lens(B), qo(B + 1), lens(G), indptr(G + 1);
+  for (auto* v : {&seq_lens, &qo, &lens, &indptr})
+    for (auto& x : *v)
+      if (std::fscanf(f, "%d", &x) != 1) return 2;
+  std::fclose(f);
+  mla::Layout lay{};
+  mla::PrefixLayout pl{};
+  if (!mla::make_prefix_layout(B, H, max_q, packed, total_q, kv_dtype, G, n_workers, sizeof(int) * mla::kHdrWords, &lay, &pl))
+    return 3;
+  const size_t starts[] = {lay.items, lay.worker_ranges, pl.entries, pl.rg_first, pl.rg_count, lay.part_o, lay.part_lse, lay.total};
+  for (size_t s : starts)
+    if (s % 256) return 5;
+  if (global_scratch) {  // as a batch that shared memory does not hold: the scratch past the rest
+    pl.scratch_in_smem = 0;
+    pl.owners = lay.part_o;
+  }
+  const size_t used = lay.part_o + (global_scratch ? pl.scratch_bytes : 0);  // (no partial is touched here)
+  std::vector<unsigned char> ws(used, 0xAB);
+  std::vector<unsigned char> scratch(pl.scratch_in_smem ? pl.scratch_bytes : 16, 0xCD);
+  g_scratch = scratch.data();
+  mla::Problem p{};
+  p.batch = B;
+  p.num_heads = H;
+  p.max_q = max_q;
+  p.max_seq_len = max_seq_len;
+  p.packed = packed;
+  p.kv_dtype = kv_dtype;
+  p.causal = causal;
+  p.cp_world = 1;
+  p.total_q = total_q;
+  p.seq_lens = seq_lens.data();
+  p.qo_indptr = packed ? qo.data() : nullptr;
+  const mla::PrefixArgs pa{G, lens.data(), uniform ? nullptr : indptr.data()};
+  const int threads = mla::partition_prefix_threads(p, pa, lay);
+  blockDim.x = threads;
+  std::barrier<> block_bar(threads);
+  g_block_barrier = &block_bar;
+  std::deque<std::barrier<>> warp_bars;  // constructed in place, never moved
+  std::vector<HostWarp> warps(threads / 32);
+  for (int w = 0; w < threads / 32; ++w) {
+    warp_bars.emplace_back(32);
+    warps[w].bar = &warp_bars[w];
+    g_warps.push_back(&warps[w]);
+  }
+  std::vector<std::thread> th;
+  for (int t = 0; t < threads; ++t)
+    th.emplace_back([&, t] {
+      threadIdx.x = t;
+      mla::partition_prefix_kernel(p, pa, lay, pl, reinterpret_cast<char*>(ws.data()));
+    });
+  for (auto& x : th) x.join();
+  const int* hdr = reinterpret_cast<const int*>(ws.data());
+  FILE* o = std::fopen(argv[2], "w");
+  if (!o) return 2;
+  std::fprintf(o, "%d %d %d %d %d\n", hdr[mla::kHdrStatus], hdr[mla::kHdrNumItems], hdr[mla::kHdrNumCombine],
+               lay.max_items, pl.max_entries);
+  const int* items = reinterpret_cast<const int*>(ws.data() + lay.items);
+  for (int i = 0; i < hdr[mla::kHdrNumItems] * 10; ++i) std::fprintf(o, "%d ", items[i]);
+  std::fprintf(o, "\n");
+  const int* wb = reinterpret_cast<const int*>(ws.data() + lay.worker_ranges);
+  for (int i = 0; i <= n_workers; ++i) std::fprintf(o, "%d ", wb[i]);
+  std::fprintf(o, "\n");
+  const mla::PrefixEntry* e = reinterpret_cast<const mla::PrefixEntry*>(ws.data() + pl.entries);
+  for (int i = 0; i < hdr[mla::kHdrNumCombine]; ++i)
+    std::fprintf(o, "%lld %d %d %d %d %d %d %d %d ", e[i].row0, e[i].rows, e[i].own, e[i].n_own, e[i].off, e[i].pre[0],
+                 e[i].n_pre[0], e[i].pre[1], e[i].n_pre[1]);
+  std::fprintf(o, "\n");
+  std::fclose(o);
+  return 0;
+}
