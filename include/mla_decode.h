@@ -542,6 +542,92 @@ int mla_cache_gather(const mla_cache_params *params, const void *kv_cache,
                      const int32_t *qo_indptr, int64_t total_q, float kv_scale, void *out,
                      int32_t *status, void *stream);
 
+/*
+ * Beam search over the paged cache.  A step is mla_beam_select over the step's
+ * logits, mla_cache_reorder by the parents that it chose, and mla_cache_append of
+ * the chosen tokens; the prompt's rows, which a request's beams share, are read once by
+ * mla_decode_run_prefix.
+ */
+typedef enum { MLA_LOGITS_FP32 = 0, MLA_LOGITS_BF16 = 1, MLA_LOGITS_FP16 = 2 } mla_logits_dtype;
+
+typedef struct mla_beam_params {
+  int32_t batch;        /* B >= 0 requests */
+  int32_t beams;        /* W beams of each, 1 .. 64 */
+  int32_t k;            /* continuations wanted of each request, 1 .. 64 */
+  int32_t vocab;        /* V tokens, 1 .. 2^28 */
+  int32_t logits_dtype; /* mla_logits_dtype */
+  int32_t end_token;    /* with `finished`: the one token that an ended beam continues with */
+} mla_beam_params;
+
+/* Workspace bytes of mla_beam_select; 0 for parameters that it refuses, or no request. */
+size_t mla_beam_workspace_size(const mla_beam_params *params);
+
+/*
+ * The k best continuations of each request's beams.  Beam w with score c and logits x
+ * offers (w, v) with the score c + x[v] - ln sum_u exp(x[u]) for every token v with
+ * x[v] > -inf; a beam that has ended offers (w, end_token) with its score c.  The k
+ * largest scores win; of equal ones the lower w, then the lower v.  (Scores are compared
+ * in 64 bits; within a beam, the logits are.)
+ *
+ * logits       [B][W] rows of V by the two strides, in elements and >= 0; the last dim is
+ *              contiguous; aligned to its type
+ * scores       fp32 [B, W]; a beam whose score is not finite offers nothing, nor does one with
+ *              a NaN or +infinity among its logits.  (A first step: -inf for all beams but one.)
+ * finished     uint8 [B, W], nonzero: the beam has ended; or NULL.  Its logits are not read.
+ * scores_out, tokens_out, parents_out
+ *              [B, k], best first: the new scores (fp32), the tokens and the beams they
+ *              continue (int32).  Where a request has fewer than k: -inf, -1 and -1.
+ * workspace    >= mla_beam_workspace_size bytes, 256-byte aligned, exclusive to the call
+ *              until the stream has passed it; needs no zeroing
+ * Inputs must not overlap outputs.  Capture-safe.  Call with the tensors' device current.
+ * Errors (nothing enqueued): MLA_ERR_INVALID_ARG (also an end_token outside the vocabulary
+ * with `finished`), MLA_ERR_UNSUPPORTED, MLA_ERR_ALIGNMENT, MLA_ERR_WORKSPACE_TOO_SMALL;
+ * MLA_ERR_CUDA if a launch fails.
+ */
+int mla_beam_select(const mla_beam_params *params, const void *logits, int64_t batch_stride, int64_t beam_stride,
+                    const float *scores, const uint8_t *finished, float *scores_out, int32_t *tokens_out,
+                    int32_t *parents_out, void *workspace, size_t workspace_bytes, void *stream);
+
+typedef struct mla_reorder_params {
+  int32_t batch;             /* B >= 0 requests */
+  int32_t beams;             /* W beams of each, 1 .. 64; beam w of request b is row b * W + w */
+  int32_t page_size;         /* 32 or 64 */
+  int32_t max_pages_per_req; /* row stride of block_tables */
+  int32_t kv_dtype;          /* mla_kv_dtype */
+  int64_t num_pages;         /* physical pages in every cache */
+} mla_reorder_params;
+
+/*
+ * Make beam w of each request the continuation of beam parents[b][w]: its first L =
+ * seq_lens rows become that beam's, in every cache (one a layer, all with the same
+ * tables).  Whole pages go by reference: the first L / page_size entries of its table
+ * become its parent's.  Of the page that is still being written the L mod page_size
+ * rows are copied into the beam's spare page, which takes its place in the table, and the
+ * page that the beam had there becomes its spare.  A beam that continues itself changes
+ * nothing.  Entries past the page of row L - 1 stay as they are, so pages that a
+ * caller has put there for rows to come are each beam's own.  So a request needs, beside its prompt's
+ * pages, W pages for every page of new rows and W spare ones, and no count of references.
+ *
+ * caches       host array of num_layers >= 0 device pointers, 16-byte aligned
+ * block_tables int32 [B * W, max_pages_per_req], changed in place; no page in
+ *              which a beam still writes is in another beam's table
+ * seq_lens     int32 [B * W], the same for all beams of a request (0 <= L <=
+ *              max_pages_per_req * page_size); a request whose differ is left as it is
+ * parents      int32 [B, W]; -1 (or anything outside [0, W)): the beam stays as it is
+ * spare_pages  int32 [B * W], changed in place: one page of each beam, in no table
+ * status       int32 device word or NULL: bits of mla_decode_status_offset are ORed in (1:
+ *              lengths, 2: a parent outside [-1, W), 16: a page id outside [0, num_pages);
+ *              its rows are not copied).
+ * Copies come first, then the tables and spare pages change; two launches, and one more for
+ * every 64 layers past the first 64.  Capture-safe; no workspace.
+ * Call with the tensors' device current.
+ * Errors (nothing enqueued): MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED, MLA_ERR_ALIGNMENT;
+ * MLA_ERR_CUDA if a launch fails.
+ */
+int mla_cache_reorder(const mla_reorder_params *params, void *const *caches, int32_t num_layers, int32_t *block_tables,
+                      const int32_t *seq_lens, const int32_t *parents, int32_t *spare_pages, int32_t *status,
+                      void *stream);
+
 /* Workspace bytes of a plan (the value mla_decode_plan returned). */
 size_t mla_decode_workspace_size(const mla_plan_t *plan);
 

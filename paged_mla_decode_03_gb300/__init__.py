@@ -13,7 +13,9 @@ caller-owned workspace, ``bmm1_scale``/``bmm2_scale``, causal or dense
 masking, bf16 output and an optional natural-log LSE.  The cache is bf16, e4m3
 or 4-bit; ``cache_append`` writes the newest tokens' rows (norm, rotation,
 quantisation) and forms their query, ``cache_gather`` reads rows back, and
-``rope_table`` makes the rotation table.
+``rope_table`` makes the rotation table.  ``beam_select`` and ``cache_reorder``
+are a beam search's step: the best continuations over the vocabulary, and the cache
+reordered by the beams that they continue.
 """
 from __future__ import annotations
 
@@ -30,7 +32,8 @@ __all__ = [
     "mla_decode_run_sparse", "mla_decode_run_prefix", "mla_decode_destroy", "mla_decode_workspace_size",
     "mla_decode_status_offset", "mla_decode_status_string", "Plan", "decode",
     "HEAD_DIM_QK", "HEAD_DIM_V", "FP4_ROW_BYTES", "MlaCacheParams", "MlaRopeParams",
-    "cache_append", "cache_gather", "rope_table",
+    "cache_append", "cache_gather", "rope_table", "MlaBeamParams", "MlaReorderParams",
+    "beam_select", "beam_workspace_bytes", "cache_reorder",
 ]
 
 HEAD_DIM_QK = 576
@@ -100,6 +103,30 @@ class MlaCacheParams(ctypes.Structure):
     ]
 
 
+class MlaBeamParams(ctypes.Structure):
+    """Mirror of ``mla_beam_params`` (natural C alignment)."""
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("beams", ctypes.c_int32),
+        ("k", ctypes.c_int32),
+        ("vocab", ctypes.c_int32),
+        ("logits_dtype", ctypes.c_int32),
+        ("end_token", ctypes.c_int32),
+    ]
+
+
+class MlaReorderParams(ctypes.Structure):
+    """Mirror of ``mla_reorder_params`` (natural C alignment)."""
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("beams", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("max_pages_per_req", ctypes.c_int32),
+        ("kv_dtype", ctypes.c_int32),
+        ("num_pages", ctypes.c_int64),
+    ]
+
+
 class MlaRopeParams(ctypes.Structure):
     """Mirror of ``mla_rope_params`` (natural C alignment)."""
     _fields_ = [
@@ -166,6 +193,14 @@ def load_library():
     lib.mla_cache_gather.argtypes = [ctypes.POINTER(MlaCacheParams), vp, vp, vp, vp, i64, f32, vp,
                                      vp, vp]
     lib.mla_cache_gather.restype = ctypes.c_int
+    lib.mla_beam_workspace_size.argtypes = [ctypes.POINTER(MlaBeamParams)]
+    lib.mla_beam_workspace_size.restype = sz
+    lib.mla_beam_select.argtypes = [ctypes.POINTER(MlaBeamParams), vp, i64, i64, vp, vp, vp, vp, vp,
+                                    vp, sz, vp]
+    lib.mla_beam_select.restype = ctypes.c_int
+    lib.mla_cache_reorder.argtypes = [ctypes.POINTER(MlaReorderParams), vp, i32, vp, vp, vp, vp, vp,
+                                      vp]
+    lib.mla_cache_reorder.restype = ctypes.c_int
     lib.mla_decode_destroy.argtypes = [vp]
     lib.mla_decode_destroy.restype = None
     lib.mla_decode_workspace_size.argtypes = [vp]
@@ -986,6 +1021,148 @@ def cache_gather(kv_cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: t
     if rc != MLA_OK:
         raise MlaDecodeError(rc, "mla_cache_gather")
     return out
+
+
+LOGITS_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def beam_select(logits: torch.Tensor, scores: torch.Tensor, *, k: Optional[int] = None,
+                finished: Optional[torch.Tensor] = None, end_token: Optional[int] = None,
+                out: Optional[Tuple[torch.Tensor, torch.Tensor, torch.Tensor]] = None,
+                workspace: Optional[torch.Tensor] = None, stream=None):
+    """The ``k`` (default: as many as beams) best continuations of each request's beams
+    (``mla_beam_select``): ``(scores, tokens, parents)``, each ``[B, k]``, best first.
+
+    ``logits`` fp32, bf16 or fp16 ``[B, W, V]`` (strides of the first two dims free) and
+    ``scores`` fp32 ``[B, W]``: beam w offers token v with the score ``scores[w] +
+    logits[w, v] - logsumexp(logits[w])``.  Of equal scores the lower beam, then the
+    lower token is first.  ``finished`` uint8 or bool ``[B, W]``: an ended beam
+    offers only ``end_token``, with its score.  Tokens of -inf are not offered, nor is anything
+    by a beam whose score is not finite or that has a NaN or +inf among its logits;
+    where a request has fewer than ``k`` continuations the rest are -inf, -1 and -1.
+    ``out``: the three results' tensors (fp32, int32, int32).  ``workspace``: a uint8 tensor
+    of at least ``beam_workspace_bytes``.  What the call makes belongs to ``stream`` (the
+    current one), where the kernels run."""
+    if logits.dim() != 3 or not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor [batch, beams, vocab]")
+    B, W, V = logits.shape
+    dev = logits.get_device()
+    kind = LOGITS_DTYPES.get(logits.dtype)
+    s_batch, s_beam, s_last = logits.stride()
+    if kind is None or (s_last != 1 and V > 1):
+        _refuse("logits", logits, "an fp32, bf16 or fp16 tensor with a contiguous last dim", dev,
+                (B, W, V))
+    if not (scores.dtype is torch.float32 and scores.get_device() == dev
+            and scores.shape == (B, W) and scores.is_contiguous()):
+        _refuse("scores", scores, "a contiguous fp32 tensor", dev, (B, W))
+    k = W if k is None else int(k)
+    if finished is not None:
+        if not (finished.dtype in (torch.uint8, torch.bool) and finished.get_device() == dev
+                and finished.shape == (B, W) and finished.is_contiguous()):
+            _refuse("finished", finished, "a contiguous uint8 or bool tensor", dev, (B, W))
+        if end_token is None:
+            raise ValueError("finished needs end_token")
+    if not 1 <= k <= 64 or not 1 <= W <= 64:
+        raise ValueError(f"k = {k} and {W} beams must lie in [1, 64]")
+    if end_token is not None and not 0 <= end_token < V:
+        raise ValueError(f"end_token {end_token} outside the vocabulary of {V}")
+    lib = load_library()
+    params = _beam_params_of(B, W, k, V, kind, 0 if end_token is None else end_token)
+    need = lib.mla_beam_workspace_size(params)
+    with _made_on(stream, dev):
+        if out is None:
+            made = torch.empty((3, B, k), dtype=torch.int32, device=logits.device)
+            new_scores, tokens, parents = made[0].view(torch.float32), made[1], made[2]
+        else:
+            new_scores, tokens, parents = out
+            if not (new_scores.dtype is torch.float32 and new_scores.get_device() == dev
+                    and new_scores.shape == (B, k) and new_scores.is_contiguous()):
+                _refuse("out[0]", new_scores, "a contiguous fp32 tensor", dev, (B, k))
+            for i, t in ((1, tokens), (2, parents)):
+                if not _is_int32(t, dev, (B, k)):
+                    _refuse(f"out[{i}]", t, _INT32, dev, (B, k))
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=logits.device)
+        elif not (workspace.dtype is torch.uint8 and workspace.get_device() == dev
+                  and workspace.is_contiguous() and workspace.numel() >= need):
+            _refuse("workspace", workspace, "a contiguous uint8 tensor", dev, (need,))
+    if B == 0:
+        return new_scores, tokens, parents
+    rc = _call_on(dev, lib.mla_beam_select, params, logits.data_ptr(), s_batch if B > 1 else 0,
+                  s_beam if W > 1 else 0, scores.data_ptr(), _ptr(finished), new_scores.data_ptr(),
+                  tokens.data_ptr(), parents.data_ptr(), workspace.data_ptr(), need,
+                  _raw_stream(dev) if stream is None else _stream_of(stream, dev))
+    if rc != MLA_OK:
+        raise MlaDecodeError(rc, "mla_beam_select")
+    return new_scores, tokens, parents
+
+
+def beam_workspace_bytes(batch: int, beams: int, k: int, vocab: int, dtype=torch.float32) -> int:
+    """Bytes of a ``workspace`` for ``beam_select`` (0: it refuses such a call)."""
+    return int(load_library().mla_beam_workspace_size(
+        _beam_params_of(batch, beams, k, vocab, LOGITS_DTYPES[dtype], 0)))
+
+
+_beam_params: Dict[tuple, MlaBeamParams] = {}
+
+
+def _beam_params_of(*key) -> MlaBeamParams:
+    p = _beam_params.get(key)
+    if p is None:
+        for v in key:
+            if not -2 ** 31 <= v < 2 ** 31:  # (ctypes would cut it to its low 32 bits)
+                raise ValueError(f"{v} does not fit 32 bits")
+        if len(_beam_params) >= 1024:
+            _beam_params.clear()
+        p = _beam_params[key] = MlaBeamParams(*key)
+    return p
+
+
+def cache_reorder(kv_caches, block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                  parents: torch.Tensor, spare_pages: torch.Tensor, *,
+                  status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Make beam w of request b the continuation of its beam ``parents[b, w]``
+    (``mla_cache_reorder``), in every cache of ``kv_caches`` (a cache, or a list of them: one a
+    layer, all with the same block tables).
+
+    ``block_tables`` int32 ``[B * W, pages]`` and ``spare_pages`` int32 ``[B * W]`` change in
+    place: whole pages of the beam's first ``seq_lens`` rows go by reference, the page
+    that is still being written is copied into the beam's spare page, and the page that
+    the beam had there is its next spare.  ``seq_lens`` int32 ``[B * W]`` is the same for all
+    beams of a request; ``parents`` int32 ``[B, W]``, -1: the beam stays as it is.
+    ``status``: int32 ``[1]``, contract violations are ORed in (see ``include/mla_decode.h``)."""
+    caches = [kv_caches] if isinstance(kv_caches, torch.Tensor) else list(kv_caches)
+    if not caches:
+        raise ValueError("kv_caches must hold a cache")
+    dev = caches[0].get_device()
+    shape, dtype = caches[0].shape, caches[0].dtype
+    for c in caches:
+        if c.get_device() != dev or dev < 0 or not c.is_contiguous() or c.shape != shape \
+                or c.dtype is not dtype:
+            _refuse("kv_caches", c, f"a contiguous {dtype} tensor, as the first,", dev, shape)
+    cache, kind = _cache_kind(caches[0])
+    pages, page_size, _ = cache.shape
+    if parents.dim() != 2 or not _is_int32(parents, dev, parents.shape):
+        _refuse("parents", parents, _INT32, dev, ("batch", "beams"))
+    B, W = parents.shape
+    if block_tables.dim() != 2 or not _is_int32(block_tables, dev, (B * W, block_tables.shape[1])):
+        _refuse("block_tables", block_tables, _INT32, dev, (B * W, "pages"))
+    if not _is_int32(seq_lens, dev, (B * W,)):
+        _refuse("seq_lens", seq_lens, _INT32, dev, (B * W,))
+    if not _is_int32(spare_pages, dev, (B * W,)):
+        _refuse("spare_pages", spare_pages, _INT32, dev, (B * W,))
+    if status is not None and not _is_int32(status, dev, (1,)):
+        _refuse("status", status, _INT32, dev, (1,))
+    if B == 0:
+        return
+    p = MlaReorderParams(B, W, page_size, block_tables.shape[1], kind, pages)
+    pointers = (ctypes.c_void_p * len(caches))(*[c.data_ptr() for c in caches])
+    rc = _call_on(dev, load_library().mla_cache_reorder, ctypes.byref(p), pointers, len(caches),
+                  block_tables.data_ptr(), seq_lens.data_ptr(), parents.data_ptr(),
+                  spare_pages.data_ptr(), _ptr(status),
+                  _raw_stream(dev) if stream is None else _stream_of(stream, dev))
+    if rc != MLA_OK:
+        raise MlaDecodeError(rc, "mla_cache_reorder")
 
 
 def dcp_gather(out: torch.Tensor, lse: torch.Tensor, group=None):
