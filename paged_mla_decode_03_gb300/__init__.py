@@ -1066,13 +1066,11 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, *, k: Optional[int] 
         raise ValueError(f"k = {k} and {W} beams must lie in [1, 64]")
     if end_token is not None and not 0 <= end_token < V:
         raise ValueError(f"end_token {end_token} outside the vocabulary of {V}")
-    lib = load_library()
-    params = _beam_params_of(B, W, k, V, kind, 0 if end_token is None else end_token)
-    need = lib.mla_beam_workspace_size(params)
+    params, need = _beam_params_of(B, W, k, V, kind, 0 if end_token is None else end_token)
     with _made_on(stream, dev):
         if out is None:
-            made = torch.empty((3, B, k), dtype=torch.int32, device=logits.device)
-            new_scores, tokens, parents = made[0].view(torch.float32), made[1], made[2]
+            new_scores = torch.empty((B, k), dtype=torch.float32, device=logits.device)
+            tokens, parents = torch.empty((2, B, k), dtype=torch.int32, device=logits.device).unbind()
         else:
             new_scores, tokens, parents = out
             if not (new_scores.dtype is torch.float32 and new_scores.get_device() == dev
@@ -1088,7 +1086,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, *, k: Optional[int] 
             _refuse("workspace", workspace, "a contiguous uint8 tensor", dev, (need,))
     if B == 0:
         return new_scores, tokens, parents
-    rc = _call_on(dev, lib.mla_beam_select, params, logits.data_ptr(), s_batch if B > 1 else 0,
+    rc = _call_on(dev, load_library().mla_beam_select, params, logits.data_ptr(), s_batch if B > 1 else 0,
                   s_beam if W > 1 else 0, scores.data_ptr(), _ptr(finished), new_scores.data_ptr(),
                   tokens.data_ptr(), parents.data_ptr(), workspace.data_ptr(), need,
                   _raw_stream(dev) if stream is None else _stream_of(stream, dev))
@@ -1099,14 +1097,14 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, *, k: Optional[int] 
 
 def beam_workspace_bytes(batch: int, beams: int, k: int, vocab: int, dtype=torch.float32) -> int:
     """Bytes of a ``workspace`` for ``beam_select`` (0: it refuses such a call)."""
-    return int(load_library().mla_beam_workspace_size(
-        _beam_params_of(batch, beams, k, vocab, LOGITS_DTYPES[dtype], 0)))
+    return _beam_params_of(batch, beams, k, vocab, LOGITS_DTYPES[dtype], 0)[1]
 
 
-_beam_params: Dict[tuple, MlaBeamParams] = {}
+_beam_params: Dict[tuple, Tuple[MlaBeamParams, int]] = {}
 
 
-def _beam_params_of(*key) -> MlaBeamParams:
+def _beam_params_of(*key) -> Tuple[MlaBeamParams, int]:
+    """The parameter record of a call (fields in order) and its workspace bytes, made once."""
     p = _beam_params.get(key)
     if p is None:
         for v in key:
@@ -1114,7 +1112,8 @@ def _beam_params_of(*key) -> MlaBeamParams:
                 raise ValueError(f"{v} does not fit 32 bits")
         if len(_beam_params) >= 1024:
             _beam_params.clear()
-        p = _beam_params[key] = MlaBeamParams(*key)
+        record = MlaBeamParams(*key)
+        p = _beam_params[key] = record, int(load_library().mla_beam_workspace_size(record))
     return p
 
 

@@ -13,11 +13,12 @@
 // in 64 bits.
 //
 // What bounds it: the bytes of the logits, where there are many; a chain of two launches, else.
-// A row goes through a block in chunks that stay in registers.  The k largest of a chunk are found
-// by a threshold: of the maxima of 64 groups of its values the k-th largest has at least k
-// values at or above it, and seldom many more; those are collected and ranked by counting.
-// From the second chunk on the k-th largest so far raises the threshold, and most chunks add
-// nothing.
+// A row goes through a block in chunks that stay in registers, the next chunk's loads on their
+// way.  A thread keeps the maximum and the sum of its own values, so a chunk takes one barrier:
+// it asks whether any value passes the k-th largest so far.  Those that do are collected and
+// ranked by counting.  The first chunk, and one with very many of them, has a threshold first:
+// of the maxima of 64 groups of its values the k-th largest has at least k values at or
+// above it, and seldom many more.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -34,11 +35,11 @@ namespace mla {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kVectors = 8;             // 16-byte units of a thread in a chunk
+constexpr int kVectors = 4;             // 16-byte units of a thread in a chunk
 constexpr int kGroups = 64;             // groups of a chunk's values: four threads each
 constexpr int kMaxK = 64;
 constexpr int kRoom = 1024;             // candidates collected at most (ties may pass it)
-constexpr int kMaxLists = 256;          // candidate lists of a request at most
+constexpr int kMaxLists = 128;          // candidate lists of a request at most
 constexpr unsigned kAll = 0xffffffffu;
 constexpr float kNone = -INFINITY;
 
@@ -75,12 +76,11 @@ __device__ __forceinline__ float value_of(uint32_t word, int half) {
   }
 }
 
+constexpr float kLog2eHi = 1.44269502162933349609375f, kLog2eLo = 1.925963033500e-8f;
 // e^d for d <= 0: the product by log2(e) in two parts, so that its rounding is not of log2(e).
-__device__ __forceinline__ float exp_of(float d) {
-  return ptx::ex2(fmaf(d, 1.44269502162933349609375f, d * 1.925963033500e-8f));
-}
+__device__ __forceinline__ float exp_of(float d) { return ptx::ex2(fmaf(d, kLog2eHi, d * kLog2eLo)); }
 
-struct Part {  // of a row: what one block found
+struct Part {  // of a row, as one block found it
   double sum;  // of exp(x - top)
   float top;
   int pad;
@@ -95,17 +95,59 @@ struct Parts {
 
 }  // namespace
 
+// The k largest values of a chunk and of the list before it, one after another: for chunks
+// with more ties than there is room for.  (Apart, and from memory: it is hardly ever called, and would
+// take the other path's registers.)
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__device__ __noinline__ int select_slowly(const T* x, int begin, int end, int k, int n_top, const float* top_x,
+                                          const int* top_i, float* next_x, int* next_i, unsigned long long* best_key) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  float last_x = INFINITY;
+  int last_i = -1, found = 0;
+  for (; found < k; ++found) {
+    unsigned long long key = 0;  // (order of the value, lowest index); 0: none
+    auto look = [&](float y, int i) {
+      if (!(y > kNone) || !before(last_x, last_i, y, i)) return;
+      const unsigned long long q = ((unsigned long long)ordered(y) << 32) | (0xffffffffu - (unsigned)i);
+      key = q > key ? q : key;
+    };
+#pragma unroll 1
+    for (int i = begin + tid; i < end; i += kThreads) look((float)x[i], i);
+    if (tid < n_top) look(top_x[tid], top_i[tid]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const unsigned long long q = __shfl_xor_sync(kAll, key, o);
+      key = q > key ? q : key;
+    }
+    if (lane == 0) best_key[warp] = key;
+    __syncthreads();
+    key = 0;
+    for (int w = 0; w < kWarps; ++w) key = best_key[w] > key ? best_key[w] : key;
+    __syncthreads();
+    if (key == 0) break;
+    const uint32_t u = (uint32_t)(key >> 32);
+    last_x = __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xffffffffu));
+    last_i = (int)(0xffffffffu - (uint32_t)key);
+    if (tid == 0) {
+      next_x[found] = last_x;
+      next_i[found] = last_i;
+    }
+  }
+  return found;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 4)
 beam_parts_kernel(Logits in, const float* __restrict__ scores, const unsigned char* __restrict__ finished, int k,
                   Parts out) {
   constexpr int kPer = 16 / (int)sizeof(T);  // values of a unit
-  constexpr int kWordsPerUnit = 4, kHalves = 4 / (int)sizeof(T);
-  __shared__ float group_max[kGroups], warp_threshold;
-  __shared__ double warp_sum[kWarps];
+  constexpr int kHalves = 4 / (int)sizeof(T), kUnits = kThreads * kVectors;
+  __shared__ float group_max[kGroups], threshold;
   __shared__ float cand_x[kRoom], top_x[2][kMaxK];
   __shared__ int cand_i[kRoom], top_i[2][kMaxK], n_cand;
   __shared__ unsigned long long best_key[kWarps];
+  __shared__ float warp_max[kWarps];
+  __shared__ double warp_sum[kWarps];
   ptx::pdl_launch_dependents();
   const int row = blockIdx.x, part = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // a beam that has ended, or has no score, offers nothing that its logits decide
@@ -114,159 +156,137 @@ beam_parts_kernel(Logits in, const float* __restrict__ scores, const unsigned ch
   const T* x = static_cast<const T*>(in.base) + (row / in.beams) * in.batch_stride + (row % in.beams) * in.beam_stride;
   // units of 16 aligned bytes; the first and last may hold values outside the row
   const int off = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
-  const T* origin = x - off;
   const int units = (off + in.vocab + kPer - 1) / kPer;
-  int n_top = 0, cur = 0;
-  float run_max = kNone;
-  double run_sum = 0.0;
-  for (int c = part * out.chunks; c < (part + 1) * out.chunks && c * kThreads * kVectors < units; ++c) {
-    uint32_t word[kVectors][kWordsPerUnit];
-    const int unit0 = c * kThreads * kVectors + tid;
+  const int c0 = part * out.chunks, c1 = min(c0 + out.chunks, (units + kUnits - 1) / kUnits);
+  auto load = [&](int c, uint4 (&w)[kVectors]) {
 #pragma unroll
     for (int v = 0; v < kVectors; ++v) {
-      const int u = unit0 + v * kThreads, i0 = u * kPer - off;
-      if (i0 >= 0 && i0 + kPer <= in.vocab) {
-        const uint4 w = *(reinterpret_cast<const uint4*>(origin) + u);
-        word[v][0] = w.x, word[v][1] = w.y, word[v][2] = w.z, word[v][3] = w.w;
-      } else {
+      const int u = c * kUnits + v * kThreads + tid, i0 = u * kPer - off;
+      if (c < c1 && i0 >= 0 && i0 + kPer <= in.vocab) {
+        w[v] = __ldcs(reinterpret_cast<const uint4*>(x + i0));
+      } else {  // -inf where there is no value
+        constexpr uint32_t none = sizeof(T) == 4 ? 0xff800000u : std::is_same<T, __nv_bfloat16>::value ? 0xff80u : 0xfc00u;
+        uint32_t e[4];
 #pragma unroll
-        for (int e = 0; e < kWordsPerUnit; ++e) {
-          uint32_t w = 0;
+        for (int j = 0; j < 4; ++j) {
+          e[j] = 0;
 #pragma unroll
           for (int h = 0; h < kHalves; ++h) {
-            const int i = i0 + e * kHalves + h;
-            const bool in_row = i >= 0 && i < in.vocab;
-            if constexpr (sizeof(T) == 4)
-              w = in_row ? reinterpret_cast<const uint32_t*>(x)[i] : 0xff800000u;  // -inf
-            else
-              w |= (uint32_t)(in_row ? reinterpret_cast<const unsigned short*>(x)[i]
-                                     : std::is_same<T, __nv_bfloat16>::value ? 0xff80 : 0xfc00)
-                   << (16 * h);
+            const int i = i0 + j * kHalves + h;
+            uint32_t bits = none;
+            if (c < c1 && i >= 0 && i < in.vocab) {
+              if constexpr (sizeof(T) == 4) bits = reinterpret_cast<const uint32_t*>(x)[i];
+              else bits = reinterpret_cast<const unsigned short*>(x)[i];
+            }
+            e[j] |= bits << (16 * h);
           }
-          word[v][e] = w;
         }
+        w[v] = make_uint4(e[0], e[1], e[2], e[3]);
       }
     }
-    auto at = [&](int v, int e) { return value_of<T>(word[v][e / kHalves], e % kHalves); };
+  };
+  auto word_of = [](const uint4& w, int j) { return j == 0 ? w.x : j == 1 ? w.y : j == 2 ? w.z : w.w; };
+  uint4 now[kVectors], next_words[kVectors];
+  load(c0, now);
+  int n_top = 0, cur = 0;
+  float so_far = kNone;        // the list's last, once it is full
+  float m = kNone, sum = 0.f, low = 0.f;  // this thread's maximum, and sum of exp(x - m) with its rounding
+  for (int c = c0; c < c1; ++c) {
+    load(c + 1, next_words);
+    auto at = [&](int v, int e) { return value_of<T>(word_of(now[v], e / kHalves), e % kHalves); };
     float mine = kNone;
 #pragma unroll
     for (int v = 0; v < kVectors; ++v)
 #pragma unroll
       for (int e = 0; e < kPer; ++e) mine = fmaxf(mine, at(v, e));
+    const bool any = __syncthreads_or(mine > so_far);
+    if (mine > m) {
+      const float f = exp_of(m - mine);  // m = -inf: 0
+      sum *= f;
+      low *= f;
+      m = mine;
+    }
     {
-      float g = fmaxf(mine, __shfl_xor_sync(kAll, mine, 1));
-      g = fmaxf(g, __shfl_xor_sync(kAll, g, 2));
-      if ((lane & 3) == 0) group_max[tid >> 2] = g;
-      if (tid == 0) n_cand = n_top;
-    }
-    __syncthreads();
-    // the chunk's maximum, in every warp; the threshold, by the first two
-    float top = fmaxf(group_max[lane], group_max[lane + 32]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-    if (tid < kGroups) {
-      const float g = group_max[tid];
-      int rank = 0;
-#pragma unroll 8
-      for (int j = 0; j < kGroups; ++j) rank += before(group_max[j], j, g, tid) ? 1 : 0;
-      if (rank == k - 1) warp_threshold = g;
-    }
-    const float ref = top == kNone ? 0.f : top;
-    float part_sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int v = 0; v < kVectors; ++v)
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) part_sum[e & 3] += exp_of(at(v, e) - ref);
-    double sum = ((double)part_sum[0] + part_sum[1]) + ((double)part_sum[2] + part_sum[3]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-    if (lane == 0) warp_sum[warp] = sum;
-    if (tid < n_top) {  // the k largest so far are candidates again
-      cand_x[tid] = top_x[cur][tid];
-      cand_i[tid] = top_i[cur][tid];
-    }
-    __syncthreads();
-    const float chunk_least = warp_threshold, so_far = n_top == k ? top_x[cur][k - 1] : kNone;
-    // (a later token loses a tie against the list: strictly above its last)
-    if (mine >= chunk_least && mine > so_far) {
+      const float ref = m == kNone ? 0.f : m;
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int v = 0; v < kVectors; ++v)
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-          const float y = at(v, e);
-          if (y >= chunk_least && y > so_far) {
-            const int p = atomicAdd(&n_cand, 1);
-            if (p < kRoom) {
-              cand_x[p] = y;
-              cand_i[p] = (unit0 + v * kThreads) * kPer + e - off;
+        for (int e = 0; e < kPer; ++e) s[e & 3] += exp_of(at(v, e) - ref);
+      const float a = (s[0] + s[1]) + (s[2] + s[3]), t = sum + a, z = t - sum;
+      low += (sum - (t - z)) + (a - z);
+      sum = t;
+    }
+    if (any) {
+      // values above the list's last; the first chunk's, or of too many, from a threshold on
+      bool thin = n_top < k;
+      int n = 0;
+      for (;;) {
+        if (thin) {
+          float g = fmaxf(mine, __shfl_xor_sync(kAll, mine, 1));
+          g = fmaxf(g, __shfl_xor_sync(kAll, g, 2));
+          if ((lane & 3) == 0) group_max[tid >> 2] = g;
+        }
+        if (tid == 0) n_cand = n_top;
+        __syncthreads();
+        if (thin && tid < kGroups) {
+          const float g = group_max[tid];
+          int rank = 0;
+#pragma unroll 8
+          for (int j = 0; j < kGroups; ++j) rank += before(group_max[j], j, g, tid) ? 1 : 0;
+          if (rank == k - 1) threshold = g;
+        }
+        if (tid < n_top) {  // the k largest so far are candidates again
+          cand_x[tid] = top_x[cur][tid];
+          cand_i[tid] = top_i[cur][tid];
+        }
+        if (thin) __syncthreads();
+        const float least = thin ? threshold : kNone;
+        // (a later token loses a tie against the list: strictly above its last)
+        if (mine >= least && mine > so_far) {
+#pragma unroll
+          for (int v = 0; v < kVectors; ++v)
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) {
+              const float y = at(v, e);
+              if (y >= least && y > so_far) {
+                const int p = atomicAdd(&n_cand, 1);
+                if (p < kRoom) {
+                  cand_x[p] = y;
+                  cand_i[p] = (c * kUnits + v * kThreads + tid) * kPer + e - off;
+                }
+              }
             }
+        }
+        __syncthreads();
+        n = n_cand;
+        if (thin || n <= kRoom) break;
+        thin = true;
+        __syncthreads();  // (every thread has read the count)
+      }
+      const int next = cur ^ 1;
+      if (n <= kRoom) {
+        for (int j = tid; j < n; j += kThreads) {
+          const float y = cand_x[j];
+          const int i = cand_i[j];
+          int rank = 0;
+          for (int o = 0; o < n; ++o) rank += before(cand_x[o], cand_i[o], y, i) ? 1 : 0;
+          if (rank < k) {
+            top_x[next][rank] = y;
+            top_i[next][rank] = i;
           }
         }
-    }
-    if (tid == 0) {
-      double s = 0.0;
-      for (int w = 0; w < kWarps; ++w) s += warp_sum[w];
-      const float m = fmaxf(run_max, top), r = m == kNone ? 0.f : m;
-      // (a sum of nothing is 0, or a NaN; its maximum of -inf makes either count as it should)
-      run_sum = run_sum * exp((double)run_max - (double)r) + s * exp((double)top - (double)r);
-      run_max = m;
-    }
-    __syncthreads();
-    const int n = n_cand, next = cur ^ 1;
-    if (n == n_top) {
-      // (nothing new)
-    } else if (n <= kRoom) {
-      for (int j = tid; j < n; j += kThreads) {
-        const float y = cand_x[j];
-        const int i = cand_i[j];
-        int rank = 0;
-        for (int o = 0; o < n; ++o) rank += before(cand_x[o], cand_i[o], y, i) ? 1 : 0;
-        if (rank < k) {
-          top_x[next][rank] = y;
-          top_i[next][rank] = i;
-        }
+        n_top = min(k, n);
+      } else {
+        n_top = select_slowly(x, max(0, c * kUnits * kPer - off), min(in.vocab, (c + 1) * kUnits * kPer - off), k, n_top,
+                              top_x[cur], top_i[cur], top_x[next], top_i[next], best_key);
       }
-      n_top = min(k, n);
       cur = next;
-    } else {
-      // more ties than there is room for: the k largest one after another
-      float last_x = INFINITY;
-      int last_i = -1, found = 0;
-      for (; found < k; ++found) {
-        unsigned long long key = 0;  // (order of the value, lowest index); 0: none
-        auto look = [&](float y, int i) {
-          if (!(y > kNone) || !before(last_x, last_i, y, i)) return;
-          const unsigned long long q = ((unsigned long long)ordered(y) << 32) | (0xffffffffu - (unsigned)i);
-          key = q > key ? q : key;
-        };
-#pragma unroll
-        for (int v = 0; v < kVectors; ++v)
-#pragma unroll
-          for (int e = 0; e < kPer; ++e) look(at(v, e), (unit0 + v * kThreads) * kPer + e - off);
-        if (tid < n_top) look(top_x[cur][tid], top_i[cur][tid]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          const unsigned long long q = __shfl_xor_sync(kAll, key, o);
-          key = q > key ? q : key;
-        }
-        if (lane == 0) best_key[warp] = key;
-        __syncthreads();
-        key = 0;
-        for (int w = 0; w < kWarps; ++w) key = best_key[w] > key ? best_key[w] : key;
-        __syncthreads();
-        if (key == 0) break;
-        const uint32_t u = (uint32_t)(key >> 32);
-        last_x = __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xffffffffu));
-        last_i = (int)(0xffffffffu - (uint32_t)key);
-        if (tid == 0) {
-          top_x[next][found] = last_x;
-          top_i[next][found] = last_i;
-        }
-      }
-      n_top = found;
-      cur = next;
+      __syncthreads();
+      so_far = n_top == k ? top_x[cur][k - 1] : kNone;
     }
-    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < kVectors; ++v) now[v] = next_words[v];
   }
   const size_t list = (size_t)row * out.parts + part;
   if (tid < k) {
@@ -274,24 +294,49 @@ beam_parts_kernel(Logits in, const float* __restrict__ scores, const unsigned ch
     out.value[list * k + tid] = on ? top_x[cur][tid] : kNone;
     out.token[list * k + tid] = on ? top_i[cur][tid] : -1;
   }
-  if (tid == 0) out.part[list] = Part{run_sum, run_max, 0};
+  // the threads' sums, each relative to its own maximum, to the part's
+  float top = m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+  if (lane == 0) warp_max[warp] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, warp_max[w]);
+  // (no value: 0; a NaN, or an infinity's, stays one)
+  double s = ((double)sum + (double)low) * (double)exp_of(m - (top == kNone ? 0.f : top));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+  if (lane == 0) warp_sum[warp] = s;
+  __syncthreads();
+  if (tid == 0) {
+    for (int w = 1; w < kWarps; ++w) s += warp_sum[w];
+    out.part[list] = Part{s, top, 0};
+  }
 }
 
 // One block a request: the rows' normalisers, then the k best of all lists.
+constexpr int kDepths = 4, kStaged = 2048;
+
 __global__ void __launch_bounds__(kThreads)
 beam_join_kernel(const float* __restrict__ scores, const unsigned char* __restrict__ finished, int beams, int k,
                  int vocab, int end_token, Parts in, float* __restrict__ scores_out, int* __restrict__ tokens_out,
                  int* __restrict__ parents_out) {
-  __shared__ double row_top[kMaxK], row_log[kMaxK], row_score[kMaxK];  // (beams: at most 64, too)
-  __shared__ int row_kind[kMaxK];                                       // 0: nothing, 1: lists, 2: has ended
-  __shared__ double head[kMaxLists], cand_s[kRoom], threshold;
-  __shared__ unsigned long long deep, least_deep;
-  __shared__ long long cand_i[kRoom];
-  __shared__ double best_s[kWarps];
-  __shared__ long long best_i[kWarps];
+  __shared__ double row_log[kMaxK], row_score[kMaxK];  // (beams are 64 at most, too)
+  __shared__ float row_top[kMaxK];
+  __shared__ int row_kind[kMaxK];  // 0: nothing, 1: lists, 2: has ended
+  __shared__ float row_least[kMaxK];
+  __shared__ unsigned long long key[kDepths][kMaxLists], cand_s[kRoom], best_s[kWarps], threshold;
+  __shared__ long long cand_i[kRoom], best_i[kWarps];
+  __shared__ float staged[kStaged];
   __shared__ int n_cand;
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int lists = beams * in.parts;
+  const size_t list0 = (size_t)b * lists;
   ptx::pdl_wait();
+  // (beside the normalisers; lists that nobody wrote are not looked at)
+  const bool near = lists * k <= kStaged;
+  if (near)
+    for (int e = tid; e < lists * k; e += kThreads) staged[e] = in.value[list0 * k + e];
   for (int w = warp; w < beams; w += kWarps) {
     const int row = b * beams + w;
     const float c = scores[row];
@@ -315,75 +360,72 @@ beam_join_kernel(const float* __restrict__ scores, const unsigned char* __restri
       row_kind[w] = scored && done ? 2 : ok ? 1 : 0;
       row_top[w] = top;
       row_log[w] = ok ? log(sum) : 0.0;
-      row_score[w] = c;
+      row_score[w] = (double)c;
     }
   }
-  if (tid == 0) {
-    n_cand = 0;
-    threshold = -INFINITY;
-    deep = 0;
-    least_deep = ~0ull;
-  }
+  if (tid == 0) n_cand = 0;
   __syncthreads();
-  const int lists = beams * in.parts;
-  const size_t list0 = (size_t)b * lists;
-  // candidate j of a list: its score (-inf: none) and its place (w, token)
-  auto candidate = [&](int l, int j, long long& place) -> double {
-    const int w = l / in.parts;
-    place = -1;
-    if (row_kind[w] == 2) {
-      if (j > 0 || l != w * in.parts) return -INFINITY;
-      place = (long long)w * vocab + end_token;
-      return row_score[w];
-    }
-    if (row_kind[w] == 0) return -INFINITY;
-    const float x = in.value[(list0 + l) * k + j];
-    if (x == kNone) return -INFINITY;
-    place = (long long)w * vocab + in.token[(list0 + l) * k + j];
-    return (((double)x - row_top[w]) - row_log[w]) + row_score[w];
+  constexpr unsigned long long kNothing = 0;  // below the key of any score
+  // candidate j of a list: its key, and its place (w, token)
+  auto logit = [&](int l, int j) { return near ? staged[l * k + j] : in.value[(list0 + l) * k + j]; };
+  auto key_of = [&](int l, int j) -> unsigned long long {
+    const int w = l / in.parts, kind = row_kind[w];
+    if (kind == 2) return j == 0 && l == w * in.parts ? ordered64(row_score[w]) : kNothing;
+    if (kind == 0) return kNothing;
+    const float x = logit(l, j);
+    return x == kNone ? kNothing : ordered64((((double)x - row_top[w]) - row_log[w]) + row_score[w]);
   };
-  auto ahead = [](double sa, long long ia, double sb, long long ib) { return sa > sb || (sa == sb && ia < ib); };
-  // A threshold that at least k candidates are at or above: the k-th largest of the lists'
-  // first; of fewer lists, the least of their d-th, d lists of which make k, or the largest
-  // k-th of one of them.
-  const int depth = (k + lists - 1) / lists;
-  for (int l = tid; l < lists; l += kThreads) {
-    long long i;
-    head[l] = candidate(l, 0, i);
-    if (lists < k) {
-      atomicMin(&least_deep, ordered64(candidate(l, depth - 1, i)));
-      atomicMax(&deep, ordered64(candidate(l, k - 1, i)));
-    }
+  auto place_of = [&](int l, int j) -> long long {
+    const int w = l / in.parts;
+    return (long long)w * vocab + (row_kind[w] == 2 ? end_token : in.token[(list0 + l) * k + j]);
+  };
+  // A threshold that at least k candidates are at or above: for some depths d, the
+  // ceil(k / d)-th largest of the lists' d-th candidates, and of these the largest.  (With d
+  // = 1, 4, 16, 64 fewer than 4 k candidates for each d pass it, ties apart, however the
+  // beams' scores lie.)
+  for (int t = tid; t < kDepths * lists; t += kThreads) {
+    const int e = t / lists, l = t - e * lists, d = min(1 << (2 * e), k);
+    key[e][l] = key_of(l, d - 1);
+  }
+  if (tid == 0) threshold = kNothing;
+  __syncthreads();
+  for (int t = tid; t < kDepths * lists; t += kThreads) {
+    const int e = t / lists, l = t - e * lists, d = min(1 << (2 * e), k), want = (k + d - 1) / d;
+    if (want > lists) continue;
+    const unsigned long long s = key[e][l];
+    int rank = 0;
+    for (int o = 0; o < lists; ++o) rank += (key[e][o] > s || (key[e][o] == s && o < l)) ? 1 : 0;
+    if (rank == want - 1) atomicMax(&threshold, s);
   }
   __syncthreads();
-  if (lists >= k) {
-    for (int l = tid; l < lists; l += kThreads) {
-      const double s = head[l];
-      int rank = 0;
-      for (int o = 0; o < lists; ++o) rank += (head[o] > s || (head[o] == s && o < l)) ? 1 : 0;
-      if (rank == k - 1) threshold = s;
-    }
-  } else if (tid == 0) {
-    threshold = from_ordered64(deep > least_deep ? deep : least_deep);
+  const unsigned long long least = max(threshold, kNothing + 1);
+  // the same for a beam's logits, a little lower, which spares most the sums in 64 bits
+  if (tid < beams) {
+    // (off by some 2^-23 of the largest term at most)
+    const float score = threshold == kNothing ? kNone : (float)from_ordered64(threshold), c = (float)row_score[tid];
+    const float log_sum = (float)row_log[tid], top = row_top[tid];
+    row_least[tid] = score - c + log_sum + top - (fabsf(score) + fabsf(c) + fabsf(log_sum) + fabsf(top)) * 1e-6f;
   }
   __syncthreads();
-  const double least = threshold;
   for (int e = tid; e < lists * k; e += kThreads) {
-    const int l = e / k;
-    if (head[l] < least) continue;
-    long long i;
-    const double s = candidate(l, e - l * k, i);
-    if (s == -INFINITY || s < least) continue;
+    const int l = e / k, j = e - l * k;
+    if (key[0][l] < least) continue;
+    if (row_kind[l / in.parts] == 1 && logit(l, j) < row_least[l / in.parts]) continue;
+    const unsigned long long s = key_of(l, j);
+    if (s < least) continue;
     const int p = atomicAdd(&n_cand, 1);
     if (p < kRoom) {
       cand_s[p] = s;
-      cand_i[p] = i;
+      cand_i[p] = place_of(l, j);
     }
   }
   __syncthreads();
   const int n = n_cand;
-  auto write = [&](int rank, double s, long long i) {
-    scores_out[(size_t)b * k + rank] = (float)s;
+  auto ahead = [](unsigned long long sa, long long ia, unsigned long long sb, long long ib) {
+    return sa > sb || (sa == sb && ia < ib);
+  };
+  auto write = [&](int rank, unsigned long long s, long long i) {
+    scores_out[(size_t)b * k + rank] = s == kNothing ? kNone : (float)from_ordered64(s);
     tokens_out[(size_t)b * k + rank] = i < 0 ? -1 : (int)(i % vocab);
     parents_out[(size_t)b * k + rank] = i < 0 ? -1 : (int)(i / vocab);
   };
@@ -393,24 +435,24 @@ beam_join_kernel(const float* __restrict__ scores, const unsigned char* __restri
       for (int o = 0; o < n; ++o) rank += ahead(cand_s[o], cand_i[o], cand_s[j], cand_i[j]) ? 1 : 0;
       if (rank < k) write(rank, cand_s[j], cand_i[j]);
     }
-    for (int r = n + tid; r < k; r += kThreads) write(r, -INFINITY, -1);
+    for (int r = n + tid; r < k; r += kThreads) write(r, kNothing, -1);
     return;
   }
   // more ties than there is room for: one after another
-  double last_s = INFINITY;
+  unsigned long long last_s = ~0ull;
   long long last_i = -1;
   for (int r = 0; r < k; ++r) {
-    double s = -INFINITY;
+    unsigned long long s = kNothing;
     long long at = -1;
     for (int e = tid; e < lists * k; e += kThreads) {
-      long long i;
-      const double q = candidate(e / k, e % k, i);
-      if (q == -INFINITY || !ahead(last_s, last_i, q, i)) continue;
-      if (at < 0 || ahead(q, i, s, at)) s = q, at = i;
+      const unsigned long long q = key_of(e / k, e % k);
+      if (q == kNothing || q < s || q > last_s) continue;
+      const long long i = place_of(e / k, e % k);
+      if (ahead(last_s, last_i, q, i) && (at < 0 || ahead(q, i, s, at))) s = q, at = i;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      const double q = __shfl_xor_sync(kAll, s, o);
+      const unsigned long long q = __shfl_xor_sync(kAll, s, o);
       const long long i = __shfl_xor_sync(kAll, at, o);
       if (i >= 0 && (at < 0 || ahead(q, i, s, at))) s = q, at = i;
     }
@@ -419,14 +461,14 @@ beam_join_kernel(const float* __restrict__ scores, const unsigned char* __restri
       best_i[warp] = at;
     }
     __syncthreads();
-    s = -INFINITY;
+    s = kNothing;
     at = -1;
     for (int w = 0; w < kWarps; ++w)
       if (best_i[w] >= 0 && (at < 0 || ahead(best_s[w], best_i[w], s, at))) s = best_s[w], at = best_i[w];
     __syncthreads();
     if (tid == 0) write(r, s, at);
     if (at < 0) {
-      for (int q = r + 1 + tid; q < k; q += kThreads) write(q, -INFINITY, -1);
+      for (int q = r + 1 + tid; q < k; q += kThreads) write(q, kNothing, -1);
       break;
     }
     last_s = s;
