@@ -22,6 +22,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import threading
 from typing import Dict, Optional, Tuple
 
 import torch
@@ -1023,6 +1024,23 @@ def cache_gather(kv_cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: t
     return out
 
 
+_scratches = threading.local()
+
+
+def _scratch(need: int, dev: int, stream) -> torch.Tensor:
+    """Scratch of a call on the current stream: this thread's, kept for the stream, on which
+    calls follow on one another.  A call that is captured, or runs on a given stream, has its own."""
+    if stream is not None or torch.cuda.is_current_stream_capturing():
+        return torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", dev))
+    kept = _scratches.__dict__
+    key = dev, _raw_stream(dev)
+    t = kept.get(key)
+    if t is None or t.numel() < need:
+        t = kept[key] = torch.empty(max(need, 1 << 16), dtype=torch.uint8,
+                                    device=torch.device("cuda", dev))
+    return t
+
+
 LOGITS_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
@@ -1041,7 +1059,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, *, k: Optional[int] 
     by a beam whose score is not finite or that has a NaN or +inf among its logits;
     where a request has fewer than ``k`` continuations the rest are -inf, -1 and -1.
     ``out``: the three results' tensors (fp32, int32, int32).  ``workspace``: a uint8 tensor
-    of at least ``beam_workspace_bytes``.  What the call makes belongs to ``stream`` (the
+    of at least ``beam_workspace_bytes`` (without one, the thread keeps one for the stream).  What the call makes belongs to ``stream`` (the
     current one), where the kernels run."""
     if logits.dim() != 3 or not logits.is_cuda:
         raise ValueError("logits must be a CUDA tensor [batch, beams, vocab]")
@@ -1069,8 +1087,10 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, *, k: Optional[int] 
     params, need = _beam_params_of(B, W, k, V, kind, 0 if end_token is None else end_token)
     with _made_on(stream, dev):
         if out is None:
-            new_scores = torch.empty((B, k), dtype=torch.float32, device=logits.device)
-            tokens, parents = torch.empty((2, B, k), dtype=torch.int32, device=logits.device).unbind()
+            where = logits.device
+            new_scores = torch.empty((B, k), dtype=torch.float32, device=where)
+            tokens = torch.empty((B, k), dtype=torch.int32, device=where)
+            parents = torch.empty((B, k), dtype=torch.int32, device=where)
         else:
             new_scores, tokens, parents = out
             if not (new_scores.dtype is torch.float32 and new_scores.get_device() == dev
@@ -1080,7 +1100,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, *, k: Optional[int] 
                 if not _is_int32(t, dev, (B, k)):
                     _refuse(f"out[{i}]", t, _INT32, dev, (B, k))
         if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=logits.device)
+            workspace = _scratch(need, dev, stream)
         elif not (workspace.dtype is torch.uint8 and workspace.get_device() == dev
                   and workspace.is_contiguous() and workspace.numel() >= need):
             _refuse("workspace", workspace, "a contiguous uint8 tensor", dev, (need,))

@@ -6,19 +6,20 @@
 //   s(w, v) = c_w + x_w[v] - lse_w,   lse_w = ln sum_v exp(x_w[v]),
 // and the k best are wanted, the lowest (w, v) first among equals.  The logits are read once.
 // Within a beam the order is that of the logits themselves, so each block keeps the k largest
-// logits of its part of a row, exactly, beside the part's maximum and sum of exponentials; one
-// block a request then compares the scores of all parts' candidates in 64 bits.  What decides
-// between nearly equal candidates of two beams is lse: exponentials are of differences from the
-// maximum, taken with the product by log2(e) in two parts, and their sums leave a thread
-// in 64 bits.
+// logits of its part of a row, exactly, beside the part's sum of exponentials; one block a
+// request then compares the scores of all parts' candidates.  What decides between nearly equal
+// candidates of two beams is lse, so no rounding of it is common to a row's values: arguments
+// of exponentials carry the product by log2(e) in two parts, sums their rounding errors,
+// parts are joined by powers of two, and scores are pairs of floats (48 bits; the card has
+// few units for 64: with those the join took 10 us instead of 5).
 //
 // What bounds it: the bytes of the logits, where there are many; a chain of two launches, else.
-// A row goes through a block in chunks that stay in registers, the next chunk's loads on their
-// way.  A thread keeps the maximum and the sum of its own values, so a chunk takes one barrier:
-// it asks whether any value passes the k-th largest so far.  Those that do are collected and
-// ranked by counting.  The first chunk, and one with very many of them, has a threshold first:
-// of the maxima of 64 groups of its values the k-th largest has at least k values at or
-// above it, and seldom many more.
+// A thread streams its own values through shared memory, with no barrier and no copy of another's,
+// two chunks ahead: it keeps their maximum and sum.  (The rows' chunks are dealt out evenly, three
+// blocks to an SM; a block may take the end of one row and the start of the next.)  The k-th
+// largest maximum of 64 groups of threads is a threshold that at least k values are at or above,
+// and seldom many more; the few stretches of a thread's values whose maximum is not below it are
+// read again, and what passes is ranked by counting.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -35,12 +36,17 @@ namespace mla {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kBlocks = 456;            // three on each of 152 SMs, all at once
+constexpr int kStages = 3;             // chunks of a block on their way
 constexpr int kVectors = 4;             // 16-byte units of a thread in a chunk
-constexpr int kGroups = 64;             // groups of a chunk's values: four threads each
+constexpr int kGroups = 64;             // groups of a part's values: four threads each
 constexpr int kMaxK = 64;
 constexpr int kRoom = 1024;             // candidates collected at most (ties may pass it)
 constexpr int kMaxLists = 128;          // candidate lists of a request at most
 constexpr unsigned kAll = 0xffffffffu;
+constexpr int kStretches = 16;          // of a thread's part, each with its maximum
+constexpr size_t kRing = (size_t)kStages * kVectors * kThreads * 16;
+constexpr size_t kSmem = kRing + sizeof(float) * kStretches * kThreads;
 constexpr float kNone = -INFINITY;
 
 // Order-preserving bits of a float (-0 as 0).
@@ -49,14 +55,6 @@ __device__ __forceinline__ uint32_t ordered(float x) {
   return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 __device__ __forceinline__ bool before(float xa, int ia, float xb, int ib) { return xa > xb || (xa == xb && ia < ib); }
-
-__device__ __forceinline__ unsigned long long ordered64(double x) {
-  const unsigned long long u = (unsigned long long)__double_as_longlong(x + 0.0);
-  return u ^ ((u >> 63) ? ~0ull : 1ull << 63);
-}
-__device__ __forceinline__ double from_ordered64(unsigned long long u) {
-  return __longlong_as_double((long long)(u ^ ((u >> 63) ? 1ull << 63 : ~0ull)));
-}
 
 struct Logits {
   const void* base;
@@ -80,40 +78,112 @@ constexpr float kLog2eHi = 1.44269502162933349609375f, kLog2eLo = 1.925963033500
 // e^d for d <= 0: the product by log2(e) in two parts, so that its rounding is not of log2(e).
 __device__ __forceinline__ float exp_of(float d) { return ptx::ex2(fmaf(d, kLog2eHi, d * kLog2eLo)); }
 
-struct Part {  // of a row, as one block found it
-  double sum;  // of exp(x - top)
-  float top;
-  int pad;
+// A number as the sum of two floats, the second at most half a step of the first.
+struct Two {
+  float h, l;
 };
+__device__ __forceinline__ Two exact_sum(float a, float b) {
+  const float s = a + b, z = s - a;
+  return {s, (a - (s - z)) + (b - z)};
+}
+__device__ __forceinline__ Two settle(float h, float l) {  // |h| >= |l|
+  const float s = h + l;
+  return {s, l - (s - h)};
+}
+__device__ __forceinline__ Two add(Two a, float b) {
+  const Two s = exact_sum(a.h, b);
+  return settle(s.h, s.l + a.l);
+}
+__device__ __forceinline__ Two add(Two a, Two b) {
+  const Two s = exact_sum(a.h, b.h);
+  return settle(s.h, s.l + (a.l + b.l));
+}
+// e ln 2 for a whole e below 2^23.
+__device__ __forceinline__ Two times_ln2(float e) {
+  constexpr float kHi = 0.693147182464599609375f, kLo = -1.90465429995776e-9f;
+  const float p = e * kHi;
+  return settle(p, fmaf(e, kHi, -p) + e * kLo);
+}
+// ln x for 0 < x < 2^120: x = 2^e f, f in [0.75, 1.5), ln f = 2 atanh z, z = (f - 1) / (f + 1),
+// |z| <= 1/5, by its series; only its first term needs more than a float.  Off by some 2^-31.
+__device__ __forceinline__ Two log_of(Two x) {
+  const uint32_t bits = __float_as_uint(x.h);
+  int e = (int)(bits >> 23) - 127;
+  if ((bits & 0x7fffffu) >= 0x400000u) ++e;
+  const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+  const Two f{x.h * down, x.l * down};
+  const Two top = add(f, -1.f), bottom = add(f, 1.f);
+  const float q = top.h / bottom.h;
+  const float rest = (fmaf(-q, bottom.h, top.h) + top.l) - q * bottom.l;
+  const Two z = settle(q, rest / bottom.h);
+  const float y = z.h * z.h;
+  float t = 1.f / 13.f;
+  t = fmaf(t, y, 1.f / 11.f);
+  t = fmaf(t, y, 1.f / 9.f);
+  t = fmaf(t, y, 1.f / 7.f);
+  t = fmaf(t, y, 1.f / 5.f);
+  t = fmaf(t, y, 1.f / 3.f);
+  return add(times_ln2((float)e), add(Two{2.f * z.h, 2.f * z.l}, 2.f * z.h * y * t));
+}
+// Order-preserving bits of a score; 0: none (one past fp32's range is none, either).
+__device__ __forceinline__ unsigned long long key_of_score(Two s) {
+  if (!(fabsf(s.h) < INFINITY)) return 0;
+  return ((unsigned long long)ordered(s.h) << 32) | ordered(s.l);
+}
+__device__ __forceinline__ float score_of_key(unsigned long long key) {
+  const uint32_t u = (uint32_t)(key >> 32);
+  return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xffffffffu));
+}
+
+// x log2(e), and 2^(a - b) for a - b of 0.5 at most: 0 far below (a of -infinity included).
+__device__ __forceinline__ Two log2_of(float x) {
+  const float h = x * kLog2eHi;
+  return {h, fmaf(x, kLog2eHi, -h) + x * kLog2eLo};
+}
+__device__ __forceinline__ float power_of(Two a, Two b) {
+  const float d = a.h - b.h;
+  return d < -150.f ? 0.f : ptx::ex2(d + (a.l - b.l));
+}
+
+// A part of a row, as one block found it: sum_v exp(x_v) = (sum.h + sum.l) 2^power, power the
+// whole number next to its maximum times log2(e).  For a maximum of 2^20 and more, whose
+// powers a float does not hold, the sum is of exp(x_v - top).
+struct Part {
+  float top;
+  int power;
+  Two sum;
+};
+__device__ __forceinline__ bool is_far(float top) { return !(fabsf(top) < 1048576.f); }
 
 struct Parts {
-  Part* part;      // [rows][parts]
-  float* value;    // [rows][parts][k], descending; -inf: none
-  int* token;      // [rows][parts][k]
-  int parts, chunks;  // parts of a row, chunks of a part
+  Part* part;    // [rows][parts]
+  float* value;  // [rows][parts][k], descending; -inf: none
+  int* token;    // [rows][parts][k]
+  int rows, parts, chunks, share;  // lists of a row at most; chunks of a row, and of a block
+  // Row r's chunks are those from r * chunks on of all; block i has `share` from i * share on.
+  __device__ int first(int row) const { return (int)((long long)row * chunks / share); }
+  __device__ int count(int row) const { return (int)(((long long)(row + 1) * chunks - 1) / share) - first(row) + 1; }
 };
 
 }  // namespace
 
-// The k largest values of a chunk and of the list before it, one after another: for chunks
-// with more ties than there is room for.  (Apart, and from memory: it is hardly ever called, and would
-// take the other path's registers.)
+// The k largest of values [begin, end) of a row, one after another: for parts with more ties
+// than there is room for.  (Apart, as it is hardly ever called.)
 template <typename T>
-__device__ __noinline__ int select_slowly(const T* x, int begin, int end, int k, int n_top, const float* top_x,
-                                          const int* top_i, float* next_x, int* next_i, unsigned long long* best_key) {
+__device__ __noinline__ void select_slowly(const T* x, int begin, int end, int k, float* out_x, int* out_i,
+                                           unsigned long long* best_key) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   float last_x = INFINITY;
-  int last_i = -1, found = 0;
-  for (; found < k; ++found) {
+  int last_i = -1;
+  for (int found = 0; found < k; ++found) {
     unsigned long long key = 0;  // (order of the value, lowest index); 0: none
-    auto look = [&](float y, int i) {
-      if (!(y > kNone) || !before(last_x, last_i, y, i)) return;
+#pragma unroll 1
+    for (int i = begin + tid; i < end; i += kThreads) {
+      const float y = (float)x[i];
+      if (!(y > kNone) || !before(last_x, last_i, y, i)) continue;
       const unsigned long long q = ((unsigned long long)ordered(y) << 32) | (0xffffffffu - (unsigned)i);
       key = q > key ? q : key;
-    };
-#pragma unroll 1
-    for (int i = begin + tid; i < end; i += kThreads) look((float)x[i], i);
-    if (tid < n_top) look(top_x[tid], top_i[tid]);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       const unsigned long long q = __shfl_xor_sync(kAll, key, o);
@@ -124,193 +194,259 @@ __device__ __noinline__ int select_slowly(const T* x, int begin, int end, int k,
     key = 0;
     for (int w = 0; w < kWarps; ++w) key = best_key[w] > key ? best_key[w] : key;
     __syncthreads();
-    if (key == 0) break;
-    const uint32_t u = (uint32_t)(key >> 32);
-    last_x = __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xffffffffu));
-    last_i = (int)(0xffffffffu - (uint32_t)key);
+    const bool on = key != 0;
+    last_x = on ? score_of_key(key) : kNone;
+    last_i = on ? (int)(0xffffffffu - (uint32_t)key) : -1;
     if (tid == 0) {
-      next_x[found] = last_x;
-      next_i[found] = last_i;
+      out_x[found] = last_x;
+      out_i[found] = last_i;
     }
   }
-  return found;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, 3)
 beam_parts_kernel(Logits in, const float* __restrict__ scores, const unsigned char* __restrict__ finished, int k,
                   Parts out) {
   constexpr int kPer = 16 / (int)sizeof(T);  // values of a unit
   constexpr int kHalves = 4 / (int)sizeof(T), kUnits = kThreads * kVectors;
+  extern __shared__ __align__(16) uint4 ring[];  // [stage][unit of a thread][thread]
   __shared__ float group_max[kGroups], threshold;
-  __shared__ float cand_x[kRoom], top_x[2][kMaxK];
-  __shared__ int cand_i[kRoom], top_i[2][kMaxK], n_cand;
+  __shared__ int n_cand, n_hot;
   __shared__ unsigned long long best_key[kWarps];
-  __shared__ float warp_max[kWarps];
-  __shared__ double warp_sum[kWarps];
+  // once the row has gone through it, the ring holds the candidates and the places to look again
+  float* cand_x = reinterpret_cast<float*>(ring);
+  int* cand_i = reinterpret_cast<int*>(cand_x + kRoom);
+  unsigned short* hot = reinterpret_cast<unsigned short*>(cand_i + kRoom);  // thread + 256 stretch
+  static_assert(8 * kRoom + 2 * kStretches * kThreads <= kRing && kThreads == 256, "room");
+  float* stretch_max = reinterpret_cast<float*>(reinterpret_cast<char*>(ring) + kRing);  // [stretch][thread]
+  __shared__ Two warp_sum[kWarps];
   ptx::pdl_launch_dependents();
-  const int row = blockIdx.x, part = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const long long g0 = (long long)blockIdx.x * out.share, g1 = min(g0 + out.share, (long long)out.rows * out.chunks);
+#pragma unroll 1
+  for (long long g = g0; g < g1;) {
+  const int row = (int)(g / out.chunks), chunk0 = (int)(g - (long long)row * out.chunks);
+  const int chunk1 = (int)min((long long)out.chunks, chunk0 + g1 - g);
+  const int part = (int)blockIdx.x - out.first(row);
+  g += chunk1 - chunk0;
   // a beam that has ended, or has no score, offers nothing that its logits decide
-  if (finished && finished[row]) return;
-  if (!(fabsf(scores[row]) < INFINITY)) return;
+  if ((finished && finished[row]) || !(fabsf(scores[row]) < INFINITY)) continue;
   const T* x = static_cast<const T*>(in.base) + (row / in.beams) * in.batch_stride + (row % in.beams) * in.beam_stride;
-  // units of 16 aligned bytes; the first and last may hold values outside the row
+  // units of 16 aligned bytes; the row's first and last may reach out of it
   const int off = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
   const int units = (off + in.vocab + kPer - 1) / kPer;
-  const int c0 = part * out.chunks, c1 = min(c0 + out.chunks, (units + kUnits - 1) / kUnits);
-  auto load = [&](int c, uint4 (&w)[kVectors]) {
+  const int u0 = chunk0 * kUnits, u1 = min(chunk1 * kUnits, units);
+  const int f0 = off > 0 ? max(u0, 1) : u0, f1 = min(u1, (off + in.vocab) / kPer);  // whole ones
+  constexpr uint32_t kNothing = sizeof(T) == 4 ? 0xff800000u
+                                : std::is_same<T, __nv_bfloat16>::value ? 0xff80ff80u : 0xfc00fc00u;  // -inf
+  auto unit_at = [&](int u) { return reinterpret_cast<const uint4*>(x + ((long long)u * kPer - off)); };
+  // an edge of the row: thread 0's the first unit, thread 1's the last, where they are not whole
+  auto edge = [&]() -> uint4 {
+    const int u = tid == 0 ? 0 : units - 1;
+    uint32_t e[4] = {kNothing, kNothing, kNothing, kNothing};
+    const bool mine = tid == 0 ? u0 == 0 && f0 > 0 : tid == 1 && u0 < units && u1 == units && f1 < units &&
+                                                                  !(units == 1 && off > 0);
+    if (mine) {
 #pragma unroll
-    for (int v = 0; v < kVectors; ++v) {
-      const int u = c * kUnits + v * kThreads + tid, i0 = u * kPer - off;
-      if (c < c1 && i0 >= 0 && i0 + kPer <= in.vocab) {
-        w[v] = __ldcs(reinterpret_cast<const uint4*>(x + i0));
-      } else {  // -inf where there is no value
-        constexpr uint32_t none = sizeof(T) == 4 ? 0xff800000u : std::is_same<T, __nv_bfloat16>::value ? 0xff80u : 0xfc00u;
-        uint32_t e[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          e[j] = 0;
-#pragma unroll
-          for (int h = 0; h < kHalves; ++h) {
-            const int i = i0 + j * kHalves + h;
-            uint32_t bits = none;
-            if (c < c1 && i >= 0 && i < in.vocab) {
-              if constexpr (sizeof(T) == 4) bits = reinterpret_cast<const uint32_t*>(x)[i];
-              else bits = reinterpret_cast<const unsigned short*>(x)[i];
-            }
-            e[j] |= bits << (16 * h);
-          }
+      for (int j = 0; j < kPer; ++j) {
+        const int i = u * kPer - off + j;
+        if (i < 0 || i >= in.vocab) continue;
+        if constexpr (sizeof(T) == 4) {
+          e[j] = reinterpret_cast<const uint32_t*>(x)[i];
+        } else {
+          const uint32_t bits = reinterpret_cast<const unsigned short*>(x)[i];
+          e[j / 2] = j & 1 ? (e[j / 2] & 0xffffu) | bits << 16 : (e[j / 2] & 0xffff0000u) | bits;
         }
-        w[v] = make_uint4(e[0], e[1], e[2], e[3]);
+      }
+    }
+    return make_uint4(e[0], e[1], e[2], e[3]);
+  };
+  auto at = [](const uint4& w, int e) {
+    const int j = e / kHalves;
+    return value_of<T>(j == 0 ? w.x : j == 1 ? w.y : j == 2 ? w.z : w.w, e % kHalves);
+  };
+  auto bring = [&](int chunk) {
+    const int u = f0 + chunk * kUnits + tid;
+    uint4* to = ring + (chunk % kStages) * kUnits + tid;
+#pragma unroll
+    for (int v = 0; v < kVectors; ++v)
+      if (u + v * kThreads < f1) ptx::cp_async_16(to + v * kThreads, unit_at(u + v * kThreads));
+    ptx::cp_async_commit();
+  };
+  const int chunks = f1 > f0 ? (f1 - f0 + kUnits - 1) / kUnits : 0;
+  for (int c = 0; c < kStages - 1; ++c) bring(c);
+  // a thread's chunks in up to kStretches stretches, whose maxima it writes down
+  const int stretch = (chunks + kStretches - 1) / kStretches;
+  float m = kNone, here = kNone;  // this thread's maximum, that of the stretch,
+  Two sum{0.f, 0.f};              // and sum of exp(x - m)
+  auto take = [&](const uint4* w, auto count) {
+    constexpr int kCount = decltype(count)::value;
+    float mine = kNone;
+#pragma unroll
+    for (int v = 0; v < kCount; ++v)
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) mine = fmaxf(mine, at(w[v], e));
+    here = fmaxf(here, mine);
+    if (mine > m) {
+      const float f = exp_of(m - mine);  // m = -inf: 0
+      sum.h *= f;
+      sum.l *= f;
+      m = mine;
+    }
+    const float ref = m == kNone ? 0.f : m;
+    const uint64_t minus = ptx::pack_f32x2(-ref, -ref), hi = ptx::pack_f32x2(kLog2eHi, kLog2eHi),
+                   lo = ptx::pack_f32x2(kLog2eLo, kLog2eLo);
+    uint64_t s[2] = {0, 0};
+#pragma unroll
+    for (int v = 0; v < kCount; ++v)
+#pragma unroll
+      for (int e = 0; e < kPer; e += 2) {
+        // exp_of, two at a time
+        const uint64_t d = ptx::add_f32x2(ptx::pack_f32x2(at(w[v], e), at(w[v], e + 1)), minus);
+        float a, b;
+        ptx::unpack_f32x2(ptx::fma_f32x2(d, hi, ptx::mul_f32x2(d, lo)), a, b);
+        s[(e >> 1) & 1] = ptx::add_f32x2(s[(e >> 1) & 1], ptx::pack_f32x2(ptx::ex2(a), ptx::ex2(b)));
+      }
+    float a, b;
+    ptx::unpack_f32x2(ptx::add_f32x2(s[0], s[1]), a, b);
+    const Two t = exact_sum(sum.h, a + b);
+    sum = {t.h, t.l + sum.l};
+  };
+  for (int c = 0; c < chunks; ++c) {
+    bring(c + kStages - 1);
+    ptx::cp_async_wait<kStages - 1>();  // this thread's copies of chunk c are there
+    const uint4* from = ring + (c % kStages) * kUnits + tid;
+    uint4 w[kVectors];
+    if (f0 + (c + 1) * kUnits <= f1) {
+#pragma unroll
+      for (int v = 0; v < kVectors; ++v) w[v] = from[v * kThreads];
+    } else {
+      const uint4 none = make_uint4(kNothing, kNothing, kNothing, kNothing);
+#pragma unroll
+      for (int v = 0; v < kVectors; ++v)
+        w[v] = f0 + c * kUnits + v * kThreads + tid < f1 ? from[v * kThreads] : none;
+    }
+    take(w, std::integral_constant<int, kVectors>());
+    if ((c + 1) % stretch == 0 || c + 1 == chunks) {
+      stretch_max[c / stretch * kThreads + tid] = here;
+      here = kNone;
+    }
+  }
+  uint4 border;
+  if (tid < 2) {
+    border = edge();
+    take(&border, std::integral_constant<int, 1>());
+  }
+  // the maxima of four threads each
+  {
+    float g = fmaxf(m, __shfl_xor_sync(kAll, m, 1));
+    g = fmaxf(g, __shfl_xor_sync(kAll, g, 2));
+    if ((lane & 3) == 0) group_max[tid >> 2] = g;
+    if (tid == 0) n_hot = n_cand = 0;
+  }
+  __syncthreads();
+  {  // a group's rank by its four threads
+    const int group = tid >> 2;
+    const float g = group_max[group];
+    int rank = 0;
+#pragma unroll
+    for (int j = 0; j < kGroups / 4; ++j) {
+      const int o = 4 * j + (lane & 3);
+      rank += before(group_max[o], o, g, group) ? 1 : 0;
+    }
+    rank += __shfl_xor_sync(kAll, rank, 1);
+    rank += __shfl_xor_sync(kAll, rank, 2);
+    if (rank == k - 1) threshold = g;
+  }
+  float top = fmaxf(group_max[lane], group_max[lane + 32]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+  // the threads' sums, relative to 2^power (far: to e^top)
+  const float power = is_far(top) ? 0.f : rintf(top * kLog2eHi);
+  {
+    // (no value: a sum of 0; a NaN, or an infinity's, stays one)
+    const float f = !is_far(top) ? power_of(log2_of(m), Two{power, 0.f}) : top > kNone ? exp_of(m - top) : 1.f;
+    sum = settle(sum.h * f, sum.l * f);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const Two other{__shfl_xor_sync(kAll, sum.h, o), __shfl_xor_sync(kAll, sum.l, o)};
+      sum = add(sum, other);
+    }
+    if (lane == 0) warp_sum[warp] = sum;
+  }
+  __syncthreads();
+  // the stretches that have a value at or above the threshold
+  const float least = threshold;
+  const int stretches = chunks > 0 ? (chunks + stretch - 1) / stretch : 0;
+  if (m >= least && m > kNone)
+    for (int z = 0; z < stretches; ++z) {
+      const float y = stretch_max[z * kThreads + tid];
+      if (y >= least && y > kNone) hot[atomicAdd(&n_hot, 1)] = (unsigned short)(tid + kThreads * z);
+    }
+  __syncthreads();
+  auto offer = [&](const uint4& w, int u) {
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const float y = at(w, e);
+      if (y >= least && y > kNone) {
+        const int p = atomicAdd(&n_cand, 1);
+        if (p < kRoom) {
+          cand_x[p] = y;
+          cand_i[p] = u * kPer + e - off;
+        }
       }
     }
   };
-  auto word_of = [](const uint4& w, int j) { return j == 0 ? w.x : j == 1 ? w.y : j == 2 ? w.z : w.w; };
-  uint4 now[kVectors], next_words[kVectors];
-  load(c0, now);
-  int n_top = 0, cur = 0;
-  float so_far = kNone;        // the list's last, once it is full
-  float m = kNone, sum = 0.f, low = 0.f;  // this thread's maximum, and sum of exp(x - m) with its rounding
-  for (int c = c0; c < c1; ++c) {
-    load(c + 1, next_words);
-    auto at = [&](int v, int e) { return value_of<T>(word_of(now[v], e / kHalves), e % kHalves); };
-    float mine = kNone;
+  const int each = stretch * kVectors, again = n_hot * each;  // units of a stretch
+  constexpr int kAgain = 4;
+  for (int q0 = tid; q0 < again; q0 += kAgain * kThreads) {
+    uint4 w[kAgain];
+    int u[kAgain];
 #pragma unroll
-    for (int v = 0; v < kVectors; ++v)
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) mine = fmaxf(mine, at(v, e));
-    const bool any = __syncthreads_or(mine > so_far);
-    if (mine > m) {
-      const float f = exp_of(m - mine);  // m = -inf: 0
-      sum *= f;
-      low *= f;
-      m = mine;
-    }
-    {
-      const float ref = m == kNone ? 0.f : m;
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int v = 0; v < kVectors; ++v)
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) s[e & 3] += exp_of(at(v, e) - ref);
-      const float a = (s[0] + s[1]) + (s[2] + s[3]), t = sum + a, z = t - sum;
-      low += (sum - (t - z)) + (a - z);
-      sum = t;
-    }
-    if (any) {
-      // values above the list's last; the first chunk's, or of too many, from a threshold on
-      bool thin = n_top < k;
-      int n = 0;
-      for (;;) {
-        if (thin) {
-          float g = fmaxf(mine, __shfl_xor_sync(kAll, mine, 1));
-          g = fmaxf(g, __shfl_xor_sync(kAll, g, 2));
-          if ((lane & 3) == 0) group_max[tid >> 2] = g;
-        }
-        if (tid == 0) n_cand = n_top;
-        __syncthreads();
-        if (thin && tid < kGroups) {
-          const float g = group_max[tid];
-          int rank = 0;
-#pragma unroll 8
-          for (int j = 0; j < kGroups; ++j) rank += before(group_max[j], j, g, tid) ? 1 : 0;
-          if (rank == k - 1) threshold = g;
-        }
-        if (tid < n_top) {  // the k largest so far are candidates again
-          cand_x[tid] = top_x[cur][tid];
-          cand_i[tid] = top_i[cur][tid];
-        }
-        if (thin) __syncthreads();
-        const float least = thin ? threshold : kNone;
-        // (a later token loses a tie against the list: strictly above its last)
-        if (mine >= least && mine > so_far) {
-#pragma unroll
-          for (int v = 0; v < kVectors; ++v)
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) {
-              const float y = at(v, e);
-              if (y >= least && y > so_far) {
-                const int p = atomicAdd(&n_cand, 1);
-                if (p < kRoom) {
-                  cand_x[p] = y;
-                  cand_i[p] = (c * kUnits + v * kThreads + tid) * kPer + e - off;
-                }
-              }
-            }
-        }
-        __syncthreads();
-        n = n_cand;
-        if (thin || n <= kRoom) break;
-        thin = true;
-        __syncthreads();  // (every thread has read the count)
+    for (int j = 0; j < kAgain; ++j) {
+      const int q = q0 + j * kThreads, h = q / each;
+      u[j] = f1;
+      if (q < again) {
+        const int z = hot[h];
+        u[j] = f0 + (z / kThreads * each + q - h * each) * kThreads + z % kThreads;
       }
-      const int next = cur ^ 1;
-      if (n <= kRoom) {
-        for (int j = tid; j < n; j += kThreads) {
-          const float y = cand_x[j];
-          const int i = cand_i[j];
-          int rank = 0;
-          for (int o = 0; o < n; ++o) rank += before(cand_x[o], cand_i[o], y, i) ? 1 : 0;
-          if (rank < k) {
-            top_x[next][rank] = y;
-            top_i[next][rank] = i;
-          }
-        }
-        n_top = min(k, n);
-      } else {
-        n_top = select_slowly(x, max(0, c * kUnits * kPer - off), min(in.vocab, (c + 1) * kUnits * kPer - off), k, n_top,
-                              top_x[cur], top_i[cur], top_x[next], top_i[next], best_key);
-      }
-      cur = next;
-      __syncthreads();
-      so_far = n_top == k ? top_x[cur][k - 1] : kNone;
+      w[j] = make_uint4(kNothing, kNothing, kNothing, kNothing);
+      if (u[j] < f1) w[j] = *unit_at(u[j]);
     }
 #pragma unroll
-    for (int v = 0; v < kVectors; ++v) now[v] = next_words[v];
+    for (int j = 0; j < kAgain; ++j) offer(w[j], u[j]);
   }
+  if (tid < 2) offer(border, tid == 0 ? 0 : units - 1);
+  __syncthreads();
   const size_t list = (size_t)row * out.parts + part;
-  if (tid < k) {
-    const bool on = tid < n_top;
-    out.value[list * k + tid] = on ? top_x[cur][tid] : kNone;
-    out.token[list * k + tid] = on ? top_i[cur][tid] : -1;
+  float* out_x = out.value + list * k;
+  int* out_i = out.token + list * k;
+  const int n = n_cand;
+  if (n <= kRoom) {
+    for (int j = tid; j < n; j += kThreads) {
+      const float y = cand_x[j];
+      const int i = cand_i[j];
+      int rank = 0;
+      for (int o = 0; o < n; ++o) rank += before(cand_x[o], cand_i[o], y, i) ? 1 : 0;
+      if (rank < k) {
+        out_x[rank] = y;
+        out_i[rank] = i;
+      }
+    }
+    for (int r = n + tid; r < k; r += kThreads) {
+      out_x[r] = kNone;
+      out_i[r] = -1;
+    }
+  } else {
+    select_slowly(x, max(0, u0 * kPer - off), min(in.vocab, u1 * kPer - off), k, out_x, out_i, best_key);
   }
-  // the threads' sums, each relative to its own maximum, to the part's
-  float top = m;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-  if (lane == 0) warp_max[warp] = top;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, warp_max[w]);
-  // (no value: 0; a NaN, or an infinity's, stays one)
-  double s = ((double)sum + (double)low) * (double)exp_of(m - (top == kNone ? 0.f : top));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
-  if (lane == 0) warp_sum[warp] = s;
-  __syncthreads();
   if (tid == 0) {
-    for (int w = 1; w < kWarps; ++w) s += warp_sum[w];
-    out.part[list] = Part{s, top, 0};
+    Two s = warp_sum[0];
+    for (int w = 1; w < kWarps; ++w) s = add(s, warp_sum[w]);
+    out.part[list] = Part{top, (int)power, s};
+  }
+  __syncthreads();  // (the next row takes the ring)
   }
 }
 
@@ -321,10 +457,10 @@ __global__ void __launch_bounds__(kThreads)
 beam_join_kernel(const float* __restrict__ scores, const unsigned char* __restrict__ finished, int beams, int k,
                  int vocab, int end_token, Parts in, float* __restrict__ scores_out, int* __restrict__ tokens_out,
                  int* __restrict__ parents_out) {
-  __shared__ double row_log[kMaxK], row_score[kMaxK];  // (beams are 64 at most, too)
-  __shared__ float row_top[kMaxK];
-  __shared__ int row_kind[kMaxK];  // 0: nothing, 1: lists, 2: has ended
+  __shared__ Two row_less[kMaxK];                    // what a row's logits are diminished by: lse - score, without `top`
+  __shared__ float row_top[kMaxK], row_score[kMaxK];  // (beams are 64 at most, too); top: 0 but for far ones
   __shared__ float row_least[kMaxK];
+  __shared__ int row_lists[kMaxK];  // of a beam; 0: it offers nothing, -1: it has ended
   __shared__ unsigned long long key[kDepths][kMaxLists], cand_s[kRoom], best_s[kWarps], threshold;
   __shared__ long long cand_i[kRoom], best_i[kWarps];
   __shared__ float staged[kStaged];
@@ -341,43 +477,70 @@ beam_join_kernel(const float* __restrict__ scores, const unsigned char* __restri
     const int row = b * beams + w;
     const float c = scores[row];
     const bool scored = fabsf(c) < INFINITY, done = finished && finished[row];
+    Two sum{0.f, 0.f};
     float top = kNone;
-    double sum = 0.0;
+    int power = -(1 << 24);
     if (scored && !done) {
-      for (int p = lane; p < in.parts; p += 32) top = fmaxf(top, in.part[(size_t)row * in.parts + p].top);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-      for (int p = lane; p < in.parts; p += 32) {
-        const Part q = in.part[(size_t)row * in.parts + p];
-        sum += q.sum * exp((double)q.top - (top == kNone ? 0.0 : (double)top));
+      const Part* of = in.part + (size_t)row * in.parts;
+      const int parts = in.count(row);
+      for (int p = lane; p < parts; p += 32) {
+        const Part q = of[p];
+        top = fmaxf(top, q.top);
+        if (!is_far(q.top)) power = max(power, q.power);
       }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+      power = __reduce_max_sync(kAll, power);
+      const bool far = is_far(top);
+      for (int p = lane; p < parts; p += 32) {
+        const Part q = of[p];
+        // (a part without a value adds 0, or a NaN that it holds)
+        float f;
+        if (far && is_far(q.top)) f = q.top > kNone ? exp_of(q.top - top) : 1.f;
+        else if (far) f = power_of(Two{(float)q.power, 0.f}, log2_of(top));
+        else f = power_of(is_far(q.top) ? log2_of(q.top) : Two{(float)q.power, 0.f}, Two{(float)power, 0.f});
+        sum = add(sum, Two{q.sum.h * f, q.sum.l * f});
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const Two other{__shfl_xor_sync(kAll, sum.h, o), __shfl_xor_sync(kAll, sum.l, o)};
+        sum = add(sum, other);
+      }
     }
     if (lane == 0) {
       // an infinity or a NaN among the logits, or nothing above -inf: no continuation
-      const bool ok = scored && !done && fabsf(top) < INFINITY && sum > 0.0 && sum < 1e300;
-      row_kind[w] = scored && done ? 2 : ok ? 1 : 0;
-      row_top[w] = top;
-      row_log[w] = ok ? log(sum) : 0.0;
-      row_score[w] = (double)c;
+      const bool ok = scored && !done && fabsf(top) < INFINITY && sum.h > 0.f && sum.h < 1e35f;
+      row_lists[w] = scored && done ? -1 : ok ? in.count(row) : 0;
+      row_top[w] = is_far(top) ? top : 0.f;
+      row_score[w] = c;
+      Two less{0.f, 0.f};
+      if (ok) {
+        less = log_of(sum);
+        if (!is_far(top)) less = add(less, times_ln2((float)power));
+        less = add(less, -c);
+      }
+      row_less[w] = less;
     }
   }
-  if (tid == 0) n_cand = 0;
+  if (tid == 0) {
+    n_cand = 0;
+    threshold = 0;
+  }
   __syncthreads();
-  constexpr unsigned long long kNothing = 0;  // below the key of any score
-  // candidate j of a list: its key, and its place (w, token)
+  // candidate j of a list: its key (0: none), and its place (w, token)
   auto logit = [&](int l, int j) { return near ? staged[l * k + j] : in.value[(list0 + l) * k + j]; };
   auto key_of = [&](int l, int j) -> unsigned long long {
-    const int w = l / in.parts, kind = row_kind[w];
-    if (kind == 2) return j == 0 && l == w * in.parts ? ordered64(row_score[w]) : kNothing;
-    if (kind == 0) return kNothing;
+    const int w = l / in.parts, lists_of = row_lists[w], p = l - w * in.parts;
+    if (lists_of < 0) return j == 0 && p == 0 ? key_of_score(Two{row_score[w], 0.f}) : 0;
+    if (p >= lists_of) return 0;
     const float x = logit(l, j);
-    return x == kNone ? kNothing : ordered64((((double)x - row_top[w]) - row_log[w]) + row_score[w]);
+    if (x == kNone) return 0;
+    const Two less = row_less[w];
+    return key_of_score(add(exact_sum(x, -row_top[w]), Two{-less.h, -less.l}));
   };
   auto place_of = [&](int l, int j) -> long long {
     const int w = l / in.parts;
-    return (long long)w * vocab + (row_kind[w] == 2 ? end_token : in.token[(list0 + l) * k + j]);
+    return (long long)w * vocab + (row_lists[w] < 0 ? end_token : in.token[(list0 + l) * k + j]);
   };
   // A threshold that at least k candidates are at or above: for some depths d, the
   // ceil(k / d)-th largest of the lists' d-th candidates, and of these the largest.  (With d
@@ -387,30 +550,28 @@ beam_join_kernel(const float* __restrict__ scores, const unsigned char* __restri
     const int e = t / lists, l = t - e * lists, d = min(1 << (2 * e), k);
     key[e][l] = key_of(l, d - 1);
   }
-  if (tid == 0) threshold = kNothing;
   __syncthreads();
   for (int t = tid; t < kDepths * lists; t += kThreads) {
     const int e = t / lists, l = t - e * lists, d = min(1 << (2 * e), k), want = (k + d - 1) / d;
-    if (want > lists) continue;
+    if (want > lists || (e > 0 && 1 << (2 * e - 2) >= k)) continue;
     const unsigned long long s = key[e][l];
     int rank = 0;
     for (int o = 0; o < lists; ++o) rank += (key[e][o] > s || (key[e][o] == s && o < l)) ? 1 : 0;
     if (rank == want - 1) atomicMax(&threshold, s);
   }
   __syncthreads();
-  const unsigned long long least = max(threshold, kNothing + 1);
-  // the same for a beam's logits, a little lower, which spares most the sums in 64 bits
+  const unsigned long long least = max(threshold, 1ull);
+  // the same for a beam's logits, a little lower (some 2^-22 of its terms), which spares most
+  // candidates their sums
   if (tid < beams) {
-    // (off by some 2^-23 of the largest term at most)
-    const float score = threshold == kNothing ? kNone : (float)from_ordered64(threshold), c = (float)row_score[tid];
-    const float log_sum = (float)row_log[tid], top = row_top[tid];
-    row_least[tid] = score - c + log_sum + top - (fabsf(score) + fabsf(c) + fabsf(log_sum) + fabsf(top)) * 1e-6f;
+    const float s = threshold == 0 ? kNone : score_of_key(threshold), less = row_less[tid].h, top = row_top[tid];
+    row_least[tid] = s + less + top - (fabsf(s) + fabsf(less) + fabsf(top) + fabsf(row_score[tid])) * 1e-6f;
   }
   __syncthreads();
   for (int e = tid; e < lists * k; e += kThreads) {
     const int l = e / k, j = e - l * k;
     if (key[0][l] < least) continue;
-    if (row_kind[l / in.parts] == 1 && logit(l, j) < row_least[l / in.parts]) continue;
+    if (row_lists[l / in.parts] > 0 && logit(l, j) < row_least[l / in.parts]) continue;
     const unsigned long long s = key_of(l, j);
     if (s < least) continue;
     const int p = atomicAdd(&n_cand, 1);
@@ -425,7 +586,7 @@ beam_join_kernel(const float* __restrict__ scores, const unsigned char* __restri
     return sa > sb || (sa == sb && ia < ib);
   };
   auto write = [&](int rank, unsigned long long s, long long i) {
-    scores_out[(size_t)b * k + rank] = s == kNothing ? kNone : (float)from_ordered64(s);
+    scores_out[(size_t)b * k + rank] = s == 0 ? kNone : score_of_key(s);
     tokens_out[(size_t)b * k + rank] = i < 0 ? -1 : (int)(i % vocab);
     parents_out[(size_t)b * k + rank] = i < 0 ? -1 : (int)(i / vocab);
   };
@@ -435,18 +596,18 @@ beam_join_kernel(const float* __restrict__ scores, const unsigned char* __restri
       for (int o = 0; o < n; ++o) rank += ahead(cand_s[o], cand_i[o], cand_s[j], cand_i[j]) ? 1 : 0;
       if (rank < k) write(rank, cand_s[j], cand_i[j]);
     }
-    for (int r = n + tid; r < k; r += kThreads) write(r, kNothing, -1);
+    for (int r = n + tid; r < k; r += kThreads) write(r, 0, -1);
     return;
   }
   // more ties than there is room for: one after another
   unsigned long long last_s = ~0ull;
   long long last_i = -1;
   for (int r = 0; r < k; ++r) {
-    unsigned long long s = kNothing;
+    unsigned long long s = 0;
     long long at = -1;
     for (int e = tid; e < lists * k; e += kThreads) {
       const unsigned long long q = key_of(e / k, e % k);
-      if (q == kNothing || q < s || q > last_s) continue;
+      if (q == 0 || q < s || q > last_s) continue;
       const long long i = place_of(e / k, e % k);
       if (ahead(last_s, last_i, q, i) && (at < 0 || ahead(q, i, s, at))) s = q, at = i;
     }
@@ -461,14 +622,14 @@ beam_join_kernel(const float* __restrict__ scores, const unsigned char* __restri
       best_i[warp] = at;
     }
     __syncthreads();
-    s = kNothing;
+    s = 0;
     at = -1;
     for (int w = 0; w < kWarps; ++w)
       if (best_i[w] >= 0 && (at < 0 || ahead(best_s[w], best_i[w], s, at))) s = best_s[w], at = best_i[w];
     __syncthreads();
     if (tid == 0) write(r, s, at);
     if (at < 0) {
-      for (int q = r + 1 + tid; q < k; q += kThreads) write(q, kNothing, -1);
+      for (int q = r + 1 + tid; q < k; q += kThreads) write(q, 0, -1);
       break;
     }
     last_s = s;
@@ -585,22 +746,24 @@ namespace {
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 struct BeamPlan {
-  int parts, chunks;
+  int parts, chunks, share, blocks;
   size_t value, token, bytes;
 };
 
-// Parts of a row.  Enough blocks for some eight on every SM, where there are so many chunks;
-// and no more lists a request than the join ranks.
-BeamPlan beam_plan(const mla_beam_params& p) {
-  const int per_chunk = kThreads * kVectors * (p.logits_dtype == MLA_LOGITS_FP32 ? 4 : 8);
+// An even share of all rows' chunks for each block; and no more lists a request than the join ranks.
+// `whole`: every row starts on a 16-byte boundary (else it may have a unit more).
+BeamPlan beam_plan(const mla_beam_params& p, bool whole) {
+  const int per = p.logits_dtype == MLA_LOGITS_FP32 ? 4 : 8, per_chunk = kThreads * kVectors * per;
   const long long rows = (long long)p.batch * p.beams;
-  // (a row that starts off a 16-byte boundary has a unit more)
-  const int chunks = (int)((p.vocab + 8LL + per_chunk - 1) / per_chunk);
-  const long long want = std::max(1LL, (1216 + rows - 1) / std::max(rows, 1LL));
+  const long long values = p.vocab + (whole ? 0LL : per - 1LL);
   BeamPlan b;
-  b.parts = (int)std::min<long long>(std::min<long long>(chunks, want), kMaxLists / p.beams);
-  b.chunks = (chunks + b.parts - 1) / b.parts;
-  b.parts = (chunks + b.chunks - 1) / b.chunks;
+  b.chunks = (int)((values + per_chunk - 1) / per_chunk);
+  // (a row of C chunks meets ceil((C - 1) / share) + 1 blocks at most)
+  const long long most = kMaxLists / p.beams - 1;
+  const long long share = std::max((rows * b.chunks + kBlocks - 1) / kBlocks, (b.chunks - 1 + most - 1) / most);
+  b.share = (int)std::max(1LL, share);
+  b.parts = b.share == 1 ? b.chunks : (b.chunks - 1 + b.share - 1) / b.share + 1;
+  b.blocks = (int)((rows * b.chunks + b.share - 1) / b.share);
   const size_t lists = (size_t)rows * b.parts;
   b.value = align_up(sizeof(Part) * lists, 256);
   b.token = b.value + align_up(sizeof(float) * lists * p.k, 256);
@@ -637,7 +800,7 @@ extern "C" {
 
 size_t mla_beam_workspace_size(const mla_beam_params* params) {
   if (mla::beam_check(params) != MLA_OK || params->batch == 0) return 0;
-  return mla::beam_plan(*params).bytes;
+  return std::max(mla::beam_plan(*params, true).bytes, mla::beam_plan(*params, false).bytes);
 }
 
 int mla_beam_select(const mla_beam_params* params, const void* logits, int64_t batch_stride, int64_t beam_stride,
@@ -655,20 +818,22 @@ int mla_beam_select(const mla_beam_params* params, const void* logits, int64_t b
   if (!aligned(logits, size) || !aligned(scores, 4) || !aligned(scores_out, 4) || !aligned(tokens_out, 4) ||
       !aligned(parents_out, 4) || !aligned(workspace, 256))
     return MLA_ERR_ALIGNMENT;
-  const BeamPlan plan = beam_plan(p);
-  if (workspace_bytes < plan.bytes) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  if (workspace_bytes < mla_beam_workspace_size(params)) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  const bool whole = aligned(logits, 16) && (p.batch == 1 || batch_stride * size % 16 == 0) &&
+                     (p.beams == 1 || beam_stride * size % 16 == 0);
+  const BeamPlan plan = beam_plan(p, whole);
   char* ws = static_cast<char*>(workspace);
   Parts parts{reinterpret_cast<Part*>(ws), reinterpret_cast<float*>(ws + plan.value),
-              reinterpret_cast<int*>(ws + plan.token), plan.parts, plan.chunks};
+              reinterpret_cast<int*>(ws + plan.token), p.batch * p.beams, plan.parts, plan.chunks, plan.share};
   const Logits in{logits, batch_stride, beam_stride, p.beams, p.vocab};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const dim3 grid((unsigned)(p.batch * p.beams), (unsigned)plan.parts);
-  if (p.logits_dtype == MLA_LOGITS_FP32)
-    beam_parts_kernel<float><<<grid, kThreads, 0, s>>>(in, scores, finished, p.k, parts);
-  else if (p.logits_dtype == MLA_LOGITS_BF16)
-    beam_parts_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(in, scores, finished, p.k, parts);
-  else
-    beam_parts_kernel<__half><<<grid, kThreads, 0, s>>>(in, scores, finished, p.k, parts);
+  const dim3 grid((unsigned)plan.blocks);
+  auto kernel = p.logits_dtype == MLA_LOGITS_FP32   ? beam_parts_kernel<float>
+                : p.logits_dtype == MLA_LOGITS_BF16 ? beam_parts_kernel<__nv_bfloat16>
+                                                    : beam_parts_kernel<__half>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  kernel<<<grid, kThreads, kSmem, s>>>(in, scores, finished, p.k, parts);
   if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
   int beams = p.beams, k = p.k, vocab = p.vocab, end = p.end_token;
   void* args[] = {&scores, &finished, &beams, &k, &vocab, &end, &parts, &scores_out, &tokens_out, &parents_out};
