@@ -32,6 +32,9 @@ cudaError_t launch_decode_sm103(const Problem& p, const Layout& lay, void* ws,
                                 cudaStream_t stream);
 cudaError_t decode_pair_setup(int kv_dtype, int sm_count, int* n_pairs);
 cudaError_t launch_decode_pair(const Problem& p, const Layout& lay, void* ws, cudaStream_t stream);
+cudaError_t decode_prefix_setup(int kv_dtype, int sm_count, int* n_pairs);
+cudaError_t launch_decode_prefix(const Problem& p, const Layout& lay, const PrefixLayout& pl, void* ws,
+                                 cudaStream_t stream);
 cudaError_t prefix_setup();
 cudaError_t launch_partition_prefix(const Problem& p, const PrefixArgs& pa, const Layout& lay, const PrefixLayout& pl,
                                     void* ws, cudaStream_t stream);
@@ -185,7 +188,8 @@ int mla_decode_plan(const mla_decode_params* params, mla_plan_t** plan, size_t* 
   int sms = 0, n_pairs = 0;
   cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, p.device);
   if (e == cudaSuccess)
-    e = uses_pair_mma(p)
+    e = p.prefix_groups > 0 ? mla::decode_prefix_setup(p.kv_dtype, sms, &n_pairs)
+        : uses_pair_mma(p)
             ? mla::decode_pair_setup(p.kv_dtype, sms, &n_pairs)
             : mla::decode_sm103_setup(p.kv_dtype, p.sparse_top_k > 0, uses_fp8_mma(p), sms, &n_pairs);
   if (e == cudaSuccess) e = mla::partition_setup();
@@ -387,7 +391,8 @@ int run_impl(const mla_plan_t* plan, const void* query, const void* kv_cache,
       cudaEventRecordWithFlags(static_cast<cudaEvent_t>(event_before_decode), s, ev_flags) !=
           cudaSuccess)
     return MLA_ERR_CUDA;
-  if ((uses_pair_mma(prm) ? mla::launch_decode_pair(p, plan->lay, workspace, s)
+  if ((prefix               ? mla::launch_decode_prefix(p, plan->lay, plan->pre, workspace, s)
+       : uses_pair_mma(prm) ? mla::launch_decode_pair(p, plan->lay, workspace, s)
                           : mla::launch_decode_sm103(p, plan->lay, workspace, s)) != cudaSuccess)
     return MLA_ERR_CUDA;
   if (event_after_decode &&

@@ -58,6 +58,7 @@
 
 #include "mla_common.cuh"
 #include "mla_fp4.cuh"
+#include "mla_prefix.cuh"
 #include "sm100_ptx.cuh"
 
 namespace mla {
@@ -390,11 +391,12 @@ __device__ __noinline__ bool first_query(Ctx c, unsigned char* sm, uint32_t tmem
 
 }  // namespace
 
-template <int kCache>
+// kShared: plans with shared prefixes, whose items walk lists of segments (mla_prefix.cuh).
+template <int kCache, bool kShared>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
                    const __grid_constant__ CUtensorMap tm_k,   // (bf16 cache only)
-                   const __grid_constant__ CUtensorMap tm_v) {
+                   const __grid_constant__ CUtensorMap tm_v, const PrefixSegment* __restrict__ segments) {
   using C = Cfg<kCache>;
   // The swizzled tiles need 1024-byte alignment, and there is no room to round
   // up: the block has no other shared memory, so its dynamic part starts at
@@ -479,7 +481,27 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
       const int n_pages = (it.kv_end - it.kv_begin + ps - 1) >> ps_shift;
       // a page's id, -1 for one that is not read; a bad id's rows are zeros (TMA:
       // the rows past the cache's end, which the copy fills with zeros)
-      auto page_at = [&](int i) -> int {
+      // (kShared: of the segment that the slot's tile lies in; and the rows in use from its first on)
+      PrefixSegment seg = {};
+      if constexpr (kShared)
+        if (lane < it.seq_len) seg = segments[(size_t)it.comb * kPrefixSegments + lane];
+      auto page_at = [&](int i, int& left) -> int {
+        if constexpr (kShared) {
+          const int tile = it.kv_begin / kTile + (npg == 2 ? i >> 1 : i);
+          int t0 = 0, b = 0, row = 0, end = 0;
+          for (int z = 0; z < it.seq_len; ++z) {
+            const int z0 = __shfl_sync(0xffffffffu, seg.tile0, z), zb = __shfl_sync(0xffffffffu, seg.b, z);
+            const int zr = __shfl_sync(0xffffffffu, seg.row0, z), ze = __shfl_sync(0xffffffffu, seg.end, z);
+            if (tile >= z0) t0 = z0, b = zb, row = zr, end = ze;
+          }
+          row += (tile - t0) * kTile + (npg == 2 ? (i & 1) * kHalf : 0);
+          left = end - row;
+          if (i >= nt * npg || left <= 0) return -1;
+          const int id = p.block_tables[(size_t)b * p.max_pages + (row >> ps_shift)];
+          if (id >= 0 && (long long)id < p.num_pages) return id;
+          if (bulk) atomicOr(c.status, kStatusPage);
+          return C::kTma ? (int)p.num_pages : -1;
+        }
         const int r = walk.row(it.kv_begin + i * ps);
         if (i >= n_pages || !walk.seen(r, r + ps - 1)) return -1;
         const int id = bt[r >> ps_shift];
@@ -487,19 +509,26 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
         if (bulk) atomicOr(c.status, kStatusPage);
         return C::kTma ? (int)p.num_pages : -1;
       };
-      int cur = page_at(lane), nxt = page_at(32 + lane);
+      int cur_left = 0, nxt_left = 0;
+      int cur = page_at(lane, cur_left), nxt = page_at(32 + lane, nxt_left);
       for (int t = 0; t < nt; ++t, ++g) {
         const int slot0 = t * npg;  // never straddles a batch: npg divides 32
         if (slot0 > 0 && (slot0 & 31) == 0) {
           cur = nxt;
-          nxt = page_at(slot0 + 32 + lane);
+          cur_left = nxt_left;
+          nxt = page_at(slot0 + 32 + lane, nxt_left);
         }
         const int id0 = __shfl_sync(0xffffffffu, cur, slot0 & 31);
         const int id1 = __shfl_sync(0xffffffffu, cur, (slot0 + npg - 1) & 31);
         // a half is read if some query row sees a row of it
         const int j0 = it.kv_begin + t * kTile, r0 = walk.row(j0);
-        const bool on0 = id0 >= 0 && walk.seen(r0, r0 + kHalf - 1);
-        const bool on1 = id1 >= 0 && j0 + kHalf < it.kv_end && walk.seen(r0 + kHalf, r0 + kTile - 1);
+        const int left = kShared ? __shfl_sync(0xffffffffu, cur_left, slot0 & 31) : 0;
+        const bool on0 = id0 >= 0 && (kShared || walk.seen(r0, r0 + kHalf - 1));
+        const bool on1 = id1 >= 0 && (kShared ? left > kHalf
+                                              : j0 + kHalf < it.kv_end && walk.seen(r0 + kHalf, r0 + kTile - 1));
+        auto in_use = [&](int i) {  // row i of the tile
+          return kShared ? i < left : j0 + i < it.kv_end && walk.seen(r0 + i, r0 + i);
+        };
         const uint32_t s = g & 1, use = g >> 1;
         unsigned char* stg = sm + C::OFF_STG + s * C::kStage;
         uint64_t* full = &c.bars[STG_FULL0 + s];
@@ -519,11 +548,8 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
           } else {
             // V: this CTA's dims of all rows, once PV of two tiles ago has, and the
             // first query, which is staged there
-            const uint32_t mask0 = __ballot_sync(0xffffffffu, on0 && j0 + lane < it.kv_end &&
-                                                                  walk.seen(r0 + lane, r0 + lane));
-            const uint32_t mask1 =
-                __ballot_sync(0xffffffffu, on1 && j0 + kHalf + lane < it.kv_end &&
-                                               walk.seen(r0 + kHalf + lane, r0 + kHalf + lane));
+            const uint32_t mask0 = __ballot_sync(0xffffffffu, on0 && in_use(lane));
+            const uint32_t mask1 = __ballot_sync(0xffffffffu, on1 && in_use(kHalf + lane));
             if (g == 0 && !wait_bar(c, Q_READ, 0)) goto fail_copy;
             if (!wait_bar(c, PV_DONE0 + s, (use & 1) ^ 1)) goto fail_copy;
             if (lane == 0) {
@@ -550,11 +576,8 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
         } else if (bulk) {
           // rows past the item's end, that no query row sees, or on a page that is
           // not read, enter as zeros
-          const uint32_t mask0 = __ballot_sync(0xffffffffu, on0 && j0 + lane < it.kv_end &&
-                                                                walk.seen(r0 + lane, r0 + lane));
-          const uint32_t mask1 =
-              __ballot_sync(0xffffffffu, on1 && j0 + kHalf + lane < it.kv_end &&
-                                             walk.seen(r0 + kHalf + lane, r0 + kHalf + lane));
+          const uint32_t mask0 = __ballot_sync(0xffffffffu, on0 && in_use(lane));
+          const uint32_t mask1 = __ballot_sync(0xffffffffu, on1 && in_use(kHalf + lane));
           if (!wait_bar(c, STG_EMPTY0 + s, (use & 1) ^ 1)) goto fail_copy;
           if (lane == 0) {
             const int row1 = npg == 1 ? kHalf : 0;  // first row of half 1 in its page
@@ -762,6 +785,20 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
       // tiles inside [clean_lo, clean_hi) need no mask for any row of the item
       const int clean_hi = last_of(0) + 1;
       const int clean_lo = p.window > 0 ? last_of(n_rows - 1) - p.window + 1 : INT_MIN;
+      // kShared: a segment a lane (first tile, row of tile 0, end, query rows, mask); of the
+      // present one the row of tile 0, the rows that this thread's query row sees and those
+      // that all do, and the tile where the next one starts
+      int z_tile = INT_MAX, z_off = 0, z_end = 0, z_rows = 0, z_mask = 0;
+      int sg_now = -1, sg_next = 0, sg_off = 0, sg_mine = 0, sg_all = 0;
+      if constexpr (kShared)
+        if (lane < it.seq_len) {
+          const PrefixSegment z = segments[(size_t)it.comb * kPrefixSegments + lane];
+          z_tile = z.tile0;
+          z_off = z.row0 - z.tile0 * kTile;
+          z_end = z.end;
+          z_rows = z.q_lo | z.q_hi << 16;
+          z_mask = z.mask;
+        }
       if (!wait_bar(c, QS_FULL0 + (n_item & 3), (n_item >> 2) & 1)) goto fail_soft;
       const float scale = bmm1 * qscale[(n_item & 3) * kCtaRows + row];
       // this group's share of the row sum, relative to its latest reference m
@@ -780,12 +817,33 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
         // (relaxed: what was read is in registers)
         if (lane == 0) mbar_arrive_cluster_relaxed(c.leader_bars + 8u * (S_EMPTY0 + grp));
         const int v0 = it.kv_begin + t * kTile;        // virtual row of the tile
-        const int r0 = walk.row(v0);                    // its row
+        int r0 = walk.row(v0);                          // its row
         const int valid = it.kv_end - v0;               // rows of the tile inside the item
-        const bool clean = valid >= kTile && r0 + kTile <= clean_hi &&
-                           (r0 >= clean_lo || r0 + kTile <= p.sinks);
+        bool clean = valid >= kTile && r0 + kTile <= clean_hi &&
+                     (r0 >= clean_lo || r0 + kTile <= p.sinks);
+        if constexpr (kShared) {
+          while (v0 / kTile >= sg_next) {
+            ++sg_now;
+            sg_next = __shfl_sync(0xffffffffu, z_tile, sg_now + 1);  // (past the last: never)
+            sg_off = __shfl_sync(0xffffffffu, z_off, sg_now);
+            const int end = __shfl_sync(0xffffffffu, z_end, sg_now), rows = __shfl_sync(0xffffffffu, z_rows, sg_now);
+            const int mask = __shfl_sync(0xffffffffu, z_mask, sg_now), lo = rows & 0xFFFF, hi = rows >> 16;
+            sg_mine = q >= lo && q < hi ? min(end, mask + ((row0 + q) >> h_shift) + 1) : 0;
+            sg_all = lo == 0 && hi >= n_rows ? min(end, mask + (row0 >> h_shift) + 1) : 0;
+          }
+          r0 = sg_off + v0;
+          clean = r0 + kTile <= sg_all;
+        }
         uint32_t hidden = 0;  // columns that the mask takes out
-        if (!clean) {
+        if constexpr (kShared) {
+          if (!clean) {
+            const int at = r0 + 32 * hh;
+            hidden = ~first_bits(sg_mine - at);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if ((hidden >> j) & 1u) v[j] = 0xFF800000u;  // -inf
+          }
+        } else if (!clean) {
           // of this thread's columns, rows r0 + 32 hh + [0, 32): those up to `last` and
           // inside the item, from the window's first row on or among the sinks
           const int at = r0 + 32 * hh;
@@ -931,7 +989,7 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
         uint32_t x[16];
         tmem_ld_32x32b_x16(tm + TM_O + 128 * grp + 16 * k, x);
         tmem_wait_ld();
-        if (!row_ok) continue;
+        if (!row_ok || (kShared && it.slot >= 0 && l_row == 0.f)) continue;  // (nothing seen: the LSE says so)
         const int chunk = 16 * hh + 8 * grp + k;  // of 16 dims
         if (C::kTma && it.slot >= 0) {  // fp32 (part_format)
 #pragma unroll
@@ -966,11 +1024,11 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
       }
       tc_fence_before();
       // both groups have read O before the next item's first PV overwrites it
-      if (it.slot >= 0) __threadfence();  // ... and the partial is visible GPU-wide
+      if (!kShared && it.slot >= 0) __threadfence();  // ... and the partial is visible GPU-wide
       __syncwarp();
       if (lane == 0) mbar_arrive(&c.bars[EPI]);
       if (!wait_bar(c, EPI, n_item & 1)) goto fail_soft;
-      if (it.slot >= 0 && warp == kFirstSoft && lane == 0 && it.comb >= 0) {
+      if (!kShared && it.slot >= 0 && warp == kFirstSoft && lane == 0 && it.comb >= 0) {
         __threadfence();
         atomicAdd(comb_done + it.comb, 1);
       }
@@ -1261,9 +1319,9 @@ cudaLaunchConfig_t pair_launch(int grid, size_t smem, cudaStream_t stream, cudaL
   return cfg;
 }
 
-template <int kCache>
+template <int kCache, bool kShared>
 cudaError_t setup_one(int sm_count, int* n_pairs) {
-  auto kernel = decode_pair_kernel<kCache>;
+  auto kernel = decode_pair_kernel<kCache, kShared>;
   constexpr size_t kSmem = Cfg<kCache>::kSmemBytes;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
@@ -1302,29 +1360,43 @@ bool encode_rows(CUtensorMap* map, const Problem& p, int chunks) {
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kCache>
-cudaError_t launch_one(const Problem& p, const Layout& lay, void* ws, cudaStream_t stream) {
+template <int kCache, bool kShared>
+cudaError_t launch_one(const Problem& p, const Layout& lay, void* ws, const PrefixSegment* segments, cudaStream_t stream) {
   CUtensorMap tm_k = {}, tm_v = {};
   if (Cfg<kCache>::kTma && !(encode_rows(&tm_k, p, kChunks) && encode_rows(&tm_v, p, 4))) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   const cudaLaunchConfig_t cfg = pair_launch(lay.n_ctas, Cfg<kCache>::kSmemBytes, stream, &attr);
-  return cudaLaunchKernelEx(&cfg, decode_pair_kernel<kCache>, p, lay, static_cast<char*>(ws), tm_k, tm_v);
+  return cudaLaunchKernelEx(&cfg, decode_pair_kernel<kCache, kShared>, p, lay, static_cast<char*>(ws), tm_k, tm_v, segments);
 }
 
 }  // namespace
 
 cudaError_t decode_pair_setup(int kv_dtype, int sm_count, int* n_pairs) {
-  return kv_dtype == 2   ? setup_one<kFp4>(sm_count, n_pairs)
-         : kv_dtype == 1 ? setup_one<kE4m3>(sm_count, n_pairs)
-                         : setup_one<kBf16>(sm_count, n_pairs);
+  return kv_dtype == 2   ? setup_one<kFp4, false>(sm_count, n_pairs)
+         : kv_dtype == 1 ? setup_one<kE4m3, false>(sm_count, n_pairs)
+                         : setup_one<kBf16, false>(sm_count, n_pairs);
 }
 
 cudaError_t launch_decode_pair(const Problem& p, const Layout& lay, void* ws, cudaStream_t stream) {
-  return p.kv_dtype == 2   ? launch_one<kFp4>(p, lay, ws, stream)
-         : p.kv_dtype == 1 ? launch_one<kE4m3>(p, lay, ws, stream)
-                           : launch_one<kBf16>(p, lay, ws, stream);
+  return p.kv_dtype == 2   ? launch_one<kFp4, false>(p, lay, ws, nullptr, stream)
+         : p.kv_dtype == 1 ? launch_one<kE4m3, false>(p, lay, ws, nullptr, stream)
+                           : launch_one<kBf16, false>(p, lay, ws, nullptr, stream);
+}
+
+cudaError_t decode_prefix_setup(int kv_dtype, int sm_count, int* n_pairs) {
+  return kv_dtype == 2   ? setup_one<kFp4, true>(sm_count, n_pairs)
+         : kv_dtype == 1 ? setup_one<kE4m3, true>(sm_count, n_pairs)
+                         : setup_one<kBf16, true>(sm_count, n_pairs);
+}
+
+cudaError_t launch_decode_prefix(const Problem& p, const Layout& lay, const PrefixLayout& pl, void* ws,
+                                 cudaStream_t stream) {
+  const PrefixSegment* segments = reinterpret_cast<const PrefixSegment*>(static_cast<char*>(ws) + pl.segments);
+  return p.kv_dtype == 2   ? launch_one<kFp4, true>(p, lay, ws, segments, stream)
+         : p.kv_dtype == 1 ? launch_one<kE4m3, true>(p, lay, ws, segments, stream)
+                           : launch_one<kBf16, true>(p, lay, ws, segments, stream);
 }
 
 }  // namespace mla

@@ -18,6 +18,7 @@ inline int __reduce_max_sync(unsigned, int v) { return host_reduce(v, [](int a, 
 inline unsigned __reduce_add_sync(unsigned, unsigned v) { return host_reduce(v, [](unsigned a, unsigned b) { return a + b; }); }
 inline unsigned __reduce_or_sync(unsigned, unsigned v) { return host_reduce(v, [](unsigned a, unsigned b) { return a | b; }); }
 inline int __popc(unsigned v) { return __builtin_popcount(v); }
+inline int atomicAdd(int* p, int v) { return std::atomic_ref<int>(*p).fetch_add(v); }
 inline int atomicMax(int* p, int v) {
   std::atomic_ref<int> a(*p);
   int old = a.load();
@@ -47,12 +48,13 @@ int main(int argc, char** argv) {
   mla::PrefixLayout pl{};
   if (!mla::make_prefix_layout(B, H, max_q, packed, total_q, kv_dtype, G, n_workers, sizeof(int) * mla::kHdrWords, &lay, &pl))
     return 3;
-  const size_t starts[] = {lay.items, lay.worker_ranges, pl.entries, pl.rg_first, pl.rg_count, lay.part_o, lay.part_lse, lay.total};
-  for (size_t s : starts)
-    if (s % 256) return 5;
+  const size_t starts[] = {lay.items, lay.worker_ranges, pl.entries, pl.segments, lay.part_o, lay.part_lse, lay.total};
+  for (size_t i = 0; i < sizeof(starts) / sizeof(starts[0]); ++i)
+    if (starts[i] % 256 || (i > 0 && starts[i] < starts[i - 1])) return 5;
+  if (pl.segments + sizeof(mla::PrefixSegment) * mla::kPrefixSegments * (size_t)lay.max_groups > lay.part_o) return 5;
   if (global_scratch) {  // as a batch that shared memory does not hold: the scratch past the rest
     pl.scratch_in_smem = 0;
-    pl.owners = lay.part_o;
+    pl.scratch = lay.part_o;
   }
   const size_t used = lay.part_o + (global_scratch ? pl.scratch_bytes : 0);  // (no partial is touched here)
   std::vector<unsigned char> ws(used, 0xAB);
@@ -92,8 +94,8 @@ int main(int argc, char** argv) {
   const int* hdr = reinterpret_cast<const int*>(ws.data());
   FILE* o = std::fopen(argv[2], "w");
   if (!o) return 2;
-  std::fprintf(o, "%d %d %d %d %d\n", hdr[mla::kHdrStatus], hdr[mla::kHdrNumItems], hdr[mla::kHdrNumCombine],
-               lay.max_items, pl.max_entries);
+  std::fprintf(o, "%d %d %d %d %d %d\n", hdr[mla::kHdrStatus], hdr[mla::kHdrNumItems], hdr[mla::kHdrNumCombine],
+               lay.max_items, lay.max_groups, lay.max_partials);
   const int* items = reinterpret_cast<const int*>(ws.data() + lay.items);
   for (int i = 0; i < hdr[mla::kHdrNumItems] * 10; ++i) std::fprintf(o, "%d ", items[i]);
   std::fprintf(o, "\n");
@@ -102,8 +104,11 @@ int main(int argc, char** argv) {
   std::fprintf(o, "\n");
   const mla::PrefixEntry* e = reinterpret_cast<const mla::PrefixEntry*>(ws.data() + pl.entries);
   for (int i = 0; i < hdr[mla::kHdrNumCombine]; ++i)
-    std::fprintf(o, "%lld %d %d %d %d %d %d %d %d ", e[i].row0, e[i].rows, e[i].own, e[i].n_own, e[i].off, e[i].pre[0],
-                 e[i].n_pre[0], e[i].pre[1], e[i].n_pre[1]);
+    std::fprintf(o, "%lld %d %d %d ", e[i].row0, e[i].rows, e[i].slot, e[i].count);
+  std::fprintf(o, "\n");
+  const mla::PrefixSegment* sg = reinterpret_cast<const mla::PrefixSegment*>(ws.data() + pl.segments);
+  for (int i = 0; i < hdr[mla::kHdrNumCombine] * mla::kPrefixSegments; ++i)
+    std::fprintf(o, "%d %d %d %d %d %d %d ", sg[i].tile0, sg[i].b, sg[i].row0, sg[i].end, sg[i].q_lo, sg[i].q_hi, sg[i].mask);
   std::fprintf(o, "\n");
   std::fclose(o);
   return 0;

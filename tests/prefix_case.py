@@ -74,5 +74,5 @@ class PrefixCase(Case):
         return self.workspace[at:at + 40 * n].view(torch.int32).view(n, 10).cpu()
 
     def shares(self):
-        """Whether some item takes the query rows of several requests."""
+        """Whether some row group takes the query rows of several requests."""
         return bool((self.items()[:, 5] > max(self.qs)).any())

@@ -54,80 +54,75 @@ def _run(runner, ls, qo, max_q, max_len, H, packed, causal, kv, lens, indptr, n_
     r = subprocess.run([str(exe), str(out / "in.txt"), str(out / "out.txt")], capture_output=True, text=True,
                        env=dict(os.environ, ASAN_OPTIONS="detect_leaks=0:abort_on_error=1"), timeout=300)
     assert r.returncode == 0, (r.returncode, r.stderr[-3000:])
-    return [[int(x) for x in line.split()] for line in open(out / "out.txt").read().split("\n")[:4]]
+    return [[int(x) for x in line.split()] for line in open(out / "out.txt").read().split("\n")[:5]]
 
 
 def _check(got, ls, qs, H, causal, lens, indptr, status=0):
     """-> the prefix groups that are shared."""
-    head, items, ranges, entries = got
+    head, items, ranges, entries, segs = got
     assert head[0] == status
-    n_items, n_entries, max_items, max_entries = head[1:]
-    assert n_items <= max_items and n_entries <= max_entries
+    n_items, n_rg, max_items, max_groups, max_partials = head[1:]
+    assert n_items <= max_items and n_rg <= max_groups
     assert ranges[0] == 0 and ranges[-1] == n_items and all(a <= b for a, b in zip(ranges, ranges[1:]))
     items = [items[10 * i:10 * i + 10] for i in range(n_items)]
-    entries = [entries[9 * i:9 * i + 9] for i in range(n_entries)]
+    entries = [entries[4 * i:4 * i + 4] for i in range(n_rg)]
+    segs = [[segs[7 * (9 * r + i):7 * (9 * r + i) + 7] for i in range(9)] for r in range(n_rg)]
     q0 = np.concatenate([[0], np.cumsum(qs)])
     if indptr is None:
         indptr = [g * (len(ls) // len(lens)) for g in range(len(lens) + 1)]
     group_of = {b: g for g in range(len(lens)) for b in range(indptr[g], indptr[g + 1])}
-    # by (first token, number of tokens, row group): a request's, or a prefix group's
-    by = {}
-    for i, it in enumerate(items):
-        assert it[4] in (-1, i) and it[8] == -1 and it[2] % TILE == 0 and it[2] < it[3]
-        by.setdefault((it[7], it[5], it[1]), []).append((i, it))
-    spans, shared = {}, {}
-    for g in range(len(lens)):
-        lo, hi = indptr[g], indptr[g + 1]
-        if hi - lo < 2:
-            continue
-        tokens, most = int(q0[hi] - q0[lo]), -(-int(q0[hi] - q0[lo]) * H // ROWS)
-        if (int(q0[lo]), tokens, 0) not in by or tokens == qs[lo]:
-            continue
-        first = next(b for b in range(lo, hi) if ls[b] > 0)
-        for k in range(most):
-            parts = by.pop((int(q0[lo]), tokens, k))
-            P = parts[-1][1][3]
-            assert parts[0][1][2] == 0 and all(a[1][3] == c[1][2] for a, c in zip(parts, parts[1:]))
-            assert [i for i, _ in parts] == list(range(parts[0][0], parts[0][0] + len(parts)))
-            assert 0 < P <= lens[g] and P % TILE == 0 and shared.setdefault(g, P) == P
-            for i, it in parts:
-                assert it[0] == first and it[4] == i and it[6] == P
-                assert it[9] >= P - 1  # the causal bound of the first query row hides nothing
-            spans[g, k] = [i for i, _ in parts]
-        seen = min(ls[b] - qs[b] + 1 if causal else ls[b] for b in range(lo, hi) if ls[b] > 0)
-        assert shared[g] == min(lens[g], seen) // TILE * TILE
-    at = 0
-    for b, (L, q) in enumerate(zip(ls, qs)):
+    request_of = np.repeat(np.arange(len(ls)), qs)
+    by, slots, shared, seen = {}, [], {}, {}
+    for it in items:
+        by.setdefault(it[8], []).append(it)
+    assert sorted(by) == list(range(n_rg))
+    assert [it[8] for it in items] == sorted(it[8] for it in items)  # in order: a row group's follow on one another
+    for r, parts in by.items():
+        _, k, _, _, _, tokens, n_seg, start, _, _ = parts[0]
+        assert all([it[1], it[5], it[6], it[7]] == [k, tokens, n_seg, start] for it in parts)
+        rows = min(ROWS, tokens * H - k * ROWS)
+        assert rows > 0 and 1 <= n_seg <= 9
+        # the parts follow on one another, and the segments fill them
+        assert parts[0][2] == 0 and all(a[3] == c[2] for a, c in zip(parts, parts[1:]))
+        assert all(it[2] % TILE == 0 and it[2] < it[3] for it in parts)
+        at = 0
+        for tile0, b, row0, end, lo, hi, mask in segs[r][:n_seg]:
+            assert tile0 == at and row0 % TILE == 0 and row0 < end <= ls[b]
+            at += -(-(end - row0) // TILE)
+            assert 0 <= lo < hi <= ROWS
+            for q in range(lo, min(hi, rows), H):
+                assert q % H == 0
+                i = (k * ROWS + q) // H  # token of the owner
+                token = start + i
+                own = request_of[token]
+                last = mask + i
+                if own != b or mask == 1 << 30 and causal:  # shared rows: whole tiles that all see, from the group's first table
+                    g = group_of[own]
+                    assert row0 == 0 and end % TILE == 0 and end <= lens[g] and group_of[b] == g
+                    assert b == next(x for x in range(indptr[g], indptr[g + 1]) if ls[x] > 0)
+                    assert shared.setdefault(g, end) == end
+                    assert end <= (ls[own] - qs[own] + 1 if causal else ls[own]) or ls[own] <= 0
+                    last = end - 1
+                elif causal:
+                    assert last == ls[own] - qs[own] + token - q0[own]
+                seen.setdefault(token, []).append((row0, min(end, last + 1)))
+        assert at * TILE == parts[-1][3]
+        row0, n, slot, count = entries[r]
+        assert row0 == start * H + k * ROWS and count == len(parts)
+        assert n == (rows if count > 1 else 0)
+        if count > 1:
+            assert [it[4] for it in parts] == list(range(slot, slot + count))
+            slots += [it[4] for it in parts]
+        else:
+            assert parts[0][4] == -1
+    assert len(set(slots)) == len(slots) and all(0 <= x < max_partials for x in slots)
+    for token, b in enumerate(request_of):  # every row that the token sees, once
+        L = ls[b]
         if L <= 0:
             continue
-        P = shared.get(group_of.get(b), 0)
-        for k in range(-(-q * H // ROWS)):
-            parts = by.pop((int(q0[b]), q, k), [])
-            assert bool(parts) == (L > P)
-            if parts:
-                assert parts[0][1][2] == P and parts[-1][1][3] == L
-                assert all(a[1][3] == c[1][2] for a, c in zip(parts, parts[1:]))
-                assert [i for i, _ in parts] == list(range(parts[0][0], parts[0][0] + len(parts)))
-            for i, it in parts:
-                assert it[0] == b and it[6] == L and it[9] == L - q
-                assert (it[4] >= 0) == (P > 0 or len(parts) > 1)
-            row0, rows, own, n_own, off, p0, n0, p1, n1 = entries[at]
-            at += 1
-            assert row0 == q0[b] * H + k * ROWS
-            if not P and len(parts) == 1:
-                assert rows == 0
-                continue
-            assert rows == min(ROWS, q * H - k * ROWS)
-            assert list(range(own, own + n_own)) == [i for i, _ in parts]
-            if not P:
-                assert n0 == n1 == 0
-                continue
-            g = group_of[b]
-            row = int(q0[b] - q0[indptr[g]]) * H + k * ROWS
-            assert off == row % ROWS and list(range(p0, p0 + n0)) == spans[g, row // ROWS]
-            assert list(range(p1, p1 + n1)) == spans.get((g, row // ROWS + 1), [])
-            assert off + rows <= ROWS or n1 > 0
-    assert at == n_entries and not by
+        end = L - qs[b] + token - q0[b] + 1 if causal else L
+        spans = sorted(x for x in seen[token] if x[0] < x[1])
+        assert spans[0][0] == 0 and spans[-1][1] == end and all(a[1] == c[0] for a, c in zip(spans, spans[1:]))
     return set(shared)
 
 
@@ -151,11 +146,11 @@ def test_a_system_prompt_is_shared(runner):
     assert _case(runner, [96], [6000], lambda i: 64 + 20 * i, [1], 16, False, True, 0, 76, global_scratch=True) == {0}
 
 
-def test_beams_are_shared_and_few_are_not(runner):
+def test_beams_are_shared_and_full_row_groups_are_not(runner):
     assert _case(runner, [8] * 16, [1000 + 400 * g for g in range(16)], lambda i: 1 + 3 * (i // 8), [1], 32, False, True, 1,
                  76, uniform=True) == set(range(16))
-    # a call that the card finishes in one item a worker gains nothing
-    assert _case(runner, [4], [500], lambda i: 1 + i, [1], 16, False, True, 0, 76, uniform=True) == set()
+    # a row group a request already, and a worker for each
+    assert _case(runner, [8] * 4, [640] * 4, lambda i: 10, [1], 128, False, True, 0, 76, uniform=True) == set()
 
 
 def test_a_group_without_rows_of_its_own(runner):
