@@ -235,7 +235,7 @@ int mla_decode_plan(const mla_decode_params* params, mla_plan_t** plan, size_t* 
   int rc = MLA_OK;
   if (p.prefix_groups == 0)
     rc = make_layout(p, n_pairs, 2 * n_pairs, rows_per_group, &pl->lay);
-  else if (!mla::make_prefix_layout(p.batch, p.num_heads, p.max_seq_len_q, p.packed != 0, p.max_total_q, p.kv_dtype,
+  else if (!mla::make_prefix_layout(p.batch, p.num_heads, p.max_seq_len_q, p.packed != 0, p.max_total_q, p.max_seq_len, p.kv_dtype,
                                     p.prefix_groups, std::min(n_pairs, mla::kPrefixWorkers), kHeaderBytes, &pl->lay,
                                     &pl->pre))
     rc = MLA_ERR_UNSUPPORTED;

@@ -30,47 +30,49 @@ namespace {
 constexpr int kPartThreads = 1024;
 constexpr unsigned kAll = 0xffffffffu;
 
-// By request: tokens, first token, rows, prefix group (-1: on its own), first token in it.
-// By prefix group: first and last + 1 request, tokens, shared tiles.  By owner: first row
-// group.  By row group: start unit; cost.
+// By request: tokens, first token, rows, prefix group (-1: on its own), first token in its
+// owner, first row group of its owner, own tiles and own segments of the requests before it.  By
+// prefix group: first and last + 1 request, tokens (0: not shared), shared tiles.  By row
+// group: start unit, and the requests of its first and last token.
 struct PrefixScratch {
-  long long* start;
-  int *cost, *q, *qs, *len, *group, *tok, *lo, *hi, *tokens, *shared, *base;
+  int *q, *qs, *len, *group, *tok, *base, *tiles, *count;  // (tiles and count: of all before the end, too)
+  int *lo, *hi, *tokens, *shared;
+  int *start, *first, *last;
   __device__ PrefixScratch(char* at, int batch, int groups, int row_groups) {
-    start = reinterpret_cast<long long*>(at);
-    cost = reinterpret_cast<int*>(at + align_up(sizeof(long long) * (size_t)(row_groups + 1), 16));
-    q = cost + row_groups;
+    q = reinterpret_cast<int*>(at);
     qs = q + batch;
     len = qs + batch;
     group = len + batch;
     tok = group + batch;
-    lo = tok + batch;
+    base = tok + batch;
+    tiles = base + batch;
+    count = tiles + batch + 1;
+    lo = count + batch + 1;
     hi = lo + groups;
     tokens = hi + groups;
     shared = tokens + groups;
-    base = shared + groups;
+    start = shared + groups;
+    first = start + row_groups + 1;
+    last = first + row_groups;
   }
 };
 
 struct PrefixShared {
-  long long w_cost[32], carry, alone;
-  int w_count[32], count, status, most, alone_most, any;
-  long long bound[kPrefixWorkers + 1];
+  int w_scan[3][32], status, most, alone, alone_most, alone_count, any;
+  int bound[kPrefixWorkers + 1];
   unsigned cut[8], first[8];
 };
 
-template <typename T>
-__device__ __forceinline__ T scan_up(T v, int lane) {  // inclusive, over the warp
+__device__ __forceinline__ int scan_up(int v, int lane) {  // inclusive, over the warp
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const T y = __shfl_up_sync(kAll, v, o);
+    const int y = __shfl_up_sync(kAll, v, o);
     if (lane >= o) v += y;
   }
   return v;
 }
 // Last index in [0, n) whose value is at most x (values ascending, the first at most x).
-template <typename T>
-__device__ __forceinline__ int last_upto(const T* v, int n, T x) {
+__device__ __forceinline__ int last_upto(const int* v, int n, int x) {
   int lo = 0;
   while (n - lo > 1) {
     const int mid = (lo + n) >> 1;
@@ -85,9 +87,30 @@ __device__ __forceinline__ int bits_under(const unsigned* words, int p) {
 }
 __device__ __forceinline__ bool bit_at(const unsigned* words, int p) { return (words[p >> 5] >> (p & 31)) & 1u; }
 
+// Sums of up to three values over all threads before this one, and over all (two barriers).
+template <int kN>
+__device__ __forceinline__ void block_scan(PrefixShared& sh, int (&v)[kN], int (&before)[kN], int (&total)[kN]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n_warps = blockDim.x >> 5;
+  int in[kN];
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    in[i] = scan_up(v[i], lane);
+    if (lane == 31) sh.w_scan[i][warp] = in[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    const int w = scan_up(lane < n_warps ? sh.w_scan[i][lane] : 0, lane);
+    const int up = __shfl_sync(kAll, w, warp == 0 ? 0 : warp - 1);
+    before[i] = (warp == 0 ? 0 : up) + in[i] - v[i];
+    total[i] = __shfl_sync(kAll, w, 31);
+  }
+  __syncthreads();
+}
+
 // The time of a list of row groups, in tiles.
-__device__ __forceinline__ long long list_estimate(long long total, long long most, long long count, int n) {
-  return partition_uncut(true, count, n, most, total) ? most : total / n + kCutTiles;
+__device__ __forceinline__ int list_estimate(int total, int most, int count, int n) {
+  return partition_uncut(true, count, n, most, total) ? most : total / n + (int)kCutTiles;
 }
 
 }  // namespace
@@ -99,30 +122,37 @@ partition_prefix_kernel(Problem p, PrefixArgs pa, Layout lay, PrefixLayout pl, c
   ptx::pdl_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_warps = blockDim.x >> 5;
   const int B = p.batch, G = pa.groups, H = p.num_heads, n = lay.n_workers;
-  const int per = kPrefixRows / H;  // tokens of a row group (H is 16, 32, 64 or 128)
+  // tokens of a row group: 128 / H, a power of two (H is 16, 32, 64 or 128)
+  const int per_shift = H == 16 ? 3 : H == 32 ? 2 : H == 64 ? 1 : 0, per = 1 << per_shift;
   const int c0 = prefix_overhead(p.kv_dtype);
   int* hdr = reinterpret_cast<int*>(ws);
   WorkItem* items = reinterpret_cast<WorkItem*>(ws + lay.items);
   int* worker_begin = reinterpret_cast<int*>(ws + lay.worker_ranges);
   PrefixEntry* entries = reinterpret_cast<PrefixEntry*>(ws + pl.entries);
   PrefixSegment* segments = reinterpret_cast<PrefixSegment*>(ws + pl.segments);
-  const int owners = G + B;
   const PrefixScratch s(pl.scratch_in_smem ? reinterpret_cast<char*>(prefix_smem) : ws + pl.scratch, B, G,
                         lay.max_groups);
   auto tiles_of = [](int rows) { return (max(rows, 0) + kKvTile - 1) / kKvTile; };
-  auto groups_of = [&](int tokens) { return (tokens + per - 1) / per; };
+  auto groups_of = [&](int tokens) { return (tokens + per - 1) >> per_shift; };
   if (tid == 0) {
-    sh.alone = 0;
-    sh.status = sh.alone_most = sh.any = 0;
-    sh.count = 0;
+    sh.status = sh.alone = sh.alone_most = sh.alone_count = sh.any = 0;
+    sh.most = 0;
+  }
+  if (tid < 8) sh.cut[tid] = sh.first[tid] = 0;
+  // a warp's first prefix group, read beside the lengths
+  const int each = B / G;
+  int g_lo = 0, g_hi = 0, g_len = 0;
+  if (warp < G) {
+    g_lo = pa.indptr ? pa.indptr[warp] : warp * each;
+    g_hi = pa.indptr ? pa.indptr[warp + 1] : g_lo + each;
+    g_len = pa.lens[warp];
   }
   __syncthreads();
 
   // 1. Requests: lengths, clamped and flagged as by the other partitioners.
-  int status = 0;
+  int status = 0, bad = 0;
   {
-    long long total = 0;
-    int most = 0, count = 0;
+    int total = 0, most = 0, count = 0;
     for (int b = tid; b < B; b += blockDim.x) {
       int q, qs, L = p.seq_lens[b];
       if (p.packed) {
@@ -148,32 +178,30 @@ partition_prefix_kernel(Problem p, PrefixArgs pa, Layout lay, PrefixLayout pl, c
       if (L > 0 && q > 0) {
         count += groups_of(q);
         most = max(most, c0 + tiles_of(L));
-        total += (long long)groups_of(q) * (c0 + tiles_of(L));
+        total += groups_of(q) * (c0 + tiles_of(L));
       }
     }
-    total = __shfl_sync(kAll, scan_up(total, lane), 31);
+    total = (int)__reduce_add_sync(kAll, (unsigned)total);
     count = (int)__reduce_add_sync(kAll, (unsigned)count);
     most = __reduce_max_sync(kAll, most);
-    if (lane == 0) {
-      atomicAdd(reinterpret_cast<unsigned long long*>(&sh.alone), (unsigned long long)total);
-      atomicAdd(&sh.count, count);
+    if (lane == 0 && count > 0) {
+      atomicAdd(&sh.alone, total);
+      atomicAdd(&sh.alone_count, count);
       atomicMax(&sh.alone_most, most);
     }
-  }
-  // 2. Prefix groups: a warp each.  Where the offsets are bad nothing is shared.
-  int bad = 0;
-  if (pa.indptr)
-    for (int g = tid; g < G; g += blockDim.x) {
-      const int lo = pa.indptr[g], hi = pa.indptr[g + 1];
+    for (int g = warp; g < G; g += n_warps) {
+      const int lo = g == warp ? g_lo : pa.indptr ? pa.indptr[g] : 0, hi = g == warp ? g_hi : pa.indptr ? pa.indptr[g + 1] : 0;
       if (lo < 0 || hi < lo || hi > B) bad = 1;
     }
-  bad = __syncthreads_or(bad);
+  }
+  bad = __syncthreads_or(bad);  // (offsets that are none: nothing is shared)
   if (bad) status |= kStatusPrefix;
-  const int alone_count = sh.count;
+
+  // 2. Prefix groups: a warp each.
   for (int g = warp; g < G; g += n_warps) {
-    const int each = B / G;
-    const int lo = bad ? 0 : pa.indptr ? pa.indptr[g] : g * each;
-    const int hi = bad ? 0 : pa.indptr ? pa.indptr[g + 1] : lo + each;
+    const int lo = bad ? 0 : g == warp ? g_lo : pa.indptr ? pa.indptr[g] : g * each;
+    const int hi = bad ? 0 : g == warp ? g_hi : pa.indptr ? pa.indptr[g + 1] : lo + each;
+    const int len = g == warp ? g_len : pa.lens[g];
     int rows = INT_MAX, apart = 0;
     for (int b = lo + lane; b < hi; b += 32) {
       if (s.len[b] > 0 && s.q[b] > 0) rows = min(rows, p.causal ? s.len[b] - s.q[b] + 1 : s.len[b]);
@@ -182,20 +210,19 @@ partition_prefix_kernel(Problem p, PrefixArgs pa, Layout lay, PrefixLayout pl, c
     }
     rows = __reduce_min_sync(kAll, rows);
     apart = (int)__reduce_or_sync(kAll, (unsigned)apart);
-    const int len = pa.lens[g];
     if (len < 0) status |= kStatusPrefix;
     const int T = apart || rows == INT_MAX ? 0 : max(0, min(len, rows)) / kKvTile;
     const int tokens = hi > lo && T > 0 ? s.qs[hi - 1] + s.q[hi - 1] - s.qs[lo] : 0;
     // fewer tiles and overheads together than each on its own?
-    long long saved = 0;
+    int saved = 0;
     if (T > 0) {
       for (int b = lo + lane; b < hi; b += 32) {
         const int q = s.q[b], L = s.len[b], tok = s.qs[b] - s.qs[lo];
         if (q <= 0 || L <= 0) continue;
-        const int touched = (tok + q - 1) / per - tok / per + 1;
-        saved += (long long)groups_of(q) * (c0 + tiles_of(L)) - (long long)touched * tiles_of(L - T * kKvTile);
+        const int touched = ((tok + q - 1) >> per_shift) - (tok >> per_shift) + 1;
+        saved += groups_of(q) * (c0 + tiles_of(L)) - touched * tiles_of(L - T * kKvTile);
       }
-      saved = __shfl_sync(kAll, scan_up(saved, lane), 31) - (long long)groups_of(tokens) * (c0 + T);
+      saved = (int)__reduce_add_sync(kAll, (unsigned)saved) - groups_of(tokens) * (c0 + T);
     }
     const bool on = T > 0 && saved > 0;
     if (lane == 0) {
@@ -216,179 +243,161 @@ partition_prefix_kernel(Problem p, PrefixArgs pa, Layout lay, PrefixLayout pl, c
 
   // 3. Row groups, their costs and start units; once more with every request on its own where
   // that is the shorter list.
-  int n_rg = 0;
+  int n_rg = 0, W = 0;
   bool room = true;
-  auto owned = [&](int o) {  // row groups of an owner
-    if (o < G) return groups_of(s.tokens[o]);
-    const int b = o - G;
-    return s.group[b] >= 0 || s.len[b] <= 0 || s.q[b] <= 0 ? 0 : groups_of(s.q[b]);
-  };
+  auto shared_tiles = [&](int b) { return s.group[b] >= 0 ? s.shared[s.group[b]] : 0; };
+  auto first_request = [&](int b) { return s.group[b] >= 0 ? s.lo[s.group[b]] : b; };  // of b's owner
   for (int pass = 0; pass < 2; ++pass) {
+    int rg = 0, tiles = 0, count = 0;
+    for (int at = 0; at < B; at += blockDim.x) {
+      const int b = at + tid;
+      int v[3] = {0, 0, 0}, before[3], total[3];
+      if (b < B) {
+        const int g = s.group[b], q = s.q[b], L = s.len[b];
+        if (g >= 0) v[0] = b == s.lo[g] ? groups_of(s.tokens[g]) : 0;
+        else v[0] = q > 0 && L > 0 ? groups_of(q) : 0;
+        v[1] = q > 0 ? tiles_of(L - shared_tiles(b) * kKvTile) : 0;
+        v[2] = v[1] > 0 ? 1 : 0;
+      }
+      block_scan(sh, v, before, total);
+      if (b < B) {
+        s.base[b] = rg + before[0];
+        s.tiles[b] = tiles + before[1];
+        s.count[b] = count + before[2];
+      }
+      rg += total[0];
+      tiles += total[1];
+      count += total[2];
+    }
     if (tid == 0) {
-      sh.count = 0;
+      s.tiles[B] = tiles;
+      s.count[B] = count;
       sh.most = 0;
-      sh.carry = 0;
     }
-    __syncthreads();
-    for (int at = 0; at < owners; at += blockDim.x) {
-      const int o = at + tid, c = o < owners ? owned(o) : 0;
-      const int in = scan_up(c, lane);
-      if (lane == 31) sh.w_count[warp] = in;
-      __syncthreads();
-      int before = sh.count;
-      for (int w = 0; w < warp; ++w) before += sh.w_count[w];
-      if (o < owners) s.base[o] = before + in - c;
-      __syncthreads();
-      if (tid == 0)
-        for (int w = 0; w < n_warps; ++w) sh.count += sh.w_count[w];
-      __syncthreads();
-    }
-    n_rg = sh.count;
-    if (tid == 0) s.base[owners] = n_rg;
+    n_rg = rg;
     // (malformed offsets may let requests overlap: more row groups than the plan has room for)
     room = n_rg <= lay.max_groups;
     if (!room) n_rg = 0;
-    for (int r = tid; r < n_rg; r += blockDim.x) s.cost[r] = c0;
     __syncthreads();
-    if (n_rg > 0) {
-      for (int g = warp; g < G; g += n_warps)
-        for (int k = lane; k < groups_of(s.tokens[g]); k += 32) atomicAdd(&s.cost[s.base[g] + k], s.shared[g]);
+    // the requests of each row group's first and last token
+    if (n_rg > 0)
       for (int b = tid; b < B; b += blockDim.x) {
         const int g = s.group[b], q = s.q[b];
-        if (q <= 0 || s.len[b] <= 0) continue;
-        const int own = tiles_of(s.len[b] - (g >= 0 ? s.shared[g] * kKvTile : 0));
-        const int first = s.base[g >= 0 ? g : G + b] + s.tok[b] / per, last = first - s.tok[b] / per + (s.tok[b] + q - 1) / per;
-        if (own > 0)
-          for (int r = first; r <= last; ++r) atomicAdd(&s.cost[r], own);
+        if (q <= 0 || (g < 0 && s.len[b] <= 0)) continue;
+        const int tok = s.tok[b], tokens = g >= 0 ? s.tokens[g] : q, base = s.base[first_request(b)];
+        for (int k = (tok + per - 1) >> per_shift; k << per_shift < tok + q; ++k) s.first[base + k] = b;
+        for (int k = tok >> per_shift; k <= (tok + q - 1) >> per_shift; ++k)
+          if (min((k + 1) << per_shift, tokens) <= tok + q) s.last[base + k] = b;
       }
-    }
     __syncthreads();
+    W = 0;
     for (int at = 0; at < n_rg; at += blockDim.x) {
-      const int r = at + tid, c = r < n_rg ? s.cost[r] : 0;
-      const long long in = scan_up((long long)c, lane);
-      const int most = __reduce_max_sync(kAll, c);
-      if (lane == 31) {
-        sh.w_cost[warp] = in;
-        atomicMax(&sh.most, most);
-      }
-      __syncthreads();
-      long long before = sh.carry;
-      for (int w = 0; w < warp; ++w) before += sh.w_cost[w];
-      if (r < n_rg) s.start[r] = before + in - c;
-      __syncthreads();
-      if (tid == 0)
-        for (int w = 0; w < n_warps; ++w) sh.carry += sh.w_cost[w];
-      __syncthreads();
+      const int r = at + tid;
+      int v[1] = {0}, before[1], total[1];
+      if (r < n_rg) v[0] = c0 + shared_tiles(s.first[r]) + s.tiles[s.last[r] + 1] - s.tiles[s.first[r]];
+      const int most = __reduce_max_sync(kAll, v[0]);
+      if (lane == 0 && most > 0) atomicMax(&sh.most, most);
+      block_scan(sh, v, before, total);
+      if (r < n_rg) s.start[r] = W + before[0];
+      W += total[0];
     }
+    if (tid == 0) s.start[n_rg] = W;
+    __syncthreads();
     if (pass == 1 || !sh.any || !room) break;
-    if (list_estimate(sh.carry, sh.most, n_rg, n) <= list_estimate(sh.alone, sh.alone_most, alone_count, n)) break;
+    if (list_estimate(W, sh.most, n_rg, n) <= list_estimate(sh.alone, sh.alone_most, sh.alone_count, n)) break;
     __syncthreads();
     for (int b = tid; b < B; b += blockDim.x) {
       s.group[b] = -1;
       s.tok[b] = 0;
     }
-    for (int g = tid; g < G; g += blockDim.x) s.tokens[g] = 0;
     __syncthreads();
   }
-  const long long W = sh.carry;
-  const int n_eff = (int)max(1LL, min((long long)n, W / kMinUnits));
+  const int n_eff = max(1, min(n, W / (int)kMinUnits));
   const bool uncut = partition_uncut(true, n_rg, n, sh.most, W);
 
   // 4. Worker boundaries, and which of them cut a row group (past its overhead).
+  const int quot = W / n_eff, rest = W % n_eff;
+  auto bound_of = [&](int w) {
+    return uncut ? w < n_rg ? s.start[w] : W : w >= n_eff ? W : w * quot + w * rest / n_eff;
+  };
   for (int w = tid; w <= n; w += blockDim.x) {
-    if (uncut)
-      sh.bound[w] = w < n_rg ? s.start[w] : W;
-    else
-      sh.bound[w] = w >= n_eff ? W : w * (W / n_eff) + w * (W % n_eff) / n_eff;
-  }
-  if (tid < 8) sh.cut[tid] = sh.first[tid] = 0;
-  __syncthreads();
-  auto group_at = [&](long long unit) { return last_upto(s.start, n_rg, unit); };
-  for (int w = tid; w <= n; w += blockDim.x) {
-    if (w == 0 || sh.bound[w] >= W) continue;
-    const long long from = s.start[group_at(sh.bound[w])] + c0;  // unit of the row group's first tile
-    if (sh.bound[w] <= from) continue;
+    const int at = bound_of(w);
+    sh.bound[w] = at;
+    if (w == 0 || at >= W) continue;
+    const int from = s.start[last_upto(s.start, n_rg, at)] + c0;  // unit of the row group's first tile
+    if (at <= from) continue;
     atomicOr(reinterpret_cast<int*>(&sh.cut[w >> 5]), (int)(1u << (w & 31)));
-    if (sh.bound[w - 1] <= from) atomicOr(reinterpret_cast<int*>(&sh.first[w >> 5]), (int)(1u << (w & 31)));
+    if (bound_of(w - 1) <= from) atomicOr(reinterpret_cast<int*>(&sh.first[w >> 5]), (int)(1u << (w & 31)));
   }
   __syncthreads();
 
   // 5. Items, segments, entries of the join, worker ranges.
   const int n_items = n_rg + bits_under(sh.cut, 255);
   const bool fits = room && n_items <= lay.max_items && n_items - n_rg + bits_under(sh.first, 255) <= lay.max_partials;
-  auto emit = [&](int at, int rg, int owner, long long t0, long long t1, int slot) {
+  auto owner_tokens = [&](int b) { return s.group[b] >= 0 ? s.tokens[s.group[b]] : s.q[b]; };
+  auto emit = [&](int at, int rg, int t0, int t1, int slot) {
+    const int b = s.first[rg], o = first_request(b);
     WorkItem it;
-    const int b = owner < G ? s.lo[owner] : owner - G;
-    it.b = b;
-    it.g = rg - s.base[owner];
-    it.kv_begin = (int)t0 * kKvTile;
-    it.kv_end = (int)t1 * kKvTile;
+    it.b = o;
+    it.g = rg - s.base[o];
+    it.kv_begin = t0 * kKvTile;
+    it.kv_end = t1 * kKvTile;
     it.slot = slot;
-    it.q_len = owner < G ? s.tokens[owner] : s.q[b];
-    it.seq_len = 0;
-    it.q_start = s.qs[b];
+    it.q_len = owner_tokens(b);
+    it.seq_len = (shared_tiles(b) > 0 ? 1 : 0) + s.count[s.last[rg] + 1] - s.count[b];
+    it.q_start = s.qs[o];
     it.comb = rg;
     it.mask_base = 0;
-    // the row group's segments (each of its items has their number)
-    const int first = it.g * per, end = min(first + per, it.q_len);  // tokens
-    const int T = owner < G ? s.shared[owner] : 0;
-    int count = 0, tile = 0;
-    PrefixSegment* seg = segments + (size_t)rg * kPrefixSegments;
-    const bool write = t0 == 0;
-    if (T > 0) {
-      int src = b;  // the first request that has rows: its table is read
-      while (src + 1 < s.hi[owner] && (s.len[src] <= 0 || s.q[src] <= 0)) ++src;
-      if (write) seg[0] = PrefixSegment{0, src, 0, T * kKvTile, 0, kPrefixRows, kPrefixNoMask, 0};
-      count = 1;
-      tile = T;
-    }
-    const int stop = owner < G ? s.hi[owner] : b + 1;
-    for (int r = owner < G ? b + last_upto(s.tok + b, stop - b, first) : b; r < stop && s.tok[r] < end; ++r) {
-      const int own = tiles_of(s.len[r] - T * kKvTile), q = s.q[r];
-      if (q <= 0 || own <= 0 || s.tok[r] + q <= first || count >= kPrefixSegments) continue;
-      if (write)
-        seg[count] = PrefixSegment{tile, r, T * kKvTile, s.len[r], max(0, s.tok[r] - first) * H,
-                                   min(per, s.tok[r] + q - first) * H,
-                                   p.causal ? s.len[r] - q - s.tok[r] : kPrefixNoMask, 0};
-      ++count;
-      tile += own;
-    }
-    it.seq_len = count;
     items[at] = it;
   };
   if (fits) {
     for (int rg = tid; rg < n_rg; rg += blockDim.x) {
-      const int owner = last_upto(s.base, owners, rg);
-      const long long from = s.start[rg] + c0, end = s.start[rg] + s.cost[rg];
+      const int from = s.start[rg] + c0, end = s.start[rg + 1];
       const int pb = sh.bound[0] > from ? 0 : last_upto(sh.bound, n + 1, from) + 1;  // boundaries up to the first tile
       int last = pb;  // past the row group's last cut
       while (last < n && bit_at(sh.cut, last) && sh.bound[last] < end) ++last;
       const bool split = last > pb;
       const int before = bits_under(sh.cut, pb), slot = before + bits_under(sh.first, pb);
-      emit(rg + before, rg, owner, 0, split ? sh.bound[pb] - from : end - from, split ? slot : -1);
+      emit(rg + before, rg, 0, (split ? sh.bound[pb] : end) - from, split ? slot : -1);
+      const int b = s.first[rg], o = first_request(b), k = rg - s.base[o], T = shared_tiles(b);
       PrefixEntry e = {};
-      const int k = rg - s.base[owner], b = owner < G ? s.lo[owner] : owner - G;
-      const int tokens = owner < G ? s.tokens[owner] : s.q[b];
-      e.row0 = ((long long)s.qs[b] + (long long)k * per) * H;
-      e.rows = split ? min(per, tokens - k * per) * H : 0;
+      e.row0 = ((long long)s.qs[o] + (k << per_shift)) * H;
+      e.rows = split ? min(per, owner_tokens(b) - (k << per_shift)) * H : 0;
       e.slot = slot;
       e.count = 1 + last - pb;
       entries[rg] = e;
+      if (T > 0) {
+        int src = o;  // the owner's first request that has rows: its table is read
+        while (src + 1 < s.hi[s.group[b]] && (s.len[src] <= 0 || s.q[src] <= 0)) ++src;
+        segments[(size_t)rg * kPrefixSegments] = PrefixSegment{0, src, 0, T * kKvTile, 0, kPrefixRows, kPrefixNoMask, 0};
+      }
+    }
+    // each request's own rows, a segment in every row group that it has query rows in
+    for (int b = tid; b < B; b += blockDim.x) {
+      const int q = s.q[b], tok = s.tok[b], T = shared_tiles(b), L = s.len[b];
+      if (q <= 0 || L <= T * kKvTile) continue;
+      const int base = s.base[first_request(b)];
+      for (int k = tok >> per_shift; k <= (tok + q - 1) >> per_shift; ++k) {
+        const int f = s.first[base + k], first = k << per_shift, z = (T > 0 ? 1 : 0) + s.count[b] - s.count[f];
+        if (z >= kPrefixSegments) continue;  // (never)
+        segments[(size_t)(base + k) * kPrefixSegments + z] =
+            PrefixSegment{T + s.tiles[b] - s.tiles[f], b, T * kKvTile, L, max(0, tok - first) * H,
+                          min(per, tok + q - first) * H, p.causal ? L - q - tok : kPrefixNoMask, 0};
+      }
     }
     for (int w = tid; w <= n; w += blockDim.x) {
       if (sh.bound[w] >= W) {
         worker_begin[w] = n_items;
         continue;
       }
-      const int rg = group_at(sh.bound[w]);
+      const int rg = last_upto(s.start, n_rg, sh.bound[w]);
       const bool cuts = bit_at(sh.cut, w);
-      // (a boundary inside a row group's overhead, or at its start, leaves the row group whole)
-      worker_begin[w] = rg + bits_under(sh.cut, w) + (cuts ? 1 : 0);
-      if (!cuts) continue;
-      const long long from = s.start[rg] + c0, tiles = s.cost[rg] - c0;
-      const long long next = w + 1 <= n ? min(tiles, sh.bound[w + 1] - from) : tiles;
       const int rank = bits_under(sh.cut, w);
-      emit(rg + 1 + rank, rg, last_upto(s.base, owners, rg), sh.bound[w] - from, next,
+      // (a boundary inside a row group's overhead, or at its start, leaves the row group whole)
+      worker_begin[w] = rg + rank + (cuts ? 1 : 0);
+      if (!cuts) continue;
+      const int from = s.start[rg] + c0, tiles = s.start[rg + 1] - from;
+      emit(rg + 1 + rank, rg, sh.bound[w] - from, w + 1 <= n ? min(tiles, sh.bound[w + 1] - from) : tiles,
            rank + bits_under(sh.first, w + 1));
     }
   } else {
@@ -399,14 +408,14 @@ partition_prefix_kernel(Problem p, PrefixArgs pa, Layout lay, PrefixLayout pl, c
     hdr[kHdrNumItems] = fits ? n_items : 0;
     hdr[kHdrWorkCounter] = 0;
     hdr[kHdrNumCombine] = fits ? n_rg : 0;
-    hdr[kHdrChunkTiles] = (int)min(W, 1LL << 30);
+    hdr[kHdrChunkTiles] = min(W, 1 << 30);
     hdr[kHdrCombineCounter] = 0;
   }
 }
 
 // A thread for each request, worker boundary and row group, a warp for each prefix group.
 inline int partition_prefix_threads(const Problem& p, const PrefixArgs& pa, const Layout& lay) {
-  const long long need = std::max(std::max((long long)p.batch, 32LL * pa.groups),
+  const long long need = std::max(std::max((long long)p.batch, std::min(256LL, 32LL * pa.groups)),
                                   std::max((long long)lay.n_workers + 1, (long long)lay.max_groups));
   return (int)std::min<long long>(kPartThreads, (need + 31) / 32 * 32);
 }
@@ -425,10 +434,13 @@ join_prefix_kernel(Problem p, Layout lay, PrefixLayout pl, char* __restrict__ ws
   const uint4* part_o = reinterpret_cast<const uint4*>(ws + lay.part_o);
   const float* part_lse = reinterpret_cast<const float*>(ws + lay.part_lse);
   const int t = threadIdx.x >> 3, r = blockIdx.x * kJoinRows + (threadIdx.x & 7);
-  ptx::pdl_wait();
+  // (the partitioner had ended before the decode kernel let this one start)
   const int n_entries = reinterpret_cast<const int*>(ws)[kHdrNumCombine];
+  PrefixEntry e = {};
+  if (blockIdx.y < n_entries) e = entries[blockIdx.y];
+  ptx::pdl_wait();
   for (int i = blockIdx.y; i < n_entries; i += gridDim.y) {
-    const PrefixEntry e = entries[i];
+    if (i != blockIdx.y) e = entries[i];
     if (r >= e.rows) continue;
     float m = -INFINITY, sum = 0.f, acc[16];
 #pragma unroll

@@ -59,23 +59,24 @@ struct PrefixLayout {
   int scratch_in_smem;
 };
 
-// Partitioner scratch: by request, prefix group, owner (a group or a request) and row group.
+// Partitioner scratch: by request, prefix group and row group.
 __host__ __device__ inline size_t prefix_scratch_bytes(long long batch, long long groups, long long row_groups) {
-  return align_up(sizeof(long long) * (size_t)(row_groups + 1), 16) +
-         sizeof(int) * (size_t)(row_groups + 5 * batch + 4 * groups + (groups + batch + 1)) + 16;
+  return align_up(sizeof(int) * (size_t)(8 * batch + 2 + 4 * groups + 3 * row_groups + 1), 16);
 }
 
-// The workspace of a plan with `groups` prefix groups.
+// The workspace of a plan with `groups` prefix groups; false: too large a plan.
 inline bool make_prefix_layout(long long batch, long long heads, long long max_q, bool packed, long long max_total_q,
-                               int kv_dtype, long long groups, int n_workers, size_t header, Layout* lay,
-                               PrefixLayout* pre) {
+                               long long max_seq_len, int kv_dtype, long long groups, int n_workers, size_t header,
+                               Layout* lay, PrefixLayout* pre) {
   const long long R = kPrefixRows;
   auto ceil_to = [](long long a, long long b) { return (a + b - 1) / b; };
   long long rg = batch * ceil_to(max_q * heads, R);
   if (packed && batch + ceil_to(max_total_q * heads, R) < rg) rg = batch + ceil_to(max_total_q * heads, R);
   rg = rg > 1 ? rg : 1;
   const long long items = rg + n_workers;
-  if (items > (1LL << 24)) return false;
+  // costs are held in 32 bits (a row group walks kPrefixSegments requests' rows at most)
+  const long long cost = rg * (prefix_overhead(0) + kPrefixSegments * (max_seq_len / kKvTile + 1));
+  if (items > (1LL << 24) || cost >= (1LL << 31)) return false;
   lay->rows_per_group = (int)R;
   lay->n_workers = n_workers;
   lay->n_ctas = 2 * n_workers;

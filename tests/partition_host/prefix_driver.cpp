@@ -46,7 +46,7 @@ int main(int argc, char** argv) {
   std::fclose(f);
   mla::Layout lay{};
   mla::PrefixLayout pl{};
-  if (!mla::make_prefix_layout(B, H, max_q, packed, total_q, kv_dtype, G, n_workers, sizeof(int) * mla::kHdrWords, &lay, &pl))
+  if (!mla::make_prefix_layout(B, H, max_q, packed, total_q, max_seq_len, kv_dtype, G, n_workers, sizeof(int) * mla::kHdrWords, &lay, &pl))
     return 3;
   const size_t starts[] = {lay.items, lay.worker_ranges, pl.entries, pl.segments, lay.part_o, lay.part_lse, lay.total};
   for (size_t i = 0; i < sizeof(starts) / sizeof(starts[0]); ++i)
