@@ -991,7 +991,7 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
         tmem_wait_ld();
         if (!row_ok || (kShared && it.slot >= 0 && l_row == 0.f)) continue;  // (nothing seen: the LSE says so)
         const int chunk = 16 * hh + 8 * grp + k;  // of 16 dims
-        if (C::kTma && it.slot >= 0) {  // fp32 (part_format)
+        if (!kShared && C::kTma && it.slot >= 0) {  // fp32 (part_format)
 #pragma unroll
           for (int u = 0; u < 4; ++u)
             part_o[part_unit_f32(it.slot, kRows, chunk, u, q)] =
@@ -1010,10 +1010,23 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
           }
           d0 = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.out) + grow * kVDim + 16 * chunk);
           d1 = d0 + 1;
-        } else {  // f16, times 2^kPartShift
+        } else {  // f16, times 2^kPartShift (kShared over bf16: a power of these dims' own, prefix_scale)
+          float by = s2;
+          if constexpr (kShared && C::kTma) {
+            uint32_t most = 0;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              x[e] = __float_as_uint(__uint_as_float(x[e]) * s2);
+              most = max(most, x[e] & 0x7FFFFFFFu);
+            }
+            const int up = prefix_scale(most);
+            reinterpret_cast<signed char*>(ws + prefix_scale_offset(lay))[((size_t)it.slot * 32 + chunk) * kRows + q] =
+                (signed char)up;
+            by = __uint_as_float((uint32_t)(127 + up) << 23);
+          }
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const __half2 h = __floats2half2_rn(__uint_as_float(x[2 * e]) * s2, __uint_as_float(x[2 * e + 1]) * s2);
+            const __half2 h = __floats2half2_rn(__uint_as_float(x[2 * e]) * by, __uint_as_float(x[2 * e + 1]) * by);
             o[e] = *reinterpret_cast<const uint32_t*>(&h);
           }
           d0 = part_o + part_unit(it.slot, kRows, chunk, 0, q);

@@ -422,17 +422,19 @@ inline int partition_prefix_threads(const Problem& p, const PrefixArgs& pa, cons
 
 // The join: O and the LSE of the rows of cut row groups from their partials.  A block takes eight
 // query rows, its threads a row and 16 dims each: eight neighbouring threads read 128
-// contiguous bytes of a partial.  A partial of a row that sees none of its tiles has an LSE of
-// -inf, and no O.  The decode kernel has ended before anything is read.
+// contiguous bytes of a partial.  What bounds it is the partials' bytes: a partial of a row
+// that sees none of its tiles has an LSE of -inf and no O, and is not read.  The decode
+// kernel has ended before a partial is.
 constexpr int kJoinThreads = 256, kJoinRows = 8, kJoinBatch = 4;
 
-template <int kFormat>
+// kScaled: over bf16 (see prefix_scale_offset).
+template <bool kScaled>
 __global__ void __launch_bounds__(kJoinThreads)
 join_prefix_kernel(Problem p, Layout lay, PrefixLayout pl, char* __restrict__ ws) {
-  constexpr int kUnits = kFormat == kPartF32 ? kPartUnitsF32 : kPartUnits;
   const PrefixEntry* entries = reinterpret_cast<const PrefixEntry*>(ws + pl.entries);
   const uint4* part_o = reinterpret_cast<const uint4*>(ws + lay.part_o);
   const float* part_lse = reinterpret_cast<const float*>(ws + lay.part_lse);
+  const signed char* part_scale = reinterpret_cast<const signed char*>(ws + prefix_scale_offset(lay));
   const int t = threadIdx.x >> 3, r = blockIdx.x * kJoinRows + (threadIdx.x & 7);
   // (the partitioner had ended before the decode kernel let this one start)
   const int n_entries = reinterpret_cast<const int*>(ws)[kHdrNumCombine];
@@ -446,22 +448,23 @@ join_prefix_kernel(Problem p, Layout lay, PrefixLayout pl, char* __restrict__ ws
 #pragma unroll
     for (int k = 0; k < 16; ++k) acc[k] = 0.f;
     for (int k0 = 0; k0 < e.count; k0 += kJoinBatch) {
-      uint4 x[kJoinBatch][kUnits];
+      uint4 x[kJoinBatch][2];
       float l[kJoinBatch];
-#pragma unroll
-      for (int u = 0; u < kJoinBatch; ++u) {
-        l[u] = -INFINITY;
-        if (k0 + u < e.count) l[u] = part_lse[(size_t)(e.slot + k0 + u) * kPrefixRows + r];
-      }
+      int down[kJoinBatch];
 #pragma unroll
       for (int u = 0; u < kJoinBatch; ++u)
+        l[u] = k0 + u < e.count ? part_lse[(size_t)(e.slot + k0 + u) * kPrefixRows + r] : -INFINITY;
 #pragma unroll
-        for (int v = 0; v < kUnits; ++v) {
-          x[u][v] = make_uint4(0, 0, 0, 0);
-          if (l[u] != -INFINITY)
-            x[u][v] = part_o[kFormat == kPartF32 ? part_unit_f32(e.slot + k0 + u, kPrefixRows, t, v, r)
-                                                 : part_unit(e.slot + k0 + u, kPrefixRows, t, v, r)];
+      for (int u = 0; u < kJoinBatch; ++u) {
+        x[u][0] = x[u][1] = make_uint4(0, 0, 0, 0);
+        down[u] = kScaled ? 0 : part_shift(p.kv_dtype);
+        if (l[u] != -INFINITY) {
+          const size_t slot = e.slot + k0 + u;
+          x[u][0] = part_o[part_unit(slot, kPrefixRows, t, 0, r)];
+          x[u][1] = part_o[part_unit(slot, kPrefixRows, t, 1, r)];
+          if constexpr (kScaled) down[u] = part_scale[(slot * 32 + t) * kPrefixRows + r];
         }
+      }
       float m_new = m;
 #pragma unroll
       for (int u = 0; u < kJoinBatch; ++u) m_new = fmaxf(m_new, l[u]);
@@ -472,28 +475,24 @@ join_prefix_kernel(Problem p, Layout lay, PrefixLayout pl, char* __restrict__ ws
       for (int k = 0; k < 16; ++k) acc[k] *= f;
 #pragma unroll
       for (int u = 0; u < kJoinBatch; ++u) {
-        const float w = expf(l[u] - ref);
+        float w = expf(l[u] - ref);  // (0 where there is no partial)
         sum += w;
+        w *= __uint_as_float((uint32_t)(127 - down[u]) << 23);
 #pragma unroll
-        for (int v = 0; v < kUnits; ++v) {
+        for (int v = 0; v < 2; ++v) {
           const uint32_t word[4] = {x[u][v].x, x[u][v].y, x[u][v].z, x[u][v].w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            if constexpr (kFormat == kPartF32) {
-              acc[4 * v + k] += w * __uint_as_float(word[k]);
-            } else {
-              const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&word[k]));
-              acc[8 * v + 2 * k] += w * h.x;
-              acc[8 * v + 2 * k + 1] += w * h.y;
-            }
+            const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&word[k]));
+            acc[8 * v + 2 * k] += w * h.x;
+            acc[8 * v + 2 * k + 1] += w * h.y;
           }
         }
       }
       m = m_new;
     }
     const bool any = sum != 0.f;  // (a NaN is no empty sum)
-    float s2 = any ? run_bmm2(p) / sum : 0.f;
-    if constexpr (kFormat == kPartF16) s2 *= 1.f / (1 << part_shift(p.kv_dtype));
+    const float s2 = any ? run_bmm2(p) / sum : 0.f;
     __nv_bfloat162 o[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) o[k] = __floats2bfloat162_rn(acc[2 * k] * s2, acc[2 * k + 1] * s2);
@@ -529,7 +528,7 @@ cudaError_t launch_join_prefix(const Problem& p, const Layout& lay, const Prefix
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  auto kernel = p.kv_dtype == kKvFp8 || p.kv_dtype == kKvFp4 ? join_prefix_kernel<kPartF16> : join_prefix_kernel<kPartF32>;
+  auto kernel = p.kv_dtype == kKvFp8 || p.kv_dtype == kKvFp4 ? join_prefix_kernel<false> : join_prefix_kernel<true>;
   return cudaLaunchKernelEx(&cfg, kernel, p, lay, pl, static_cast<char*>(ws));
 }
 

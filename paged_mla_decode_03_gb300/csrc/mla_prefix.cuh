@@ -59,6 +59,22 @@ struct PrefixLayout {
   int scratch_in_smem;
 };
 
+// Partials are f16, laid out as part_unit says: over 4 bits and e4m3 times 2^part_shift; over
+// bf16, whose values have no bound, 16 dims of a row times a power of two that brings the
+// largest of them to [2^14, 2^15), so that each is off by 2^-11 of itself or 2^-39 of the
+// largest.  The powers, a byte for each row and 16 dims, follow the LSEs.  (fp32 partials were
+// as near and twice the bytes, which bound the join: 6 x 10 requests of 1 to 4 tokens, 64
+// heads: 143 us instead of 136.)
+__host__ __device__ inline size_t prefix_scale_offset(const Layout& lay) {
+  return align_up(lay.part_lse + sizeof(float) * kPrefixRows * (size_t)lay.max_partials, 256);
+}
+// The power: 0 for zeros, a NaN or an infinity.
+__host__ __device__ inline int prefix_scale(unsigned max_bits) {
+  const int e = (int)(max_bits >> 23);
+  if (max_bits == 0 || e == 255) return 0;
+  return 141 - e < 126 ? 141 - e : 126;
+}
+
 // Partitioner scratch: by request, prefix group and row group.
 __host__ __device__ inline size_t prefix_scratch_bytes(long long batch, long long groups, long long row_groups) {
   return align_up(sizeof(int) * (size_t)(8 * batch + 2 + 4 * groups + 3 * row_groups + 1), 16);
@@ -101,8 +117,9 @@ inline bool make_prefix_layout(long long batch, long long heads, long long max_q
   lay->req_scratch = lay->group_scratch = pre->scratch;
   lay->scratch_bytes = 0;
   lay->scratch_in_smem = 1;
-  lay->part_o = take(part_row_bytes(kv_dtype, 1) * (size_t)R * (size_t)lay->max_partials);
+  lay->part_o = take(kPartBytesPerRow * (size_t)R * (size_t)lay->max_partials);
   lay->part_lse = take(sizeof(float) * (size_t)R * (size_t)lay->max_partials);
+  if (kv_dtype == 0) take(32 * (size_t)R * (size_t)lay->max_partials);  // (prefix_scale_offset)
   lay->comb_done = take(sizeof(int));
   lay->total = off;
   return true;
