@@ -38,6 +38,8 @@ cudaError_t launch_decode_prefix(const Problem& p, const Layout& lay, const Pref
 cudaError_t prefix_setup();
 cudaError_t launch_partition_prefix(const Problem& p, const PrefixArgs& pa, const Layout& lay, const PrefixLayout& pl,
                                     void* ws, cudaStream_t stream);
+cudaError_t launch_widen_prefix(const Problem& p, int groups, const PrefixLayout& pl, void* ws, int sm_count,
+                                cudaStream_t stream);
 cudaError_t launch_join_prefix(const Problem& p, const Layout& lay, const PrefixLayout& pl, void* ws, int sm_count,
                                cudaStream_t stream);
 }  // namespace mla
@@ -381,6 +383,9 @@ int run_impl(const mla_plan_t* plan, const void* query, const void* kv_cache,
   if ((prefix ? mla::launch_partition_prefix(p, *prefix, plan->lay, plan->pre, workspace, s)
               : mla::launch_partition(p, plan->lay, workspace, s)) != cudaSuccess)
     return MLA_ERR_CUDA;
+  if (prefix && plan->pre.wide_tiles > 0 &&
+      mla::launch_widen_prefix(p, prefix->groups, plan->pre, workspace, plan->sm_count, s) != cudaSuccess)
+    return MLA_ERR_CUDA;
   // work enqueued elsewhere that the decode needs (the host entry's query copy)
   if (join_before_decode && cudaStreamWaitEvent(s, join_before_decode, 0) != cudaSuccess)
     return MLA_ERR_CUDA;
@@ -606,6 +611,7 @@ int mla_decode_work_list_layout(const mla_plan_t* plan, size_t* items_offset,
 int32_t mla_decode_kernels_per_run(const mla_plan_t* plan) {
   if (!plan) return -1;
   if (plan->prm.batch == 0) return 0;
+  if (plan->prm.prefix_groups > 0) return plan->pre.wide_tiles > 0 ? 5 : 3;
   return uses_q_split(plan->prm) ? 4 : 3;
 }
 

@@ -98,11 +98,13 @@ constexpr uint32_t OFF_P = OFF_V + 2 * kVStage;
 
 // The cache's format: 4 bits; e4m3 (576 bytes a row, values exact in f16); bf16
 // (bf16 MMAs, and TMA brings K and V where the MMAs read them: no staging, and
-// the conversion warps only load queries and clear unused rows).
-enum Cache { kFp4, kE4m3, kBf16 };
+// the conversion warps only load queries and clear unused rows); f16 rows that shared
+// prefixes of the first two were widened to (mla_prefix.cu): as bf16, with their arithmetic.
+enum Cache { kFp4, kE4m3, kBf16, kF16 };
 template <int kCache> struct Cfg {
-  static constexpr bool kTma = kCache == kBf16;
-  static constexpr float kPShift = kTma ? 0.f : 7.f;  // P is stored times 2^kPShift (bf16 has the range)
+  static constexpr bool kTma = kCache == kBf16 || kCache == kF16;
+  static constexpr bool kBf = kCache == kBf16;  // bf16 MMAs
+  static constexpr float kPShift = kBf ? 0.f : 7.f;  // P is stored times 2^kPShift (bf16 has the range)
   static constexpr uint32_t kCodeBytes = kCache == kFp4 ? kFp4CodeBytes : kTma ? 2 * kQkDim : kQkDim;  // of a row
   static constexpr uint32_t kScaleBytes = kCache == kFp4 ? kFp4ScaleBytes : 0;
   static constexpr uint32_t kVBytes = kCache == kFp4 ? 128 : 256;  // codes of 256 dims
@@ -345,7 +347,7 @@ __device__ __noinline__ bool first_query(Ctx c, unsigned char* sm, uint32_t tmem
 #pragma unroll 1
   for (int r = 4 * w; r < 4 * w + 4; ++r) {
     int e = 0;
-    if (!q.fp8 && kCache != kBf16) {
+    if (!q.fp8 && !Cfg<kCache>::kBf) {
       const uint4 a = q.unit(r, lane), b = q.unit(r, 32 + lane), d = q.unit(r, 64 + (lane & 7));
       uint32_t mb = __vmaxu2(__vmaxu2(max_bits(a), max_bits(b)), max_bits(d));
       mb = __reduce_max_sync(0xffffffffu, max(mb & 0xFFFFu, mb >> 16));
@@ -360,7 +362,7 @@ __device__ __noinline__ bool first_query(Ctx c, unsigned char* sm, uint32_t tmem
   }
   if (!wait_bar(c, QX, 0)) return false;
   auto as_operand = [&](const uint4 x, float up) {  // f16, or bf16 for bf16 MMAs
-    if constexpr (Cfg<kCache>::kTma) return q.fp8 ? e4m3x8_to_bf16(make_uint2(x.x, x.y)) : x;
+    if constexpr (Cfg<kCache>::kBf) return q.fp8 ? e4m3x8_to_bf16(make_uint2(x.x, x.y)) : x;
     return q.fp8 ? e4m3x8_to_f16(make_uint2(x.x, x.y)) : bf16x8_to_f16(x, up);
   };
   // as in load_query
@@ -396,7 +398,7 @@ template <int kCache, bool kShared>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
                    const __grid_constant__ CUtensorMap tm_k,   // (bf16 cache only)
-                   const __grid_constant__ CUtensorMap tm_v, const PrefixSegment* __restrict__ segments) {
+                   const __grid_constant__ CUtensorMap tm_v, const PrefixSegment* __restrict__ segments, const int late) {
   using C = Cfg<kCache>;
   // The swizzled tiles need 1024-byte alignment, and there is no room to round
   // up: the block has no other shared memory, so its dynamic part starts at
@@ -453,7 +455,9 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
   cluster_sync();  // the other CTA's barriers exist before any remote arrival
   // the work list comes from the partitioner; the combine kernel may be
   // scheduled from here on (it waits on counters that the epilogues bump)
-  pdl_wait();
+  // (late: the second decode of a run, whose list was there before the first one let it start)
+  constexpr bool kLate = kShared && !C::kTma;  // (a plan that widens walks 4 bits or e4m3 second)
+  if (!kLate || !late) pdl_wait();
   pdl_launch_dependents();
   const uint32_t tmem = *tmem_slot;
   const int item_begin = worker_begin[worker], item_end = worker_begin[worker + 1];
@@ -497,6 +501,7 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
           row += (tile - t0) * kTile + (npg == 2 ? (i & 1) * kHalf : 0);
           left = end - row;
           if (i >= nt * npg || left <= 0) return -1;
+          if constexpr (kCache == kF16) return row >> ps_shift;  // (rows follow on one another)
           const int id = p.block_tables[(size_t)b * p.max_pages + (row >> ps_shift)];
           if (id >= 0 && (long long)id < p.num_pages) return id;
           if (bulk) atomicOr(c.status, kStatusPage);
@@ -651,7 +656,7 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
     // ------------------------------------------------------------ QK issue
     // The whole warp walks the loops and one lane issues (see elect_one).
     if (rank == 0) {
-      constexpr uint32_t idesc = C::kTma ? idesc_f16(kRows, kTile, false, false) : idesc_half(kRows, kTile, false, false);
+      constexpr uint32_t idesc = C::kBf ? idesc_f16(kRows, kTile, false, false) : idesc_half(kRows, kTile, false, false);
       // operand descriptors; a step along an operand adds its bytes / 16
       const uint64_t q_desc = smem_desc(smem_u32(sm + OFF_Q), 16, 1024, kSwizzle128B);
       const uint64_t k_desc = smem_desc(smem_u32(sm + OFF_K), 16, 1024, kSwizzle128B);
@@ -712,7 +717,7 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
     // ------------------------------------------------------------ PV issue
     // A warp of its own: its waits for P would hold up the next tile's QK.
     if (rank == 0) {
-      constexpr uint32_t idesc = C::kTma ? idesc_f16(kRows, 256, false, true) : idesc_half(kRows, 256, false, true);
+      constexpr uint32_t idesc = C::kBf ? idesc_f16(kRows, 256, false, true) : idesc_half(kRows, 256, false, true);
       const uint64_t p_desc = smem_desc(smem_u32(sm + OFF_P), 16, 1024, kSwizzle128B);
       const uint64_t v_desc = smem_desc(smem_u32(sm + OFF_V), C::kVChunkStep, 1024, kSwizzle128B);
       uint32_t g = 0;
@@ -905,7 +910,7 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
             if ((hidden >> (2 * j + 1)) & 1u) b = 0.f;
           }
           rs[j & 1] = add_f32x2(rs[j & 1], pack_f32x2(a, b));
-          if constexpr (C::kTma) {
+          if constexpr (C::kBf) {
             const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
             v[j] = *reinterpret_cast<const uint32_t*>(&h);
             rr = add_f32x2(rr, pack_f32x2(__uint_as_float(v[j] << 16), __uint_as_float(v[j] & 0xFFFF0000u)));
@@ -918,7 +923,7 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
           float a, b;
           unpack_f32x2(add_f32x2(rs[0], rs[1]), a, b);
           l_part += a + b;
-          if constexpr (C::kTma) {
+          if constexpr (C::kBf) {
             unpack_f32x2(rr, a, b);
             r_part += a + b;
           }
@@ -955,7 +960,7 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
       // the row's sum: two threads of each group, each relative to its reference
       xsum[384 * grp + l] = l_part;
       xsum[384 * grp + 128 + l] = m;
-      if constexpr (C::kTma) xsum[384 * grp + 256 + l] = r_part;
+      if constexpr (C::kBf) xsum[384 * grp + 256 + l] = r_part;
       __syncwarp();
       if (lane == 0) mbar_arrive(&c.bars[XS0 + pair]);
       if (!wait_bar(c, XS0 + pair, n_item & 1)) goto fail_soft;
@@ -968,7 +973,7 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
           return (xsum[at + row] + xsum[at + row + 64]) * f0 + (xsum[384 + at + row] + xsum[384 + at + row + 64]) * f1;
         };
         l_row = joined(0);
-        r_row = C::kTma ? joined(256) : l_row;
+        r_row = C::kBf ? joined(256) : l_row;
       }
       // (0: the row sees nothing; a NaN among its scores stays one)
       const float lse = l_row != 0.f ? (m_fin - C::kPShift + log2f(l_row)) * kLn2 : -INFINITY;
@@ -982,7 +987,9 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
       }
       if (!wait_bar(c, PV_DONE0 + ((g - 1) & 1), ((g - 1) >> 1) & 1)) goto fail_soft;
       tc_fence_after();
-      const float s2 = it.slot < 0 ? inv * bmm2 : C::kTma ? inv : inv * (1 << C::kPartShift);
+      const float s2 = it.slot < 0 ? inv * bmm2
+                       : C::kBf    ? inv
+                                   : inv * (1 << (kCache == kF16 ? part_shift(p.kv_dtype) : C::kPartShift));
       // columns of O, V dims 256 hh + 128 grp + [0, 128), 16 at a time
 #pragma unroll 1
       for (int k = 0; k < 8; ++k) {
@@ -991,7 +998,7 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
         tmem_wait_ld();
         if (!row_ok || (kShared && it.slot >= 0 && l_row == 0.f)) continue;  // (nothing seen: the LSE says so)
         const int chunk = 16 * hh + 8 * grp + k;  // of 16 dims
-        if (!kShared && C::kTma && it.slot >= 0) {  // fp32 (part_format)
+        if (!kShared && C::kBf && it.slot >= 0) {  // fp32 (part_format)
 #pragma unroll
           for (int u = 0; u < 4; ++u)
             part_o[part_unit_f32(it.slot, kRows, chunk, u, q)] =
@@ -1012,7 +1019,7 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
           d1 = d0 + 1;
         } else {  // f16, times 2^kPartShift (kShared over bf16: a power of these dims' own, prefix_scale)
           float by = s2;
-          if constexpr (kShared && C::kTma) {
+          if constexpr (kShared && C::kBf) {
             uint32_t most = 0;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
@@ -1204,7 +1211,7 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
 #pragma unroll 2
       for (int r = 0; r < 4; ++r) {
         int e = 0;
-        if (!p.q_fp8 && !C::kTma) {
+        if (!p.q_fp8 && !C::kBf) {
           const uint4 a = unit_of(q0 + r, lane), b = unit_of(q0 + r, 32 + lane),
                       d = unit_of(q0 + r, 64 + (lane & 7));
           uint32_t mb = __vmaxu2(__vmaxu2(max_bits(a), max_bits(b)), max_bits(d));
@@ -1227,7 +1234,7 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
       const long long q0 = first_row(it);
       const float* scales = qscale + (n & 3) * kCtaRows;
       auto as_f16 = [&](const uint4 x, float up) {  // (as bf16 for bf16 MMAs)
-        if constexpr (C::kTma) return p.q_fp8 ? e4m3x8_to_bf16(make_uint2(x.x, x.y)) : x;
+        if constexpr (C::kBf) return p.q_fp8 ? e4m3x8_to_bf16(make_uint2(x.x, x.y)) : x;
         return p.q_fp8 ? e4m3x8_to_f16(make_uint2(x.x, x.y)) : bf16x8_to_f16(x, up);
       };
       const int quad = warp & 3, row = (32 * quad + lane) & 63, part = w >> 2;
@@ -1312,6 +1319,7 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
   tc_fence_before();
   __syncthreads();
   if (tid == 0 && *c.abort) atomicOr(c.status, kStatusTimeout);
+  if (kLate && late) pdl_wait();  // so that the join, which waits for this kernel, follows both
   cluster_sync();  // neither CTA touches the other's memory or TMEM any more
   if (warp == 1) {
     tc_fence_after();
@@ -1374,14 +1382,16 @@ bool encode_rows(CUtensorMap* map, const Problem& p, int chunks) {
 }
 
 template <int kCache, bool kShared>
-cudaError_t launch_one(const Problem& p, const Layout& lay, void* ws, const PrefixSegment* segments, cudaStream_t stream) {
+cudaError_t launch_one(const Problem& p, const Layout& lay, void* ws, const PrefixSegment* segments, int late,
+                       cudaStream_t stream) {
   CUtensorMap tm_k = {}, tm_v = {};
   if (Cfg<kCache>::kTma && !(encode_rows(&tm_k, p, kChunks) && encode_rows(&tm_v, p, 4))) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   const cudaLaunchConfig_t cfg = pair_launch(lay.n_ctas, Cfg<kCache>::kSmemBytes, stream, &attr);
-  return cudaLaunchKernelEx(&cfg, decode_pair_kernel<kCache, kShared>, p, lay, static_cast<char*>(ws), tm_k, tm_v, segments);
+  return cudaLaunchKernelEx(&cfg, decode_pair_kernel<kCache, kShared>, p, lay, static_cast<char*>(ws), tm_k, tm_v, segments,
+                            late);
 }
 
 }  // namespace
@@ -1393,23 +1403,43 @@ cudaError_t decode_pair_setup(int kv_dtype, int sm_count, int* n_pairs) {
 }
 
 cudaError_t launch_decode_pair(const Problem& p, const Layout& lay, void* ws, cudaStream_t stream) {
-  return p.kv_dtype == 2   ? launch_one<kFp4, false>(p, lay, ws, nullptr, stream)
-         : p.kv_dtype == 1 ? launch_one<kE4m3, false>(p, lay, ws, nullptr, stream)
-                           : launch_one<kBf16, false>(p, lay, ws, nullptr, stream);
+  return p.kv_dtype == 2   ? launch_one<kFp4, false>(p, lay, ws, nullptr, 0, stream)
+         : p.kv_dtype == 1 ? launch_one<kE4m3, false>(p, lay, ws, nullptr, 0, stream)
+                           : launch_one<kBf16, false>(p, lay, ws, nullptr, 0, stream);
 }
 
 cudaError_t decode_prefix_setup(int kv_dtype, int sm_count, int* n_pairs) {
-  return kv_dtype == 2   ? setup_one<kFp4, true>(sm_count, n_pairs)
-         : kv_dtype == 1 ? setup_one<kE4m3, true>(sm_count, n_pairs)
-                         : setup_one<kBf16, true>(sm_count, n_pairs);
+  int n = 0;
+  const cudaError_t e = kv_dtype == 0 ? cudaSuccess : setup_one<kF16, true>(sm_count, &n);
+  if (e != cudaSuccess) return e;
+  const cudaError_t f = kv_dtype == 2   ? setup_one<kFp4, true>(sm_count, n_pairs)
+                        : kv_dtype == 1 ? setup_one<kE4m3, true>(sm_count, n_pairs)
+                                        : setup_one<kBf16, true>(sm_count, n_pairs);
+  if (f == cudaSuccess && kv_dtype != 0) *n_pairs = std::min(*n_pairs, n);
+  return f;
 }
 
+// The items of the shared rows that were widened, where the plan widens, then the others'.
 cudaError_t launch_decode_prefix(const Problem& p, const Layout& lay, const PrefixLayout& pl, void* ws,
                                  cudaStream_t stream) {
-  const PrefixSegment* segments = reinterpret_cast<const PrefixSegment*>(static_cast<char*>(ws) + pl.segments);
-  return p.kv_dtype == 2   ? launch_one<kFp4, true>(p, lay, ws, segments, stream)
-         : p.kv_dtype == 1 ? launch_one<kE4m3, true>(p, lay, ws, segments, stream)
-                           : launch_one<kBf16, true>(p, lay, ws, segments, stream);
+  char* base = static_cast<char*>(ws);
+  const PrefixSegment* segments = reinterpret_cast<const PrefixSegment*>(base + pl.segments);
+  if (pl.wide_tiles > 0) {
+    Layout first = lay;
+    first.items = pl.wide_items;
+    first.worker_ranges = pl.wide_ranges;
+    Problem over = p;  // its cache: the widened rows, as pages of a tile
+    over.kv_cache = base + pl.wide_rows;
+    over.num_pages = pl.wide_tiles;
+    over.page_size = kTile;
+    const cudaError_t e =
+        launch_one<kF16, true>(over, first, ws, reinterpret_cast<const PrefixSegment*>(base + pl.wide_segments), 0, stream);
+    if (e != cudaSuccess) return e;
+  }
+  const int late = pl.wide_tiles > 0;
+  return p.kv_dtype == 2   ? launch_one<kFp4, true>(p, lay, ws, segments, late, stream)
+         : p.kv_dtype == 1 ? launch_one<kE4m3, true>(p, lay, ws, segments, late, stream)
+                           : launch_one<kBf16, true>(p, lay, ws, segments, late, stream);
 }
 
 }  // namespace mla

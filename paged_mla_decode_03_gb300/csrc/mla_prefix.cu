@@ -20,6 +20,7 @@
 #include <cuda_fp16.h>
 
 #include "mla_common.cuh"
+#include "mla_fp4.cuh"
 #include "mla_prefix.cuh"
 #include "sm100_ptx.cuh"
 
@@ -32,12 +33,13 @@ constexpr unsigned kAll = 0xffffffffu;
 
 // By request: tokens, first token, rows, prefix group (-1: on its own), first token in its
 // owner, first row group of its owner, own tiles and own segments of the requests before it.  By
-// prefix group: first and last + 1 request, tokens (0: not shared), shared tiles.  By row
-// group: start unit, and the requests of its first and last token.
+// prefix group: first and last + 1 request, tokens (0: not shared), shared tiles, and whether they
+// are widened.  By row group: start unit and place in a list, and the requests of its first and last
+// token.
 struct PrefixScratch {
   int *q, *qs, *len, *group, *tok, *base, *tiles, *count;  // (tiles and count: of all before the end, too)
-  int *lo, *hi, *tokens, *shared;
-  int *start, *first, *last;
+  int *lo, *hi, *tokens, *shared, *wide;
+  int *start, *place, *first, *last;
   __device__ PrefixScratch(char* at, int batch, int groups, int row_groups) {
     q = reinterpret_cast<int*>(at);
     qs = q + batch;
@@ -51,14 +53,16 @@ struct PrefixScratch {
     hi = lo + groups;
     tokens = hi + groups;
     shared = tokens + groups;
-    start = shared + groups;
-    first = start + row_groups + 1;
+    wide = shared + groups;
+    start = wide + groups;
+    place = start + row_groups + 1;
+    first = place + row_groups + 1;
     last = first + row_groups;
   }
 };
 
 struct PrefixShared {
-  int w_scan[3][32], status, most, alone, alone_most, alone_count, any;
+  int w_scan[3][32], status, most, alone, alone_most, alone_count, any, any_wide, total;
   int bound[kPrefixWorkers + 1];
   unsigned cut[8], first[8];
 };
@@ -115,6 +119,8 @@ __device__ __forceinline__ int list_estimate(int total, int most, int count, int
 
 }  // namespace
 
+// kWide: plans that widen (a kernel of its own: the others' calls are 1 us shorter without).
+template <bool kWide>
 __global__ void __launch_bounds__(kPartThreads, 1)
 partition_prefix_kernel(Problem p, PrefixArgs pa, Layout lay, PrefixLayout pl, char* __restrict__ ws) {
   extern __shared__ __align__(16) unsigned char prefix_smem[];
@@ -135,10 +141,8 @@ partition_prefix_kernel(Problem p, PrefixArgs pa, Layout lay, PrefixLayout pl, c
   auto tiles_of = [](int rows) { return (max(rows, 0) + kKvTile - 1) / kKvTile; };
   auto groups_of = [&](int tokens) { return (tokens + per - 1) >> per_shift; };
   if (tid == 0) {
-    sh.status = sh.alone = sh.alone_most = sh.alone_count = sh.any = 0;
-    sh.most = 0;
+    sh.status = sh.alone = sh.alone_most = sh.alone_count = sh.any = sh.any_wide = 0;
   }
-  if (tid < 8) sh.cut[tid] = sh.first[tid] = 0;
   // a warp's first prefix group, read beside the lengths
   const int each = B / G;
   int g_lo = 0, g_hi = 0, g_len = 0;
@@ -222,15 +226,19 @@ partition_prefix_kernel(Problem p, PrefixArgs pa, Layout lay, PrefixLayout pl, c
         const int touched = ((tok + q - 1) >> per_shift) - (tok >> per_shift) + 1;
         saved += groups_of(q) * (c0 + tiles_of(L)) - touched * tiles_of(L - T * kKvTile);
       }
-      saved = (int)__reduce_add_sync(kAll, (unsigned)saved) - groups_of(tokens) * (c0 + T);
+      saved = (int)__reduce_add_sync(kAll, (unsigned)saved) - groups_of(tokens) * c0;
     }
+    const bool wide = kWide && groups_of(tokens) >= kWideRowGroups;
+    saved -= groups_of(tokens) * (wide ? min(T, (kWideOverhead + T) * kWideTenths / 10) : T);
     const bool on = T > 0 && saved > 0;
     if (lane == 0) {
       s.lo[g] = lo;
       s.hi[g] = hi;
       s.tokens[g] = on ? tokens : 0;
       s.shared[g] = T;
+      s.wide[g] = on && wide;
       if (on) sh.any = 1;
+      if (on && wide) sh.any_wide = 1;
     }
     if (on)
       for (int b = lo + lane; b < hi; b += 32) {
@@ -243,10 +251,47 @@ partition_prefix_kernel(Problem p, PrefixArgs pa, Layout lay, PrefixLayout pl, c
 
   // 3. Row groups, their costs and start units; once more with every request on its own where
   // that is the shorter list.
-  int n_rg = 0, W = 0;
+  int n_rg = 0;
   bool room = true;
   auto shared_tiles = [&](int b) { return s.group[b] >= 0 ? s.shared[s.group[b]] : 0; };
   auto first_request = [&](int b) { return s.group[b] >= 0 ? s.lo[s.group[b]] : b; };  // of b's owner
+  // first of the widened tiles of b's owner, -1: none (before they are placed: 0)
+  bool widens = false;
+  auto wide_base = [&](int b) { return kWide && widens && s.group[b] >= 0 ? s.wide[s.group[b]] - 1 : -1; };
+  // cost of row group r in a list, 0: it is not in it
+  auto units = [&](int list, int r) {
+    const int b = s.first[r], wide = wide_base(b);
+    if (list == 1) return wide >= 0 ? kWideOverhead + shared_tiles(b) : 0;
+    const int t = (wide < 0 ? shared_tiles(b) : 0) + s.tiles[s.last[r] + 1] - s.tiles[b];
+    return t > 0 ? c0 + t : 0;
+  };
+  // start units of a list's row groups, and each one's place among them
+  int W = 0, members = 0;
+  auto scan_list = [&](int list) {
+    if (tid == 0) sh.most = sh.total = 0;
+    if (tid < 8) sh.cut[tid] = sh.first[tid] = 0;
+    W = members = 0;
+    __syncthreads();
+    for (int at = 0; at < n_rg; at += blockDim.x) {
+      const int r = at + tid;
+      int v[2] = {r < n_rg ? units(list, r) : 0, 0}, before[2], total[2];
+      v[1] = v[0] > 0 ? 1 : 0;
+      const int most = __reduce_max_sync(kAll, v[0]);
+      if (lane == 0 && most > 0) atomicMax(&sh.most, most);
+      block_scan(sh, v, before, total);
+      if (r < n_rg) {
+        s.start[r] = W + before[0];
+        s.place[r] = members + before[1];
+      }
+      W += total[0];
+      members += total[1];
+    }
+    if (tid == 0) {
+      s.start[n_rg] = W;
+      s.place[n_rg] = members;
+    }
+    __syncthreads();
+  };
   for (int pass = 0; pass < 2; ++pass) {
     int rg = 0, tiles = 0, count = 0;
     for (int at = 0; at < B; at += blockDim.x) {
@@ -272,7 +317,6 @@ partition_prefix_kernel(Problem p, PrefixArgs pa, Layout lay, PrefixLayout pl, c
     if (tid == 0) {
       s.tiles[B] = tiles;
       s.count[B] = count;
-      sh.most = 0;
     }
     n_rg = rg;
     // (malformed offsets may let requests overlap: more row groups than the plan has room for)
@@ -290,21 +334,24 @@ partition_prefix_kernel(Problem p, PrefixArgs pa, Layout lay, PrefixLayout pl, c
           if (min((k + 1) << per_shift, tokens) <= tok + q) s.last[base + k] = b;
       }
     __syncthreads();
-    W = 0;
-    for (int at = 0; at < n_rg; at += blockDim.x) {
-      const int r = at + tid;
-      int v[1] = {0}, before[1], total[1];
-      if (r < n_rg) v[0] = c0 + shared_tiles(s.first[r]) + s.tiles[s.last[r] + 1] - s.tiles[s.first[r]];
-      const int most = __reduce_max_sync(kAll, v[0]);
-      if (lane == 0 && most > 0) atomicMax(&sh.most, most);
-      block_scan(sh, v, before, total);
-      if (r < n_rg) s.start[r] = W + before[0];
-      W += total[0];
-    }
-    if (tid == 0) s.start[n_rg] = W;
-    __syncthreads();
+    scan_list(0);
     if (pass == 1 || !sh.any || !room) break;
-    if (list_estimate(W, sh.most, n_rg, n) <= list_estimate(sh.alone, sh.alone_most, sh.alone_count, n)) break;
+    const int alone = list_estimate(sh.alone, sh.alone_most, sh.alone_count, n);
+    const int shared = list_estimate(W, sh.most, members, n);
+    if (kWide && sh.any_wide) {  // both lists' units, the second one's first tiles, and the copy
+      widens = true;
+      int other = 0;
+      for (int r = tid; r < n_rg; r += blockDim.x) other += units(0, r) + units(1, r) * kWideTenths / 10;
+      other = (int)__reduce_add_sync(kAll, (unsigned)other);
+      if (lane == 0) atomicAdd(&sh.total, other);
+      __syncthreads();
+      widens = sh.total / n + 3 * (int)kCutTiles < min(alone, shared);
+      if (widens) {
+        scan_list(0);
+        break;
+      }
+    }
+    if (shared <= alone) break;
     __syncthreads();
     for (int b = tid; b < B; b += blockDim.x) {
       s.group[b] = -1;
@@ -312,103 +359,151 @@ partition_prefix_kernel(Problem p, PrefixArgs pa, Layout lay, PrefixLayout pl, c
     }
     __syncthreads();
   }
-  const int n_eff = max(1, min(n, W / (int)kMinUnits));
-  const bool uncut = partition_uncut(true, n_rg, n, sh.most, W);
 
-  // 4. Worker boundaries, and which of them cut a row group (past its overhead).
-  const int quot = W / n_eff, rest = W % n_eff;
-  auto bound_of = [&](int w) {
-    return uncut ? w < n_rg ? s.start[w] : W : w >= n_eff ? W : w * quot + w * rest / n_eff;
-  };
-  for (int w = tid; w <= n; w += blockDim.x) {
-    const int at = bound_of(w);
-    sh.bound[w] = at;
-    if (w == 0 || at >= W) continue;
-    const int from = s.start[last_upto(s.start, n_rg, at)] + c0;  // unit of the row group's first tile
-    if (at <= from) continue;
-    atomicOr(reinterpret_cast<int*>(&sh.cut[w >> 5]), (int)(1u << (w & 31)));
-    if (bound_of(w - 1) <= from) atomicOr(reinterpret_cast<int*>(&sh.first[w >> 5]), (int)(1u << (w & 31)));
+  // the groups' widened rows, one after another
+  if constexpr (kWide) {
+    PrefixWide* of = reinterpret_cast<PrefixWide*>(ws + pl.wide_groups);
+    int all = 0;
+    for (int at = 0; at < G; at += blockDim.x) {
+      const int g = at + tid;
+      int v[1] = {widens && g < G && s.wide[g] ? s.shared[g] : 0}, before[1], total[1];
+      block_scan(sh, v, before, total);
+      if (g < G) {
+        int b = s.lo[g];
+        while (v[0] > 0 && b + 1 < s.hi[g] && (s.len[b] <= 0 || s.q[b] <= 0)) ++b;
+        of[g] = PrefixWide{all + before[0], v[0], b, 0};
+        if (widens) s.wide[g] = v[0] > 0 ? 1 + all + before[0] : 0;
+      }
+      all += total[0];
+    }
+    if (tid == 0) of[G] = PrefixWide{all, 0, 0, 0};
+    __syncthreads();
   }
-  __syncthreads();
 
-  // 5. Items, segments, entries of the join, worker ranges.
-  const int n_items = n_rg + bits_under(sh.cut, 255);
-  const bool fits = room && n_items <= lay.max_items && n_items - n_rg + bits_under(sh.first, 255) <= lay.max_partials;
+  // 4. The lists: row groups and what they walk outside widened rows, and these.
+  int n_items = 0;
+  bool fits = room;
   auto owner_tokens = [&](int b) { return s.group[b] >= 0 ? s.tokens[s.group[b]] : s.q[b]; };
-  auto emit = [&](int at, int rg, int t0, int t1, int slot) {
-    const int b = s.first[rg], o = first_request(b);
-    WorkItem it;
-    it.b = o;
-    it.g = rg - s.base[o];
-    it.kv_begin = t0 * kKvTile;
-    it.kv_end = t1 * kKvTile;
-    it.slot = slot;
-    it.q_len = owner_tokens(b);
-    it.seq_len = (shared_tiles(b) > 0 ? 1 : 0) + s.count[s.last[rg] + 1] - s.count[b];
-    it.q_start = s.qs[o];
-    it.comb = rg;
-    it.mask_base = 0;
-    items[at] = it;
-  };
-  if (fits) {
-    for (int rg = tid; rg < n_rg; rg += blockDim.x) {
-      const int from = s.start[rg] + c0, end = s.start[rg + 1];
-      const int pb = sh.bound[0] > from ? 0 : last_upto(sh.bound, n + 1, from) + 1;  // boundaries up to the first tile
-      int last = pb;  // past the row group's last cut
-      while (last < n && bit_at(sh.cut, last) && sh.bound[last] < end) ++last;
-      const bool split = last > pb;
-      const int before = bits_under(sh.cut, pb), slot = before + bits_under(sh.first, pb);
-      emit(rg + before, rg, 0, (split ? sh.bound[pb] : end) - from, split ? slot : -1);
-      const int b = s.first[rg], o = first_request(b), k = rg - s.base[o], T = shared_tiles(b);
-      PrefixEntry e = {};
-      e.row0 = ((long long)s.qs[o] + (k << per_shift)) * H;
-      e.rows = split ? min(per, owner_tokens(b) - (k << per_shift)) * H : 0;
-      e.slot = slot;
-      e.count = 1 + last - pb;
-      entries[rg] = e;
-      if (T > 0) {
-        int src = o;  // the owner's first request that has rows: its table is read
-        while (src + 1 < s.hi[s.group[b]] && (s.len[src] <= 0 || s.q[src] <= 0)) ++src;
-        segments[(size_t)rg * kPrefixSegments] = PrefixSegment{0, src, 0, T * kKvTile, 0, kPrefixRows, kPrefixNoMask, 0};
-      }
+  for (int list = 0; list < (kWide ? 2 : 1); ++list) {
+    const int over = list ? kWideOverhead : c0;
+    WorkItem* to = list ? reinterpret_cast<WorkItem*>(ws + pl.wide_items) : items;
+    int* ranges = list ? reinterpret_cast<int*>(ws + pl.wide_ranges) : worker_begin;
+    if (list == 1) scan_list(1);  // (the first one's is there)
+    const int n_eff = max(1, min(n, W / (int)kMinUnits));
+    const bool uncut = partition_uncut(true, members, n, sh.most, W);
+    // worker boundaries, and which of them cut a row group (past its overhead)
+    const int quot = W / n_eff, rest = W % n_eff;
+    if (uncut) {  // worker w's range starts where row group w of the list does
+      for (int r = tid; r < n_rg; r += blockDim.x)
+        if (s.place[r + 1] > s.place[r]) sh.bound[s.place[r]] = s.start[r];
+      for (int w = members + tid; w <= n; w += blockDim.x) sh.bound[w] = W;
+    } else {
+      for (int w = tid; w <= n; w += blockDim.x) sh.bound[w] = w >= n_eff ? W : w * quot + w * rest / n_eff;
     }
-    // each request's own rows, a segment in every row group that it has query rows in
-    for (int b = tid; b < B; b += blockDim.x) {
-      const int q = s.q[b], tok = s.tok[b], T = shared_tiles(b), L = s.len[b];
-      if (q <= 0 || L <= T * kKvTile) continue;
-      const int base = s.base[first_request(b)];
-      for (int k = tok >> per_shift; k <= (tok + q - 1) >> per_shift; ++k) {
-        const int f = s.first[base + k], first = k << per_shift, z = (T > 0 ? 1 : 0) + s.count[b] - s.count[f];
-        if (z >= kPrefixSegments) continue;  // (never)
-        segments[(size_t)(base + k) * kPrefixSegments + z] =
-            PrefixSegment{T + s.tiles[b] - s.tiles[f], b, T * kKvTile, L, max(0, tok - first) * H,
-                          min(per, tok + q - first) * H, p.causal ? L - q - tok : kPrefixNoMask, 0};
-      }
-    }
+    __syncthreads();
+    // (of row groups that start at the same unit the last is the one that has units)
     for (int w = tid; w <= n; w += blockDim.x) {
-      if (sh.bound[w] >= W) {
-        worker_begin[w] = n_items;
-        continue;
-      }
-      const int rg = last_upto(s.start, n_rg, sh.bound[w]);
-      const bool cuts = bit_at(sh.cut, w);
-      const int rank = bits_under(sh.cut, w);
-      // (a boundary inside a row group's overhead, or at its start, leaves the row group whole)
-      worker_begin[w] = rg + rank + (cuts ? 1 : 0);
-      if (!cuts) continue;
-      const int from = s.start[rg] + c0, tiles = s.start[rg + 1] - from;
-      emit(rg + 1 + rank, rg, sh.bound[w] - from, w + 1 <= n ? min(tiles, sh.bound[w + 1] - from) : tiles,
-           rank + bits_under(sh.first, w + 1));
+      const int at = sh.bound[w];
+      if (w == 0 || at >= W) continue;
+      const int from = s.start[last_upto(s.start, n_rg, at)] + over;  // unit of the row group's first tile
+      if (at <= from) continue;
+      atomicOr(reinterpret_cast<int*>(&sh.cut[w >> 5]), (int)(1u << (w & 31)));
+      if (sh.bound[w - 1] <= from) atomicOr(reinterpret_cast<int*>(&sh.first[w >> 5]), (int)(1u << (w & 31)));
     }
-  } else {
-    for (int w = tid; w <= n; w += blockDim.x) worker_begin[w] = 0;
+    __syncthreads();
+    const int n_list = members + bits_under(sh.cut, 255);
+    // a plan that widens has a slot for every item, another one for those of cut row groups
+    const bool enough = n_list <= lay.max_items &&
+                        (kWide || n_list - members + bits_under(sh.first, 255) <= lay.max_partials);
+    fits = fits && enough;
+    if (list == 0) n_items = n_list;
+    auto emit = [&](int at, int rg, int t0, int t1, int slot) {
+      const int b = s.first[rg], o = first_request(b), shared = shared_tiles(b), wide = wide_base(b);
+      WorkItem it;
+      it.b = o;
+      it.g = rg - s.base[o];
+      it.kv_begin = t0 * kKvTile;
+      it.kv_end = t1 * kKvTile;
+      it.slot = slot;
+      it.q_len = owner_tokens(b);
+      it.seq_len = list ? 1 : (shared > 0 && wide < 0 ? 1 : 0) + s.count[s.last[rg] + 1] - s.count[b];
+      it.q_start = s.qs[o];
+      it.comb = rg;
+      it.mask_base = 0;
+      to[at] = it;
+    };
+    if (fits) {
+      for (int rg = tid; rg < n_rg; rg += blockDim.x) {
+        const bool member = s.place[rg + 1] > s.place[rg];
+        const int from = s.start[rg] + over, end = s.start[rg + 1];
+        const int b = s.first[rg], o = first_request(b), k = rg - s.base[o], T = shared_tiles(b), wide = wide_base(b);
+        PrefixEntry* e = entries + rg;
+        if (list == 0) {
+          e->row0 = ((long long)s.qs[o] + (k << per_shift)) * H;
+          e->rows = e->count[0] = e->count[1] = 0;
+        }
+        if (!member) continue;
+        const int pb = sh.bound[0] > from ? 0 : last_upto(sh.bound, n + 1, from) + 1;  // boundaries up to the first tile
+        int last = pb;  // past the row group's last cut
+        while (last < n && bit_at(sh.cut, last) && sh.bound[last] < end) ++last;
+        const bool split = last > pb, partial = split || wide >= 0;
+        const int before = bits_under(sh.cut, pb), at = s.place[rg] + before;
+        const int slot = kWide ? list * lay.max_items + at : before + bits_under(sh.first, pb);
+        emit(at, rg, 0, (split ? sh.bound[pb] : end) - from, partial ? slot : -1);
+        if (partial) {
+          e->rows = min(per, owner_tokens(b) - (k << per_shift)) * H;
+          e->slot[list] = slot;
+          e->count[list] = 1 + last - pb;
+        }
+        if (list == 1) {
+          reinterpret_cast<PrefixSegment*>(ws + pl.wide_segments)[(size_t)rg * kPrefixSegments] =
+              PrefixSegment{0, 0, wide * kKvTile, (wide + T) * kKvTile, 0, kPrefixRows, kPrefixNoMask, 0};
+        } else if (T > 0 && wide < 0) {
+          int src = o;  // the owner's first request that has rows: its table is read
+          while (src + 1 < s.hi[s.group[b]] && (s.len[src] <= 0 || s.q[src] <= 0)) ++src;
+          segments[(size_t)rg * kPrefixSegments] = PrefixSegment{0, src, 0, T * kKvTile, 0, kPrefixRows, kPrefixNoMask, 0};
+        }
+      }
+      // each request's own rows, a segment in every row group that it has query rows in
+      if (list == 0)
+        for (int b = tid; b < B; b += blockDim.x) {
+          const int q = s.q[b], tok = s.tok[b], T = shared_tiles(b), L = s.len[b], in_list = wide_base(b) < 0 ? T : 0;
+          if (q <= 0 || L <= T * kKvTile) continue;
+          const int base = s.base[first_request(b)];
+          for (int k = tok >> per_shift; k <= (tok + q - 1) >> per_shift; ++k) {
+            const int f = s.first[base + k], first = k << per_shift, z = (in_list > 0 ? 1 : 0) + s.count[b] - s.count[f];
+            if (z >= kPrefixSegments) continue;  // (never)
+            segments[(size_t)(base + k) * kPrefixSegments + z] =
+                PrefixSegment{in_list + s.tiles[b] - s.tiles[f], b, T * kKvTile, L, max(0, tok - first) * H,
+                              min(per, tok + q - first) * H, p.causal ? L - q - tok : kPrefixNoMask, 0};
+          }
+        }
+      for (int w = tid; w <= n; w += blockDim.x) {
+        if (sh.bound[w] >= W) {
+          ranges[w] = n_list;
+          continue;
+        }
+        const int rg = last_upto(s.start, n_rg, sh.bound[w]);
+        const bool cuts = bit_at(sh.cut, w);
+        const int rank = bits_under(sh.cut, w), at = s.place[rg] + rank;
+        // (a boundary inside a row group's overhead, or at its start, leaves the row group whole)
+        ranges[w] = at + (cuts ? 1 : 0);
+        if (!cuts) continue;
+        const int from = s.start[rg] + over, tiles = s.start[rg + 1] - from;
+        emit(at + 1, rg, sh.bound[w] - from, w + 1 <= n ? min(tiles, sh.bound[w + 1] - from) : tiles,
+             kWide ? list * lay.max_items + at + 1 : rank + bits_under(sh.first, w + 1));
+      }
+    } else {
+      for (int w = tid; w <= n; w += blockDim.x) worker_begin[w] = ranges[w] = 0;
+    }
+    __syncthreads();
   }
   if (tid == 0) {
     hdr[kHdrStatus] = fits ? sh.status : sh.status | kStatusCapacity;
     hdr[kHdrNumItems] = fits ? n_items : 0;
     hdr[kHdrWorkCounter] = 0;
     hdr[kHdrNumCombine] = fits ? n_rg : 0;
-    hdr[kHdrChunkTiles] = min(W, 1 << 30);
+    hdr[kHdrChunkTiles] = 0;
     hdr[kHdrCombineCounter] = 0;
   }
 }
@@ -426,6 +521,10 @@ inline int partition_prefix_threads(const Problem& p, const PrefixArgs& pa, cons
 // that sees none of its tiles has an LSE of -inf and no O, and is not read.  The decode
 // kernel has ended before a partial is.
 constexpr int kJoinThreads = 256, kJoinRows = 8, kJoinBatch = 4;
+
+__device__ __forceinline__ int slot_of(const PrefixEntry& e, int k) {
+  return k < e.count[0] ? e.slot[0] + k : e.slot[1] + k - e.count[0];
+}
 
 // kScaled: over bf16 (see prefix_scale_offset).
 template <bool kScaled>
@@ -447,19 +546,20 @@ join_prefix_kernel(Problem p, Layout lay, PrefixLayout pl, char* __restrict__ ws
     float m = -INFINITY, sum = 0.f, acc[16];
 #pragma unroll
     for (int k = 0; k < 16; ++k) acc[k] = 0.f;
-    for (int k0 = 0; k0 < e.count; k0 += kJoinBatch) {
+    const int count = e.count[0] + e.count[1];
+    for (int k0 = 0; k0 < count; k0 += kJoinBatch) {
       uint4 x[kJoinBatch][2];
       float l[kJoinBatch];
       int down[kJoinBatch];
 #pragma unroll
       for (int u = 0; u < kJoinBatch; ++u)
-        l[u] = k0 + u < e.count ? part_lse[(size_t)(e.slot + k0 + u) * kPrefixRows + r] : -INFINITY;
+        l[u] = k0 + u < count ? part_lse[(size_t)slot_of(e, k0 + u) * kPrefixRows + r] : -INFINITY;
 #pragma unroll
       for (int u = 0; u < kJoinBatch; ++u) {
         x[u][0] = x[u][1] = make_uint4(0, 0, 0, 0);
         down[u] = kScaled ? 0 : part_shift(p.kv_dtype);
         if (l[u] != -INFINITY) {
-          const size_t slot = e.slot + k0 + u;
+          const size_t slot = slot_of(e, k0 + u);
           x[u][0] = part_o[part_unit(slot, kPrefixRows, t, 0, r)];
           x[u][1] = part_o[part_unit(slot, kPrefixRows, t, 1, r)];
           if constexpr (kScaled) down[u] = part_scale[(slot * 32 + t) * kPrefixRows + r];
@@ -505,16 +605,92 @@ join_prefix_kernel(Problem p, Layout lay, PrefixLayout pl, char* __restrict__ ws
 }
 
 cudaError_t prefix_setup() {
-  return cudaFuncSetAttribute(partition_prefix_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)kPartitionSmemMax);
+  const cudaError_t e = cudaFuncSetAttribute(partition_prefix_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)kPartitionSmemMax);
+  return e != cudaSuccess ? e
+                          : cudaFuncSetAttribute(partition_prefix_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 (int)kPartitionSmemMax);
 }
 
 cudaError_t launch_partition_prefix(const Problem& p, const PrefixArgs& pa, const Layout& lay, const PrefixLayout& pl,
                                     void* ws, cudaStream_t stream) {
   const int threads = partition_prefix_threads(p, pa, lay);
-  partition_prefix_kernel<<<1, threads, pl.scratch_in_smem ? pl.scratch_bytes : 0, stream>>>(
-      p, pa, lay, pl, static_cast<char*>(ws));
+  auto kernel = pl.wide_tiles > 0 ? partition_prefix_kernel<true> : partition_prefix_kernel<false>;
+  kernel<<<1, threads, pl.scratch_in_smem ? pl.scratch_bytes : 0, stream>>>(p, pa, lay, pl, static_cast<char*>(ws));
   return cudaGetLastError();
+}
+
+// The shared rows of groups that are widened, once, to f16 (exact).  A block takes a tile of 64
+// rows, a thread eight dims of a row at a time: reads and writes are contiguous across a warp.
+// What bounds it is the bytes: 65536 rows of 4 bits, 97 MB read and written.
+constexpr int kWidenThreads = 256;
+
+template <bool kFp4>
+__global__ void __launch_bounds__(kWidenThreads)
+widen_prefix_kernel(Problem p, int groups, PrefixLayout pl, char* __restrict__ ws) {
+  ptx::pdl_launch_dependents();
+  ptx::pdl_wait();
+  const PrefixWide* of = reinterpret_cast<const PrefixWide*>(ws + pl.wide_groups);
+  uint4* rows = reinterpret_cast<uint4*>(ws + pl.wide_rows);
+  int* status = reinterpret_cast<int*>(ws) + kHdrStatus;
+  const int total = min(of[groups].base, pl.wide_tiles), ps = p.page_size, shift = ps == 64 ? 6 : 5;
+  for (int t = blockIdx.x; t < total; t += gridDim.x) {
+    int lo = 0, hi = groups;  // the last group whose tiles start at or before t
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (of[mid].base <= t) lo = mid; else hi = mid;
+    }
+    const int tile = t - of[lo].base;
+    const int* table = p.block_tables + (size_t)of[lo].b * p.max_pages;
+    constexpr int kUnits = kQkDim / 8;  // of a row
+#pragma unroll 6
+    for (int i = threadIdx.x; i < kKvTile * kUnits; i += kWidenThreads) {
+      const int r = i / kUnits, u = i - r * kUnits, row = tile * kKvTile + r, in = row & (ps - 1);
+      const int id = table[row >> shift];
+      uint32_t h[4] = {0, 0, 0, 0};
+      if (id >= 0 && (long long)id < p.num_pages) {
+        if constexpr (kFp4) {
+          const unsigned char* page = static_cast<const unsigned char*>(p.kv_cache) + (size_t)id * ps * kFp4RowBytes;
+          ptx::e2m1x8_to_f16x2(reinterpret_cast<const uint32_t*>(page + in * kFp4CodeBytes)[u], h);
+          const uint32_t code = page[(size_t)ps * kFp4CodeBytes + in * kFp4ScaleBytes + (u >> 1)];
+          uint32_t two;
+          asm("{\n .reg .b16 lo;\n mov.b32 {lo, _}, %1;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n}" : "=r"(two) : "r"(code | code << 8));
+          const __half2 scale = *reinterpret_cast<const __half2*>(&two);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&h[k]), scale);
+            h[k] = *reinterpret_cast<const uint32_t*>(&v);
+          }
+        } else {
+          const unsigned char* at = static_cast<const unsigned char*>(p.kv_cache) + ((size_t)id * ps + in) * kQkDim;
+          const uint2 c = reinterpret_cast<const uint2*>(at)[u];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            asm("{\n .reg .b16 lo;\n mov.b32 {lo, _}, %1;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n}"
+                : "=r"(h[k])
+                : "r"((k < 2 ? c.x : c.y) >> (16 * (k & 1))));
+        }
+      } else if (u == 0) {
+        atomicOr(status, kStatusPage);
+      }
+      rows[((size_t)t * kKvTile + r) * kUnits + u] = make_uint4(h[0], h[1], h[2], h[3]);
+    }
+  }
+}
+
+cudaError_t launch_widen_prefix(const Problem& p, int groups, const PrefixLayout& pl, void* ws, int sm_count,
+                                cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(std::min(pl.wide_tiles, 4 * sm_count), 1, 1);
+  cfg.blockDim = dim3(kWidenThreads, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, p.kv_dtype == kKvFp4 ? widen_prefix_kernel<true> : widen_prefix_kernel<false>, p, groups, pl,
+                            static_cast<char*>(ws));
 }
 
 cudaError_t launch_join_prefix(const Problem& p, const Layout& lay, const PrefixLayout& pl, void* ws, int sm_count,

@@ -40,14 +40,33 @@ struct PrefixSegment {
 };
 constexpr int kPrefixNoMask = 1 << 30;  // `mask` of a segment that is seen whole
 
+// Widening.  Over 4 bits and e4m3 a tile's time goes into its conversion to f16 (1.25 and 1.35 us,
+// where rows that come by TMA take 0.88).  Where four row groups and more walk the same shared rows
+// these are widened once, into the workspace, and walked there, by a list of items of its
+// own; the row groups' own rows stay in the first list, and all their query rows are joined.
+// (32 x 128 heads over 65536 rows of 4 bits: 568 us a call without.  Below four the copy, its launch and
+// the join take what it saves.)
+constexpr int kWideRowGroups = 4;
+constexpr long long kWideBytes = 1LL << 30;  // of widened rows at most
+constexpr int kWideOverhead = 8;             // of an item over them, in their tiles
+constexpr int kWideTenths = 7;               // one of their tiles, in tenths of another's
+
+// A prefix group's widened rows: tiles [base, base + tiles) from request b's table; the entry
+// past the last group has the number of all in `base`.
+struct PrefixWide {
+  int base, tiles, b, pad;
+};
+
 // The items of a plan with prefix groups: g is the row group of its owner's q_len tokens from
 // q_start on, [kv_begin, kv_end) its tiles times 64, comb its number among all row
 // groups and seq_len its segments.
 
-// A row group that is cut: its query rows from row0 of the output on (0: uncut) and its partials.
+// A row group that is joined: its query rows from row0 of the output on (0: it is not) and its
+// partials of either list.
 struct PrefixEntry {
   long long row0;
-  int rows, slot, count, pad;
+  int rows, pad;
+  int slot[2], count[2];
 };
 
 // The regions of the workspace beside those that the decode kernel knows (Layout).
@@ -57,6 +76,10 @@ struct PrefixLayout {
   size_t scratch;   // the partitioner's, where shared memory does not hold it
   size_t scratch_bytes;
   int scratch_in_smem;
+  // plans that widen (wide_tiles > 0: tiles of widened rows): the second list, its row groups'
+  // one segment each (kPrefixSegments apart), PrefixWide[groups + 1], f16 rows of 576
+  int wide_tiles;
+  size_t wide_items, wide_ranges, wide_segments, wide_groups, wide_rows;
 };
 
 // Partials are f16, laid out as part_unit says: over 4 bits and e4m3 times 2^part_shift; over
@@ -77,7 +100,7 @@ __host__ __device__ inline int prefix_scale(unsigned max_bits) {
 
 // Partitioner scratch: by request, prefix group and row group.
 __host__ __device__ inline size_t prefix_scratch_bytes(long long batch, long long groups, long long row_groups) {
-  return align_up(sizeof(int) * (size_t)(8 * batch + 2 + 4 * groups + 3 * row_groups + 1), 16);
+  return align_up(sizeof(int) * (size_t)(8 * batch + 2 + 5 * groups + 4 * row_groups + 2), 16);
 }
 
 // The workspace of a plan with `groups` prefix groups; false: too large a plan.
@@ -98,7 +121,14 @@ inline bool make_prefix_layout(long long batch, long long heads, long long max_q
   lay->n_ctas = 2 * n_workers;
   lay->max_groups = (int)rg;
   lay->max_items = (int)items;
-  lay->max_partials = (int)(items < 2LL * n_workers ? items : 2LL * n_workers);
+  // widening pays for four row groups a prefix group on the average, and has its room
+  const long long tokens = packed ? max_total_q : batch * max_q;
+  const long long tiles = groups * ((max_seq_len + kKvTile - 1) / kKvTile);
+  const bool wide = kv_dtype != 0 && ceil_to(tokens * heads, R) >= kWideRowGroups * groups &&
+                    tiles * kKvTile * 2 * kQkDim <= kWideBytes;
+  pre->wide_tiles = wide ? (int)tiles : 0;
+  // cut row groups have partials, all of those with widened rows
+  lay->max_partials = (int)(wide ? 2 * items : items < 2LL * n_workers ? items : 2LL * n_workers);
   lay->max_combine = 0;
   size_t off = header;
   auto take = [&off](size_t bytes) {
@@ -121,6 +151,14 @@ inline bool make_prefix_layout(long long batch, long long heads, long long max_q
   lay->part_lse = take(sizeof(float) * (size_t)R * (size_t)lay->max_partials);
   if (kv_dtype == 0) take(32 * (size_t)R * (size_t)lay->max_partials);  // (prefix_scale_offset)
   lay->comb_done = take(sizeof(int));
+  pre->wide_items = pre->wide_ranges = pre->wide_segments = pre->wide_groups = pre->wide_rows = off;
+  if (wide) {
+    pre->wide_items = take(sizeof(WorkItem) * (size_t)items);
+    pre->wide_ranges = take(sizeof(int) * (size_t)(n_workers + 1));
+    pre->wide_segments = take(sizeof(PrefixSegment) * (size_t)(kPrefixSegments * rg));
+    pre->wide_groups = take(sizeof(PrefixWide) * (size_t)(groups + 1));
+    pre->wide_rows = take((size_t)tiles * kKvTile * 2 * kQkDim);
+  }
   lay->total = off;
   return true;
 }

@@ -48,7 +48,8 @@ int main(int argc, char** argv) {
   mla::PrefixLayout pl{};
   if (!mla::make_prefix_layout(B, H, max_q, packed, total_q, max_seq_len, kv_dtype, G, n_workers, sizeof(int) * mla::kHdrWords, &lay, &pl))
     return 3;
-  const size_t starts[] = {lay.items, lay.worker_ranges, pl.entries, pl.segments, lay.part_o, lay.part_lse, lay.total};
+  const size_t starts[] = {lay.items, lay.worker_ranges, pl.entries, pl.segments, lay.part_o, lay.part_lse, lay.comb_done, pl.wide_items,
+                           pl.wide_ranges, pl.wide_segments, pl.wide_groups, pl.wide_rows, lay.total};
   for (size_t i = 0; i < sizeof(starts) / sizeof(starts[0]); ++i)
     if (starts[i] % 256 || (i > 0 && starts[i] < starts[i - 1])) return 5;
   if (pl.segments + sizeof(mla::PrefixSegment) * mla::kPrefixSegments * (size_t)lay.max_groups > lay.part_o) return 5;
@@ -56,7 +57,18 @@ int main(int argc, char** argv) {
     pl.scratch_in_smem = 0;
     pl.scratch = lay.part_o;
   }
-  const size_t used = lay.part_o + (global_scratch ? pl.scratch_bytes : 0);  // (no partial is touched here)
+  if (pl.wide_tiles > 0) {
+    if (pl.wide_segments + sizeof(mla::PrefixSegment) * mla::kPrefixSegments * (size_t)lay.max_groups > pl.wide_groups ||
+        pl.wide_groups + sizeof(mla::PrefixWide) * (size_t)(G + 1) > pl.wide_rows ||
+        pl.wide_rows + (size_t)pl.wide_tiles * mla::kKvTile * 1152 > lay.total)
+      return 5;
+    // (no partial is touched here: the second list right behind the first)
+    const size_t back = pl.wide_items - lay.part_o;
+    for (size_t* at : {&pl.wide_items, &pl.wide_ranges, &pl.wide_segments, &pl.wide_groups, &pl.wide_rows}) *at -= back;
+  }
+  const size_t end = pl.wide_tiles > 0 ? pl.wide_rows : lay.part_o;
+  if (global_scratch) pl.scratch = end;
+  const size_t used = end + (global_scratch ? pl.scratch_bytes : 0);
   std::vector<unsigned char> ws(used, 0xAB);
   std::vector<unsigned char> scratch(pl.scratch_in_smem ? pl.scratch_bytes : 16, 0xCD);
   g_scratch = scratch.data();
@@ -88,7 +100,8 @@ int main(int argc, char** argv) {
   for (int t = 0; t < threads; ++t)
     th.emplace_back([&, t] {
       threadIdx.x = t;
-      mla::partition_prefix_kernel(p, pa, lay, pl, reinterpret_cast<char*>(ws.data()));
+      (pl.wide_tiles > 0 ? mla::partition_prefix_kernel<true> : mla::partition_prefix_kernel<false>)(
+          p, pa, lay, pl, reinterpret_cast<char*>(ws.data()));
     });
   for (auto& x : th) x.join();
   const int* hdr = reinterpret_cast<const int*>(ws.data());
@@ -104,12 +117,29 @@ int main(int argc, char** argv) {
   std::fprintf(o, "\n");
   const mla::PrefixEntry* e = reinterpret_cast<const mla::PrefixEntry*>(ws.data() + pl.entries);
   for (int i = 0; i < hdr[mla::kHdrNumCombine]; ++i)
-    std::fprintf(o, "%lld %d %d %d ", e[i].row0, e[i].rows, e[i].slot, e[i].count);
+    std::fprintf(o, "%lld %d %d %d %d %d ", e[i].row0, e[i].rows, e[i].slot[0], e[i].count[0], e[i].slot[1], e[i].count[1]);
   std::fprintf(o, "\n");
   const mla::PrefixSegment* sg = reinterpret_cast<const mla::PrefixSegment*>(ws.data() + pl.segments);
   for (int i = 0; i < hdr[mla::kHdrNumCombine] * mla::kPrefixSegments; ++i)
     std::fprintf(o, "%d %d %d %d %d %d %d ", sg[i].tile0, sg[i].b, sg[i].row0, sg[i].end, sg[i].q_lo, sg[i].q_hi, sg[i].mask);
   std::fprintf(o, "\n");
+  const bool wide = pl.wide_tiles > 0;
+  const int* wr = reinterpret_cast<const int*>(ws.data() + pl.wide_ranges);
+  const int n_wide = wide ? wr[n_workers] : 0;
+  const int* wi = reinterpret_cast<const int*>(ws.data() + pl.wide_items);
+  for (int i = 0; i < n_wide * 10; ++i) std::fprintf(o, "%d ", wi[i]);
+  std::fprintf(o, "\n");
+  for (int i = 0; wide && i <= n_workers; ++i) std::fprintf(o, "%d ", wr[i]);
+  std::fprintf(o, "\n");
+  const mla::PrefixSegment* wsg = reinterpret_cast<const mla::PrefixSegment*>(ws.data() + pl.wide_segments);
+  for (int i = 0; i < n_wide; ++i) {  // by item: its row group's one segment
+    const mla::PrefixSegment& z = wsg[(size_t)wi[10 * i + 8] * mla::kPrefixSegments];
+    std::fprintf(o, "%d %d %d %d %d %d %d ", z.tile0, z.b, z.row0, z.end, z.q_lo, z.q_hi, z.mask);
+  }
+  std::fprintf(o, "\n");
+  const mla::PrefixWide* wg = reinterpret_cast<const mla::PrefixWide*>(ws.data() + pl.wide_groups);
+  for (int i = 0; wide && i <= G; ++i) std::fprintf(o, "%d %d %d ", wg[i].base, wg[i].tiles, wg[i].b);
+  std::fprintf(o, "\n%d\n", pl.wide_tiles);
   std::fclose(o);
   return 0;
 }

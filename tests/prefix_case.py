@@ -4,7 +4,7 @@ A page that the shared rows end in is each request's own, with the same rows in 
 import torch
 
 import paged_mla_decode_03_gb300 as mla
-from attention_ref import Case, poison
+from attention_ref import Case
 
 
 class PrefixCase(Case):
@@ -31,13 +31,12 @@ class PrefixCase(Case):
                 continue
             whole, rest = divmod(shared[g], ps)
             first = self.tables[indptr[g]]
-            seen = ls[b] if not self.causal else ls[b]
+            seen = ls[b]
             for k in range(min(whole, -(-seen // ps))):
                 mine = int(self.tables[b, k])
                 if same_pages:
                     self.tables[b, k] = first[k]
-                    for row in range(ps):
-                        poison(self.cache, mine, row)
+                    raw[mine, ps * 288 if kind == "fp4" else 0:] = 0xFF if kind == "bf16" else 0x7F  # NaN
                 else:
                     raw[mine] = raw[int(first[k])]
             if rest and whole < -(-seen // ps):

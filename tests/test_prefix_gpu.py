@@ -57,6 +57,47 @@ def test_random_groups(kind, seed):
                seed=seed).run().check(**P[kind])
 
 
+WIDE = [  # page, group sizes, shared rows, own rows, query lengths, heads, options: four row groups a group and more
+    (64, [16], [3000], [5, 100], [1], 128, dict(uniform=True)),
+    (32, [16], [3000], [0], [1], 128, {}),                          # none has a row of its own
+    (32, [12, 0, 9, 1], [2500, 500, 4001, 300], [0, 1, 300], [1, 2, 3], 64, dict(gap=2, pad=1)),
+    (64, [14], [2000], [64, 3], [2], 64, dict(causal=False, q_fp8=True)),
+    (64, [40, 2], [1500, 2000], [64, 3], [1], 32, dict(same_pages=False)),  # one of the groups is not widened
+    (64, [5], [30000], [70], [1], 128, {}),                         # few row groups, cut over all workers
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["e4m3", "fp4"])
+@pytest.mark.parametrize("ps,sizes,shared,own,qs,heads,kw", WIDE)
+def test_widened_prefix(kind, ps, sizes, shared, own, qs, heads, kw):
+    c = PrefixCase(kind, ps, sizes, shared, own, qs, heads, seed=heads + sum(sizes), **kw).run()
+    assert mla.mla_decode_kernels_per_run(c.plan.handle) == 5
+    c.check(**P[kind])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["e4m3", "fp4"])
+def test_widened_rows_in_a_graph_with_other_lengths(kind):
+    c = PrefixCase(kind, 64, [16], [3000], [5, 100], [1], 128, uniform=True, seed=40)
+    c.run().check(**P[kind])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.run()
+    for lens in ([700], [0], [2999]):  # fewer widened, none, all again
+        c.prefix_lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        c.workspace.fill_(0xFF)
+        c.out.fill_(3.0)
+        g.replay()
+        c.check(**P[kind])
+    page = int(c.tables[0, 3])
+    c.tables[:, 3] = -1
+    g.replay()
+    c.tables[:, 3] = page
+    c.cache[page].zero_()
+    c.check(status=16, **P[kind])
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", ["bf16", "e4m3", "fp4"])
 def test_one_long_prefix_is_cut_over_every_worker(kind):

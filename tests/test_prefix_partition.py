@@ -25,7 +25,7 @@ def runner(tmp_path_factory):
     (out / "mla_prefix_host.h").write_text(
         open(os.path.join(CSRC, "mla_prefix.cuh")).read().replace('#include "mla_common.cuh"\n', ""))
     src = open(os.path.join(CSRC, "mla_prefix.cu")).read()
-    for inc in ("<cuda_bf16.h>", "<cuda_fp16.h>", '"mla_common.cuh"', '"mla_prefix.cuh"', '"sm100_ptx.cuh"'):
+    for inc in ("<cuda_bf16.h>", "<cuda_fp16.h>", '"mla_common.cuh"', '"mla_fp4.cuh"', '"mla_prefix.cuh"', '"sm100_ptx.cuh"'):
         src = src.replace(f"#include {inc}\n", "")
     src = src.replace("ptx::pdl_launch_dependents();", "")
     src = src.replace("extern __shared__ __align__(16) unsigned char prefix_smem[];",
@@ -54,67 +54,97 @@ def _run(runner, ls, qo, max_q, max_len, H, packed, causal, kv, lens, indptr, n_
     r = subprocess.run([str(exe), str(out / "in.txt"), str(out / "out.txt")], capture_output=True, text=True,
                        env=dict(os.environ, ASAN_OPTIONS="detect_leaks=0:abort_on_error=1"), timeout=300)
     assert r.returncode == 0, (r.returncode, r.stderr[-3000:])
-    return [[int(x) for x in line.split()] for line in open(out / "out.txt").read().split("\n")[:5]]
+    return [[int(x) for x in line.split()] for line in open(out / "out.txt").read().split("\n")[:10]]
 
 
 def _check(got, ls, qs, H, causal, lens, indptr, status=0):
     """-> the prefix groups that are shared."""
-    head, items, ranges, entries, segs = got
+    head, items, ranges, entries, segs, wide_items, wide_ranges, wide_segs, wide_groups, (wide_tiles,) = got
     assert head[0] == status
     n_items, n_rg, max_items, max_groups, max_partials = head[1:]
     assert n_items <= max_items and n_rg <= max_groups
-    assert ranges[0] == 0 and ranges[-1] == n_items and all(a <= b for a, b in zip(ranges, ranges[1:]))
     items = [items[10 * i:10 * i + 10] for i in range(n_items)]
-    entries = [entries[4 * i:4 * i + 4] for i in range(n_rg)]
+    wide_items = [wide_items[i:i + 10] for i in range(0, len(wide_items), 10)]
+    entries = [entries[6 * i:6 * i + 6] for i in range(n_rg)]
     segs = [[segs[7 * (9 * r + i):7 * (9 * r + i) + 7] for i in range(9)] for r in range(n_rg)]
     q0 = np.concatenate([[0], np.cumsum(qs)])
     if indptr is None:
         indptr = [g * (len(ls) // len(lens)) for g in range(len(lens) + 1)]
     group_of = {b: g for g in range(len(lens)) for b in range(indptr[g], indptr[g + 1])}
     request_of = np.repeat(np.arange(len(ls)), qs)
-    by, slots, shared, seen = {}, [], {}, {}
-    for it in items:
-        by.setdefault(it[8], []).append(it)
-    assert sorted(by) == list(range(n_rg))
-    assert [it[8] for it in items] == sorted(it[8] for it in items)  # in order: a row group's follow on one another
-    for r, parts in by.items():
-        _, k, _, _, _, tokens, n_seg, start, _, _ = parts[0]
-        assert all([it[1], it[5], it[6], it[7]] == [k, tokens, n_seg, start] for it in parts)
-        rows = min(ROWS, tokens * H - k * ROWS)
-        assert rows > 0 and 1 <= n_seg <= 9
-        # the parts follow on one another, and the segments fill them
-        assert parts[0][2] == 0 and all(a[3] == c[2] for a, c in zip(parts, parts[1:]))
-        assert all(it[2] % TILE == 0 and it[2] < it[3] for it in parts)
+    slots, shared, seen, joined = [], {}, {}, {}
+    # widened rows: the groups' follow on one another, and fit
+    wide = {}
+    if wide_tiles:
         at = 0
-        for tile0, b, row0, end, lo, hi, mask in segs[r][:n_seg]:
-            assert tile0 == at and row0 % TILE == 0 and row0 < end <= ls[b]
-            at += -(-(end - row0) // TILE)
-            assert 0 <= lo < hi <= ROWS
-            for q in range(lo, min(hi, rows), H):
-                assert q % H == 0
-                i = (k * ROWS + q) // H  # token of the owner
-                token = start + i
-                own = request_of[token]
-                last = mask + i
-                if own != b or mask == 1 << 30 and causal:  # shared rows: whole tiles that all see, from the group's first table
-                    g = group_of[own]
-                    assert row0 == 0 and end % TILE == 0 and end <= lens[g] and group_of[b] == g
-                    assert b == next(x for x in range(indptr[g], indptr[g + 1]) if ls[x] > 0)
-                    assert shared.setdefault(g, end) == end
-                    assert end <= (ls[own] - qs[own] + 1 if causal else ls[own]) or ls[own] <= 0
-                    last = end - 1
-                elif causal:
-                    assert last == ls[own] - qs[own] + token - q0[own]
-                seen.setdefault(token, []).append((row0, min(end, last + 1)))
-        assert at * TILE == parts[-1][3]
-        row0, n, slot, count = entries[r]
-        assert row0 == start * H + k * ROWS and count == len(parts)
-        assert n == (rows if count > 1 else 0)
-        if count > 1:
-            assert [it[4] for it in parts] == list(range(slot, slot + count))
-            slots += [it[4] for it in parts]
-        else:
-            assert parts[0][4] == -1
+        for g in range(len(lens)):
+            base, tiles, b = wide_groups[3 * g:3 * g + 3]
+            assert base == at
+            at += tiles
+            if tiles:
+                wide[g] = base, tiles
+                assert b == next(x for x in range(indptr[g], indptr[g + 1]) if ls[x] > 0)
+        assert wide_groups[3 * len(lens)] == at <= wide_tiles
+    for which, (its, rng) in enumerate([(items, ranges), (wide_items, wide_ranges)]):
+        if not rng:
+            continue
+        assert rng[0] == 0 and rng[-1] == len(its) and all(a <= b for a, b in zip(rng, rng[1:]))
+        assert [it[8] for it in its] == sorted(it[8] for it in its)  # a row group's follow on one another
+        by = {}
+        for i, it in enumerate(its):
+            by.setdefault(it[8], []).append((i, it))
+        for r, found in by.items():
+            parts = [it for _, it in found]
+            _, k, _, _, _, tokens, n_seg, start, _, _ = parts[0]
+            assert all([it[1], it[5], it[6], it[7]] == [k, tokens, n_seg, start] for it in parts)
+            rows = min(ROWS, tokens * H - k * ROWS)
+            assert rows > 0 and 1 <= n_seg <= 9
+            # the parts follow on one another, and the segments fill them
+            assert parts[0][2] == 0 and all(a[3] == c[2] for a, c in zip(parts, parts[1:]))
+            assert all(it[2] % TILE == 0 and it[2] < it[3] for it in parts)
+            at, is_wide = 0, False
+            row_segs = segs[r][:n_seg] if which == 0 else [wide_segs[7 * found[0][0]:7 * found[0][0] + 7]]
+            for tile0, b, row0, end, lo, hi, mask in row_segs:
+                assert tile0 == at and row0 % TILE == 0 and row0 < end
+                at += -(-(end - row0) // TILE)
+                assert 0 <= lo < hi <= ROWS
+                for q in range(lo, min(hi, rows), H):
+                    assert q % H == 0
+                    i = (k * ROWS + q) // H  # token of the owner
+                    token = start + i
+                    own = request_of[token]
+                    last, first = mask + i, row0
+                    g = group_of.get(own)
+                    if which == 1:  # widened rows, in the group's place
+                        assert (row0, end) == (wide[g][0] * TILE, sum(wide[g]) * TILE) and mask == 1 << 30
+                        last, first = end - row0 - 1, 0
+                        assert shared.setdefault(g, last + 1) == last + 1 <= lens[g]
+                        assert last + 1 <= (ls[own] - qs[own] + 1 if causal else ls[own]) or ls[own] <= 0
+                        seen.setdefault(token, []).append((0, last + 1))
+                        continue
+                    assert end <= ls[b]
+                    if own != b or mask == 1 << 30 and causal:  # shared rows: whole tiles that all see, from the group's first table
+                        assert row0 == 0 and end % TILE == 0 and end <= lens[g] and group_of[b] == g and g not in wide
+                        assert b == next(x for x in range(indptr[g], indptr[g + 1]) if ls[x] > 0)
+                        assert shared.setdefault(g, end) == end
+                        assert end <= (ls[own] - qs[own] + 1 if causal else ls[own]) or ls[own] <= 0
+                        last = end - 1
+                    elif causal:
+                        assert last == ls[own] - qs[own] + token - q0[own]
+                    seen.setdefault(token, []).append((row0, min(end, last + 1)))
+            assert at * TILE == parts[-1][3]
+            e = entries[r]
+            assert e[0] == start * H + k * ROWS
+            needs = len(parts) > 1 or group_of.get(request_of[start + k * ROWS // H]) in wide
+            assert e[3 + 2 * which] == (len(parts) if needs else 0)
+            if needs:
+                joined[r] = rows
+                first = e[2 + 2 * which]
+                assert [it[4] for it in parts] == list(range(first, first + len(parts)))
+                slots += [it[4] for it in parts]
+            else:
+                assert parts[0][4] == -1
+    assert all(e[1] == joined.get(r, 0) for r, e in enumerate(entries))
     assert len(set(slots)) == len(slots) and all(0 <= x < max_partials for x in slots)
     for token, b in enumerate(request_of):  # every row that the token sees, once
         L = ls[b]
@@ -126,7 +156,7 @@ def _check(got, ls, qs, H, causal, lens, indptr, status=0):
     return set(shared)
 
 
-def _case(runner, sizes, lens, own, qs, H, packed, causal, kv, n_workers, uniform=False, gap=0, **kw):
+def _case(runner, sizes, lens, own, qs, H, packed, causal, kv, n_workers, uniform=False, gap=0, wide=None, **kw):
     """Groups of `sizes` requests with `lens` shared rows, after and before `gap` requests of
     their own; own(rng-free callable of request) rows past the shared ones."""
     ls, indptr = [own(i) for i in range(gap)], [gap]
@@ -138,6 +168,7 @@ def _case(runner, sizes, lens, own, qs, H, packed, causal, kv, n_workers, unifor
     ls = [max(L, q) if L else 0 for L, q in zip(ls, qs)]
     qo = np.concatenate([[0], np.cumsum(qs)])
     got = _run(runner, ls, qo, max(qs), max(ls), H, packed, causal, kv, lens, None if uniform else indptr, n_workers, **kw)
+    assert wide is None or wide == (len(got[5]) > 0)
     return _check(got, ls, qs, H, causal, lens, indptr)
 
 
@@ -151,6 +182,16 @@ def test_beams_are_shared_and_full_row_groups_are_not(runner):
                  76, uniform=True) == set(range(16))
     # a row group a request already, and a worker for each
     assert _case(runner, [8] * 4, [640] * 4, lambda i: 10, [1], 128, False, True, 0, 76, uniform=True) == set()
+
+
+@pytest.mark.parametrize("kv", [1, 2])
+def test_rows_that_many_row_groups_walk_are_widened(runner, kv):
+    for own in (lambda i: 100 + 30 * i, lambda i: 0, lambda i: i % 2):
+        assert _case(runner, [32], [20000], own, [1], 128, False, True, kv, 76, uniform=True, wide=True) == {0}
+    assert _case(runner, [40, 2, 50], [9000, 4000, 7000], lambda i: 3 + i, [3, 1, 2], 64, True, True, kv, 76, gap=2, wide=True) >= {0, 2}
+    # not over bf16, nor where a prefix group has few row groups
+    _case(runner, [32], [20000], lambda i: 9, [1], 128, False, True, 0, 76, uniform=True, wide=False)
+    assert _case(runner, [8] * 16, [5000] * 16, lambda i: 9, [1], 32, False, True, kv, 76, uniform=True, wide=False)
 
 
 def test_a_group_without_rows_of_its_own(runner):
