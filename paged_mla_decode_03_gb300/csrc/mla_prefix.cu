@@ -621,9 +621,16 @@ cudaError_t launch_partition_prefix(const Problem& p, const PrefixArgs& pa, cons
 }
 
 // The shared rows of groups that are widened, once, to f16 (exact).  A block takes a tile of 64
-// rows, a thread eight dims of a row at a time: reads and writes are contiguous across a warp.
-// What bounds it is the bytes: 65536 rows of 4 bits, 97 MB read and written.
-constexpr int kWidenThreads = 256;
+// rows, four at a time, a thread the same eight dims of every fourth: reads and writes are
+// contiguous across a warp, and eight rows are on their way at once.  What bounds it is the
+// bytes: 65536 rows of 4 bits, 97 MB read and written.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
+  uint32_t h;
+  asm("{\n .reg .b16 lo;\n mov.b32 {lo, _}, %1;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n}" : "=r"(h) : "r"(codes));
+  return h;
+}
+
+constexpr int kWidenUnits = kQkDim / 8, kWidenRows = 4, kWidenThreads = kWidenRows * kWidenUnits;
 
 template <bool kFp4>
 __global__ void __launch_bounds__(kWidenThreads)
@@ -631,49 +638,59 @@ widen_prefix_kernel(Problem p, int groups, PrefixLayout pl, char* __restrict__ w
   ptx::pdl_launch_dependents();
   ptx::pdl_wait();
   const PrefixWide* of = reinterpret_cast<const PrefixWide*>(ws + pl.wide_groups);
-  uint4* rows = reinterpret_cast<uint4*>(ws + pl.wide_rows);
   int* status = reinterpret_cast<int*>(ws) + kHdrStatus;
   const int total = min(of[groups].base, pl.wide_tiles), ps = p.page_size, shift = ps == 64 ? 6 : 5;
+  const int u = threadIdx.x % kWidenUnits, r0 = threadIdx.x / kWidenUnits;
   for (int t = blockIdx.x; t < total; t += gridDim.x) {
     int lo = 0, hi = groups;  // the last group whose tiles start at or before t
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (of[mid].base <= t) lo = mid; else hi = mid;
     }
-    const int tile = t - of[lo].base;
+    const int row0 = (t - of[lo].base) * kKvTile;
     const int* table = p.block_tables + (size_t)of[lo].b * p.max_pages;
-    constexpr int kUnits = kQkDim / 8;  // of a row
-#pragma unroll 6
-    for (int i = threadIdx.x; i < kKvTile * kUnits; i += kWidenThreads) {
-      const int r = i / kUnits, u = i - r * kUnits, row = tile * kKvTile + r, in = row & (ps - 1);
-      const int id = table[row >> shift];
-      uint32_t h[4] = {0, 0, 0, 0};
-      if (id >= 0 && (long long)id < p.num_pages) {
-        if constexpr (kFp4) {
-          const unsigned char* page = static_cast<const unsigned char*>(p.kv_cache) + (size_t)id * ps * kFp4RowBytes;
-          ptx::e2m1x8_to_f16x2(reinterpret_cast<const uint32_t*>(page + in * kFp4CodeBytes)[u], h);
-          const uint32_t code = page[(size_t)ps * kFp4CodeBytes + in * kFp4ScaleBytes + (u >> 1)];
-          uint32_t two;
-          asm("{\n .reg .b16 lo;\n mov.b32 {lo, _}, %1;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n}" : "=r"(two) : "r"(code | code << 8));
-          const __half2 scale = *reinterpret_cast<const __half2*>(&two);
+    uint4* to = reinterpret_cast<uint4*>(ws + pl.wide_rows) + (size_t)t * kKvTile * kWidenUnits + u;
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {  // 32 rows, of one page
+      const int id = table[(row0 + 32 * half) >> shift], in0 = (32 * half & (ps - 1)) + r0;
+      const bool on = id >= 0 && (long long)id < p.num_pages;
+      if (!on && threadIdx.x == 0) atomicOr(status, kStatusPage);
+      const unsigned char* page =
+          static_cast<const unsigned char*>(p.kv_cache) + (on ? (size_t)id * ps * (kFp4 ? kFp4RowBytes : kQkDim) : 0);
+      constexpr int kN = 32 / kWidenRows;
+      uint32_t code[kN][2], scale[kN];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&h[k]), scale);
-            h[k] = *reinterpret_cast<const uint32_t*>(&v);
+      for (int k = 0; k < kN; ++k) {
+        const int in = in0 + kWidenRows * k;
+        code[k][0] = code[k][1] = scale[k] = 0;
+        if (!on) continue;
+        if constexpr (kFp4) {
+          code[k][0] = reinterpret_cast<const uint32_t*>(page + in * kFp4CodeBytes)[u];
+          scale[k] = page[(size_t)ps * kFp4CodeBytes + in * kFp4ScaleBytes + (u >> 1)];
+        } else {
+          const uint2 c = reinterpret_cast<const uint2*>(page + in * kQkDim)[u];
+          code[k][0] = c.x;
+          code[k][1] = c.y;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kN; ++k) {
+        uint32_t h[4];
+        if constexpr (kFp4) {
+          ptx::e2m1x8_to_f16x2(code[k][0], h);
+          const uint32_t two = e4m3x2_to_f16x2(scale[k] | scale[k] << 8);
+          const __half2 by = *reinterpret_cast<const __half2*>(&two);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&h[e]), by);
+            h[e] = *reinterpret_cast<const uint32_t*>(&v);
           }
         } else {
-          const unsigned char* at = static_cast<const unsigned char*>(p.kv_cache) + ((size_t)id * ps + in) * kQkDim;
-          const uint2 c = reinterpret_cast<const uint2*>(at)[u];
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            asm("{\n .reg .b16 lo;\n mov.b32 {lo, _}, %1;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n}"
-                : "=r"(h[k])
-                : "r"((k < 2 ? c.x : c.y) >> (16 * (k & 1))));
+          for (int e = 0; e < 4; ++e) h[e] = e4m3x2_to_f16x2(code[k][e >> 1] >> (16 * (e & 1)));
         }
-      } else if (u == 0) {
-        atomicOr(status, kStatusPage);
+        to[(32 * half + r0 + kWidenRows * k) * kWidenUnits] = make_uint4(h[0], h[1], h[2], h[3]);
       }
-      rows[((size_t)t * kKvTile + r) * kUnits + u] = make_uint4(h[0], h[1], h[2], h[3]);
     }
   }
 }
@@ -681,7 +698,7 @@ widen_prefix_kernel(Problem p, int groups, PrefixLayout pl, char* __restrict__ w
 cudaError_t launch_widen_prefix(const Problem& p, int groups, const PrefixLayout& pl, void* ws, int sm_count,
                                 cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(std::min(pl.wide_tiles, 4 * sm_count), 1, 1);
+  cfg.gridDim = dim3(std::min(pl.wide_tiles, 7 * sm_count), 1, 1);
   cfg.blockDim = dim3(kWidenThreads, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr;
