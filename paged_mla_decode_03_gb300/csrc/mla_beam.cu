@@ -75,6 +75,29 @@ __device__ __forceinline__ float value_of(uint32_t word, int half) {
 }
 
 constexpr float kLog2eHi = 1.44269502162933349609375f, kLog2eLo = 1.925963033500e-8f;
+// The largest of kCount units' values, two at a time in 16 bits (a NaN is none).
+template <typename T, int kCount>
+__device__ __forceinline__ float largest(const uint4* w) {
+  if constexpr (sizeof(T) == 4) {
+    float m = kNone;
+#pragma unroll
+    for (int v = 0; v < kCount; ++v)
+      m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(w[v].x), __uint_as_float(w[v].y)),
+                         fmaxf(__uint_as_float(w[v].z), __uint_as_float(w[v].w))));
+    return m;
+  } else {
+    using Pair = typename std::conditional<std::is_same<T, __nv_bfloat16>::value, __nv_bfloat162, __half2>::type;
+    auto pair = [](const uint32_t& x) { return *reinterpret_cast<const Pair*>(&x); };
+    Pair m = __hmax2(__hmax2(pair(w[0].x), pair(w[0].y)), __hmax2(pair(w[0].z), pair(w[0].w)));
+#pragma unroll
+    for (int v = 1; v < kCount; ++v)
+      m = __hmax2(m, __hmax2(__hmax2(pair(w[v].x), pair(w[v].y)), __hmax2(pair(w[v].z), pair(w[v].w))));
+    const uint32_t bits = *reinterpret_cast<const uint32_t*>(&m);
+    // (two NaN leave one: no maximum)
+    return fmaxf(fmaxf(value_of<T>(bits, 0), value_of<T>(bits, 1)), kNone);
+  }
+}
+
 // e^d for d <= 0: the product by log2(e) in two parts, so that its rounding is not of log2(e).
 __device__ __forceinline__ float exp_of(float d) { return ptx::ex2(fmaf(d, kLog2eHi, d * kLog2eLo)); }
 
@@ -220,7 +243,7 @@ beam_parts_kernel(Logits in, const float* __restrict__ scores, const unsigned ch
   unsigned short* hot = reinterpret_cast<unsigned short*>(cand_i + kRoom);  // thread + 256 stretch
   static_assert(8 * kRoom + 2 * kStretches * kThreads <= kRing && kThreads == 256, "room");
   float* stretch_max = reinterpret_cast<float*>(reinterpret_cast<char*>(ring) + kRing);  // [stretch][thread]
-  __shared__ Two warp_sum[kWarps];
+  __shared__ unsigned long long warp_sum[kWarps];
   ptx::pdl_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long g0 = (long long)blockIdx.x * out.share, g1 = min(g0 + out.share, (long long)out.rows * out.chunks);
@@ -282,11 +305,7 @@ beam_parts_kernel(Logits in, const float* __restrict__ scores, const unsigned ch
   Two sum{0.f, 0.f};              // and sum of exp(x - m)
   auto take = [&](const uint4* w, auto count) {
     constexpr int kCount = decltype(count)::value;
-    float mine = kNone;
-#pragma unroll
-    for (int v = 0; v < kCount; ++v)
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) mine = fmaxf(mine, at(w[v], e));
+    const float mine = largest<T, kCount>(w);
     here = fmaxf(here, mine);
     if (mine > m) {
       const float f = exp_of(m - mine);  // m = -inf: 0
@@ -346,34 +365,46 @@ beam_parts_kernel(Logits in, const float* __restrict__ scores, const unsigned ch
     if (tid == 0) n_hot = n_cand = 0;
   }
   __syncthreads();
-  {  // a group's rank by its four threads
-    const int group = tid >> 2;
-    const float g = group_max[group];
+  // the rank of a group by its four threads; of two together by their eight, for a small k, in a
+  // quarter of the steps
+  auto rank_groups = [&](auto wide) {
+    constexpr int kPerGroup = decltype(wide)::value, kAll2 = kThreads / kPerGroup;
+    auto value = [&](int i) { return kPerGroup == 4 ? group_max[i] : fmaxf(group_max[2 * i], group_max[2 * i + 1]); };
+    const int group = tid / kPerGroup;
+    const float g = value(group);
     int rank = 0;
 #pragma unroll
-    for (int j = 0; j < kGroups / 4; ++j) {
-      const int o = 4 * j + (lane & 3);
-      rank += before(group_max[o], o, g, group) ? 1 : 0;
+    for (int j = 0; j < kAll2 / kPerGroup; ++j) {
+      const int o = kPerGroup * j + (lane & (kPerGroup - 1));
+      rank += before(value(o), o, g, group) ? 1 : 0;
     }
-    rank += __shfl_xor_sync(kAll, rank, 1);
-    rank += __shfl_xor_sync(kAll, rank, 2);
-    if (rank == k - 1) threshold = g;
-  }
-  float top = fmaxf(group_max[lane], group_max[lane + 32]);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+    for (int o = 1; o < kPerGroup; o <<= 1) rank += __shfl_xor_sync(kAll, rank, o);
+    if (rank == k - 1) threshold = g;
+  };
+  if (k <= 16) rank_groups(std::integral_constant<int, 8>());
+  else rank_groups(std::integral_constant<int, 4>());
+  float top = fmaxf(group_max[lane], group_max[lane + 32]);
+  {
+    const uint32_t u = __reduce_max_sync(kAll, ordered(top));
+    top = __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xffffffffu));
+  }
   // the threads' sums, relative to 2^power (far: to e^top)
   const float power = is_far(top) ? 0.f : rintf(top * kLog2eHi);
   {
     // (no value: a sum of 0; a NaN, or an infinity's, stays one)
     const float f = !is_far(top) ? power_of(log2_of(m), Two{power, 0.f}) : top > kNone ? exp_of(m - top) : 1.f;
-    sum = settle(sum.h * f, sum.l * f);
+    // whole multiples of 2^-32 add up without rounding, 22 bits at a time (a thread's sum is
+    // below 2^21: of 2^20 values at most, each below e^0.7)
+    const float h = sum.h * f, l = sum.l * f;
+    const bool odd = !(h < 2097152.f);  // a NaN, then
+    const long long q = odd ? 0 : __float2ll_rn(h * 4294967296.f) + __float2ll_rn(l * 4294967296.f);
+    unsigned long long all = 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const Two other{__shfl_xor_sync(kAll, sum.h, o), __shfl_xor_sync(kAll, sum.l, o)};
-      sum = add(sum, other);
-    }
-    if (lane == 0) warp_sum[warp] = sum;
+    for (int i = 0; i < 3; ++i)
+      all += (unsigned long long)__reduce_add_sync(kAll, (unsigned)(q >> (22 * i)) & 0x3fffffu) << (22 * i);
+    const bool none = __any_sync(kAll, odd);
+    if (lane == 0) warp_sum[warp] = none ? ~0ull : all;
   }
   __syncthreads();
   // the stretches that have a value at or above the threshold
@@ -442,9 +473,17 @@ beam_parts_kernel(Logits in, const float* __restrict__ scores, const unsigned ch
     select_slowly(x, max(0, u0 * kPer - off), min(in.vocab, u1 * kPer - off), k, out_x, out_i, best_key);
   }
   if (tid == 0) {
-    Two s = warp_sum[0];
-    for (int w = 1; w < kWarps; ++w) s = add(s, warp_sum[w]);
-    out.part[list] = Part{top, (int)power, s};
+    unsigned long long s = 0;
+    bool odd = false;
+    for (int w = 0; w < kWarps; ++w) {
+      s += warp_sum[w];
+      odd = odd || warp_sum[w] == ~0ull;
+    }
+    // the sum as two floats: its upper 24 bits and the rest
+    const int shift = max(0, 40 - __clzll(s));
+    const float h = (float)(s >> shift << shift) * 2.3283064365386963e-10f;
+    const float l = (float)(s & ((1ull << shift) - 1)) * 2.3283064365386963e-10f;
+    out.part[list] = Part{top, (int)power, odd ? Two{NAN, 0.f} : settle(h, l)};
   }
   __syncthreads();  // (the next row takes the ring)
   }

@@ -77,7 +77,7 @@ def inputs(kind, B, W, V, seed, spread=3.0, pad=0, off=0):
 @pytest.mark.parametrize("B,W,V,k,pad,off", [
     (1, 1, 1, 1, 0, 0), (1, 1, 1, 3, 0, 0), (2, 3, 2, 5, 0, 0), (1, 4, 33, 4, 1, 0), (3, 2, 100, 64, 0, 3), (1, 4, 8192, 8, 0, 0),
     (2, 4, 16384, 8, 0, 0), (2, 4, 16385, 8, 0, 1), (5, 3, 32768, 6, 7, 0), (1, 8, 100003, 16, 0, 0), (64, 4, 5003, 8, 0, 5),
-    (1, 64, 9001, 64, 0, 0), (2, 16, 65537, 32, 3, 2), (300, 5, 1000, 10, 0, 0), (1, 2, 300000, 64, 0, 0)])
+    (1, 64, 9001, 64, 0, 0), (700, 3, 9, 4, 2, 1), (500, 7, 3, 5, 0, 2), (900, 2, 13, 3, 0, 3), (2, 16, 65537, 32, 3, 2), (300, 5, 1000, 10, 0, 0), (1, 2, 300000, 64, 0, 0)])
 def test_select(kind, B, W, V, k, pad, off):
     check(*inputs(kind, B, W, V, 7 * V + k, pad=pad, off=off), k)
 
