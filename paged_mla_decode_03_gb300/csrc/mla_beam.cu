@@ -15,8 +15,7 @@
 //
 // What bounds it: the bytes of the logits, where there are many; a chain of two launches, else.
 // A thread streams its own values through shared memory, with no barrier and no copy of another's,
-// two chunks ahead: it keeps their maximum and sum.  (The rows' chunks are dealt out evenly, three
-// blocks to an SM; a block may take the end of one row and the start of the next.)  The k-th
+// two chunks ahead: it keeps their maximum and sum.  The k-th
 // largest maximum of 64 groups of threads is a threshold that at least k values are at or above,
 // and seldom many more; the few stretches of a thread's values whose maximum is not below it are
 // read again, and what passes is ranked by counting.
@@ -182,10 +181,7 @@ struct Parts {
   Part* part;    // [rows][parts]
   float* value;  // [rows][parts][k], descending; -inf: none
   int* token;    // [rows][parts][k]
-  int rows, parts, chunks, share;  // lists of a row at most; chunks of a row, and of a block
-  // Row r's chunks are those from r * chunks on of all; block i has `share` from i * share on.
-  __device__ int first(int row) const { return (int)((long long)row * chunks / share); }
-  __device__ int count(int row) const { return (int)(((long long)(row + 1) * chunks - 1) / share) - first(row) + 1; }
+  int parts, share;  // parts of a row, chunks of a part
 };
 
 }  // namespace
@@ -246,20 +242,14 @@ beam_parts_kernel(Logits in, const float* __restrict__ scores, const unsigned ch
   __shared__ unsigned long long warp_sum[kWarps];
   ptx::pdl_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const long long g0 = (long long)blockIdx.x * out.share, g1 = min(g0 + out.share, (long long)out.rows * out.chunks);
-#pragma unroll 1
-  for (long long g = g0; g < g1;) {
-  const int row = (int)(g / out.chunks), chunk0 = (int)(g - (long long)row * out.chunks);
-  const int chunk1 = (int)min((long long)out.chunks, chunk0 + g1 - g);
-  const int part = (int)blockIdx.x - out.first(row);
-  g += chunk1 - chunk0;
+  const int row = blockIdx.x / out.parts, part = blockIdx.x - row * out.parts;
   // a beam that has ended, or has no score, offers nothing that its logits decide
-  if ((finished && finished[row]) || !(fabsf(scores[row]) < INFINITY)) continue;
+  if ((finished && finished[row]) || !(fabsf(scores[row]) < INFINITY)) return;
   const T* x = static_cast<const T*>(in.base) + (row / in.beams) * in.batch_stride + (row % in.beams) * in.beam_stride;
   // units of 16 aligned bytes; the row's first and last may reach out of it
   const int off = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
   const int units = (off + in.vocab + kPer - 1) / kPer;
-  const int u0 = chunk0 * kUnits, u1 = min(chunk1 * kUnits, units);
+  const int u0 = part * out.share * kUnits, u1 = min(u0 + out.share * kUnits, units);
   const int f0 = off > 0 ? max(u0, 1) : u0, f1 = min(u1, (off + in.vocab) / kPer);  // whole ones
   constexpr uint32_t kNothing = sizeof(T) == 4 ? 0xff800000u
                                 : std::is_same<T, __nv_bfloat16>::value ? 0xff80ff80u : 0xfc00fc00u;  // -inf
@@ -485,8 +475,6 @@ beam_parts_kernel(Logits in, const float* __restrict__ scores, const unsigned ch
     const float l = (float)(s & ((1ull << shift) - 1)) * 2.3283064365386963e-10f;
     out.part[list] = Part{top, (int)power, odd ? Two{NAN, 0.f} : settle(h, l)};
   }
-  __syncthreads();  // (the next row takes the ring)
-  }
 }
 
 // One block a request: the rows' normalisers, then the k best of all lists.
@@ -503,6 +491,7 @@ beam_join_kernel(const float* __restrict__ scores, const unsigned char* __restri
   __shared__ unsigned long long key[kDepths][kMaxLists], cand_s[kRoom], best_s[kWarps], threshold;
   __shared__ long long cand_i[kRoom], best_i[kWarps];
   __shared__ float staged[kStaged];
+  __shared__ int staged_token[kStaged];
   __shared__ int n_cand;
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int lists = beams * in.parts;
@@ -511,27 +500,33 @@ beam_join_kernel(const float* __restrict__ scores, const unsigned char* __restri
   // (beside the normalisers; lists that nobody wrote are not looked at)
   const bool near = lists * k <= kStaged;
   if (near)
-    for (int e = tid; e < lists * k; e += kThreads) staged[e] = in.value[list0 * k + e];
-  for (int w = warp; w < beams; w += kWarps) {
-    const int row = b * beams + w;
-    const float c = scores[row];
-    const bool scored = fabsf(c) < INFINITY, done = finished && finished[row];
+    for (int e = tid; e < lists * k; e += kThreads) {
+      staged[e] = in.value[list0 * k + e];
+      staged_token[e] = in.token[list0 * k + e];
+    }
+  constexpr int kLanes = 8;  // of a row
+  for (int w0 = 0; w0 < beams; w0 += kThreads / kLanes) {
+    const int w = w0 + tid / kLanes, part0 = tid % kLanes, row = b * beams + w;
+    const float c = w < beams ? scores[row] : kNone;
+    const bool scored = fabsf(c) < INFINITY, done = w < beams && finished && finished[row];
     Two sum{0.f, 0.f};
     float top = kNone;
     int power = -(1 << 24);
-    if (scored && !done) {
-      const Part* of = in.part + (size_t)row * in.parts;
-      const int parts = in.count(row);
-      for (int p = lane; p < parts; p += 32) {
-        const Part q = of[p];
-        top = fmaxf(top, q.top);
-        if (!is_far(q.top)) power = max(power, q.power);
-      }
+    const int parts = scored && !done ? in.parts : 0;
+    const Part* of = in.part + (size_t)row * in.parts;
+    for (int p = part0; p < parts; p += kLanes) {
+      const Part q = of[p];
+      top = fmaxf(top, q.top);
+      if (!is_far(q.top)) power = max(power, q.power);
+    }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-      power = __reduce_max_sync(kAll, power);
+    for (int o = kLanes / 2; o > 0; o >>= 1) {
+      top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+      power = max(power, __shfl_xor_sync(kAll, power, o));
+    }
+    {
       const bool far = is_far(top);
-      for (int p = lane; p < parts; p += 32) {
+      for (int p = part0; p < parts; p += kLanes) {
         const Part q = of[p];
         // (a part without a value adds 0, or a NaN that it holds)
         float f;
@@ -541,15 +536,15 @@ beam_join_kernel(const float* __restrict__ scores, const unsigned char* __restri
         sum = add(sum, Two{q.sum.h * f, q.sum.l * f});
       }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
+      for (int o = kLanes / 2; o > 0; o >>= 1) {
         const Two other{__shfl_xor_sync(kAll, sum.h, o), __shfl_xor_sync(kAll, sum.l, o)};
         sum = add(sum, other);
       }
     }
-    if (lane == 0) {
+    if (part0 == 0 && w < beams) {
       // an infinity or a NaN among the logits, or nothing above -inf: no continuation
       const bool ok = scored && !done && fabsf(top) < INFINITY && sum.h > 0.f && sum.h < 1e35f;
-      row_lists[w] = scored && done ? -1 : ok ? in.count(row) : 0;
+      row_lists[w] = scored && done ? -1 : ok ? in.parts : 0;
       row_top[w] = is_far(top) ? top : 0.f;
       row_score[w] = c;
       Two less{0.f, 0.f};
@@ -579,7 +574,7 @@ beam_join_kernel(const float* __restrict__ scores, const unsigned char* __restri
   };
   auto place_of = [&](int l, int j) -> long long {
     const int w = l / in.parts;
-    return (long long)w * vocab + (row_lists[w] < 0 ? end_token : in.token[(list0 + l) * k + j]);
+    return (long long)w * vocab + (row_lists[w] < 0 ? end_token : near ? staged_token[l * k + j] : in.token[(list0 + l) * k + j]);
   };
   // A threshold that at least k candidates are at or above: for some depths d, the
   // ceil(k / d)-th largest of the lists' d-th candidates, and of these the largest.  (With d
@@ -785,24 +780,24 @@ namespace {
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 struct BeamPlan {
-  int parts, chunks, share, blocks;
+  int parts, share, blocks;
   size_t value, token, bytes;
 };
 
-// An even share of all rows' chunks for each block; and no more lists a request than the join ranks.
-// `whole`: every row starts on a 16-byte boundary (else it may have a unit more).
+// Even parts of each row: as many as make up to kBlocks blocks, which run all at once; and no more
+// lists a request than the join ranks.  (Shares of all rows' chunks that end inside a row kept every SM as
+// busy, but each end of a part costs 4 us: 64 x 4 beams over 131071 tokens took 30 us instead of
+// 24.)  `whole`: every row starts on a 16-byte boundary (else it may have a unit more).
 BeamPlan beam_plan(const mla_beam_params& p, bool whole) {
   const int per = p.logits_dtype == MLA_LOGITS_FP32 ? 4 : 8, per_chunk = kThreads * kVectors * per;
   const long long rows = (long long)p.batch * p.beams;
   const long long values = p.vocab + (whole ? 0LL : per - 1LL);
   BeamPlan b;
-  b.chunks = (int)((values + per_chunk - 1) / per_chunk);
-  // (a row of C chunks meets ceil((C - 1) / share) + 1 blocks at most)
-  const long long most = kMaxLists / p.beams - 1;
-  const long long share = std::max((rows * b.chunks + kBlocks - 1) / kBlocks, (b.chunks - 1 + most - 1) / most);
-  b.share = (int)std::max(1LL, share);
-  b.parts = b.share == 1 ? b.chunks : (b.chunks - 1 + b.share - 1) / b.share + 1;
-  b.blocks = (int)((rows * b.chunks + b.share - 1) / b.share);
+  const long long chunks = (values + per_chunk - 1) / per_chunk;
+  const long long want = std::min({chunks, std::max(1LL, kBlocks / std::max(rows, 1LL)), (long long)kMaxLists / p.beams});
+  b.share = (int)((chunks + want - 1) / want);
+  b.parts = (int)((chunks + b.share - 1) / b.share);
+  b.blocks = (int)(rows * b.parts);
   const size_t lists = (size_t)rows * b.parts;
   b.value = align_up(sizeof(Part) * lists, 256);
   b.token = b.value + align_up(sizeof(float) * lists * p.k, 256);
@@ -863,7 +858,7 @@ int mla_beam_select(const mla_beam_params* params, const void* logits, int64_t b
   const BeamPlan plan = beam_plan(p, whole);
   char* ws = static_cast<char*>(workspace);
   Parts parts{reinterpret_cast<Part*>(ws), reinterpret_cast<float*>(ws + plan.value),
-              reinterpret_cast<int*>(ws + plan.token), p.batch * p.beams, plan.parts, plan.chunks, plan.share};
+              reinterpret_cast<int*>(ws + plan.token), plan.parts, plan.share};
   const Logits in{logits, batch_stride, beam_stride, p.beams, p.vocab};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const dim3 grid((unsigned)plan.blocks);
