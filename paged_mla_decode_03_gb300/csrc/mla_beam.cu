@@ -15,7 +15,7 @@
 //
 // What bounds it: the bytes of the logits, where there are many; a chain of two launches, else.
 // A thread streams its own values through shared memory, with no barrier and no copy of another's,
-// two chunks ahead: it keeps their maximum and sum.  The k-th
+// a chunk ahead, four blocks to an SM: it keeps their maximum and sum.  The k-th
 // largest maximum of 64 groups of threads is a threshold that at least k values are at or above,
 // and seldom many more; the few stretches of a thread's values whose maximum is not below it are
 // read again, and what passes is ranked by counting.
@@ -35,8 +35,8 @@ namespace mla {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kBlocks = 456;            // three on each of 152 SMs, all at once
-constexpr int kStages = 3;             // chunks of a block on their way
+constexpr int kBlocks = 608;            // four on each of 152 SMs, all at once
+constexpr int kStages = 2;             // chunks of a block on their way
 constexpr int kVectors = 4;             // 16-byte units of a thread in a chunk
 constexpr int kGroups = 64;             // groups of a part's values: four threads each
 constexpr int kMaxK = 64;
@@ -224,7 +224,7 @@ __device__ __noinline__ void select_slowly(const T* x, int begin, int end, int k
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, 4)
 beam_parts_kernel(Logits in, const float* __restrict__ scores, const unsigned char* __restrict__ finished, int k,
                   Parts out) {
   constexpr int kPer = 16 / (int)sizeof(T);  // values of a unit
