@@ -10,9 +10,9 @@
 //
 // A group's rows are shared where that costs fewer tiles, overheads included (the own tiles
 // of a request that straddles one row group more count once more), and groups are shared at all
-// where the call's estimate falls: the largest row group where none needs to be cut, else an even
-// share and the join (kCutTiles).  So a few beams over a short prompt stay apart: each is
-// done on a worker of its own while a common row group would be one worker's work.
+// where the call's estimate falls by prefix_gain tiles: the largest row group where none needs to
+// be cut, else an even share and the join (kCutTiles).  So a few beams over a short prompt stay
+// apart.
 #include <algorithm>
 #include <climits>
 
@@ -351,7 +351,7 @@ partition_prefix_kernel(Problem p, PrefixArgs pa, Layout lay, PrefixLayout pl, c
         break;
       }
     }
-    if (shared <= alone) break;
+    if (shared + prefix_gain(p.kv_dtype) <= alone) break;
     __syncthreads();
     for (int b = tid; b < B; b += blockDim.x) {
       s.group[b] = -1;
