@@ -370,7 +370,8 @@ int mla_decode_run_sparse(const mla_plan_t *plan, const void *query, const void 
  * Decode over a batch whose requests share their first rows: a system prompt,
  * a document, the prompt of a beam search.  The result is mla_decode_run's, to
  * rounding; the shared rows are read once for 128 query rows of a group, whichever requests
- * they belong to, where each request reads them for itself otherwise.
+ * they belong to, where each request reads them for itself otherwise.  Over 4 bits and e4m3,
+ * rows that four and more such sets of query rows share are widened to f16 in the workspace.
  *
  * prefix_lens    device int32 [G], G = params.prefix_groups: the first
  *                prefix_lens[g] rows of group g's requests hold the same values.
@@ -387,8 +388,11 @@ int mla_decode_run_sparse(const mla_plan_t *plan, const void *query, const void 
  * bmm1_dev, bmm2_dev  both NULL, or both one fp32 in device memory that
  *                stands in for bmm1_scale and bmm2_scale (mla_decode_run_device_scales).
  *
- * A NaN or an infinity in a shared row may reach the query rows of all requests of its
- * group.  plan: made with params.prefix_groups > 0.  All other arguments, errors and
+ * Query rows of several requests of a group are multiplied together: a NaN or an infinity in
+ * any row that one request of a shared group sees, its own rows too, may reach the query rows
+ * of the group's other requests.  Rows past a request's length reach nothing.  A
+ * request of length 0 in a shared group, which breaks the contract (status bit 1), may have its
+ * output rows written.  plan: made with params.prefix_groups > 0.  All other arguments, errors and
  * capture rules as mla_decode_run; the other run entry points refuse such a
  * plan and this one refuses any other (MLA_ERR_INVALID_ARG).  Status bit 256
  * (mla_decode_status_offset): a bad prefix_indptr (then nothing is shared) or a
@@ -579,7 +583,8 @@ size_t mla_beam_workspace_size(const mla_beam_params *params);
  *              continue (int32).  Where a request has fewer than k: -inf, -1 and -1.
  * workspace    >= mla_beam_workspace_size bytes, 256-byte aligned, exclusive to the call
  *              until the stream has passed it; needs no zeroing
- * Inputs must not overlap outputs.  Capture-safe.  Call with the tensors' device current.
+ * Inputs must not overlap outputs, but where k is W scores_out may be `scores`.  Capture-safe.
+ * Call with the tensors' device current.
  * Errors (nothing enqueued): MLA_ERR_INVALID_ARG (also an end_token outside the vocabulary
  * with `finished`), MLA_ERR_UNSUPPORTED, MLA_ERR_ALIGNMENT, MLA_ERR_WORKSPACE_TOO_SMALL;
  * MLA_ERR_CUDA if a launch fails.
@@ -644,6 +649,9 @@ size_t mla_decode_workspace_size(const mla_plan_t *plan);
  *                               causal mask base
  *   worker_ranges_offset        int32[n_workers + 1]: persistent worker w (a CTA
  *                               pair) runs items [r[w], r[w + 1])
+ * With prefix groups an item's group is 128 query rows of several requests: g counts from
+ * its owner's first token, [kv_begin, kv_end) are its tiles times 64, the combine entry is its
+ * number among all such groups and seq_len its segments (shared rows, then each request's own).
  * Errors: MLA_ERR_INVALID_ARG on a NULL argument.
  */
 int mla_decode_work_list_layout(const mla_plan_t *plan, size_t *items_offset,
@@ -654,7 +662,9 @@ int mla_decode_work_list_layout(const mla_plan_t *plan, size_t *items_offset,
  * plan property; batch 0 launches none): the partitioner, the decode kernel
  * and the combine kernel, plus, on the FP8 MMA path with a bf16 query (an
  * e4m3 cache, no sparse top-k, no window, e4m3_widen 0), the query split that precedes
- * the decode.  Returns -1 for a NULL plan.
+ * the decode; with prefix groups the partitioner, the decode kernel and the join, plus, where
+ * the plan can widen shared rows, the widening and a decode of the widened rows (3 or 5).
+ * Returns -1 for a NULL plan.
  */
 int32_t mla_decode_kernels_per_run(const mla_plan_t *plan);
 

@@ -502,6 +502,8 @@ class Plan:
         ``sparse_top_k`` > 0 a sparse top-k decode over ``sparse_indices``, one with
         ``prefix_groups`` > 0 a decode over the shared prefixes that ``prefix_lens`` and
         ``prefix_indptr`` give."""
+        if self.prefix_groups == 0 and (prefix_lens is not None or prefix_indptr is not None):
+            raise ValueError("prefix_lens goes with a plan with prefix_groups")
         if self.prefix_groups > 0:
             mla_decode_run_prefix(self.handle, query, kv_cache, block_tables, seq_lens, qo_indptr,
                                   total_q, prefix_lens, prefix_indptr, bmm1_scale, bmm2_scale, out,
@@ -1058,9 +1060,10 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, *, k: Optional[int] 
     offers only ``end_token``, with its score.  Tokens of -inf are not offered, nor is anything
     by a beam whose score is not finite or that has a NaN or +inf among its logits;
     where a request has fewer than ``k`` continuations the rest are -inf, -1 and -1.
-    ``out``: the three results' tensors (fp32, int32, int32).  ``workspace``: a uint8 tensor
-    of at least ``beam_workspace_bytes`` (without one, the thread keeps one for the stream).  What the call makes belongs to ``stream`` (the
-    current one), where the kernels run."""
+    ``out``: the three results' tensors (fp32, int32, int32); the first may be ``scores`` itself,
+    otherwise they overlap no input.  ``workspace``: a uint8 tensor of at least
+    ``beam_workspace_bytes`` (without one, the thread keeps one for the stream).  What the call
+    makes belongs to ``stream`` (the current one), where the kernels run."""
     if logits.dim() != 3 or not logits.is_cuda:
         raise ValueError("logits must be a CUDA tensor [batch, beams, vocab]")
     B, W, V = logits.shape

@@ -11,7 +11,7 @@
 // candidates of two beams is lse, so no rounding of it is common to a row's values: arguments
 // of exponentials carry the product by log2(e) in two parts, sums their rounding errors,
 // parts are joined by powers of two, and scores are pairs of floats (48 bits; the card has
-// few units for 64: with those the join took 10 us instead of 5).
+// few units for 64).
 //
 // What bounds it: the bytes of the logits, where there are many; a chain of two launches, else.
 // A thread streams its own values through shared memory, with no barrier and no copy of another's,
@@ -477,12 +477,13 @@ beam_parts_kernel(Logits in, const float* __restrict__ scores, const unsigned ch
   }
 }
 
-// One block a request: the rows' normalisers, then the k best of all lists.
+// One block a request: the rows' normalisers, then the k best of all lists.  scores_out may be
+// `scores` where k is `beams`: a block reads its request's before a barrier that its results follow.
 constexpr int kDepths = 4, kStaged = 2048;
 
 __global__ void __launch_bounds__(kThreads)
-beam_join_kernel(const float* __restrict__ scores, const unsigned char* __restrict__ finished, int beams, int k,
-                 int vocab, int end_token, Parts in, float* __restrict__ scores_out, int* __restrict__ tokens_out,
+beam_join_kernel(const float* scores, const unsigned char* __restrict__ finished, int beams, int k,
+                 int vocab, int end_token, Parts in, float* scores_out, int* __restrict__ tokens_out,
                  int* __restrict__ parents_out) {
   __shared__ Two row_less[kMaxK];                    // what a row's logits are diminished by: lse - score, without `top`
   __shared__ float row_top[kMaxK], row_score[kMaxK];  // (beams are 64 at most, too); top: 0 but for far ones

@@ -1,5 +1,5 @@
 // Paged MLA decode over a 4-bit cache (mla_fp4.cuh), and over a cache of any format
-// with a sliding window, on sm_103a: a persistent kernel of CTA pairs whose tcgen05
+// with a sliding window or shared prefixes (mla_prefix.cuh), on sm_103a: a persistent kernel of CTA pairs whose tcgen05
 // MMAs span both CTAs (cta_group::2).
 //
 // What it computes, for the 128 query rows of a work item and the KV rows
@@ -35,14 +35,15 @@
 // V and 16 KB of P, its conversion writes 68 KB and reads 15.  (With all of Q in
 // shared memory the MMAs read 48 KB more; with the staged codes read across bank
 // conflicts a long call took 476 us instead of 417.)  bf16 rows come by TMA where the
-// MMAs read them.
+// MMAs read them, and so do shared rows that were widened to f16 once (kF16).
 //
 // Measured, a call: 8 x 2 x 128 heads over 64-128k rows of 4 bits 377 us, 1.08 PFLOP/s
 // (56% of the bf16 rate of a large library product; tensor pipes busy 45% of all cycles,
 // shared memory some 90% of a tile's, bank conflicts among them); 64 x 128 heads over 1-8k
 // rows 103 us, 779 TFLOP/s; window 4096, e4m3, 32 x 4 x 128 heads 182 us, 801 TFLOP/s;
 // window 1024, bf16, 64 x 128 heads 38.8 us, of which some 12 are the launch chain, the
-// first loads and the epilogue.
+// first loads and the epilogue; 32 x 128 heads behind 65536 shared rows of 4 bits, widened,
+// this kernel by itself 346 us, 1.69 PFLOP/s.
 //
 // Warp roles (896 threads): 0 and 3 copy, 1 issues QK (even CTA) and owns TMEM, 2
 // issues PV, 4-11 softmax, correction and epilogue, 12-27 conversion and query

@@ -46,11 +46,11 @@ struct PrefixSegment {
 };
 constexpr int kPrefixNoMask = 1 << 30;  // `mask` of a segment that is seen whole
 
-// Widening.  Over 4 bits and e4m3 a tile's time goes into its conversion to f16 (1.25 and 1.35 us,
+// Widening.  Over 4 bits and e4m3 a tile's time goes into its conversion to f16 (1.25 and 1.36 us,
 // where rows that come by TMA take 0.88).  Where four row groups and more walk the same shared rows
 // these are widened once, into the workspace, and walked there, by a list of items of its
 // own; the row groups' own rows stay in the first list, and all their query rows are joined.
-// (32 x 128 heads over 65536 rows of 4 bits: 568 us a call without.  Below four the copy, its launch and
+// (32 x 128 heads over 65536 rows of 4 bits: 569 us a call without, 396-399 with.  Below four the copy, its launch and
 // the join take what it saves.)
 constexpr int kWideRowGroups = 4;
 constexpr long long kWideBytes = 1LL << 30;  // of widened rows at most
@@ -93,7 +93,7 @@ struct PrefixLayout {
 // largest of them to [2^14, 2^15), so that each is off by 2^-11 of itself or 2^-39 of the
 // largest.  The powers, a byte for each row and 16 dims, follow the LSEs.  (fp32 partials were
 // as near and twice the bytes, which bound the join: 6 x 10 requests of 1 to 4 tokens, 64
-// heads: 143 us instead of 136.)
+// heads: 143 us instead of 132.)
 __host__ __device__ inline size_t prefix_scale_offset(const Layout& lay) {
   return align_up(lay.part_lse + sizeof(float) * kPrefixRows * (size_t)lay.max_partials, 256);
 }

@@ -332,3 +332,17 @@ def test_reorder_in_a_graph_and_on_a_stream():
     torch.cuda.synchronize()
     assert torch.equal(b.tables, c.tables) and torch.equal(b.spare, c.spare)
     assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(b.caches, c.caches))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,W,V,ties", [(1, 1, 1, False), (5, 4, 20011, False), (3, 64, 300, False), (4, 8, 9000, True)])
+def test_scores_in_place(B, W, V, ties):
+    # (rows that are all equal offer more ties than the join has room for)
+    x, c = inputs("fp32", B, W, V, 31)
+    if ties:
+        x.zero_()
+        c.zero_()
+    want = mla.beam_select(x, c, k=W)
+    out = (c, torch.empty_like(want[1]), torch.empty_like(want[2]))
+    mla.beam_select(x, c, k=W, out=out)
+    assert all(torch.equal(a, b) for a, b in zip(want, out))

@@ -1,6 +1,8 @@
 """Decode over a batch whose requests share their first rows, over caches of every format,
 against a plain 64-bit form that takes every request by itself (tests/attention_ref.py).
 Rows that no query row sees, and the pages that other requests' shared ones replace, are NaN."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -206,3 +208,44 @@ def test_refusals():
     with pytest.raises(mla.MlaDecodeError):
         mla.Plan(batch=4, num_heads=16, max_seq_len_q=1, max_seq_len=200, page_size=64, max_pages_per_req=8,
                  num_pages=64, packed=False, prefix_groups=5)
+
+
+@pytest.mark.gpu
+def test_a_plan_without_groups_refuses_their_lengths():
+    c = PrefixCase("bf16", 64, [4], [100], [10], [1], 16, seed=1)
+    p = mla.Plan(batch=4, num_heads=16, max_seq_len_q=1, max_seq_len=c.max_len, page_size=64,
+                 max_pages_per_req=c.tables.shape[1], num_pages=c.cache.shape[0], packed=False)
+    for kw in (dict(prefix_lens=c.prefix_lens), dict(prefix_indptr=c.prefix_lens)):
+        with pytest.raises(ValueError):
+            p.run(c.query, c.cache, c.tables, c.lens, c.out, workspace=c.workspace, **kw)
+
+
+@pytest.mark.gpu
+def test_the_static_workspace_refuses_a_prefix_plan():
+    c = PrefixCase("bf16", 64, [4], [100], [10], [1], 16, seed=1)
+    before = c.out.clone()
+    rc = mla.load_library().mla_decode_run_static_workspace(
+        ctypes.c_void_p(c.plan.handle), c.query.data_ptr(), c.cache.data_ptr(), c.tables.data_ptr(),
+        c.lens.data_ptr(), None, ctypes.c_int64(0), ctypes.c_float(1.0), ctypes.c_float(1.0),
+        ctypes.c_void_p(c.out.data_ptr()), None, ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    assert rc != mla.MLA_OK
+    torch.cuda.synchronize()
+    assert torch.equal(c.out.view(torch.int16), before.view(torch.int16))
+
+
+@pytest.mark.gpu
+def test_repeated_pages_and_no_lse():
+    """Every request's table names one page again and again; no LSE is wanted."""
+    c = PrefixCase("bf16", 64, [12], [640], [70], [1], 16, seed=3)
+    q = c.query.view(12, 1, 16, 576)
+    tables = c.tables[:1, :1].repeat(12, c.tables.shape[1]).contiguous()
+    lens = torch.full((12,), 640, dtype=torch.int32, device="cuda")
+    call = lambda **kw: mla.decode(q, c.cache, c.workspace, tables, lens, 640, bmm1_scale=0.07, **kw)  # noqa: E731
+    got = call(prefix_lens=torch.tensor([640], dtype=torch.int32, device="cuda"))
+    rows = c.cache.view(-1, 64, 576)[tables[0, 0].item()].double().repeat(10, 1)
+    s = q[:, 0].double() @ rows.T * 0.07
+    p = torch.softmax(s, -1)
+    want, size = p @ rows[:, :512], p @ rows[:, :512].abs()
+    # P rounds to bf16 in the sum and in its divisor (2^-8 of `size` each), O once more; a partial
+    # to f16, 2^-11 of itself and 2^-39 of its largest, and scores in fp32: 2^-10 of `size`
+    assert ((got[:, 0].double() - want).abs() <= 2 ** -8 * (2 * size + want.abs()) + 2 ** -10 * size).all()
