@@ -50,7 +50,7 @@ constexpr int kPrefixNoMask = 1 << 30;  // `mask` of a segment that is seen whol
 // where rows that come by TMA take 0.88).  Where four row groups and more walk the same shared rows
 // these are widened once, into the workspace, and walked there, by a list of items of its
 // own; the row groups' own rows stay in the first list, and all their query rows are joined.
-// (32 x 128 heads over 65536 rows of 4 bits: 569 us a call without, 396-399 with.  Below four the copy, its launch and
+// (32 x 128 heads over 65536 rows of 4 bits: 569 us a call without, 396-401 with.  Below four the copy, its launch and
 // the join take what it saves.)
 constexpr int kWideRowGroups = 4;
 constexpr long long kWideBytes = 1LL << 30;  // of widened rows at most
