@@ -335,9 +335,10 @@ def test_reorder_in_a_graph_and_on_a_stream():
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("B,W,V,ties", [(1, 1, 1, False), (5, 4, 20011, False), (3, 64, 300, False), (4, 8, 9000, True)])
+@pytest.mark.parametrize("B,W,V,ties", [(1, 1, 1, False), (5, 4, 20011, False), (3, 64, 300, False), (4, 8, 9000, True),
+                                         (3, 64, 300, True), (2, 64, 9000, True)])
 def test_scores_in_place(B, W, V, ties):
-    # (rows that are all equal offer more ties than the join has room for)
+    # (rows that are all equal: 64 lists of 64 are more ties than the join has room for)
     x, c = inputs("fp32", B, W, V, 31)
     if ties:
         x.zero_()
@@ -346,3 +347,30 @@ def test_scores_in_place(B, W, V, ties):
     out = (c, torch.empty_like(want[1]), torch.empty_like(want[2]))
     mla.beam_select(x, c, k=W, out=out)
     assert all(torch.equal(a, b) for a, b in zip(want, out))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "fp4"])
+def test_reorder_past_32_bits_of_the_cache(kind):
+    """Pages at the end of a cache of more than 4 GiB."""
+    W, ps, rest = 4, 64, 29
+    row = {"bf16": 1152, "e4m3": 576, "fp4": 324}[kind]
+    dtype, width = {"bf16": (torch.bfloat16, 576), "e4m3": (torch.float8_e4m3fn, 576), "fp4": (torch.uint8, 324)}[kind]
+    above = (1 << 32) // (ps * row) + 1
+    raw = torch.zeros((above + 2 * W, ps * row), dtype=torch.uint8, device="cuda")
+    raw[above:above + W] = torch.randint(0, 256, (W, ps * row), dtype=torch.uint8, device="cuda")
+    before = raw[above:above + W].clone()
+    ids = torch.arange(above, above + 2 * W, dtype=torch.int32, device="cuda")
+    tables, spare = ids[:W].view(W, 1).contiguous(), ids[W:].contiguous()
+    lens = torch.full((W,), rest, dtype=torch.int32, device="cuda")
+    mla.cache_reorder(raw.view(-1).view(dtype).view(-1, ps, width), tables, lens,
+                      torch.tensor([[2, 1, 0, 2]], dtype=torch.int32, device="cuda"), spare)
+    assert tables[:, 0].tolist() == [above + W, above + 1, above + W + 2, above + W + 3]
+    assert spare.tolist() == [above, above + W + 1, above + 2, above + 3]
+    code = 288 if kind == "fp4" else row
+    for b, p in enumerate([2, 1, 0, 2]):
+        now = raw[int(tables[b, 0])]
+        assert torch.equal(now[:rest * code], before[p][:rest * code])
+        if kind == "fp4":
+            assert torch.equal(now[ps * 288:ps * 288 + rest * 36], before[p][ps * 288:ps * 288 + rest * 36])
+    assert torch.equal(raw[above:above + W], before)

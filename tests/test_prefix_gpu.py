@@ -249,3 +249,28 @@ def test_repeated_pages_and_no_lse():
     # P rounds to bf16 in the sum and in its divisor (2^-8 of `size` each), O once more; a partial
     # to f16, 2^-11 of itself and 2^-39 of its largest, and scores in fp32: 2^-10 of `size`
     assert ((got[:, 0].double() - want).abs() <= 2 ** -8 * (2 * size + want.abs()) + 2 ** -10 * size).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "fp4"])
+def test_pages_past_32_bits_of_the_cache(kind):
+    """The same pages at the end of a cache of more than 4 GiB, to the bit."""
+    c = PrefixCase(kind, 64, [64], [1500], [20, 300], [1], 16, seed=5)
+    q = c.query.view(64, 1, 16, 576)
+    page = c.cache[0].numel() * c.cache.element_size()
+    above = (1 << 32) // page + 1
+    big = torch.zeros((above + c.cache.shape[0], page), dtype=torch.uint8, device="cuda").view(c.cache.dtype)
+    big = big.view(-1, *c.cache.shape[1:])
+    big.view(torch.uint8)[above:] = c.cache.view(torch.uint8)
+    got = [mla.decode(q, cache, c.workspace, tables, c.lens, c.max_len, bmm1_scale=0.07, prefix_lens=c.prefix_lens,
+                      prefix_indptr=c.prefix_indptr)
+           for cache, tables in ((c.cache, c.tables), (big, c.tables + above))]
+    assert torch.equal(got[0].view(torch.int16), got[1].view(torch.int16))
+
+
+@pytest.mark.gpu
+def test_no_request():
+    c = PrefixCase("bf16", 64, [4], [100], [10], [1], 16, seed=1)
+    out = mla.decode(c.query.view(4, 1, 16, 576)[:0], c.cache, c.workspace, c.tables[:0], c.lens[:0], c.max_len,
+                     prefix_lens=c.prefix_lens)
+    assert out.shape[0] == 0
