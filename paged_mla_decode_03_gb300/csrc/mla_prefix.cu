@@ -237,8 +237,8 @@ partition_prefix_kernel(Problem p, PrefixArgs pa, Layout lay, PrefixLayout pl, c
       s.tokens[g] = on ? tokens : 0;
       s.shared[g] = T;
       s.wide[g] = on && wide;
-      if (on) sh.any = 1;
-      if (on && wide) sh.any_wide = 1;
+      if (on) atomicOr(&sh.any, 1);
+      if (on && wide) atomicOr(&sh.any_wide, 1);
     }
     if (on)
       for (int b = lo + lane; b < hi; b += 32) {
@@ -346,6 +346,7 @@ partition_prefix_kernel(Problem p, PrefixArgs pa, Layout lay, PrefixLayout pl, c
       if (lane == 0) atomicAdd(&sh.total, other);
       __syncthreads();
       widens = sh.total / n + 3 * (int)kCutTiles < min(alone, shared);
+      __syncthreads();  // (every thread has read the sum before a scan clears it)
       if (widens) {
         scan_list(0);
         break;
