@@ -121,7 +121,8 @@ typedef struct mla_plan_s mla_plan_t; /* opaque; host memory only */
  * and size the workspace.  Host only; not capture-safe (it sets kernel
  * attributes).  On success *plan receives a new plan (free with
  * mla_decode_destroy) and *workspace_bytes the number of bytes the caller must
- * provide to every mla_decode_run of this plan.
+ * provide to every mla_decode_run of this plan (mla_decode_run_prefix takes less,
+ * down to mla_decode_workspace_least).
  * Errors: MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED, MLA_ERR_CUDA.
  */
 int mla_decode_plan(const mla_decode_params *params, mla_plan_t **plan,
@@ -372,6 +373,13 @@ int mla_decode_run_sparse(const mla_plan_t *plan, const void *query, const void 
  * rounding; the shared rows are read once for 128 query rows of a group, whichever requests
  * they belong to, where each request reads them for itself otherwise.  Over 4 bits and e4m3,
  * rows that four and more such sets of query rows share are widened to f16 in the workspace.
+ *
+ * workspace      a plan can widen where its cache is of 4 bits or e4m3, its query rows make
+ *                four sets a group on the average, and G * max_seq_len rows of f16 (1152
+ *                bytes each) are 1 GiB at most.  The planned size has that room.  A run that
+ *                is given less, but mla_decode_workspace_least bytes, widens nothing and
+ *                launches three kernels instead of five; so a caller whose prefixes are few
+ *                or short may decline.
  *
  * prefix_lens    device int32 [G], G = params.prefix_groups: the first
  *                prefix_lens[g] rows of group g's requests hold the same values.
@@ -635,6 +643,9 @@ int mla_cache_reorder(const mla_reorder_params *params, void *const *caches, int
 
 /* Workspace bytes of a plan (the value mla_decode_plan returned). */
 size_t mla_decode_workspace_size(const mla_plan_t *plan);
+/* Workspace bytes below which a run of the plan returns MLA_ERR_WORKSPACE_TOO_SMALL: the same, but
+ * for plans with prefix groups that can widen (mla_decode_run_prefix). */
+size_t mla_decode_workspace_least(const mla_plan_t *plan);
 
 /*
  * Where a run leaves its split-KV work list in the workspace, for tests and
@@ -663,7 +674,8 @@ int mla_decode_work_list_layout(const mla_plan_t *plan, size_t *items_offset,
  * and the combine kernel, plus, on the FP8 MMA path with a bf16 query (an
  * e4m3 cache, no sparse top-k, no window, e4m3_widen 0), the query split that precedes
  * the decode; with prefix groups the partitioner, the decode kernel and the join, plus, where
- * the plan can widen shared rows, the widening and a decode of the widened rows (3 or 5).
+ * the plan can widen shared rows, the widening and a decode of the widened rows (3 or 5; a run
+ * in less than the planned workspace 3).
  * Returns -1 for a NULL plan.
  */
 int32_t mla_decode_kernels_per_run(const mla_plan_t *plan);

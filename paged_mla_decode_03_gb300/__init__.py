@@ -31,6 +31,7 @@ __all__ = [
     "MLA_OK", "MlaDecodeError", "MlaDecodeParams", "load_library", "library_path",
     "mla_decode_plan", "mla_decode_run", "mla_decode_run_profiled", "mla_decode_run_dcp",
     "mla_decode_run_sparse", "mla_decode_run_prefix", "mla_decode_destroy", "mla_decode_workspace_size",
+    "mla_decode_workspace_least",
     "mla_decode_status_offset", "mla_decode_status_string", "Plan", "decode",
     "HEAD_DIM_QK", "HEAD_DIM_V", "FP4_ROW_BYTES", "MlaCacheParams", "MlaRopeParams",
     "cache_append", "cache_gather", "rope_table", "MlaBeamParams", "MlaReorderParams",
@@ -206,6 +207,8 @@ def load_library():
     lib.mla_decode_destroy.restype = None
     lib.mla_decode_workspace_size.argtypes = [vp]
     lib.mla_decode_workspace_size.restype = sz
+    lib.mla_decode_workspace_least.argtypes = [vp]
+    lib.mla_decode_workspace_least.restype = sz
     lib.mla_decode_work_list_layout.argtypes = [vp, ctypes.POINTER(sz), ctypes.POINTER(sz),
                                                 ctypes.POINTER(i32)]
     lib.mla_decode_work_list_layout.restype = ctypes.c_int
@@ -245,6 +248,12 @@ def mla_decode_destroy(plan: Optional[int]) -> None:
 
 def mla_decode_workspace_size(plan: int) -> int:
     return int(load_library().mla_decode_workspace_size(ctypes.c_void_p(plan)))
+
+
+def mla_decode_workspace_least(plan: int) -> int:
+    """Workspace bytes below which a run of the plan is refused: less than its size only where
+    shared prefixes may be widened."""
+    return int(load_library().mla_decode_workspace_least(ctypes.c_void_p(plan)))
 
 
 def mla_decode_work_list_layout(plan: int) -> Tuple[int, int, int]:
@@ -462,7 +471,8 @@ def mla_decode_run_profiled(plan: int, query, kv_cache, block_tables, seq_lens, 
 
 
 class Plan:
-    """Owns one C plan; ``run`` enqueues a decode with it."""
+    """Owns one C plan; ``run`` enqueues a decode with it, in a workspace of ``workspace_bytes``
+    (of ``workspace_least`` where shared prefixes need not be widened)."""
 
     def __init__(self, *, batch: int, num_heads: int, max_seq_len_q: int, max_seq_len: int,
                  page_size: int, max_pages_per_req: int, num_pages: int, packed: bool,
@@ -491,6 +501,7 @@ class Plan:
         self.prefix_groups = prefix_groups
         self.sparse_top_k = sparse_top_k
         self.handle, self.workspace_bytes = mla_decode_plan(self.params)
+        self.workspace_least = mla_decode_workspace_least(self.handle)
 
     def run(self, query, kv_cache, block_tables, seq_lens, out, *, qo_indptr=None, total_q=0,
             lse=None, workspace=None, bmm1_scale=1.0, bmm2_scale=1.0, stream=None,
@@ -577,7 +588,8 @@ def decode(query: torch.Tensor, kv_cache: torch.Tensor, workspace_buffer: torch.
     ``kv_cache``: bf16 or float8_e4m3fn, ``[pages, page_size, 576]`` or
     ``[pages, 1, page_size, 576]``, or 4-bit, uint8 ``[pages, page_size, 324]``
     (``MLA_KV_FP4_E2M1`` in the header).  ``workspace_buffer`` must hold at least
-    the plan's workspace bytes (see ``Plan``).  Plans are cached per static key.
+    the plan's workspace bytes (see ``Plan``); with shared prefixes its ``workspace_least``
+    will do, without the room to widen rows that many requests share.  Plans are cached per static key.
     ``bmm1_scale`` / ``bmm2_scale``: floats, or one-element fp32 CUDA tensors the
     kernels read at run time (for scales that change between graph replays).
     ``cp_world`` / ``cp_rank`` / ``causal_seqlens_kv_global``: one rank of a
@@ -648,8 +660,8 @@ def decode(query: torch.Tensor, kv_cache: torch.Tensor, workspace_buffer: torch.
                     cp_rank=int(cp_rank), sparse_top_k=top_k, e4m3_widen=e4m3_widen,
                     window=int(window), sinks=int(sinks), prefix_groups=groups)
         _plans[key] = plan
-    if workspace_buffer.numel() * workspace_buffer.element_size() < plan.workspace_bytes:
-        raise ValueError(f"workspace_buffer needs {plan.workspace_bytes} bytes")
+    if workspace_buffer.numel() * workspace_buffer.element_size() < plan.workspace_least:
+        raise ValueError(f"workspace_buffer needs {plan.workspace_least} bytes")
     if out is None:
         out = torch.empty(out_shape, dtype=torch.bfloat16, device=query.device)
     if return_lse and lse is None:

@@ -48,6 +48,9 @@ struct mla_plan_s {
   mla_decode_params prm;
   mla::Layout lay;
   mla::PrefixLayout pre;  // plans with prefix groups
+  // what a run cannot do without: the same, but for prefix groups without the room to widen
+  mla::Layout lay_least;
+  mla::PrefixLayout pre_least;
   int sm_count;
   int combine_grid;
   // mla_decode_run_host copies the query on this stream while the
@@ -237,10 +240,13 @@ int mla_decode_plan(const mla_decode_params* params, mla_plan_t** plan, size_t* 
   int rc = MLA_OK;
   if (p.prefix_groups == 0)
     rc = make_layout(p, n_pairs, 2 * n_pairs, rows_per_group, &pl->lay);
-  else if (!mla::make_prefix_layout(p.batch, p.num_heads, p.max_seq_len_q, p.packed != 0, p.max_total_q, p.max_seq_len, p.kv_dtype,
-                                    p.prefix_groups, std::min(n_pairs, mla::kPrefixWorkers), kHeaderBytes, &pl->lay,
-                                    &pl->pre))
-    rc = MLA_ERR_UNSUPPORTED;
+  else
+    for (const bool widen : {true, false})
+      if (!mla::make_prefix_layout(p.batch, p.num_heads, p.max_seq_len_q, p.packed != 0, p.max_total_q, p.max_seq_len,
+                                   p.kv_dtype, p.prefix_groups, std::min(n_pairs, mla::kPrefixWorkers), kHeaderBytes,
+                                   widen ? &pl->lay : &pl->lay_least, widen ? &pl->pre : &pl->pre_least, widen))
+        rc = MLA_ERR_UNSUPPORTED;
+  if (p.prefix_groups == 0) pl->lay_least = pl->lay;
   if (rc != MLA_OK) {
     delete pl;
     return rc;
@@ -331,7 +337,11 @@ int run_impl(const mla_plan_t* plan, const void* query, const void* kv_cache,
   } else if (qo_indptr) {
     return MLA_ERR_INVALID_ARG;
   }
-  if (workspace_bytes < plan->lay.total) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  if (workspace_bytes < plan->lay_least.total) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  // a smaller workspace than the plan's: nothing is widened
+  const bool least = workspace_bytes < plan->lay.total;
+  const mla::Layout& lay = least ? plan->lay_least : plan->lay;
+  const mla::PrefixLayout& pre = least ? plan->pre_least : plan->pre;
   if (!aligned(query, 16) || !aligned(kv_cache, 16) || !aligned(out, 16) ||
       !aligned(workspace, 256) || !aligned(block_tables, 4) || !aligned(seq_lens, 4) ||
       (lse && !aligned(lse, 4)) || (qo_indptr && !aligned(qo_indptr, 4)))
@@ -380,32 +390,32 @@ int run_impl(const mla_plan_t* plan, const void* query, const void* kv_cache,
     if (cudaStreamIsCapturing(s, &cs) != cudaSuccess) return MLA_ERR_CUDA;
     if (cs == cudaStreamCaptureStatusActive) ev_flags = cudaEventRecordExternal;
   }
-  if ((prefix ? mla::launch_partition_prefix(p, *prefix, plan->lay, plan->pre, workspace, s)
-              : mla::launch_partition(p, plan->lay, workspace, s)) != cudaSuccess)
+  if ((prefix ? mla::launch_partition_prefix(p, *prefix, lay, pre, workspace, s)
+              : mla::launch_partition(p, lay, workspace, s)) != cudaSuccess)
     return MLA_ERR_CUDA;
-  if (prefix && plan->pre.wide_tiles > 0 &&
-      mla::launch_widen_prefix(p, prefix->groups, plan->pre, workspace, plan->sm_count, s) != cudaSuccess)
+  if (prefix && pre.wide_tiles > 0 &&
+      mla::launch_widen_prefix(p, prefix->groups, pre, workspace, plan->sm_count, s) != cudaSuccess)
     return MLA_ERR_CUDA;
   // work enqueued elsewhere that the decode needs (the host entry's query copy)
   if (join_before_decode && cudaStreamWaitEvent(s, join_before_decode, 0) != cudaSuccess)
     return MLA_ERR_CUDA;
   if (uses_q_split(prm) &&
-      mla::launch_qsplit(p, plan->lay, workspace, plan->sm_count, s) != cudaSuccess)
+      mla::launch_qsplit(p, lay, workspace, plan->sm_count, s) != cudaSuccess)
     return MLA_ERR_CUDA;
   if (event_before_decode &&
       cudaEventRecordWithFlags(static_cast<cudaEvent_t>(event_before_decode), s, ev_flags) !=
           cudaSuccess)
     return MLA_ERR_CUDA;
-  if ((prefix               ? mla::launch_decode_prefix(p, plan->lay, plan->pre, workspace, s)
-       : uses_pair_mma(prm) ? mla::launch_decode_pair(p, plan->lay, workspace, s)
-                          : mla::launch_decode_sm103(p, plan->lay, workspace, s)) != cudaSuccess)
+  if ((prefix               ? mla::launch_decode_prefix(p, lay, pre, workspace, s)
+       : uses_pair_mma(prm) ? mla::launch_decode_pair(p, lay, workspace, s)
+                          : mla::launch_decode_sm103(p, lay, workspace, s)) != cudaSuccess)
     return MLA_ERR_CUDA;
   if (event_after_decode &&
       cudaEventRecordWithFlags(static_cast<cudaEvent_t>(event_after_decode), s, ev_flags) !=
           cudaSuccess)
     return MLA_ERR_CUDA;
-  if ((prefix ? mla::launch_join_prefix(p, plan->lay, plan->pre, workspace, plan->sm_count, s)
-              : mla::launch_combine(p, plan->lay, workspace, plan->combine_grid, s)) != cudaSuccess)
+  if ((prefix ? mla::launch_join_prefix(p, lay, pre, workspace, plan->sm_count, s)
+              : mla::launch_combine(p, lay, workspace, plan->combine_grid, s)) != cudaSuccess)
     return MLA_ERR_CUDA;
   return MLA_OK;
 }
@@ -597,6 +607,7 @@ void mla_decode_destroy(mla_plan_t* plan) {
 }
 
 size_t mla_decode_workspace_size(const mla_plan_t* plan) { return plan ? plan->lay.total : 0; }
+size_t mla_decode_workspace_least(const mla_plan_t* plan) { return plan ? plan->lay_least.total : 0; }
 
 int mla_decode_work_list_layout(const mla_plan_t* plan, size_t* items_offset,
                                 size_t* worker_ranges_offset, int32_t* n_workers) {

@@ -109,10 +109,11 @@ __host__ __device__ inline size_t prefix_scratch_bytes(long long batch, long lon
   return align_up(sizeof(int) * (size_t)(8 * batch + 2 + 5 * groups + 4 * row_groups + 2), 16);
 }
 
-// The workspace of a plan with `groups` prefix groups; false: too large a plan.
+// The workspace of a plan with `groups` prefix groups; false: too large a plan.  may_widen: with the room
+// that widening wants, where it may pay at all.  Without, it is what every run of the plan needs.
 inline bool make_prefix_layout(long long batch, long long heads, long long max_q, bool packed, long long max_total_q,
                                long long max_seq_len, int kv_dtype, long long groups, int n_workers, size_t header,
-                               Layout* lay, PrefixLayout* pre) {
+                               Layout* lay, PrefixLayout* pre, bool may_widen = true) {
   const long long R = kPrefixRows;
   auto ceil_to = [](long long a, long long b) { return (a + b - 1) / b; };
   long long rg = batch * ceil_to(max_q * heads, R);
@@ -130,7 +131,7 @@ inline bool make_prefix_layout(long long batch, long long heads, long long max_q
   // widening pays for four row groups a prefix group on the average, and has its room
   const long long tokens = packed ? max_total_q : batch * max_q;
   const long long tiles = groups * ((max_seq_len + kKvTile - 1) / kKvTile);
-  const bool wide = kv_dtype != 0 && ceil_to(tokens * heads, R) >= kWideRowGroups * groups &&
+  const bool wide = may_widen && kv_dtype != 0 && ceil_to(tokens * heads, R) >= kWideRowGroups * groups &&
                     tiles * kKvTile * 2 * kQkDim <= kWideBytes;
   pre->wide_tiles = wide ? (int)tiles : 0;
   // cut row groups have partials, all of those with widened rows
