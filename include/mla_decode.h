@@ -629,8 +629,9 @@ typedef struct mla_reorder_params {
  * parents      int32 [B, W]; -1 (or anything outside [0, W)): the beam stays as it is
  * spare_pages  int32 [B * W], changed in place: one page of each beam, in no table
  * status       int32 device word or NULL: bits of mla_decode_status_offset are ORed in (1:
- *              lengths, 2: a parent outside [-1, W), 16: a page id outside [0, num_pages);
- *              its rows are not copied).
+ *              lengths, 2: a parent outside [-1, W), 16: a spare page, or the parent's page of
+ *              the last rows, outside [0, num_pages): these rows are not copied, and the
+ *              beam's entry for them and its spare page stay as they are).
  * Copies come first, then the tables and spare pages change; two launches, and one more for
  * every 64 layers past the first 64.  Capture-safe; no workspace.
  * Call with the tensors' device current.

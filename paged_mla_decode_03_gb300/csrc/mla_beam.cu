@@ -708,6 +708,7 @@ __device__ __forceinline__ int parent_of(const ReorderArgs& a, int b, int w) {
   const int p = a.parents[b];
   return p >= 0 && p < a.beams ? p : w;  // none: the beam stays as it is
 }
+__device__ __forceinline__ bool is_page(const ReorderArgs& a, int id) { return id >= 0 && id < a.num_pages; }
 
 __global__ void __launch_bounds__(kThreads)
 reorder_copy_kernel(const __grid_constant__ ReorderArgs a) {
@@ -719,7 +720,7 @@ reorder_copy_kernel(const __grid_constant__ ReorderArgs a) {
   if (threadIdx.x == 0 && a.status && (a.parents[b] < -1 || a.parents[b] >= a.beams)) atomicOr(a.status, kStatusQLen);
   if (p == w || rest == 0) return;
   const int src = a.block_tables[(size_t)(request * a.beams + p) * a.max_pages + whole], dst = a.spare[b];
-  if (src < 0 || src >= a.num_pages || dst < 0 || dst >= a.num_pages) {
+  if (!is_page(a, src) || !is_page(a, dst)) {
     if (threadIdx.x == 0 && a.status) atomicOr(a.status, kStatusPage);
     return;
   }
@@ -768,7 +769,9 @@ reorder_tables_kernel(const __grid_constant__ ReorderArgs a) {
       if (c < whole) {
         tables[(size_t)w * a.max_pages + c] = tile[p][lane];
       } else {
-        tables[(size_t)w * a.max_pages + c] = a.spare[b];
+        const int src = tile[p][lane], dst = a.spare[b];
+        if (!is_page(a, src) || !is_page(a, dst)) continue;  // (nothing was copied, and it is flagged)
+        tables[(size_t)w * a.max_pages + c] = dst;
         a.spare[b] = tile[w][lane];
       }
     }
