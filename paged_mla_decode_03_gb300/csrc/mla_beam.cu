@@ -8,10 +8,14 @@
 // Within a beam the order is that of the logits themselves, so each block keeps the k largest
 // logits of its part of a row, exactly, beside the part's sum of exponentials; one block a
 // request then compares the scores of all parts' candidates.  What decides between nearly equal
-// candidates of two beams is lse, so no rounding of it is common to a row's values: arguments
-// of exponentials carry the product by log2(e) in two parts, sums their rounding errors,
-// parts are joined by powers of two, and scores are pairs of floats (48 bits; the card has
-// few units for 64).
+// candidates of two beams is lse.  Its sum is of 2^(x log2(e) - n), n whole: the product in two
+// parts, sums with their rounding errors, everything else powers of two, which are exact; and
+// the largest logit's own term divides it, so that what is wrong with that term, which may
+// be all of a sum, leaves lse.  So lse is off by some 2^-25, and by the exponential's own 2^-21
+// at most where terms far below the largest make up the sum.  Scores are pairs of floats (48
+// bits; the card has few units for 64).  Which thread takes a value, and in which order,
+// is by its index alone and not by where the row lies in memory: rows with the same logits have the
+// same lse, to the bit, and their ties go by index.
 //
 // What bounds it: the bytes of the logits, where there are many; a chain of two launches, else.
 // A thread streams its own values through shared memory, with no barrier and no copy of another's,
@@ -44,7 +48,8 @@ constexpr int kRoom = 1024;             // candidates collected at most (ties ma
 constexpr int kMaxLists = 128;          // candidate lists of a request at most
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kStretches = 16;          // of a thread's part, each with its maximum
-constexpr size_t kRing = (size_t)kStages * kVectors * kThreads * 16;
+constexpr int kWarpUnits = 33;          // of a warp's 32 units, and the one behind them
+constexpr size_t kRing = (size_t)kStages * kVectors * kWarps * kWarpUnits * 16;
 constexpr size_t kSmem = kRing + sizeof(float) * kStretches * kThreads;
 constexpr float kNone = -INFINITY;
 
@@ -99,6 +104,10 @@ __device__ __forceinline__ float largest(const uint4* w) {
 
 // e^d for d <= 0: the product by log2(e) in two parts, so that its rounding is not of log2(e).
 __device__ __forceinline__ float exp_of(float d) { return ptx::ex2(fmaf(d, kLog2eHi, d * kLog2eLo)); }
+// 2^d for a whole d of 0 at most, exact; 0 below 2^-126.
+__device__ __forceinline__ float whole_power(float d) {
+  return d < -126.f ? 0.f : __uint_as_float((uint32_t)(127 + (int)d) << 23);
+}
 
 // A number as the sum of two floats, the second at most half a step of the first.
 struct Two {
@@ -167,15 +176,29 @@ __device__ __forceinline__ float power_of(Two a, Two b) {
   return d < -150.f ? 0.f : ptx::ex2(d + (a.l - b.l));
 }
 
-// A part of a row, as one block found it: sum_v exp(x_v) = (sum.h + sum.l) 2^power, power the
-// whole number next to its maximum times log2(e).  For a maximum of 2^20 and more, whose
-// powers a float does not hold, the sum is of exp(x_v - top).
-struct Part {
-  float top;
-  int power;
-  Two sum;
+// What a sum of exponentials is relative to: 2^power, the whole number next to its largest
+// argument times log2(e); where that is of 2^20 and more, whose powers a float does not hold,
+// e^top.  A sum of nothing (top of -infinity) is 0, or a NaN that it has met.
+struct Reference {
+  float top, power;
 };
 __device__ __forceinline__ bool is_far(float top) { return !(fabsf(top) < 1048576.f); }
+__device__ __forceinline__ Reference reference_of(float top) {
+  return {top, is_far(top) ? 0.f : rintf(top * kLog2eHi)};
+}
+// The factor that takes a sum from a to b, b the higher one.
+__device__ __forceinline__ float between(Reference a, Reference b) {
+  if (!is_far(a.top) && !is_far(b.top)) return whole_power(a.power - b.power);
+  if (b.top == kNone) return 1.f;
+  if (is_far(a.top) && is_far(b.top)) return exp_of(a.top - b.top);
+  return power_of(is_far(a.top) ? log2_of(a.top) : Two{a.power, 0.f}, is_far(b.top) ? log2_of(b.top) : Two{b.power, 0.f});
+}
+
+// A part of a row, as one block found it.
+struct Part {
+  Reference at;
+  Two sum;
+};
 
 struct Parts {
   Part* part;    // [rows][parts]
@@ -246,75 +269,94 @@ beam_parts_kernel(Logits in, const float* __restrict__ scores, const unsigned ch
   // a beam that has ended, or has no score, offers nothing that its logits decide
   if ((finished && finished[row]) || !(fabsf(scores[row]) < INFINITY)) return;
   const T* x = static_cast<const T*>(in.base) + (row / in.beams) * in.batch_stride + (row % in.beams) * in.beam_stride;
-  // units of 16 aligned bytes; the row's first and last may reach out of it
+  // Units of values [u kPer, (u + 1) kPer).  Copies are of 16 aligned bytes; where the row does not
+  // start on one, `off` values before it do, and a unit is the end of one copy and the start of the next.
   const int off = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
-  const int units = (off + in.vocab + kPer - 1) / kPer;
+  const int units = (in.vocab + kPer - 1) / kPer;
   const int u0 = part * out.share * kUnits, u1 = min(u0 + out.share * kUnits, units);
-  const int f0 = off > 0 ? max(u0, 1) : u0, f1 = min(u1, (off + in.vocab) / kPer);  // whole ones
+  const int f0 = off > 0 ? 1 : 0, f1 = (off + in.vocab) / kPer;  // copies [f0, f1) lie inside the row
   constexpr uint32_t kNothing = sizeof(T) == 4 ? 0xff800000u
                                 : std::is_same<T, __nv_bfloat16>::value ? 0xff80ff80u : 0xfc00fc00u;  // -inf
-  auto unit_at = [&](int u) { return reinterpret_cast<const uint4*>(x + ((long long)u * kPer - off)); };
-  // an edge of the row: thread 0's the first unit, thread 1's the last, where they are not whole
-  auto edge = [&]() -> uint4 {
-    const int u = tid == 0 ? 0 : units - 1;
+  auto copy_at = [&](int u) { return reinterpret_cast<const uint4*>(x + ((long long)u * kPer - off)); };
+  // values [first, first + kPer) one by one, -inf where the row has none
+  auto pieces = [&](int first) -> uint4 {
     uint32_t e[4] = {kNothing, kNothing, kNothing, kNothing};
-    const bool mine = tid == 0 ? u0 == 0 && f0 > 0 : tid == 1 && u0 < units && u1 == units && f1 < units &&
-                                                                  !(units == 1 && off > 0);
-    if (mine) {
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const int i = u * kPer - off + j;
-        if (i < 0 || i >= in.vocab) continue;
-        if constexpr (sizeof(T) == 4) {
-          e[j] = reinterpret_cast<const uint32_t*>(x)[i];
-        } else {
-          const uint32_t bits = reinterpret_cast<const unsigned short*>(x)[i];
-          e[j / 2] = j & 1 ? (e[j / 2] & 0xffffu) | bits << 16 : (e[j / 2] & 0xffff0000u) | bits;
-        }
+    for (int j = 0; j < kPer; ++j) {
+      const int i = first + j;
+      if (i < 0 || i >= in.vocab) continue;
+      if constexpr (sizeof(T) == 4) {
+        e[j] = reinterpret_cast<const uint32_t*>(x)[i];
+      } else {
+        const uint32_t bits = reinterpret_cast<const unsigned short*>(x)[i];
+        e[j / 2] = j & 1 ? (e[j / 2] & 0xffffu) | bits << 16 : (e[j / 2] & 0xffff0000u) | bits;
       }
     }
     return make_uint4(e[0], e[1], e[2], e[3]);
+  };
+  // the unit that starts `off` values into copy a (b: the next one)
+  auto joined = [&](const uint4& a, const uint4& b) -> uint4 {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    const int words = off * (int)sizeof(T) / 4;
+    uint32_t y[6], z[5];
+#pragma unroll
+    for (int j = 0; j < 6; ++j) y[j] = words & 2 ? w[j + 2] : w[j];
+#pragma unroll
+    for (int j = 0; j < 5; ++j) z[j] = words & 1 ? y[j + 1] : y[j];
+    if constexpr (sizeof(T) == 2) {
+      const int bits = off & 1 ? 16 : 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) z[j] = __funnelshift_r(z[j], z[j + 1], bits);
+    }
+    return make_uint4(z[0], z[1], z[2], z[3]);
   };
   auto at = [](const uint4& w, int e) {
     const int j = e / kHalves;
     return value_of<T>(j == 0 ? w.x : j == 1 ? w.y : j == 2 ? w.z : w.w, e % kHalves);
   };
+  auto slot = [&](int chunk, int v) { return ring + ((chunk % kStages * kVectors + v) * kWarps + warp) * kWarpUnits + lane; };
+  auto bring_one = [&](uint4* to, int u) {
+    if (u >= f0 && u < f1) ptx::cp_async_16(to, copy_at(u));
+    else *to = pieces(u * kPer - off);
+  };
+  const int chunks = u1 > u0 ? (u1 - u0 + kUnits - 1) / kUnits : 0;
   auto bring = [&](int chunk) {
-    const int u = f0 + chunk * kUnits + tid;
-    uint4* to = ring + (chunk % kStages) * kUnits + tid;
+    if (chunk < chunks) {
+      const int u = u0 + chunk * kUnits + tid;
 #pragma unroll
-    for (int v = 0; v < kVectors; ++v)
-      if (u + v * kThreads < f1) ptx::cp_async_16(to + v * kThreads, unit_at(u + v * kThreads));
+      for (int v = 0; v < kVectors; ++v) bring_one(slot(chunk, v), u + v * kThreads);
+      if (off > 0 && lane < kVectors)  // the copy behind the warp's, one a lane
+        bring_one(slot(chunk, lane) - lane + 32, u - lane + lane * kThreads + 32);
+    }
     ptx::cp_async_commit();
   };
-  const int chunks = f1 > f0 ? (f1 - f0 + kUnits - 1) / kUnits : 0;
   for (int c = 0; c < kStages - 1; ++c) bring(c);
   // a thread's chunks in up to kStretches stretches, whose maxima it writes down
   const int stretch = (chunks + kStretches - 1) / kStretches;
-  float m = kNone, here = kNone;  // this thread's maximum, that of the stretch,
-  Two sum{0.f, 0.f};              // and sum of exp(x - m)
-  auto take = [&](const uint4* w, auto count) {
-    constexpr int kCount = decltype(count)::value;
-    const float mine = largest<T, kCount>(w);
+  Reference ref{kNone, 0.f};  // of this thread's maximum,
+  float here = kNone;         // the maximum of the stretch,
+  Two sum{0.f, 0.f};          // and the sum
+  auto take = [&](const uint4* w) {
+    const float mine = largest<T, kVectors>(w);
     here = fmaxf(here, mine);
-    if (mine > m) {
-      const float f = exp_of(m - mine);  // m = -inf: 0
+    if (mine > ref.top) {
+      const Reference higher = reference_of(mine);
+      const float f = between(ref, higher);
       sum.h *= f;
       sum.l *= f;
-      m = mine;
+      ref = higher;
     }
-    const float ref = m == kNone ? 0.f : m;
-    const uint64_t minus = ptx::pack_f32x2(-ref, -ref), hi = ptx::pack_f32x2(kLog2eHi, kLog2eHi),
-                   lo = ptx::pack_f32x2(kLog2eLo, kLog2eLo);
+    const float from = is_far(ref.top) && ref.top != kNone ? -ref.top : 0.f;
+    const uint64_t minus = ptx::pack_f32x2(from, from), down = ptx::pack_f32x2(-ref.power, -ref.power),
+                   hi = ptx::pack_f32x2(kLog2eHi, kLog2eHi), lo = ptx::pack_f32x2(kLog2eLo, kLog2eLo);
     uint64_t s[2] = {0, 0};
 #pragma unroll
-    for (int v = 0; v < kCount; ++v)
+    for (int v = 0; v < kVectors; ++v)
 #pragma unroll
       for (int e = 0; e < kPer; e += 2) {
-        // exp_of, two at a time
         const uint64_t d = ptx::add_f32x2(ptx::pack_f32x2(at(w[v], e), at(w[v], e + 1)), minus);
         float a, b;
-        ptx::unpack_f32x2(ptx::fma_f32x2(d, hi, ptx::mul_f32x2(d, lo)), a, b);
+        ptx::unpack_f32x2(ptx::fma_f32x2(d, lo, ptx::fma_f32x2(d, hi, down)), a, b);
         s[(e >> 1) & 1] = ptx::add_f32x2(s[(e >> 1) & 1], ptx::pack_f32x2(ptx::ex2(a), ptx::ex2(b)));
       }
     float a, b;
@@ -323,30 +365,25 @@ beam_parts_kernel(Logits in, const float* __restrict__ scores, const unsigned ch
     sum = {t.h, t.l + sum.l};
   };
   for (int c = 0; c < chunks; ++c) {
+    if (off > 0) __syncwarp();  // (its neighbour has read what a lane brings the next chunk to)
     bring(c + kStages - 1);
     ptx::cp_async_wait<kStages - 1>();  // this thread's copies of chunk c are there
-    const uint4* from = ring + (c % kStages) * kUnits + tid;
     uint4 w[kVectors];
-    if (f0 + (c + 1) * kUnits <= f1) {
+    if (off > 0) {
+      __syncwarp();  // the warp's are
 #pragma unroll
-      for (int v = 0; v < kVectors; ++v) w[v] = from[v * kThreads];
+      for (int v = 0; v < kVectors; ++v) w[v] = joined(slot(c, v)[0], slot(c, v)[1]);
     } else {
-      const uint4 none = make_uint4(kNothing, kNothing, kNothing, kNothing);
 #pragma unroll
-      for (int v = 0; v < kVectors; ++v)
-        w[v] = f0 + c * kUnits + v * kThreads + tid < f1 ? from[v * kThreads] : none;
+      for (int v = 0; v < kVectors; ++v) w[v] = *slot(c, v);
     }
-    take(w, std::integral_constant<int, kVectors>());
+    take(w);
     if ((c + 1) % stretch == 0 || c + 1 == chunks) {
       stretch_max[c / stretch * kThreads + tid] = here;
       here = kNone;
     }
   }
-  uint4 border;
-  if (tid < 2) {
-    border = edge();
-    take(&border, std::integral_constant<int, 1>());
-  }
+  const float m = ref.top;
   // the maxima of four threads each
   {
     float g = fmaxf(m, __shfl_xor_sync(kAll, m, 1));
@@ -379,13 +416,13 @@ beam_parts_kernel(Logits in, const float* __restrict__ scores, const unsigned ch
     const uint32_t u = __reduce_max_sync(kAll, ordered(top));
     top = __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xffffffffu));
   }
-  // the threads' sums, relative to 2^power (far: to e^top)
-  const float power = is_far(top) ? 0.f : rintf(top * kLog2eHi);
+  // the threads' sums, relative to the part's maximum
+  const Reference all_of = reference_of(top);
   {
     // (no value: a sum of 0; a NaN, or an infinity's, stays one)
-    const float f = !is_far(top) ? power_of(log2_of(m), Two{power, 0.f}) : top > kNone ? exp_of(m - top) : 1.f;
+    const float f = between(ref, all_of);
     // whole multiples of 2^-32 add up without rounding, 22 bits at a time (a thread's sum is
-    // below 2^21: of 2^20 values at most, each below e^0.7)
+    // below 2^21: of 2^20 values at most, each below 2^0.6)
     const float h = sum.h * f, l = sum.l * f;
     const bool odd = !(h < 2097152.f);  // a NaN, then
     const long long q = odd ? 0 : __float2ll_rn(h * 4294967296.f) + __float2ll_rn(l * 4294967296.f);
@@ -414,7 +451,7 @@ beam_parts_kernel(Logits in, const float* __restrict__ scores, const unsigned ch
         const int p = atomicAdd(&n_cand, 1);
         if (p < kRoom) {
           cand_x[p] = y;
-          cand_i[p] = u * kPer + e - off;
+          cand_i[p] = u * kPer + e;
         }
       }
     }
@@ -427,18 +464,20 @@ beam_parts_kernel(Logits in, const float* __restrict__ scores, const unsigned ch
 #pragma unroll
     for (int j = 0; j < kAgain; ++j) {
       const int q = q0 + j * kThreads, h = q / each;
-      u[j] = f1;
+      u[j] = u1;
       if (q < again) {
         const int z = hot[h];
-        u[j] = f0 + (z / kThreads * each + q - h * each) * kThreads + z % kThreads;
+        u[j] = u0 + (z / kThreads * each + q - h * each) * kThreads + z % kThreads;
       }
       w[j] = make_uint4(kNothing, kNothing, kNothing, kNothing);
-      if (u[j] < f1) w[j] = *unit_at(u[j]);
+      if (u[j] < u1) {
+        if (u[j] < f0 || u[j] + f0 >= f1) w[j] = pieces(u[j] * kPer);
+        else w[j] = off > 0 ? joined(*copy_at(u[j]), *copy_at(u[j] + 1)) : *copy_at(u[j]);
+      }
     }
 #pragma unroll
     for (int j = 0; j < kAgain; ++j) offer(w[j], u[j]);
   }
-  if (tid < 2) offer(border, tid == 0 ? 0 : units - 1);
   __syncthreads();
   const size_t list = (size_t)row * out.parts + part;
   float* out_x = out.value + list * k;
@@ -460,7 +499,7 @@ beam_parts_kernel(Logits in, const float* __restrict__ scores, const unsigned ch
       out_i[r] = -1;
     }
   } else {
-    select_slowly(x, max(0, u0 * kPer - off), min(in.vocab, u1 * kPer - off), k, out_x, out_i, best_key);
+    select_slowly(x, u0 * kPer, min(in.vocab, u1 * kPer), k, out_x, out_i, best_key);
   }
   if (tid == 0) {
     unsigned long long s = 0;
@@ -473,7 +512,7 @@ beam_parts_kernel(Logits in, const float* __restrict__ scores, const unsigned ch
     const int shift = max(0, 40 - __clzll(s));
     const float h = (float)(s >> shift << shift) * 2.3283064365386963e-10f;
     const float l = (float)(s & ((1ull << shift) - 1)) * 2.3283064365386963e-10f;
-    out.part[list] = Part{top, (int)power, odd ? Two{NAN, 0.f} : settle(h, l)};
+    out.part[list] = Part{all_of, odd ? Two{NAN, 0.f} : settle(h, l)};
   }
 }
 
@@ -485,8 +524,8 @@ __global__ void __launch_bounds__(kThreads)
 beam_join_kernel(const float* scores, const unsigned char* __restrict__ finished, int beams, int k,
                  int vocab, int end_token, Parts in, float* scores_out, int* __restrict__ tokens_out,
                  int* __restrict__ parents_out) {
-  __shared__ Two row_less[kMaxK];                    // what a row's logits are diminished by: lse - score, without `top`
-  __shared__ float row_top[kMaxK], row_score[kMaxK];  // (beams are 64 at most, too); top: 0 but for far ones
+  __shared__ Two row_less[kMaxK];                    // what a row's logits are diminished by beside `top`: lse - top - score
+  __shared__ float row_top[kMaxK], row_score[kMaxK];  // (beams are 64 at most, too)
   __shared__ float row_least[kMaxK];
   __shared__ int row_lists[kMaxK];  // of a beam; 0: it offers nothing, -1: it has ended
   __shared__ unsigned long long key[kDepths][kMaxLists], cand_s[kRoom], best_s[kWarps], threshold;
@@ -512,28 +551,17 @@ beam_join_kernel(const float* scores, const unsigned char* __restrict__ finished
     const bool scored = fabsf(c) < INFINITY, done = w < beams && finished && finished[row];
     Two sum{0.f, 0.f};
     float top = kNone;
-    int power = -(1 << 24);
     const int parts = scored && !done ? in.parts : 0;
     const Part* of = in.part + (size_t)row * in.parts;
-    for (int p = part0; p < parts; p += kLanes) {
-      const Part q = of[p];
-      top = fmaxf(top, q.top);
-      if (!is_far(q.top)) power = max(power, q.power);
-    }
+    for (int p = part0; p < parts; p += kLanes) top = fmaxf(top, of[p].at.top);
 #pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) {
-      top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-      power = max(power, __shfl_xor_sync(kAll, power, o));
-    }
+    for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+    const Reference whole = reference_of(top);
     {
-      const bool far = is_far(top);
       for (int p = part0; p < parts; p += kLanes) {
         const Part q = of[p];
         // (a part without a value adds 0, or a NaN that it holds)
-        float f;
-        if (far && is_far(q.top)) f = q.top > kNone ? exp_of(q.top - top) : 1.f;
-        else if (far) f = power_of(Two{(float)q.power, 0.f}, log2_of(top));
-        else f = power_of(is_far(q.top) ? log2_of(q.top) : Two{(float)q.power, 0.f}, Two{(float)power, 0.f});
+        const float f = between(q.at, whole);
         sum = add(sum, Two{q.sum.h * f, q.sum.l * f});
       }
 #pragma unroll
@@ -546,13 +574,14 @@ beam_join_kernel(const float* scores, const unsigned char* __restrict__ finished
       // an infinity or a NaN among the logits, or nothing above -inf: no continuation
       const bool ok = scored && !done && fabsf(top) < INFINITY && sum.h > 0.f && sum.h < 1e35f;
       row_lists[w] = scored && done ? -1 : ok ? in.parts : 0;
-      row_top[w] = is_far(top) ? top : 0.f;
+      row_top[w] = top;
       row_score[w] = c;
       Two less{0.f, 0.f};
       if (ok) {
-        less = log_of(sum);
-        if (!is_far(top)) less = add(less, times_ln2((float)power));
-        less = add(less, -c);
+        // beside the largest term, as the sum took it
+        const float own = is_far(top) ? 1.f : ptx::ex2(fmaf(top, kLog2eLo, fmaf(top, kLog2eHi, -whole.power)));
+        const Two ln_own = log_of(Two{own, 0.f});
+        less = add(add(log_of(sum), Two{-ln_own.h, -ln_own.l}), -c);
       }
       row_less[w] = less;
     }
@@ -791,13 +820,12 @@ struct BeamPlan {
 // Even parts of each row: as many as make up to kBlocks blocks, which run all at once; and no more
 // lists a request than the join ranks.  (Shares of all rows' chunks that end inside a row kept every SM as
 // busy, but each end of a part costs 4 us: 64 x 4 beams over 131071 tokens took 30 us instead of
-// 24.)  `whole`: every row starts on a 16-byte boundary (else it may have a unit more).
-BeamPlan beam_plan(const mla_beam_params& p, bool whole) {
-  const int per = p.logits_dtype == MLA_LOGITS_FP32 ? 4 : 8, per_chunk = kThreads * kVectors * per;
+// 24.)
+BeamPlan beam_plan(const mla_beam_params& p) {
+  const int per_chunk = kThreads * kVectors * (p.logits_dtype == MLA_LOGITS_FP32 ? 4 : 8);
   const long long rows = (long long)p.batch * p.beams;
-  const long long values = p.vocab + (whole ? 0LL : per - 1LL);
   BeamPlan b;
-  const long long chunks = (values + per_chunk - 1) / per_chunk;
+  const long long chunks = ((long long)p.vocab + per_chunk - 1) / per_chunk;
   const long long want = std::min({chunks, std::max(1LL, kBlocks / std::max(rows, 1LL)), (long long)kMaxLists / p.beams});
   b.share = (int)((chunks + want - 1) / want);
   b.parts = (int)((chunks + b.share - 1) / b.share);
@@ -838,7 +866,7 @@ extern "C" {
 
 size_t mla_beam_workspace_size(const mla_beam_params* params) {
   if (mla::beam_check(params) != MLA_OK || params->batch == 0) return 0;
-  return std::max(mla::beam_plan(*params, true).bytes, mla::beam_plan(*params, false).bytes);
+  return mla::beam_plan(*params).bytes;
 }
 
 int mla_beam_select(const mla_beam_params* params, const void* logits, int64_t batch_stride, int64_t beam_stride,
@@ -857,9 +885,7 @@ int mla_beam_select(const mla_beam_params* params, const void* logits, int64_t b
       !aligned(parents_out, 4) || !aligned(workspace, 256))
     return MLA_ERR_ALIGNMENT;
   if (workspace_bytes < mla_beam_workspace_size(params)) return MLA_ERR_WORKSPACE_TOO_SMALL;
-  const bool whole = aligned(logits, 16) && (p.batch == 1 || batch_stride * size % 16 == 0) &&
-                     (p.beams == 1 || beam_stride * size % 16 == 0);
-  const BeamPlan plan = beam_plan(p, whole);
+  const BeamPlan plan = beam_plan(p);
   char* ws = static_cast<char*>(workspace);
   Parts parts{reinterpret_cast<Part*>(ws), reinterpret_cast<float*>(ws + plan.value),
               reinterpret_cast<int*>(ws + plan.token), plan.parts, plan.share};
