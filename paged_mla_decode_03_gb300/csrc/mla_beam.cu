@@ -246,7 +246,9 @@ __device__ __noinline__ void select_slowly(const T* x, int begin, int end, int k
   }
 }
 
-template <typename T>
+// kApart: rows that need not start on a 16-byte boundary (a kernel of its own: the others' calls are
+// shorter without).
+template <typename T, bool kApart>
 __global__ void __launch_bounds__(kThreads, 4)
 beam_parts_kernel(Logits in, const float* __restrict__ scores, const unsigned char* __restrict__ finished, int k,
                   Parts out) {
@@ -271,7 +273,7 @@ beam_parts_kernel(Logits in, const float* __restrict__ scores, const unsigned ch
   const T* x = static_cast<const T*>(in.base) + (row / in.beams) * in.batch_stride + (row % in.beams) * in.beam_stride;
   // Units of values [u kPer, (u + 1) kPer).  Copies are of 16 aligned bytes; where the row does not
   // start on one, `off` values before it do, and a unit is the end of one copy and the start of the next.
-  const int off = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
+  const int off = kApart ? (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T)) : 0;
   const int units = (in.vocab + kPer - 1) / kPer;
   const int u0 = part * out.share * kUnits, u1 = min(u0 + out.share * kUnits, units);
   const int f0 = off > 0 ? 1 : 0, f1 = (off + in.vocab) / kPer;  // copies [f0, f1) lie inside the row
@@ -294,10 +296,10 @@ beam_parts_kernel(Logits in, const float* __restrict__ scores, const unsigned ch
     }
     return make_uint4(e[0], e[1], e[2], e[3]);
   };
-  // the unit that starts `off` values into copy a (b: the next one)
-  auto joined = [&](const uint4& a, const uint4& b) -> uint4 {
+  // the unit that starts `off` values, `words` whole words, into copy a (b: the next one)
+  const int off_words = off * (int)sizeof(T) / 4;
+  auto joined = [&](const uint4& a, const uint4& b, int words) -> uint4 {
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    const int words = off * (int)sizeof(T) / 4;
     uint32_t y[6], z[5];
 #pragma unroll
     for (int j = 0; j < 6; ++j) y[j] = words & 2 ? w[j + 2] : w[j];
@@ -315,18 +317,28 @@ beam_parts_kernel(Logits in, const float* __restrict__ scores, const unsigned ch
     return value_of<T>(j == 0 ? w.x : j == 1 ? w.y : j == 2 ? w.z : w.w, e % kHalves);
   };
   auto slot = [&](int chunk, int v) { return ring + ((chunk % kStages * kVectors + v) * kWarps + warp) * kWarpUnits + lane; };
-  auto bring_one = [&](uint4* to, int u) {
-    if (u >= f0 && u < f1) ptx::cp_async_16(to, copy_at(u));
-    else *to = pieces(u * kPer - off);
-  };
   const int chunks = u1 > u0 ? (u1 - u0 + kUnits - 1) / kUnits : 0;
   auto bring = [&](int chunk) {
     if (chunk < chunks) {
-      const int u = u0 + chunk * kUnits + tid;
+      const int first = u0 + chunk * kUnits, u = first + tid;
+      // the copy behind each of the warp's, one a lane
+      const bool behind = kApart && lane < kVectors;
+      uint4* to = slot(chunk, lane & (kVectors - 1)) - lane + 32;
+      const int next = u - lane + (lane & (kVectors - 1)) * kThreads + 32;
+      if (first >= f0 && first + kUnits < f1) {
 #pragma unroll
-      for (int v = 0; v < kVectors; ++v) bring_one(slot(chunk, v), u + v * kThreads);
-      if (off > 0 && lane < kVectors)  // the copy behind the warp's, one a lane
-        bring_one(slot(chunk, lane) - lane + 32, u - lane + lane * kThreads + 32);
+        for (int v = 0; v < kVectors; ++v) ptx::cp_async_16(slot(chunk, v), copy_at(u + v * kThreads));
+        if (behind) ptx::cp_async_16(to, copy_at(next));
+      } else {
+#pragma unroll 1
+        for (int v = 0; v < kVectors + 1; ++v) {
+          uint4* here = v < kVectors ? slot(chunk, v) : to;
+          const int one = v < kVectors ? u + v * kThreads : next;
+          if (v == kVectors && !behind) break;
+          if (one >= f0 && one < f1) ptx::cp_async_16(here, copy_at(one));
+          else *here = pieces(one * kPer - off);
+        }
+      }
     }
     ptx::cp_async_commit();
   };
@@ -364,25 +376,27 @@ beam_parts_kernel(Logits in, const float* __restrict__ scores, const unsigned ch
     const Two t = exact_sum(sum.h, a + b);
     sum = {t.h, t.l + sum.l};
   };
-  for (int c = 0; c < chunks; ++c) {
-    if (off > 0) __syncwarp();  // (its neighbour has read what a lane brings the next chunk to)
-    bring(c + kStages - 1);
-    ptx::cp_async_wait<kStages - 1>();  // this thread's copies of chunk c are there
-    uint4 w[kVectors];
-    if (off > 0) {
-      __syncwarp();  // the warp's are
+  auto stream = [&](auto shift) {  // (whole words that the row starts past a boundary)
+    for (int c = 0; c < chunks; ++c) {
+      if (kApart) __syncwarp();  // (its neighbour has read what a lane brings the next chunk to)
+      bring(c + kStages - 1);
+      ptx::cp_async_wait<kStages - 1>();  // this thread's copies of chunk c are there
+      if (kApart) __syncwarp();           // the warp's are
+      uint4 w[kVectors];
 #pragma unroll
-      for (int v = 0; v < kVectors; ++v) w[v] = joined(slot(c, v)[0], slot(c, v)[1]);
-    } else {
-#pragma unroll
-      for (int v = 0; v < kVectors; ++v) w[v] = *slot(c, v);
+      for (int v = 0; v < kVectors; ++v)
+        w[v] = kApart ? joined(slot(c, v)[0], slot(c, v)[1], decltype(shift)::value) : *slot(c, v);
+      take(w);
+      if ((c + 1) % stretch == 0 || c + 1 == chunks) {
+        stretch_max[c / stretch * kThreads + tid] = here;
+        here = kNone;
+      }
     }
-    take(w);
-    if ((c + 1) % stretch == 0 || c + 1 == chunks) {
-      stretch_max[c / stretch * kThreads + tid] = here;
-      here = kNone;
-    }
-  }
+  };
+  if (!kApart || off_words == 0) stream(std::integral_constant<int, 0>());
+  else if (off_words == 1) stream(std::integral_constant<int, 1>());
+  else if (off_words == 2) stream(std::integral_constant<int, 2>());
+  else stream(std::integral_constant<int, 3>());
   const float m = ref.top;
   // the maxima of four threads each
   {
@@ -472,7 +486,7 @@ beam_parts_kernel(Logits in, const float* __restrict__ scores, const unsigned ch
       w[j] = make_uint4(kNothing, kNothing, kNothing, kNothing);
       if (u[j] < u1) {
         if (u[j] < f0 || u[j] + f0 >= f1) w[j] = pieces(u[j] * kPer);
-        else w[j] = off > 0 ? joined(*copy_at(u[j]), *copy_at(u[j] + 1)) : *copy_at(u[j]);
+        else w[j] = off > 0 ? joined(*copy_at(u[j]), *copy_at(u[j] + 1), off_words) : *copy_at(u[j]);
       }
     }
 #pragma unroll
@@ -892,9 +906,12 @@ int mla_beam_select(const mla_beam_params* params, const void* logits, int64_t b
   const Logits in{logits, batch_stride, beam_stride, p.beams, p.vocab};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const dim3 grid((unsigned)plan.blocks);
-  auto kernel = p.logits_dtype == MLA_LOGITS_FP32   ? beam_parts_kernel<float>
-                : p.logits_dtype == MLA_LOGITS_BF16 ? beam_parts_kernel<__nv_bfloat16>
-                                                    : beam_parts_kernel<__half>;
+  const bool whole = aligned(logits, 16) && (p.batch == 1 || batch_stride * size % 16 == 0) &&
+                     (p.beams == 1 || beam_stride * size % 16 == 0);
+  auto kernel = p.logits_dtype == MLA_LOGITS_FP32 ? (whole ? beam_parts_kernel<float, false> : beam_parts_kernel<float, true>)
+                : p.logits_dtype == MLA_LOGITS_BF16
+                    ? (whole ? beam_parts_kernel<__nv_bfloat16, false> : beam_parts_kernel<__nv_bfloat16, true>)
+                    : (whole ? beam_parts_kernel<__half, false> : beam_parts_kernel<__half, true>);
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess)
     return MLA_ERR_CUDA;
   kernel<<<grid, kThreads, kSmem, s>>>(in, scores, finished, p.k, parts);
