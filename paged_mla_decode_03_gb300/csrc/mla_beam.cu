@@ -58,6 +58,8 @@ __device__ __forceinline__ uint32_t ordered(float x) {
   const uint32_t u = __float_as_uint(x + 0.f);
   return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
+// The largest float below x, and -inf of it.
+__device__ __forceinline__ float below(float x) { return x == kNone ? x : -nextafterf(-x, INFINITY); }
 __device__ __forceinline__ bool before(float xa, int ia, float xb, int ib) { return xa > xb || (xa == xb && ia < ib); }
 
 struct Logits {
@@ -209,8 +211,8 @@ struct Parts {
 
 }  // namespace
 
-// The k largest of values [begin, end) of a row, one after another: for parts with more ties
-// than there is room for.  (Apart, as it is hardly ever called.)
+// The k largest of values [begin, end) of a row, one after another: for parts whose threshold more values
+// pass than there is room for.  (Apart, as it is hardly ever called.)
 template <typename T>
 __device__ __noinline__ void select_slowly(const T* x, int begin, int end, int k, float* out_x, int* out_i,
                                            unsigned long long* best_key) {
@@ -258,6 +260,7 @@ beam_parts_kernel(Logits in, const float* __restrict__ scores, const unsigned ch
   __shared__ float group_max[kGroups], threshold;
   __shared__ int n_cand, n_hot;
   __shared__ unsigned long long best_key[kWarps];
+  __shared__ int equal_sum[kWarps];
   // once the row has gone through it, the ring holds the candidates and the places to look again
   float* cand_x = reinterpret_cast<float*>(ring);
   int* cand_i = reinterpret_cast<int*>(cand_x + kRoom);
@@ -451,51 +454,106 @@ beam_parts_kernel(Logits in, const float* __restrict__ scores, const unsigned ch
   // the stretches that have a value at or above the threshold
   const float least = threshold;
   const int stretches = chunks > 0 ? (chunks + stretch - 1) / stretch : 0;
-  if (m >= least && m > kNone)
-    for (int z = 0; z < stretches; ++z) {
-      const float y = stretch_max[z * kThreads + tid];
-      if (y >= least && y > kNone) hot[atomicAdd(&n_hot, 1)] = (unsigned short)(tid + kThreads * z);
-    }
+  if (m >= least && m > kNone) {
+    int mine = 0;
+    for (int z = 0; z < stretches; ++z) mine += stretch_max[z * kThreads + tid] >= least;
+    int p = atomicAdd(&n_hot, mine);
+    for (int z = 0; z < stretches; ++z)
+      if (stretch_max[z * kThreads + tid] >= least) hot[p++] = (unsigned short)(tid + kThreads * z);
+  }
   __syncthreads();
-  auto offer = [&](const uint4& w, int u) {
+  auto unit_again = [&](int u) -> uint4 {
+    if (u >= u1) return make_uint4(kNothing, kNothing, kNothing, kNothing);
+    if (u < f0 || u + f0 >= f1) return pieces(u * kPer);
+    return off > 0 ? joined(*copy_at(u), *copy_at(u + 1), off_words) : *copy_at(u);
+  };
+  // values that are kNone, or `low` and less, are no candidates
+  auto offer = [&](const uint4& w, int u, float low) {
+    int mine = 0;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) mine += at(w, e) > low;
+    if (mine == 0) return;
+    int p = atomicAdd(&n_cand, mine);
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
       const float y = at(w, e);
-      if (y >= least && y > kNone) {
-        const int p = atomicAdd(&n_cand, 1);
+      if (y > low) {
         if (p < kRoom) {
           cand_x[p] = y;
           cand_i[p] = u * kPer + e;
         }
+        ++p;
       }
     }
   };
   const int each = stretch * kVectors, again = n_hot * each;  // units of a stretch
-  constexpr int kAgain = 4;
-  for (int q0 = tid; q0 < again; q0 += kAgain * kThreads) {
-    uint4 w[kAgain];
-    int u[kAgain];
+  // (once there are too many, how many there are does not matter)
+  auto collect = [&](float low) {
+    constexpr int kAgain = 4;
+    for (int q0 = tid; q0 < again && *(volatile int*)&n_cand <= kRoom; q0 += kAgain * kThreads) {
+      uint4 w[kAgain];
+      int u[kAgain];
 #pragma unroll
-    for (int j = 0; j < kAgain; ++j) {
-      const int q = q0 + j * kThreads, h = q / each;
-      u[j] = u1;
-      if (q < again) {
-        const int z = hot[h];
-        u[j] = u0 + (z / kThreads * each + q - h * each) * kThreads + z % kThreads;
+      for (int j = 0; j < kAgain; ++j) {
+        const int q = q0 + j * kThreads, h = q / each;
+        u[j] = u1;
+        if (q < again) {
+          const int z = hot[h];
+          u[j] = u0 + (z / kThreads * each + q - h * each) * kThreads + z % kThreads;
+        }
+        w[j] = unit_again(u[j]);
       }
-      w[j] = make_uint4(kNothing, kNothing, kNothing, kNothing);
-      if (u[j] < u1) {
-        if (u[j] < f0 || u[j] + f0 >= f1) w[j] = pieces(u[j] * kPer);
-        else w[j] = off > 0 ? joined(*copy_at(u[j]), *copy_at(u[j] + 1), off_words) : *copy_at(u[j]);
-      }
+#pragma unroll
+      for (int j = 0; j < kAgain; ++j) offer(w[j], u[j], low);
     }
-#pragma unroll
-    for (int j = 0; j < kAgain; ++j) offer(w[j], u[j]);
-  }
-  __syncthreads();
+    __syncthreads();
+  };
+  collect(below(least));
   const size_t list = (size_t)row * out.parts + part;
   float* out_x = out.value + list * k;
   int* out_i = out.token + list * k;
+  // Where too many pass, many equal the threshold (tokens masked by a finite value): the ones above
+  // it then, and of its equals the first in the order of their index.  (64 x 4 beams over 131071 tokens
+  // of which five are not masked: 51 us, and 495 with all k places found one after another.)
+  const bool equals = n_cand > kRoom;
+  int first_equal = k;  // places from here on are theirs
+  if (equals) {
+    __syncthreads();
+    if (tid == 0) n_cand = 0;
+    __syncthreads();
+    collect(least);
+    first_equal = min(n_cand, k);
+    if (n_cand <= kRoom)
+      for (int from = u0, place = first_equal; from < u1 && place < k; from += kThreads) {
+        const uint4 w = unit_again(from + tid);
+        int mine = 0;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) mine += at(w, e) == least;
+        int up = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(kAll, up, o);
+          if (lane >= o) up += y;
+        }
+        __syncthreads();
+        if (lane == 31) equal_sum[warp] = up;
+        __syncthreads();
+        int p = place + up - mine;
+        for (int o = 0; o < kWarps; ++o) {
+          if (o < warp) p += equal_sum[o];
+          place += equal_sum[o];
+        }
+#pragma unroll
+        for (int e = 0; e < kPer; ++e)
+          if (at(w, e) == least) {
+            if (p < k) {
+              out_x[p] = least;
+              out_i[p] = (from + tid) * kPer + e;
+            }
+            ++p;
+          }
+      }
+  }
   const int n = n_cand;
   if (n <= kRoom) {
     for (int j = tid; j < n; j += kThreads) {
@@ -508,7 +566,7 @@ beam_parts_kernel(Logits in, const float* __restrict__ scores, const unsigned ch
         out_i[rank] = i;
       }
     }
-    for (int r = n + tid; r < k; r += kThreads) {
+    for (int r = n + tid; r < first_equal; r += kThreads) {
       out_x[r] = kNone;
       out_i[r] = -1;
     }
