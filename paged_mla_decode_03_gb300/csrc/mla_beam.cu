@@ -593,8 +593,7 @@ beam_parts_kernel(Logits in, const float* __restrict__ scores, const unsigned ch
 constexpr int kDepths = 4, kStaged = 2048;
 
 __global__ void __launch_bounds__(kThreads)
-beam_join_kernel(const float* scores, const unsigned char* __restrict__ finished, int beams, int k,
-                 int vocab, int end_token, Parts in, float* scores_out, int* __restrict__ tokens_out,
+beam_join_kernel(const float* scores, const unsigned char* __restrict__ finished, int beams, int k, int end_token, Parts in, float* scores_out, int* __restrict__ tokens_out,
                  int* __restrict__ parents_out) {
   __shared__ Two row_less[kMaxK];                    // what a row's logits are diminished by beside `top`: lse - top - score
   __shared__ float row_top[kMaxK], row_score[kMaxK];  // (beams are 64 at most, too)
@@ -602,6 +601,7 @@ beam_join_kernel(const float* scores, const unsigned char* __restrict__ finished
   __shared__ int row_lists[kMaxK];  // of a beam; 0: it offers nothing, -1: it has ended
   __shared__ unsigned long long key[kDepths][kMaxLists], cand_s[kRoom], best_s[kWarps], threshold;
   __shared__ long long cand_i[kRoom], best_i[kWarps];
+  __shared__ float cand_x[kRoom], best_x[kWarps];
   __shared__ float staged[kStaged];
   __shared__ int staged_token[kStaged];
   __shared__ int n_cand;
@@ -676,8 +676,9 @@ beam_join_kernel(const float* scores, const unsigned char* __restrict__ finished
   };
   auto place_of = [&](int l, int j) -> long long {
     const int w = l / in.parts;
-    return (long long)w * vocab + (row_lists[w] < 0 ? end_token : near ? staged_token[l * k + j] : in.token[(list0 + l) * k + j]);
+    return (long long)w << 32 | (row_lists[w] < 0 ? end_token : near ? staged_token[l * k + j] : in.token[(list0 + l) * k + j]);
   };
+  auto value_at = [&](int l, int j) { return row_lists[l / in.parts] < 0 ? 0.f : logit(l, j); };
   // A threshold that at least k candidates are at or above: for some depths d, the
   // ceil(k / d)-th largest of the lists' d-th candidates, and of these the largest.  (With d
   // = 1, 4, 16, 64 fewer than 4 k candidates for each d pass it, ties apart, however the
@@ -714,22 +715,31 @@ beam_join_kernel(const float* scores, const unsigned char* __restrict__ finished
     if (p < kRoom) {
       cand_s[p] = s;
       cand_i[p] = place_of(l, j);
+      cand_x[p] = value_at(l, j);
     }
   }
   __syncthreads();
   const int n = n_cand;
-  auto ahead = [](unsigned long long sa, long long ia, unsigned long long sb, long long ib) {
-    return sa > sb || (sa == sb && ia < ib);
+  // By score, beam, logit and token: logits of one beam may be nearer than 48 bits of their scores
+  // tell (a beam whose score is -1e9).
+  auto ahead = [](unsigned long long sa, long long ia, float xa, unsigned long long sb, long long ib, float xb) {
+    if (sa != sb) return sa > sb;
+    return ia >> 32 == ib >> 32 && xa != xb ? xa > xb : ia < ib;
   };
   auto write = [&](int rank, unsigned long long s, long long i) {
     scores_out[(size_t)b * k + rank] = s == 0 ? kNone : score_of_key(s);
-    tokens_out[(size_t)b * k + rank] = i < 0 ? -1 : (int)(i % vocab);
-    parents_out[(size_t)b * k + rank] = i < 0 ? -1 : (int)(i / vocab);
+    tokens_out[(size_t)b * k + rank] = i < 0 ? -1 : (int)i;
+    parents_out[(size_t)b * k + rank] = i < 0 ? -1 : (int)(i >> 32);
   };
   if (n <= kRoom) {
     for (int j = tid; j < n; j += kThreads) {
+      const unsigned long long mine = cand_s[j];
       int rank = 0;
-      for (int o = 0; o < n; ++o) rank += ahead(cand_s[o], cand_i[o], cand_s[j], cand_i[j]) ? 1 : 0;
+      for (int o = 0; o < n; ++o) {
+        const unsigned long long other = cand_s[o];
+        rank += other > mine ? 1 : 0;
+        if (other == mine && o != j) rank += ahead(other, cand_i[o], cand_x[o], mine, cand_i[j], cand_x[j]) ? 1 : 0;
+      }
       if (rank < k) write(rank, cand_s[j], cand_i[j]);
     }
     for (int r = n + tid; r < k; r += kThreads) write(r, 0, -1);
@@ -738,30 +748,35 @@ beam_join_kernel(const float* scores, const unsigned char* __restrict__ finished
   // more ties than there is room for: one after another
   unsigned long long last_s = ~0ull;
   long long last_i = -1;
+  float last_x = 0.f;
   for (int r = 0; r < k; ++r) {
     unsigned long long s = 0;
     long long at = -1;
+    float x = 0.f;
     for (int e = tid; e < lists * k; e += kThreads) {
       const unsigned long long q = key_of(e / k, e % k);
       if (q == 0 || q < s || q > last_s) continue;
       const long long i = place_of(e / k, e % k);
-      if (ahead(last_s, last_i, q, i) && (at < 0 || ahead(q, i, s, at))) s = q, at = i;
+      const float y = value_at(e / k, e % k);
+      if (ahead(last_s, last_i, last_x, q, i, y) && (at < 0 || ahead(q, i, y, s, at, x))) s = q, at = i, x = y;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       const unsigned long long q = __shfl_xor_sync(kAll, s, o);
       const long long i = __shfl_xor_sync(kAll, at, o);
-      if (i >= 0 && (at < 0 || ahead(q, i, s, at))) s = q, at = i;
+      const float y = __shfl_xor_sync(kAll, x, o);
+      if (i >= 0 && (at < 0 || ahead(q, i, y, s, at, x))) s = q, at = i, x = y;
     }
     if (lane == 0) {
       best_s[warp] = s;
       best_i[warp] = at;
+      best_x[warp] = x;
     }
     __syncthreads();
     s = 0;
     at = -1;
     for (int w = 0; w < kWarps; ++w)
-      if (best_i[w] >= 0 && (at < 0 || ahead(best_s[w], best_i[w], s, at))) s = best_s[w], at = best_i[w];
+      if (best_i[w] >= 0 && (at < 0 || ahead(best_s[w], best_i[w], best_x[w], s, at, x))) s = best_s[w], at = best_i[w], x = best_x[w];
     __syncthreads();
     if (tid == 0) write(r, s, at);
     if (at < 0) {
@@ -770,6 +785,7 @@ beam_join_kernel(const float* scores, const unsigned char* __restrict__ finished
     }
     last_s = s;
     last_i = at;
+    last_x = x;
   }
 }
 
@@ -974,8 +990,8 @@ int mla_beam_select(const mla_beam_params* params, const void* logits, int64_t b
     return MLA_ERR_CUDA;
   kernel<<<grid, kThreads, kSmem, s>>>(in, scores, finished, p.k, parts);
   if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
-  int beams = p.beams, k = p.k, vocab = p.vocab, end = p.end_token;
-  void* args[] = {&scores, &finished, &beams, &k, &vocab, &end, &parts, &scores_out, &tokens_out, &parents_out};
+  int beams = p.beams, k = p.k, end = p.end_token;
+  void* args[] = {&scores, &finished, &beams, &k, &end, &parts, &scores_out, &tokens_out, &parents_out};
   return launch_dependent(reinterpret_cast<const void*>(beam_join_kernel), dim3((unsigned)p.batch), s, args) == cudaSuccess
              ? MLA_OK
              : MLA_ERR_CUDA;

@@ -3,9 +3,9 @@
 A row's normaliser is its largest logit plus the logarithm of the sum of its terms over the largest
 one's own.  Terms of e^-60 and less vanish beside it, so the sum of a row with one logit far above the
 others is that logit's term and the quotient 1: such rows' scores are their beams' to the bit.  In
-any row a term is off by an exponential's 2^-22, its own argument's rounding (2^-23 of an argument
-of at most some 16 where it counts) and the largest term's 2^-22, and chains of ten sums by 2^-24
-each: 2^-19 bounds them together."""
+any row a term is off by an exponential's 2^-22, its own argument's rounding (ln 2 times 2^-23 of an
+argument of at most some 16 where it counts) and the largest term's 2^-22, and chains of ten sums
+by 2^-24 each: 2^-18 bounds them together, were all roundings one way; half of it is asked."""
 import math
 
 import numpy as np
@@ -130,3 +130,59 @@ def test_results_hang_on_no_alignment():
             torch.cuda.synchronize()
             first = first or got
             assert all(torch.equal(a, b) for a, b in zip(first, got)), (kind, off)
+
+
+def near_logits(kind, step, k, W, n):
+    """Rows with n tokens of logits base + step * (0 .. 199), the others far below."""
+    g = torch.Generator().manual_seed(k)
+    V = 20011
+    x = torch.randn(1, W, V, generator=g) * 0.1 - 3
+    base = 0 if step < 2.0 ** -20 else 1
+    for w in range(W):
+        x[0, w, torch.randperm(V, generator=g)[:n]] = base + step * torch.arange(n).remainder(200)
+    return x.to(TYPES[kind])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind,step,k", [("fp32", 2.0 ** -20, 1), ("fp32", 2.0 ** -20, 7), ("fp32", 2.0 ** -20, 64), ("bf16", 2.0 ** -8, 1),
+                                         ("bf16", 2.0 ** -8, 7), ("fp16", 2.0 ** -11, 1), ("fp16", 2.0 ** -11, 7)])
+def test_beams_of_one_large_score_come_by_what_they_add(kind, step, k):
+    """40 beams of -1e30: 64 bits do not tell their continuations apart, pairs of floats do."""
+    W = 40
+    x = near_logits(kind, step, k, W, 900)
+    got = mla.beam_select(x.cuda(), torch.full((1, W), -1e30, device="cuda"), k=k)
+    d = x[0].double()
+    d = (d - torch.logsumexp(d, -1, keepdim=True)).numpy()
+    rows = [(-d[w, v], w, int(v)) for w in range(W) for v in np.lexsort((np.arange(d.shape[1]), -d[w]))[:k + 1]]
+    rows.sort()
+    assert all(a[1] == b[1] or b[0] - a[0] > 2.0 ** -19 for a, b in zip(rows[:k], rows[1:k + 1])), "an open order"
+    s, t, p = (y[0].cpu() for y in got)
+    assert [(int(w), int(v)) for w, v in zip(p, t)] == [(w, v) for _, w, v in rows[:k]]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind,step", [("fp32", 2.0 ** -30), ("bf16", 2.0 ** -30), ("fp16", 2.0 ** -24)])
+@pytest.mark.parametrize("k", [1, 7, 64])
+@pytest.mark.parametrize("many", [False, True])
+def test_tokens_of_a_beam_come_by_logit_whatever_its_score(kind, step, k, many):
+    """Beside a score of -1e9, logits that differ little make scores that are the same in 48 bits.
+    (many: 40 beams that are the same, whose candidates are more than the join has room for.)"""
+    W = 40 if many else 3
+    x = near_logits(kind, step, k, W, 900 if many else 100)
+    c = -1e9 * torch.arange(1, W + 1).float()[None]
+    if many:
+        x, c = x[:, :1].expand(-1, W, -1).contiguous(), torch.full((1, W), -1e9)
+    by_logit = [np.lexsort((np.arange(x.shape[2]), -x[0, w].double().numpy())) for w in range(W)]
+
+    def each_in_order():
+        s, t, p = (y[0].cpu() for y in mla.beam_select(x.cuda(), c.cuda(), k=k))
+        for w in set(p.tolist()):
+            mine = t[p == w].tolist()
+            assert mine == [int(v) for v in by_logit[w][:len(mine)]]
+        return set(p.tolist())
+
+    # (of beams that are the same, logits whose scores 48 bits tell apart come by turns: 200 steps of
+    # 2^-24 are some 25 of a score's)
+    assert each_in_order() == {0} or many
+    c[0, 1] = c[0, 0]  # two beams of one score
+    assert each_in_order() <= {0, 1} or many
