@@ -396,9 +396,9 @@ int mla_decode_run_sparse(const mla_plan_t *plan, const void *query, const void 
  * bmm1_dev, bmm2_dev  both NULL, or both one fp32 in device memory that
  *                stands in for bmm1_scale and bmm2_scale (mla_decode_run_device_scales).
  *
- * Query rows of several requests of a group are multiplied together: a NaN or an infinity in
- * any row that one request of a shared group sees, its own rows too, may reach the query rows
- * of the group's other requests.  Rows past a request's length reach nothing.  A
+ * Query rows of several requests of a group are multiplied together, but a NaN or an infinity in a
+ * row that one request alone sees reaches that request alone; in a shared row it reaches all that
+ * share it.  Rows past a request's length reach nothing.  A
  * request of length 0 in a shared group, which breaks the contract (status bit 1), may have its
  * output rows written.  plan: made with params.prefix_groups > 0.  All other arguments, errors and
  * capture rules as mla_decode_run; the other run entry points refuse such a

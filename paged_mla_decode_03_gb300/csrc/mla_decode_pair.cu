@@ -134,8 +134,9 @@ template <int kCache> struct Cfg {
   static constexpr uint32_t OFF_QSCALE = OFF_XSUM + 6 * 128 * 4;    // float [4][64]: 2^-k by item
   static constexpr uint32_t OFF_TMEM = OFF_QSCALE + 4 * kCtaRows * 4;
   static constexpr uint32_t OFF_ABORT = OFF_TMEM + 8;
-  static constexpr uint32_t OFF_MASK = OFF_ABORT + 8;  // uint32 [2][2]: rows in use, by stage and half
-  static constexpr uint32_t kSmemBytes = OFF_MASK + 16;
+  // uint32 [2][2]: rows in use, by stage and half; [2]: tiles that only some of the query rows see
+  static constexpr uint32_t OFF_MASK = OFF_ABORT + 8;
+  static constexpr uint32_t kSmemBytes = OFF_MASK + 24;
   static_assert(kSmemBytes <= 232448, "shared memory budget");
   static_assert((kTma ? OFF_K2 % 1024 == 0 : OFF_STG % 16 == 0) && kStage % 16 == 0 && STG_OTHER % 16 == 0 && STG_SCALES % 16 == 0 &&
                     OFF_BARS % 8 == 0,
@@ -336,6 +337,43 @@ struct Query {
   }
 };
 
+// Tiles that only some of an item's requests see (kShared): a NaN or an infinity in V would reach the
+// others' O, as 0 times it is a NaN.  Who sees a NaN has one among its scores, and so in its
+// sum, whatever V holds; so V may hold something finite there.  f16: the lowest value for a NaN
+// (4 bits and e4m3 have no infinity), at their conversion; bf16, which TMA brings, only where a score
+// that is not finite shows it.  (In a graph 96 x 16 heads behind 6000 rows of bf16 take 62.1 us with it
+// and 60.0 without, 16 x 8 x 32 heads over e4m3 86.1 and 83.6.  Looking at all of V before it is
+// passed on, by four warps, took 64.4.)
+__device__ __forceinline__ bool any_nan(uint32_t codes) {  // of four e4m3
+  return (((codes & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+}
+__device__ __forceinline__ void keep_finite(uint4& x) {
+  uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t low = 0xFBFFFBFFu;
+    const __half2 h = __hmax2(*reinterpret_cast<const __half2*>(&w[e]), *reinterpret_cast<const __half2*>(&low));
+    w[e] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  x = make_uint4(w[0], w[1], w[2], w[3]);
+}
+// bf16, in place and by one warp: 32 rows of a chunk of 64 dims after another; 0 for a NaN or an
+// infinity.  (Where a row with an infinity scores -infinity its weight is 0, and what it adds
+// is then 0, too.)
+__device__ __noinline__ void keep_finite_rows(uint32_t rows, uint32_t chunk_step) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i) {
+    const uint32_t at = rows + (i >> 3) * chunk_step + (i & 7) * 512 + lane * 16;
+    const uint4 x = ld_shared_v4(at);
+    uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)  // (an exponent of all ones, and one more, is the sign's place)
+      w[e] &= ~(((((w[e] & 0x7F807F80u) + 0x00800080u) >> 15) & 0x00010001u) * 0xFFFFu);
+    st_shared_v4(at, make_uint4(w[0], w[1], w[2], w[3]));
+  }
+}
+
 // The block's first query, from rows staged in shared memory (see below).  A
 // function of its own leaves the conversion loops their registers: inlined, those
 // spilled and a long call took 6% more.
@@ -490,6 +528,12 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
       PrefixSegment seg = {};
       if constexpr (kShared)
         if (lane < it.seq_len) seg = segments[(size_t)it.comb * kPrefixSegments + lane];
+      int mixed = INT_MAX;  // the first tile that some of the query rows do not see at all
+      if constexpr (kShared && !C::kTma) {
+        const bool some = lane < it.seq_len && (seg.q_lo > 0 || seg.q_hi < min(kRows, it.q_len * H - it.g * kRows));
+        const uint32_t which = __ballot_sync(0xffffffffu, some);
+        if (which != 0) mixed = __shfl_sync(0xffffffffu, seg.tile0, __ffs(which) - 1);
+      }
       auto page_at = [&](int i, int& left) -> int {
         if constexpr (kShared) {
           const int tile = it.kv_begin / kTile + (npg == 2 ? i >> 1 : i);
@@ -595,6 +639,7 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
             const bool own = rank == 0 ? on0 : on1;
             row_mask[2 * s] = mask0;
             row_mask[2 * s + 1] = mask1;
+            if (kShared) row_mask[4 + s] = it.kv_begin / kTile + t >= mixed;
             mbar_arrive_expect_tx(full, (on0 ? kScales : 0) + (on1 ? kScales : 0) + (own ? kCodes : 0));
             if (own) bulk_load(stg + C::STG_OWN, rank == 0 ? pg0 : pg1 + row1 * C::kCodeBytes, kCodes, full);
             if constexpr (kCache == kE4m3) {
@@ -844,6 +889,25 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
         if constexpr (kShared) {
           if (!clean) {
             const int at = r0 + 32 * hh;
+            if constexpr (kCache == kBf16) {
+              // a row in use with a NaN or an infinity shows in every query row's score
+              const int used = __shfl_sync(0xffffffffu, z_end, sg_now) - at;
+              if (used < 32) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (j >= used) v[j] = 0;
+              }
+              uint64_t none[2] = {0, 0};
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                none[j & 1] = fma_f32x2(pack_f32x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), 0, none[j & 1]);
+              float a, b;
+              unpack_f32x2(add_f32x2(none[0], none[1]), a, b);
+              if (__any_sync(0xffffffffu, !(a + b == 0.f))) {
+                if (!wait_bar(c, STG_EMPTY0 + grp, (g >> 1) & 1)) goto fail_soft;  // V is there
+                keep_finite_rows(smem_u32(sm) + OFF_V + grp * kVStage + hh * (kVStage / 2), C::kVChunkStep);
+              }
+            }
             hidden = ~first_bits(sg_mine - at);
 #pragma unroll
             for (int j = 0; j < 32; ++j)
@@ -1115,6 +1179,7 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
       // whether this lane's rows are in use (the others are zeros)
       const uint32_t m1 = row_mask[2 * s + rank], m2 = in_half ? m1 : row_mask[2 * s + (rank ^ 1)];
       const bool on1 = (m1 >> lane) & 1u, on2 = (m2 >> lane) & 1u;
+      bool some = kShared && row_mask[4 + s];
       uint4 x[8];
       uint32_t s2 = 0;  // 4 bits: the second part's scales
       if constexpr (kCache == kFp4) {
@@ -1131,6 +1196,7 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
                      : *reinterpret_cast<const uint32_t*>(sc_oth + 16 * rank + 4 * vc);
         if (!on1) sc = 0u;
         if (!on2) s2 = 0u;
+        if (some) some = any_nan(sc) || any_nan(s2);
         convert64(swap ? b : a, swap ? a : b, sc, x);
       } else {
         // (rows are 36 units apart: pairs of rows start at four places of the order,
@@ -1184,6 +1250,10 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
         __syncwarp();
       }
       if (lane == 0) mbar_arrive(&c.bars[STG_EMPTY0 + s]);  // every code is in registers
+      if (some) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) keep_finite(x[e]);
+      }
       if (!wait_bar(c, PV_DONE0 + grp, ((g >> 1) & 1) ^ 1)) return false;
 #pragma unroll
       for (int e = 0; e < 8; ++e) put(v_row, e, x[e]);
