@@ -437,7 +437,7 @@ template <int kCache, bool kShared>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
                    const __grid_constant__ CUtensorMap tm_k,   // (bf16 cache only)
-                   const __grid_constant__ CUtensorMap tm_v, const PrefixSegment* __restrict__ segments, const int late) {
+                   const __grid_constant__ CUtensorMap tm_v, const PrefixSegment* __restrict__ segments) {
   using C = Cfg<kCache>;
   // The swizzled tiles need 1024-byte alignment, and there is no room to round
   // up: the block has no other shared memory, so its dynamic part starts at
@@ -494,9 +494,7 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
   cluster_sync();  // the other CTA's barriers exist before any remote arrival
   // the work list comes from the partitioner; the combine kernel may be
   // scheduled from here on (it waits on counters that the epilogues bump)
-  // (late: the second decode of a run, whose list was there before the first one let it start)
-  constexpr bool kLate = kShared && !C::kTma;  // (a plan that widens walks 4 bits or e4m3 second)
-  if (!kLate || !late) pdl_wait();
+  pdl_wait();
   pdl_launch_dependents();
   const uint32_t tmem = *tmem_slot;
   const int item_begin = worker_begin[worker], item_end = worker_begin[worker + 1];
@@ -1390,7 +1388,6 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
   tc_fence_before();
   __syncthreads();
   if (tid == 0 && *c.abort) atomicOr(c.status, kStatusTimeout);
-  if (kLate && late) pdl_wait();  // so that the join, which waits for this kernel, follows both
   cluster_sync();  // neither CTA touches the other's memory or TMEM any more
   if (warp == 1) {
     tc_fence_after();
@@ -1453,16 +1450,14 @@ bool encode_rows(CUtensorMap* map, const Problem& p, int chunks) {
 }
 
 template <int kCache, bool kShared>
-cudaError_t launch_one(const Problem& p, const Layout& lay, void* ws, const PrefixSegment* segments, int late,
-                       cudaStream_t stream) {
+cudaError_t launch_one(const Problem& p, const Layout& lay, void* ws, const PrefixSegment* segments, cudaStream_t stream) {
   CUtensorMap tm_k = {}, tm_v = {};
   if (Cfg<kCache>::kTma && !(encode_rows(&tm_k, p, kChunks) && encode_rows(&tm_v, p, 4))) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   const cudaLaunchConfig_t cfg = pair_launch(lay.n_ctas, Cfg<kCache>::kSmemBytes, stream, &attr);
-  return cudaLaunchKernelEx(&cfg, decode_pair_kernel<kCache, kShared>, p, lay, static_cast<char*>(ws), tm_k, tm_v, segments,
-                            late);
+  return cudaLaunchKernelEx(&cfg, decode_pair_kernel<kCache, kShared>, p, lay, static_cast<char*>(ws), tm_k, tm_v, segments);
 }
 
 }  // namespace
@@ -1474,9 +1469,9 @@ cudaError_t decode_pair_setup(int kv_dtype, int sm_count, int* n_pairs) {
 }
 
 cudaError_t launch_decode_pair(const Problem& p, const Layout& lay, void* ws, cudaStream_t stream) {
-  return p.kv_dtype == 2   ? launch_one<kFp4, false>(p, lay, ws, nullptr, 0, stream)
-         : p.kv_dtype == 1 ? launch_one<kE4m3, false>(p, lay, ws, nullptr, 0, stream)
-                           : launch_one<kBf16, false>(p, lay, ws, nullptr, 0, stream);
+  return p.kv_dtype == 2   ? launch_one<kFp4, false>(p, lay, ws, nullptr, stream)
+         : p.kv_dtype == 1 ? launch_one<kE4m3, false>(p, lay, ws, nullptr, stream)
+                           : launch_one<kBf16, false>(p, lay, ws, nullptr, stream);
 }
 
 cudaError_t decode_prefix_setup(int kv_dtype, int sm_count, int* n_pairs) {
@@ -1504,13 +1499,12 @@ cudaError_t launch_decode_prefix(const Problem& p, const Layout& lay, const Pref
     over.num_pages = pl.wide_tiles;
     over.page_size = kTile;
     const cudaError_t e =
-        launch_one<kF16, true>(over, first, ws, reinterpret_cast<const PrefixSegment*>(base + pl.wide_segments), 0, stream);
+        launch_one<kF16, true>(over, first, ws, reinterpret_cast<const PrefixSegment*>(base + pl.wide_segments), stream);
     if (e != cudaSuccess) return e;
   }
-  const int late = pl.wide_tiles > 0;
-  return p.kv_dtype == 2   ? launch_one<kFp4, true>(p, lay, ws, segments, late, stream)
-         : p.kv_dtype == 1 ? launch_one<kE4m3, true>(p, lay, ws, segments, late, stream)
-                           : launch_one<kBf16, true>(p, lay, ws, segments, late, stream);
+  return p.kv_dtype == 2   ? launch_one<kFp4, true>(p, lay, ws, segments, stream)
+         : p.kv_dtype == 1 ? launch_one<kE4m3, true>(p, lay, ws, segments, stream)
+                           : launch_one<kBf16, true>(p, lay, ws, segments, stream);
 }
 
 }  // namespace mla

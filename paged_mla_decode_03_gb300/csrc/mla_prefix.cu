@@ -536,11 +536,11 @@ join_prefix_kernel(Problem p, Layout lay, PrefixLayout pl, char* __restrict__ ws
   const float* part_lse = reinterpret_cast<const float*>(ws + lay.part_lse);
   const signed char* part_scale = reinterpret_cast<const signed char*>(ws + prefix_scale_offset(lay));
   const int t = threadIdx.x >> 3, r = blockIdx.x * kJoinRows + (threadIdx.x & 7);
-  // (the partitioner had ended before the decode kernel let this one start)
+  // (before the entries, too: a grid sees what others wrote once it has waited itself)
+  ptx::pdl_wait();
   const int n_entries = reinterpret_cast<const int*>(ws)[kHdrNumCombine];
   PrefixEntry e = {};
   if (blockIdx.y < n_entries) e = entries[blockIdx.y];
-  ptx::pdl_wait();
   for (int i = blockIdx.y; i < n_entries; i += gridDim.y) {
     if (i != blockIdx.y) e = entries[i];
     if (r >= e.rows) continue;
