@@ -120,7 +120,7 @@ enum HeaderWord {
 // Byte layout of the workspace; computed on the host at plan time.
 struct Layout {
   size_t items;          // WorkItem[max_items]
-  size_t combine;        // CombineItem[max_combine]
+  size_t combine;        // CombineItem[max_combine]; with shared prefixes the segments of row groups
   size_t worker_ranges;  // int[n_workers + 1]: worker w owns items [r[w], r[w+1])
   size_t req_scratch;    // int[4 * batch]: partitioner scratch
   size_t group_scratch;  // partitioner scratch per row group / item

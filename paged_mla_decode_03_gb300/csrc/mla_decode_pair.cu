@@ -437,7 +437,7 @@ template <int kCache, bool kShared>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
                    const __grid_constant__ CUtensorMap tm_k,   // (bf16 cache only)
-                   const __grid_constant__ CUtensorMap tm_v, const PrefixSegment* __restrict__ segments) {
+                   const __grid_constant__ CUtensorMap tm_v) {
   using C = Cfg<kCache>;
   // The swizzled tiles need 1024-byte alignment, and there is no room to round
   // up: the block has no other shared memory, so its dynamic part starts at
@@ -453,6 +453,7 @@ decode_pair_kernel(const Problem p, const Layout lay, char* __restrict__ ws,
   const int worker = (int)cluster_id_x();
   const WorkItem* items = reinterpret_cast<const WorkItem*>(ws + lay.items);
   const int* worker_begin = reinterpret_cast<const int*>(ws + lay.worker_ranges);
+  const PrefixSegment* segments = reinterpret_cast<const PrefixSegment*>(ws + lay.combine);  // kShared
 
   Ctx c;
   c.bars = reinterpret_cast<uint64_t*>(sm + C::OFF_BARS);
@@ -1450,14 +1451,14 @@ bool encode_rows(CUtensorMap* map, const Problem& p, int chunks) {
 }
 
 template <int kCache, bool kShared>
-cudaError_t launch_one(const Problem& p, const Layout& lay, void* ws, const PrefixSegment* segments, cudaStream_t stream) {
+cudaError_t launch_one(const Problem& p, const Layout& lay, void* ws, cudaStream_t stream) {
   CUtensorMap tm_k = {}, tm_v = {};
   if (Cfg<kCache>::kTma && !(encode_rows(&tm_k, p, kChunks) && encode_rows(&tm_v, p, 4))) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   const cudaLaunchConfig_t cfg = pair_launch(lay.n_ctas, Cfg<kCache>::kSmemBytes, stream, &attr);
-  return cudaLaunchKernelEx(&cfg, decode_pair_kernel<kCache, kShared>, p, lay, static_cast<char*>(ws), tm_k, tm_v, segments);
+  return cudaLaunchKernelEx(&cfg, decode_pair_kernel<kCache, kShared>, p, lay, static_cast<char*>(ws), tm_k, tm_v);
 }
 
 }  // namespace
@@ -1469,9 +1470,9 @@ cudaError_t decode_pair_setup(int kv_dtype, int sm_count, int* n_pairs) {
 }
 
 cudaError_t launch_decode_pair(const Problem& p, const Layout& lay, void* ws, cudaStream_t stream) {
-  return p.kv_dtype == 2   ? launch_one<kFp4, false>(p, lay, ws, nullptr, stream)
-         : p.kv_dtype == 1 ? launch_one<kE4m3, false>(p, lay, ws, nullptr, stream)
-                           : launch_one<kBf16, false>(p, lay, ws, nullptr, stream);
+  return p.kv_dtype == 2   ? launch_one<kFp4, false>(p, lay, ws, stream)
+         : p.kv_dtype == 1 ? launch_one<kE4m3, false>(p, lay, ws, stream)
+                           : launch_one<kBf16, false>(p, lay, ws, stream);
 }
 
 cudaError_t decode_prefix_setup(int kv_dtype, int sm_count, int* n_pairs) {
@@ -1489,22 +1490,21 @@ cudaError_t decode_prefix_setup(int kv_dtype, int sm_count, int* n_pairs) {
 cudaError_t launch_decode_prefix(const Problem& p, const Layout& lay, const PrefixLayout& pl, void* ws,
                                  cudaStream_t stream) {
   char* base = static_cast<char*>(ws);
-  const PrefixSegment* segments = reinterpret_cast<const PrefixSegment*>(base + pl.segments);
   if (pl.wide_tiles > 0) {
     Layout first = lay;
     first.items = pl.wide_items;
     first.worker_ranges = pl.wide_ranges;
+    first.combine = pl.wide_segments;
     Problem over = p;  // its cache: the widened rows, as pages of a tile
     over.kv_cache = base + pl.wide_rows;
     over.num_pages = pl.wide_tiles;
     over.page_size = kTile;
-    const cudaError_t e =
-        launch_one<kF16, true>(over, first, ws, reinterpret_cast<const PrefixSegment*>(base + pl.wide_segments), stream);
+    const cudaError_t e = launch_one<kF16, true>(over, first, ws, stream);
     if (e != cudaSuccess) return e;
   }
-  return p.kv_dtype == 2   ? launch_one<kFp4, true>(p, lay, ws, segments, stream)
-         : p.kv_dtype == 1 ? launch_one<kE4m3, true>(p, lay, ws, segments, stream)
-                           : launch_one<kBf16, true>(p, lay, ws, segments, stream);
+  return p.kv_dtype == 2   ? launch_one<kFp4, true>(p, lay, ws, stream)
+         : p.kv_dtype == 1 ? launch_one<kE4m3, true>(p, lay, ws, stream)
+                           : launch_one<kBf16, true>(p, lay, ws, stream);
 }
 
 }  // namespace mla

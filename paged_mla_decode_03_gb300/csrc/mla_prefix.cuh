@@ -144,10 +144,9 @@ inline bool make_prefix_layout(long long batch, long long heads, long long max_q
     return at;
   };
   lay->items = take(sizeof(WorkItem) * (size_t)items);
-  lay->combine = off;
   lay->worker_ranges = take(sizeof(int) * (size_t)(n_workers + 1));
   pre->entries = take(sizeof(PrefixEntry) * (size_t)rg);
-  pre->segments = take(sizeof(PrefixSegment) * (size_t)(kPrefixSegments * rg));
+  lay->combine = pre->segments = take(sizeof(PrefixSegment) * (size_t)(kPrefixSegments * rg));
   pre->scratch_bytes = prefix_scratch_bytes(batch, groups, rg);
   pre->scratch_in_smem = pre->scratch_bytes <= kPartitionSmemMax ? 1 : 0;
   pre->scratch = take(pre->scratch_in_smem ? 0 : pre->scratch_bytes);
