@@ -342,10 +342,11 @@ partition_prefix_kernel(Problem p, PrefixArgs pa, Layout lay, PrefixLayout pl, c
       widens = true;
       int other = 0;
       for (int r = tid; r < n_rg; r += blockDim.x) other += units(0, r) + units(1, r) * kWideTenths / 10;
+      for (int g = tid; g < G; g += blockDim.x) other += s.wide[g] ? s.shared[g] * n / kWideCopy : 0;
       other = (int)__reduce_add_sync(kAll, (unsigned)other);
       if (lane == 0) atomicAdd(&sh.total, other);
       __syncthreads();
-      widens = sh.total / n + 3 * (int)kCutTiles < min(alone, shared);
+      widens = sh.total / n + kWideFixed < min(alone, shared);
       __syncthreads();  // (every thread has read the sum before a scan clears it)
       if (widens) {
         scan_list(0);

@@ -50,9 +50,17 @@ constexpr int kPrefixNoMask = 1 << 30;  // `mask` of a segment that is seen whol
 // where rows that come by TMA take 0.88).  Where four row groups and more walk the same shared rows
 // these are widened once, into the workspace, and walked there, by a list of items of its
 // own; the row groups' own rows stay in the first list, and all their query rows are joined.
-// (32 x 128 heads over 65536 rows of 4 bits: 569 us a call without, 396-401 with.  Below four the copy, its launch and
-// the join take what it saves.)
+// Measured without and with, us in a graph, 128 heads, e4m3 (4 bits save less, 0.40 us a tile of a worker
+// instead of 0.46): 32 row groups over 65536 rows 591 and 395, over 8192 98 and 89, over 2048 45 and 59; 16
+// over 20480 115 and 99, over 8192 62 and 69; 8 over 65536 170 and 150, over 20480 73 and 76; 4 over 65536 104 and
+// 111; 12 groups of 8 over 8192 260 and 233, of 4 142 and 153.  So what is saved has to pay for the copy (a row
+// read and written: kWideCopy), items and partials of both lists, and kWideFixed: the partitioner judges
+// that, by the lengths it finds.  A plan whose groups have fewer than four row groups has no room for it
+// (4 groups of 2, 8 requests of 32 heads each, over 16384 rows: 65 and 95).  One that has, and whose rows are not
+// widened, takes some 10 us for the two kernels more.
 constexpr int kWideRowGroups = 4;
+constexpr int kWideCopy = 75;   // tiles that are widened in the time of one of the first list's
+constexpr int kWideFixed = 11;  // of the second list's join and first loads, in the first one's tiles
 constexpr long long kWideBytes = 1LL << 30;  // of widened rows at most
 constexpr int kWideOverhead = 8;             // of an item over them, in their tiles
 constexpr int kWideTenths = 7;               // one of their tiles, in tenths of another's
