@@ -582,7 +582,7 @@ size_t mla_beam_workspace_size(const mla_beam_params *params);
  *   Within a beam the order is that of the logits, exactly.  Beams with the same logits and the same score
  * have the same scores to the bit, wherever their rows lie in memory, and so come by index.  Between
  * other beams scores are compared as pairs of floats (48 bits and more) over ln sum exp, which is formed
- * in fp32 and off by some 2^-25, by 2^-18 at most: what is nearer than that may come in either order.
+ * in fp32 and off by some 2^-24, by 2^-18 at most: what is nearer than that may come in either order.
  *
  * logits       [B][W] rows of V by the two strides, in elements and >= 0; the last dim is
  *              contiguous; aligned to its type

@@ -1069,7 +1069,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, *, k: Optional[int] 
     ``scores`` fp32 ``[B, W]``: beam w offers token v with the score ``scores[w] +
     logits[w, v] - logsumexp(logits[w])``.  Of equal scores the lower beam, then the
     lower token is first: exactly so within a beam, and between beams with the same logits and score;
-    the logsumexp is off by some 2^-25 (2^-18 at most), so continuations of other beams
+    the logsumexp is off by some 2^-24 (2^-18 at most), so continuations of other beams
     that are nearer than that may come in either order.  ``finished`` uint8 or bool ``[B, W]``: an ended beam
     offers only ``end_token``, with its score.  Tokens of -inf are not offered, nor is anything
     by a beam whose score is not finite or that has a NaN or +inf among its logits;

@@ -11,15 +11,17 @@
 // candidates of two beams is lse.  Its sum is of 2^(x log2(e) - n), n whole: the product in two
 // parts, sums with their rounding errors, everything else powers of two, which are exact; and
 // the largest logit's own term divides it, so that what is wrong with that term, which may
-// be all of a sum, leaves lse.  So lse is off by some 2^-25, and by the exponential's own 2^-21
-// at most where terms far below the largest make up the sum.  Scores are pairs of floats (48
-// bits; the card has few units for 64).  Which thread takes a value, and in which order,
+// be all of a sum, leaves lse.  Measured over rows of 100003 tokens, of ordinary, peaked and flat
+// shapes: lse off by 2^-25 to 2^-23.4 in the mean, by 2^-21.7 at most; were all roundings of a sum one
+// way it would be 2^-18.  Scores are pairs of floats (48 bits; the card has few units for 64).  Which thread takes a value, and in which order,
 // is by its index alone and not by where the row lies in memory: rows with the same logits have the
 // same lse, to the bit, and their ties go by index.
 //
 // What bounds it: the bytes of the logits, where there are many; a chain of two launches, else.
-// A thread streams its own values through shared memory, with no barrier and no copy of another's,
-// a chunk ahead, four blocks to an SM: it keeps their maximum and sum.  The k-th
+// A thread streams its own values through shared memory, with no barrier, a chunk ahead, four blocks
+// to an SM: it keeps their maximum and sum.  (Where rows start off 16 bytes its units are the ends of
+// its own copies and the starts of its neighbour's: 24 x 16 beams over 100003 fp32 tokens 41.5 us
+// in a graph, and 39.8 when a value's thread hung on where its row starts.)  The k-th
 // largest maximum of 64 groups of threads is a threshold that at least k values are at or above,
 // and seldom many more; the few stretches of a thread's values whose maximum is not below it are
 // read again, and what passes is ranked by counting.
@@ -115,6 +117,7 @@ __device__ __forceinline__ float whole_power(float d) {
 struct Two {
   float h, l;
 };
+// (Knuth's sum of two with its rounding error; `settle` is Dekker's, for a larger first.)
 __device__ __forceinline__ Two exact_sum(float a, float b) {
   const float s = a + b, z = s - a;
   return {s, (a - (s - z)) + (b - z)};
