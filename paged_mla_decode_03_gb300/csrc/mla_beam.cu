@@ -12,7 +12,7 @@
 // parts, sums with their rounding errors, everything else powers of two, which are exact; and
 // the largest logit's own term divides it, so that what is wrong with that term, which may
 // be all of a sum, leaves lse.  Measured over rows of 100003 tokens, of ordinary, peaked and flat
-// shapes: lse off by 2^-25 to 2^-23.4 in the mean, by 2^-21.7 at most; were all roundings of a sum one
+// shapes: lse off by 2^-25 to 2^-23.4 (root mean square), by 2^-21.7 at most; were all roundings of a sum one
 // way it would be 2^-18.  Scores are pairs of floats (48 bits; the card has few units for 64).  Which thread takes a value, and in which order,
 // is by its index alone and not by where the row lies in memory: rows with the same logits have the
 // same lse, to the bit, and their ties go by index.
