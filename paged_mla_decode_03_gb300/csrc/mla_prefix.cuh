@@ -54,7 +54,7 @@ constexpr int kPrefixNoMask = 1 << 30;  // `mask` of a segment that is seen whol
 // instead of 0.46): 32 row groups over 65536 rows 591 and 395, over 8192 98 and 89, over 2048 45 and 59; 16
 // over 20480 115 and 99, over 8192 62 and 69; 8 over 65536 170 and 150, over 20480 73 and 76; 4 over 65536 104 and
 // 111; 12 groups of 8 over 8192 260 and 233, of 4 142 and 153.  So what is saved has to pay for the copy (a row
-// read and written: kWideCopy), items and partials of both lists, and kWideFixed: the partitioner judges
+// read and written: kWideCopy), items and partials of both lists, and kWideFixed: the partitioner weighs
 // that, by the lengths it finds.  A plan whose groups have fewer than four row groups has no room for it
 // (4 groups of 2, 8 requests of 32 heads each, over 16384 rows: 65 and 95).  One that has, and whose rows are not
 // widened, takes some 10 us for the two kernels more.
