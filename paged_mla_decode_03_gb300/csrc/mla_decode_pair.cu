@@ -341,9 +341,9 @@ struct Query {
 // others' O, as 0 times it is a NaN.  Who sees a NaN has one among its scores, and so in its
 // sum, whatever V holds; so V may hold something finite there.  f16: the lowest value for a NaN
 // (4 bits and e4m3 have no infinity), at their conversion; bf16, which TMA brings, only where a score
-// that is not finite shows it.  (In a graph 96 x 16 heads behind 6000 rows of bf16 take 62.1 us with it
-// and 60.0 without, 16 x 8 x 32 heads over e4m3 86.1 and 83.6.  Looking at all of V before it is
-// passed on, by four warps, took 64.4.)
+// that is not finite shows it.  (In a graph 96 x 16 heads behind 6000 rows of bf16 take 62.8 us with it
+// and 60.7 without, 16 x 8 x 32 heads over e4m3 85.3 and 83.9.  Looking at all of V before it is
+// passed on, by four warps, took 4.5 us of the first.)
 __device__ __forceinline__ bool any_nan(uint32_t codes) {  // of four e4m3
   return (((codes & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
 }
